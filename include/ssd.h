@@ -335,6 +335,71 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_shape_t *shape, const void *x, co
                                      const float *A, const void *B, const void *C, const float *D,
                                      float *state, void *y, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the scan: the short causal convolution, the
+ * selective scan with a decay per channel and state, and the block norm.
+ *
+ * Rows.  Token-major operands are given as ssd_rows_t: element (b, t, c) is
+ * data[b * batch_stride + t * row_stride + c], strides in elements, c
+ * contiguous.  So a column slice of a wider projection is read (or a slice
+ * of its gradient written) in place.  `data` needs only its element type's
+ * alignment; 16-byte aligned rows (pointer and strides) take the vector
+ * path.  Rows that are written must not overlap each other or any operand.
+ * Batches.  cu_seqlens NULL: `batch` sequences of `seqlen` tokens (nseq is
+ * ignored, and is `batch` below).  Otherwise batch is 1 and the `nseq`
+ * sequences lie back to back along seqlen: cu_seqlens is a HOST array of
+ * nseq + 1 offsets, 0 first and seqlen last, non-decreasing (empty sequences
+ * are allowed), read before the call returns.  Nothing crosses a sequence's
+ * boundary, not even a non-finite value.  An empty sequence hands its
+ * initial state on as its final state, and the other way for gradients.
+ * State and parameter arrays are contiguous and need their element type's
+ * alignment.  Everything else (streams, ownership, errors, reproducibility)
+ * is as for the other entry points; dtype is fp32 or bf16.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *data;
+    int64_t batch_stride, row_stride;
+} ssd_rows_t;
+
+/*
+ * Short causal convolution, depthwise, with bias and SiLU:
+ *   p[t, c] = bias[c] + sum_{k < W} weight[c, k] * x[t - (W-1) + k, c]
+ *   y[t, c] = silu ? p / (1 + exp(-p)) : p
+ * where the rows before a sequence's first token come from init_state
+ * (zeros when NULL), the W-1 rows that precede it in time order.
+ *   x [b, L, C] T, weight [C, W] fp32, bias [C] fp32 (NULL: none),
+ *   init_state, final_state [nseq, W-1, C] T (either NULL).
+ * y is written as `nparts` arrays of part[i] columns each, in channel order
+ * (sum of part = C): the x, B and C that ssd_fwd takes, from one pass.
+ * Supported: W 2, 3 or 4.
+ * ssd_conv_bwd: dy (in the same parts), dfinal_state (NULL: zero) ->
+ *   dx [b, L, C] T, dweight [C, W], dbias [C] fp32, dinit_state T (each of
+ *   the last three may be NULL).  The sums run over tiles of tokens in a
+ *   fixed order; `workspace` holds ssd_conv_bwd_workspace_size() bytes.
+ * ssd_conv_step: one token per sequence, x and y [b, C] (row_stride
+ *   ignored), state [b, W-1, C] T shifted in place.
+ */
+#define SSD_CONV_MAX_PARTS 4
+typedef struct {
+    int64_t batch, seqlen, channels, width;
+    int64_t nparts, part[SSD_CONV_MAX_PARTS];
+    ssd_dtype_t dtype;
+    int silu;
+} ssd_conv_shape_t;
+
+SSD_API ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                  const ssd_rows_t *x, const float *weight, const float *bias,
+                                  const void *init_state, const ssd_rows_t *y, void *final_state,
+                                  cudaStream_t stream);
+SSD_API size_t ssd_conv_bwd_workspace_size(const ssd_conv_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq);
+SSD_API ssd_status_t ssd_conv_bwd(const ssd_conv_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                  const ssd_rows_t *dy, const ssd_rows_t *x, const float *weight,
+                                  const float *bias, const void *init_state, const void *dfinal_state,
+                                  const ssd_rows_t *dx, float *dweight, float *dbias, void *dinit_state,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+SSD_API ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, const ssd_rows_t *x, const float *weight,
+                                   const float *bias, void *state, const ssd_rows_t *y, cudaStream_t stream);
+
 /*
  * Launch timing (instrumentation; the pages have no counterpart).  While
  * enabled, every entry point records a CUDA event on its stream before each

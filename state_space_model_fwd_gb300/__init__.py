@@ -19,6 +19,8 @@ import threading
 
 import torch
 
+from . import _layer
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libssd.so")
 
@@ -32,7 +34,8 @@ EXPORTED = ("ssd_status_string", "ssd_abi_version", "ssd_fwd_workspace_size", "s
             "selective_scan_fwd", "ssd_launch_timing_enable", "ssd_launch_timing_read",
             "ssd_launch_timing_name", "ssd_fwd_noalloc", "ssd_chunk_scan_workspace_size",
             "ssd_get_device_status", "ssd_selftest_scan_timeout", "ssd_decode_step",
-            "ssd_fwd_varlen_workspace_size", "ssd_fwd_varlen", "ssd_fwd_quadratic")
+            "ssd_fwd_varlen_workspace_size", "ssd_fwd_varlen", "ssd_fwd_quadratic",
+            "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step")
 
 
 class ssd_shape_t(ctypes.Structure):
@@ -95,6 +98,7 @@ def load_library(path: str = LIB_PATH):
                      "ssd_fwd_noalloc", "ssd_get_device_status", "ssd_selftest_scan_timeout", "ssd_decode_step",
                      "ssd_fwd_varlen", "ssd_fwd_quadratic"):
             getattr(lib, name).restype = i32
+        _layer.declare(lib)
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -444,6 +448,8 @@ def launch_times_ms() -> list:
     return [((lib.ssd_launch_timing_name(i) or b"?").decode(), float(buf[i])) for i in range(min(n, 16))]
 
 
-__all__ = ["ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
+from ._layer import ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step  # noqa: E402  (built on the helpers above)
+
+__all__ = ["ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
            "ssd_state_passing", "ssd_chunk_scan", "selective_scan_fwd", "ssd_shape_t", "SSDError",
            "load_library", "status_string", "EXPORTED", "LIB_PATH"]

@@ -1,0 +1,243 @@
+"""Binding of the operators around the scan: the short causal convolution.
+
+Token-major operands (x, y, gradients) may be strided views whose last
+dimension is contiguous, such as column slices of a projection's rows; states
+and parameters are contiguous.  ``cu_seqlens`` is a host sequence of
+nseq + 1 offsets as for ssd_fwd_varlen; without it every batch row is one
+sequence.  Argument marshalling only, as everywhere in this package.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+_F32 = torch.float32
+_CODE = {torch.float32: 0, torch.bfloat16: 1}
+_MAX_PARTS = 4
+
+
+class _rows_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class _conv_shape_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("nparts", ctypes.c_int64), ("part", ctypes.c_int64 * _MAX_PARTS),
+                ("dtype", ctypes.c_int), ("silu", ctypes.c_int)]
+
+
+def declare(lib):
+    """Declare this module's entry points on the loaded library."""
+    vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
+    lib.ssd_conv_fwd.argtypes = [vp, vp, i64] + [vp] * 7
+    lib.ssd_conv_bwd_workspace_size.argtypes = [vp, vp, i64]
+    lib.ssd_conv_bwd_workspace_size.restype = sz
+    lib.ssd_conv_bwd.argtypes = [vp, vp, i64] + [vp] * 11 + [sz, vp]
+    lib.ssd_conv_step.argtypes = [vp] * 7
+    for name in ("ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step"):
+        getattr(lib, name).restype = i32
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _raise(fn, status):
+    from . import _check
+    _check(fn, status)
+
+
+def _stream_of(x, stream):
+    return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
+
+
+def _code(x, name="x"):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _CODE.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
+    return code
+
+
+def _rows(t, name, dtype, shape, dev):
+    """ssd_rows_t of a [b, L, ...] tensor whose trailing dimensions are
+    contiguous; of [b, ...] where ``shape`` has no token dimension."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    want = 1
+    for i in range(len(shape) - 1, 1, -1):
+        if st[i] != want and shape[i] > 1:
+            raise ValueError(f"{name} must be contiguous in its trailing dimensions")
+        want *= shape[i]
+    return _rows_t(t.data_ptr(), st[0], st[1])
+
+
+def _rows2(t, name, dtype, shape, dev):
+    """The same for one token per sequence, [b, ...] (no token dimension)."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    want = 1
+    for i in range(len(shape) - 1, 0, -1):
+        if st[i] != want and shape[i] > 1:
+            raise ValueError(f"{name} must be contiguous in its trailing dimensions")
+        want *= shape[i]
+    return _rows_t(t.data_ptr(), st[0], 0)
+
+
+def _flat(t, name, dtype, shape, dev):
+    """data pointer of a contiguous tensor; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _offsets(cu_seqlens, batch):
+    """(ctypes array or None, number of sequences)."""
+    if cu_seqlens is None:
+        return None, batch
+    cu = cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens
+    if len(cu) == 0:
+        raise ValueError("cu_seqlens needs at least one offset")
+    return (ctypes.c_int64 * len(cu))(*cu), len(cu) - 1
+
+
+def _workspace(workspace, need, dev):
+    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
+        return workspace
+    return torch.empty(max(need, 16), device=dev, dtype=torch.uint8)
+
+
+# ---------------------------------------------------------------------------
+# short causal convolution
+# ---------------------------------------------------------------------------
+def _conv_shape(x, weight, parts, silu):
+    if x.dim() != 3 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must be [b, L, C] and weight [C, W]")
+    if not 1 <= len(parts) <= _MAX_PARTS:
+        raise ValueError(f"1 to {_MAX_PARTS} parts, got {len(parts)}")
+    b, L, C = x.shape
+    return _conv_shape_t(b, L, C, weight.shape[1], len(parts), (ctypes.c_int64 * _MAX_PARTS)(*parts), _code(x),
+                         1 if silu else 0)
+
+
+def ssd_conv_fwd(x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens=None, split=None, y=None,
+                 final_state=None, return_final_state=True, stream=None):
+    """Causal depthwise convolution over the last W tokens with bias and SiLU.
+
+    x [b, L, C], weight [C, W] fp32 (W 2 to 4), bias [C] fp32; the rows before
+    a sequence come from ``init_state`` [nseq, W-1, C] (zeros without it).
+    Returns ``(y, final_state)``, the final state being each sequence's last
+    W-1 rows of x.  With ``split``, widths that sum to C, y is a list of
+    contiguous tensors [b, L, width]: the x, B and C a scan takes.  ``y`` and
+    ``final_state`` may be given; they must not overlap the inputs."""
+    lib = _lib()
+    code = _code(x)
+    dev, dt = x.device, x.dtype
+    parts = [x.shape[-1]] if split is None else [int(v) for v in split]
+    shape = _conv_shape(x, weight, parts, silu)
+    b, L, C = x.shape
+    W = weight.shape[1]
+    cu, nseq = _offsets(cu_seqlens, b)
+    xr = _rows(x, "x", dt, (b, L, C), dev)
+    wp = _flat(weight, "weight", _F32, (C, W), dev)
+    bp = _flat(bias, "bias", _F32, (C,), dev)
+    ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
+    if y is None:
+        ys = [torch.empty((b, L, p), device=dev, dtype=dt) for p in parts]
+    else:
+        ys = [y] if split is None else list(y)
+        if len(ys) != len(parts):
+            raise ValueError(f"y must hold {len(parts)} tensors")
+    yr = (_rows_t * len(parts))(*[_rows(t, "y", dt, (b, L, p), dev) for t, p in zip(ys, parts)])
+    if final_state is None and return_final_state:
+        final_state = torch.empty((nseq, W - 1, C), device=dev, dtype=dt)
+    fp = _flat(final_state, "final_state", dt, (nseq, W - 1, C), dev)
+    if fp is not None and fp == ip:
+        raise ValueError("final_state must not be init_state")
+    with torch.cuda.device(dev):
+        _raise("ssd_conv_fwd", lib.ssd_conv_fwd(ctypes.byref(shape), cu, nseq, ctypes.byref(xr), wp, bp, ip, yr, fp,
+                                                _stream_of(x, stream)))
+    return (ys[0] if split is None else ys), final_state
+
+
+def ssd_conv_bwd(dy, x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens=None, dfinal_state=None, dx=None,
+                 workspace=None, stream=None):
+    """Gradient of ssd_conv_fwd.  ``dy`` is a tensor [b, L, C] or the list of
+    parts' gradients; ``dfinal_state`` [nseq, W-1, C] that of the final state
+    (zero without it).  Returns ``(dx, dweight, dbias, dinit_state)``: dbias
+    and dinit_state None where the input was None; dweight and dbias fp32."""
+    lib = _lib()
+    _code(x)
+    dev, dt = x.device, x.dtype
+    dys = [dy] if isinstance(dy, torch.Tensor) else list(dy)
+    parts = [t.shape[-1] for t in dys]
+    shape = _conv_shape(x, weight, parts, silu)
+    b, L, C = x.shape
+    W = weight.shape[1]
+    cu, nseq = _offsets(cu_seqlens, b)
+    xr = _rows(x, "x", dt, (b, L, C), dev)
+    gr = (_rows_t * len(parts))(*[_rows(t, "dy", dt, (b, L, p), dev) for t, p in zip(dys, parts)])
+    wp = _flat(weight, "weight", _F32, (C, W), dev)
+    bp = _flat(bias, "bias", _F32, (C,), dev)
+    ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
+    gp = _flat(dfinal_state, "dfinal_state", dt, (nseq, W - 1, C), dev)
+    if dx is None:
+        dx = torch.empty((b, L, C), device=dev, dtype=dt)
+    dxr = _rows(dx, "dx", dt, (b, L, C), dev)
+    dweight = torch.empty((C, W), device=dev, dtype=_F32)
+    dbias = None if bias is None else torch.empty((C,), device=dev, dtype=_F32)
+    dinit = None if init_state is None else torch.empty((nseq, W - 1, C), device=dev, dtype=dt)
+    workspace = _workspace(workspace, lib.ssd_conv_bwd_workspace_size(ctypes.byref(shape), cu, nseq), dev)
+    with torch.cuda.device(dev):
+        _raise("ssd_conv_bwd", lib.ssd_conv_bwd(
+            ctypes.byref(shape), cu, nseq, gr, ctypes.byref(xr), wp, bp, ip, gp, ctypes.byref(dxr), dweight.data_ptr(),
+            None if dbias is None else dbias.data_ptr(), None if dinit is None else dinit.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_of(x, stream)))
+    return dx, dweight, dbias, dinit
+
+
+def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None, stream=None):
+    """One token per sequence: x [b, C]; ``state`` [b, W-1, C], the rows before
+    it, moves up by one in place.  Returns y [b, C]."""
+    lib = _lib()
+    code = _code(x)
+    if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must be [b, C] and weight [C, W]")
+    dev, dt = x.device, x.dtype
+    b, C = x.shape
+    W = weight.shape[1]
+    xr = _rows2(x, "x", dt, (b, C), dev)
+    wp = _flat(weight, "weight", _F32, (C, W), dev)
+    bp = _flat(bias, "bias", _F32, (C,), dev)
+    if state is None:
+        raise TypeError("state must be a CUDA tensor")
+    sp = _flat(state, "state", dt, (b, W - 1, C), dev)
+    if y is None:
+        y = torch.empty((b, C), device=dev, dtype=dt)
+    yr = _rows2(y, "y", dt, (b, C), dev)
+    shape = _conv_shape_t(b, 1, C, W, 1, (ctypes.c_int64 * _MAX_PARTS)(C), code, 1 if silu else 0)
+    with torch.cuda.device(dev):
+        _raise("ssd_conv_step", lib.ssd_conv_step(ctypes.byref(shape), ctypes.byref(xr), wp, bp, sp, ctypes.byref(yr),
+                                                  _stream_of(x, stream)))
+    return y
