@@ -401,6 +401,56 @@ SSD_API ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, const ssd_rows
                                    const float *bias, void *state, const ssd_rows_t *y, cudaStream_t stream);
 
 /*
+ * Channel scan: the selective scan with a decay per channel and state.
+ *   delta = dt_softplus ? log(1 + exp(dt + dt_bias)) : dt + dt_bias
+ *   h[c, n] <- exp(delta[t, c] A[c, n]) h[c, n] + delta[t, c] x[t, c] B[t, g(c), n]
+ *   y[t, c]  = (sum_n h[c, n] C[t, g(c), n] + D[c] x[t, c]) * silu(z[t, c])
+ * x, dt, z, y [b, L, Ch] T; B, C rows of [b, L, G, N] T (G N contiguous;
+ * channels g Ch/G .. share group g); A [Ch, N], D, dt_bias [Ch] fp32; states
+ * [nseq, Ch, N] fp32.  z (data NULL), D, dt_bias, init_state, final_state may
+ * be absent.  A must be finite.  N 8, 16 or 32; A and the state arrays are
+ * 16-byte aligned.  States, sums and gradients are held in fp32; y is rounded
+ * once.  The workspace (size 0 where none is needed) holds chunk states and
+ * the packed offsets, and needs no initialisation.
+ * ssd_channel_scan_bwd: dy and dfinal_state (NULL: zero) -> the gradients of
+ * every input given: rows dx, ddt, dz, dB, dC in T, dA, dD, ddt_bias,
+ * dinit_state in fp32 (any of the latter four NULL: not written; dz ignored
+ * without z).  Nothing from the forward call is needed.
+ * ssd_channel_scan_step: one token per sequence; rows are [b, ...]
+ * (row_stride ignored), state [b, Ch, N] advanced in place, init_state
+ * ignored.
+ */
+typedef struct {
+    int64_t batch, seqlen, channels, dstate, ngroups;
+    ssd_dtype_t dtype;
+    int dt_softplus;
+} ssd_channel_shape_t;
+
+typedef struct {
+    ssd_rows_t x, dt, z, B, C;
+    const float *A, *D, *dt_bias, *init_state;
+} ssd_channel_inputs_t;
+
+typedef struct {
+    ssd_rows_t dx, ddt, dz, dB, dC;
+    float *dA, *dD, *ddt_bias, *dinit_state;
+} ssd_channel_grads_t;
+
+SSD_API size_t ssd_channel_scan_workspace_size(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens,
+                                               int64_t nseq);
+SSD_API ssd_status_t ssd_channel_scan_fwd(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                          const ssd_channel_inputs_t *in, const ssd_rows_t *y, float *final_state,
+                                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+SSD_API size_t ssd_channel_scan_bwd_workspace_size(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens,
+                                                   int64_t nseq);
+SSD_API ssd_status_t ssd_channel_scan_bwd(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                          const ssd_rows_t *dy, const ssd_channel_inputs_t *in,
+                                          const float *dfinal_state, const ssd_channel_grads_t *out, void *workspace,
+                                          size_t workspace_bytes, cudaStream_t stream);
+SSD_API ssd_status_t ssd_channel_scan_step(const ssd_channel_shape_t *shape, const ssd_channel_inputs_t *in,
+                                           float *state, const ssd_rows_t *y, cudaStream_t stream);
+
+/*
  * Launch timing (instrumentation; the pages have no counterpart).  While
  * enabled, every entry point records a CUDA event on its stream before each
  * kernel it launches and one after the last, so a caller can read the device

@@ -35,7 +35,9 @@ EXPORTED = ("ssd_status_string", "ssd_abi_version", "ssd_fwd_workspace_size", "s
             "ssd_launch_timing_name", "ssd_fwd_noalloc", "ssd_chunk_scan_workspace_size",
             "ssd_get_device_status", "ssd_selftest_scan_timeout", "ssd_decode_step",
             "ssd_fwd_varlen_workspace_size", "ssd_fwd_varlen", "ssd_fwd_quadratic",
-            "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step")
+            "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step",
+            "ssd_channel_scan_workspace_size", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd_workspace_size",
+            "ssd_channel_scan_bwd", "ssd_channel_scan_step")
 
 
 class ssd_shape_t(ctypes.Structure):
@@ -448,8 +450,9 @@ def launch_times_ms() -> list:
     return [((lib.ssd_launch_timing_name(i) or b"?").decode(), float(buf[i])) for i in range(min(n, 16))]
 
 
-from ._layer import ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step  # noqa: E402  (built on the helpers above)
+from ._layer import (  # noqa: E402  (built on the helpers above)
+    ssd_channel_scan_bwd, ssd_channel_scan_fwd, ssd_channel_scan_step, ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step)
 
-__all__ = ["ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
+__all__ = ["ssd_channel_scan_fwd", "ssd_channel_scan_bwd", "ssd_channel_scan_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
            "ssd_state_passing", "ssd_chunk_scan", "selective_scan_fwd", "ssd_shape_t", "SSDError",
            "load_library", "status_string", "EXPORTED", "LIB_PATH"]

@@ -1,4 +1,5 @@
-"""Binding of the operators around the scan: the short causal convolution.
+"""Binding of the operators around the scan: the short causal convolution and
+the channel scan.
 
 Token-major operands (x, y, gradients) may be strided views whose last
 dimension is contiguous, such as column slices of a projection's rows; states
@@ -27,6 +28,24 @@ class _conv_shape_t(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("silu", ctypes.c_int)]
 
 
+class _channel_shape_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("dt_softplus", ctypes.c_int)]
+
+
+class _channel_inputs_t(ctypes.Structure):
+    _fields_ = [("x", _rows_t), ("dt", _rows_t), ("z", _rows_t), ("B", _rows_t), ("C", _rows_t),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("init_state", ctypes.c_void_p)]
+
+
+class _channel_grads_t(ctypes.Structure):
+    _fields_ = [("dx", _rows_t), ("ddt", _rows_t), ("dz", _rows_t), ("dB", _rows_t), ("dC", _rows_t),
+                ("dA", ctypes.c_void_p), ("dD", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p),
+                ("dinit_state", ctypes.c_void_p)]
+
+
 def declare(lib):
     """Declare this module's entry points on the loaded library."""
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
@@ -35,7 +54,14 @@ def declare(lib):
     lib.ssd_conv_bwd_workspace_size.restype = sz
     lib.ssd_conv_bwd.argtypes = [vp, vp, i64] + [vp] * 11 + [sz, vp]
     lib.ssd_conv_step.argtypes = [vp] * 7
-    for name in ("ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step"):
+    for name in ("ssd_channel_scan_workspace_size", "ssd_channel_scan_bwd_workspace_size"):
+        getattr(lib, name).argtypes = [vp, vp, i64]
+        getattr(lib, name).restype = sz
+    lib.ssd_channel_scan_fwd.argtypes = [vp, vp, i64] + [vp] * 4 + [sz, vp]
+    lib.ssd_channel_scan_bwd.argtypes = [vp, vp, i64] + [vp] * 5 + [sz, vp]
+    lib.ssd_channel_scan_step.argtypes = [vp] * 5
+    for name in ("ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd",
+                 "ssd_channel_scan_step"):
         getattr(lib, name).restype = i32
 
 
@@ -240,4 +266,121 @@ def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None, stream=None
     with torch.cuda.device(dev):
         _raise("ssd_conv_step", lib.ssd_conv_step(ctypes.byref(shape), ctypes.byref(xr), wp, bp, sp, ctypes.byref(yr),
                                                   _stream_of(x, stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# channel scan
+# ---------------------------------------------------------------------------
+def _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, rows, tok):
+    """(inputs struct, channels, states, groups); ``rows`` is _rows or _rows2
+    and ``tok`` the leading dimensions (b, L) or (b,)."""
+    dev, ty = x.device, x.dtype
+    if x.dim() != len(tok) + 1 or not isinstance(B, torch.Tensor) or B.dim() != len(tok) + 2:
+        raise ValueError("x must be [b, L, Ch] and B, C [b, L, G, N] (without L for one token)")
+    ch = x.shape[-1]
+    G, N = B.shape[-2], B.shape[-1]
+    full, bc = (*tok, ch), (*tok, G, N)
+    return _channel_inputs_t(
+        rows(x, "x", ty, full, dev), rows(dt, "dt", ty, full, dev),
+        _rows_t(None, 0, 0) if z is None else rows(z, "z", ty, full, dev),
+        rows(B, "B", ty, bc, dev), rows(C, "C", ty, bc, dev), _flat(A, "A", _F32, (ch, N), dev),
+        _flat(D, "D", _F32, (ch,), dev), _flat(dt_bias, "dt_bias", _F32, (ch,), dev),
+        _flat(init_state, "init_state", _F32, (nseq, ch, N), dev)), ch, N, G
+
+
+def ssd_channel_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, *, dt_softplus=True,
+                         cu_seqlens=None, y=None, final_state=None, return_final_state=True, workspace=None,
+                         stream=None):
+    """Selective scan with a decay per channel and state:
+
+        delta = softplus(dt + dt_bias)   (dt + dt_bias with dt_softplus=False)
+        h <- exp(delta A) h + delta x B,   y = (sum_n h C + D x) * silu(z)
+
+    x, dt, z [b, L, Ch]; A [Ch, N] fp32 (N 8, 16 or 32); B, C [b, L, G, N];
+    D, dt_bias [Ch] fp32; states [nseq, Ch, N] fp32.  Returns
+    ``(y, final_state)``."""
+    lib = _lib()
+    code = _code(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, Ch]")
+    b, L = x.shape[0], x.shape[1]
+    dev = x.device
+    cu, nseq = _offsets(cu_seqlens, b)
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L))
+    if y is None:
+        y = torch.empty((b, L, ch), device=dev, dtype=x.dtype)
+    yr = _rows(y, "y", x.dtype, (b, L, ch), dev)
+    if final_state is None and return_final_state:
+        final_state = torch.empty((nseq, ch, N), device=dev, dtype=_F32)
+    fp = _flat(final_state, "final_state", _F32, (nseq, ch, N), dev)
+    if fp is not None and fp == ins.init_state:
+        raise ValueError("final_state must not be init_state")
+    shape = _channel_shape_t(b, L, ch, N, G, code, 1 if dt_softplus else 0)
+    with torch.cuda.device(dev):
+        need = lib.ssd_channel_scan_workspace_size(ctypes.byref(shape), cu, nseq)
+        ws = _workspace(workspace, need, dev) if need else None
+        _raise("ssd_channel_scan_fwd", lib.ssd_channel_scan_fwd(
+            ctypes.byref(shape), cu, nseq, ctypes.byref(ins), ctypes.byref(yr), fp, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    return y, final_state
+
+
+def ssd_channel_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, *, dt_softplus=True,
+                         cu_seqlens=None, dfinal_state=None, workspace=None, stream=None):
+    """Gradient of ssd_channel_scan_fwd from its inputs and dy (and that of the
+    final state, zero without it).  Returns ``(dx, ddt, dA, dB, dC, dD, dz,
+    ddt_bias, dinit_state)``, None where the input was None; dA, dD, ddt_bias
+    and dinit_state in fp32, the others in x's type."""
+    lib = _lib()
+    code = _code(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, Ch]")
+    b, L = x.shape[0], x.shape[1]
+    dev, ty = x.device, x.dtype
+    cu, nseq = _offsets(cu_seqlens, b)
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L))
+    gr = _rows(dy, "dy", ty, (b, L, ch), dev)
+    fp = _flat(dfinal_state, "dfinal_state", _F32, (nseq, ch, N), dev)
+    dx, ddt = (torch.empty((b, L, ch), device=dev, dtype=ty) for _ in range(2))
+    dz = None if z is None else torch.empty((b, L, ch), device=dev, dtype=ty)
+    dB, dC = (torch.empty((b, L, G, N), device=dev, dtype=ty) for _ in range(2))
+    dA = torch.empty((ch, N), device=dev, dtype=_F32)
+    dD = None if D is None else torch.empty((ch,), device=dev, dtype=_F32)
+    dbias = None if dt_bias is None else torch.empty((ch,), device=dev, dtype=_F32)
+    dinit = None if init_state is None else torch.empty((nseq, ch, N), device=dev, dtype=_F32)
+    row = lambda t, w: _rows_t(None, 0, 0) if t is None else _rows_t(t.data_ptr(), L * w, w)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    grads = _channel_grads_t(row(dx, ch), row(ddt, ch), row(dz, ch), row(dB, G * N), row(dC, G * N), ptr(dA), ptr(dD),
+                             ptr(dbias), ptr(dinit))
+    shape = _channel_shape_t(b, L, ch, N, G, code, 1 if dt_softplus else 0)
+    with torch.cuda.device(dev):
+        ws = _workspace(workspace, lib.ssd_channel_scan_bwd_workspace_size(ctypes.byref(shape), cu, nseq), dev)
+        _raise("ssd_channel_scan_bwd", lib.ssd_channel_scan_bwd(
+            ctypes.byref(shape), cu, nseq, ctypes.byref(gr), ctypes.byref(ins), fp, ctypes.byref(grads), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    return dx, ddt, dA, dB, dC, dD, dz, dbias, dinit
+
+
+def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state, dt_softplus=True, y=None,
+                          stream=None):
+    """One token per sequence: x, dt, z [b, Ch], B, C [b, G, N]; ``state``
+    [b, Ch, N] fp32 is advanced in place.  Returns y [b, Ch]."""
+    lib = _lib()
+    code = _code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [b, Ch]")
+    b = x.shape[0]
+    dev = x.device
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, None, b, _rows2, (b,))
+    if state is None:
+        raise TypeError("state must be a CUDA tensor")
+    sp = _flat(state, "state", _F32, (b, ch, N), dev)
+    if y is None:
+        y = torch.empty((b, ch), device=dev, dtype=x.dtype)
+    yr = _rows2(y, "y", x.dtype, (b, ch), dev)
+    shape = _channel_shape_t(b, 1, ch, N, G, code, 1 if dt_softplus else 0)
+    with torch.cuda.device(dev):
+        _raise("ssd_channel_scan_step", lib.ssd_channel_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp,
+                                                                  ctypes.byref(yr), _stream_of(x, stream)))
     return y

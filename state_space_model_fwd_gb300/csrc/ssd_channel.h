@@ -1,0 +1,46 @@
+// ssd_channel.h -- arguments and host helpers of the channel scan's kernels.
+#pragma once
+
+#include "ssd_channel.cuh"
+
+namespace ssd {
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;  // tokens are counted in 32 bits, offsets in 64
+
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+template <typename T>
+struct ChannelArgs {
+    Rows<const T> x, dt, z, B, C;  // z.p null: no gate
+    Rows<T> y;
+    const float *A, *D, *bias, *init;
+    float *fin;
+    int ch, per, nblk_g, nblk;  // channels, channels per group, blocks of 32 per group and in all
+    int nseq, soft;
+    Seqs seqs;
+    int chunk, nchunk, units;  // tokens per chunk, chunks (per sequence when lengths are equal), chunks in all
+    float4 *local;             // [unit][block][N / 4][32]: a chunk's own end state
+    float *sums;               // [unit][block][32]: sum of a chunk's deltas
+};
+
+template <typename T>
+ChannelArgs<T> channel_args(const ssd_channel_shape_t *s, const ssd_channel_inputs_t *in, int64_t nseq) {
+    ChannelArgs<T> a{};
+    a.x = rows_of<const T>(in->x), a.dt = rows_of<const T>(in->dt), a.z = rows_of<const T>(in->z);
+    a.B = rows_of<const T>(in->B), a.C = rows_of<const T>(in->C);
+    a.A = in->A, a.D = in->D, a.bias = in->dt_bias, a.init = in->init_state;
+    a.ch = (int)s->channels, a.per = (int)(s->channels / s->ngroups);
+    a.nblk_g = (a.per + 31) / 32, a.nblk = a.nblk_g * (int)s->ngroups;
+    a.nseq = (int)nseq, a.soft = s->dt_softplus != 0;
+    a.seqs = Seqs{nullptr, (int)nseq, (int)s->seqlen};
+    return a;
+}
+
+ssd_status_t check_channel(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq);
+bool channel_inputs_ok(const ssd_channel_shape_t *s, const ssd_channel_inputs_t *in, bool rows);
+
+cudaError_t write_offsets(const int64_t *cu, int64_t nseq, int *dst, cudaStream_t st);
+cudaError_t pass_empty_states(const int *start, int64_t nseq, int64_t each, const float *src, float *dst,
+                              cudaStream_t st);
+
+}  // namespace ssd

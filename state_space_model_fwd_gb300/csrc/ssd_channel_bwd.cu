@@ -1,0 +1,705 @@
+// ssd_channel_bwd.cu -- gradient of the channel scan.
+//
+// With g = dy silu(z), a_t = exp(delta_t A) and the gradient dh_t of the
+// state after token t:
+//   dh_t = g_t C_t + a_{t+1} dh_{t+1}
+//   dC_t = sum_c g_t h_t,  dB_t = sum_c delta_t x_t dh_t
+//   du_t = sum_n dh_t B_t,  w_t = dh_t a_t h_{t-1}
+//   dx_t = delta_t du_t + D g_t,  ddelta_t = x_t du_t + sum_n w_t A,  dA = sum_t w_t delta_t
+// Four launches over chunks of 32 tokens (16 for 32 states):
+//   1 chunk summaries: the state a chunk leaves from a zero start, the
+//     gradient its outputs send back to the state before it, its sum of
+//     deltas (exp(A sum delta) is its decay);
+//   2 the two recurrences over chunks, in place: the state entering and the
+//     gradient leaving every chunk;
+//   3 per chunk: forward once, keeping every kTB-th state in shared memory;
+//     then backward kTB tokens at a time, whose states and decays are formed
+//     again and stay in registers.  dB and dC are summed over the lanes of a
+//     warp, then over the block's 128 channels; dA, dD and ddt_bias over the
+//     chunks a block walks;
+//   4 the sums over channel blocks and over blocks, in a fixed order.
+// About 15 issue slots a state (1 and 3 together), most of it arithmetic:
+// bound by issue, with eight warps an SM (their registers).
+#include "ssd_channel.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kWarps = 4;
+
+template <int N>
+struct Geo {
+    static constexpr int CH = N == 32 ? 16 : 32;  // tokens per chunk
+    static constexpr int TB = N == 32 ? 2 : 4;    // tokens whose states are in registers
+    static constexpr int NS = CH / TB;
+};
+
+template <typename T>
+struct BwdArgs {
+    ChannelArgs<T> f;  // the forward call's arguments
+    Rows<const T> dy;
+    Rows<T> dx, ddt, dz, dB, dC;
+    const float *dfinal;
+    float *dA, *dD, *dbias, *dinit;
+    float4 *back;       // [unit][block][N / 4][32]: gradient for the state before (2: after) the chunk
+    int *flags;         // [unit]: 1 a sequence starts in the chunk, 2 the one at its first token ends in it
+    float *part_bc;     // [group][quad][token][2 N]
+    float *part_a;      // [slot][block][N + 2][32]
+    int quads, slots;   // quads of channel blocks per group; blocks that share a quad's chunks
+    int64_t tokens;
+};
+
+template <int N>
+__device__ __forceinline__ void zero_tile(f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
+#pragma unroll
+    for (int i = 0; i < Tile<N>::K; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile<N>::M2; ++j) v[i][j] = 0;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_decay(const ChannelArgs<T> &a, const Block &k, int lane,
+                                           f2 (&A2)[Tile<N>::K][Tile<N>::M2]) {
+    load_tile<N>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
+#pragma unroll
+    for (int i = 0; i < Tile<N>::K; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile<N>::M2; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
+}
+
+// The channel's delta before and after softplus.
+template <typename T>
+__device__ __forceinline__ float delta_of(const ChannelArgs<T> &a, float pre) {
+    return a.soft ? softplus(pre) : pre;
+}
+
+// ---------------------------------------------------------------------------
+// 1: chunk summaries.  One forward walk: with P the decay from the chunk's
+// start to t, the gradient for the state before the chunk is sum_t P g_t C_t.
+// ---------------------------------------------------------------------------
+template <int N>
+struct alignas(16) SumStage {
+    float d[8][32], u[8][32], g[8][32], bc[8][2 * N];
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __grid_constant__ BwdArgs<T> b) {
+    constexpr int K = Tile<N>::K, M = Tile<N>::M, M2 = Tile<N>::M2, TB = 8;
+    __shared__ SumStage<N> stage[kWarps];
+    const ChannelArgs<T> &a = b.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+    if (id >= (int64_t)a.units * a.nblk) return;
+    const int blk = (int)(id % a.nblk), unit = (int)(id / a.nblk);
+    SumStage<N> &sm = stage[warp];
+    const Block k = block_of(blk, a.per, a.nblk_g);
+    const int cg = lane / K, q = lane % K;
+    const bool mine = lane < k.nc;
+    const int own = k.c0 + (mine ? lane : 0);
+    const bool packed = a.seqs.start != nullptr;
+    const int row = packed ? 0 : unit / a.nchunk;
+    const int t0 = (packed ? unit : unit % a.nchunk) * a.chunk, t1 = min(a.seqs.L, t0 + a.chunk);
+    int s = row, S = 0, E = a.seqs.L;
+    if (packed) {
+        s = seq_of(a.seqs, t0);
+        S = a.seqs.start[s], E = a.seqs.start[s + 1];
+    }
+    if (blk == 0 && lane == 0) {
+        const bool starts = S == t0 || E < t1;  // (E < t1: another sequence starts at or after E, inside)
+        b.flags[unit] = (starts ? 1 : 0) | (E <= t1 ? 2 : 0);
+    }
+    f2 A2[K][M2], h[K][M2], P[K][M2], R[K][M2];
+    load_decay<T, N>(a, k, lane, A2);
+    const float bias = a.bias && mine ? a.bias[own] : 0.f;
+    const int64_t at = (int64_t)unit * a.nblk + blk;
+    int t = t0;
+    while (true) {
+        const int e = min(t1, E);
+        const bool head = t == t0 && S < t0;  // a gradient goes back to the chunk before
+        const bool tail = E > t1;             // a state goes on to the chunk after
+        if (head || tail) {
+            zero_tile<N>(h), zero_tile<N>(R);
+            if (t == S && a.init) load_tile<N>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+#pragma unroll
+                for (int j = 0; j < M2; ++j) P[i][j] = pack2(1.f, 1.f);
+            float total = 0.f;
+            for (int tb = t; tb < e; tb += TB) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    const bool in = mine && tb + j < e;
+                    float d = 0.f, x = 0.f, g = 0.f;
+                    if (in) {
+                        d = delta_of(a, to_f32(a.dt.at(row, tb + j)[own]) + bias);
+                        x = to_f32(a.x.at(row, tb + j)[own]);
+                        g = to_f32(b.dy.at(row, tb + j)[own]);
+                        if (a.z.p) g *= silu(to_f32(a.z.at(row, tb + j)[own]));
+                    }
+                    total += d;
+                    sm.d[j][lane] = d, sm.u[j][lane] = d * x, sm.g[j][lane] = g;
+                }
+#pragma unroll
+                for (int i = 0; i < TB * 2 * N / 32; ++i) {
+                    const int el = i * 32 + lane, j = el / (2 * N), w = el % (2 * N);
+                    float v = 0.f;
+                    if (tb + j < e)
+                        v = to_f32(w < N ? a.B.at(row, tb + j)[k.g * N + w] : a.C.at(row, tb + j)[k.g * N + w - N]);
+                    (&sm.bc[0][0])[el] = v;
+                }
+                __syncwarp();
+#pragma unroll 2
+                for (int j = 0; j < TB; ++j) {
+                    float d[K], u[K], g[K];
+                    f2 B[M2], C[M2];
+                    load_k<K>(&sm.d[j][cg * K], d);
+                    load_k<K>(&sm.u[j][cg * K], u);
+                    load_k<K>(&sm.g[j][cg * K], g);
+                    load_m<M>(&sm.bc[j][q * M], B);
+                    load_m<M>(&sm.bc[j][N + q * M], C);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]), gg = pack2(g[i], g[i]);
+#pragma unroll
+                        for (int m = 0; m < M2; ++m) {
+                            const f2 decay = ex2x2(mul2(A2[i][m], dd));
+                            h[i][m] = fma2(decay, h[i][m], mul2(uu, B[m]));
+                            P[i][m] = mul2(P[i][m], decay);
+                            R[i][m] = fma2(P[i][m], mul2(gg, C[m]), R[i][m]);
+                        }
+                    }
+                }
+            }
+            if (head) {
+                if (e == E && b.dfinal) {
+                    f2 f[K][M2];
+                    load_tile<N>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, f);
+#pragma unroll
+                    for (int i = 0; i < K; ++i)
+#pragma unroll
+                        for (int m = 0; m < M2; ++m) R[i][m] = fma2(P[i][m], f[i][m], R[i][m]);
+                }
+                store_lanes<N>(b.back + at * (N / 4 * 32), lane, R);
+            }
+            if (tail) store_lanes<N>(a.local + at * (N / 4 * 32), lane, h);
+            if (tail && head) a.sums[at * 32 + lane] = total;
+        }
+        if (e == t1) return;
+        t = e;
+        do ++s;
+        while (a.seqs.start[s + 1] <= t);
+        S = a.seqs.start[s], E = a.seqs.start[s + 1];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 2: the recurrences over chunks.  A thread carries one float4 of a block's
+// states over all chunks of a sequence row; blockIdx.y picks the direction.
+// ---------------------------------------------------------------------------
+template <typename T, int N>
+__global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
+    constexpr int K = Tile<N>::K, M = Tile<N>::M, AHEAD = 8;
+    const ChannelArgs<T> &a = b.f;
+    const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (id >= (int64_t)rows * a.nblk * (N / 4) * 32) return;
+    const int lane = (int)(id % 32), f = (int)(id / 32 % (N / 4));
+    const int blk = (int)(id / (32 * (N / 4)) % a.nblk), row = (int)(id / (32 * (N / 4)) / a.nblk);
+    const Block k = block_of(blk, a.per, a.nblk_g);
+    const int cg = lane / K, q = lane % K, c = cg * K + 4 * f / M;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < k.nc) A = *reinterpret_cast<const float4 *>(a.A + (int64_t)(k.c0 + c) * N + q * M + 4 * f % M);
+    A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
+    const bool fwd = blockIdx.y == 0;
+    float4 *arr = fwd ? a.local : b.back;
+    const int n = a.nchunk, u0 = row * n;
+    float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        float4 v[AHEAD];
+        float sd[AHEAD];
+        int fl[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (i0 + j >= n) break;
+            const int u = u0 + (fwd ? i0 + j : n - 1 - i0 - j);
+            const int64_t at = (int64_t)u * a.nblk + blk;
+            v[j] = arr[at * (N / 4 * 32) + f * 32 + lane];
+            sd[j] = a.sums[at * 32 + c];
+            fl[j] = b.flags[u] & (fwd ? 1 : 2);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (i0 + j >= n) break;
+            const int u = u0 + (fwd ? i0 + j : n - 1 - i0 - j);
+            arr[((int64_t)u * a.nblk + blk) * (N / 4 * 32) + f * 32 + lane] = carry;
+            if (fl[j]) {  // the chunk's own value is the whole of it
+                carry = v[j];
+            } else {
+                carry.x = fmaf(ex2(A.x * sd[j]), carry.x, v[j].x);
+                carry.y = fmaf(ex2(A.y * sd[j]), carry.y, v[j].y);
+                carry.z = fmaf(ex2(A.z * sd[j]), carry.z, v[j].z);
+                carry.w = fmaf(ex2(A.w * sd[j]), carry.w, v[j].w);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 3: the gradients inside chunks
+// ---------------------------------------------------------------------------
+template <int N>
+struct alignas(16) GradStage {
+    float4 kept[Geo<N>::NS - 1][N / 4 * 32];  // states before the 0th .. next to last TB tokens
+    float d[Geo<N>::CH][32], u[Geo<N>::CH][32];  // by token of the piece
+    float bc[Geo<N>::CH + 1][2 * N];             // by token of the chunk, turning into the warp's dB and dC; a zero row
+    float g[Geo<N>::TB][32];
+};
+
+// Sums over the lanes whose index differs in the bits from K up, of V values:
+// halving the values while there are any to halve.  Lane l ends with the
+// V / left values from `first` on.
+template <int K, int V>
+struct LaneSums {
+    static constexpr int LANES = 32 / K, LEFT = V > LANES ? V / LANES : 1;
+    static __device__ __forceinline__ int reduce(float (&v)[V], int lane) {
+        int first = 0;
+        int cnt = V;
+#pragma unroll
+        for (int bit = 16; bit >= K; bit >>= 1) {
+            const bool up = lane & bit;
+            if (cnt > 1) {
+                cnt >>= 1;
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    if (i < cnt) {
+                        const float s = up ? v[i] : v[i + cnt];
+                        v[i] = (up ? v[i + cnt] : v[i]) + __shfl_xor_sync(0xffffffffu, s, bit);
+                    }
+                }
+                if (up) first += cnt;
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+            }
+        }
+        return first;
+    }
+};
+
+template <typename T, int N, bool GATE>
+__global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_constant__ BwdArgs<T> b) {
+    constexpr int K = Tile<N>::K, M = Tile<N>::M, M2 = Tile<N>::M2, TB = Geo<N>::TB, CH = Geo<N>::CH;
+    constexpr int R = GATE ? 3 : 2;
+    extern __shared__ __align__(16) char smem[];
+    const ChannelArgs<T> &a = b.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    GradStage<N> *all = reinterpret_cast<GradStage<N> *>(smem);
+    GradStage<N> &sm = all[warp];
+    const int gq = blockIdx.x % (b.quads * (a.nblk / a.nblk_g)), slot = blockIdx.x / (b.quads * (a.nblk / a.nblk_g));
+    const int grp = gq / b.quads, quad = gq % b.quads;
+    const int in_g = quad * kWarps + warp;
+    const bool live = in_g < a.nblk_g;  // a warp without channels only joins the barriers
+    const int lives = min(kWarps, a.nblk_g - quad * kWarps);
+    const int blk = grp * a.nblk_g + (live ? in_g : 0);
+    Block k = block_of(blk, a.per, a.nblk_g);
+    if (!live) k.nc = 0;
+    const int cg = lane / K, q = lane % K;
+    const bool mine = lane < k.nc;
+    const int own = k.c0 + (mine ? lane : 0);
+    const bool packed = a.seqs.start != nullptr;
+
+    f2 A2[K][M2], dA[K][M2];
+    load_decay<T, N>(a, k, lane, A2);
+    zero_tile<N>(dA);
+    const float bias = a.bias && mine ? a.bias[own] : 0.f;
+    const float D = a.D && mine ? a.D[own] : 0.f;
+    float dD = 0.f, dbias = 0.f;
+    for (int i = lane; i < 2 * N; i += 32) sm.bc[CH][i] = 0.f;
+
+    for (int unit = slot; unit < a.units; unit += b.slots) {
+        const int row = packed ? 0 : unit / a.nchunk;
+        const int t0 = (packed ? unit : unit % a.nchunk) * CH, t1 = min(a.seqs.L, t0 + CH);
+        const int64_t at = (int64_t)unit * a.nblk + blk;
+        // the chunk's pieces of sequences, last one first
+        int s = row, S = 0, E = a.seqs.L, e = t1;
+        if (packed) {
+            s = seq_of(a.seqs, t1 - 1);
+            S = a.seqs.start[s], E = a.seqs.start[s + 1];
+        }
+        while (live) {
+            const int begin = max(t0, S), off = begin - t0, ns = (e - begin + TB - 1) / TB;
+            f2 h[K][M2], r[K][M2];
+            if (begin == S) {
+                zero_tile<N>(h);
+                if (a.init) load_tile<N>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+            } else {
+                load_lanes<N>(a.local + at * (N / 4 * 32), lane, h);
+            }
+            if (e == E) {
+                zero_tile<N>(r);
+                if (b.dfinal) load_tile<N>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
+            } else {
+                load_lanes<N>(b.back + at * (N / 4 * 32), lane, r);
+            }
+            // forward, keeping the state before every TB tokens
+            __syncwarp();
+            for (int j = 0; j < ns * TB; ++j) {
+                const bool in = mine && begin + j < e;
+                float d = 0.f, x = 0.f;
+                if (in) {
+                    d = delta_of(a, to_f32(a.dt.at(row, begin + j)[own]) + bias);
+                    x = to_f32(a.x.at(row, begin + j)[own]);
+                }
+                sm.d[j][lane] = d, sm.u[j][lane] = d * x;
+            }
+            for (int el = lane; el < (e - begin) * 2 * N; el += 32) {
+                const int j = el / (2 * N), w = el % (2 * N);
+                sm.bc[off + j][w] =
+                    to_f32(w < N ? a.B.at(row, begin + j)[k.g * N + w] : a.C.at(row, begin + j)[k.g * N + w - N]);
+            }
+            __syncwarp();
+            for (int sb = 0; sb + 1 < ns; ++sb) {
+                store_lanes<N>(sm.kept[sb], lane, h);
+#pragma unroll
+                for (int jj = 0; jj < TB; ++jj) {
+                    const int j = sb * TB + jj;
+                    float d[K], u[K];
+                    f2 B[M2];
+                    load_k<K>(&sm.d[j][cg * K], d);
+                    load_k<K>(&sm.u[j][cg * K], u);
+                    load_m<M>(&sm.bc[off + j][q * M], B);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]);
+#pragma unroll
+                        for (int m = 0; m < M2; ++m)
+                            h[i][m] = fma2(ex2x2(mul2(A2[i][m], dd)), h[i][m], mul2(uu, B[m]));
+                    }
+                }
+            }
+            // backward
+            for (int sb = ns - 1; sb >= 0; --sb) {
+                float x[TB], dy[TB], z[TB], sig[TB];
+                __syncwarp();
+#pragma unroll
+                for (int jj = 0; jj < TB; ++jj) {
+                    const int t = begin + sb * TB + jj;
+                    const bool in = mine && t < e;
+                    x[jj] = in ? to_f32(a.x.at(row, t)[own]) : 0.f;
+                    dy[jj] = in ? to_f32(b.dy.at(row, t)[own]) : 0.f;
+                    sig[jj] = in && a.soft ? sigmoid(to_f32(a.dt.at(row, t)[own]) + bias) : 1.f;
+                    float g = dy[jj];
+                    if (GATE) {
+                        z[jj] = in ? to_f32(a.z.at(row, t)[own]) : 0.f;
+                        g *= silu(z[jj]);
+                    }
+                    sm.g[jj][lane] = g;
+                }
+                __syncwarp();
+                if (sb + 1 < ns) load_lanes<N>(sm.kept[sb], lane, h);
+                f2 before[TB][K][M2], decay[TB][K][M2];
+#pragma unroll
+                for (int jj = 0; jj < TB; ++jj) {
+                    const int j = sb * TB + jj;
+                    float d[K], u[K];
+                    f2 B[M2];
+                    load_k<K>(&sm.d[j][cg * K], d);
+                    load_k<K>(&sm.u[j][cg * K], u);
+                    // (tokens past the piece: delta = g = 0 and the zero row)
+                    load_m<M>(&sm.bc[begin + j < e ? off + j : CH][q * M], B);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]);
+#pragma unroll
+                        for (int m = 0; m < M2; ++m) {
+                            before[jj][i][m] = h[i][m];
+                            decay[jj][i][m] = ex2x2(mul2(A2[i][m], dd));
+                            h[i][m] = fma2(decay[jj][i][m], h[i][m], mul2(uu, B[m]));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int jj = TB - 1; jj >= 0; --jj) {
+                    const int j = sb * TB + jj, t = begin + j;
+                    float d[K], u[K], g[K];
+                    f2 B[M2], C[M2], dBp[M2], dCp[M2];
+                    load_k<K>(&sm.d[j][cg * K], d);
+                    load_k<K>(&sm.u[j][cg * K], u);
+                    load_k<K>(&sm.g[jj][cg * K], g);
+                    const int at_bc = t < e ? off + j : CH;
+                    load_m<M>(&sm.bc[at_bc][q * M], B);
+                    load_m<M>(&sm.bc[at_bc][N + q * M], C);
+#pragma unroll
+                    for (int m = 0; m < M2; ++m) dBp[m] = 0, dCp[m] = 0;
+                    float sums[K][R];
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]), gg = pack2(g[i], g[i]);
+                        f2 du = 0, dd_A = 0, yy = 0;
+#pragma unroll
+                        for (int m = 0; m < M2; ++m) {
+                            const f2 after = jj + 1 < TB ? before[jj + 1 < TB ? jj + 1 : 0][i][m] : h[i][m];
+                            const f2 dh = fma2(gg, C[m], r[i][m]);
+                            if (GATE) yy = fma2(after, C[m], yy);
+                            dCp[m] = fma2(gg, after, dCp[m]);
+                            dBp[m] = fma2(uu, dh, dBp[m]);
+                            du = fma2(dh, B[m], du);
+                            r[i][m] = mul2(decay[jj][i][m], dh);
+                            const f2 w = mul2(r[i][m], before[jj][i][m]);
+                            dd_A = fma2(w, A2[i][m], dd_A);
+                            dA[i][m] = fma2(w, dd, dA[i][m]);
+                        }
+                        sums[i][0] = sum2(du);
+                        sums[i][1] = sum2(dd_A);
+                        if (GATE) sums[i][R - 1] = sum2(yy);
+                    }
+                    float o[R];
+                    channel_sums<K, R>(sums, lane, o);
+                    float v[2 * M];
+#pragma unroll
+                    for (int m = 0; m < M2; ++m) {
+                        unpack2(dBp[m], v[2 * m], v[2 * m + 1]);
+                        unpack2(dCp[m], v[M + 2 * m], v[M + 2 * m + 1]);
+                    }
+                    const int first = LaneSums<K, 2 * M>::reduce(v, lane);
+                    __syncwarp();  // every lane has read this token's B and C
+                    if (t < e) {
+#pragma unroll
+                        for (int i = 0; i < LaneSums<K, 2 * M>::LEFT; ++i) {
+                            const int w = first + i;  // < M: dB, else dC, of state q M + w % M
+                            sm.bc[at_bc][(w < M ? 0 : N) + q * M + w % M] = v[i];
+                        }
+                    }
+                    if (mine && t < e) {
+                        const float delta = sm.d[j][lane];
+                        const float gx = sm.g[jj][lane];
+                        const float ddl = (x[jj] * o[0] + kLn2 * o[1]) * sig[jj];
+                        b.dx.at(row, t)[own] = from_f32<T>(fmaf(delta, o[0], D * gx));
+                        b.ddt.at(row, t)[own] = from_f32<T>(ddl);
+                        dD = fmaf(gx, x[jj], dD);
+                        dbias += ddl;
+                        if (GATE) {
+                            const float y = fmaf(D, x[jj], o[R - 1]);
+                            b.dz.at(row, t)[own] = from_f32<T>(dy[jj] * y * silu_slope(z[jj], sigmoid(z[jj])));
+                        }
+                    }
+                }
+            }
+            if (begin == S && b.dinit) store_tile<N>(b.dinit + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
+            if (begin == t0) break;
+            e = begin;
+            do --s;
+            while (a.seqs.start[s] == a.seqs.start[s + 1]);
+            S = a.seqs.start[s], E = a.seqs.start[s + 1];
+        }
+        // add the block's warps
+        __syncthreads();
+        float4 *dst = reinterpret_cast<float4 *>(b.part_bc + ((int64_t)gq * b.tokens + (int64_t)row * a.seqs.L + t0) * (2 * N));
+        for (int el = threadIdx.x; el < (t1 - t0) * (2 * N / 4); el += kWarps * 32) {
+            float4 v = reinterpret_cast<const float4 *>(all[0].bc)[el];
+            for (int w = 1; w < lives; ++w) {
+                const float4 o = reinterpret_cast<const float4 *>(all[w].bc)[el];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            dst[el] = v;
+        }
+        __syncthreads();
+    }
+    if (live) {
+        float *dst = b.part_a + ((int64_t)slot * a.nblk + blk) * ((N + 2) * 32);
+        store_lanes<N>(reinterpret_cast<float4 *>(dst), lane, dA);
+        dst[N * 32 + lane] = dD;
+        dst[(N + 1) * 32 + lane] = dbias;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 4: sums over channel blocks (dB, dC) and over slots (dA, dD, ddt_bias)
+// ---------------------------------------------------------------------------
+template <typename T, int N>
+__global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_constant__ BwdArgs<T> b, int64_t bc_blocks) {
+    constexpr int K = Tile<N>::K, M = Tile<N>::M;
+    const ChannelArgs<T> &a = b.f;
+    if (blockIdx.x < bc_blocks) {
+        const int groups = a.nblk / a.nblk_g;
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= b.tokens * groups * 2 * N) return;
+        const int w = (int)(i % (2 * N)), g = (int)(i / (2 * N) % groups);
+        const int64_t token = i / (2 * N) / groups;
+        const float *src = b.part_bc + ((int64_t)g * b.quads * b.tokens + token) * (2 * N) + w;
+        float s = 0.f;
+        for (int q = 0; q < b.quads; ++q) s += src[(int64_t)q * b.tokens * (2 * N)];
+        const int row = (int)(token / a.seqs.L), t = (int)(token % a.seqs.L);
+        if (w < N)
+            b.dB.at(row, t)[g * N + w] = from_f32<T>(s);
+        else
+            b.dC.at(row, t)[g * N + w - N] = from_f32<T>(s);
+        return;
+    }
+    constexpr int each = (N + 2) * 32;
+    const int64_t i = ((int64_t)blockIdx.x - bc_blocks) * 256 + threadIdx.x;
+    if (i >= (int64_t)a.nblk * each) return;
+    const int blk = (int)(i / each), idx = (int)(i % each);
+    float s = 0.f;
+    for (int q = 0; q < b.slots; ++q) s += b.part_a[((int64_t)q * a.nblk + blk) * each + idx];
+    const Block k = block_of(blk, a.per, a.nblk_g);
+    if (idx >= N * 32) {
+        const int lane = idx % 32;
+        float *dst = idx < (N + 1) * 32 ? b.dD : b.dbias;
+        if (dst && lane < k.nc) dst[k.c0 + lane] = s;
+        return;
+    }
+    const int lane = idx / 4 % 32, el = idx / 128 * 4 + idx % 4;
+    const int c = lane / K * K + el / M, n = lane % K * M + el % M;
+    if (b.dA && c < k.nc) b.dA[(int64_t)(k.c0 + c) * N + n] = s;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int N>
+struct BwdPlan {
+    int nchunk, quads, slots;
+    int64_t units, nblk;
+    size_t offsets, flags, local, back, sums, part_bc, part_a, bytes;
+
+    BwdPlan(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) {
+        const int64_t nblk_g = (s->channels / s->ngroups + 31) / 32;
+        nblk = s->ngroups * nblk_g;
+        quads = (int)((nblk_g + kWarps - 1) / kWarps);
+        nchunk = (int)((s->seqlen + Geo<N>::CH - 1) / Geo<N>::CH);
+        units = (cu ? 1 : s->batch) * nchunk;
+        // one wave of the blocks that fit two to an SM
+        const int64_t want = (152 * 2 + s->ngroups * quads - 1) / (s->ngroups * quads);
+        slots = (int)(units < want ? units : want);
+        size_t at = 0;
+        auto take = [&at](size_t n) {
+            const size_t r = at;
+            at += align256(n);
+            return r;
+        };
+        offsets = take(cu ? sizeof(int) * (nseq + 1) : 0);
+        flags = take(sizeof(int) * units);
+        local = take(sizeof(float) * units * nblk * N * 32);
+        back = take(sizeof(float) * units * nblk * N * 32);
+        sums = take(sizeof(float) * units * nblk * 32);
+        part_bc = take(sizeof(float) * s->ngroups * quads * s->batch * s->seqlen * 2 * N);
+        part_a = take(sizeof(float) * slots * nblk * (N + 2) * 32);
+        bytes = at;
+    }
+};
+
+template <typename T, int N>
+ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq, char *ws,
+                     size_t ws_bytes, cudaStream_t st) {
+    const BwdPlan<N> p(s, cu, nseq);
+    if (p.bytes > 0 && (!ws || ws_bytes < p.bytes || !aligned(ws, 16))) return SSD_ERR_WORKSPACE;
+    ChannelArgs<T> &a = b.f;
+    timing_begin(st);
+    cudaError_t e = cudaSuccess;
+    const int64_t each = s->channels * s->dstate;
+    if (cu) {
+        int *dst = reinterpret_cast<int *>(ws + p.offsets);
+        e = write_offsets(cu, nseq, dst, st);
+        if (e != cudaSuccess) return status_of(e);
+        a.seqs.start = dst;
+        bool empty = false;
+        for (int64_t i = 0; i < nseq && !empty; ++i) empty = cu[i] == cu[i + 1];
+        if (empty && b.dinit) e = pass_empty_states(dst, nseq, each, b.dfinal, b.dinit, st);
+    } else if (s->seqlen == 0 && b.dinit && nseq > 0) {
+        e = pass_empty_states(nullptr, nseq, each, b.dfinal, b.dinit, st);
+    }
+    if (e != cudaSuccess) return status_of(e);
+    a.chunk = Geo<N>::CH, a.nchunk = p.nchunk, a.units = (int)p.units;
+    a.local = reinterpret_cast<float4 *>(ws + p.local);
+    a.sums = reinterpret_cast<float *>(ws + p.sums);
+    b.back = reinterpret_cast<float4 *>(ws + p.back);
+    b.flags = reinterpret_cast<int *>(ws + p.flags);
+    b.part_bc = reinterpret_cast<float *>(ws + p.part_bc);
+    b.part_a = reinterpret_cast<float *>(ws + p.part_a);
+    b.quads = p.quads, b.slots = p.slots;
+    b.tokens = s->batch * s->seqlen;
+    if (p.units > 0) {
+        const int rows = cu ? 1 : (int)s->batch;
+        const int64_t warps = (p.units * p.nblk + kWarps - 1) / kWarps;
+        const int64_t threads = (int64_t)rows * p.nblk * (N / 4) * 32;
+        const int64_t grads = (int64_t)s->ngroups * p.quads * p.slots;
+        if (warps > 0x7FFFFFFF || threads / 128 >= 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+        if (p.nchunk > 1) {
+            channel_bwd_chunk_kernel<T, N><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
+            timing_mark(st, "channel_bwd_chunk");
+            channel_bwd_pass_kernel<T, N><<<dim3((unsigned)((threads + 127) / 128), 2), 128, 0, st>>>(b, rows);
+            timing_mark(st, "channel_bwd_pass");
+        }
+        const size_t smem = sizeof(GradStage<N>) * kWarps;
+        auto kernel = a.z.p ? channel_bwd_kernel<T, N, true> : channel_bwd_kernel<T, N, false>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return status_of(e);
+        kernel<<<(unsigned)grads, kWarps * 32, smem, st>>>(b);
+        timing_mark(st, "channel_bwd");
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return status_of(e);
+    }
+    const int64_t bc = (b.tokens * s->ngroups * 2 * N + 255) / 256, ab = (p.nblk * (N + 2) * 32 + 255) / 256;
+    if (bc + ab > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+    channel_bwd_reduce_kernel<T, N><<<(unsigned)(bc + ab), 256, 0, st>>>(b, bc);
+    timing_mark(st, "channel_bwd_reduce");
+    return status_of(cudaGetLastError());
+}
+
+template <typename T>
+ssd_status_t bwd_typed(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq, const ssd_rows_t *dy,
+                       const ssd_channel_inputs_t *in, const float *dfinal, const ssd_channel_grads_t *out, void *ws,
+                       size_t ws_bytes, cudaStream_t st) {
+    BwdArgs<T> b{};
+    b.f = channel_args<T>(s, in, nseq);
+    b.dy = rows_of<const T>(*dy);
+    b.dx = rows_of<T>(out->dx), b.ddt = rows_of<T>(out->ddt), b.dz = rows_of<T>(out->dz);
+    b.dB = rows_of<T>(out->dB), b.dC = rows_of<T>(out->dC);
+    b.dfinal = dfinal;
+    b.dA = out->dA, b.dD = out->dD, b.dbias = out->ddt_bias, b.dinit = out->dinit_state;
+    char *w = static_cast<char *>(ws);
+    if (s->dstate == 8) return run_bwd<T, 8>(b, s, cu, nseq, w, ws_bytes, st);
+    if (s->dstate == 16) return run_bwd<T, 16>(b, s, cu, nseq, w, ws_bytes, st);
+    return run_bwd<T, 32>(b, s, cu, nseq, w, ws_bytes, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" {
+
+size_t ssd_channel_scan_bwd_workspace_size(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq) {
+    using namespace ssd;
+    if (check_channel(shape, cu_seqlens, nseq) != SSD_OK) return 0;
+    if (shape->dstate == 8) return BwdPlan<8>(shape, cu_seqlens, nseq).bytes;
+    if (shape->dstate == 16) return BwdPlan<16>(shape, cu_seqlens, nseq).bytes;
+    return BwdPlan<32>(shape, cu_seqlens, nseq).bytes;
+}
+
+ssd_status_t ssd_channel_scan_bwd(const ssd_channel_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                  const ssd_rows_t *dy, const ssd_channel_inputs_t *in, const float *dfinal_state,
+                                  const ssd_channel_grads_t *out, void *workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+    using namespace ssd;
+    const ssd_status_t st = check_channel(shape, cu_seqlens, nseq);
+    if (st != SSD_OK) return st;
+    if (!cu_seqlens) nseq = shape->batch;
+    const bool rows = shape->seqlen > 0 && nseq > 0;
+    if (!channel_inputs_ok(shape, in, rows) || !dy || !out || !aligned(dfinal_state, 16) || !aligned(out->dA, 4) ||
+        !aligned(out->dD, 4) || !aligned(out->ddt_bias, 4) || !aligned(out->dinit_state, 16))
+        return SSD_ERR_INVALID_ARG;
+    if (rows) {
+        const size_t es = dtype_size(shape->dtype);
+        const int64_t b = shape->batch, L = shape->seqlen, gn = shape->ngroups * shape->dstate;
+        if (!rows_in_ok(*dy, es) || !rows_out_ok(out->dx, es, b, L, shape->channels) ||
+            !rows_out_ok(out->ddt, es, b, L, shape->channels) || !rows_out_ok(out->dB, es, b, L, gn) ||
+            !rows_out_ok(out->dC, es, b, L, gn))
+            return SSD_ERR_INVALID_ARG;
+        if (in->z.data && !rows_out_ok(out->dz, es, b, L, shape->channels)) return SSD_ERR_INVALID_ARG;
+    }
+    return shape->dtype == SSD_DTYPE_BF16
+               ? bwd_typed<bf16>(shape, cu_seqlens, nseq, dy, in, dfinal_state, out, workspace, workspace_bytes, stream)
+               : bwd_typed<float>(shape, cu_seqlens, nseq, dy, in, dfinal_state, out, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
