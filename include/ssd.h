@@ -340,8 +340,8 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_shape_t *shape, const void *x, co
  * selective scan with a decay per channel and state, and the block norm.
  *
  * Rows.  Token-major operands are given as ssd_rows_t: element (b, t, c) is
- * data[b * batch_stride + t * row_stride + c], strides in elements, c
- * contiguous.  So a column slice of a wider projection is read (or a slice
+ * data[b * batch_stride + t * row_stride + c], strides in elements (row
+ * strides below 2^31), c contiguous.  So a column slice of a wider projection is read (or a slice
  * of its gradient written) in place.  `data` needs only its element type's
  * alignment; 16-byte aligned rows (pointer and strides) take the vector
  * path.  Rows that are written must not overlap each other or any operand.
@@ -449,6 +449,39 @@ SSD_API ssd_status_t ssd_channel_scan_bwd(const ssd_channel_shape_t *shape, cons
                                           size_t workspace_bytes, cudaStream_t stream);
 SSD_API ssd_status_t ssd_channel_scan_step(const ssd_channel_shape_t *shape, const ssd_channel_inputs_t *in,
                                            float *state, const ssd_rows_t *y, cudaStream_t stream);
+
+/*
+ * Block norm: the RMS norm before or after a block, fused with its gate and
+ * the scaled residual.  Per row of `dim` columns, in groups of group_size:
+ *   v = z && !gate_after ? x silu(z) : x
+ *   s = residual + scale v      (scale NULL: 1; residual NULL: 0)
+ *   out = s / sqrt(mean_group(s^2) + eps) * weight  (times silu(z) with gate_after)
+ * and residual_out = s (which may be the residual itself).  x, z, out [rows, dim] T; residual, residual_out in
+ * residual_dtype (fp32, or T); weight, scale [dim] fp32.  Rows use row_stride
+ * (batch_stride is ignored).  The norm is of s before it is rounded to
+ * residual_dtype.  Supported: group_size up to 32768.
+ * ssd_block_norm_bwd: dout, and dresidual_out (NULL: zero) for the sum's own
+ * use elsewhere -> dx, dz, dresidual, dweight, dscale.  With a residual it
+ * takes the stored sum, residual_out, in the residual's place; x is then read
+ * only for the gate before and the scale.  dweight, dscale may be NULL.
+ */
+typedef struct {
+    int64_t rows, dim, group_size;
+    float eps;
+    ssd_dtype_t dtype, residual_dtype;
+    int gate_after;
+} ssd_norm_shape_t;
+
+SSD_API ssd_status_t ssd_block_norm_fwd(const ssd_norm_shape_t *shape, const ssd_rows_t *x, const float *weight,
+                                        const ssd_rows_t *z, const ssd_rows_t *residual, const float *scale,
+                                        const ssd_rows_t *out, const ssd_rows_t *residual_out, cudaStream_t stream);
+SSD_API size_t ssd_block_norm_bwd_workspace_size(const ssd_norm_shape_t *shape);
+SSD_API ssd_status_t ssd_block_norm_bwd(const ssd_norm_shape_t *shape, const ssd_rows_t *dout, const ssd_rows_t *x,
+                                        const float *weight, const ssd_rows_t *z, const float *scale,
+                                        const ssd_rows_t *residual_out, const ssd_rows_t *dresidual_out,
+                                        const ssd_rows_t *dx, float *dweight, const ssd_rows_t *dz,
+                                        const ssd_rows_t *dresidual, float *dscale, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Launch timing (instrumentation; the pages have no counterpart).  While

@@ -37,7 +37,8 @@ EXPORTED = ("ssd_status_string", "ssd_abi_version", "ssd_fwd_workspace_size", "s
             "ssd_fwd_varlen_workspace_size", "ssd_fwd_varlen", "ssd_fwd_quadratic",
             "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step",
             "ssd_channel_scan_workspace_size", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd_workspace_size",
-            "ssd_channel_scan_bwd", "ssd_channel_scan_step")
+            "ssd_channel_scan_bwd", "ssd_channel_scan_step",
+            "ssd_block_norm_fwd", "ssd_block_norm_bwd_workspace_size", "ssd_block_norm_bwd")
 
 
 class ssd_shape_t(ctypes.Structure):
@@ -451,8 +452,9 @@ def launch_times_ms() -> list:
 
 
 from ._layer import (  # noqa: E402  (built on the helpers above)
-    ssd_channel_scan_bwd, ssd_channel_scan_fwd, ssd_channel_scan_step, ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step)
+    ssd_block_norm_bwd, ssd_block_norm_fwd, ssd_channel_scan_bwd, ssd_channel_scan_fwd, ssd_channel_scan_step,
+    ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step)
 
-__all__ = ["ssd_channel_scan_fwd", "ssd_channel_scan_bwd", "ssd_channel_scan_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
+__all__ = ["ssd_block_norm_fwd", "ssd_block_norm_bwd", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd", "ssd_channel_scan_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
            "ssd_state_passing", "ssd_chunk_scan", "selective_scan_fwd", "ssd_shape_t", "SSDError",
            "load_library", "status_string", "EXPORTED", "LIB_PATH"]

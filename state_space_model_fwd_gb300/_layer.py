@@ -1,5 +1,5 @@
-"""Binding of the operators around the scan: the short causal convolution and
-the channel scan.
+"""Binding of the operators around the scan: the short causal convolution, the
+channel scan and the block norm.
 
 Token-major operands (x, y, gradients) may be strided views whose last
 dimension is contiguous, such as column slices of a projection's rows; states
@@ -46,6 +46,12 @@ class _channel_grads_t(ctypes.Structure):
                 ("dinit_state", ctypes.c_void_p)]
 
 
+class _norm_shape_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("group_size", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("gate_after", ctypes.c_int)]
+
+
 def declare(lib):
     """Declare this module's entry points on the loaded library."""
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
@@ -57,11 +63,15 @@ def declare(lib):
     for name in ("ssd_channel_scan_workspace_size", "ssd_channel_scan_bwd_workspace_size"):
         getattr(lib, name).argtypes = [vp, vp, i64]
         getattr(lib, name).restype = sz
+    lib.ssd_block_norm_fwd.argtypes = [vp] * 9
+    lib.ssd_block_norm_bwd_workspace_size.argtypes = [vp]
+    lib.ssd_block_norm_bwd_workspace_size.restype = sz
+    lib.ssd_block_norm_bwd.argtypes = [vp] * 14 + [sz, vp]
     lib.ssd_channel_scan_fwd.argtypes = [vp, vp, i64] + [vp] * 4 + [sz, vp]
     lib.ssd_channel_scan_bwd.argtypes = [vp, vp, i64] + [vp] * 5 + [sz, vp]
     lib.ssd_channel_scan_step.argtypes = [vp] * 5
     for name in ("ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd",
-                 "ssd_channel_scan_step"):
+                 "ssd_channel_scan_step", "ssd_block_norm_fwd", "ssd_block_norm_bwd"):
         getattr(lib, name).restype = i32
 
 
@@ -384,3 +394,117 @@ def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state
         _raise("ssd_channel_scan_step", lib.ssd_channel_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp,
                                                                   ctypes.byref(yr), _stream_of(x, stream)))
     return y
+
+
+# ---------------------------------------------------------------------------
+# block norm
+# ---------------------------------------------------------------------------
+def _norm_rows(t, name, dtype, shape, dev):
+    """ssd_rows_t of a [..., dim] tensor whose rows lie at one stride; None
+    for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    rs = want = 0
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if want == 0:
+            rs, want = st[i], st[i] * shape[i]
+        elif st[i] != want:
+            raise ValueError(f"{name}'s rows must lie at one stride")
+        else:
+            want *= shape[i]
+    return _rows_t(t.data_ptr(), 0, rs)
+
+
+def _ref(r):
+    return None if r is None else ctypes.byref(r)
+
+
+def _norm_shape(x, group_size, eps, residual, gate_after):
+    code = _code(x)
+    if x.dim() < 2:
+        raise ValueError("x must be [..., dim]")
+    dim = x.shape[-1]
+    rcode = code if residual is None else _code(residual, "residual")
+    return _norm_shape_t(x.numel() // dim if dim else 0, dim, group_size or dim, eps, code, rcode, 1 if gate_after else 0)
+
+
+def ssd_block_norm_fwd(x, weight, *, z=None, residual=None, scale=None, eps=1e-5, group_size=None, gate_after=False,
+                       out=None, residual_out=None, stream=None):
+    """RMS norm before or after a block, with its gate and scaled residual:
+
+        v = x * silu(z)  (x without z or with gate_after)
+        s = residual + scale * v
+        out = s / sqrt(mean(s^2) + eps) * weight  (* silu(z) with gate_after)
+
+    the mean over groups of ``group_size`` columns (all by default).  x, z
+    [..., dim]; residual the same shape in x's type or fp32; weight, scale
+    [dim] fp32.  Returns ``(out, residual_out)``, residual_out = s in the
+    residual's type (None without a residual)."""
+    lib = _lib()
+    shape = _norm_shape(x, group_size, eps, residual, gate_after)
+    dev, ty, full, dim = x.device, x.dtype, x.shape, x.shape[-1]
+    xr = _norm_rows(x, "x", ty, full, dev)
+    zr = _norm_rows(z, "z", ty, full, dev)
+    wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
+    if out is None:
+        out = torch.empty(full, device=dev, dtype=ty)
+    outr = _norm_rows(out, "out", ty, full, dev)
+    rr = ror = None
+    if residual is not None:
+        rr = _norm_rows(residual, "residual", residual.dtype, full, dev)
+        if residual_out is None:
+            residual_out = torch.empty(full, device=dev, dtype=residual.dtype)
+        ror = _norm_rows(residual_out, "residual_out", residual.dtype, full, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    with torch.cuda.device(dev):
+        _raise("ssd_block_norm_fwd", lib.ssd_block_norm_fwd(ctypes.byref(shape), _ref(xr), wp, _ref(zr), _ref(rr), sp,
+                                                            _ref(outr), _ref(ror), _stream_of(x, stream)))
+    return out, residual_out
+
+
+def ssd_block_norm_bwd(dout, x, weight, *, z=None, scale=None, residual_out=None, dresidual_out=None, eps=1e-5,
+                       group_size=None, gate_after=False, workspace=None, stream=None):
+    """Gradient of ssd_block_norm_fwd.  ``residual_out`` is the sum the forward
+    call returned (where it had a residual) and ``dresidual_out`` the gradient
+    of its other uses (zero without it).  Returns ``(dx, dweight, dz,
+    dresidual, dscale)``, None where the input was None."""
+    lib = _lib()
+    shape = _norm_shape(x, group_size, eps, residual_out, gate_after)
+    dev, ty, full, dim = x.device, x.dtype, x.shape, x.shape[-1]
+    gr, xr = _norm_rows(dout, "dout", ty, full, dev), _norm_rows(x, "x", ty, full, dev)
+    if gr is None:
+        raise TypeError("dout must be a CUDA tensor")
+    zr = _norm_rows(z, "z", ty, full, dev)
+    wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
+    dx = torch.empty(full, device=dev, dtype=ty)
+    dz = None if z is None else torch.empty(full, device=dev, dtype=ty)
+    dweight = torch.empty((dim,), device=dev, dtype=_F32)
+    dscale = None if scale is None else torch.empty((dim,), device=dev, dtype=_F32)
+    sr = dsr = drr = dres = None
+    if residual_out is not None:
+        sr = _norm_rows(residual_out, "residual_out", residual_out.dtype, full, dev)
+        dsr = _norm_rows(dresidual_out, "dresidual_out", residual_out.dtype, full, dev)
+        dres = torch.empty(full, device=dev, dtype=residual_out.dtype)
+        drr = _norm_rows(dres, "dresidual", residual_out.dtype, full, dev)
+    elif dresidual_out is not None:
+        raise ValueError("dresidual_out needs residual_out")
+    dxr, dzr = _norm_rows(dx, "dx", ty, full, dev), _norm_rows(dz, "dz", ty, full, dev)
+    with torch.cuda.device(dev):
+        ws = _workspace(workspace, lib.ssd_block_norm_bwd_workspace_size(ctypes.byref(shape)), dev)
+        _raise("ssd_block_norm_bwd", lib.ssd_block_norm_bwd(
+            ctypes.byref(shape), _ref(gr), _ref(xr), wp, _ref(zr), sp, _ref(sr), _ref(dsr), _ref(dxr),
+            dweight.data_ptr(), _ref(dzr), _ref(drr), None if dscale is None else dscale.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    return dx, dweight, dz, dres, dscale

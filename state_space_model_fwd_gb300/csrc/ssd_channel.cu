@@ -15,175 +15,195 @@ namespace ssd {
 namespace {
 
 constexpr int kTB = 8;     // tokens staged at a time
-constexpr int kWarps = 4;  // warps per block
+constexpr int kWarps = 4;  // warps per block, one for each of an SM's schedulers
 
-template <int N>
-struct alignas(16) Stage {
-    float d[kTB][32], u[kTB][32], bc[kTB][2 * N];
-};
-
-// What a lane has in flight for the next kTB tokens: its own channel's
-// values and its share of their B and C.
-template <typename T, int N, bool FULL>
+// What a lane has in flight for the next kTB tokens: its channel's values and
+// its share of B and C.  A lane without a channel reads the block's first one:
+// its states have A = 0 and are never stored.
+template <typename T, int N, bool FULL, bool GATE>
 struct Ahead {
     static constexpr int NB = kTB * 2 * N / 32;
-    T x[kTB], dt[kTB], z[FULL ? kTB : 1], bc[NB];
+    T x[kTB], dt[kTB], z[GATE ? kTB : 1], bc[NB];
 
-    __device__ __forceinline__ void load(const ChannelArgs<T> &a, const Block &k, int row, int t, int n, int lane) {
-        const bool mine = lane < k.nc;
-        const int c = k.c0 + lane;
+    __device__ __forceinline__ void load(const T *px, const T *pdt, const T *pz, const T *pb, const T *pc,
+                                         const ChannelArgs<T> &a, int n, int lane) {
+        if (n >= kTB) {
 #pragma unroll
-        for (int j = 0; j < kTB; ++j) {
-            const bool in = j < n && mine;
-            x[j] = in ? a.x.at(row, t + j)[c] : from_f32<T>(0.f);
-            dt[j] = in ? a.dt.at(row, t + j)[c] : from_f32<T>(0.f);
-            if (FULL && a.z.p) z[FULL ? j : 0] = in ? a.z.at(row, t + j)[c] : from_f32<T>(0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int e = i * 32 + lane, j = e / (2 * N), w = e % (2 * N);
-            T v = from_f32<T>(0.f);
-            if (j < n && (FULL || w < N))
-                v = w < N ? a.B.at(row, t + j)[k.g * N + w] : a.C.at(row, t + j)[k.g * N + w - N];
-            bc[i] = v;
-        }
-    }
-};
-
-// FULL: outputs; otherwise only the chunk's end state and sum of deltas.
-template <typename T, int N, bool FULL>
-__global__ void __launch_bounds__(kWarps * 32) channel_fwd_kernel(const __grid_constant__ ChannelArgs<T> a) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M, M2 = Tile<N>::M2;
-    __shared__ Stage<N> stage[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
-    if (id >= (int64_t)a.units * a.nblk) return;  // whole warps; only warp barriers below
-    const int blk = (int)(id % a.nblk), unit = (int)(id / a.nblk);
-    Stage<N> &sm = stage[warp];
-    const Block k = block_of(blk, a.per, a.nblk_g);
-    const int cg = lane / K, q = lane % K;
-    const bool mine = lane < k.nc;
-    const int own = k.c0 + (mine ? lane : 0);
-
-    f2 A2[K][M2], h[K][M2];
-    load_tile<N>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-#pragma unroll
-        for (int j = 0; j < M2; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
-    const float bias = a.bias && mine ? a.bias[own] : 0.f;
-    const float D = FULL && a.D && mine ? a.D[own] : 0.f;
-
-    // this unit's tokens
-    const bool packed = a.seqs.start != nullptr;
-    const int seq0 = packed ? 0 : unit / a.nchunk, row = seq0;
-    const int c_in = packed ? unit : unit % a.nchunk;
-    const int t0 = c_in * a.chunk, t1 = min(a.seqs.L, t0 + a.chunk);
-    int s = seq0, S = 0, E = a.seqs.L, t = t0;
-    if (packed) {
-        s = seq_of(a.seqs, FULL ? t0 : t1 - 1);
-        S = a.seqs.start[s], E = a.seqs.start[s + 1];
-        if (!FULL) t = max(t, S);  // only what reaches the chunk's end
-    }
-    if (!FULL && E <= t1) return;  // nothing passes to the next chunk
-
-    while (true) {
-        const int e = min(t1, E);
-        // the state before token t
-        if (t == S) {
-            if (a.init) {
-                load_tile<N>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
-            } else {
-#pragma unroll
-                for (int i = 0; i < K; ++i)
-#pragma unroll
-                    for (int j = 0; j < M2; ++j) h[i][j] = 0;
-            }
-        } else if (FULL) {
-            const int first = packed ? S / a.chunk : unit - c_in;
-            load_lanes<N>(a.local + ((int64_t)first * a.nblk + blk) * (N / 4 * 32), lane, h);
-            for (int c = first + 1; c < unit; ++c) {
-                const int64_t at = (int64_t)c * a.nblk + blk;
-                f2 l[K][M2];
-                float sd[K];
-                load_lanes<N>(a.local + at * (N / 4 * 32), lane, l);
-                load_k<K>(a.sums + at * 32 + cg * K, sd);
-#pragma unroll
-                for (int i = 0; i < K; ++i)
-#pragma unroll
-                    for (int j = 0; j < M2; ++j)
-                        h[i][j] = fma2(ex2x2(mul2(A2[i][j], pack2(sd[i], sd[i]))), h[i][j], l[i][j]);
+            for (int j = 0; j < kTB; ++j) {
+                x[j] = px[a.x.step(j)];
+                dt[j] = pdt[a.dt.step(j)];
+                if (GATE) z[GATE ? j : 0] = pz[a.z.step(j)];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < K; ++i)
+            for (int j = 0; j < kTB; ++j) {
+                x[j] = j < n ? px[a.x.step(j)] : from_f32<T>(0.f);
+                dt[j] = j < n ? pdt[a.dt.step(j)] : from_f32<T>(0.f);
+                if (GATE) z[GATE ? j : 0] = j < n ? pz[a.z.step(j)] : from_f32<T>(0.f);
+            }
+        }
 #pragma unroll
-                for (int j = 0; j < M2; ++j) h[i][j] = 0;
+        for (int i = 0; i < NB; ++i) {
+            const int j = (i * 32 + lane) / (2 * N);
+            const bool is_b = (i * 32 + lane) % (2 * N) < N;
+            bc[i] = from_f32<T>(0.f);
+            if (j < n && (FULL || is_b)) bc[i] = is_b ? pb[a.B.step(j)] : pc[a.C.step(j)];
+        }
+    }
+};
+
+// A lane is a channel: its N states, their decay rates and its delta stay in
+// registers, nothing is summed over lanes, and B and C come from shared
+// memory as broadcasts (N / 2 reads of 16 bytes a token, which bounds how
+// fast this can go at 4 N cycles an SM for 32 channels; the arithmetic takes
+// about as long).  A square tile of channels and states a lane reads a third
+// of that but pays 40 instructions a token to stage delta and to transpose
+// the sums: 1.06 ms against 1.26-1.77 for 8 x 4096 x 5120.
+//
+// FULL: outputs; otherwise only the chunk's end state and sum of deltas.  The
+// warps of a block share nothing.
+template <typename T, int N, bool FULL, bool GATE>
+__global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __grid_constant__ ChannelArgs<T> a) {
+    using G = Tile<N, 1, 1>;
+    constexpr int N2 = N / 2, E = N / 4;
+    __shared__ __align__(16) float stage[kWarps][kTB][2 * N];
+    const int lane = threadIdx.x % 32;
+    auto &sm = stage[threadIdx.x / 32];
+    const int64_t warp = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+    if (warp >= (FULL ? a.whole : 0) + (int64_t)a.cut * a.nchunk) return;  // (only warp barriers below)
+    // a block row is a channel block of a sequence row; those from a.whole on
+    // are cut into chunks
+    const bool packed = a.seqs.start != nullptr;
+    const bool whole = FULL && warp < a.whole;
+    const int id = (int)warp - (FULL ? a.whole : 0);
+    const int r = whole ? 0 : id % a.cut, c_in = whole ? 0 : id / a.cut, brow = whole ? (int)warp : a.whole + r;
+    const int blk = brow % a.nblk, row = brow / a.nblk;
+    const Block k = block_of(blk, a.per, a.nblk_g, 32);
+    const bool mine = lane < k.nc;
+    const int own = k.c0 + (mine ? lane : 0);
+
+    typename G::Regs A2, h;
+    load_tile<G>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
+#pragma unroll
+    for (int m = 0; m < N2; ++m) A2[0][m] = mul2(A2[0][m], pack2(kLog2e, kLog2e));
+    const float bias = a.bias ? a.bias[own] : 0.f;
+    const float D = FULL && a.D ? a.D[own] : 0.f;
+
+    // this warp's tokens
+    const int t0 = c_in * a.chunk, t1 = whole ? a.seqs.L : min(a.seqs.L, t0 + a.chunk);
+    int s = row, S0 = 0, S1 = a.seqs.L, t = t0;
+    if (packed) {
+        s = seq_of(a.seqs, FULL ? t0 : t1 - 1);
+        S0 = a.seqs.start[s], S1 = a.seqs.start[s + 1];
+        if (!FULL) t = max(t, S0);  // only what reaches the chunk's end
+    }
+    if (!FULL && S1 <= t1) return;  // nothing passes to the next chunk
+    // (pointers may come to stand past the last token: they are read through only where a token is)
+    const T *px = a.x.at(row, t) + own, *pdt = a.dt.at(row, t) + own;
+    const T *pz = GATE ? a.z.at(row, t) + own : nullptr;
+    const T *pb = a.B.at(row, t) + k.g * N + lane % N, *pc = a.C.at(row, t) + k.g * N + lane % N;
+    T *py = FULL ? a.y.at(row, t) + own : nullptr;
+
+    while (true) {
+        const int e = min(t1, S1);
+        Ahead<T, N, FULL, GATE> nxt;
+        nxt.load(px, pdt, pz, pb, pc, a, e - t, lane);
+        // the state before token t
+        zero_tile<G>(h);
+        if (t == S0) {
+            if (a.init) load_tile<G>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+        } else if (FULL) {
+            const int first = S0 / a.chunk;
+            load_lanes<G>(a.local + ((int64_t)first * a.cut + r) * (E * 32), lane, h);
+#pragma unroll 4
+            for (int c = first + 1; c < c_in; ++c) {
+                const int64_t at = (int64_t)c * a.cut + r;
+                typename G::Regs l;
+                load_lanes<G>(a.local + at * (E * 32), lane, l);
+                const float sd = a.sums[at * 32 + lane];
+#pragma unroll
+                for (int m = 0; m < N2; ++m)
+                    h[0][m] = fma2(ex2x2(mul2(A2[0][m], pack2(sd, sd))), h[0][m], l[0][m]);
+            }
         }
         float total = 0.f;
-        Ahead<T, N, FULL> nxt;
-        nxt.load(a, k, row, t, e - t, lane);
         for (; t < e; t += kTB) {
-            float x[kTB], z[kTB];
-            __syncwarp();
+            const int n = e - t;
+            // (straight-line code from here to the stores, so that the tokens' chains overlap)
+            float d[kTB], x[kTB], z[GATE ? kTB : 1], o[kTB];
 #pragma unroll
             for (int j = 0; j < kTB; ++j) {
-                // tokens past the end have delta = 0: they leave the state alone
-                float d = to_f32(nxt.dt[j]) + bias;
-                if (a.soft) d = softplus(d);
-                if (t + j >= e || !mine) d = 0.f;
+                d[j] = to_f32(nxt.dt[j]) + bias;
                 x[j] = to_f32(nxt.x[j]);
-                if (FULL && a.z.p) z[j] = to_f32(nxt.z[FULL ? j : 0]);
-                if (!FULL) total += d;
-                sm.d[j][lane] = d;
-                sm.u[j][lane] = d * x[j];
+                if (GATE) z[GATE ? j : 0] = to_f32(nxt.z[GATE ? j : 0]);
             }
+            if (a.soft) {
 #pragma unroll
-            for (int i = 0; i < Ahead<T, N, FULL>::NB; ++i) (&sm.bc[0][0])[i * 32 + lane] = to_f32(nxt.bc[i]);
+                for (int j = 0; j < kTB; ++j) d[j] = softplus(d[j]);
+            }
+            if (n < kTB) {  // tokens past the end leave the state alone
+#pragma unroll
+                for (int j = 0; j < kTB; ++j) d[j] = j < n ? d[j] : 0.f;
+            }
+            if (!FULL) {
+#pragma unroll
+                for (int j = 0; j < kTB; ++j) total += d[j];
+            }
             __syncwarp();
-            if (t + kTB < e) nxt.load(a, k, row, t + kTB, e - t - kTB, lane);
+#pragma unroll
+            for (int i = 0; i < Ahead<T, N, FULL, GATE>::NB; ++i) (&sm[0][0])[i * 32 + lane] = to_f32(nxt.bc[i]);
+            __syncwarp();
+            px += a.x.step(kTB), pdt += a.dt.step(kTB), pb += a.B.step(kTB), pc += a.C.step(kTB);
+            if (GATE) pz += a.z.step(kTB);
+            if (n > kTB) nxt.load(px, pdt, pz, pb, pc, a, n - kTB, lane);
 #pragma unroll
             for (int j = 0; j < kTB; ++j) {
-                float d[K], u[K];
-                f2 B[M2], C[M2];
-                load_k<K>(&sm.d[j][cg * K], d);
-                load_k<K>(&sm.u[j][cg * K], u);
-                load_m<M>(&sm.bc[j][q * M], B);
-                if (FULL) load_m<M>(&sm.bc[j][N + q * M], C);
-                float p[K][1];
+                f2 acc[2] = {0, 0};
+                const f2 dd = pack2(d[j], d[j]), uu = pack2(d[j] * x[j], d[j] * x[j]);
 #pragma unroll
-                for (int i = 0; i < K; ++i) {
-                    const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]);
-                    f2 acc = 0;
-#pragma unroll
-                    for (int m = 0; m < M2; ++m) {
-                        const f2 decay = ex2x2(mul2(A2[i][m], dd));
-                        h[i][m] = fma2(decay, h[i][m], mul2(uu, B[m]));
-                        if (FULL) acc = fma2(h[i][m], C[m], acc);
+                for (int m = 0; m < N2; m += 2) {
+                    const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sm[j][2 * m]);
+                    h[0][m] = fma2(ex2x2(mul2(A2[0][m], dd)), h[0][m], mul2(uu, B.x));
+                    h[0][m + 1] = fma2(ex2x2(mul2(A2[0][m + 1], dd)), h[0][m + 1], mul2(uu, B.y));
+                    if (FULL) {
+                        const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sm[j][N + 2 * m]);
+                        acc[0] = m ? fma2(h[0][m], C.x, acc[0]) : mul2(h[0][m], C.x);
+                        acc[1] = m ? fma2(h[0][m + 1], C.y, acc[1]) : mul2(h[0][m + 1], C.y);
                     }
-                    p[i][0] = sum2(acc);
                 }
                 if (FULL) {
-                    float y[1];
-                    channel_sums<K, 1>(p, lane, y);
-                    float o = fmaf(D, x[j], y[0]);
-                    if (a.z.p) o *= silu(z[j]);
-                    if (mine && t + j < e) a.y.at(row, t + j)[own] = from_f32<T>(o);
+                    o[j] = fmaf(D, x[j], sum2(acc[0]) + sum2(acc[1]));
+                    if (GATE) o[j] *= silu(z[GATE ? j : 0]);
                 }
             }
+            if (FULL && mine) {
+                if (n >= kTB) {
+#pragma unroll
+                    for (int j = 0; j < kTB; ++j) py[a.y.step(j)] = from_f32<T>(o[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kTB; ++j)
+                        if (j < n) py[a.y.step(j)] = from_f32<T>(o[j]);
+                }
+            }
+            if (FULL) py += a.y.step(kTB);
         }
         if (!FULL) {
-            const int64_t at = (int64_t)unit * a.nblk + blk;
-            store_lanes<N>(a.local + at * (N / 4 * 32), lane, h);
+            const int64_t at = (int64_t)c_in * a.cut + r;
+            store_lanes<G>(a.local + at * (E * 32), lane, h);
             a.sums[at * 32 + lane] = total;
             return;
         }
-        if (e == E && a.fin) store_tile<N>(a.fin + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+        if (e == S1 && a.fin) store_tile<G>(a.fin + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
         if (e == t1) return;
+        const int over = t - e;  // the last step went past the piece
+        px -= a.x.step(over), pdt -= a.dt.step(over), pb -= a.B.step(over), pc -= a.C.step(over);
+        py -= a.y.step(over);
+        if (GATE) pz -= a.z.step(over);
         t = e;
         do ++s;
         while (a.seqs.start[s + 1] <= t);
-        S = a.seqs.start[s], E = a.seqs.start[s + 1];
+        S0 = a.seqs.start[s], S1 = a.seqs.start[s + 1];
     }
 }
 
@@ -296,32 +316,42 @@ bool channel_inputs_ok(const ssd_channel_shape_t *s, const ssd_channel_inputs_t 
 
 namespace {
 
-// Chunks: one per sequence where the warps suffice, otherwise enough for
-// about eight warps an SM, of at least 64 tokens.
+// How block rows (a channel block of a sequence row, one warp each) are cut.
+// An SM has four warp schedulers and the kernel two warps for each (its
+// registers: with 168 instead of 255 a third warp fits, but one warp's tokens
+// overlap less: 1097 against 790 us at 8 x 4096 x 5120).  As many block rows
+// as give every scheduler the same number run whole; the rest, which would
+// set the time on a few schedulers, are cut into chunks that spread over all.
+// With fewer than two a scheduler all are cut, in chunks of at least 64
+// tokens.
+constexpr int64_t kSched = 152 * 4;
 struct FwdPlan {
-    int chunk, nchunk;  // tokens per chunk; chunks of a sequence (equal lengths) or of the batch (packed)
-    int64_t units;
+    int chunk, nchunk;  // tokens per chunk, chunks of a block row that is cut
+    int64_t whole, cut;
     size_t offsets, local, sums, bytes;  // workspace offsets
 };
 FwdPlan plan_fwd(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) {
     FwdPlan p{};
     const int64_t nblk = s->ngroups * ((s->channels / s->ngroups + 31) / 32);
-    const int64_t rows = cu ? 1 : s->batch, L = s->seqlen;
-    const int64_t base = nblk * (rows > 0 ? rows : 1);
-    int64_t want = base >= 152 * 6 ? 1 : (152 * 8 + base - 1) / base;
+    const int64_t L = s->seqlen, base = nblk * (cu ? 1 : s->batch);
+    p.whole = cu || base < 2 * kSched ? 0 : base / kSched * kSched;
+    p.cut = base - p.whole;
+    // a tail of more than 7/8 of a round, or behind eight rounds, is not worth cutting
+    if (p.whole && (p.cut * 8 > kSched * 7 || base >= 8 * kSched)) p.whole = base, p.cut = 0;
+    int64_t want = p.cut ? (2 * kSched + p.cut - 1) / p.cut : 1;
     if (want > (L + 63) / 64) want = (L + 63) / 64;
     if (want < 1) want = 1;
+    if (want == 1) p.whole = cu ? 0 : base, p.cut = base - p.whole;
     p.chunk = (int)(((L + want - 1) / want + kTB - 1) / kTB * kTB);
     if (p.chunk < kTB) p.chunk = kTB;
     p.nchunk = (int)((L + p.chunk - 1) / p.chunk);
-    p.units = rows * p.nchunk;
     size_t at = 0;
     p.offsets = at;
     if (cu) at += align256(sizeof(int) * (nseq + 1));
     p.local = at;
-    if (p.nchunk > 1) at += align256(sizeof(float) * p.units * nblk * s->dstate * 32);
+    if (p.nchunk > 1) at += align256(sizeof(float) * p.cut * p.nchunk * s->dstate * 32);
     p.sums = at;
-    if (p.nchunk > 1) at += align256(sizeof(float) * p.units * nblk * 32);
+    if (p.nchunk > 1) at += align256(sizeof(float) * p.cut * p.nchunk * 32);
     p.bytes = at;
     return p;
 }
@@ -345,16 +375,21 @@ ssd_status_t run_fwd(ChannelArgs<T> &a, const ssd_channel_shape_t *s, const int6
     }
     if (e != cudaSuccess) return status_of(e);
     if (s->seqlen == 0) return SSD_OK;
-    a.chunk = p.chunk, a.nchunk = p.nchunk, a.units = (int)p.units;
+    a.chunk = p.chunk, a.nchunk = p.nchunk;
     a.local = reinterpret_cast<float4 *>(ws + p.local);
     a.sums = reinterpret_cast<float *>(ws + p.sums);
-    const int64_t blocks = (p.units * a.nblk + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
-    if (p.nchunk > 1) {
-        channel_fwd_kernel<T, N, false><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
+    const int64_t cut = p.cut * p.nchunk;
+    if (p.whole + cut > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+    a.whole = (int)p.whole, a.cut = (int)p.cut;
+    const int64_t blocks = (p.whole + cut + kWarps - 1) / kWarps;
+    if (p.cut && p.nchunk > 1) {
+        channel_fwd_kernel<T, N, false, false><<<(unsigned)((cut + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a);
         timing_mark(st, "channel_chunk_state");
     }
-    channel_fwd_kernel<T, N, true><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
+    if (a.z.p)
+        channel_fwd_kernel<T, N, true, true><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
+    else
+        channel_fwd_kernel<T, N, true, false><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
     timing_mark(st, "channel_scan");
     return status_of(cudaGetLastError());
 }

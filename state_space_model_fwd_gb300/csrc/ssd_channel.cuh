@@ -4,24 +4,23 @@
 //   delta = softplus(dt + dt_bias),  h_n <- exp(delta A_n) h_n + delta x B_n,
 //   y = sum_n h_n C_n + D x  (times silu(z)).
 //
-// A warp owns 32 channels of one group.  Lane l = cg * K + q holds, for the K
-// channels cg * K .. cg * K + K - 1, the M = N / K states q * M ..: a tile of
-// K x M states, so that one token's B and C (M values each) serve K channels
-// and its delta and delta x (K values each) serve M states.  Four operations,
-// one exponential and (M + K) / (K M) * 8 bytes of shared memory a state: with
-// one channel a lane the shared-memory reads alone would take twice the time
-// of the arithmetic.  Everything per channel (softplus, gates, D x, loads and
-// stores) is done by lane l for channel l, whatever the alignment of rows;
-// sums over the states of a channel are transposed on the way through the
-// shuffles so that lane l ends with channel l.
+// A warp owns a block of channels of one group.  Q lanes share a channel's
+// states; lane l = cg * Q + q holds, for the K channels cg * K .. cg * K + K - 1,
+// the M = N / Q states q * M ..: a tile of K x M states, so that one token's B
+// and C (M values each) serve K channels and its delta and delta x (K values
+// each) serve M states.  Four operations, one exponential and
+// (M + K) / (K M) * 8 bytes of shared memory a state: with one channel a lane
+// the shared-memory reads alone would take twice the time of the arithmetic.
+// Everything per channel and token (softplus, gates, D x, loads and stores,
+// whatever the alignment of rows) is spread over the lanes: W = Q / K tokens
+// at a time, lane l takes channel cg * K + q / W of token q % W of them.  Sums
+// over a channel's states are transposed on the way through the shuffles, so
+// that they end in that lane.
 #pragma once
 
 #include "ssd_layer.cuh"
 
 namespace ssd {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // Two fp32 values in one register pair.
 using f2 = unsigned long long;
@@ -43,11 +42,6 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 __device__ __forceinline__ f2 ex2x2(f2 v) {
     float a, b;
     unpack2(v, a, b);
@@ -59,17 +53,30 @@ __device__ __forceinline__ float sum2(f2 v) {
     return a + b;
 }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(exp(-|v|)): no overflow, and accurate
-// for v far below zero, where the result is exp(v).
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v))); }
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|): no overflow, and
+// accurate for v far below zero, where the result is e.  With s = e / (2 + e),
+// log(1 + e) = 2 atanh(s) = s q(s^2); q is the polynomial of degree 4 of least
+// relative error (4e-9, by the exchange algorithm) on s^2 in [0, 1/9].  2.5e-7
+// relative in fp32.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = ex2(-kLog2e * fabsf(v));
+    const float s = e * rcp(2.f + e), w = s * s;
+    float q = fmaf(0.28178334f, w, 0.27960601f);
+    q = fmaf(q, w, 0.40024909f);
+    q = fmaf(q, w, 0.66666317f);
+    q = fmaf(q, w, 2.f);
+    return fmaf(s, q, fmaxf(v, 0.f));
+}
 
-// Tile shape for N states.
-template <int N>
+// Tile shape for N states on Q lanes, K channels a lane.
+template <int N_, int Q_, int K_>
 struct Tile {
-    static constexpr int K = N == 8 ? 2 : 4;  // channels a lane holds, and lanes a channel's states lie on
-    static constexpr int M = N / K;           // states a lane holds of each
-    static constexpr int M2 = M / 2;
-    static constexpr int E4 = N / 4;  // float4s a lane holds (K * M == N)
+    static constexpr int N = N_, Q = Q_, K = K_;
+    static constexpr int M = N / Q, M2 = M / 2;  // states a lane holds of each channel
+    static constexpr int W = Q / K;              // tokens the lanes of a group take at a time
+    static constexpr int CW = 32 / Q * K;        // channels of a block
+    static constexpr int E4 = K * M / 4;         // float4s a lane holds
+    using Regs = f2[K][M2];
 };
 
 // A sequence's stretch of a chunk: tokens [a, e) of sequence s = [S, E).
@@ -93,70 +100,73 @@ __device__ __forceinline__ int seq_of(const Seqs &q, int t) {  // start[s] <= t 
     return lo;
 }
 
-// Channel block: 32 channels (or what is left) of one group.
+// Channel block: cw channels (or what is left) of one group.
 struct Block {
     int g, c0, nc;
 };
-__device__ __forceinline__ Block block_of(int blk, int per, int nblk_g) {
+__device__ __forceinline__ Block block_of(int blk, int per, int nblk_g, int cw) {
     const int g = blk / nblk_g, k = blk % nblk_g;
-    return {g, g * per + 32 * k, min(32, per - 32 * k)};
+    return {g, g * per + cw * k, min(cw, per - cw * k)};
 }
 
 // Lane-tile access of a [ch, N] fp32 array at channel c0: channels past nc
 // read as zero and are not written.
-template <int N>
-__device__ __forceinline__ void load_tile(const float *p, int lane, int nc, f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M;
-    const int cg = lane / K, q = lane % K;
+template <typename G>
+__device__ __forceinline__ void load_tile(const float *p, int lane, int nc, typename G::Regs &v) {
+    const int cg = lane / G::Q, q = lane % G::Q;
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int c = cg * K + i;
+    for (int i = 0; i < G::K; ++i) {
+        const int c = cg * G::K + i;
 #pragma unroll
-        for (int j = 0; j < M; j += 4) {
+        for (int j = 0; j < G::M; j += 4) {
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < nc) r = *reinterpret_cast<const float4 *>(p + (int64_t)c * N + q * M + j);
+            if (c < nc) r = *reinterpret_cast<const float4 *>(p + (int64_t)c * G::N + q * G::M + j);
             v[i][j / 2] = pack2(r.x, r.y);
             v[i][j / 2 + 1] = pack2(r.z, r.w);
         }
     }
 }
-template <int N>
-__device__ __forceinline__ void store_tile(float *p, int lane, int nc, const f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M;
-    const int cg = lane / K, q = lane % K;
+template <typename G>
+__device__ __forceinline__ void store_tile(float *p, int lane, int nc, const typename G::Regs &v) {
+    const int cg = lane / G::Q, q = lane % G::Q;
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int c = cg * K + i;
+    for (int i = 0; i < G::K; ++i) {
+        const int c = cg * G::K + i;
 #pragma unroll
-        for (int j = 0; j < M; j += 4) {
+        for (int j = 0; j < G::M; j += 4) {
             float4 r;
             unpack2(v[i][j / 2], r.x, r.y);
             unpack2(v[i][j / 2 + 1], r.z, r.w);
-            if (c < nc) *reinterpret_cast<float4 *>(p + (int64_t)c * N + q * M + j) = r;
+            if (c < nc) *reinterpret_cast<float4 *>(p + (int64_t)c * G::N + q * G::M + j) = r;
         }
     }
 }
 // The same through a lane-interleaved scratch array [E4][32] of float4.
-template <int N>
-__device__ __forceinline__ void load_lanes(const float4 *p, int lane, f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
-    constexpr int M = Tile<N>::M;
+template <typename G>
+__device__ __forceinline__ void load_lanes(const float4 *p, int lane, typename G::Regs &v) {
 #pragma unroll
-    for (int f = 0; f < Tile<N>::E4; ++f) {
+    for (int f = 0; f < G::E4; ++f) {
         const float4 r = p[f * 32 + lane];
-        v[4 * f / M][4 * f % M / 2] = pack2(r.x, r.y);
-        v[4 * f / M][4 * f % M / 2 + 1] = pack2(r.z, r.w);
+        v[4 * f / G::M][4 * f % G::M / 2] = pack2(r.x, r.y);
+        v[4 * f / G::M][4 * f % G::M / 2 + 1] = pack2(r.z, r.w);
     }
 }
-template <int N>
-__device__ __forceinline__ void store_lanes(float4 *p, int lane, const f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
-    constexpr int M = Tile<N>::M;
+template <typename G>
+__device__ __forceinline__ void store_lanes(float4 *p, int lane, const typename G::Regs &v) {
 #pragma unroll
-    for (int f = 0; f < Tile<N>::E4; ++f) {
+    for (int f = 0; f < G::E4; ++f) {
         float4 r;
-        unpack2(v[4 * f / M][4 * f % M / 2], r.x, r.y);
-        unpack2(v[4 * f / M][4 * f % M / 2 + 1], r.z, r.w);
+        unpack2(v[4 * f / G::M][4 * f % G::M / 2], r.x, r.y);
+        unpack2(v[4 * f / G::M][4 * f % G::M / 2 + 1], r.z, r.w);
         p[f * 32 + lane] = r;
     }
+}
+template <typename G>
+__device__ __forceinline__ void zero_tile(typename G::Regs &v) {
+#pragma unroll
+    for (int i = 0; i < G::K; ++i)
+#pragma unroll
+        for (int j = 0; j < G::M2; ++j) v[i][j] = 0;
 }
 
 // K consecutive floats of shared (or global) memory.
@@ -180,11 +190,30 @@ __device__ __forceinline__ void load_m(const float *p, f2 (&v)[M / 2]) {
     }
 }
 
-// Sums over lanes whose index differs in the bits below K, of R values for
-// each of K channels: lane q of the K ends with the R sums of channel q.
-template <int K, int R>
-__device__ __forceinline__ void channel_sums(float (&v)[K][R], int lane, float (&out)[R]) {
-    if constexpr (K == 4) {
+// Per-channel values staged twice each, (v, v), so that a load gives packed
+// operands: channel i of its lane group's K sits in 16-byte row i / 2, and the
+// 32 / Q groups of a row are contiguous (no bank conflicts).
+template <typename G>
+__device__ __forceinline__ int pair_slot(int cg, int i) {
+    return i / 2 * (128 / G::Q) + cg * 4 + i % 2 * 2;
+}
+__device__ __forceinline__ void store_pair(float *row, int slot, float v) {
+    *reinterpret_cast<float2 *>(row + slot) = make_float2(v, v);
+}
+template <typename G>
+__device__ __forceinline__ void load_pairs(const float *row, int cg, f2 (&v)[G::K]) {
+#pragma unroll
+    for (int h = 0; h < G::K / 2; ++h) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(row + h * (128 / G::Q) + cg * 4);
+        v[2 * h] = r.x, v[2 * h + 1] = r.y;
+    }
+}
+
+// Sums over the Q lanes of a group, R of each of Q values: lane q ends with
+// the R sums of value q.
+template <int Q, int R>
+__device__ __forceinline__ void group_sums(float (&v)[Q][R], int lane, float (&out)[R]) {
+    if constexpr (Q == 4) {
         const bool up = lane & 2;
 #pragma unroll
         for (int r = 0; r < R; ++r) {

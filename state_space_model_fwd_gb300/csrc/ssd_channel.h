@@ -18,9 +18,11 @@ struct ChannelArgs {
     int ch, per, nblk_g, nblk;  // channels, channels per group, blocks of 32 per group and in all
     int nseq, soft;
     Seqs seqs;
-    int chunk, nchunk, units;  // tokens per chunk, chunks (per sequence when lengths are equal), chunks in all
-    float4 *local;             // [unit][block][N / 4][32]: a chunk's own end state
-    float *sums;               // [unit][block][32]: sum of a chunk's deltas
+    int chunk, nchunk;  // tokens per chunk; chunks of a sequence row
+    int whole, cut;     // forward: block rows run whole, and cut into chunks
+    int units;          // gradient: chunks in all
+    float4 *local;      // a chunk's own end state, [N / 4][32] each: by [chunk][cut] forward, [unit][block] gradient
+    float *sums;        // sum of a chunk's deltas, [32] each
 };
 
 template <typename T>

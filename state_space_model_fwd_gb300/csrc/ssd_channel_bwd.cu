@@ -20,6 +20,8 @@
 //   4 the sums over channel blocks and over blocks, in a fixed order.
 // About 15 issue slots a state (1 and 3 together), most of it arithmetic:
 // bound by issue, with eight warps an SM (their registers).
+#include <type_traits>
+
 #include "ssd_channel.h"
 
 namespace ssd {
@@ -49,22 +51,18 @@ struct BwdArgs {
     int64_t tokens;
 };
 
+// The square tile: 32 channels a warp, lane l the one channel l.
 template <int N>
-__device__ __forceinline__ void zero_tile(f2 (&v)[Tile<N>::K][Tile<N>::M2]) {
-#pragma unroll
-    for (int i = 0; i < Tile<N>::K; ++i)
-#pragma unroll
-        for (int j = 0; j < Tile<N>::M2; ++j) v[i][j] = 0;
-}
+using BwdTile = std::conditional_t<N == 8, Tile<8, 2, 2>, Tile<N, 4, 4>>;
 
 template <typename T, int N>
 __device__ __forceinline__ void load_decay(const ChannelArgs<T> &a, const Block &k, int lane,
-                                           f2 (&A2)[Tile<N>::K][Tile<N>::M2]) {
-    load_tile<N>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
+                                           typename BwdTile<N>::Regs &A2) {
+    load_tile<BwdTile<N>>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
 #pragma unroll
-    for (int i = 0; i < Tile<N>::K; ++i)
+    for (int i = 0; i < BwdTile<N>::K; ++i)
 #pragma unroll
-        for (int j = 0; j < Tile<N>::M2; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
+        for (int j = 0; j < BwdTile<N>::M2; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
 }
 
 // The channel's delta before and after softplus.
@@ -82,9 +80,9 @@ struct alignas(16) SumStage {
     float d[8][32], u[8][32], g[8][32], bc[8][2 * N];
 };
 
-template <typename T, int N>
+template <typename T, int N, bool GATE>
 __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __grid_constant__ BwdArgs<T> b) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M, M2 = Tile<N>::M2, TB = 8;
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, M2 = BwdTile<N>::M2, TB = 8, NB = TB * 2 * N / 32;
     __shared__ SumStage<N> stage[kWarps];
     const ChannelArgs<T> &a = b.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -92,7 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
     if (id >= (int64_t)a.units * a.nblk) return;
     const int blk = (int)(id % a.nblk), unit = (int)(id / a.nblk);
     SumStage<N> &sm = stage[warp];
-    const Block k = block_of(blk, a.per, a.nblk_g);
+    const Block k = block_of(blk, a.per, a.nblk_g, 32);
     const int cg = lane / K, q = lane % K;
     const bool mine = lane < k.nc;
     const int own = k.c0 + (mine ? lane : 0);
@@ -110,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
     }
     f2 A2[K][M2], h[K][M2], P[K][M2], R[K][M2];
     load_decay<T, N>(a, k, lane, A2);
-    const float bias = a.bias && mine ? a.bias[own] : 0.f;
+    const float bias = a.bias ? a.bias[own] : 0.f;
     const int64_t at = (int64_t)unit * a.nblk + blk;
     int t = t0;
     while (true) {
@@ -118,37 +116,45 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
         const bool head = t == t0 && S < t0;  // a gradient goes back to the chunk before
         const bool tail = E > t1;             // a state goes on to the chunk after
         if (head || tail) {
-            zero_tile<N>(h), zero_tile<N>(R);
-            if (t == S && a.init) load_tile<N>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+            zero_tile<BwdTile<N>>(h), zero_tile<BwdTile<N>>(R);
+            if (t == S && a.init) load_tile<BwdTile<N>>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
 #pragma unroll
             for (int i = 0; i < K; ++i)
 #pragma unroll
                 for (int j = 0; j < M2; ++j) P[i][j] = pack2(1.f, 1.f);
             float total = 0.f;
+            // (tokens past the piece read its last one, lanes without a channel the block's first: delta = g = 0)
+            T rd[TB], rx[TB], rg[TB], rz[TB], rbc[NB];
+            auto fetch = [&](int tb) {
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    const int tt = min(tb + j, e - 1);
+                    rd[j] = a.dt.at(row, tt)[own];
+                    rx[j] = a.x.at(row, tt)[own];
+                    rg[j] = b.dy.at(row, tt)[own];
+                    if (GATE) rz[j] = a.z.at(row, tt)[own];
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int el = i * 32 + lane, tt = min(tb + el / (2 * N), e - 1), w = el % (2 * N);
+                    rbc[i] = w < N ? a.B.at(row, tt)[k.g * N + w] : a.C.at(row, tt)[k.g * N + w - N];
+                }
+            };
+            fetch(t);
             for (int tb = t; tb < e; tb += TB) {
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    const bool in = mine && tb + j < e;
-                    float d = 0.f, x = 0.f, g = 0.f;
-                    if (in) {
-                        d = delta_of(a, to_f32(a.dt.at(row, tb + j)[own]) + bias);
-                        x = to_f32(a.x.at(row, tb + j)[own]);
-                        g = to_f32(b.dy.at(row, tb + j)[own]);
-                        if (a.z.p) g *= silu(to_f32(a.z.at(row, tb + j)[own]));
-                    }
+                    float d = delta_of(a, to_f32(rd[j]) + bias), u = d * to_f32(rx[j]), g = to_f32(rg[j]);
+                    if (GATE) g *= silu(to_f32(rz[j]));
+                    if (tb + j >= e || !mine) d = u = g = 0.f;
                     total += d;
-                    sm.d[j][lane] = d, sm.u[j][lane] = d * x, sm.g[j][lane] = g;
+                    sm.d[j][lane] = d, sm.u[j][lane] = u, sm.g[j][lane] = g;
                 }
 #pragma unroll
-                for (int i = 0; i < TB * 2 * N / 32; ++i) {
-                    const int el = i * 32 + lane, j = el / (2 * N), w = el % (2 * N);
-                    float v = 0.f;
-                    if (tb + j < e)
-                        v = to_f32(w < N ? a.B.at(row, tb + j)[k.g * N + w] : a.C.at(row, tb + j)[k.g * N + w - N]);
-                    (&sm.bc[0][0])[el] = v;
-                }
+                for (int i = 0; i < NB; ++i) (&sm.bc[0][0])[i * 32 + lane] = tb + (i * 32 + lane) / (2 * N) < e ? to_f32(rbc[i]) : 0.f;
                 __syncwarp();
+                if (tb + TB < e) fetch(tb + TB);
 #pragma unroll 2
                 for (int j = 0; j < TB; ++j) {
                     float d[K], u[K], g[K];
@@ -174,15 +180,15 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
             if (head) {
                 if (e == E && b.dfinal) {
                     f2 f[K][M2];
-                    load_tile<N>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, f);
+                    load_tile<BwdTile<N>>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, f);
 #pragma unroll
                     for (int i = 0; i < K; ++i)
 #pragma unroll
                         for (int m = 0; m < M2; ++m) R[i][m] = fma2(P[i][m], f[i][m], R[i][m]);
                 }
-                store_lanes<N>(b.back + at * (N / 4 * 32), lane, R);
+                store_lanes<BwdTile<N>>(b.back + at * (N / 4 * 32), lane, R);
             }
-            if (tail) store_lanes<N>(a.local + at * (N / 4 * 32), lane, h);
+            if (tail) store_lanes<BwdTile<N>>(a.local + at * (N / 4 * 32), lane, h);
             if (tail && head) a.sums[at * 32 + lane] = total;
         }
         if (e == t1) return;
@@ -199,13 +205,13 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
 // ---------------------------------------------------------------------------
 template <typename T, int N>
 __global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M, AHEAD = 8;
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 8;
     const ChannelArgs<T> &a = b.f;
     const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (id >= (int64_t)rows * a.nblk * (N / 4) * 32) return;
     const int lane = (int)(id % 32), f = (int)(id / 32 % (N / 4));
     const int blk = (int)(id / (32 * (N / 4)) % a.nblk), row = (int)(id / (32 * (N / 4)) / a.nblk);
-    const Block k = block_of(blk, a.per, a.nblk_g);
+    const Block k = block_of(blk, a.per, a.nblk_g, 32);
     const int cg = lane / K, q = lane % K, c = cg * K + 4 * f / M;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < k.nc) A = *reinterpret_cast<const float4 *>(a.A + (int64_t)(k.c0 + c) * N + q * M + 4 * f % M);
@@ -287,8 +293,8 @@ struct LaneSums {
 
 template <typename T, int N, bool GATE>
 __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_constant__ BwdArgs<T> b) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M, M2 = Tile<N>::M2, TB = Geo<N>::TB, CH = Geo<N>::CH;
-    constexpr int R = GATE ? 3 : 2;
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, M2 = BwdTile<N>::M2, TB = Geo<N>::TB, CH = Geo<N>::CH;
+    constexpr int R = GATE ? 3 : 2, LEFT = LaneSums<BwdTile<N>::K, 2 * BwdTile<N>::M>::LEFT;
     extern __shared__ __align__(16) char smem[];
     const ChannelArgs<T> &a = b.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
     const bool live = in_g < a.nblk_g;  // a warp without channels only joins the barriers
     const int lives = min(kWarps, a.nblk_g - quad * kWarps);
     const int blk = grp * a.nblk_g + (live ? in_g : 0);
-    Block k = block_of(blk, a.per, a.nblk_g);
+    Block k = block_of(blk, a.per, a.nblk_g, 32);
     if (!live) k.nc = 0;
     const int cg = lane / K, q = lane % K;
     const bool mine = lane < k.nc;
@@ -309,8 +315,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
 
     f2 A2[K][M2], dA[K][M2];
     load_decay<T, N>(a, k, lane, A2);
-    zero_tile<N>(dA);
-    const float bias = a.bias && mine ? a.bias[own] : 0.f;
+    zero_tile<BwdTile<N>>(dA);
+    const float bias = a.bias ? a.bias[own] : 0.f;
     const float D = a.D && mine ? a.D[own] : 0.f;
     float dD = 0.f, dbias = 0.f;
     for (int i = lane; i < 2 * N; i += 32) sm.bc[CH][i] = 0.f;
@@ -329,36 +335,52 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             const int begin = max(t0, S), off = begin - t0, ns = (e - begin + TB - 1) / TB;
             f2 h[K][M2], r[K][M2];
             if (begin == S) {
-                zero_tile<N>(h);
-                if (a.init) load_tile<N>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+                zero_tile<BwdTile<N>>(h);
+                if (a.init) load_tile<BwdTile<N>>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
             } else {
-                load_lanes<N>(a.local + at * (N / 4 * 32), lane, h);
+                load_lanes<BwdTile<N>>(a.local + at * (N / 4 * 32), lane, h);
             }
             if (e == E) {
-                zero_tile<N>(r);
-                if (b.dfinal) load_tile<N>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
+                zero_tile<BwdTile<N>>(r);
+                if (b.dfinal) load_tile<BwdTile<N>>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
             } else {
-                load_lanes<N>(b.back + at * (N / 4 * 32), lane, r);
+                load_lanes<BwdTile<N>>(b.back + at * (N / 4 * 32), lane, r);
             }
             // forward, keeping the state before every TB tokens
             __syncwarp();
-            for (int j = 0; j < ns * TB; ++j) {
-                const bool in = mine && begin + j < e;
-                float d = 0.f, x = 0.f;
-                if (in) {
-                    d = delta_of(a, to_f32(a.dt.at(row, begin + j)[own]) + bias);
-                    x = to_f32(a.x.at(row, begin + j)[own]);
+            // (likewise: delta = 0)
+            for (int j0 = 0; j0 < ns * TB; j0 += 8) {
+                T rd[8], rx[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = min(begin + j0 + j, e - 1);
+                    rd[j] = a.dt.at(row, t)[own];
+                    rx[j] = a.x.at(row, t)[own];
                 }
-                sm.d[j][lane] = d, sm.u[j][lane] = d * x;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float d = delta_of(a, to_f32(rd[j]) + bias), u = d * to_f32(rx[j]);
+                    if (begin + j0 + j >= e || !mine) d = u = 0.f;
+                    if (j0 + j < CH) sm.d[j0 + j][lane] = d, sm.u[j0 + j][lane] = u;
+                }
             }
-            for (int el = lane; el < (e - begin) * 2 * N; el += 32) {
-                const int j = el / (2 * N), w = el % (2 * N);
-                sm.bc[off + j][w] =
-                    to_f32(w < N ? a.B.at(row, begin + j)[k.g * N + w] : a.C.at(row, begin + j)[k.g * N + w - N]);
+#pragma unroll 1
+            for (int el0 = 0; el0 < (e - begin) * 2 * N; el0 += 256) {
+                T v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int el = el0 + i * 32 + lane, t = min(begin + el / (2 * N), e - 1), w = el % (2 * N);
+                    v[i] = w < N ? a.B.at(row, t)[k.g * N + w] : a.C.at(row, t)[k.g * N + w - N];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int el = el0 + i * 32 + lane;
+                    if (el < (e - begin) * 2 * N) sm.bc[off][el] = to_f32(v[i]);
+                }
             }
             __syncwarp();
             for (int sb = 0; sb + 1 < ns; ++sb) {
-                store_lanes<N>(sm.kept[sb], lane, h);
+                store_lanes<BwdTile<N>>(sm.kept[sb], lane, h);
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
                     const int j = sb * TB + jj;
@@ -378,24 +400,17 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             }
             // backward
             for (int sb = ns - 1; sb >= 0; --sb) {
-                float x[TB], dy[TB], z[TB], sig[TB];
-                __syncwarp();
+                // this channel's values, in flight while the states are formed again
+                T rx[TB], rg[TB], rz[TB], rd[TB];
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
-                    const int t = begin + sb * TB + jj;
-                    const bool in = mine && t < e;
-                    x[jj] = in ? to_f32(a.x.at(row, t)[own]) : 0.f;
-                    dy[jj] = in ? to_f32(b.dy.at(row, t)[own]) : 0.f;
-                    sig[jj] = in && a.soft ? sigmoid(to_f32(a.dt.at(row, t)[own]) + bias) : 1.f;
-                    float g = dy[jj];
-                    if (GATE) {
-                        z[jj] = in ? to_f32(a.z.at(row, t)[own]) : 0.f;
-                        g *= silu(z[jj]);
-                    }
-                    sm.g[jj][lane] = g;
+                    const int t = min(begin + sb * TB + jj, e - 1);
+                    rx[jj] = a.x.at(row, t)[own];
+                    rg[jj] = b.dy.at(row, t)[own];
+                    rd[jj] = a.dt.at(row, t)[own];
+                    if (GATE) rz[jj] = a.z.at(row, t)[own];
                 }
-                __syncwarp();
-                if (sb + 1 < ns) load_lanes<N>(sm.kept[sb], lane, h);
+                if (sb + 1 < ns) load_lanes<BwdTile<N>>(sm.kept[sb], lane, h);
                 f2 before[TB][K][M2], decay[TB][K][M2];
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
@@ -417,6 +432,16 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                         }
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int jj = 0; jj < TB; ++jj) {
+                    float g = to_f32(rg[jj]);
+                    if (GATE) g *= silu(to_f32(rz[jj]));
+                    sm.g[jj][lane] = mine && begin + sb * TB + jj < e ? g : 0.f;
+                }
+                __syncwarp();
+                float o[TB][R], dbc[TB][LEFT];
+                int first = 0;
 #pragma unroll
                 for (int jj = TB - 1; jj >= 0; --jj) {
                     const int j = sb * TB + jj, t = begin + j;
@@ -452,39 +477,50 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                         sums[i][1] = sum2(dd_A);
                         if (GATE) sums[i][R - 1] = sum2(yy);
                     }
-                    float o[R];
-                    channel_sums<K, R>(sums, lane, o);
+                    group_sums<K, R>(sums, lane, o[jj]);
                     float v[2 * M];
 #pragma unroll
                     for (int m = 0; m < M2; ++m) {
                         unpack2(dBp[m], v[2 * m], v[2 * m + 1]);
                         unpack2(dCp[m], v[M + 2 * m], v[M + 2 * m + 1]);
                     }
-                    const int first = LaneSums<K, 2 * M>::reduce(v, lane);
-                    __syncwarp();  // every lane has read this token's B and C
-                    if (t < e) {
+                    first = LaneSums<K, 2 * M>::reduce(v, lane);
 #pragma unroll
-                        for (int i = 0; i < LaneSums<K, 2 * M>::LEFT; ++i) {
+                    for (int i = 0; i < LEFT; ++i) dbc[jj][i] = v[i];
+                }
+                // (outputs only here: a branch inside the loop would keep its tokens from overlapping)
+                __syncwarp();
+                const int left = e - begin - sb * TB;  // tokens of these TB that are the piece's
+#pragma unroll
+                for (int jj = 0; jj < TB; ++jj) {
+                    if (jj < left) {
+#pragma unroll
+                        for (int i = 0; i < LEFT; ++i) {
                             const int w = first + i;  // < M: dB, else dC, of state q M + w % M
-                            sm.bc[at_bc][(w < M ? 0 : N) + q * M + w % M] = v[i];
+                            sm.bc[off + sb * TB + jj][(w < M ? 0 : N) + q * M + w % M] = dbc[jj][i];
                         }
                     }
-                    if (mine && t < e) {
-                        const float delta = sm.d[j][lane];
-                        const float gx = sm.g[jj][lane];
-                        const float ddl = (x[jj] * o[0] + kLn2 * o[1]) * sig[jj];
-                        b.dx.at(row, t)[own] = from_f32<T>(fmaf(delta, o[0], D * gx));
+                }
+                if (mine) {
+#pragma unroll
+                    for (int jj = 0; jj < TB; ++jj) {
+                        if (jj >= left) break;
+                        const int t = begin + sb * TB + jj;
+                        const float delta = sm.d[sb * TB + jj][lane], gx = sm.g[jj][lane], x = to_f32(rx[jj]);
+                        float ddl = x * o[jj][0] + kLn2 * o[jj][1];
+                        if (a.soft) ddl *= sigmoid(to_f32(rd[jj]) + bias);
+                        b.dx.at(row, t)[own] = from_f32<T>(fmaf(delta, o[jj][0], D * gx));
                         b.ddt.at(row, t)[own] = from_f32<T>(ddl);
-                        dD = fmaf(gx, x[jj], dD);
+                        dD = fmaf(gx, x, dD);
                         dbias += ddl;
                         if (GATE) {
-                            const float y = fmaf(D, x[jj], o[R - 1]);
-                            b.dz.at(row, t)[own] = from_f32<T>(dy[jj] * y * silu_slope(z[jj], sigmoid(z[jj])));
+                            const float y = fmaf(D, x, o[jj][R - 1]), z = to_f32(rz[jj]);
+                            b.dz.at(row, t)[own] = from_f32<T>(to_f32(rg[jj]) * y * silu_slope(z, sigmoid(z)));
                         }
                     }
                 }
             }
-            if (begin == S && b.dinit) store_tile<N>(b.dinit + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
+            if (begin == S && b.dinit) store_tile<BwdTile<N>>(b.dinit + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, r);
             if (begin == t0) break;
             e = begin;
             do --s;
@@ -506,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
     }
     if (live) {
         float *dst = b.part_a + ((int64_t)slot * a.nblk + blk) * ((N + 2) * 32);
-        store_lanes<N>(reinterpret_cast<float4 *>(dst), lane, dA);
+        store_lanes<BwdTile<N>>(reinterpret_cast<float4 *>(dst), lane, dA);
         dst[N * 32 + lane] = dD;
         dst[(N + 1) * 32 + lane] = dbias;
     }
@@ -517,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 template <typename T, int N>
 __global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_constant__ BwdArgs<T> b, int64_t bc_blocks) {
-    constexpr int K = Tile<N>::K, M = Tile<N>::M;
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M;
     const ChannelArgs<T> &a = b.f;
     if (blockIdx.x < bc_blocks) {
         const int groups = a.nblk / a.nblk_g;
@@ -541,7 +577,7 @@ __global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_co
     const int blk = (int)(i / each), idx = (int)(i % each);
     float s = 0.f;
     for (int q = 0; q < b.slots; ++q) s += b.part_a[((int64_t)q * a.nblk + blk) * each + idx];
-    const Block k = block_of(blk, a.per, a.nblk_g);
+    const Block k = block_of(blk, a.per, a.nblk_g, 32);
     if (idx >= N * 32) {
         const int lane = idx % 32;
         float *dst = idx < (N + 1) * 32 ? b.dD : b.dbias;
@@ -625,7 +661,10 @@ ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t 
         const int64_t grads = (int64_t)s->ngroups * p.quads * p.slots;
         if (warps > 0x7FFFFFFF || threads / 128 >= 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
         if (p.nchunk > 1) {
-            channel_bwd_chunk_kernel<T, N><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
+            if (a.z.p)
+                channel_bwd_chunk_kernel<T, N, true><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
+            else
+                channel_bwd_chunk_kernel<T, N, false><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
             timing_mark(st, "channel_bwd_chunk");
             channel_bwd_pass_kernel<T, N><<<dim3((unsigned)((threads + 127) / 128), 2), 128, 0, st>>>(b, rows);
             timing_mark(st, "channel_bwd_pass");

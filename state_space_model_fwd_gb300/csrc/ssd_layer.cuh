@@ -9,9 +9,22 @@ namespace ssd {
 // ---------------------------------------------------------------------------
 // device math
 // ---------------------------------------------------------------------------
-// 1 / (1 + exp(-v)).  exp(-v) overflows to inf for v < -88.7, where the
-// quotient's limit 0 is what __fdividef gives too.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 1 / (1 + exp(-v)); exp(-v) overflows to inf for v < -88, whose reciprocal
+// is the limit 0.
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d/dv [v sigmoid(v)] given s = sigmoid(v)
 __device__ __forceinline__ float silu_slope(float v, float s) { return s * fmaf(v, 1.f - s, 1.f); }
@@ -109,8 +122,10 @@ __device__ __forceinline__ Vec<T, V> narrow(const float *f) {
 template <typename T>
 struct Rows {
     T *p;
-    int64_t bs, rs;  // elements between batch rows, between tokens
-    __device__ __forceinline__ T *at(int64_t b, int64_t t) const { return p + b * bs + t * rs; }
+    int64_t bs;  // elements between batch rows
+    int rs;      // and between tokens (32 bits: one multiplication an address)
+    __device__ __forceinline__ int64_t step(int tokens) const { return (int64_t)tokens * rs; }
+    __device__ __forceinline__ T *at(int64_t b, int t) const { return p + b * bs + step(t); }
 };
 
 // ---------------------------------------------------------------------------
@@ -126,12 +141,13 @@ inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr
 
 inline size_t dtype_size(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
 
-constexpr int64_t kMaxStride = int64_t(1) << 40;  // keeps every offset far inside 63 bits
+constexpr int64_t kMaxBatchStride = int64_t(1) << 40;  // keeps every offset far inside 63 bits
+constexpr int64_t kMaxRowStride = int64_t(1) << 31;
 
 // A readable array of rows: element-aligned, strides not negative.
 inline bool rows_in_ok(const ssd_rows_t &r, size_t esize) {
-    return r.data && aligned(r.data, esize) && r.batch_stride >= 0 && r.row_stride >= 0 && r.batch_stride < kMaxStride &&
-           r.row_stride < kMaxStride;
+    return r.data && aligned(r.data, esize) && r.batch_stride >= 0 && r.row_stride >= 0 && r.batch_stride < kMaxBatchStride &&
+           r.row_stride < kMaxRowStride;
 }
 // A writable one: no two rows share an element.
 inline bool rows_out_ok(const ssd_rows_t &r, size_t esize, int64_t b, int64_t L, int64_t cols) {
@@ -156,7 +172,7 @@ inline bool offsets_ok(const int64_t *cu, int64_t nseq, int64_t total) {
 
 template <typename T>
 inline Rows<T> rows_of(const ssd_rows_t &r) {
-    return {static_cast<T *>(r.data), r.batch_stride, r.row_stride};
+    return {static_cast<T *>(r.data), r.batch_stride, (int)r.row_stride};
 }
 
 }  // namespace ssd

@@ -65,7 +65,7 @@ def norm(x, weight, z, residual, scale, group, gate_after, eps):
         v = v * silu(z)
     v = v if scale is None else v * scale
     v = v if residual is None else v + residual
-    q = v.reshape(v.shape[0], -1, group)
+    q = v.reshape(v.shape[0], v.shape[1] // group, group)
     out = (q / torch.sqrt((q * q).mean(-1, keepdim=True) + eps)).reshape(v.shape) * weight
     if z is not None and gate_after:
         out = out * silu(z)
