@@ -9,6 +9,8 @@
 // exp(A sum delta), and writes y.  That costs up to 1.75 times the arithmetic
 // on SMs that would otherwise idle.  Chunks are cut without regard to
 // sequences, which restart the state inside a chunk.
+#include <type_traits>
+
 #include "ssd_channel.h"
 
 namespace ssd {
@@ -209,46 +211,87 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
 
 // One token per sequence.  The fp32 state is read and written once, all else
 // is small: bound by memory.  N / 4 lanes hold a channel's states, a float4
-// each; a thread has kUnroll channels' states in flight.
-constexpr int kUnroll = 4;
-template <typename T, int N>
+// each, for kRows sequences at a time: kRows state loads in flight, the decay
+// rates read once for all of them.  What is per channel and sequence is done
+// by one lane (lane q for sequences q, q + N / 4, ..) and passed on by
+// shuffles, and the sums over states are transposed back to that lane.
+constexpr int kRows = 4;
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(256) channel_step_kernel(const __grid_constant__ ChannelArgs<T> a, float *state) {
-    constexpr int Q = N / 4;
-    const int64_t total = (int64_t)a.nseq * a.ch * Q;  // float4s
-    const int64_t base = (int64_t)blockIdx.x * (256 * kUnroll) + threadIdx.x;
-    float4 *s4 = reinterpret_cast<float4 *>(state);
-    float4 h[kUnroll];
+    constexpr int Q = N / 4, MINE = kRows / Q > 0 ? kRows / Q : 1;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool in = i < (int64_t)a.ch * Q;  // whole groups of Q lanes
+    const int c = in ? (int)(i / Q) : 0, q = threadIdx.x % Q, g = c / a.per;
+    const int b0 = blockIdx.y * kRows, nb = min(kRows, a.nseq - b0);
+    float4 *s4 = reinterpret_cast<float4 *>(state) + ((int64_t)b0 * a.ch + c) * Q + q;
+    const int64_t row4 = (int64_t)a.ch * Q;
+    float4 h[kRows];
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r)
-        if (base + r * 256 < total) h[r] = __ldcs(s4 + base + r * 256);
+    for (int r = 0; r < kRows; ++r)
+        if (in && r < nb) h[r] = __ldcs(s4 + r * row4);
+    // this lane's sequences
+    float d[MINE], x[MINE], z[MINE];
+    const float bias = a.bias ? a.bias[c] : 0.f;
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
-        const int64_t i = base + r * 256;
-        const bool in = i < total;  // whole groups of Q lanes
-        const int64_t bc = in ? i / Q : 0;
-        const int q = (int)(i % Q), b = (int)(bc / a.ch), c = (int)(bc % a.ch);
-        const int g = c / a.per;
-        const float x = to_f32(a.x.at(b, 0)[c]);
-        float d = to_f32(a.dt.at(b, 0)[c]) + (a.bias ? a.bias[c] : 0.f);
-        if (a.soft) d = softplus(d);
-        const float u = d * x;
-        const float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)c * N + 4 * q);
-        const T *Bp = a.B.at(b, 0) + g * N + 4 * q, *Cp = a.C.at(b, 0) + g * N + 4 * q;
-        float4 v = h[r];
-        d *= kLog2e;
-        v.x = fmaf(ex2(d * A.x), v.x, u * to_f32(Bp[0]));
-        v.y = fmaf(ex2(d * A.y), v.y, u * to_f32(Bp[1]));
-        v.z = fmaf(ex2(d * A.z), v.z, u * to_f32(Bp[2]));
-        v.w = fmaf(ex2(d * A.w), v.w, u * to_f32(Bp[3]));
-        if (in) __stcs(s4 + i, v);
-        float y = fmaf(v.x, to_f32(Cp[0]),
-                       fmaf(v.y, to_f32(Cp[1]), fmaf(v.z, to_f32(Cp[2]), v.w * to_f32(Cp[3]))));
+    for (int k = 0; k < MINE; ++k) {
+        const int r = q + k * Q;
+        d[k] = x[k] = z[k] = 0.f;
+        if (r < nb) {
+            d[k] = to_f32(a.dt.at(b0 + r, 0)[c]) + bias;
+            x[k] = to_f32(a.x.at(b0 + r, 0)[c]);
+            if (a.z.p) z[k] = to_f32(a.z.at(b0 + r, 0)[c]);
+            if (a.soft) d[k] = softplus(d[k]);
+        }
+    }
+    float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)c * N + 4 * q);
+    A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
+    float y[kRows];
 #pragma unroll
-        for (int off = Q / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-        if (in && q == 0) {
-            float o = fmaf(a.D ? a.D[c] : 0.f, x, y);
-            if (a.z.p) o *= silu(to_f32(a.z.at(b, 0)[c]));
-            a.y.at(b, 0)[c] = from_f32<T>(o);
+    for (int r = 0; r < kRows; ++r) {
+        const int k = r / Q < MINE ? r / Q : 0;
+        const float dr = __shfl_sync(0xffffffffu, d[k], r % Q, Q);
+        const float ur = dr * __shfl_sync(0xffffffffu, x[k], r % Q, Q);
+        y[r] = 0.f;
+        if (in && r < nb) {
+            float B[4], C[4];
+            const T *pb = a.B.at(b0 + r, 0) + g * N + 4 * q, *pc = a.C.at(b0 + r, 0) + g * N + 4 * q;
+            if constexpr (VEC) {
+                widen<T, 4>(load_vec<T, 4>(pb), B);
+                widen<T, 4>(load_vec<T, 4>(pc), C);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) B[j] = to_f32(pb[j]), C[j] = to_f32(pc[j]);
+            }
+            float4 v = h[r];
+            v.x = fmaf(ex2(dr * A.x), v.x, ur * B[0]);
+            v.y = fmaf(ex2(dr * A.y), v.y, ur * B[1]);
+            v.z = fmaf(ex2(dr * A.z), v.z, ur * B[2]);
+            v.w = fmaf(ex2(dr * A.w), v.w, ur * B[3]);
+            __stcs(s4 + r * row4, v);
+            y[r] = fmaf(v.x, C[0], fmaf(v.y, C[1], fmaf(v.z, C[2], v.w * C[3])));
+        }
+    }
+    // lane q ends with the sums of its own sequences
+    float o[MINE];
+    if constexpr (Q == 2) {
+        float v[2][2] = {{y[0], y[2]}, {y[1], y[3]}};
+        group_sums<2, 2>(v, threadIdx.x, o);
+    } else {
+        if constexpr (Q == 8) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], 4);
+        }
+        float v[4][1] = {{y[0]}, {y[1]}, {y[2]}, {y[3]}};
+        group_sums<4, 1>(v, threadIdx.x, o);
+    }
+    const float D = a.D ? a.D[c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+        const int r = q + k * Q;
+        if (in && r < nb) {
+            float v = fmaf(D, x[k], o[k]);
+            if (a.z.p) v *= silu(z[k]);
+            a.y.at(b0 + r, 0)[c] = from_f32<T>(v);
         }
     }
 }
@@ -411,15 +454,24 @@ ssd_status_t step_typed(const ssd_channel_shape_t *s, const ssd_channel_inputs_t
                         cudaStream_t st) {
     ChannelArgs<T> a = channel_args<T>(s, in, s->batch);
     a.y = rows_of<T>(*y);
-    const int64_t blocks = (s->batch * s->channels * (s->dstate / 4) + 256 * kUnroll - 1) / (256 * kUnroll);
-    if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+    const int64_t blocks = (s->channels * (s->dstate / 4) + 255) / 256, rows = (s->batch + kRows - 1) / kRows;
+    if (blocks > 0x7FFFFFFF || rows > 65535) return SSD_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, (unsigned)rows);
+    const bool vec = rows_vec(in->B, sizeof(T), s->batch, 1) && rows_vec(in->C, sizeof(T), s->batch, 1);
     timing_begin(st);
+    auto launch = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        if (vec)
+            channel_step_kernel<T, N, true><<<grid, 256, 0, st>>>(a, state);
+        else
+            channel_step_kernel<T, N, false><<<grid, 256, 0, st>>>(a, state);
+    };
     if (s->dstate == 8)
-        channel_step_kernel<T, 8><<<(unsigned)blocks, 256, 0, st>>>(a, state);
+        launch(std::integral_constant<int, 8>{});
     else if (s->dstate == 16)
-        channel_step_kernel<T, 16><<<(unsigned)blocks, 256, 0, st>>>(a, state);
+        launch(std::integral_constant<int, 16>{});
     else
-        channel_step_kernel<T, 32><<<(unsigned)blocks, 256, 0, st>>>(a, state);
+        launch(std::integral_constant<int, 32>{});
     timing_mark(st, "channel_step");
     return status_of(cudaGetLastError());
 }

@@ -31,8 +31,9 @@ constexpr int kWarps = 4;
 
 template <int N>
 struct Geo {
-    static constexpr int CH = N == 32 ? 16 : 32;  // tokens per chunk
-    static constexpr int TB = N == 32 ? 2 : 4;    // tokens whose states are in registers
+    // tokens per chunk: with 16 states what lets eight warps share an SM's memory
+    static constexpr int CH = N == 32 ? 16 : N == 16 ? 28 : 32;
+    static constexpr int TB = N == 32 ? 2 : 4;  // tokens whose states are in registers
     static constexpr int NS = CH / TB;
 };
 
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
 // ---------------------------------------------------------------------------
 template <typename T, int N>
 __global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
-    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 8;
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 16;
     const ChannelArgs<T> &a = b.f;
     const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (id >= (int64_t)rows * a.nblk * (N / 4) * 32) return;
@@ -256,9 +257,8 @@ __global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_cons
 template <int N>
 struct alignas(16) GradStage {
     float4 kept[Geo<N>::NS - 1][N / 4 * 32];  // states before the 0th .. next to last TB tokens
-    float d[Geo<N>::CH][32], u[Geo<N>::CH][32];  // by token of the piece
-    float bc[Geo<N>::CH + 1][2 * N];             // by token of the chunk, turning into the warp's dB and dC; a zero row
-    float g[Geo<N>::TB][32];
+    float d[Geo<N>::CH][32], u[Geo<N>::CH][32], g[Geo<N>::CH][32];  // by token of the piece
+    float bc[Geo<N>::CH + 1][2 * N];                                // by token of the chunk, turning into the warp's dB and dC; a zero row
 };
 
 // Sums over the lanes whose index differs in the bits from K up, of V values:
@@ -346,36 +346,37 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             } else {
                 load_lanes<BwdTile<N>>(b.back + at * (N / 4 * 32), lane, r);
             }
-            // forward, keeping the state before every TB tokens
+            // forward, keeping the state before every TB tokens.  (Many loads at a
+            // time; tokens past the piece read its last one, lanes without a
+            // channel the block's first: delta = g = 0.)
             __syncwarp();
-            // (likewise: delta = 0)
-            for (int j0 = 0; j0 < ns * TB; j0 += 8) {
-                T rd[8], rx[8];
+            constexpr int AT = CH / 2, AB = AT * 2 * N / 32;
+            for (int j0 = 0; j0 < ns * TB; j0 += AT) {
+                T rd[AT], rx[AT], rg[AT], rz[AT], rb[AB];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < AT; ++j) {
                     const int t = min(begin + j0 + j, e - 1);
                     rd[j] = a.dt.at(row, t)[own];
                     rx[j] = a.x.at(row, t)[own];
+                    rg[j] = b.dy.at(row, t)[own];
+                    if (GATE) rz[j] = a.z.at(row, t)[own];
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float d = delta_of(a, to_f32(rd[j]) + bias), u = d * to_f32(rx[j]);
-                    if (begin + j0 + j >= e || !mine) d = u = 0.f;
-                    if (j0 + j < CH) sm.d[j0 + j][lane] = d, sm.u[j0 + j][lane] = u;
-                }
-            }
-#pragma unroll 1
-            for (int el0 = 0; el0 < (e - begin) * 2 * N; el0 += 256) {
-                T v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int el = el0 + i * 32 + lane, t = min(begin + el / (2 * N), e - 1), w = el % (2 * N);
-                    v[i] = w < N ? a.B.at(row, t)[k.g * N + w] : a.C.at(row, t)[k.g * N + w - N];
+                for (int i = 0; i < AB; ++i) {
+                    const int el = i * 32 + lane, t = min(begin + j0 + el / (2 * N), e - 1), w = el % (2 * N);
+                    rb[i] = w < N ? a.B.at(row, t)[k.g * N + w] : a.C.at(row, t)[k.g * N + w - N];
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int el = el0 + i * 32 + lane;
-                    if (el < (e - begin) * 2 * N) sm.bc[off][el] = to_f32(v[i]);
+                for (int j = 0; j < AT; ++j) {
+                    float d = delta_of(a, to_f32(rd[j]) + bias), u = d * to_f32(rx[j]), g = to_f32(rg[j]);
+                    if (GATE) g *= silu(to_f32(rz[j]));
+                    if (begin + j0 + j >= e || !mine) d = u = g = 0.f;
+                    sm.d[j0 + j][lane] = d, sm.u[j0 + j][lane] = u, sm.g[j0 + j][lane] = g;
+                }
+#pragma unroll
+                for (int i = 0; i < AB; ++i) {
+                    const int el = i * 32 + lane, j = j0 + el / (2 * N);
+                    if (begin + j < e) sm.bc[off + j][el % (2 * N)] = to_f32(rb[i]);
                 }
             }
             __syncwarp();
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             }
             // backward
             for (int sb = ns - 1; sb >= 0; --sb) {
-                // this channel's values, in flight while the states are formed again
+                // this channel's values, in flight until the outputs
                 T rx[TB], rg[TB], rz[TB], rd[TB];
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
@@ -432,14 +433,6 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                         }
                     }
                 }
-                __syncwarp();
-#pragma unroll
-                for (int jj = 0; jj < TB; ++jj) {
-                    float g = to_f32(rg[jj]);
-                    if (GATE) g *= silu(to_f32(rz[jj]));
-                    sm.g[jj][lane] = mine && begin + sb * TB + jj < e ? g : 0.f;
-                }
-                __syncwarp();
                 float o[TB][R], dbc[TB][LEFT];
                 int first = 0;
 #pragma unroll
@@ -449,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                     f2 B[M2], C[M2], dBp[M2], dCp[M2];
                     load_k<K>(&sm.d[j][cg * K], d);
                     load_k<K>(&sm.u[j][cg * K], u);
-                    load_k<K>(&sm.g[jj][cg * K], g);
+                    load_k<K>(&sm.g[j][cg * K], g);
                     const int at_bc = t < e ? off + j : CH;
                     load_m<M>(&sm.bc[at_bc][q * M], B);
                     load_m<M>(&sm.bc[at_bc][N + q * M], C);
@@ -506,7 +499,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                     for (int jj = 0; jj < TB; ++jj) {
                         if (jj >= left) break;
                         const int t = begin + sb * TB + jj;
-                        const float delta = sm.d[sb * TB + jj][lane], gx = sm.g[jj][lane], x = to_f32(rx[jj]);
+                        const float delta = sm.d[sb * TB + jj][lane], gx = sm.g[sb * TB + jj][lane], x = to_f32(rx[jj]);
                         float ddl = x * o[jj][0] + kLn2 * o[jj][1];
                         if (a.soft) ddl *= sigmoid(to_f32(rd[jj]) + bias);
                         b.dx.at(row, t)[own] = from_f32<T>(fmaf(delta, o[jj][0], D * gx));
@@ -604,8 +597,9 @@ struct BwdPlan {
         quads = (int)((nblk_g + kWarps - 1) / kWarps);
         nchunk = (int)((s->seqlen + Geo<N>::CH - 1) / Geo<N>::CH);
         units = (cu ? 1 : s->batch) * nchunk;
-        // one wave of the blocks that fit two to an SM
-        const int64_t want = (152 * 2 + s->ngroups * quads - 1) / (s->ngroups * quads);
+        // at most one wave of the blocks that fit two to an SM
+        int64_t want = 152 * 2 / (s->ngroups * quads);
+        if (want < 1) want = 1;
         slots = (int)(units < want ? units : want);
         size_t at = 0;
         auto take = [&at](size_t n) {

@@ -24,7 +24,8 @@ namespace {
 constexpr int kVec = 4;       // channels per thread (8 bytes of bf16, 16 of fp32)
 constexpr int kLanes = 32;    // channel vectors per block
 constexpr int kSub = 8;       // tiles of tokens per block, one per warp
-constexpr int kAhead = 4;     // rows in flight
+constexpr int kAhead = 8;     // rows in flight, forward
+constexpr int kStep = 4;      // and in the gradient (of x and of dy)
 constexpr int kMaxSet = 960;  // sequences whose offsets fit one launch's parameters
 
 // Offsets of the packed sequences first .. first + n - 1.
@@ -103,11 +104,36 @@ __device__ __forceinline__ Vec<T, V> row_at(const ConvArgs<T> &a, const Rows<con
 
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_weights(const ConvArgs<T> &a, int c0, float (&w)[W][V], float (&b)[V]) {
+    const float *src = a.weight + (int64_t)c0 * W;  // V W floats: 16-byte aligned where V is 4
+    float f[W * V];
+    if constexpr (V == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) widen<float, 4>(load_vec<float, 4>(src + 4 * i), f + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W * V; ++i) f[i] = src[i];
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][v] = a.weight[(int64_t)(c0 + v) * W + k];
+        for (int k = 0; k < W; ++k) w[k][v] = f[v * W + k];
         b[v] = a.bias ? a.bias[c0 + v] : 0.f;
+    }
+}
+
+// p = bias + sum_k w[k] (window, then cur): the window moves up by one.
+template <int W, int V>
+__device__ __forceinline__ void taps(const float (&w)[W][V], const float (&bias)[V], float (&win)[W - 1][V],
+                                     const float (&cur)[V], float (&p)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = bias[v];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) s = fmaf(w[k][v], win[k][v], s);
+        p[v] = fmaf(w[W - 1][v], cur[v], s);
+#pragma unroll
+        for (int k = 0; k + 1 < W - 1; ++k) win[k][v] = win[k + 1][v];
+        win[W - 2][v] = cur[v];
     }
 }
 
@@ -140,7 +166,7 @@ __device__ void copy_states(const ConvArgs<T> &a, const Set &set, int64_t block)
 }
 
 template <typename T, int W, int V, bool PACKED, typename Set>
-__global__ void __launch_bounds__(kLanes *kSub) conv_fwd_kernel(const __grid_constant__ ConvArgs<T> a,
+__global__ void __launch_bounds__(kLanes *kSub, 2) conv_fwd_kernel(const __grid_constant__ ConvArgs<T> a,
                                                                 const __grid_constant__ Set set) {
     if (blockIdx.x >= a.tblocks) {
         copy_states<T, W, V, PACKED, false>(a, set, blockIdx.x - a.tblocks);
@@ -158,6 +184,8 @@ __global__ void __launch_bounds__(kLanes *kSub) conv_fwd_kernel(const __grid_con
     for_pieces<PACKED>(tile, a.tile, a.L, set, [&](const Piece &p, int row) {
         Vec<T, V> nxt[kAhead];
 #pragma unroll
+        for (int i = 0; i < kAhead; ++i) nxt[i] = zero_vec<T, V>();
+#pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (p.a + i < p.e) nxt[i] = load_vec<T, V>(x.at(row, p.a + i));
         float win[W - 1][V];
@@ -167,29 +195,39 @@ __global__ void __launch_bounds__(kLanes *kSub) conv_fwd_kernel(const __grid_con
             widen<T, V>(v, win[j]);
         }
         for (int t = p.a; t < p.e; t += kAhead) {
+            const int n = p.e - t;
+            float o[kAhead][V];
             Vec<T, V> cur[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                cur[i] = nxt[i];
-                if (t + kAhead + i < p.e) nxt[i] = load_vec<T, V>(x.at(row, t + kAhead + i));
+            for (int i = 0; i < kAhead; ++i) cur[i] = nxt[i];
+            if (n >= 2 * kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) nxt[i] = load_vec<T, V>(x.at(row, t + kAhead + i));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (kAhead + i < n) nxt[i] = load_vec<T, V>(x.at(row, t + kAhead + i));
             }
+            // (rows past the end are computed from what was loaded last and not stored)
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (t + i >= p.e) break;
-                float c[V], o[V];
+                float c[V];
                 widen<T, V>(cur[i], c);
+                taps<W, V>(w, bias, win, c, o[i]);
+            }
+            if (a.use_silu) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float s = bias[v];
+                for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) s = fmaf(w[k][v], win[k][v], s);
-                    s = fmaf(w[W - 1][v], c[v], s);
-                    o[v] = a.use_silu ? silu(s) : s;
+                    for (int v = 0; v < V; ++v) o[i][v] = silu(o[i][v]);
+            }
+            if (n >= kAhead) {
 #pragma unroll
-                    for (int k = 0; k + 1 < W - 1; ++k) win[k][v] = win[k + 1][v];
-                    win[W - 2][v] = c[v];
-                }
-                store_vec<T, V>(y.at(row, t + i), narrow<T, V>(o));
+                for (int i = 0; i < kAhead; ++i) store_vec<T, V>(y.at(row, t + i), narrow<T, V>(o[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (i < n) store_vec<T, V>(y.at(row, t + i), narrow<T, V>(o[i]));
             }
         }
     });
@@ -205,7 +243,7 @@ __global__ void __launch_bounds__(kLanes *kSub) conv_fwd_kernel(const __grid_con
 // added over the block's warps, and the blocks' partial sums by a second
 // kernel in a fixed order.
 template <typename T, int W, int V, bool PACKED, typename Set>
-__global__ void __launch_bounds__(kLanes *kSub) conv_bwd_kernel(const __grid_constant__ ConvArgs<T> a,
+__global__ void __launch_bounds__(kLanes *kSub, 2) conv_bwd_kernel(const __grid_constant__ ConvArgs<T> a,
                                                                 const __grid_constant__ Set set, int slots, int slot0) {
     if (blockIdx.x >= a.tblocks) {
         copy_states<T, W, V, PACKED, true>(a, set, blockIdx.x - a.tblocks);
@@ -231,11 +269,21 @@ __global__ void __launch_bounds__(kLanes *kSub) conv_bwd_kernel(const __grid_con
         dx.p += c0;
         for (int64_t tile = (int64_t)slot * kSub + threadIdx.y; tile < a.ntiles; tile += (int64_t)slots * kSub) {
             for_pieces<PACKED>(tile, a.tile, a.L, set, [&](const Piece &p, int row) {
-                const int stop = min(p.E, p.e + W - 1);  // dp is wanted up to here
-                Vec<T, V> nx, ng;
-                nx = load_vec<T, V>(x.at(row, p.a));
-                ng = load_vec<T, V>(dy.at(row, p.a));
+                // a sequence's first rows complete the rows before it
+                const bool back = p.a == p.S && a.final_state;
+                const int tail = a.dfinal ? p.E - (W - 1) : p.E;  // rows from here on add the final state's gradient
                 float win[W - 1][V], dpw[W - 1][V];
+                Vec<T, V> nx[kStep], ng[kStep];
+                auto fetch = [&](int t) {
+                    // (rows past the sequence read its last one; their dp is set to zero)
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) {
+                        const int tt = min(t + i, p.E - 1);
+                        nx[i] = load_vec<T, V>(x.at(row, tt));
+                        ng[i] = load_vec<T, V>(dy.at(row, tt));
+                    }
+                };
+                fetch(p.a);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) {
                     const Vec<T, V> v = row_at<T, W, V>(a, x, p, row, p.a - (W - 1) + j, c0);
@@ -243,65 +291,61 @@ __global__ void __launch_bounds__(kLanes *kSub) conv_bwd_kernel(const __grid_con
 #pragma unroll
                     for (int v2 = 0; v2 < V; ++v2) dpw[j][v2] = 0.f;
                 }
-#pragma unroll 4
-                for (int t = p.a; t < p.e + W - 1; ++t) {
-                    float dp[V], o[V];
-                    if (t < stop) {
-                        float c[V], g[V];
-                        widen<T, V>(nx, c);
-                        widen<T, V>(ng, g);
-                        if (t + 1 < stop) {
-                            nx = load_vec<T, V>(x.at(row, t + 1));
-                            ng = load_vec<T, V>(dy.at(row, t + 1));
-                        }
-                        const bool mine = t < p.e;
+                const int end = p.e + W - 1;
+                for (int t = p.a; t < end; t += kStep) {
+                    float c[kStep][V], dp[kStep][V], o[kStep][V];
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) widen<T, V>(nx[i], c[i]), widen<T, V>(ng[i], dp[i]);
+                    if (t + kStep < end) fetch(t + kStep);
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) {
+                        float old[W - 1][V], s[V];
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                            for (int v = 0; v < V; ++v) old[k][v] = win[k][v];
+                        taps<W, V>(w, bias, win, c[i], s);
 #pragma unroll
                         for (int v = 0; v < V; ++v) {
-                            float s = bias[v];
+                            if (a.use_silu) dp[i][v] *= silu_slope(s[v], sigmoid(s[v]));
+                            dp[i][v] = t + i < p.E ? dp[i][v] : 0.f;
+                            const float own = t + i < p.e ? dp[i][v] : 0.f;
 #pragma unroll
-                            for (int k = 0; k < W - 1; ++k) s = fmaf(w[k][v], win[k][v], s);
-                            s = fmaf(w[W - 1][v], c[v], s);
-                            dp[v] = a.use_silu ? g[v] * silu_slope(s, sigmoid(s)) : g[v];
-                            if (mine) {
+                            for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(own, old[k][v], dw[k][v]);
+                            dw[W - 1][v] = fmaf(own, c[i][v], dw[W - 1][v]);
+                            db[v] += own;
+                            // row t + i - (W-1) is complete; dpw holds the last W-1 dp
+                            float r = w[0][v] * dp[i][v];
 #pragma unroll
-                                for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(dp[v], win[k][v], dw[k][v]);
-                                dw[W - 1][v] = fmaf(dp[v], c[v], dw[W - 1][v]);
-                                db[v] += dp[v];
-                            }
+                            for (int k = 1; k < W; ++k) r = fmaf(w[k][v], dpw[W - 1 - k][v], r);
+                            o[i][v] = r;
 #pragma unroll
-                            for (int k = 0; k + 1 < W - 1; ++k) win[k][v] = win[k + 1][v];
-                            win[W - 2][v] = c[v];
+                            for (int k = 0; k + 1 < W - 1; ++k) dpw[k][v] = dpw[k + 1][v];
+                            dpw[W - 2][v] = dp[i][v];
                         }
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) dp[v] = 0.f;
                     }
-                    // row t - (W-1) is complete; dpw holds dp[t - (W-1)] .. dp[t - 1]
-                    const int r = t - (W - 1);
+                    const int r0 = t - (W - 1);
+                    if (r0 >= p.a && r0 + kStep <= min(p.e, tail)) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float s = w[0][v] * dp[v];
-#pragma unroll
-                        for (int k = 1; k < W; ++k) s = fmaf(w[k][v], dpw[W - 1 - k][v], s);
-                        o[v] = s;
-#pragma unroll
-                        for (int k = 0; k + 1 < W - 1; ++k) dpw[k][v] = dpw[k + 1][v];
-                        dpw[W - 2][v] = dp[v];
+                        for (int i = 0; i < kStep; ++i) store_vec<T, V>(dx.at(row, r0 + i), narrow<T, V>(o[i]));
+                        continue;
                     }
-                    if (r < p.a && !(p.a == p.S && a.final_state)) continue;
-                    if (a.dfinal && r >= p.E - (W - 1)) {
-                        float f[V];
-                        const Vec<T, V> fv = load_vec<T, V>(
-                            a.dfinal + ((int64_t)p.s * (W - 1) + (r - (p.E - (W - 1)))) * a.C + c0);
-                        widen<T, V>(fv, f);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] += f[v];
+                    for (int i = 0; i < kStep; ++i) {
+                        const int r = r0 + i;
+                        if (r >= p.e || (r < p.a && !back)) continue;
+                        if (a.dfinal && r >= tail) {
+                            float f[V];
+                            widen<T, V>(load_vec<T, V>(a.dfinal + ((int64_t)p.s * (W - 1) + (r - tail)) * a.C + c0), f);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) o[i][v] += f[v];
+                        }
+                        if (r >= p.a)
+                            store_vec<T, V>(dx.at(row, r), narrow<T, V>(o[i]));
+                        else
+                            store_vec<T, V>(a.final_state + ((int64_t)p.s * (W - 1) + (r - p.S + W - 1)) * a.C + c0,
+                                            narrow<T, V>(o[i]));
                     }
-                    if (r >= p.a)
-                        store_vec<T, V>(dx.at(row, r), narrow<T, V>(o));
-                    else
-                        store_vec<T, V>(a.final_state + ((int64_t)p.s * (W - 1) + (r - p.S + W - 1)) * a.C + c0,
-                                        narrow<T, V>(o));
                 }
             });
         }
@@ -400,11 +444,11 @@ struct Plan {
     int V, nvec, ncb, tile;
 };
 
-// Tokens per tile: the longest of 32, 16, 8, 4 that still gives every SM 16
-// warps (a tile reads W-1 rows beyond its own).
+// Tokens per tile: the longest of 32, 16, 8 that still makes three rounds of
+// the 16 warps an SM holds (a tile reads W-1 rows beyond its own).
 int pick_tile(int64_t ncb, int64_t tokens) {
     int tile = 32;
-    while (tile > 4 && ncb * (tokens / tile) < 152 * 16) tile /= 2;
+    while (tile > 8 && ncb * (tokens / tile) < 152 * 16 * 3) tile /= 2;
     return tile;
 }
 
@@ -413,7 +457,7 @@ bool fill(const ssd_conv_shape_t *s, int64_t nseq, const ssd_rows_t *x, const ss
           std::initializer_list<const void *> states, ConvArgs<T> &a) {
     const size_t es = sizeof(T);
     const int V = kVec;
-    bool vec = s->channels * es % 16 == 0 && rows_vec(*x, es, s->batch, s->seqlen);
+    bool vec = aligned(a.weight, 16) && s->channels * es % 16 == 0 && rows_vec(*x, es, s->batch, s->seqlen);
     if (dx) vec = vec && rows_vec(*dx, es, s->batch, s->seqlen);
     int64_t end = 0;
     for (int i = 0; i < SSD_CONV_MAX_PARTS; ++i) {
@@ -481,37 +525,41 @@ ssd_status_t run_fwd(ConvArgs<T> &a, const ssd_conv_shape_t *s, const int64_t *c
 }
 
 // The gradient's blocks per channel block (a slot's block walks every
-// slots-th group of kSub tiles): enough for four blocks an SM.
-constexpr int kBwdTile = 32;
-int pick_slots(int64_t ncb, int64_t ntiles) {
-    const int64_t groups = (ntiles + kSub - 1) / kSub;
-    const int64_t want = (152 * 4 + ncb - 1) / ncb;
-    return (int)(groups < want ? groups : want);
+// slots-th group of kSub tiles), two an SM, and tiles of 32 to 256 tokens that
+// give every warp of them the same number.
+struct BwdPlan {
+    int slots, tile;
+    int64_t ntiles;
+};
+BwdPlan plan_bwd(int64_t ncb, int64_t rows, int64_t L) {
+    int64_t want = 152 * 2 / ncb;
+    if (want < 1) want = 1;
+    const int64_t warps = want * kSub, tokens = rows * L;
+    const int64_t each = (tokens + warps - 1) / warps, rounds = (each + 255) / 256;
+    int64_t tile = rounds ? (each + rounds - 1) / rounds : 32;
+    if (tile < 32) tile = 32;
+    BwdPlan p;
+    p.tile = (int)tile;
+    p.ntiles = rows * ((L + tile - 1) / tile);
+    const int64_t groups = (p.ntiles + kSub - 1) / kSub;
+    p.slots = (int)(groups < want ? groups : want);
+    return p;
 }
-int64_t bwd_tiles(const ssd_conv_shape_t *s, bool packed, int64_t tokens) {
-    return packed ? (tokens + kBwdTile - 1) / kBwdTile : s->batch * ((s->seqlen + kBwdTile - 1) / kBwdTile);
-}
-// Slots of the whole call, for the finest channel blocks (one element a
-// lane), so that the size does not depend on alignment.
+// The most slots that the call may use: with vectors of kVec channels (single
+// ones make more channel blocks and so fewer slots).
 int64_t total_slots(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nseq) {
-    const int V = kVec;
-    const int64_t ncb = ((s->channels + V - 1) / V + kLanes - 1) / kLanes;
-    if (!cu) return pick_slots(ncb, bwd_tiles(s, false, 0));
-    int64_t n = 0;
-    for (int64_t f = 0; f < nseq; f += kMaxSet) {
-        const int64_t l = f + kMaxSet < nseq ? f + kMaxSet : nseq;
-        n += pick_slots(ncb, bwd_tiles(s, true, cu[l] - cu[f]));
-    }
-    return n;
+    const int64_t ncb = ((s->channels + kVec - 1) / kVec + kLanes - 1) / kLanes;
+    int64_t want = 152 * 2 / ncb;
+    if (want < 1) want = 1;
+    return want * (cu ? (nseq + kMaxSet - 1) / kMaxSet : 1);
 }
 
 template <typename T, int W, int V, bool PACKED, typename Set>
 ssd_status_t launch_bwd(ConvArgs<T> &a, const ssd_conv_shape_t *s, const Set &set, int64_t tokens, int64_t nseq, int slot0,
                         int *used, cudaStream_t st) {
-    a.tile = kBwdTile;
-    const int64_t ntiles = bwd_tiles(s, PACKED, tokens);
-    a.ntiles = (int)ntiles;
-    const int slots = pick_slots(a.ncb, ntiles);
+    const BwdPlan p = plan_bwd(a.ncb, PACKED ? 1 : s->batch, PACKED ? tokens : s->seqlen);
+    a.tile = p.tile, a.ntiles = (int)p.ntiles;
+    const int slots = p.slots;
     a.tblocks = (int64_t)a.ncb * slots;
     int64_t blocks = a.tblocks;
     if (a.final_state) blocks += (nseq * (W - 1) * a.nvec + kLanes * kSub - 1) / (kLanes * kSub);
@@ -567,8 +615,8 @@ ssd_status_t fwd_typed(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nse
                        const float *weight, const float *bias, const void *init, const ssd_rows_t *y, void *fin,
                        cudaStream_t st) {
     ConvArgs<T> a{};
-    const bool vec = fill<T>(s, nseq, x, y, nullptr, {init, fin}, a);
     a.weight = weight, a.bias = bias;
+    const bool vec = fill<T>(s, nseq, x, y, nullptr, {init, fin}, a);
     a.init = static_cast<const T *>(init), a.final_state = static_cast<T *>(fin);
     return dispatch<kVec>(s->width, vec, [&](auto w, auto v) {
         return run_fwd<T, decltype(w)::value, decltype(v)::value>(a, s, cu, nseq, st);
@@ -580,9 +628,9 @@ ssd_status_t bwd_typed(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nse
                        const ssd_rows_t *x, const float *weight, const float *bias, const void *init, const void *dfin,
                        const ssd_rows_t *dx, float *dweight, float *dbias, void *dinit, void *ws, cudaStream_t st) {
     ConvArgs<T> a{};
+    a.weight = weight, a.bias = bias;
     const bool vec = fill<T>(s, nseq, x, dy, dx, {init, dfin, dinit}, a);
     a.dx = rows_of<T>(*dx);
-    a.weight = weight, a.bias = bias;
     a.init = static_cast<const T *>(init), a.dfinal = static_cast<const T *>(dfin);
     a.final_state = static_cast<T *>(dinit);
     a.partial = static_cast<float *>(ws);
@@ -595,8 +643,8 @@ template <typename T>
 ssd_status_t step_typed(const ssd_conv_shape_t *s, const ssd_rows_t *x, const float *weight, const float *bias,
                         void *state, const ssd_rows_t *y, cudaStream_t st) {
     ConvArgs<T> a{};
-    const bool vec = fill<T>(s, s->batch, x, y, nullptr, {state}, a);
     a.weight = weight, a.bias = bias;
+    const bool vec = fill<T>(s, s->batch, x, y, nullptr, {state}, a);
     return dispatch<kVec>(s->width, vec, [&](auto w, auto v) {
         const int64_t blocks = (s->batch * a.nvec + 127) / 128;
         if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;

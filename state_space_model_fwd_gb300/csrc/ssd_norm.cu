@@ -5,10 +5,10 @@
 //
 // the mean over groups of `group` columns; forward and gradient.  A few
 // operations an element against 2 to 6 element transfers: bound by memory.
-// A (row, group) is read once into registers by a team of threads, reduced
-// over the team, and written from registers.  The team is 32 to 1024 threads
-// with at most kMax values each, so that short rows share a block and long
-// rows fill one.
+// A (row, group) is read once, all its loads in flight together, reduced over
+// a team of threads and written from registers.  The team is a warp for short
+// groups, several to a block, and otherwise a block of just enough threads
+// for NV vectors each, so that few threads idle whatever the width.
 #include <type_traits>
 
 #include "ssd_layer.cuh"
@@ -16,8 +16,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kMaxPer = 32;  // values of a group that a thread holds at most
-constexpr int64_t kMaxGroup = 1024 * kMaxPer;
+constexpr int64_t kMaxGroup = 32768;
 
 enum Gate : int { kNone, kBefore, kAfter };
 
@@ -45,111 +44,127 @@ struct NormArgs {
     float eps;
 };
 
-// V consecutive values as fp32 and back, 16 bytes an access (V > 1).
-template <int V, typename T>
-__device__ __forceinline__ void load_f32(const T *p, float (&f)[V]) {
-    constexpr int W = V == 1 ? 1 : 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+// V consecutive elements as loaded: 16 bytes an access, or one element (V = 1).
+template <typename T, int V>
+struct Raw {
+    static constexpr int N = V == 1 ? 1 : V * (int)sizeof(T) / 16, W = V / N;
+    Vec<T, W> p[N];
+    __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-    for (int i = 0; i < V; i += W) widen<T, W>(load_vec<T, W>(p + i), f + i);
-}
-template <int V, typename T>
-__device__ __forceinline__ void store_f32(T *p, const float (&f)[V]) {
-    constexpr int W = V == 1 ? 1 : 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+        for (int i = 0; i < N; ++i) p[i] = load_vec<T, W>(src + i * W);
+    }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < V; i += W) store_vec<T, W>(p + i, narrow<T, W>(f + i));
+        for (int i = 0; i < N; ++i) p[i] = zero_vec<T, W>();
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) widen<T, W>(p[i], f + i * W);
+    }
+    static __device__ __forceinline__ void store(T *dst, const float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) store_vec<T, W>(dst + i * W, narrow<T, W>(f + i * W));
+    }
+};
+template <int V>
+__device__ __forceinline__ void load_param(const float *p, float (&f)[V]) {
+    Raw<float, V> r;
+    r.load(p);
+    r.get(f);
 }
 
-// Sum over a team of TEAM threads (a warp, several warps, or the block).
-template <int TEAM, int R>
-__device__ __forceinline__ void team_sum(float (&v)[R], float *smem, int tid) {
+// Sum over a team: a warp, or the whole block.
+template <bool WARP, int R>
+__device__ __forceinline__ void team_sum(float (&v)[R], float *smem) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], off);
-    if constexpr (TEAM > 32) {
-        constexpr int W = TEAM / 32;
-        const int warp = tid / 32, team = tid / TEAM;
+    if constexpr (!WARP) {
+        const int warps = blockDim.x / 32;
         __syncthreads();
-        if ((tid & 31) == 0)
+        if (threadIdx.x % 32 == 0)
 #pragma unroll
-            for (int r = 0; r < R; ++r) smem[warp * R + r] = v[r];
+            for (int r = 0; r < R; ++r) smem[threadIdx.x / 32 * R + r] = v[r];
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float s = 0.f;
-            for (int w = 0; w < W; ++w) s += smem[(team * W + w) * R + r];
-            v[r] = s;
-        }
+        for (int r = 0; r < R; ++r) v[r] = 0.f;
+        for (int w = 0; w < warps; ++w)
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r] += smem[w * R + r];
     }
 }
 
-template <int TEAM>
-constexpr int block_of_team() {
-    return TEAM < 256 ? 256 : TEAM;
-}
+constexpr int kWarpTeams = 4;  // warp teams per block
 
-// NV vectors of V values per thread: TEAM * NV * V >= group.
-template <typename T, typename TR, int V, int NV, int TEAM>
-__global__ void __launch_bounds__(block_of_team<TEAM>()) norm_fwd_kernel(const __grid_constant__ NormArgs<T, TR> a) {
-    constexpr int BLOCK = block_of_team<TEAM>();
-    __shared__ float smem[BLOCK / 32];
-    const int64_t id = (int64_t)blockIdx.x * (BLOCK / TEAM) + threadIdx.x / TEAM;
-    const bool live = id < a.rows * a.ngroups;
-    const int64_t row = live ? id / a.ngroups : 0;
-    const int c0 = live ? (int)(id % a.ngroups) * a.group : 0;
-    const int lane = threadIdx.x % TEAM;
+// NV vectors of V values per thread cover the group.
+template <typename T, typename TR, int V, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16 ? 1024 : 512, 1)
+    norm_fwd_kernel(const __grid_constant__ NormArgs<T, TR> a) {
+    __shared__ float smem[32];
+    const int team = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + threadIdx.x / 32 : blockIdx.x;
+    if (id >= a.rows * a.ngroups) return;  // (whole teams)
+    const int64_t row = id / a.ngroups;
+    const int c0 = (int)(id % a.ngroups) * a.group;
+    Raw<T, V> x[NV], z[NV];
+    Raw<TR, V> res[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int at = (i * team + lane) * V, c = c0 + at;
+        x[i].zero(), z[i].zero(), res[i].zero();
+        if (at < a.group) {
+            x[i].load(a.x + row * a.x_rs + c);
+            if (a.gate != kNone) z[i].load(a.z + row * a.z_rs + c);
+            if (a.res) res[i].load(a.res + row * a.res_rs + c);
+        }
+    }
     float s[NV][V];
     float sq[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int at = (i * TEAM + lane) * V, c = c0 + at;
-        if (live && at < a.group) load_f32<V>(a.x + row * a.x_rs + c, s[i]);
-    }
+        const int at = (i * team + lane) * V, c = c0 + at;
+        x[i].get(s[i]);
+        if (a.gate == kBefore) {
+            float f[V];
+            z[i].get(f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int at = (i * TEAM + lane) * V, c = c0 + at;
-        if (live && at < a.group) {
-            if (a.gate == kBefore) {
-                float z[V];
-                load_f32<V>(a.z + row * a.z_rs + c, z);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[i][v] *= silu(z[v]);
-            }
-            if (a.scale) {
-                float f[V];
-                load_f32<V>(a.scale + c, f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[i][v] *= f[v];
-            }
-            if (a.res) {
-                float r[V];
-                load_f32<V>(a.res + row * a.res_rs + c, r);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[i][v] += r[v];
-                store_f32<V>(a.res_out + row * a.res_out_rs + c, s[i]);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) sq[0] = fmaf(s[i][v], s[i][v], sq[0]);
+            for (int v = 0; v < V; ++v) s[i][v] *= silu(f[v]);
         }
+        if (a.scale && at < a.group) {
+            float f[V];
+            load_param<V>(a.scale + c, f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[i][v] *= f[v];
+        }
+        if (a.res) {
+            float f[V];
+            res[i].get(f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[i][v] += f[v];
+            if (at < a.group) Raw<TR, V>::store(a.res_out + row * a.res_out_rs + c, s[i]);
+        }
+        // (vectors past the group are zero)
+#pragma unroll
+        for (int v = 0; v < V; ++v) sq[0] = fmaf(s[i][v], s[i][v], sq[0]);
     }
-    team_sum<TEAM, 1>(sq, smem, threadIdx.x);
+    team_sum<WARP, 1>(sq, smem);
     const float rstd = rsqrtf(sq[0] / (float)a.group + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int at = (i * TEAM + lane) * V, c = c0 + at;
-        if (live && at < a.group) {
-            float w[V];
-            load_f32<V>(a.weight + c, w);
+        const int at = (i * team + lane) * V, c = c0 + at;
+        if (at >= a.group) break;
+        float w[V];
+        load_param<V>(a.weight + c, w);
 #pragma unroll
-            for (int v = 0; v < V; ++v) w[v] *= s[i][v] * rstd;
-            if (a.gate == kAfter) {
-                float z[V];
-                load_f32<V>(a.z + row * a.z_rs + c, z);
+        for (int v = 0; v < V; ++v) w[v] *= s[i][v] * rstd;
+        if (a.gate == kAfter) {
+            float f[V];
+            z[i].get(f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) w[v] *= silu(z[v]);
-            }
-            store_f32<V>(a.out + row * a.out_rs + c, w);
+            for (int v = 0; v < V; ++v) w[v] *= silu(f[v]);
         }
+        Raw<T, V>::store(a.out + row * a.out_rs + c, w);
     }
 }
 
@@ -157,55 +172,69 @@ __global__ void __launch_bounds__(block_of_team<TEAM>()) norm_fwd_kernel(const _
 //   ds = rstd (gw - hat mean(gw hat)) + dres,  both means from one reduction;
 //   dresidual = ds, dv = scale ds, dscale = sum_rows ds v, dweight = sum_rows dout (silu z) hat.
 // A team walks rows of its own group of columns, its column sums in
-// registers; the block's teams are added at the end, the blocks' partial
-// sums by a second kernel, both in a fixed order.  dout, x and z are read
-// again after the reduction (from L1 or L2) rather than held.
-template <typename T, typename TR, int V, int NV, int TEAM>
-__global__ void __launch_bounds__(block_of_team<TEAM>())
+// registers; the teams' partial sums are added by a second kernel in a fixed
+// order.
+template <typename T, typename TR, int V, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16 ? 1024 : 512, 1)
     norm_bwd_kernel(const __grid_constant__ NormArgs<T, TR> a, int slots) {
-    constexpr int BLOCK = block_of_team<TEAM>(), TEAMS = BLOCK / TEAM;
-    __shared__ float smem[BLOCK / 32 * 2];
-    const int g = blockIdx.x % a.ngroups, slot = blockIdx.x / a.ngroups;
-    const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM;
+    __shared__ float smem[64];
+    const int team = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + threadIdx.x / 32 : blockIdx.x;
+    if (id >= (int64_t)slots * a.ngroups) return;  // (whole teams)
+    const int g = (int)(id % a.ngroups), slot = (int)(id / a.ngroups);
     const int c0 = g * a.group;
     float dw[NV][V], dsc[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[i][v] = dsc[i][v] = 0.f;
-    const int64_t step = (int64_t)slots * TEAMS;
-    for (int64_t base = (int64_t)slot * TEAMS; base < a.rows; base += step) {  // block-uniform
-        const int64_t row = base + team;
-        const bool live = row < a.rows;
+    const bool need_x = !a.res || a.gate == kBefore || a.scale;
+    for (int64_t row = slot; row < a.rows; row += slots) {
+        Raw<T, V> x[NV], z[NV], go[NV];
+        Raw<TR, V> res[NV], dres[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * team + lane) * V, c = c0 + at;
+            x[i].zero(), z[i].zero(), go[i].zero(), res[i].zero(), dres[i].zero();
+            if (at < a.group) {
+                go[i].load(a.dout + row * a.dout_rs + c);
+                if (a.res) res[i].load(a.res + row * a.res_rs + c);
+                if (need_x) x[i].load(a.x + row * a.x_rs + c);
+                if (a.gate != kNone) z[i].load(a.z + row * a.z_rs + c);
+                if (a.dres) dres[i].load(a.dres + row * a.dres_rs + c);
+            }
+        }
         float s[NV][V];
         float sums[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int at = (i * TEAM + lane) * V, c = c0 + at;
-            if (live && at < a.group) {
-                float z[V], f[V], gw[V];
-                if (a.res)
-                    load_f32<V>(a.res + row * a.res_rs + c, s[i]);
-                else
-                    load_f32<V>(a.x + row * a.x_rs + c, s[i]);
-                load_f32<V>(a.dout + row * a.dout_rs + c, gw);
-                if (a.gate != kNone) {
-                    load_f32<V>(a.z + row * a.z_rs + c, z);
+            const int at = (i * team + lane) * V, c = c0 + at;
+            float gw[V];
+            go[i].get(gw);
+            if (a.res)
+                res[i].get(s[i]);
+            else
+                x[i].get(s[i]);
+            if (a.gate != kNone) {
+                float f[V];
+                z[i].get(f);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float gate = silu(z[v]);
-                        if (a.gate == kAfter)
-                            gw[v] *= gate;
-                        else if (!a.res)
-                            s[i][v] *= gate;
-                    }
+                for (int v = 0; v < V; ++v) {
+                    const float gate = silu(f[v]);
+                    if (a.gate == kAfter)
+                        gw[v] *= gate;
+                    else if (!a.res)
+                        s[i][v] *= gate;
                 }
+            }
+            if (at < a.group) {
+                float f[V];
                 if (a.scale && !a.res) {
-                    load_f32<V>(a.scale + c, f);
+                    load_param<V>(a.scale + c, f);
 #pragma unroll
                     for (int v = 0; v < V; ++v) s[i][v] *= f[v];
                 }
-                load_f32<V>(a.weight + c, f);
+                load_param<V>(a.weight + c, f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     sums[0] = fmaf(s[i][v], s[i][v], sums[0]);
@@ -213,91 +242,63 @@ __global__ void __launch_bounds__(block_of_team<TEAM>())
                 }
             }
         }
-        team_sum<TEAM, 2>(sums, smem, threadIdx.x);
+        team_sum<WARP, 2>(sums, smem);
         const float rstd = rsqrtf(sums[0] / (float)a.group + a.eps);
         const float proj = sums[1] / (float)a.group * rstd * rstd;  // mean(gw hat) rstd, per unit of s
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int at = (i * TEAM + lane) * V, c = c0 + at;
-            if (live && at < a.group) {
-                float z[V], f[V], go[V], dz[V], ds[V];
-                load_f32<V>(a.dout + row * a.dout_rs + c, go);
-                load_f32<V>(a.weight + c, f);
-                if (a.gate != kNone) load_f32<V>(a.z + row * a.z_rs + c, z);
+            const int at = (i * team + lane) * V, c = c0 + at;
+            if (at >= a.group) break;
+            float zf[V], f[V], gf[V], dz[V], ds[V];
+            go[i].get(gf);
+            z[i].get(zf);
+            load_param<V>(a.weight + c, f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float hat = s[i][v] * rstd;
+                if (a.gate == kAfter) {
+                    const float sg = sigmoid(zf[v]);
+                    dz[v] = gf[v] * hat * f[v] * silu_slope(zf[v], sg);
+                    gf[v] *= zf[v] * sg;
+                }
+                dw[i][v] = fmaf(gf[v], hat, dw[i][v]);
+                ds[v] = rstd * (gf[v] * f[v] - s[i][v] * proj);
+            }
+            if (a.res) {
+                dres[i].get(f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) ds[v] += f[v];
+                Raw<TR, V>::store(a.res_out + row * a.res_out_rs + c, ds);
+            }
+            float xv[V];
+            x[i].get(xv);
+            if (a.scale) {
+                load_param<V>(a.scale + c, f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float hat = s[i][v] * rstd;
-                    if (a.gate == kAfter) {
-                        const float sg = sigmoid(z[v]);
-                        dz[v] = go[v] * hat * f[v] * silu_slope(z[v], sg);
-                        go[v] *= z[v] * sg;
-                    }
-                    dw[i][v] = fmaf(go[v], hat, dw[i][v]);
-                    ds[v] = rstd * (go[v] * f[v] - s[i][v] * proj);
+                    dsc[i][v] = fmaf(ds[v], a.gate == kBefore ? xv[v] * silu(zf[v]) : xv[v], dsc[i][v]);
+                    ds[v] *= f[v];
                 }
-                if (a.res) {
-                    if (a.dres) {
-                        load_f32<V>(a.dres + row * a.dres_rs + c, f);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) ds[v] += f[v];
-                    }
-                    store_f32<V>(a.res_out + row * a.res_out_rs + c, ds);
-                }
-                float xv[V];
-                if (a.gate == kBefore || a.scale) load_f32<V>(a.x + row * a.x_rs + c, xv);
-                if (a.scale) {
-                    load_f32<V>(a.scale + c, f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        dsc[i][v] = fmaf(ds[v], a.gate == kBefore ? xv[v] * silu(z[v]) : xv[v], dsc[i][v]);
-                        ds[v] *= f[v];
-                    }
-                }
-                if (a.gate == kBefore) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float sg = sigmoid(z[v]);
-                        dz[v] = ds[v] * xv[v] * silu_slope(z[v], sg);
-                        ds[v] *= z[v] * sg;
-                    }
-                }
-                store_f32<V>(a.dx + row * a.dx_rs + c, ds);
-                if (a.gate != kNone) store_f32<V>(a.dz + row * a.dz_rs + c, dz);
             }
+            if (a.gate == kBefore) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float sg = sigmoid(zf[v]);
+                    dz[v] = ds[v] * xv[v] * silu_slope(zf[v], sg);
+                    ds[v] *= zf[v] * sg;
+                }
+            }
+            Raw<T, V>::store(a.dx + row * a.dx_rs + c, ds);
+            if (a.gate != kNone) Raw<T, V>::store(a.dz + row * a.dz_rs + c, dz);
         }
     }
-    // the block's teams, one after another, through shared memory
-    if constexpr (TEAMS == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int at = (i * TEAM + lane) * V;
-            if (at < a.group) {
+    for (int i = 0; i < NV; ++i) {
+        const int at = (i * team + lane) * V;
+        if (at >= a.group) break;
+        float *dst = a.partial + (int64_t)slot * 2 * a.dim + c0 + at;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    a.partial[(int64_t)slot * 2 * a.dim + c0 + at + v] = dw[i][v];
-                    a.partial[((int64_t)slot * 2 + 1) * a.dim + c0 + at + v] = dsc[i][v];
-                }
-            }
-        }
-    } else {
-        __shared__ float red[TEAMS][TEAM];
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    __syncthreads();
-                    red[team][lane] = k ? dsc[i][v] : dw[i][v];
-                    __syncthreads();
-                    const int at = (i * TEAM + lane) * V + v;
-                    if (team == 0 && at < a.group) {
-                        float t = 0.f;
-#pragma unroll
-                        for (int q = 0; q < TEAMS; ++q) t += red[q][lane];
-                        a.partial[((int64_t)slot * 2 + k) * a.dim + c0 + at] = t;
-                    }
-                }
+        for (int v = 0; v < V; ++v) dst[v] = dw[i][v], dst[a.dim + v] = dsc[i][v];
     }
 }
 
@@ -324,19 +325,21 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restric
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(V, NV, TEAM): the smallest team whose threads hold the group in 16 values
-// each (32 in the largest); one value at a time where rows are not 16-byte
+// f(V, NV, WARP, threads): a warp a group for up to 512 values, for more a
+// block of just enough warps; one value at a time where rows are not 16-byte
 // aligned.
 template <int VF, typename F>
 ssd_status_t pick_team(int64_t group, bool vec, F f) {
-    constexpr int F16 = 16 / VF;
-    if (!vec) return group <= 256 * 16 ? f(Int<1>{}, Int<16>{}, Int<256>{}) : f(Int<1>{}, Int<kMaxPer>{}, Int<1024>{});
-    if (group <= 32 * 16) return f(Int<VF>{}, Int<F16>{}, Int<32>{});
-    if (group <= 128 * 16) return f(Int<VF>{}, Int<F16>{}, Int<128>{});
-    if (group <= 256 * 16) return f(Int<VF>{}, Int<F16>{}, Int<256>{});
-    if (group <= 512 * 16) return f(Int<VF>{}, Int<F16>{}, Int<512>{});
-    if (group <= 1024 * 16) return f(Int<VF>{}, Int<F16>{}, Int<1024>{});
-    return f(Int<VF>{}, Int<2 * F16>{}, Int<1024>{});
+    auto threads = [](int64_t n, int nv) { return (int)((n + 32 * nv - 1) / (32 * nv) * 32); };
+    if (!vec) {
+        if (group <= 8192) return f(Int<1>{}, Int<8>{}, Int<0>{}, threads(group, 8));
+        return f(Int<1>{}, Int<32>{}, Int<0>{}, threads(group, 32));
+    }
+    constexpr int NV = 16 / VF;    // 16 values a thread
+    const int64_t n = group / VF;  // vectors
+    if (group <= 512) return f(Int<VF>{}, Int<NV>{}, Int<1>{}, 32);
+    if (group <= 8192) return f(Int<VF>{}, Int<NV>{}, Int<0>{}, threads(n, NV));
+    return f(Int<VF>{}, Int<2 * NV>{}, Int<0>{}, threads(n, 2 * NV));
 }
 
 ssd_status_t check(const ssd_norm_shape_t *s) {
@@ -348,11 +351,12 @@ ssd_status_t check(const ssd_norm_shape_t *s) {
     return SSD_OK;
 }
 
-// Blocks that share the rows of a group of columns in the gradient: four an
-// SM, or fewer where there are fewer rows.
+// Teams that share the rows of a group of columns in the gradient: enough to
+// fill the SMs (16 warps each), one at least for each row where there are few.
 int64_t bwd_slots(const ssd_norm_shape_t *s) {
-    const int64_t ngroups = s->dim / s->group_size;
-    int64_t slots = (152 * 4 + ngroups - 1) / ngroups;
+    const int64_t ngroups = s->dim / s->group_size, warps = (s->group_size + 511) / 512;
+    int64_t slots = 152 * 16 / (ngroups * warps);
+    if (slots < 1) slots = 1;
     if (slots > s->rows) slots = s->rows;
     return slots;
 }
@@ -381,13 +385,13 @@ ssd_status_t fwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *x, const flo
     if (res) vec = vec && rows_vec(*res, sizeof(TR), 1, s->rows) && rows_vec(*res_out, sizeof(TR), 1, s->rows);
     vec = vec && aligned(weight, 16) && aligned(scale, 16);
     a.gate = !z ? kNone : s->gate_after ? kAfter : kBefore;
-    return pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto team) {
-        constexpr int V = decltype(v)::value, NV = decltype(nv)::value, TEAM = decltype(team)::value;
-        constexpr int BLOCK = block_of_team<TEAM>();
-        const int64_t blocks = (s->rows * a.ngroups + BLOCK / TEAM - 1) / (BLOCK / TEAM);
+    return pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto w, int threads) {
+        constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+        constexpr bool WARP = decltype(w)::value;
+        const int64_t teams = s->rows * a.ngroups, blocks = WARP ? (teams + kWarpTeams - 1) / kWarpTeams : teams;
         if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
         timing_begin(st);
-        norm_fwd_kernel<T, TR, V, NV, TEAM><<<(unsigned)blocks, BLOCK, 0, st>>>(a);
+        norm_fwd_kernel<T, TR, V, NV, WARP><<<(unsigned)blocks, WARP ? kWarpTeams * 32 : threads, 0, st>>>(a);
         timing_mark(st, "norm_fwd");
         return status_of(cudaGetLastError());
     });
@@ -427,10 +431,13 @@ ssd_status_t bwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *dout, const 
     const int slots = (int)bwd_slots(s);
     timing_begin(st);
     if (slots > 0) {
-        const ssd_status_t e = pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto team) {
-            constexpr int V = decltype(v)::value, NV = decltype(nv)::value, TEAM = decltype(team)::value;
-            norm_bwd_kernel<T, TR, V, NV, TEAM>
-                <<<(unsigned)(slots * a.ngroups), block_of_team<TEAM>(), 0, st>>>(a, slots);
+        const ssd_status_t e = pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto w, int threads) {
+            constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+            constexpr bool WARP = decltype(w)::value;
+            const int64_t teams = (int64_t)slots * a.ngroups, blocks = WARP ? (teams + kWarpTeams - 1) / kWarpTeams : teams;
+            if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+            norm_bwd_kernel<T, TR, V, NV, WARP>
+                <<<(unsigned)blocks, WARP ? kWarpTeams * 32 : threads, 0, st>>>(a, slots);
             timing_mark(st, "norm_bwd");
             return status_of(cudaGetLastError());
         });
