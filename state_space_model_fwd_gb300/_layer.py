@@ -5,11 +5,13 @@ Token-major operands (x, y, gradients) may be strided views whose last
 dimension is contiguous, such as column slices of a projection's rows; states
 and parameters are contiguous.  ``cu_seqlens`` is a host sequence of
 nseq + 1 offsets as for ssd_fwd_varlen; without it every batch row is one
-sequence.  Argument marshalling only, as everywhere in this package.
+sequence.  Every function takes ``stream`` (the current one by default).
+Argument marshalling only, as everywhere in this package.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -75,74 +77,85 @@ def declare(lib):
         getattr(lib, name).restype = i32
 
 
+_LIB = None
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    global _LIB
+    if _LIB is None:
+        from . import load_library
+        _LIB = load_library()
+    return _LIB
 
 
-def _raise(fn, status):
+def _fail(fn, status):
     from . import _check
     _check(fn, status)
 
 
-def _stream_of(x, stream):
-    return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
+def _on_stream(fn):
+    """Adds ``stream``: the whole call, its allocations included, then belongs
+    to that stream instead of the current one."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
+# These run several times a call, and a call for one token takes a few
+# microseconds on the GPU: the checks that pass are few and plain.
 def _code(x, name="x"):
+    """(dtype code, device index)"""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     code = _CODE.get(x.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
-    return code
+    return code, x.get_device()
 
 
-def _rows(t, name, dtype, shape, dev):
-    """ssd_rows_t of a [b, L, ...] tensor whose trailing dimensions are
-    contiguous; of [b, ...] where ``shape`` has no token dimension."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
+def _refuse(t, name, dtype, shape, idx):
+    if not isinstance(t, torch.Tensor) or t.get_device() != idx:
+        raise TypeError(f"{name} must be a CUDA tensor on cuda:{idx}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _is(t, dtype, shape, idx):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == idx
+
+
+def _rows(t, name, dtype, shape, idx):
+    """ssd_rows_t of a [b, L, C] or [b, L, G, N] tensor whose trailing
+    dimensions are contiguous."""
+    if not _is(t, dtype, shape, idx):
+        _refuse(t, name, dtype, shape, idx)
     st = t.stride()
-    want = 1
-    for i in range(len(shape) - 1, 1, -1):
-        if st[i] != want and shape[i] > 1:
-            raise ValueError(f"{name} must be contiguous in its trailing dimensions")
-        want *= shape[i]
+    if (st[-1] != 1 and shape[-1] > 1) or (len(st) == 4 and st[2] != shape[3] and shape[2] > 1):
+        raise ValueError(f"{name} must be contiguous in its trailing dimensions")
     return _rows_t(t.data_ptr(), st[0], st[1])
 
 
-def _rows2(t, name, dtype, shape, dev):
-    """The same for one token per sequence, [b, ...] (no token dimension)."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _rows2(t, name, dtype, shape, idx):
+    """The same for one token per sequence: [b, C] or [b, G, N]."""
+    if not _is(t, dtype, shape, idx):
+        _refuse(t, name, dtype, shape, idx)
     st = t.stride()
-    want = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if st[i] != want and shape[i] > 1:
-            raise ValueError(f"{name} must be contiguous in its trailing dimensions")
-        want *= shape[i]
+    if (st[-1] != 1 and shape[-1] > 1) or (len(st) == 3 and st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous in its trailing dimensions")
     return _rows_t(t.data_ptr(), st[0], 0)
 
 
-def _flat(t, name, dtype, shape, dev):
+def _flat(t, name, dtype, shape, idx):
     """data pointer of a contiguous tensor; None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not _is(t, dtype, shape, idx):
+        _refuse(t, name, dtype, shape, idx)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -158,27 +171,32 @@ def _offsets(cu_seqlens, batch):
     return (ctypes.c_int64 * len(cu))(*cu), len(cu) - 1
 
 
-def _workspace(workspace, need, dev):
+def _empty(shape, dtype, x):
+    return torch.empty(shape, dtype=dtype, device=x.device)
+
+
+def _workspace(workspace, need, x):
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         return workspace
-    return torch.empty(max(need, 16), device=dev, dtype=torch.uint8)
+    return x.new_empty((max(need, 16),), dtype=torch.uint8)
 
 
 # ---------------------------------------------------------------------------
 # short causal convolution
 # ---------------------------------------------------------------------------
-def _conv_shape(x, weight, parts, silu):
+def _conv_shape(x, weight, parts, silu, code):
     if x.dim() != 3 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [b, L, C] and weight [C, W]")
     if not 1 <= len(parts) <= _MAX_PARTS:
         raise ValueError(f"1 to {_MAX_PARTS} parts, got {len(parts)}")
     b, L, C = x.shape
-    return _conv_shape_t(b, L, C, weight.shape[1], len(parts), (ctypes.c_int64 * _MAX_PARTS)(*parts), _code(x),
+    return _conv_shape_t(b, L, C, weight.shape[1], len(parts), (ctypes.c_int64 * _MAX_PARTS)(*parts), code,
                          1 if silu else 0)
 
 
+@_on_stream
 def ssd_conv_fwd(x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens=None, split=None, y=None,
-                 final_state=None, return_final_state=True, stream=None):
+                 final_state=None, return_final_state=True):
     """Causal depthwise convolution over the last W tokens with bias and SiLU.
 
     x [b, L, C], weight [C, W] fp32 (W 2 to 4), bias [C] fp32; the rows before
@@ -188,10 +206,10 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens
     contiguous tensors [b, L, width]: the x, B and C a scan takes.  ``y`` and
     ``final_state`` may be given; they must not overlap the inputs."""
     lib = _lib()
-    code = _code(x)
-    dev, dt = x.device, x.dtype
+    code, dev = _code(x)
+    dt = x.dtype
     parts = [x.shape[-1]] if split is None else [int(v) for v in split]
-    shape = _conv_shape(x, weight, parts, silu)
+    shape = _conv_shape(x, weight, parts, silu, code)
     b, L, C = x.shape
     W = weight.shape[1]
     cu, nseq = _offsets(cu_seqlens, b)
@@ -200,35 +218,37 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens
     bp = _flat(bias, "bias", _F32, (C,), dev)
     ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
     if y is None:
-        ys = [torch.empty((b, L, p), device=dev, dtype=dt) for p in parts]
+        ys = [_empty((b, L, p), x.dtype, x) for p in parts]
     else:
         ys = [y] if split is None else list(y)
         if len(ys) != len(parts):
             raise ValueError(f"y must hold {len(parts)} tensors")
     yr = (_rows_t * len(parts))(*[_rows(t, "y", dt, (b, L, p), dev) for t, p in zip(ys, parts)])
     if final_state is None and return_final_state:
-        final_state = torch.empty((nseq, W - 1, C), device=dev, dtype=dt)
+        final_state = _empty((nseq, W - 1, C), x.dtype, x)
     fp = _flat(final_state, "final_state", dt, (nseq, W - 1, C), dev)
-    if fp is not None and fp == ip:
+    if fp and fp == ip:
         raise ValueError("final_state must not be init_state")
-    with torch.cuda.device(dev):
-        _raise("ssd_conv_fwd", lib.ssd_conv_fwd(ctypes.byref(shape), cu, nseq, ctypes.byref(xr), wp, bp, ip, yr, fp,
-                                                _stream_of(x, stream)))
+    st = lib.ssd_conv_fwd(ctypes.byref(shape), cu, nseq, ctypes.byref(xr), wp, bp, ip, yr, fp,
+                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_conv_fwd", st)
     return (ys[0] if split is None else ys), final_state
 
 
+@_on_stream
 def ssd_conv_bwd(dy, x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens=None, dfinal_state=None, dx=None,
-                 workspace=None, stream=None):
+                 workspace=None):
     """Gradient of ssd_conv_fwd.  ``dy`` is a tensor [b, L, C] or the list of
     parts' gradients; ``dfinal_state`` [nseq, W-1, C] that of the final state
     (zero without it).  Returns ``(dx, dweight, dbias, dinit_state)``: dbias
     and dinit_state None where the input was None; dweight and dbias fp32."""
     lib = _lib()
-    _code(x)
-    dev, dt = x.device, x.dtype
+    code, dev = _code(x)
+    dt = x.dtype
     dys = [dy] if isinstance(dy, torch.Tensor) else list(dy)
     parts = [t.shape[-1] for t in dys]
-    shape = _conv_shape(x, weight, parts, silu)
+    shape = _conv_shape(x, weight, parts, silu, code)
     b, L, C = x.shape
     W = weight.shape[1]
     cu, nseq = _offsets(cu_seqlens, b)
@@ -239,28 +259,30 @@ def ssd_conv_bwd(dy, x, weight, bias=None, init_state=None, *, silu=True, cu_seq
     ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
     gp = _flat(dfinal_state, "dfinal_state", dt, (nseq, W - 1, C), dev)
     if dx is None:
-        dx = torch.empty((b, L, C), device=dev, dtype=dt)
+        dx = _empty((b, L, C), x.dtype, x)
     dxr = _rows(dx, "dx", dt, (b, L, C), dev)
-    dweight = torch.empty((C, W), device=dev, dtype=_F32)
-    dbias = None if bias is None else torch.empty((C,), device=dev, dtype=_F32)
-    dinit = None if init_state is None else torch.empty((nseq, W - 1, C), device=dev, dtype=dt)
-    workspace = _workspace(workspace, lib.ssd_conv_bwd_workspace_size(ctypes.byref(shape), cu, nseq), dev)
-    with torch.cuda.device(dev):
-        _raise("ssd_conv_bwd", lib.ssd_conv_bwd(
-            ctypes.byref(shape), cu, nseq, gr, ctypes.byref(xr), wp, bp, ip, gp, ctypes.byref(dxr), dweight.data_ptr(),
-            None if dbias is None else dbias.data_ptr(), None if dinit is None else dinit.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_of(x, stream)))
+    dweight = _empty((C, W), _F32, x)
+    dbias = None if bias is None else _empty((C,), _F32, x)
+    dinit = None if init_state is None else _empty((nseq, W - 1, C), x.dtype, x)
+    workspace = _workspace(workspace, lib.ssd_conv_bwd_workspace_size(ctypes.byref(shape), cu, nseq), x)
+    st = lib.ssd_conv_bwd(
+        ctypes.byref(shape), cu, nseq, gr, ctypes.byref(xr), wp, bp, ip, gp, ctypes.byref(dxr), dweight.data_ptr(),
+        None if dbias is None else dbias.data_ptr(), None if dinit is None else dinit.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_conv_bwd", st)
     return dx, dweight, dbias, dinit
 
 
-def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None, stream=None):
+@_on_stream
+def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None):
     """One token per sequence: x [b, C]; ``state`` [b, W-1, C], the rows before
     it, moves up by one in place.  Returns y [b, C]."""
     lib = _lib()
-    code = _code(x)
+    code, dev = _code(x)
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [b, C] and weight [C, W]")
-    dev, dt = x.device, x.dtype
+    dt = x.dtype
     b, C = x.shape
     W = weight.shape[1]
     xr = _rows2(x, "x", dt, (b, C), dev)
@@ -270,22 +292,23 @@ def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None, stream=None
         raise TypeError("state must be a CUDA tensor")
     sp = _flat(state, "state", dt, (b, W - 1, C), dev)
     if y is None:
-        y = torch.empty((b, C), device=dev, dtype=dt)
+        y = _empty((b, C), x.dtype, x)
     yr = _rows2(y, "y", dt, (b, C), dev)
     shape = _conv_shape_t(b, 1, C, W, 1, (ctypes.c_int64 * _MAX_PARTS)(C), code, 1 if silu else 0)
-    with torch.cuda.device(dev):
-        _raise("ssd_conv_step", lib.ssd_conv_step(ctypes.byref(shape), ctypes.byref(xr), wp, bp, sp, ctypes.byref(yr),
-                                                  _stream_of(x, stream)))
+    st = lib.ssd_conv_step(ctypes.byref(shape), ctypes.byref(xr), wp, bp, sp, ctypes.byref(yr),
+                           torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_conv_step", st)
     return y
 
 
 # ---------------------------------------------------------------------------
 # channel scan
 # ---------------------------------------------------------------------------
-def _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, rows, tok):
+def _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, rows, tok, dev):
     """(inputs struct, channels, states, groups); ``rows`` is _rows or _rows2
     and ``tok`` the leading dimensions (b, L) or (b,)."""
-    dev, ty = x.device, x.dtype
+    ty = x.dtype
     if x.dim() != len(tok) + 1 or not isinstance(B, torch.Tensor) or B.dim() != len(tok) + 2:
         raise ValueError("x must be [b, L, Ch] and B, C [b, L, G, N] (without L for one token)")
     ch = x.shape[-1]
@@ -299,9 +322,9 @@ def _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, rows, tok):
         _flat(init_state, "init_state", _F32, (nseq, ch, N), dev)), ch, N, G
 
 
+@_on_stream
 def ssd_channel_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, *, dt_softplus=True,
-                         cu_seqlens=None, y=None, final_state=None, return_final_state=True, workspace=None,
-                         stream=None):
+                         cu_seqlens=None, y=None, final_state=None, return_final_state=True, workspace=None):
     """Selective scan with a decay per channel and state:
 
         delta = softplus(dt + dt_bias)   (dt + dt_bias with dt_softplus=False)
@@ -311,108 +334,108 @@ def ssd_channel_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, init_stat
     D, dt_bias [Ch] fp32; states [nseq, Ch, N] fp32.  Returns
     ``(y, final_state)``."""
     lib = _lib()
-    code = _code(x)
+    code, dev = _code(x)
     if x.dim() != 3:
         raise ValueError("x must be [b, L, Ch]")
     b, L = x.shape[0], x.shape[1]
-    dev = x.device
     cu, nseq = _offsets(cu_seqlens, b)
-    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L))
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L), dev)
     if y is None:
-        y = torch.empty((b, L, ch), device=dev, dtype=x.dtype)
+        y = _empty((b, L, ch), x.dtype, x)
     yr = _rows(y, "y", x.dtype, (b, L, ch), dev)
     if final_state is None and return_final_state:
-        final_state = torch.empty((nseq, ch, N), device=dev, dtype=_F32)
+        final_state = _empty((nseq, ch, N), _F32, x)
     fp = _flat(final_state, "final_state", _F32, (nseq, ch, N), dev)
-    if fp is not None and fp == ins.init_state:
+    if fp and fp == ins.init_state:
         raise ValueError("final_state must not be init_state")
     shape = _channel_shape_t(b, L, ch, N, G, code, 1 if dt_softplus else 0)
-    with torch.cuda.device(dev):
-        need = lib.ssd_channel_scan_workspace_size(ctypes.byref(shape), cu, nseq)
-        ws = _workspace(workspace, need, dev) if need else None
-        _raise("ssd_channel_scan_fwd", lib.ssd_channel_scan_fwd(
-            ctypes.byref(shape), cu, nseq, ctypes.byref(ins), ctypes.byref(yr), fp, None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    need = lib.ssd_channel_scan_workspace_size(ctypes.byref(shape), cu, nseq)
+    ws = _workspace(workspace, need, x) if need else None
+    st = lib.ssd_channel_scan_fwd(
+        ctypes.byref(shape), cu, nseq, ctypes.byref(ins), ctypes.byref(yr), fp, None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_channel_scan_fwd", st)
     return y, final_state
 
 
+@_on_stream
 def ssd_channel_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, *, dt_softplus=True,
-                         cu_seqlens=None, dfinal_state=None, workspace=None, stream=None):
+                         cu_seqlens=None, dfinal_state=None, workspace=None):
     """Gradient of ssd_channel_scan_fwd from its inputs and dy (and that of the
     final state, zero without it).  Returns ``(dx, ddt, dA, dB, dC, dD, dz,
     ddt_bias, dinit_state)``, None where the input was None; dA, dD, ddt_bias
     and dinit_state in fp32, the others in x's type."""
     lib = _lib()
-    code = _code(x)
+    code, dev = _code(x)
     if x.dim() != 3:
         raise ValueError("x must be [b, L, Ch]")
     b, L = x.shape[0], x.shape[1]
-    dev, ty = x.device, x.dtype
+    ty = x.dtype
     cu, nseq = _offsets(cu_seqlens, b)
-    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L))
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L), dev)
     gr = _rows(dy, "dy", ty, (b, L, ch), dev)
     fp = _flat(dfinal_state, "dfinal_state", _F32, (nseq, ch, N), dev)
-    dx, ddt = (torch.empty((b, L, ch), device=dev, dtype=ty) for _ in range(2))
-    dz = None if z is None else torch.empty((b, L, ch), device=dev, dtype=ty)
-    dB, dC = (torch.empty((b, L, G, N), device=dev, dtype=ty) for _ in range(2))
-    dA = torch.empty((ch, N), device=dev, dtype=_F32)
-    dD = None if D is None else torch.empty((ch,), device=dev, dtype=_F32)
-    dbias = None if dt_bias is None else torch.empty((ch,), device=dev, dtype=_F32)
-    dinit = None if init_state is None else torch.empty((nseq, ch, N), device=dev, dtype=_F32)
+    dx, ddt = (_empty((b, L, ch), x.dtype, x) for _ in range(2))
+    dz = None if z is None else _empty((b, L, ch), x.dtype, x)
+    dB, dC = (_empty((b, L, G, N), x.dtype, x) for _ in range(2))
+    dA = _empty((ch, N), _F32, x)
+    dD = None if D is None else _empty((ch,), _F32, x)
+    dbias = None if dt_bias is None else _empty((ch,), _F32, x)
+    dinit = None if init_state is None else _empty((nseq, ch, N), _F32, x)
     row = lambda t, w: _rows_t(None, 0, 0) if t is None else _rows_t(t.data_ptr(), L * w, w)
     ptr = lambda t: None if t is None else t.data_ptr()
     grads = _channel_grads_t(row(dx, ch), row(ddt, ch), row(dz, ch), row(dB, G * N), row(dC, G * N), ptr(dA), ptr(dD),
                              ptr(dbias), ptr(dinit))
     shape = _channel_shape_t(b, L, ch, N, G, code, 1 if dt_softplus else 0)
-    with torch.cuda.device(dev):
-        ws = _workspace(workspace, lib.ssd_channel_scan_bwd_workspace_size(ctypes.byref(shape), cu, nseq), dev)
-        _raise("ssd_channel_scan_bwd", lib.ssd_channel_scan_bwd(
-            ctypes.byref(shape), cu, nseq, ctypes.byref(gr), ctypes.byref(ins), fp, ctypes.byref(grads), ws.data_ptr(),
-            ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    ws = _workspace(workspace, lib.ssd_channel_scan_bwd_workspace_size(ctypes.byref(shape), cu, nseq), x)
+    st = lib.ssd_channel_scan_bwd(
+        ctypes.byref(shape), cu, nseq, ctypes.byref(gr), ctypes.byref(ins), fp, ctypes.byref(grads), ws.data_ptr(),
+        ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_channel_scan_bwd", st)
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dinit
 
 
-def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state, dt_softplus=True, y=None,
-                          stream=None):
+@_on_stream
+def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state, dt_softplus=True, y=None):
     """One token per sequence: x, dt, z [b, Ch], B, C [b, G, N]; ``state``
     [b, Ch, N] fp32 is advanced in place.  Returns y [b, Ch]."""
     lib = _lib()
-    code = _code(x)
+    code, dev = _code(x)
     if x.dim() != 2:
         raise ValueError("x must be [b, Ch]")
     b = x.shape[0]
-    dev = x.device
-    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, None, b, _rows2, (b,))
+    ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, None, b, _rows2, (b,), dev)
     if state is None:
         raise TypeError("state must be a CUDA tensor")
     sp = _flat(state, "state", _F32, (b, ch, N), dev)
     if y is None:
-        y = torch.empty((b, ch), device=dev, dtype=x.dtype)
+        y = _empty((b, ch), x.dtype, x)
     yr = _rows2(y, "y", x.dtype, (b, ch), dev)
     shape = _channel_shape_t(b, 1, ch, N, G, code, 1 if dt_softplus else 0)
-    with torch.cuda.device(dev):
-        _raise("ssd_channel_scan_step", lib.ssd_channel_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp,
-                                                                  ctypes.byref(yr), _stream_of(x, stream)))
+    st = lib.ssd_channel_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp,
+                                   ctypes.byref(yr), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_channel_scan_step", st)
     return y
 
 
 # ---------------------------------------------------------------------------
 # block norm
 # ---------------------------------------------------------------------------
-def _norm_rows(t, name, dtype, shape, dev):
+def _norm_rows(t, name, dtype, shape, idx):
     """ssd_rows_t of a [..., dim] tensor whose rows lie at one stride; None
     for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a CUDA tensor on {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not _is(t, dtype, shape, idx):
+        _refuse(t, name, dtype, shape, idx)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    if len(st) == 2:
+        return _rows_t(t.data_ptr(), 0, st[0])
     rs = want = 0
     for i in range(len(shape) - 2, -1, -1):
         if shape[i] == 1:
@@ -431,16 +454,18 @@ def _ref(r):
 
 
 def _norm_shape(x, group_size, eps, residual, gate_after):
-    code = _code(x)
+    code, dev = _code(x)
     if x.dim() < 2:
         raise ValueError("x must be [..., dim]")
     dim = x.shape[-1]
-    rcode = code if residual is None else _code(residual, "residual")
-    return _norm_shape_t(x.numel() // dim if dim else 0, dim, group_size or dim, eps, code, rcode, 1 if gate_after else 0)
+    rcode = code if residual is None else _code(residual, "residual")[0]
+    return _norm_shape_t(x.numel() // dim if dim else 0, dim, group_size or dim, eps, code, rcode,
+                         1 if gate_after else 0), dev
 
 
+@_on_stream
 def ssd_block_norm_fwd(x, weight, *, z=None, residual=None, scale=None, eps=1e-5, group_size=None, gate_after=False,
-                       out=None, residual_out=None, stream=None):
+                       out=None, residual_out=None):
     """RMS norm before or after a block, with its gate and scaled residual:
 
         v = x * silu(z)  (x without z or with gate_after)
@@ -452,59 +477,62 @@ def ssd_block_norm_fwd(x, weight, *, z=None, residual=None, scale=None, eps=1e-5
     [dim] fp32.  Returns ``(out, residual_out)``, residual_out = s in the
     residual's type (None without a residual)."""
     lib = _lib()
-    shape = _norm_shape(x, group_size, eps, residual, gate_after)
-    dev, ty, full, dim = x.device, x.dtype, x.shape, x.shape[-1]
+    shape, dev = _norm_shape(x, group_size, eps, residual, gate_after)
+    ty, full, dim = x.dtype, x.shape, x.shape[-1]
     xr = _norm_rows(x, "x", ty, full, dev)
     zr = _norm_rows(z, "z", ty, full, dev)
     wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
     if out is None:
-        out = torch.empty(full, device=dev, dtype=ty)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     outr = _norm_rows(out, "out", ty, full, dev)
     rr = ror = None
     if residual is not None:
         rr = _norm_rows(residual, "residual", residual.dtype, full, dev)
         if residual_out is None:
-            residual_out = torch.empty(full, device=dev, dtype=residual.dtype)
+            residual_out = _empty(full, residual.dtype, x)
         ror = _norm_rows(residual_out, "residual_out", residual.dtype, full, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    with torch.cuda.device(dev):
-        _raise("ssd_block_norm_fwd", lib.ssd_block_norm_fwd(ctypes.byref(shape), _ref(xr), wp, _ref(zr), _ref(rr), sp,
-                                                            _ref(outr), _ref(ror), _stream_of(x, stream)))
+    st = lib.ssd_block_norm_fwd(ctypes.byref(shape), _ref(xr), wp, _ref(zr), _ref(rr), sp,
+                                _ref(outr), _ref(ror), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_block_norm_fwd", st)
     return out, residual_out
 
 
+@_on_stream
 def ssd_block_norm_bwd(dout, x, weight, *, z=None, scale=None, residual_out=None, dresidual_out=None, eps=1e-5,
-                       group_size=None, gate_after=False, workspace=None, stream=None):
+                       group_size=None, gate_after=False, workspace=None):
     """Gradient of ssd_block_norm_fwd.  ``residual_out`` is the sum the forward
     call returned (where it had a residual) and ``dresidual_out`` the gradient
     of its other uses (zero without it).  Returns ``(dx, dweight, dz,
     dresidual, dscale)``, None where the input was None."""
     lib = _lib()
-    shape = _norm_shape(x, group_size, eps, residual_out, gate_after)
-    dev, ty, full, dim = x.device, x.dtype, x.shape, x.shape[-1]
+    shape, dev = _norm_shape(x, group_size, eps, residual_out, gate_after)
+    ty, full, dim = x.dtype, x.shape, x.shape[-1]
     gr, xr = _norm_rows(dout, "dout", ty, full, dev), _norm_rows(x, "x", ty, full, dev)
     if gr is None:
         raise TypeError("dout must be a CUDA tensor")
     zr = _norm_rows(z, "z", ty, full, dev)
     wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
-    dx = torch.empty(full, device=dev, dtype=ty)
-    dz = None if z is None else torch.empty(full, device=dev, dtype=ty)
-    dweight = torch.empty((dim,), device=dev, dtype=_F32)
-    dscale = None if scale is None else torch.empty((dim,), device=dev, dtype=_F32)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dz = None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format)
+    dweight = _empty((dim,), _F32, x)
+    dscale = None if scale is None else _empty((dim,), _F32, x)
     sr = dsr = drr = dres = None
     if residual_out is not None:
         sr = _norm_rows(residual_out, "residual_out", residual_out.dtype, full, dev)
         dsr = _norm_rows(dresidual_out, "dresidual_out", residual_out.dtype, full, dev)
-        dres = torch.empty(full, device=dev, dtype=residual_out.dtype)
+        dres = _empty(full, residual_out.dtype, x)
         drr = _norm_rows(dres, "dresidual", residual_out.dtype, full, dev)
     elif dresidual_out is not None:
         raise ValueError("dresidual_out needs residual_out")
     dxr, dzr = _norm_rows(dx, "dx", ty, full, dev), _norm_rows(dz, "dz", ty, full, dev)
-    with torch.cuda.device(dev):
-        ws = _workspace(workspace, lib.ssd_block_norm_bwd_workspace_size(ctypes.byref(shape)), dev)
-        _raise("ssd_block_norm_bwd", lib.ssd_block_norm_bwd(
-            ctypes.byref(shape), _ref(gr), _ref(xr), wp, _ref(zr), sp, _ref(sr), _ref(dsr), _ref(dxr),
-            dweight.data_ptr(), _ref(dzr), _ref(drr), None if dscale is None else dscale.data_ptr(), ws.data_ptr(),
-            ws.numel() * ws.element_size(), _stream_of(x, stream)))
+    ws = _workspace(workspace, lib.ssd_block_norm_bwd_workspace_size(ctypes.byref(shape)), x)
+    st = lib.ssd_block_norm_bwd(
+        ctypes.byref(shape), _ref(gr), _ref(xr), wp, _ref(zr), sp, _ref(sr), _ref(dsr), _ref(dxr),
+        dweight.data_ptr(), _ref(dzr), _ref(drr), None if dscale is None else dscale.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_block_norm_bwd", st)
     return dx, dweight, dz, dres, dscale

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kLanes *kSub, 2) conv_fwd_kernel(const __grid_
 // sums over tokens stay in fp32 registers over all tiles of a block, are
 // added over the block's warps, and the blocks' partial sums by a second
 // kernel in a fixed order.
-template <typename T, int W, int V, bool PACKED, typename Set>
+template <typename T, int W, int V, bool PACKED, bool SILU, typename Set>
 __global__ void __launch_bounds__(kLanes *kSub, 2) conv_bwd_kernel(const __grid_constant__ ConvArgs<T> a,
                                                                 const __grid_constant__ Set set, int slots, int slot0) {
     if (blockIdx.x >= a.tblocks) {
@@ -291,60 +291,72 @@ __global__ void __launch_bounds__(kLanes *kSub, 2) conv_bwd_kernel(const __grid_
 #pragma unroll
                     for (int v2 = 0; v2 < V; ++v2) dpw[j][v2] = 0.f;
                 }
-                const int end = p.e + W - 1;
-                for (int t = p.a; t < end; t += kStep) {
-                    float c[kStep][V], dp[kStep][V], o[kStep][V];
+                // one token: dp from x and dy, dweight's and dbias' terms, and the row that it completes
+                auto token = [&](auto inside, const float (&c)[V], float (&g)[V], bool in_seq, bool mine, float (&o)[V]) {
+                    float old[W - 1][V], s[V];
 #pragma unroll
-                    for (int i = 0; i < kStep; ++i) widen<T, V>(nx[i], c[i]), widen<T, V>(ng[i], dp[i]);
-                    if (t + kStep < end) fetch(t + kStep);
+                    for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-                    for (int i = 0; i < kStep; ++i) {
-                        float old[W - 1][V], s[V];
+                        for (int v = 0; v < V; ++v) old[k][v] = win[k][v];
+                    taps<W, V>(w, bias, win, c, s);
+                    if constexpr (SILU) {
 #pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                            for (int v = 0; v < V; ++v) old[k][v] = win[k][v];
-                        taps<W, V>(w, bias, win, c[i], s);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            if (a.use_silu) dp[i][v] *= silu_slope(s[v], sigmoid(s[v]));
-                            dp[i][v] = t + i < p.E ? dp[i][v] : 0.f;
-                            const float own = t + i < p.e ? dp[i][v] : 0.f;
-#pragma unroll
-                            for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(own, old[k][v], dw[k][v]);
-                            dw[W - 1][v] = fmaf(own, c[i][v], dw[W - 1][v]);
-                            db[v] += own;
-                            // row t + i - (W-1) is complete; dpw holds the last W-1 dp
-                            float r = w[0][v] * dp[i][v];
-#pragma unroll
-                            for (int k = 1; k < W; ++k) r = fmaf(w[k][v], dpw[W - 1 - k][v], r);
-                            o[i][v] = r;
-#pragma unroll
-                            for (int k = 0; k + 1 < W - 1; ++k) dpw[k][v] = dpw[k + 1][v];
-                            dpw[W - 2][v] = dp[i][v];
-                        }
+                        for (int v = 0; v < V; ++v) g[v] *= silu_slope(s[v], sigmoid(s[v]));
                     }
-                    const int r0 = t - (W - 1);
-                    if (r0 >= p.a && r0 + kStep <= min(p.e, tail)) {
 #pragma unroll
-                        for (int i = 0; i < kStep; ++i) store_vec<T, V>(dx.at(row, r0 + i), narrow<T, V>(o[i]));
+                    for (int v = 0; v < V; ++v) {
+                        if constexpr (!decltype(inside)::value) g[v] = in_seq ? g[v] : 0.f;
+                        float own = g[v];
+                        if constexpr (!decltype(inside)::value) own = mine ? own : 0.f;
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(own, old[k][v], dw[k][v]);
+                        dw[W - 1][v] = fmaf(own, c[v], dw[W - 1][v]);
+                        db[v] += own;
+                        // dpw holds the last W-1 dp
+                        float r = w[0][v] * g[v];
+#pragma unroll
+                        for (int k = 1; k < W; ++k) r = fmaf(w[k][v], dpw[W - 1 - k][v], r);
+                        o[v] = r;
+#pragma unroll
+                        for (int k = 0; k + 1 < W - 1; ++k) dpw[k][v] = dpw[k + 1][v];
+                        dpw[W - 2][v] = g[v];
+                    }
+                };
+                const int end = p.e + W - 1, plain = min(p.e, tail);
+                for (int t = p.a; t < end; t += kStep) {
+                    const int r0 = t - (W - 1);
+                    Vec<T, V> cx[kStep], cg[kStep];
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) cx[i] = nx[i], cg[i] = ng[i];
+                    if (t + kStep < end) fetch(t + kStep);
+                    if (r0 >= p.a && t + kStep <= plain) {  // nothing special about these tokens and rows
+#pragma unroll
+                        for (int i = 0; i < kStep; ++i) {
+                            float c[V], g[V], o[V];
+                            widen<T, V>(cx[i], c), widen<T, V>(cg[i], g);
+                            token(std::true_type{}, c, g, true, true, o);
+                            store_vec<T, V>(dx.at(row, r0 + i), narrow<T, V>(o));
+                        }
                         continue;
                     }
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
+                        float c[V], g[V], o[V];
+                        widen<T, V>(cx[i], c), widen<T, V>(cg[i], g);
+                        token(std::false_type{}, c, g, t + i < p.E, t + i < p.e, o);
                         const int r = r0 + i;
                         if (r >= p.e || (r < p.a && !back)) continue;
                         if (a.dfinal && r >= tail) {
                             float f[V];
                             widen<T, V>(load_vec<T, V>(a.dfinal + ((int64_t)p.s * (W - 1) + (r - tail)) * a.C + c0), f);
 #pragma unroll
-                            for (int v = 0; v < V; ++v) o[i][v] += f[v];
+                            for (int v = 0; v < V; ++v) o[v] += f[v];
                         }
                         if (r >= p.a)
-                            store_vec<T, V>(dx.at(row, r), narrow<T, V>(o[i]));
+                            store_vec<T, V>(dx.at(row, r), narrow<T, V>(o));
                         else
                             store_vec<T, V>(a.final_state + ((int64_t)p.s * (W - 1) + (r - p.S + W - 1)) * a.C + c0,
-                                            narrow<T, V>(o[i]));
+                                            narrow<T, V>(o));
                     }
                 }
             });
@@ -566,7 +578,10 @@ ssd_status_t launch_bwd(ConvArgs<T> &a, const ssd_conv_shape_t *s, const Set &se
     *used = slots;
     if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
     if (blocks == 0) return SSD_OK;
-    conv_bwd_kernel<T, W, V, PACKED, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set, slots, slot0);
+    if (a.use_silu)
+        conv_bwd_kernel<T, W, V, PACKED, true, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set, slots, slot0);
+    else
+        conv_bwd_kernel<T, W, V, PACKED, false, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set, slots, slot0);
     timing_mark(st, "conv_bwd");
     return status_of(cudaGetLastError());
 }

@@ -20,28 +20,29 @@ constexpr int64_t kMaxGroup = 32768;
 
 enum Gate : int { kNone, kBefore, kAfter };
 
+// A [rows, dim] array; a thread's place in it.
+template <typename T>
+struct Mat {
+    T *p;
+    int64_t rs;
+    __device__ __forceinline__ T *at(int64_t row, int c) const { return p + row * rs + c; }
+};
+
 template <typename T, typename TR>
 struct NormArgs {
-    const T *x, *z;
-    int64_t x_rs, z_rs;
-    const TR *res;  // forward: the residual; gradient: the stored sum
-    int64_t res_rs;
+    Mat<const T> x, z;
+    Mat<const TR> res;  // forward: the residual; gradient: the stored sum (p null: none)
     const float *weight, *scale;
-    T *out;
-    int64_t out_rs;
-    TR *res_out;  // forward: the sum; gradient: the residual's gradient
-    int64_t res_out_rs;
+    Mat<T> out;
+    Mat<TR> res_out;  // forward: the sum; gradient: the residual's gradient
     // gradient
-    const T *dout;
-    int64_t dout_rs;
-    const TR *dres;  // gradient of the sum from elsewhere (null: zero)
-    int64_t dres_rs;
-    T *dx, *dz;
-    int64_t dx_rs, dz_rs;
+    Mat<const T> dout;
+    Mat<const TR> dres;  // gradient of the sum from elsewhere (p null: zero)
+    Mat<T> dx, dz;
     float *partial;  // [slots][2][dim]: dweight, dscale
     int64_t rows;
     int dim, group, ngroups, gate;
-    float eps;
+    float eps, inv_group;
 };
 
 // V consecutive elements as loaded: 16 bytes an access, or one element (V = 1).
@@ -73,16 +74,16 @@ __device__ __forceinline__ void load_param(const float *p, float (&f)[V]) {
     r.get(f);
 }
 
-// Sum over a team: a warp, or the whole block.
+// Sum over a team: a warp, or the whole block (one barrier; the caller
+// alternates between two arrays when it sums again).
 template <bool WARP, int R>
-__device__ __forceinline__ void team_sum(float (&v)[R], float *smem) {
+__device__ __forceinline__ void team_sum(float (&v)[R], float (&smem)[32 * R]) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], off);
     if constexpr (!WARP) {
         const int warps = blockDim.x / 32;
-        __syncthreads();
         if (threadIdx.x % 32 == 0)
 #pragma unroll
             for (int r = 0; r < R; ++r) smem[threadIdx.x / 32 * R + r] = v[r];
@@ -96,17 +97,19 @@ __device__ __forceinline__ void team_sum(float (&v)[R], float *smem) {
 }
 
 constexpr int kWarpTeams = 4;  // warp teams per block
+constexpr int kAnyGate = -1;   // the gate is read at run time (rare widths)
 
 // NV vectors of V values per thread cover the group.
-template <typename T, typename TR, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16 ? 1024 : 512, 1)
+template <typename T, typename TR, int V, int NV, bool WARP, int GATE>
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 1024 : 512, 1)
     norm_fwd_kernel(const __grid_constant__ NormArgs<T, TR> a) {
     __shared__ float smem[32];
+    const int gate = GATE == kAnyGate ? a.gate : GATE;
     const int team = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x % 32 : threadIdx.x;
     const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + threadIdx.x / 32 : blockIdx.x;
     if (id >= a.rows * a.ngroups) return;  // (whole teams)
-    const int64_t row = id / a.ngroups;
-    const int c0 = (int)(id % a.ngroups) * a.group;
+    const int64_t row = a.ngroups == 1 ? id : id / a.ngroups;
+    const int c0 = a.ngroups == 1 ? 0 : (int)(id % a.ngroups) * a.group;
     Raw<T, V> x[NV], z[NV];
     Raw<TR, V> res[NV];
 #pragma unroll
@@ -114,9 +117,9 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
         const int at = (i * team + lane) * V, c = c0 + at;
         x[i].zero(), z[i].zero(), res[i].zero();
         if (at < a.group) {
-            x[i].load(a.x + row * a.x_rs + c);
-            if (a.gate != kNone) z[i].load(a.z + row * a.z_rs + c);
-            if (a.res) res[i].load(a.res + row * a.res_rs + c);
+            x[i].load(a.x.at(row, c));
+            if (gate != kNone) z[i].load(a.z.at(row, c));
+            if (a.res.p) res[i].load(a.res.at(row, c));
         }
     }
     float s[NV][V];
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
     for (int i = 0; i < NV; ++i) {
         const int at = (i * team + lane) * V, c = c0 + at;
         x[i].get(s[i]);
-        if (a.gate == kBefore) {
+        if (gate == kBefore) {
             float f[V];
             z[i].get(f);
 #pragma unroll
@@ -137,19 +140,19 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
 #pragma unroll
             for (int v = 0; v < V; ++v) s[i][v] *= f[v];
         }
-        if (a.res) {
+        if (a.res.p) {
             float f[V];
             res[i].get(f);
 #pragma unroll
             for (int v = 0; v < V; ++v) s[i][v] += f[v];
-            if (at < a.group) Raw<TR, V>::store(a.res_out + row * a.res_out_rs + c, s[i]);
+            if (at < a.group) Raw<TR, V>::store(a.res_out.at(row, c), s[i]);
         }
         // (vectors past the group are zero)
 #pragma unroll
         for (int v = 0; v < V; ++v) sq[0] = fmaf(s[i][v], s[i][v], sq[0]);
     }
     team_sum<WARP, 1>(sq, smem);
-    const float rstd = rsqrtf(sq[0] / (float)a.group + a.eps);
+    const float rstd = rsqrtf(fmaf(sq[0], a.inv_group, a.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int at = (i * team + lane) * V, c = c0 + at;
@@ -158,13 +161,13 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
         load_param<V>(a.weight + c, w);
 #pragma unroll
         for (int v = 0; v < V; ++v) w[v] *= s[i][v] * rstd;
-        if (a.gate == kAfter) {
+        if (gate == kAfter) {
             float f[V];
             z[i].get(f);
 #pragma unroll
             for (int v = 0; v < V; ++v) w[v] *= silu(f[v]);
         }
-        Raw<T, V>::store(a.out + row * a.out_rs + c, w);
+        Raw<T, V>::store(a.out.at(row, c), w);
     }
 }
 
@@ -174,10 +177,11 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
 // A team walks rows of its own group of columns, its column sums in
 // registers; the teams' partial sums are added by a second kernel in a fixed
 // order.
-template <typename T, typename TR, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16 ? 1024 : 512, 1)
+template <typename T, typename TR, int V, int NV, bool WARP, int GATE>
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 1024 : 512, WARP ? 3 : 1)
     norm_bwd_kernel(const __grid_constant__ NormArgs<T, TR> a, int slots) {
-    __shared__ float smem[64];
+    __shared__ float smem[2][64];
+    const int gate = GATE == kAnyGate ? a.gate : GATE;
     const int team = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x % 32 : threadIdx.x;
     const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + threadIdx.x / 32 : blockIdx.x;
     if (id >= (int64_t)slots * a.ngroups) return;  // (whole teams)
@@ -188,8 +192,9 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[i][v] = dsc[i][v] = 0.f;
-    const bool need_x = !a.res || a.gate == kBefore || a.scale;
-    for (int64_t row = slot; row < a.rows; row += slots) {
+    const bool need_x = !a.res.p || gate == kBefore || a.scale;
+    int turn = 0;
+    for (int64_t row = slot; row < a.rows; row += slots, turn ^= 1) {
         Raw<T, V> x[NV], z[NV], go[NV];
         Raw<TR, V> res[NV], dres[NV];
 #pragma unroll
@@ -197,90 +202,93 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
             const int at = (i * team + lane) * V, c = c0 + at;
             x[i].zero(), z[i].zero(), go[i].zero(), res[i].zero(), dres[i].zero();
             if (at < a.group) {
-                go[i].load(a.dout + row * a.dout_rs + c);
-                if (a.res) res[i].load(a.res + row * a.res_rs + c);
-                if (need_x) x[i].load(a.x + row * a.x_rs + c);
-                if (a.gate != kNone) z[i].load(a.z + row * a.z_rs + c);
-                if (a.dres) dres[i].load(a.dres + row * a.dres_rs + c);
+                go[i].load(a.dout.at(row, c));
+                if (a.res.p) res[i].load(a.res.at(row, c));
+                if (need_x) x[i].load(a.x.at(row, c));
+                if (gate != kNone) z[i].load(a.z.at(row, c));
+                if (a.dres.p) dres[i].load(a.dres.at(row, c));
             }
         }
-        float s[NV][V];
+        float s[NV][V], w[NV][V];
         float sums[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = (i * team + lane) * V, c = c0 + at;
             float gw[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) w[i][v] = 0.f;
+            if (at < a.group) load_param<V>(a.weight + c, w[i]);
             go[i].get(gw);
-            if (a.res)
+            if (a.res.p)
                 res[i].get(s[i]);
             else
                 x[i].get(s[i]);
-            if (a.gate != kNone) {
+            if (gate != kNone) {
                 float f[V];
                 z[i].get(f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float gate = silu(f[v]);
-                    if (a.gate == kAfter)
-                        gw[v] *= gate;
-                    else if (!a.res)
-                        s[i][v] *= gate;
-                }
-            }
-            if (at < a.group) {
-                float f[V];
-                if (a.scale && !a.res) {
-                    load_param<V>(a.scale + c, f);
+                for (int v = 0; v < V; ++v) f[v] = silu(f[v]);
+                if (gate == kAfter) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) gw[v] *= f[v];
+                } else if (!a.res.p) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) s[i][v] *= f[v];
                 }
-                load_param<V>(a.weight + c, f);
+            }
+            if (a.scale && !a.res.p && at < a.group) {
+                float f[V];
+                load_param<V>(a.scale + c, f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    sums[0] = fmaf(s[i][v], s[i][v], sums[0]);
-                    sums[1] = fmaf(gw[v] * f[v], s[i][v], sums[1]);
-                }
+                for (int v = 0; v < V; ++v) s[i][v] *= f[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                sums[0] = fmaf(s[i][v], s[i][v], sums[0]);
+                sums[1] = fmaf(gw[v] * w[i][v], s[i][v], sums[1]);
             }
         }
-        team_sum<WARP, 2>(sums, smem);
-        const float rstd = rsqrtf(sums[0] / (float)a.group + a.eps);
-        const float proj = sums[1] / (float)a.group * rstd * rstd;  // mean(gw hat) rstd, per unit of s
+        team_sum<WARP, 2>(sums, smem[turn]);
+        const float rstd = rsqrtf(fmaf(sums[0], a.inv_group, a.eps));
+        const float proj = sums[1] * a.inv_group * rstd * rstd * rstd;  // mean(gw hat) rstd, per unit of s
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = (i * team + lane) * V, c = c0 + at;
             if (at >= a.group) break;
-            float zf[V], f[V], gf[V], dz[V], ds[V];
+            float zf[V], gf[V], dz[V], ds[V];
             go[i].get(gf);
-            z[i].get(zf);
-            load_param<V>(a.weight + c, f);
+            if (gate != kNone) z[i].get(zf);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float hat = s[i][v] * rstd;
-                if (a.gate == kAfter) {
+                if (gate == kAfter) {
                     const float sg = sigmoid(zf[v]);
-                    dz[v] = gf[v] * hat * f[v] * silu_slope(zf[v], sg);
+                    dz[v] = gf[v] * hat * w[i][v] * silu_slope(zf[v], sg);
                     gf[v] *= zf[v] * sg;
                 }
                 dw[i][v] = fmaf(gf[v], hat, dw[i][v]);
-                ds[v] = rstd * (gf[v] * f[v] - s[i][v] * proj);
+                ds[v] = fmaf(-proj, s[i][v], rstd * (gf[v] * w[i][v]));
             }
-            if (a.res) {
+            if (a.res.p) {
+                float f[V];
                 dres[i].get(f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) ds[v] += f[v];
-                Raw<TR, V>::store(a.res_out + row * a.res_out_rs + c, ds);
+                Raw<TR, V>::store(a.res_out.at(row, c), ds);
             }
-            float xv[V];
-            x[i].get(xv);
             if (a.scale) {
+                float f[V], xv[V];
+                x[i].get(xv);
                 load_param<V>(a.scale + c, f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    dsc[i][v] = fmaf(ds[v], a.gate == kBefore ? xv[v] * silu(zf[v]) : xv[v], dsc[i][v]);
+                    dsc[i][v] = fmaf(ds[v], gate == kBefore ? xv[v] * silu(zf[v]) : xv[v], dsc[i][v]);
                     ds[v] *= f[v];
                 }
             }
-            if (a.gate == kBefore) {
+            if (gate == kBefore) {
+                float xv[V];
+                x[i].get(xv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float sg = sigmoid(zf[v]);
@@ -288,8 +296,8 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : V == 1 || NV * V > 16
                     ds[v] *= zf[v] * sg;
                 }
             }
-            Raw<T, V>::store(a.dx + row * a.dx_rs + c, ds);
-            if (a.gate != kNone) Raw<T, V>::store(a.dz + row * a.dz_rs + c, dz);
+            Raw<T, V>::store(a.dx.at(row, c), ds);
+            if (gate != kNone) Raw<T, V>::store(a.dz.at(row, c), dz);
         }
     }
 #pragma unroll
@@ -325,21 +333,25 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restric
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(V, NV, WARP, threads): a warp a group for up to 512 values, for more a
-// block of just enough warps; one value at a time where rows are not 16-byte
-// aligned.
+// f(V, NV, WARP, GATE, threads): a warp a group for up to 512 values, for
+// more a block of just enough warps; one value at a time where rows are not
+// 16-byte aligned.
 template <int VF, typename F>
-ssd_status_t pick_team(int64_t group, bool vec, F f) {
+ssd_status_t pick_team(int64_t group, bool vec, int gate, F f) {
     auto threads = [](int64_t n, int nv) { return (int)((n + 32 * nv - 1) / (32 * nv) * 32); };
     if (!vec) {
-        if (group <= 8192) return f(Int<1>{}, Int<8>{}, Int<0>{}, threads(group, 8));
-        return f(Int<1>{}, Int<32>{}, Int<0>{}, threads(group, 32));
+        if (group <= 8192) return f(Int<1>{}, Int<8>{}, Int<0>{}, Int<kAnyGate>{}, threads(group, 8));
+        return f(Int<1>{}, Int<32>{}, Int<0>{}, Int<kAnyGate>{}, threads(group, 32));
     }
-    constexpr int NV = 16 / VF;    // 16 values a thread
-    const int64_t n = group / VF;  // vectors
-    if (group <= 512) return f(Int<VF>{}, Int<NV>{}, Int<1>{}, 32);
-    if (group <= 8192) return f(Int<VF>{}, Int<NV>{}, Int<0>{}, threads(n, NV));
-    return f(Int<VF>{}, Int<2 * NV>{}, Int<0>{}, threads(n, 2 * NV));
+    constexpr int NV = 16 / VF;  // 16 values a thread
+    const int64_t n = group / VF;
+    if (group > 8192) return f(Int<VF>{}, Int<2 * NV>{}, Int<0>{}, Int<kAnyGate>{}, threads(n, 2 * NV));
+    auto gated = [&](auto w, int t) {
+        if (gate == kNone) return f(Int<VF>{}, Int<NV>{}, w, Int<kNone>{}, t);
+        if (gate == kBefore) return f(Int<VF>{}, Int<NV>{}, w, Int<kBefore>{}, t);
+        return f(Int<VF>{}, Int<NV>{}, w, Int<kAfter>{}, t);
+    };
+    return group <= 512 ? gated(Int<1>{}, 32) : gated(Int<0>{}, threads(n, NV));
 }
 
 ssd_status_t check(const ssd_norm_shape_t *s) {
@@ -351,11 +363,12 @@ ssd_status_t check(const ssd_norm_shape_t *s) {
     return SSD_OK;
 }
 
-// Teams that share the rows of a group of columns in the gradient: enough to
-// fill the SMs (16 warps each), one at least for each row where there are few.
+// Teams that share the rows of a group of columns in the gradient: one wave
+// of the 12 (warp teams) or 15 warps that fit an SM beside each other.
 int64_t bwd_slots(const ssd_norm_shape_t *s) {
     const int64_t ngroups = s->dim / s->group_size, warps = (s->group_size + 511) / 512;
-    int64_t slots = 152 * 16 / (ngroups * warps);
+    const int64_t per_sm = warps == 1 ? 12 : warps < 15 ? 15 / warps : 1;
+    int64_t slots = 152 * per_sm / ngroups;
     if (slots < 1) slots = 1;
     if (slots > s->rows) slots = s->rows;
     return slots;
@@ -363,21 +376,26 @@ int64_t bwd_slots(const ssd_norm_shape_t *s) {
 
 bool row_ok(const ssd_rows_t &r, size_t es) { return rows_in_ok(r, es); }
 
+template <typename T>
+Mat<T> mat(const ssd_rows_t &r) {
+    return {static_cast<T *>(r.data), r.row_stride};
+}
+
 template <typename T, typename TR>
 ssd_status_t fwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *x, const float *weight, const ssd_rows_t *z,
                        const ssd_rows_t *res, const float *scale, const ssd_rows_t *out, const ssd_rows_t *res_out,
                        cudaStream_t st) {
     NormArgs<T, TR> a{};
-    a.x = static_cast<const T *>(x->data), a.x_rs = x->row_stride;
-    if (z) a.z = static_cast<const T *>(z->data), a.z_rs = z->row_stride;
+    a.x = mat<const T>(*x);
+    if (z) a.z = mat<const T>(*z);
     if (res) {
-        a.res = static_cast<const TR *>(res->data), a.res_rs = res->row_stride;
-        a.res_out = static_cast<TR *>(res_out->data), a.res_out_rs = res_out->row_stride;
+        a.res = mat<const TR>(*res);
+        a.res_out = mat<TR>(*res_out);
     }
     a.weight = weight, a.scale = scale;
-    a.out = static_cast<T *>(out->data), a.out_rs = out->row_stride;
+    a.out = mat<T>(*out);
     a.rows = s->rows, a.dim = (int)s->dim, a.group = (int)s->group_size, a.ngroups = (int)(s->dim / s->group_size);
-    a.eps = s->eps;
+    a.eps = s->eps, a.inv_group = 1.f / (float)s->group_size;
     constexpr int VF = 16 / sizeof(T);
     const size_t es = sizeof(T);
     bool vec = s->group_size % VF == 0 && rows_vec(*x, es, 1, s->rows) && rows_vec(*out, es, 1, s->rows);
@@ -385,13 +403,13 @@ ssd_status_t fwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *x, const flo
     if (res) vec = vec && rows_vec(*res, sizeof(TR), 1, s->rows) && rows_vec(*res_out, sizeof(TR), 1, s->rows);
     vec = vec && aligned(weight, 16) && aligned(scale, 16);
     a.gate = !z ? kNone : s->gate_after ? kAfter : kBefore;
-    return pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto w, int threads) {
-        constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+    return pick_team<VF>(s->group_size, vec, a.gate, [&](auto v, auto nv, auto w, auto gt, int threads) {
+        constexpr int V = decltype(v)::value, NV = decltype(nv)::value, GATE = decltype(gt)::value;
         constexpr bool WARP = decltype(w)::value;
         const int64_t teams = s->rows * a.ngroups, blocks = WARP ? (teams + kWarpTeams - 1) / kWarpTeams : teams;
         if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
         timing_begin(st);
-        norm_fwd_kernel<T, TR, V, NV, WARP><<<(unsigned)blocks, WARP ? kWarpTeams * 32 : threads, 0, st>>>(a);
+        norm_fwd_kernel<T, TR, V, NV, WARP, GATE><<<(unsigned)blocks, WARP ? kWarpTeams * 32 : threads, 0, st>>>(a);
         timing_mark(st, "norm_fwd");
         return status_of(cudaGetLastError());
     });
@@ -403,22 +421,22 @@ ssd_status_t bwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *dout, const 
                        const ssd_rows_t *dx, float *dweight, const ssd_rows_t *dz, const ssd_rows_t *dres, float *dscale,
                        void *ws, cudaStream_t st) {
     NormArgs<T, TR> a{};
-    a.x = static_cast<const T *>(x->data), a.x_rs = x->row_stride;
+    a.x = mat<const T>(*x);
     if (z) {
-        a.z = static_cast<const T *>(z->data), a.z_rs = z->row_stride;
-        a.dz = static_cast<T *>(dz->data), a.dz_rs = dz->row_stride;
+        a.z = mat<const T>(*z);
+        a.dz = mat<T>(*dz);
     }
     if (sum) {
-        a.res = static_cast<const TR *>(sum->data), a.res_rs = sum->row_stride;
-        a.res_out = static_cast<TR *>(dres->data), a.res_out_rs = dres->row_stride;
-        if (dsum) a.dres = static_cast<const TR *>(dsum->data), a.dres_rs = dsum->row_stride;
+        a.res = mat<const TR>(*sum);
+        a.res_out = mat<TR>(*dres);
+        if (dsum) a.dres = mat<const TR>(*dsum);
     }
     a.weight = weight, a.scale = scale;
-    a.dout = static_cast<const T *>(dout->data), a.dout_rs = dout->row_stride;
-    a.dx = static_cast<T *>(dx->data), a.dx_rs = dx->row_stride;
+    a.dout = mat<const T>(*dout);
+    a.dx = mat<T>(*dx);
     a.partial = static_cast<float *>(ws);
     a.rows = s->rows, a.dim = (int)s->dim, a.group = (int)s->group_size, a.ngroups = (int)(s->dim / s->group_size);
-    a.eps = s->eps;
+    a.eps = s->eps, a.inv_group = 1.f / (float)s->group_size;
     constexpr int VF = 16 / sizeof(T);
     const size_t es = sizeof(T);
     bool vec = s->group_size % VF == 0 && rows_vec(*x, es, 1, s->rows) && rows_vec(*dout, es, 1, s->rows) &&
@@ -431,12 +449,12 @@ ssd_status_t bwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *dout, const 
     const int slots = (int)bwd_slots(s);
     timing_begin(st);
     if (slots > 0) {
-        const ssd_status_t e = pick_team<VF>(s->group_size, vec, [&](auto v, auto nv, auto w, int threads) {
-            constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+        const ssd_status_t e = pick_team<VF>(s->group_size, vec, a.gate, [&](auto v, auto nv, auto w, auto gt, int threads) {
+            constexpr int V = decltype(v)::value, NV = decltype(nv)::value, GATE = decltype(gt)::value;
             constexpr bool WARP = decltype(w)::value;
             const int64_t teams = (int64_t)slots * a.ngroups, blocks = WARP ? (teams + kWarpTeams - 1) / kWarpTeams : teams;
             if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
-            norm_bwd_kernel<T, TR, V, NV, WARP>
+            norm_bwd_kernel<T, TR, V, NV, WARP, GATE>
                 <<<(unsigned)blocks, WARP ? kWarpTeams * 32 : threads, 0, st>>>(a, slots);
             timing_mark(st, "norm_bwd");
             return status_of(cudaGetLastError());
