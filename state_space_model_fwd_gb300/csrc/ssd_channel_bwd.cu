@@ -76,23 +76,33 @@ __device__ __forceinline__ float delta_of(const ChannelArgs<T> &a, float pre) {
 // 1: chunk summaries.  One forward walk: with P the decay from the chunk's
 // start to t, the gradient for the state before the chunk is sum_t P g_t C_t.
 // ---------------------------------------------------------------------------
+// A lane is a channel, as in the forward kernel; the results are stored as the
+// square tiles of 3 hold them.
 template <int N>
-struct alignas(16) SumStage {
-    float d[8][32], u[8][32], g[8][32], bc[8][2 * N];
-};
+__device__ __forceinline__ void store_square(float4 *p, int c, const f2 (&v)[1][N / 2]) {
+    using G = BwdTile<N>;
+    const int cg = c / G::K, i = c % G::K;
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        float4 r;
+        unpack2(v[0][n / 2], r.x, r.y);
+        unpack2(v[0][n / 2 + 1], r.z, r.w);
+        p[(i * G::M + n % G::M) / 4 * 32 + cg * G::K + n / G::M] = r;
+    }
+}
 
 template <typename T, int N, bool GATE>
-__global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __grid_constant__ BwdArgs<T> b) {
-    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, M2 = BwdTile<N>::M2, TB = 8, NB = TB * 2 * N / 32;
-    __shared__ SumStage<N> stage[kWarps];
+__global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chunk_kernel(const __grid_constant__ BwdArgs<T> b) {
+    using G = Tile<N, 1, 1>;
+    constexpr int N2 = N / 2, TB = 4, NB = TB * 2 * N / 32;
+    __shared__ __align__(16) float stage[kWarps][TB][2 * N];
     const ChannelArgs<T> &a = b.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
     if (id >= (int64_t)a.units * a.nblk) return;
     const int blk = (int)(id % a.nblk), unit = (int)(id / a.nblk);
-    SumStage<N> &sm = stage[warp];
+    auto &sm = stage[warp];
     const Block k = block_of(blk, a.per, a.nblk_g, 32);
-    const int cg = lane / K, q = lane % K;
     const bool mine = lane < k.nc;
     const int own = k.c0 + (mine ? lane : 0);
     const bool packed = a.seqs.start != nullptr;
@@ -107,8 +117,10 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
         const bool starts = S == t0 || E < t1;  // (E < t1: another sequence starts at or after E, inside)
         b.flags[unit] = (starts ? 1 : 0) | (E <= t1 ? 2 : 0);
     }
-    f2 A2[K][M2], h[K][M2], P[K][M2], R[K][M2];
-    load_decay<T, N>(a, k, lane, A2);
+    typename G::Regs A2, h, P, R;
+    load_tile<G>(a.A + (int64_t)k.c0 * N, lane, k.nc, A2);
+#pragma unroll
+    for (int m = 0; m < N2; ++m) A2[0][m] = mul2(A2[0][m], pack2(kLog2e, kLog2e));
     const float bias = a.bias ? a.bias[own] : 0.f;
     const int64_t at = (int64_t)unit * a.nblk + blk;
     int t = t0;
@@ -117,12 +129,10 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
         const bool head = t == t0 && S < t0;  // a gradient goes back to the chunk before
         const bool tail = E > t1;             // a state goes on to the chunk after
         if (head || tail) {
-            zero_tile<BwdTile<N>>(h), zero_tile<BwdTile<N>>(R);
-            if (t == S && a.init) load_tile<BwdTile<N>>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
+            zero_tile<G>(h), zero_tile<G>(R);
+            if (t == S && a.init) load_tile<G>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
 #pragma unroll
-            for (int i = 0; i < K; ++i)
-#pragma unroll
-                for (int j = 0; j < M2; ++j) P[i][j] = pack2(1.f, 1.f);
+            for (int m = 0; m < N2; ++m) P[0][m] = pack2(1.f, 1.f);
             float total = 0.f;
             // (tokens past the piece read its last one, lanes without a channel the block's first: delta = g = 0)
             T rd[TB], rx[TB], rg[TB], rz[TB], rbc[NB];
@@ -143,53 +153,57 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_chunk_kernel(const __
             };
             fetch(t);
             for (int tb = t; tb < e; tb += TB) {
-                __syncwarp();
+                float d[TB], u[TB], g[TB];
 #pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    float d = delta_of(a, to_f32(rd[j]) + bias), u = d * to_f32(rx[j]), g = to_f32(rg[j]);
-                    if (GATE) g *= silu(to_f32(rz[j]));
-                    if (tb + j >= e || !mine) d = u = g = 0.f;
-                    total += d;
-                    sm.d[j][lane] = d, sm.u[j][lane] = u, sm.g[j][lane] = g;
+                    d[j] = to_f32(rd[j]) + bias, u[j] = to_f32(rx[j]), g[j] = to_f32(rg[j]);
+                    if (GATE) g[j] *= silu(to_f32(rz[j]));
+                }
+                if (a.soft) {
+#pragma unroll
+                    for (int j = 0; j < TB; ++j) d[j] = softplus(d[j]);
                 }
 #pragma unroll
-                for (int i = 0; i < NB; ++i) (&sm.bc[0][0])[i * 32 + lane] = tb + (i * 32 + lane) / (2 * N) < e ? to_f32(rbc[i]) : 0.f;
+                for (int j = 0; j < TB; ++j) {
+                    const bool in = tb + j < e && mine;
+                    d[j] = in ? d[j] : 0.f, u[j] = in ? d[j] * u[j] : 0.f, g[j] = in ? g[j] : 0.f;
+                    total += d[j];
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int el = i * 32 + lane;
+                    (&sm[0][0])[el] = tb + el / (2 * N) < e ? to_f32(rbc[i]) : 0.f;
+                }
                 __syncwarp();
                 if (tb + TB < e) fetch(tb + TB);
-#pragma unroll 2
+#pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    float d[K], u[K], g[K];
-                    f2 B[M2], C[M2];
-                    load_k<K>(&sm.d[j][cg * K], d);
-                    load_k<K>(&sm.u[j][cg * K], u);
-                    load_k<K>(&sm.g[j][cg * K], g);
-                    load_m<M>(&sm.bc[j][q * M], B);
-                    load_m<M>(&sm.bc[j][N + q * M], C);
+                    const f2 dd = pack2(d[j], d[j]), uu = pack2(u[j], u[j]), gg = pack2(g[j], g[j]);
 #pragma unroll
-                    for (int i = 0; i < K; ++i) {
-                        const f2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]), gg = pack2(g[i], g[i]);
-#pragma unroll
-                        for (int m = 0; m < M2; ++m) {
-                            const f2 decay = ex2x2(mul2(A2[i][m], dd));
-                            h[i][m] = fma2(decay, h[i][m], mul2(uu, B[m]));
-                            P[i][m] = mul2(P[i][m], decay);
-                            R[i][m] = fma2(P[i][m], mul2(gg, C[m]), R[i][m]);
-                        }
+                    for (int m = 0; m < N2; m += 2) {
+                        const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&sm[j][2 * m]);
+                        const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(&sm[j][N + 2 * m]);
+                        const f2 d0 = ex2x2(mul2(A2[0][m], dd)), d1 = ex2x2(mul2(A2[0][m + 1], dd));
+                        h[0][m] = fma2(d0, h[0][m], mul2(uu, B.x));
+                        h[0][m + 1] = fma2(d1, h[0][m + 1], mul2(uu, B.y));
+                        P[0][m] = mul2(P[0][m], d0);
+                        P[0][m + 1] = mul2(P[0][m + 1], d1);
+                        R[0][m] = fma2(P[0][m], mul2(gg, C.x), R[0][m]);
+                        R[0][m + 1] = fma2(P[0][m + 1], mul2(gg, C.y), R[0][m + 1]);
                     }
                 }
             }
             if (head) {
                 if (e == E && b.dfinal) {
-                    f2 f[K][M2];
-                    load_tile<BwdTile<N>>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, f);
+                    typename G::Regs f;
+                    load_tile<G>(b.dfinal + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, f);
 #pragma unroll
-                    for (int i = 0; i < K; ++i)
-#pragma unroll
-                        for (int m = 0; m < M2; ++m) R[i][m] = fma2(P[i][m], f[i][m], R[i][m]);
+                    for (int m = 0; m < N2; ++m) R[0][m] = fma2(P[0][m], f[0][m], R[0][m]);
                 }
-                store_lanes<BwdTile<N>>(b.back + at * (N / 4 * 32), lane, R);
+                store_square<N>(b.back + at * (N / 4 * 32), lane, R);
             }
-            if (tail) store_lanes<BwdTile<N>>(a.local + at * (N / 4 * 32), lane, h);
+            if (tail) store_square<N>(a.local + at * (N / 4 * 32), lane, h);
             if (tail && head) a.sums[at * 32 + lane] = total;
         }
         if (e == t1) return;

@@ -24,7 +24,7 @@ namespace {
 constexpr int kVec = 4;       // channels per thread (8 bytes of bf16, 16 of fp32)
 constexpr int kLanes = 32;    // channel vectors per block
 constexpr int kSub = 8;       // tiles of tokens per block, one per warp
-constexpr int kAhead = 8;     // rows in flight, forward
+constexpr int kAhead = 4;     // rows in flight, forward
 constexpr int kStep = 4;      // and in the gradient (of x and of dy)
 constexpr int kMaxSet = 960;  // sequences whose offsets fit one launch's parameters
 
@@ -104,11 +104,11 @@ __device__ __forceinline__ Vec<T, V> row_at(const ConvArgs<T> &a, const Rows<con
 
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_weights(const ConvArgs<T> &a, int c0, float (&w)[W][V], float (&b)[V]) {
-    const float *src = a.weight + (int64_t)c0 * W;  // V W floats: 16-byte aligned where V is 4
+    const float *src = a.weight + (int64_t)c0 * W;  // V W floats: 16-byte aligned where V is 4 or 8
     float f[W * V];
-    if constexpr (V == 4) {
+    if constexpr (V >= 4) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) widen<float, 4>(load_vec<float, 4>(src + 4 * i), f + 4 * i);
+        for (int i = 0; i < W * V / 4; ++i) widen<float, 4>(load_vec<float, 4>(src + 4 * i), f + 4 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < W * V; ++i) f[i] = src[i];
@@ -165,8 +165,8 @@ __device__ void copy_states(const ConvArgs<T> &a, const Set &set, int64_t block)
     }
 }
 
-template <typename T, int W, int V, bool PACKED, typename Set>
-__global__ void __launch_bounds__(kLanes *kSub, 2) conv_fwd_kernel(const __grid_constant__ ConvArgs<T> a,
+template <typename T, int W, int V, bool PACKED, bool SILU, typename Set>
+__global__ void __launch_bounds__(kLanes *kSub, 3) conv_fwd_kernel(const __grid_constant__ ConvArgs<T> a,
                                                                 const __grid_constant__ Set set) {
     if (blockIdx.x >= a.tblocks) {
         copy_states<T, W, V, PACKED, false>(a, set, blockIdx.x - a.tblocks);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kLanes *kSub, 2) conv_fwd_kernel(const __grid_
                 widen<T, V>(cur[i], c);
                 taps<W, V>(w, bias, win, c, o[i]);
             }
-            if (a.use_silu) {
+            if constexpr (SILU) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
 #pragma unroll
@@ -456,19 +456,18 @@ struct Plan {
     int V, nvec, ncb, tile;
 };
 
-// Tokens per tile: the longest of 32, 16, 8 that still makes three rounds of
-// the 16 warps an SM holds (a tile reads W-1 rows beyond its own).
+// Tokens per tile: the longest of 128, 64, .. 8 that still makes 16 warps an SM
+// (a tile reads W-1 rows beyond its own).
 int pick_tile(int64_t ncb, int64_t tokens) {
-    int tile = 32;
-    while (tile > 8 && ncb * (tokens / tile) < 152 * 16 * 3) tile /= 2;
+    int tile = 128;
+    while (tile > 8 && ncb * (tokens / tile) < 152 * 16) tile /= 2;
     return tile;
 }
 
 template <typename T>
 bool fill(const ssd_conv_shape_t *s, int64_t nseq, const ssd_rows_t *x, const ssd_rows_t *y, const ssd_rows_t *dx,
-          std::initializer_list<const void *> states, ConvArgs<T> &a) {
+          std::initializer_list<const void *> states, int V, ConvArgs<T> &a) {
     const size_t es = sizeof(T);
-    const int V = kVec;
     bool vec = aligned(a.weight, 16) && s->channels * es % 16 == 0 && rows_vec(*x, es, s->batch, s->seqlen);
     if (dx) vec = vec && rows_vec(*dx, es, s->batch, s->seqlen);
     int64_t end = 0;
@@ -517,7 +516,10 @@ ssd_status_t launch_fwd(ConvArgs<T> &a, const Set &set, int64_t tokens, int64_t 
     if (a.final_state) blocks += (nseq * (W - 1) * a.nvec + kLanes * kSub - 1) / (kLanes * kSub);
     if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
     if (blocks == 0) return SSD_OK;
-    conv_fwd_kernel<T, W, V, PACKED, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set);
+    if (a.use_silu)
+        conv_fwd_kernel<T, W, V, PACKED, true, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set);
+    else
+        conv_fwd_kernel<T, W, V, PACKED, false, Set><<<(unsigned)blocks, dim3(kLanes, kSub), 0, st>>>(a, set);
     timing_mark(st, "conv_fwd");
     return status_of(cudaGetLastError());
 }
@@ -631,7 +633,7 @@ ssd_status_t fwd_typed(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nse
                        cudaStream_t st) {
     ConvArgs<T> a{};
     a.weight = weight, a.bias = bias;
-    const bool vec = fill<T>(s, nseq, x, y, nullptr, {init, fin}, a);
+    const bool vec = fill<T>(s, nseq, x, y, nullptr, {init, fin}, kVec, a);
     a.init = static_cast<const T *>(init), a.final_state = static_cast<T *>(fin);
     return dispatch<kVec>(s->width, vec, [&](auto w, auto v) {
         return run_fwd<T, decltype(w)::value, decltype(v)::value>(a, s, cu, nseq, st);
@@ -644,7 +646,7 @@ ssd_status_t bwd_typed(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nse
                        const ssd_rows_t *dx, float *dweight, float *dbias, void *dinit, void *ws, cudaStream_t st) {
     ConvArgs<T> a{};
     a.weight = weight, a.bias = bias;
-    const bool vec = fill<T>(s, nseq, x, dy, dx, {init, dfin, dinit}, a);
+    const bool vec = fill<T>(s, nseq, x, dy, dx, {init, dfin, dinit}, kVec, a);
     a.dx = rows_of<T>(*dx);
     a.init = static_cast<const T *>(init), a.dfinal = static_cast<const T *>(dfin);
     a.final_state = static_cast<T *>(dinit);
@@ -659,7 +661,7 @@ ssd_status_t step_typed(const ssd_conv_shape_t *s, const ssd_rows_t *x, const fl
                         void *state, const ssd_rows_t *y, cudaStream_t st) {
     ConvArgs<T> a{};
     a.weight = weight, a.bias = bias;
-    const bool vec = fill<T>(s, s->batch, x, y, nullptr, {state}, a);
+    const bool vec = fill<T>(s, s->batch, x, y, nullptr, {state}, kVec, a);
     return dispatch<kVec>(s->width, vec, [&](auto w, auto v) {
         const int64_t blocks = (s->batch * a.nvec + 127) / 128;
         if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
