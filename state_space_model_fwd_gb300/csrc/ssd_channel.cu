@@ -75,7 +75,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
     if (warp >= (FULL ? a.whole : 0) + (int64_t)a.cut * a.nchunk) return;  // (only warp barriers below)
     // a block row is a channel block of a sequence row; those from a.whole on
     // are cut into chunks
+    launch_next();
     const bool packed = a.seqs.start != nullptr;
+    if (packed) wait_previous();  // the offsets
     const bool whole = FULL && warp < a.whole;
     const int id = (int)warp - (FULL ? a.whole : 0);
     const int r = whole ? 0 : id % a.cut, c_in = whole ? 0 : id / a.cut, brow = whole ? (int)warp : a.whole + r;
@@ -115,6 +117,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
         if (t == S0) {
             if (a.init) load_tile<G>(a.init + ((int64_t)s * a.ch + k.c0) * N, lane, k.nc, h);
         } else if (FULL) {
+            wait_previous();
             const int first = S0 / a.chunk;
             load_lanes<G>(a.local + ((int64_t)first * a.cut + r) * (E * 32), lane, h);
 #pragma unroll 4
@@ -305,6 +308,7 @@ struct OffsetSet {
     int v[kMaxSet];
 };
 static __global__ void __launch_bounds__(256) write_offsets_kernel(const __grid_constant__ OffsetSet s, int *dst) {
+    launch_next();
     for (int i = threadIdx.x; i < s.n; i += 256) dst[s.first + i] = s.v[i];
 }
 cudaError_t write_offsets(const int64_t *cu, int64_t nseq, int *dst, cudaStream_t st) {
@@ -381,7 +385,7 @@ FwdPlan plan_fwd(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) 
     p.cut = base - p.whole;
     // a tail of more than 7/8 of a round, or behind eight rounds, is not worth cutting
     if (p.whole && (p.cut * 8 > kSched * 7 || base >= 8 * kSched)) p.whole = base, p.cut = 0;
-    int64_t want = p.cut ? (2 * kSched + p.cut - 1) / p.cut : 1;
+    int64_t want = p.cut ? 2 * kSched / p.cut : 1;  // one round of all of them
     if (want > (L + 63) / 64) want = (L + 63) / 64;
     if (want < 1) want = 1;
     if (want == 1) p.whole = cu ? 0 : base, p.cut = base - p.whole;
@@ -425,16 +429,18 @@ ssd_status_t run_fwd(ChannelArgs<T> &a, const ssd_channel_shape_t *s, const int6
     if (p.whole + cut > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
     a.whole = (int)p.whole, a.cut = (int)p.cut;
     const int64_t blocks = (p.whole + cut + kWarps - 1) / kWarps;
+    bool after = cu != nullptr;
     if (p.cut && p.nchunk > 1) {
-        channel_fwd_kernel<T, N, false, false><<<(unsigned)((cut + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a);
+        e = launch(channel_fwd_kernel<T, N, false, false>, dim3((unsigned)((cut + kWarps - 1) / kWarps)), kWarps * 32, 0, st,
+                   after, a);
         timing_mark(st, "channel_chunk_state");
+        if (e != cudaSuccess) return status_of(e);
+        after = true;
     }
-    if (a.z.p)
-        channel_fwd_kernel<T, N, true, true><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-    else
-        channel_fwd_kernel<T, N, true, false><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
+    e = launch(a.z.p ? channel_fwd_kernel<T, N, true, true> : channel_fwd_kernel<T, N, true, false>, dim3((unsigned)blocks),
+               kWarps * 32, 0, st, after, a);
     timing_mark(st, "channel_scan");
-    return status_of(cudaGetLastError());
+    return status_of(e);
 }
 
 template <typename T>

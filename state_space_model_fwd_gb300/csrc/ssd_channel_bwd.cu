@@ -34,7 +34,8 @@ struct Geo {
     // tokens per chunk: with 16 states what lets eight warps share an SM's memory
     static constexpr int CH = N == 32 ? 16 : N == 16 ? 28 : 32;
     static constexpr int TB = N == 32 ? 2 : 4;  // tokens whose states are in registers
-    static constexpr int NS = CH / TB;
+    static constexpr int EV = 4;                // tokens between states kept in shared memory
+    static constexpr int NK = EV == TB ? CH / EV - 1 : CH / EV;  // how many (the last TB's stays in registers)
 };
 
 template <typename T>
@@ -99,6 +100,8 @@ __global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chun
     const ChannelArgs<T> &a = b.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+    launch_next();
+    wait_previous();
     if (id >= (int64_t)a.units * a.nblk) return;
     const int blk = (int)(id % a.nblk), unit = (int)(id / a.nblk);
     auto &sm = stage[warp];
@@ -219,10 +222,12 @@ __global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chun
 // states over all chunks of a sequence row; blockIdx.y picks the direction.
 // ---------------------------------------------------------------------------
 template <typename T, int N>
-__global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
-    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 16;
+__global__ void __launch_bounds__(32) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 32;
     const ChannelArgs<T> &a = b.f;
-    const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    const int64_t id = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    launch_next();
+    wait_previous();
     if (id >= (int64_t)rows * a.nblk * (N / 4) * 32) return;
     const int lane = (int)(id % 32), f = (int)(id / 32 % (N / 4));
     const int blk = (int)(id / (32 * (N / 4)) % a.nblk), row = (int)(id / (32 * (N / 4)) / a.nblk);
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(128) channel_bwd_pass_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 template <int N>
 struct alignas(16) GradStage {
-    float4 kept[Geo<N>::NS - 1][N / 4 * 32];  // states before the 0th .. next to last TB tokens
+    float4 kept[Geo<N>::NK][N / 4 * 32];         // the state before every EV tokens
     float d[Geo<N>::CH][32], u[Geo<N>::CH][32], g[Geo<N>::CH][32];  // by token of the piece
     float bc[Geo<N>::CH + 1][2 * N];                                // by token of the chunk, turning into the warp's dB and dC; a zero row
 };
@@ -308,6 +313,7 @@ struct LaneSums {
 template <typename T, int N, bool GATE>
 __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_constant__ BwdArgs<T> b) {
     constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, M2 = BwdTile<N>::M2, TB = Geo<N>::TB, CH = Geo<N>::CH;
+    constexpr int EV = Geo<N>::EV;
     constexpr int R = GATE ? 3 : 2, LEFT = LaneSums<BwdTile<N>::K, 2 * BwdTile<N>::M>::LEFT;
     extern __shared__ __align__(16) char smem[];
     const ChannelArgs<T> &a = b.f;
@@ -334,6 +340,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
     const float D = a.D && mine ? a.D[own] : 0.f;
     float dD = 0.f, dbias = 0.f;
     for (int i = lane; i < 2 * N; i += 32) sm.bc[CH][i] = 0.f;
+    launch_next();
+    wait_previous();
 
     for (int unit = slot; unit < a.units; unit += b.slots) {
         const int row = packed ? 0 : unit / a.nchunk;
@@ -394,8 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                 }
             }
             __syncwarp();
-            for (int sb = 0; sb + 1 < ns; ++sb) {
-                store_lanes<BwdTile<N>>(sm.kept[sb], lane, h);
+            auto advance = [&](int sb) {  // the state over TB tokens of the piece
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
                     const int j = sb * TB + jj;
@@ -412,6 +419,10 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                             h[i][m] = fma2(ex2x2(mul2(A2[i][m], dd)), h[i][m], mul2(uu, B[m]));
                     }
                 }
+            };
+            for (int sb = 0; sb < ns; ++sb) {
+                if (sb * TB % EV == 0 && (EV != TB || sb + 1 < ns)) store_lanes<BwdTile<N>>(sm.kept[sb * TB / EV], lane, h);
+                if (sb + 1 < ns) advance(sb);
             }
             // backward
             for (int sb = ns - 1; sb >= 0; --sb) {
@@ -425,7 +436,10 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                     rd[jj] = a.dt.at(row, t)[own];
                     if (GATE) rz[jj] = a.z.at(row, t)[own];
                 }
-                if (sb + 1 < ns) load_lanes<BwdTile<N>>(sm.kept[sb], lane, h);
+                if (sb + 1 < ns) load_lanes<BwdTile<N>>(sm.kept[sb * TB / EV], lane, h);
+                if (EV != TB && sb + 1 < ns) {
+                    for (int s2 = sb * TB / EV * EV / TB; s2 < sb; ++s2) advance(s2);
+                }
                 f2 before[TB][K][M2], decay[TB][K][M2];
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
@@ -562,6 +576,7 @@ template <typename T, int N>
 __global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_constant__ BwdArgs<T> b, int64_t bc_blocks) {
     constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M;
     const ChannelArgs<T> &a = b.f;
+    wait_previous();
     if (blockIdx.x < bc_blocks) {
         const int groups = a.nblk / a.nblk_g;
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -667,30 +682,31 @@ ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t 
         const int64_t warps = (p.units * p.nblk + kWarps - 1) / kWarps;
         const int64_t threads = (int64_t)rows * p.nblk * (N / 4) * 32;
         const int64_t grads = (int64_t)s->ngroups * p.quads * p.slots;
-        if (warps > 0x7FFFFFFF || threads / 128 >= 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+        if (warps > 0x7FFFFFFF || threads / 32 > 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+        bool after = cu != nullptr;
         if (p.nchunk > 1) {
-            if (a.z.p)
-                channel_bwd_chunk_kernel<T, N, true><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
-            else
-                channel_bwd_chunk_kernel<T, N, false><<<(unsigned)warps, kWarps * 32, 0, st>>>(b);
+            e = launch(a.z.p ? channel_bwd_chunk_kernel<T, N, true> : channel_bwd_chunk_kernel<T, N, false>,
+                       dim3((unsigned)warps), kWarps * 32, 0, st, after, b);
             timing_mark(st, "channel_bwd_chunk");
-            channel_bwd_pass_kernel<T, N><<<dim3((unsigned)((threads + 127) / 128), 2), 128, 0, st>>>(b, rows);
+            if (e == cudaSuccess)
+                e = launch(channel_bwd_pass_kernel<T, N>, dim3((unsigned)(threads / 32), 2), 32, 0, st, true, b,
+                           rows);
             timing_mark(st, "channel_bwd_pass");
+            if (e != cudaSuccess) return status_of(e);
+            after = true;
         }
         const size_t smem = sizeof(GradStage<N>) * kWarps;
         auto kernel = a.z.p ? channel_bwd_kernel<T, N, true> : channel_bwd_kernel<T, N, false>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return status_of(e);
-        kernel<<<(unsigned)grads, kWarps * 32, smem, st>>>(b);
+        if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)grads), kWarps * 32, smem, st, after, b);
         timing_mark(st, "channel_bwd");
-        e = cudaGetLastError();
         if (e != cudaSuccess) return status_of(e);
     }
     const int64_t bc = (b.tokens * s->ngroups * 2 * N + 255) / 256, ab = (p.nblk * (N + 2) * 32 + 255) / 256;
     if (bc + ab > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
-    channel_bwd_reduce_kernel<T, N><<<(unsigned)(bc + ab), 256, 0, st>>>(b, bc);
+    e = launch(channel_bwd_reduce_kernel<T, N>, dim3((unsigned)(bc + ab)), 256, 0, st, p.units > 0 || cu, b, bc);
     timing_mark(st, "channel_bwd_reduce");
-    return status_of(cudaGetLastError());
+    return status_of(e);
 }
 
 template <typename T>

@@ -2,6 +2,8 @@
 // packed-sequence tables, small device math and host checks.
 #pragma once
 
+#include <utility>
+
 #include "ssd_common.cuh"
 
 namespace ssd {
@@ -128,9 +130,33 @@ struct Rows {
     __device__ __forceinline__ T *at(int64_t b, int t) const { return p + b * bs + step(t); }
 };
 
+// Programmatic dependency between the launches of one call: a kernel lets the
+// next one start once all its blocks run, and waits for the whole of the
+// previous one (and so, one after another, of all before it) before it reads
+// what that wrote.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // host checks
 // ---------------------------------------------------------------------------
+// `after`: with a programmatic dependency on the launch before.  A call's first
+// launch has none, so it waits for everything before it on the stream.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 inline ssd_status_t status_of(cudaError_t e) {
     if (e == cudaSuccess) return SSD_OK;
     (void)cudaGetLastError();  // a failed call also records itself as the thread's last error
