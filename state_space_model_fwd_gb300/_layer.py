@@ -18,6 +18,7 @@ import torch
 _F32 = torch.float32
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
 _MAX_PARTS = 4
+_Parts = ctypes.c_int64 * _MAX_PARTS
 
 
 class _rows_t(ctypes.Structure):
@@ -52,6 +53,9 @@ class _norm_shape_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("group_size", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
                 ("gate_after", ctypes.c_int)]
+
+
+_RowsOf = [None] + [_rows_t * n for n in range(1, _MAX_PARTS + 1)]
 
 
 def declare(lib):
@@ -178,7 +182,7 @@ def _empty(shape, dtype, x):
 def _workspace(workspace, need, x):
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         return workspace
-    return x.new_empty((max(need, 16),), dtype=torch.uint8)
+    return _empty((max(need, 16),), torch.uint8, x)
 
 
 # ---------------------------------------------------------------------------
@@ -190,7 +194,7 @@ def _conv_shape(x, weight, parts, silu, code):
     if not 1 <= len(parts) <= _MAX_PARTS:
         raise ValueError(f"1 to {_MAX_PARTS} parts, got {len(parts)}")
     b, L, C = x.shape
-    return _conv_shape_t(b, L, C, weight.shape[1], len(parts), (ctypes.c_int64 * _MAX_PARTS)(*parts), code,
+    return _conv_shape_t(b, L, C, weight.shape[1], len(parts), _Parts(*parts), code,
                          1 if silu else 0)
 
 
@@ -218,17 +222,21 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, *, silu=True, cu_seqlens
     bp = _flat(bias, "bias", _F32, (C,), dev)
     ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
     if y is None:
-        ys = [_empty((b, L, p), x.dtype, x) for p in parts]
+        ys = [_empty((b, L, p), dt, x) for p in parts]
+        yr = _RowsOf[len(parts)](*[_rows_t(t.data_ptr(), L * p, p) for t, p in zip(ys, parts)])
     else:
         ys = [y] if split is None else list(y)
         if len(ys) != len(parts):
             raise ValueError(f"y must hold {len(parts)} tensors")
-    yr = (_rows_t * len(parts))(*[_rows(t, "y", dt, (b, L, p), dev) for t, p in zip(ys, parts)])
-    if final_state is None and return_final_state:
-        final_state = _empty((nseq, W - 1, C), x.dtype, x)
-    fp = _flat(final_state, "final_state", dt, (nseq, W - 1, C), dev)
-    if fp and fp == ip:
-        raise ValueError("final_state must not be init_state")
+        yr = _RowsOf[len(parts)](*[_rows(t, "y", dt, (b, L, p), dev) for t, p in zip(ys, parts)])
+    fp = None
+    if final_state is not None:
+        fp = _flat(final_state, "final_state", dt, (nseq, W - 1, C), dev)
+        if fp and fp == ip:
+            raise ValueError("final_state must not be init_state")
+    elif return_final_state:
+        final_state = _empty((nseq, W - 1, C), dt, x)
+        fp = final_state.data_ptr()
     st = lib.ssd_conv_fwd(ctypes.byref(shape), cu, nseq, ctypes.byref(xr), wp, bp, ip, yr, fp,
                           torch._C._cuda_getCurrentRawStream(dev))
     if st:
@@ -253,14 +261,16 @@ def ssd_conv_bwd(dy, x, weight, bias=None, init_state=None, *, silu=True, cu_seq
     W = weight.shape[1]
     cu, nseq = _offsets(cu_seqlens, b)
     xr = _rows(x, "x", dt, (b, L, C), dev)
-    gr = (_rows_t * len(parts))(*[_rows(t, "dy", dt, (b, L, p), dev) for t, p in zip(dys, parts)])
+    gr = _RowsOf[len(parts)](*[_rows(t, "dy", dt, (b, L, p), dev) for t, p in zip(dys, parts)])
     wp = _flat(weight, "weight", _F32, (C, W), dev)
     bp = _flat(bias, "bias", _F32, (C,), dev)
     ip = _flat(init_state, "init_state", dt, (nseq, W - 1, C), dev)
     gp = _flat(dfinal_state, "dfinal_state", dt, (nseq, W - 1, C), dev)
     if dx is None:
-        dx = _empty((b, L, C), x.dtype, x)
-    dxr = _rows(dx, "dx", dt, (b, L, C), dev)
+        dx = _empty((b, L, C), dt, x)
+        dxr = _rows_t(dx.data_ptr(), L * C, C)
+    else:
+        dxr = _rows(dx, "dx", dt, (b, L, C), dev)
     dweight = _empty((C, W), _F32, x)
     dbias = None if bias is None else _empty((C,), _F32, x)
     dinit = None if init_state is None else _empty((nseq, W - 1, C), x.dtype, x)
@@ -292,9 +302,11 @@ def ssd_conv_step(x, weight, bias=None, *, state, silu=True, y=None):
         raise TypeError("state must be a CUDA tensor")
     sp = _flat(state, "state", dt, (b, W - 1, C), dev)
     if y is None:
-        y = _empty((b, C), x.dtype, x)
-    yr = _rows2(y, "y", dt, (b, C), dev)
-    shape = _conv_shape_t(b, 1, C, W, 1, (ctypes.c_int64 * _MAX_PARTS)(C), code, 1 if silu else 0)
+        y = _empty((b, C), dt, x)
+        yr = _rows_t(y.data_ptr(), C, 0)
+    else:
+        yr = _rows2(y, "y", dt, (b, C), dev)
+    shape = _conv_shape_t(b, 1, C, W, 1, _Parts(C), code, 1 if silu else 0)
     st = lib.ssd_conv_step(ctypes.byref(shape), ctypes.byref(xr), wp, bp, sp, ctypes.byref(yr),
                            torch._C._cuda_getCurrentRawStream(dev))
     if st:
@@ -342,12 +354,17 @@ def ssd_channel_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, init_stat
     ins, ch, N, G = _channel_inputs(x, dt, A, B, C, D, z, dt_bias, init_state, nseq, _rows, (b, L), dev)
     if y is None:
         y = _empty((b, L, ch), x.dtype, x)
-    yr = _rows(y, "y", x.dtype, (b, L, ch), dev)
-    if final_state is None and return_final_state:
+        yr = _rows_t(y.data_ptr(), L * ch, ch)
+    else:
+        yr = _rows(y, "y", x.dtype, (b, L, ch), dev)
+    fp = None
+    if final_state is not None:
+        fp = _flat(final_state, "final_state", _F32, (nseq, ch, N), dev)
+        if fp and fp == ins.init_state:
+            raise ValueError("final_state must not be init_state")
+    elif return_final_state:
         final_state = _empty((nseq, ch, N), _F32, x)
-    fp = _flat(final_state, "final_state", _F32, (nseq, ch, N), dev)
-    if fp and fp == ins.init_state:
-        raise ValueError("final_state must not be init_state")
+        fp = final_state.data_ptr()
     shape = _channel_shape_t(b, L, ch, N, G, code, 1 if dt_softplus else 0)
     need = lib.ssd_channel_scan_workspace_size(ctypes.byref(shape), cu, nseq)
     ws = _workspace(workspace, need, x) if need else None
@@ -412,7 +429,9 @@ def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state
     sp = _flat(state, "state", _F32, (b, ch, N), dev)
     if y is None:
         y = _empty((b, ch), x.dtype, x)
-    yr = _rows2(y, "y", x.dtype, (b, ch), dev)
+        yr = _rows_t(y.data_ptr(), ch, 0)
+    else:
+        yr = _rows2(y, "y", x.dtype, (b, ch), dev)
     shape = _channel_shape_t(b, 1, ch, N, G, code, 1 if dt_softplus else 0)
     st = lib.ssd_channel_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp,
                                    ctypes.byref(yr), torch._C._cuda_getCurrentRawStream(dev))
@@ -483,14 +502,18 @@ def ssd_block_norm_fwd(x, weight, *, z=None, residual=None, scale=None, eps=1e-5
     zr = _norm_rows(z, "z", ty, full, dev)
     wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    outr = _norm_rows(out, "out", ty, full, dev)
+        out = _empty(full, ty, x)
+        outr = _rows_t(out.data_ptr(), 0, dim)
+    else:
+        outr = _norm_rows(out, "out", ty, full, dev)
     rr = ror = None
     if residual is not None:
         rr = _norm_rows(residual, "residual", residual.dtype, full, dev)
         if residual_out is None:
             residual_out = _empty(full, residual.dtype, x)
-        ror = _norm_rows(residual_out, "residual_out", residual.dtype, full, dev)
+            ror = _rows_t(residual_out.data_ptr(), 0, dim)
+        else:
+            ror = _norm_rows(residual_out, "residual_out", residual.dtype, full, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     st = lib.ssd_block_norm_fwd(ctypes.byref(shape), _ref(xr), wp, _ref(zr), _ref(rr), sp,
@@ -515,8 +538,8 @@ def ssd_block_norm_bwd(dout, x, weight, *, z=None, scale=None, residual_out=None
         raise TypeError("dout must be a CUDA tensor")
     zr = _norm_rows(z, "z", ty, full, dev)
     wp, sp = _flat(weight, "weight", _F32, (dim,), dev), _flat(scale, "scale", _F32, (dim,), dev)
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-    dz = None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format)
+    dx = _empty(full, ty, x)
+    dz = None if z is None else _empty(full, ty, x)
     dweight = _empty((dim,), _F32, x)
     dscale = None if scale is None else _empty((dim,), _F32, x)
     sr = dsr = drr = dres = None
@@ -524,10 +547,11 @@ def ssd_block_norm_bwd(dout, x, weight, *, z=None, scale=None, residual_out=None
         sr = _norm_rows(residual_out, "residual_out", residual_out.dtype, full, dev)
         dsr = _norm_rows(dresidual_out, "dresidual_out", residual_out.dtype, full, dev)
         dres = _empty(full, residual_out.dtype, x)
-        drr = _norm_rows(dres, "dresidual", residual_out.dtype, full, dev)
+        drr = _rows_t(dres.data_ptr(), 0, dim)
     elif dresidual_out is not None:
         raise ValueError("dresidual_out needs residual_out")
-    dxr, dzr = _norm_rows(dx, "dx", ty, full, dev), _norm_rows(dz, "dz", ty, full, dev)
+    dxr = _rows_t(dx.data_ptr(), 0, dim)
+    dzr = None if z is None else _rows_t(dz.data_ptr(), 0, dim)
     ws = _workspace(workspace, lib.ssd_block_norm_bwd_workspace_size(ctypes.byref(shape)), x)
     st = lib.ssd_block_norm_bwd(
         ctypes.byref(shape), _ref(gr), _ref(xr), wp, _ref(zr), sp, _ref(sr), _ref(dsr), _ref(dxr),

@@ -71,13 +71,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
     __shared__ __align__(16) float stage[kWarps][kTB][2 * N];
     const int lane = threadIdx.x % 32;
     auto &sm = stage[threadIdx.x / 32];
+    const bool packed = a.seqs.packed;
+    const int *start = a.seqs.offsets();
+    launch_next();
+    if (a.seqs.start) wait_previous();  // the offsets
+    if (FULL && blockIdx.x >= a.blocks) {
+        pass_empty_states(start, a.seqs.n, (int64_t)a.ch * N, a.init, a.fin, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
     const int64_t warp = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
     if (warp >= (FULL ? a.whole : 0) + (int64_t)a.cut * a.nchunk) return;  // (only warp barriers below)
     // a block row is a channel block of a sequence row; those from a.whole on
     // are cut into chunks
-    launch_next();
-    const bool packed = a.seqs.start != nullptr;
-    if (packed) wait_previous();  // the offsets
     const bool whole = FULL && warp < a.whole;
     const int id = (int)warp - (FULL ? a.whole : 0);
     const int r = whole ? 0 : id % a.cut, c_in = whole ? 0 : id / a.cut, brow = whole ? (int)warp : a.whole + r;
@@ -97,8 +102,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
     const int t0 = c_in * a.chunk, t1 = whole ? a.seqs.L : min(a.seqs.L, t0 + a.chunk);
     int s = row, S0 = 0, S1 = a.seqs.L, t = t0;
     if (packed) {
-        s = seq_of(a.seqs, FULL ? t0 : t1 - 1);
-        S0 = a.seqs.start[s], S1 = a.seqs.start[s + 1];
+        s = seq_of(start, a.seqs.n, FULL ? t0 : t1 - 1);
+        S0 = start[s], S1 = start[s + 1];
         if (!FULL) t = max(t, S0);  // only what reaches the chunk's end
     }
     if (!FULL && S1 <= t1) return;  // nothing passes to the next chunk
@@ -207,8 +212,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
         if (GATE) pz -= a.z.step(over);
         t = e;
         do ++s;
-        while (a.seqs.start[s + 1] <= t);
-        S0 = a.seqs.start[s], S1 = a.seqs.start[s + 1];
+        while (start[s + 1] <= t);
+        S0 = start[s], S1 = start[s + 1];
     }
 }
 
@@ -311,7 +316,14 @@ static __global__ void __launch_bounds__(256) write_offsets_kernel(const __grid_
     launch_next();
     for (int i = threadIdx.x; i < s.n; i += 256) dst[s.first + i] = s.v[i];
 }
-cudaError_t write_offsets(const int64_t *cu, int64_t nseq, int *dst, cudaStream_t st) {
+cudaError_t place_offsets(const int64_t *cu, int64_t nseq, int *dst, Seqs &seqs, bool *launched, cudaStream_t st) {
+    seqs.packed = 1;
+    *launched = nseq + 1 > kInline;
+    if (!*launched) {
+        for (int64_t i = 0; i <= nseq; ++i) seqs.few[i] = (int)cu[i];
+        return cudaSuccess;
+    }
+    seqs.start = dst;
     OffsetSet set;
     for (int64_t f = 0; f <= nseq; f += kMaxSet) {
         set.first = (int)f;
@@ -323,20 +335,15 @@ cudaError_t write_offsets(const int64_t *cu, int64_t nseq, int *dst, cudaStream_
     return cudaGetLastError();
 }
 
-// Empty sequences hand a state on unchanged: dst[s] = src[s] (zero without
-// src) for every s with start[s] == start[s + 1], or for all (start null).
-static __global__ void __launch_bounds__(256) empty_states_kernel(const int *start, int64_t each, const float *src,
-                                                                  float *dst) {
-    const int64_t s = blockIdx.x;
-    if (start && start[s] != start[s + 1]) return;
-    for (int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x; i < each; i += (int64_t)gridDim.y * 256)
-        dst[s * each + i] = src ? src[s * each + i] : 0.f;
+int empty_blocks(const int64_t *cu, int64_t nseq) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < nseq; ++i) n += cu[i] == cu[i + 1];
+    return (int)(n == 0 ? 0 : nseq <= 64 ? nseq * 16 : 1024);
 }
-cudaError_t pass_empty_states(const int *start, int64_t nseq, int64_t each, const float *src, float *dst,
-                              cudaStream_t st) {
-    empty_states_kernel<<<dim3((unsigned)nseq, 8), 256, 0, st>>>(start, each, src, dst);
-    timing_mark(st, "empty_states");
-    return cudaGetLastError();
+
+cudaError_t copy_states(const float *src, float *dst, int64_t count, cudaStream_t st) {
+    return src ? cudaMemcpyAsync(dst, src, sizeof(float) * count, cudaMemcpyDeviceToDevice, st)
+               : cudaMemsetAsync(dst, 0, sizeof(float) * count, st);
 }
 
 ssd_status_t check_channel(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) {
@@ -394,7 +401,7 @@ FwdPlan plan_fwd(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) 
     p.nchunk = (int)((L + p.chunk - 1) / p.chunk);
     size_t at = 0;
     p.offsets = at;
-    if (cu) at += align256(sizeof(int) * (nseq + 1));
+    at += offsets_bytes(cu, nseq);
     p.local = at;
     if (p.nchunk > 1) at += align256(sizeof(float) * p.cut * p.nchunk * s->dstate * 32);
     p.sums = at;
@@ -409,27 +416,18 @@ ssd_status_t run_fwd(ChannelArgs<T> &a, const ssd_channel_shape_t *s, const int6
     const FwdPlan p = plan_fwd(s, cu, nseq);
     timing_begin(st);
     cudaError_t e = cudaSuccess;
-    if (cu) {
-        int *dst = reinterpret_cast<int *>(ws + p.offsets);
-        e = write_offsets(cu, nseq, dst, st);
-        if (e != cudaSuccess) return status_of(e);
-        a.seqs.start = dst;
-        bool empty = false;
-        for (int64_t i = 0; i < nseq && !empty; ++i) empty = cu[i] == cu[i + 1];
-        if (empty && a.fin) e = pass_empty_states(dst, nseq, s->channels * s->dstate, a.init, a.fin, st);
-    } else if (s->seqlen == 0 && a.fin) {
-        e = pass_empty_states(nullptr, nseq, s->channels * s->dstate, a.init, a.fin, st);
-    }
+    if (s->seqlen == 0) return status_of(a.fin ? copy_states(a.init, a.fin, nseq * s->channels * s->dstate, st) : e);
+    bool after = false;
+    if (cu) e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws + p.offsets), a.seqs, &after, st);
     if (e != cudaSuccess) return status_of(e);
-    if (s->seqlen == 0) return SSD_OK;
     a.chunk = p.chunk, a.nchunk = p.nchunk;
     a.local = reinterpret_cast<float4 *>(ws + p.local);
     a.sums = reinterpret_cast<float *>(ws + p.sums);
     const int64_t cut = p.cut * p.nchunk;
     if (p.whole + cut > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
     a.whole = (int)p.whole, a.cut = (int)p.cut;
-    const int64_t blocks = (p.whole + cut + kWarps - 1) / kWarps;
-    bool after = cu != nullptr;
+    a.blocks = (unsigned)((p.whole + cut + kWarps - 1) / kWarps);
+    const unsigned blocks = a.blocks + (cu && a.fin ? empty_blocks(cu, nseq) : 0);
     if (p.cut && p.nchunk > 1) {
         e = launch(channel_fwd_kernel<T, N, false, false>, dim3((unsigned)((cut + kWarps - 1) / kWarps)), kWarps * 32, 0, st,
                    after, a);
@@ -437,7 +435,7 @@ ssd_status_t run_fwd(ChannelArgs<T> &a, const ssd_channel_shape_t *s, const int6
         if (e != cudaSuccess) return status_of(e);
         after = true;
     }
-    e = launch(a.z.p ? channel_fwd_kernel<T, N, true, true> : channel_fwd_kernel<T, N, true, false>, dim3((unsigned)blocks),
+    e = launch(a.z.p ? channel_fwd_kernel<T, N, true, true> : channel_fwd_kernel<T, N, true, false>, dim3(blocks),
                kWarps * 32, 0, st, after, a);
     timing_mark(st, "channel_scan");
     return status_of(e);
@@ -503,6 +501,7 @@ ssd_status_t ssd_channel_scan_fwd(const ssd_channel_shape_t *shape, const int64_
     if (nseq == 0) return SSD_OK;
     const bool rows = shape->seqlen > 0;
     if (!channel_inputs_ok(shape, in, rows) || !y || !aligned(final_state, 16)) return SSD_ERR_INVALID_ARG;
+    if (final_state && final_state == in->init_state) return SSD_ERR_INVALID_ARG;  // one is read while the other is written
     if (rows && !rows_out_ok(*y, dtype_size(shape->dtype), shape->batch, shape->seqlen, shape->channels))
         return SSD_ERR_INVALID_ARG;
     const size_t need = plan_fwd(shape, cu_seqlens, nseq).bytes;

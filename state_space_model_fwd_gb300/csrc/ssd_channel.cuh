@@ -84,20 +84,41 @@ struct Span {
     int s, a, e, S, E;
 };
 
-// Sequence offsets on the device (packed batches), or equal lengths.
+// The sequences: equal lengths, or packed offsets, which travel in the launch's
+// parameters when they are few and otherwise lie in the workspace.
+constexpr int kInline = 96;
 struct Seqs {
-    const int *start;  // nullptr: equal lengths
-    int n, L;
+    const int *start;  // nullptr: in `few` (packed) or none
+    int n, L, packed;
+    int few[kInline];
+    // (of a __grid_constant__ parameter)
+    __device__ __forceinline__ const int *offsets() const { return start ? start : few; }
 };
 
-__device__ __forceinline__ int seq_of(const Seqs &q, int t) {  // start[s] <= t < start[s + 1]
-    int lo = 0, hi = q.n;
+__device__ __forceinline__ int seq_of(const int *start, int n, int t) {  // start[s] <= t < start[s + 1]
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int m = (lo + hi) / 2;
-        (q.start[m] <= t ? lo : hi) = m;
+        (start[m] <= t ? lo : hi) = m;
     }
-    while (q.start[lo + 1] <= t) ++lo;  // (empty sequences share an offset)
+    while (start[lo + 1] <= t) ++lo;  // (empty sequences share an offset)
     return lo;
+}
+
+// Empty sequences hand a state on unchanged: dst[s] = src[s] (zero without
+// src) for every s with start[s] == start[s + 1]; `each` floats, a multiple
+// of four.  Run by the last `blocks` blocks of a launch, several a sequence.
+__device__ inline void pass_empty_states(const int *start, int n, int64_t each, const float *src, float *dst, int block,
+                                         int blocks) {
+    const int parts = blocks > n ? blocks / n : 1, part = block / n;
+    if (part >= parts) return;
+    for (int s = block % n; s < n; s += blocks) {
+        if (start[s] != start[s + 1]) continue;
+        const float4 *from = reinterpret_cast<const float4 *>(src + s * each);
+        float4 *to = reinterpret_cast<float4 *>(dst + s * each);
+        for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < each / 4; i += (int64_t)parts * blockDim.x)
+            to[i] = src ? from[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 }
 
 // Channel block: cw channels (or what is left) of one group.

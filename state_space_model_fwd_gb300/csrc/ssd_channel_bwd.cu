@@ -108,13 +108,14 @@ __global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chun
     const Block k = block_of(blk, a.per, a.nblk_g, 32);
     const bool mine = lane < k.nc;
     const int own = k.c0 + (mine ? lane : 0);
-    const bool packed = a.seqs.start != nullptr;
+    const bool packed = a.seqs.packed;
+    const int *start = a.seqs.offsets();
     const int row = packed ? 0 : unit / a.nchunk;
     const int t0 = (packed ? unit : unit % a.nchunk) * a.chunk, t1 = min(a.seqs.L, t0 + a.chunk);
     int s = row, S = 0, E = a.seqs.L;
     if (packed) {
-        s = seq_of(a.seqs, t0);
-        S = a.seqs.start[s], E = a.seqs.start[s + 1];
+        s = seq_of(start, a.seqs.n, t0);
+        S = start[s], E = start[s + 1];
     }
     if (blk == 0 && lane == 0) {
         const bool starts = S == t0 || E < t1;  // (E < t1: another sequence starts at or after E, inside)
@@ -212,25 +213,31 @@ __global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chun
         if (e == t1) return;
         t = e;
         do ++s;
-        while (a.seqs.start[s + 1] <= t);
-        S = a.seqs.start[s], E = a.seqs.start[s + 1];
+        while (start[s + 1] <= t);
+        S = start[s], E = start[s + 1];
     }
 }
 
 // ---------------------------------------------------------------------------
-// 2: the recurrences over chunks.  A thread carries one float4 of a block's
-// states over all chunks of a sequence row; blockIdx.y picks the direction.
+// 2: the recurrences over chunks.  A block owns one float4 a lane of a channel
+// block's states over all chunks of a sequence row; blockIdx.y picks the
+// direction.  One warp walks them all where there are enough blocks (it is
+// then bound by memory: 29 MB each way in 20 us at 4 x 2048 x 1536).  With few
+// blocks the latency of the loads bounds it, and RUNS warps take a run of
+// chunks each: every warp combines its run from zero, then starts it again
+// from the runs before (257 chunks of 640 channels: 37 -> 25 us).
 // ---------------------------------------------------------------------------
-template <typename T, int N>
-__global__ void __launch_bounds__(32) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b, int rows) {
-    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = 32;
+template <typename T, int N, int RUNS>
+__global__ void __launch_bounds__(RUNS * 32) channel_bwd_pass_kernel(const __grid_constant__ BwdArgs<T> b) {
+    constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M, AHEAD = RUNS == 1 ? 16 : 8;
+    __shared__ float4 end[RUNS][32];
+    __shared__ float sum[RUNS][32];
+    __shared__ int reset[RUNS];
     const ChannelArgs<T> &a = b.f;
-    const int64_t id = (int64_t)blockIdx.x * 32 + threadIdx.x;
     launch_next();
     wait_previous();
-    if (id >= (int64_t)rows * a.nblk * (N / 4) * 32) return;
-    const int lane = (int)(id % 32), f = (int)(id / 32 % (N / 4));
-    const int blk = (int)(id / (32 * (N / 4)) % a.nblk), row = (int)(id / (32 * (N / 4)) / a.nblk);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, f = (int)(blockIdx.x % (N / 4));
+    const int blk = (int)(blockIdx.x / (N / 4) % a.nblk), row = (int)(blockIdx.x / (N / 4) / a.nblk);
     const Block k = block_of(blk, a.per, a.nblk_g, 32);
     const int cg = lane / K, q = lane % K, c = cg * K + 4 * f / M;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -239,32 +246,62 @@ __global__ void __launch_bounds__(32) channel_bwd_pass_kernel(const __grid_const
     const bool fwd = blockIdx.y == 0;
     float4 *arr = fwd ? a.local : b.back;
     const int n = a.nchunk, u0 = row * n;
-    float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += AHEAD) {
-        float4 v[AHEAD];
-        float sd[AHEAD];
-        int fl[AHEAD];
+    const int per = (n + RUNS - 1) / RUNS, i_begin = min(n, warp * per), i_end = min(n, i_begin + per);
+    float4 carry;
+    // what leaves a chunk: its own value, and unless that is the whole of it the decayed rest
+    auto combine = [&](bool whole, float sd, const float4 &v) {
+        if (whole) {
+            carry = v;
+        } else {
+            carry.x = fmaf(ex2(A.x * sd), carry.x, v.x);
+            carry.y = fmaf(ex2(A.y * sd), carry.y, v.y);
+            carry.z = fmaf(ex2(A.z * sd), carry.z, v.z);
+            carry.w = fmaf(ex2(A.w * sd), carry.w, v.w);
+        }
+    };
+    float4 v[AHEAD];
+    float sd[AHEAD];
+    int fl[AHEAD];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            if (i0 + j >= n) break;
-            const int u = u0 + (fwd ? i0 + j : n - 1 - i0 - j);
+            if (RUNS == 1 && i0 + j >= i_end) break;
+            const int i = min(i0 + j, i_end - 1), u = u0 + (fwd ? i : n - 1 - i);
             const int64_t at = (int64_t)u * a.nblk + blk;
             v[j] = arr[at * (N / 4 * 32) + f * 32 + lane];
             sd[j] = a.sums[at * 32 + c];
             fl[j] = b.flags[u] & (fwd ? 1 : 2);
         }
+    };
+    carry = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (RUNS > 1) {
+        float total = 0.f;
+        int whole = 0;
+        for (int i0 = i_begin; i0 < i_end; i0 += AHEAD) {
+            load(i0);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                if (i0 + j < i_end) {
+                    combine(fl[j], sd[j], v[j]);
+                    total += sd[j];
+                    whole |= fl[j];
+                }
+            }
+        }
+        end[warp][lane] = carry, sum[warp][lane] = total;
+        if (lane == 0) reset[warp] = whole;
+        __syncthreads();
+        carry = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < warp; ++w) combine(reset[w], sum[w][lane], end[w][lane]);
+    }
+    for (int i0 = i_begin; i0 < i_end; i0 += AHEAD) {
+        load(i0);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            if (i0 + j >= n) break;
-            const int u = u0 + (fwd ? i0 + j : n - 1 - i0 - j);
-            arr[((int64_t)u * a.nblk + blk) * (N / 4 * 32) + f * 32 + lane] = carry;
-            if (fl[j]) {  // the chunk's own value is the whole of it
-                carry = v[j];
-            } else {
-                carry.x = fmaf(ex2(A.x * sd[j]), carry.x, v[j].x);
-                carry.y = fmaf(ex2(A.y * sd[j]), carry.y, v[j].y);
-                carry.z = fmaf(ex2(A.z * sd[j]), carry.z, v[j].z);
-                carry.w = fmaf(ex2(A.w * sd[j]), carry.w, v[j].w);
+            if (i0 + j < i_end) {
+                const int u = u0 + (fwd ? i0 + j : n - 1 - i0 - j);
+                arr[((int64_t)u * a.nblk + blk) * (N / 4 * 32) + f * 32 + lane] = carry;
+                combine(fl[j], sd[j], v[j]);
             }
         }
     }
@@ -331,7 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
     const int cg = lane / K, q = lane % K;
     const bool mine = lane < k.nc;
     const int own = k.c0 + (mine ? lane : 0);
-    const bool packed = a.seqs.start != nullptr;
+    const bool packed = a.seqs.packed;
+    const int *start = a.seqs.offsets();
 
     f2 A2[K][M2], dA[K][M2];
     load_decay<T, N>(a, k, lane, A2);
@@ -350,8 +388,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
         // the chunk's pieces of sequences, last one first
         int s = row, S = 0, E = a.seqs.L, e = t1;
         if (packed) {
-            s = seq_of(a.seqs, t1 - 1);
-            S = a.seqs.start[s], E = a.seqs.start[s + 1];
+            s = seq_of(start, a.seqs.n, t1 - 1);
+            S = start[s], E = start[s + 1];
         }
         while (live) {
             const int begin = max(t0, S), off = begin - t0, ns = (e - begin + TB - 1) / TB;
@@ -545,8 +583,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             if (begin == t0) break;
             e = begin;
             do --s;
-            while (a.seqs.start[s] == a.seqs.start[s + 1]);
-            S = a.seqs.start[s], E = a.seqs.start[s + 1];
+            while (start[s] == start[s + 1]);
+            S = start[s], E = start[s + 1];
         }
         // add the block's warps
         __syncthreads();
@@ -573,10 +611,16 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
 // 4: sums over channel blocks (dB, dC) and over slots (dA, dD, ddt_bias)
 // ---------------------------------------------------------------------------
 template <typename T, int N>
-__global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_constant__ BwdArgs<T> b, int64_t bc_blocks) {
+__global__ void __launch_bounds__(256) channel_bwd_reduce_kernel(const __grid_constant__ BwdArgs<T> b, int64_t bc_blocks,
+                                                                 unsigned blocks) {
     constexpr int K = BwdTile<N>::K, M = BwdTile<N>::M;
     const ChannelArgs<T> &a = b.f;
     wait_previous();
+    if (blockIdx.x >= blocks) {
+        pass_empty_states(a.seqs.offsets(), a.seqs.n, (int64_t)a.ch * N, b.dfinal, b.dinit, blockIdx.x - blocks,
+                          gridDim.x - blocks);
+        return;
+    }
     if (blockIdx.x < bc_blocks) {
         const int groups = a.nblk / a.nblk_g;
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -636,7 +680,7 @@ struct BwdPlan {
             at += align256(n);
             return r;
         };
-        offsets = take(cu ? sizeof(int) * (nseq + 1) : 0);
+        offsets = take(offsets_bytes(cu, nseq));
         flags = take(sizeof(int) * units);
         local = take(sizeof(float) * units * nblk * N * 32);
         back = take(sizeof(float) * units * nblk * N * 32);
@@ -655,18 +699,11 @@ ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t 
     ChannelArgs<T> &a = b.f;
     timing_begin(st);
     cudaError_t e = cudaSuccess;
-    const int64_t each = s->channels * s->dstate;
-    if (cu) {
-        int *dst = reinterpret_cast<int *>(ws + p.offsets);
-        e = write_offsets(cu, nseq, dst, st);
-        if (e != cudaSuccess) return status_of(e);
-        a.seqs.start = dst;
-        bool empty = false;
-        for (int64_t i = 0; i < nseq && !empty; ++i) empty = cu[i] == cu[i + 1];
-        if (empty && b.dinit) e = pass_empty_states(dst, nseq, each, b.dfinal, b.dinit, st);
-    } else if (s->seqlen == 0 && b.dinit && nseq > 0) {
-        e = pass_empty_states(nullptr, nseq, each, b.dfinal, b.dinit, st);
-    }
+    bool after = false;
+    if (s->seqlen == 0 && b.dinit && nseq > 0)
+        e = copy_states(b.dfinal, b.dinit, nseq * s->channels * s->dstate, st);
+    else if (cu)
+        e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws + p.offsets), a.seqs, &after, st);
     if (e != cudaSuccess) return status_of(e);
     a.chunk = Geo<N>::CH, a.nchunk = p.nchunk, a.units = (int)p.units;
     a.local = reinterpret_cast<float4 *>(ws + p.local);
@@ -678,19 +715,17 @@ ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t 
     b.quads = p.quads, b.slots = p.slots;
     b.tokens = s->batch * s->seqlen;
     if (p.units > 0) {
-        const int rows = cu ? 1 : (int)s->batch;
         const int64_t warps = (p.units * p.nblk + kWarps - 1) / kWarps;
-        const int64_t threads = (int64_t)rows * p.nblk * (N / 4) * 32;
+        const int64_t passes = (int64_t)(cu ? 1 : s->batch) * p.nblk * (N / 4);
         const int64_t grads = (int64_t)s->ngroups * p.quads * p.slots;
-        if (warps > 0x7FFFFFFF || threads / 32 > 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
-        bool after = cu != nullptr;
+        if (warps > 0x7FFFFFFF || passes > 0x7FFFFFFF || grads > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
         if (p.nchunk > 1) {
             e = launch(a.z.p ? channel_bwd_chunk_kernel<T, N, true> : channel_bwd_chunk_kernel<T, N, false>,
                        dim3((unsigned)warps), kWarps * 32, 0, st, after, b);
             timing_mark(st, "channel_bwd_chunk");
             if (e == cudaSuccess)
-                e = launch(channel_bwd_pass_kernel<T, N>, dim3((unsigned)(threads / 32), 2), 32, 0, st, true, b,
-                           rows);
+                e = passes < 304 ? launch(channel_bwd_pass_kernel<T, N, 8>, dim3((unsigned)passes, 2), 256, 0, st, true, b)
+                                 : launch(channel_bwd_pass_kernel<T, N, 1>, dim3((unsigned)passes, 2), 32, 0, st, true, b);
             timing_mark(st, "channel_bwd_pass");
             if (e != cudaSuccess) return status_of(e);
             after = true;
@@ -703,8 +738,9 @@ ssd_status_t run_bwd(BwdArgs<T> &b, const ssd_channel_shape_t *s, const int64_t 
         if (e != cudaSuccess) return status_of(e);
     }
     const int64_t bc = (b.tokens * s->ngroups * 2 * N + 255) / 256, ab = (p.nblk * (N + 2) * 32 + 255) / 256;
-    if (bc + ab > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
-    e = launch(channel_bwd_reduce_kernel<T, N>, dim3((unsigned)(bc + ab)), 256, 0, st, p.units > 0 || cu, b, bc);
+    if (bc + ab > 0x7FFFF000) return SSD_ERR_UNSUPPORTED;
+    const unsigned blocks = (unsigned)(bc + ab), empty = cu && b.dinit && s->seqlen > 0 ? empty_blocks(cu, nseq) : 0;
+    e = launch(channel_bwd_reduce_kernel<T, N>, dim3(blocks + empty), 256, 0, st, p.units > 0, b, bc, blocks);
     timing_mark(st, "channel_bwd_reduce");
     return status_of(e);
 }

@@ -689,6 +689,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, const int64_t *cu_seqle
     if (nseq == 0) return SSD_OK;
     if (!x || !y || !weight || !aligned(weight, 4) || !aligned(bias, 4)) return SSD_ERR_INVALID_ARG;
     if (!states_ok({init_state, final_state}, es)) return SSD_ERR_INVALID_ARG;
+    if (final_state && final_state == init_state) return SSD_ERR_INVALID_ARG;  // one is read while the other is written
     if (shape->seqlen > 0) {
         if (!rows_in_ok(*x, es)) return SSD_ERR_INVALID_ARG;
         for (int64_t i = 0; i < shape->nparts; ++i)
