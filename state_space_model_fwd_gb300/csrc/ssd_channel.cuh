@@ -4,18 +4,18 @@
 //   delta = softplus(dt + dt_bias),  h_n <- exp(delta A_n) h_n + delta x B_n,
 //   y = sum_n h_n C_n + D x  (times silu(z)).
 //
-// A warp owns a block of channels of one group.  Q lanes share a channel's
-// states; lane l = cg * Q + q holds, for the K channels cg * K .. cg * K + K - 1,
-// the M = N / Q states q * M ..: a tile of K x M states, so that one token's B
-// and C (M values each) serve K channels and its delta and delta x (K values
-// each) serve M states.  Four operations, one exponential and
-// (M + K) / (K M) * 8 bytes of shared memory a state: with one channel a lane
-// the shared-memory reads alone would take twice the time of the arithmetic.
-// Everything per channel and token (softplus, gates, D x, loads and stores,
-// whatever the alignment of rows) is spread over the lanes: W = Q / K tokens
-// at a time, lane l takes channel cg * K + q / W of token q % W of them.  Sums
-// over a channel's states are transposed on the way through the shuffles, so
-// that they end in that lane.
+// A warp owns 32 channels of one group, in one of two arrangements:
+//   one channel a lane (Tile<N, 1, 1>): a lane has its channel's N states and
+//     its delta in registers and sums over states by itself; B and C are read
+//     from shared memory as broadcasts, N / 2 reads of 16 bytes a token;
+//   square (Tile<N, Q, Q>): lane l = cg * Q + q has the M = N / Q states q * M ..
+//     of the Q channels cg * Q ..: a third of the reads, an eighth of the
+//     lanes to sum dB and dC over, but sums over a channel's states go through
+//     shuffles, transposed on the way so that lane l ends with channel l.
+// The forward kernel and the chunk summaries take the first, the gradient
+// inside chunks the second.  Either way what is per channel and token
+// (softplus, gates, D x, loads and stores, whatever the alignment of rows) is
+// done by lane l for channel l.
 #pragma once
 
 #include "ssd_layer.cuh"
@@ -68,20 +68,13 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(s, q, fmaxf(v, 0.f));
 }
 
-// Tile shape for N states on Q lanes, K channels a lane.
+// Tile shape for N states: K channels on Q lanes.
 template <int N_, int Q_, int K_>
 struct Tile {
     static constexpr int N = N_, Q = Q_, K = K_;
     static constexpr int M = N / Q, M2 = M / 2;  // states a lane holds of each channel
-    static constexpr int W = Q / K;              // tokens the lanes of a group take at a time
-    static constexpr int CW = 32 / Q * K;        // channels of a block
     static constexpr int E4 = K * M / 4;         // float4s a lane holds
     using Regs = f2[K][M2];
-};
-
-// A sequence's stretch of a chunk: tokens [a, e) of sequence s = [S, E).
-struct Span {
-    int s, a, e, S, E;
 };
 
 // The sequences: equal lengths, or packed offsets, which travel in the launch's
@@ -208,25 +201,6 @@ __device__ __forceinline__ void load_m(const float *p, f2 (&v)[M / 2]) {
     for (int j = 0; j < M; j += 4) {
         const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(p + j);
         v[j / 2] = r.x, v[j / 2 + 1] = r.y;
-    }
-}
-
-// Per-channel values staged twice each, (v, v), so that a load gives packed
-// operands: channel i of its lane group's K sits in 16-byte row i / 2, and the
-// 32 / Q groups of a row are contiguous (no bank conflicts).
-template <typename G>
-__device__ __forceinline__ int pair_slot(int cg, int i) {
-    return i / 2 * (128 / G::Q) + cg * 4 + i % 2 * 2;
-}
-__device__ __forceinline__ void store_pair(float *row, int slot, float v) {
-    *reinterpret_cast<float2 *>(row + slot) = make_float2(v, v);
-}
-template <typename G>
-__device__ __forceinline__ void load_pairs(const float *row, int cg, f2 (&v)[G::K]) {
-#pragma unroll
-    for (int h = 0; h < G::K / 2; ++h) {
-        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(row + h * (128 / G::Q) + cg * 4);
-        v[2 * h] = r.x, v[2 * h + 1] = r.y;
     }
 }
 

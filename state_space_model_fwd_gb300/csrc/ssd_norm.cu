@@ -24,8 +24,8 @@ enum Gate : int { kNone, kBefore, kAfter };
 template <typename T>
 struct Mat {
     T *p;
-    int64_t rs;
-    __device__ __forceinline__ T *at(int64_t row, int c) const { return p + row * rs + c; }
+    int rs;
+    __device__ __forceinline__ T *at(int row, int c) const { return p + (int64_t)row * rs + c; }
 };
 
 template <typename T, typename TR>
@@ -88,11 +88,13 @@ __device__ __forceinline__ void team_sum(float (&v)[R], float (&smem)[32 * R]) {
 #pragma unroll
             for (int r = 0; r < R; ++r) smem[threadIdx.x / 32 * R + r] = v[r];
         __syncthreads();
+        const int lane = threadIdx.x % 32;
 #pragma unroll
-        for (int r = 0; r < R; ++r) v[r] = 0.f;
-        for (int w = 0; w < warps; ++w)
+        for (int r = 0; r < R; ++r) v[r] = lane < warps ? smem[lane * R + r] : 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) v[r] += smem[w * R + r];
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], off);
     }
 }
 
@@ -101,14 +103,14 @@ constexpr int kAnyGate = -1;   // the gate is read at run time (rare widths)
 
 // NV vectors of V values per thread cover the group.
 template <typename T, typename TR, int V, int NV, bool WARP, int GATE>
-__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 1024 : 512, 1)
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 1024 : 512, WARP || GATE == kAnyGate ? 1 : 3)
     norm_fwd_kernel(const __grid_constant__ NormArgs<T, TR> a) {
     __shared__ float smem[32];
     const int gate = GATE == kAnyGate ? a.gate : GATE;
     const int team = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x % 32 : threadIdx.x;
     const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + threadIdx.x / 32 : blockIdx.x;
     if (id >= a.rows * a.ngroups) return;  // (whole teams)
-    const int64_t row = a.ngroups == 1 ? id : id / a.ngroups;
+    const int row = (int)(a.ngroups == 1 ? id : id / a.ngroups);
     const int c0 = a.ngroups == 1 ? 0 : (int)(id % a.ngroups) * a.group;
     Raw<T, V> x[NV], z[NV];
     Raw<TR, V> res[NV];
@@ -194,7 +196,8 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 10
         for (int v = 0; v < V; ++v) dw[i][v] = dsc[i][v] = 0.f;
     const bool need_x = !a.res.p || gate == kBefore || a.scale;
     int turn = 0;
-    for (int64_t row = slot; row < a.rows; row += slots, turn ^= 1) {
+    for (int64_t r64 = slot; r64 < a.rows; r64 += slots, turn ^= 1) {
+        const int row = (int)r64;
         Raw<T, V> x[NV], z[NV], go[NV];
         Raw<TR, V> res[NV], dres[NV];
 #pragma unroll
@@ -310,18 +313,19 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 10
     }
 }
 
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ partial, int slots, int dim,
-                                                          float *__restrict__ dweight, float *__restrict__ dscale) {
-    __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ partial, int slots, int dim,
+                                                           float *__restrict__ dweight, float *__restrict__ dscale) {
+    __shared__ float red[32][32];
     const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
     float s = 0.f;
     if (c < dim)
-        for (int q = threadIdx.y; q < slots; q += 8) s += partial[((int64_t)q * 2 + k) * dim + c];
+#pragma unroll 4
+        for (int q = threadIdx.y; q < slots; q += 32) s += partial[((int64_t)q * 2 + k) * dim + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < dim) {
 #pragma unroll
-        for (int q = 1; q < 8; ++q) s += red[q][threadIdx.x];
+        for (int q = 1; q < 32; ++q) s += red[q][threadIdx.x];
         float *dst = k ? dscale : dweight;
         if (dst) dst[c] = s;
     }
@@ -378,7 +382,7 @@ bool row_ok(const ssd_rows_t &r, size_t es) { return rows_in_ok(r, es); }
 
 template <typename T>
 Mat<T> mat(const ssd_rows_t &r) {
-    return {static_cast<T *>(r.data), r.row_stride};
+    return {static_cast<T *>(r.data), (int)r.row_stride};
 }
 
 template <typename T, typename TR>
@@ -461,7 +465,7 @@ ssd_status_t bwd_typed(const ssd_norm_shape_t *s, const ssd_rows_t *dout, const 
         });
         if (e != SSD_OK) return e;
     }
-    norm_reduce_kernel<<<dim3((unsigned)((a.dim + 31) / 32), scale && dscale ? 2 : 1), dim3(32, 8), 0, st>>>(
+    norm_reduce_kernel<<<dim3((unsigned)((a.dim + 31) / 32), scale && dscale ? 2 : 1), dim3(32, 32), 0, st>>>(
         a.partial, slots, a.dim, dweight, dscale);
     timing_mark(st, "norm_reduce");
     return status_of(cudaGetLastError());
