@@ -353,7 +353,7 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_shape_t *shape, const void *x, co
  * boundary, not even a non-finite value.  An empty sequence hands its
  * initial state on as its final state, and the other way for gradients.
  * State and parameter arrays are contiguous and need their element type's
- * alignment.  Everything else (streams, ownership, errors, reproducibility)
+ * alignment; a final state must not be the initial state's array.  Everything else (streams, ownership, errors, reproducibility)
  * is as for the other entry points; dtype is fp32 or bf16.
  * ------------------------------------------------------------------------ */
 typedef struct {

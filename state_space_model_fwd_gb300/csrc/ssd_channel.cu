@@ -1,14 +1,20 @@
 // ssd_channel.cu -- the channel scan over prompts and single tokens, and the
 // host side of all its entry points.  (Gradient kernels: ssd_channel_bwd.cu.)
 //
-// Forward.  With b * channels / 32 warps enough to fill the SMs, one pass
-// walks every sequence.  With fewer, the tokens are cut into chunks: a first
-// launch forms every chunk's end state from a zero start (or from the
-// sequence's own start) and the sum of its deltas; the second starts a chunk
-// from the combination of the earlier ones, where a chunk's decay is
-// exp(A sum delta), and writes y.  That costs up to 1.75 times the arithmetic
-// on SMs that would otherwise idle.  Chunks are cut without regard to
-// sequences, which restart the state inside a chunk.
+// Forward.  A block row is 32 channels of a sequence row, one warp's work.  Where
+// there are two for every warp scheduler, one pass walks every sequence.  With
+// fewer, the tokens are cut into chunks: a first launch forms every chunk's end
+// state from a zero start (or from the sequence's own start) and the sum of its
+// deltas; the second starts a chunk from the combination of the earlier ones,
+// where a chunk's decay is exp(A sum delta), and writes y.  That costs up to
+// 1.6 times the arithmetic on SMs that would otherwise idle.  Chunks are cut
+// without regard to sequences, which restart the state inside a chunk.
+//
+// Bound by instruction issue and what two warps a scheduler leave uncovered of
+// the instructions' latencies: 109 instructions a token and warp (16 states), 32
+// of them packed multiply-adds that take two issue cycles, 16 exponentials; 816
+// us at 8 x 4096 x 5120 bf16 with gate, three quarters of the issue cycles.  The
+// bytes would take 199 us, the fp32 results alone (4 a state) 290 us.
 #include <type_traits>
 
 #include "ssd_channel.h"
@@ -56,11 +62,12 @@ struct Ahead {
 
 // A lane is a channel: its N states, their decay rates and its delta stay in
 // registers, nothing is summed over lanes, and B and C come from shared
-// memory as broadcasts (N / 2 reads of 16 bytes a token, which bounds how
-// fast this can go at 4 N cycles an SM for 32 channels; the arithmetic takes
-// about as long).  A square tile of channels and states a lane reads a third
-// of that but pays 40 instructions a token to stage delta and to transpose
-// the sums: 1.06 ms against 1.26-1.77 for 8 x 4096 x 5120.
+// memory as broadcasts, N / 2 reads of 16 bytes a token.  A square tile of
+// channels and states a lane reads a third of that but needs 25 instructions
+// more a token to stage delta and to transpose the sums.
+// Nothing branches between the staging and the stores: with the gate's switch
+// and predicated stores inside the token loop, tokens did not overlap and the
+// same case took 1400 us.
 //
 // FULL: outputs; otherwise only the chunk's end state and sum of deltas.  The
 // warps of a block share nothing.

@@ -6,20 +6,25 @@
 //   dC_t = sum_c g_t h_t,  dB_t = sum_c delta_t x_t dh_t
 //   du_t = sum_n dh_t B_t,  w_t = dh_t a_t h_{t-1}
 //   dx_t = delta_t du_t + D g_t,  ddelta_t = x_t du_t + sum_n w_t A,  dA = sum_t w_t delta_t
-// Four launches over chunks of 32 tokens (16 for 32 states):
+// Four launches over chunks of 28 tokens (32 with 8 states, 16 with 32):
 //   1 chunk summaries: the state a chunk leaves from a zero start, the
 //     gradient its outputs send back to the state before it, its sum of
 //     deltas (exp(A sum delta) is its decay);
 //   2 the two recurrences over chunks, in place: the state entering and the
 //     gradient leaving every chunk;
-//   3 per chunk: forward once, keeping every kTB-th state in shared memory;
-//     then backward kTB tokens at a time, whose states and decays are formed
+//   3 per chunk: forward once, keeping every fourth state in shared memory;
+//     then backward TB tokens at a time, whose states and decays are formed
 //     again and stay in registers.  dB and dC are summed over the lanes of a
 //     warp, then over the block's 128 channels; dA, dD and ddt_bias over the
 //     chunks a block walks;
 //   4 the sums over channel blocks and over blocks, in a fixed order.
-// About 15 issue slots a state (1 and 3 together), most of it arithmetic:
-// bound by issue, with eight warps an SM (their registers).
+// Bound by instruction issue.  At 4 x 2048 x 1536, 16 states, bf16 with gate
+// the launches take 95, 15, 270 and 5 us: 162 and 449 instructions a token and
+// warp in 1 and 3, 48 and 125 of them packed multiply-adds of two issue cycles
+// each.  3 runs eight warps an SM (254 registers: the states and decays of four
+// tokens are 128 of them) at 55 % issue; what its loads cost it was hidden by
+// taking a chunk's values half a chunk at a time, all in flight (618 -> 272 us
+// with a grid of one wave).
 #include <type_traits>
 
 #include "ssd_channel.h"

@@ -4,12 +4,16 @@
 //   p[t, c] = bias[c] + sum_k weight[c, k] x[t - (W-1) + k, c],  y = silu(p)
 //
 // W + 5 operations an element against 2 (forward) or 3 (gradient) element
-// transfers: bound by memory.  A thread owns four channels
-// and walks down the tokens with the last W-1 rows in registers, so each row
-// is read once (and W-1 rows more per tile); a warp reads 256 (bf16) or 512
-// consecutive bytes of a row, and the next rows are in flight while one is computed.
-// Channels are independent, so y is written straight into the x, B and C
+// transfers: bound by memory, with instruction issue not far behind in bf16.
+// A thread owns four channels and walks down the tokens with the last W-1 rows
+// in registers, so each row is read once (and W-1 rows more per tile); a warp
+// reads 256 (bf16) or 512 consecutive bytes of a row, and the next four rows
+// are in flight while four are computed.  (Eight channels a thread halve the
+// address arithmetic but leave 16 warps an SM instead of 24: 292 against 261
+// us.)  Channels are independent, so y is written straight into the x, B and C
 // arrays a scan takes, out of the projection's rows in place.
+// bf16, W 4: 65537 packed tokens x 5376 channels in 256 us, 5.5 TB/s; the
+// gradient at 4 x 4095 x 2560 in 55 us and 4 for the sums, 4.2 TB/s.
 //
 // Tokens are cut into tiles without regard to sequences: a tile walks its
 // pieces of sequences one after another and rebuilds the window (from the

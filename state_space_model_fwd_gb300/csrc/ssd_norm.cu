@@ -8,7 +8,11 @@
 // A (row, group) is read once, all its loads in flight together, reduced over
 // a team of threads and written from registers.  The team is a warp for short
 // groups, several to a block, and otherwise a block of just enough threads
-// for NV vectors each, so that few threads idle whatever the width.
+// for NV vectors each, so that few threads idle whatever the width.  The gate
+// is fixed at compile time for widths up to 8192 (read at run time inside the
+// loops it cost the gradient 117 us instead of 73).
+// bf16: 16384 x 5120 gated in 81 us, 6.2 TB/s; the gradient with an fp32
+// residual and scale at 8191 x 2560 in 70 us and 4 for the sums, 5.1 TB/s.
 #include <type_traits>
 
 #include "ssd_layer.cuh"
