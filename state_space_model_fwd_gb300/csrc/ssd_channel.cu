@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
                     }
                 }
                 if (FULL) {
-                    o[j] = fmaf(D, x[j], sum2(acc[0]) + sum2(acc[1]));
+                    o[j] = fmaf(D, x[j], sum2(add2(acc[0], acc[1])));
                     if (GATE) o[j] *= silu(z[GATE ? j : 0]);
                 }
             }
