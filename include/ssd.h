@@ -418,7 +418,7 @@ SSD_API ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, const ssd_rows
  * without z).  Nothing from the forward call is needed.
  * ssd_channel_scan_step: one token per sequence; rows are [b, ...]
  * (row_stride ignored), state [b, Ch, N] advanced in place, init_state
- * ignored.
+ * ignored; up to 262140 sequences.
  */
 typedef struct {
     int64_t batch, seqlen, channels, dstate, ngroups;

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kLanes *kSub, 3) conv_fwd_kernel(const __grid_
             const Vec<T, V> v = row_at<T, W, V>(a, x, p, row, p.a - (W - 1) + j, c0);
             widen<T, V>(v, win[j]);
         }
+#pragma unroll 2  // (two steps swap the rows in flight and those computed without copies)
         for (int t = p.a; t < p.e; t += kAhead) {
             const int n = p.e - t;
             float o[kAhead][V];
