@@ -12,7 +12,7 @@
 //
 // Bound by instruction issue and what two warps a scheduler leave uncovered of
 // the instructions' latencies: 109 instructions a token and warp (16 states), 32
-// of them packed multiply-adds that take two issue cycles, 16 exponentials; 816
+// of them packed multiply-adds that take two issue cycles, 16 exponentials; 804
 // us at 8 x 4096 x 5120 bf16 with gate, three quarters of the issue cycles.  The
 // bytes would take 199 us, the fp32 results alone (4 a state) 290 us.
 #include <type_traits>
@@ -397,9 +397,11 @@ FwdPlan plan_fwd(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) 
     const int64_t L = s->seqlen, base = nblk * (cu ? 1 : s->batch);
     p.whole = cu || base < 2 * kSched ? 0 : base / kSched * kSched;
     p.cut = base - p.whole;
-    // a tail of more than 7/8 of a round, or behind eight rounds, is not worth cutting
+    // A tail of more than 7/8 of a warp for every scheduler, or behind eight of them, is not worth cutting
+    // (11 x 2048 x 5120, 2.9 warps each: 633 us whole, 685 cut; 60 x 512 x 5120, 15.8: 756 and 788; on the
+    // other side 8 x 4096 x 5120, 2.1: 1180 and 804).
     if (p.whole && (p.cut * 8 > kSched * 7 || base >= 8 * kSched)) p.whole = base, p.cut = 0;
-    int64_t want = p.cut ? 2 * kSched / p.cut : 1;  // one round of all of them
+    int64_t want = p.cut ? 2 * kSched / p.cut : 1;  // two for every scheduler, at most
     if (want > (L + 63) / 64) want = (L + 63) / 64;
     if (want < 1) want = 1;
     if (want == 1) p.whole = cu ? 0 : base, p.cut = base - p.whole;
