@@ -177,6 +177,8 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 10
     }
 }
 
+__device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Gradient.  With hat = s rstd and gw = dout (silu z) w:
 //   ds = rstd (gw - hat mean(gw hat)) + dres,  both means from one reduction;
 //   dresidual = ds, dv = scale ds, dscale = sum_rows ds v, dweight = sum_rows dout (silu z) hat.
@@ -214,6 +216,20 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 10
                 if (need_x) x[i].load(a.x.at(row, c));
                 if (gate != kNone) z[i].load(a.z.at(row, c));
                 if (a.dres.p) dres[i].load(a.dres.at(row, c));
+            }
+        }
+        if (r64 + slots < a.rows) {  // the next row on its way to L2 meanwhile (4096 x 5120: 89 -> 70 us, narrow rows alike)
+            const int next = row + slots;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int at = (i * team + lane) * V, c = c0 + at;
+                if (at < a.group) {
+                    prefetch(a.dout.at(next, c));
+                    if (a.res.p) prefetch(a.res.at(next, c));
+                    if (need_x) prefetch(a.x.at(next, c));
+                    if (gate != kNone) prefetch(a.z.at(next, c));
+                    if (a.dres.p) prefetch(a.dres.at(next, c));
+                }
             }
         }
         float s[NV][V], w[NV][V];
