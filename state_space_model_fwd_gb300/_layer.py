@@ -455,16 +455,17 @@ def _norm_rows(t, name, dtype, shape, idx):
         raise ValueError(f"{name} must be contiguous in its last dimension")
     if len(st) == 2:
         return _rows_t(t.data_ptr(), 0, st[0])
-    rs = want = 0
+    if 0 in shape:  # no rows
+        return _rows_t(t.data_ptr(), 0, shape[-1])
+    rs, span = 0, None  # span: the stride that the next dimension out has to have (None: none seen yet)
     for i in range(len(shape) - 2, -1, -1):
         if shape[i] == 1:
             continue
-        if want == 0:
-            rs, want = st[i], st[i] * shape[i]
-        elif st[i] != want:
-            raise ValueError(f"{name}'s rows must lie at one stride")
-        else:
-            want *= shape[i]
+        if span is None:
+            rs = st[i]
+        elif st[i] != span:
+            raise ValueError(f"{name}'s rows must lie at one stride, got strides {st}")
+        span = st[i] * shape[i]
     return _rows_t(t.data_ptr(), 0, rs)
 
 
@@ -492,8 +493,8 @@ def ssd_block_norm_fwd(x, weight, *, z=None, residual=None, scale=None, eps=1e-5
         out = s / sqrt(mean(s^2) + eps) * weight  (* silu(z) with gate_after)
 
     the mean over groups of ``group_size`` columns (all by default).  x, z
-    [..., dim]; residual the same shape in x's type or fp32; weight, scale
-    [dim] fp32.  Returns ``(out, residual_out)``, residual_out = s in the
+    [..., dim], all rows of an operand at one stride (0: one row for all);
+    residual the same shape in x's type or fp32; weight, scale [dim] fp32.  Returns ``(out, residual_out)``, residual_out = s in the
     residual's type (None without a residual)."""
     lib = _lib()
     shape, dev = _norm_shape(x, group_size, eps, residual, gate_after)
