@@ -151,6 +151,8 @@ def _need(t, name, dtype=None, shape=None):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _layer._current_device():  # kernels run there, whatever the stream
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_layer._current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:

@@ -5,7 +5,8 @@ Token-major operands (x, y, gradients) may be strided views whose last
 dimension is contiguous, such as column slices of a projection's rows; states
 and parameters are contiguous.  ``cu_seqlens`` is a host sequence of
 nseq + 1 offsets as for ssd_fwd_varlen; without it every batch row is one
-sequence.  Every function takes ``stream`` (the current one by default).
+sequence.  Operands are on the current device; every function takes
+``stream`` (the current one by default).
 Argument marshalling only, as everywhere in this package.
 """
 from __future__ import annotations
@@ -109,6 +110,10 @@ def _on_stream(fn):
     return call
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 # These run several times a call, and a call for one token takes a few
 # microseconds on the GPU: the checks that pass are few and plain.
 def _code(x, name="x"):
@@ -118,7 +123,10 @@ def _code(x, name="x"):
     code = _CODE.get(x.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
-    return code, x.get_device()
+    idx, current = x.get_device(), _current_device()
+    if idx != current:  # kernels run on the current device, whatever the stream
+        raise ValueError(f"{name} is on cuda:{idx}, the current device is cuda:{current}")
+    return code, idx
 
 
 def _refuse(t, name, dtype, shape, idx):

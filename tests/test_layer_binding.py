@@ -3,7 +3,14 @@ strides, devices, workspaces and arguments.  No call here reaches a kernel."""
 import pytest
 import torch
 
-from state_space_model_fwd_gb300 import _layer
+import state_space_model_fwd_gb300 as ssd
+from state_space_model_fwd_gb300 import _build, _layer
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    _build.build()
+    return ssd.load_library()
 
 
 # ---- rows of the block norm: every leading dimension at one stride ---------
@@ -53,3 +60,46 @@ def test_a_sums_gradient_is_such_a_tensor():
     assert dout.stride() == (64, 0, 1)
     with pytest.raises(ValueError, match="one stride"):
         norm_rows(dout)
+
+
+# ---- devices ---------------------------------------------------------------
+class OnCuda1(torch.Tensor):
+    """A tensor that says it is on the second GPU."""
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", 1))
+
+    def get_device(self):
+        return 1
+
+
+def on_cuda1(*shape):
+    return torch.zeros(*shape).as_subclass(OnCuda1)
+
+
+t = on_cuda1
+ENTRIES = {
+    "ssd_conv_fwd": lambda: ssd.ssd_conv_fwd(t(1, 8, 16), t(16, 4)),
+    "ssd_conv_bwd": lambda: ssd.ssd_conv_bwd(t(1, 8, 16), t(1, 8, 16), t(16, 4)),
+    "ssd_conv_step": lambda: ssd.ssd_conv_step(t(1, 16), t(16, 4), state=t(1, 3, 16)),
+    "ssd_channel_scan_fwd": lambda: ssd.ssd_channel_scan_fwd(t(1, 8, 32), t(1, 8, 32), t(32, 16), t(1, 8, 1, 16),
+                                                             t(1, 8, 1, 16)),
+    "ssd_channel_scan_bwd": lambda: ssd.ssd_channel_scan_bwd(t(1, 8, 32), t(1, 8, 32), t(1, 8, 32), t(32, 16),
+                                                             t(1, 8, 1, 16), t(1, 8, 1, 16)),
+    "ssd_channel_scan_step": lambda: ssd.ssd_channel_scan_step(t(1, 32), t(1, 32), t(32, 16), t(1, 1, 16), t(1, 1, 16),
+                                                               state=t(1, 32, 16)),
+    "ssd_block_norm_fwd": lambda: ssd.ssd_block_norm_fwd(t(4, 64), t(64)),
+    "ssd_block_norm_bwd": lambda: ssd.ssd_block_norm_bwd(t(4, 64), t(4, 64), t(64)),
+    "ssd_fwd": lambda: ssd.ssd_fwd(t(1, 64, 2, 16), t(1, 64, 2), t(2), t(1, 64, 1, 16), t(1, 64, 1, 16)),
+    "ssd_fwd_varlen": lambda: ssd.ssd_fwd_varlen(t(1, 64, 2, 16), t(1, 64, 2), t(2), t(1, 64, 1, 16), t(1, 64, 1, 16),
+                                                 cu_seqlens=[0, 64]),
+    "selective_scan_fwd": lambda: ssd.selective_scan_fwd(t(1, 8, 2, 16), t(1, 8, 2), t(2), t(1, 8, 1, 16), t(1, 8, 1, 16)),
+    "ssd_decode_step": lambda: ssd.ssd_decode_step(t(1, 2, 16), t(1, 2), t(2), t(1, 1, 16), t(1, 1, 16),
+                                                   state=t(1, 2, 16, 16)),
+}
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_operands_on_another_than_the_current_device_are_refused(entry, monkeypatch):
+    monkeypatch.setattr(_layer, "_current_device", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        ENTRIES[entry]()
