@@ -204,6 +204,7 @@ def ssd_fwd(x, dt, A, B, C, D=None, init_state=None, chunk_size=64, *, y=None, f
         final_state = torch.empty((b, H, P, N), device=x.device, dtype=torch.float32)
     _need(final_state, "final_state", torch.float32, (b, H, P, N))
     ws_bytes = int(lib.ssd_fwd_workspace_size(ctypes.byref(shape)))
+    _need(workspace, "workspace")
     if workspace is None or workspace.numel() < ws_bytes:
         workspace = torch.empty(max(ws_bytes, 16), device=x.device, dtype=torch.uint8)
     st = lib.ssd_fwd(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -309,6 +310,7 @@ def ssd_chunk_scan(x, dt, B, C, dA_cumsum, states_in, D=None, *, out=None, y_dty
     _need(out, "y", y_dtype, x.shape)
     shape = make_shape(x, B, Q, y_dtype)
     ws_bytes = int(lib.ssd_chunk_scan_workspace_size(ctypes.byref(shape)))
+    _need(workspace, "workspace")
     if ws_bytes and (workspace is None or workspace.numel() < ws_bytes):
         workspace = torch.empty(ws_bytes, device=x.device, dtype=torch.uint8)
     _check("ssd_chunk_scan", lib.ssd_chunk_scan(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(B), _ptr(C),
@@ -381,6 +383,7 @@ def ssd_fwd_varlen(x, dt, A, B, C, D=None, init_states=None, cu_seqlens=None, ch
     _need(final_states, "final_states", torch.float32, (nseq, H, P, N))
     cu_arr = (ctypes.c_int64 * len(cu))(*cu)
     ws_bytes = int(lib.ssd_fwd_varlen_workspace_size(ctypes.byref(shape), cu_arr, nseq))
+    _need(workspace, "workspace")
     if workspace is None or workspace.numel() < ws_bytes:
         workspace = torch.empty(max(ws_bytes, 16), device=x.device, dtype=torch.uint8)
     _check("ssd_fwd_varlen", lib.ssd_fwd_varlen(ctypes.byref(shape), cu_arr, nseq, _ptr(x), _ptr(dt), _ptr(A),

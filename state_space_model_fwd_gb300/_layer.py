@@ -188,8 +188,14 @@ def _empty(shape, dtype, x):
 
 
 def _workspace(workspace, need, x):
-    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
-        return workspace
+    """The given workspace where it is large enough, else a new one."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != x.get_device():
+            raise TypeError(f"workspace must be a CUDA tensor on {x.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
     return _empty((max(need, 16),), torch.uint8, x)
 
 

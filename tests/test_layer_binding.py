@@ -103,3 +103,51 @@ def test_operands_on_another_than_the_current_device_are_refused(entry, monkeypa
     monkeypatch.setattr(_layer, "_current_device", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
         ENTRIES[entry]()
+
+
+# ---- workspaces ------------------------------------------------------------
+def test_a_given_workspace_is_checked():
+    x = torch.zeros(1)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    assert _layer._workspace(ws, 64, x) is ws
+    assert _layer._workspace(torch.zeros(16), 64, x).dtype == torch.float32  # any type: its bytes count
+    assert _layer._workspace(ws, 65, x).numel() == 65                        # too small: a new one
+    with pytest.raises(ValueError, match="contiguous"):
+        _layer._workspace(torch.zeros(128, dtype=torch.uint8)[::2], 64, x)
+    with pytest.raises(TypeError, match="workspace"):
+        _layer._workspace(ws, 64, on_cuda1(1))
+    with pytest.raises(TypeError, match="workspace"):
+        _layer._workspace(on_cuda1(64), 64, x)
+    with pytest.raises(TypeError, match="workspace"):
+        _layer._workspace(1 << 20, 64, x)
+
+
+class OnCuda0(OnCuda1):
+    device = property(lambda self: torch.device("cuda", 0))
+
+    def get_device(self):
+        return 0
+
+
+@pytest.mark.parametrize("ws,error", [(torch.zeros(1 << 20, dtype=torch.uint8), TypeError),
+                                      (torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(OnCuda0)[::2], ValueError)],
+                         ids=["host", "strided"])
+def test_the_scans_workspace_is_checked(ws, error, monkeypatch):
+    monkeypatch.setattr(_layer, "_current_device", lambda: 0)
+    monkeypatch.setattr(ssd, "load_library", NoLaunch)
+    z = lambda *shape: torch.zeros(*shape).as_subclass(OnCuda0)
+    x, dt, A, B, y = z(1, 64, 2, 16), z(1, 64, 2), z(2), z(1, 64, 1, 16), z(1, 64, 2, 16)
+    with pytest.raises(error, match="workspace"):
+        ssd.ssd_fwd(x, dt, A, B, B, y=y, return_final_state=False, workspace=ws)
+    with pytest.raises(error, match="workspace"):
+        ssd.ssd_fwd_varlen(x, dt, A, B, B, cu_seqlens=[0, 64], y=y, return_final_states=False, workspace=ws)
+    with pytest.raises(error, match="workspace"):
+        ssd.ssd_chunk_scan(x, dt, B, B, z(1, 2, 1, 64), z(1, 1, 2, 16, 16), out=y, workspace=ws)
+
+
+class NoLaunch:
+    """Stands for the library: sizes, and no call that would launch."""
+    def __getattr__(self, name):
+        if name.endswith("_workspace_size"):
+            return lambda *args: 1024
+        raise AssertionError(f"{name} reached")
