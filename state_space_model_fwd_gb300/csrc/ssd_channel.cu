@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) channel_fwd_kernel(const __gri
     const float D = FULL && a.D ? a.D[own] : 0.f;
 
     // this warp's tokens
-    const int t0 = c_in * a.chunk, t1 = whole ? a.seqs.L : min(a.seqs.L, t0 + a.chunk);
+    // (the last chunk's end is formed from what is left: t0 + a.chunk may pass 2^31)
+    const int t0 = c_in * a.chunk, t1 = whole || a.seqs.L - t0 <= a.chunk ? a.seqs.L : t0 + a.chunk;
     int s = row, S0 = 0, S1 = a.seqs.L, t = t0;
     if (packed) {
         s = seq_of(start, a.seqs.n, FULL ? t0 : t1 - 1);

@@ -36,3 +36,28 @@ def test_broadcast_rows_of_the_norm(name, dtype, dim):
     wide = rnd(dim).to(dtype).expand(b, L, dim)
     for u, v in zip(norm_calls(dict(t, **{name: wide})), norm_calls(dict(t, **{name: wide.contiguous()}))):
         assert torch.equal(u, v)
+
+
+# ---- the longest sequence --------------------------------------------------
+def test_channel_scan_over_the_longest_sequence():
+    """2^31 - 4096 tokens of one channel: the last of 1216 chunks ends less than
+    a chunk before 2^31.  One token repeated by stride 0, so the state tends to
+    h = delta x B / (1 - exp(delta A)) and stays there."""
+    L, N = (1 << 31) - 4096, 8
+    x, dt = torch.full((1, 1, 1), 0.75, device="cuda").bfloat16(), torch.zeros(1, 1, 1, device="cuda").bfloat16()
+    B, C = (torch.randn(1, 1, 1, N, device="cuda").bfloat16() for _ in range(2))
+    A, D = -torch.arange(1.0, N + 1, device="cuda")[None], torch.ones(1, device="cuda")
+    y = torch.full((1, L, 1), float("nan"), device="cuda", dtype=torch.bfloat16)
+    wide = lambda t: t.expand(1, L, *t.shape[2:])
+    _, fin = ssd.ssd_channel_scan_fwd(wide(x), wide(dt), A, wide(B), wide(C), D, y=y)
+    delta = torch.log(torch.tensor(2.0, dtype=torch.float64))
+    h = delta * 0.75 * B.double().cpu().flatten() / (1 - torch.exp(delta * A.double().cpu().flatten()))
+    # a state is at rest within one rounding a step of terms its own size, divided by 1 - exp(delta A) >= 1/2, and the
+    # exponential's 2^-22: 1e-6; 256 tokens leave exp(-delta 256) = 2^-256 of the start
+    assert float((fin.double().cpu().flatten() - h).abs().max()) <= 1e-6 * float(h.abs().max())
+    want = float((h * C.double().cpu().flatten()).sum() + 0.75)
+    size = float((h * C.double().cpu().flatten()).abs().sum() + 0.75)
+    tail = y[0, 256:, 0]
+    lo, hi = float(tail.min()), float(tail.max())  # (a token that was not written is NaN, and so are these)
+    bound = 2.0 ** -8 * abs(want) + 2e-6 * size
+    assert abs(lo - want) <= bound and abs(hi - want) <= bound, (lo, hi, want)
