@@ -33,7 +33,7 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
+    return [f for kind in ("*.cu", "*.cuh", "*.h") for f in sorted(glob.glob(os.path.join(CSRC, kind)))] + [
         os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]
 
 

@@ -1,5 +1,8 @@
 """Host side of the operators around the scan: what the binding makes of
 strides, devices, workspaces and arguments.  No call here reaches a kernel."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -151,3 +154,30 @@ class NoLaunch:
         if name.endswith("_workspace_size"):
             return lambda *args: 1024
         raise AssertionError(f"{name} reached")
+
+
+# ---- the library is rebuilt after any change of what it is made from ---------
+def test_every_included_file_is_an_input_of_the_build():
+    inputs = {os.path.realpath(f) for f in _build._inputs()}
+    seen, todo = set(), [f for f in inputs if f.endswith(".cu")]
+    assert todo
+    while todo:
+        path = todo.pop()
+        if path in seen:
+            continue
+        seen.add(path)
+        for name in re.findall(r'^\s*#\s*include\s+"([^"]+)"', open(path, encoding="utf-8").read(), re.M):
+            found = [os.path.realpath(os.path.join(d, name)) for d in (_build.CSRC, _build.INCLUDE)
+                     if os.path.exists(os.path.join(d, name))]
+            assert found, (path, name)
+            todo.append(found[0])
+    assert seen <= inputs, seen - inputs
+
+
+def test_a_newer_header_makes_the_library_stale(monkeypatch):
+    assert _build.up_to_date()
+    newest = os.path.getmtime(_build.LIB) + 10
+    true = os.path.getmtime
+    header = os.path.join(_build.CSRC, "ssd_channel.h")
+    monkeypatch.setattr(os.path, "getmtime", lambda f: newest if os.path.realpath(f) == header else true(f))
+    assert not _build.up_to_date()
