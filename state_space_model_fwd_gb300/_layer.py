@@ -493,7 +493,7 @@ def _norm_shape(x, group_size, eps, residual, gate_after):
         raise ValueError("x must be [..., dim]")
     dim = x.shape[-1]
     rcode = code if residual is None else _code(residual, "residual")[0]
-    return _norm_shape_t(x.numel() // dim if dim else 0, dim, group_size or dim, eps, code, rcode,
+    return _norm_shape_t(x.numel() // dim if dim else 0, dim, dim if group_size is None else group_size, eps, code, rcode,
                          1 if gate_after else 0), dev
 
 

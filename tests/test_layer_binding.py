@@ -181,3 +181,19 @@ def test_a_newer_header_makes_the_library_stale(monkeypatch):
     header = os.path.join(_build.CSRC, "ssd_channel.h")
     monkeypatch.setattr(os.path, "getmtime", lambda f: newest if os.path.realpath(f) == header else true(f))
     assert not _build.up_to_date()
+
+
+# ---- groups of the block norm ----------------------------------------------
+@pytest.mark.parametrize("group", [0, -64, 48])
+def test_a_group_size_that_does_not_divide_the_columns_is_refused(group, monkeypatch):
+    x = torch.zeros(4, 64).as_subclass(OnCuda0)
+    monkeypatch.setattr(_layer, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+    with pytest.raises(ssd.SSDError, match="INVALID"):
+        ssd.ssd_block_norm_fwd(x, torch.ones(64).as_subclass(OnCuda0), out=x, group_size=group)
+
+
+def test_without_a_group_size_all_columns_are_one_group(monkeypatch):
+    monkeypatch.setattr(_layer, "_current_device", lambda: 0)
+    shape, _ = _layer._norm_shape(torch.zeros(4, 64).as_subclass(OnCuda0), None, 1e-5, None, False)
+    assert shape.group_size == 64
