@@ -463,7 +463,8 @@ SSD_API ssd_status_t ssd_channel_scan_step(const ssd_channel_shape_t *shape, con
  * ssd_block_norm_bwd: dout, and dresidual_out (NULL: zero) for the sum's own
  * use elsewhere -> dx, dz, dresidual, dweight, dscale.  With a residual it
  * takes the stored sum, residual_out, in the residual's place; x is then read
- * only for the gate before and the scale.  dweight, dscale may be NULL.
+ * only for the gate before and the scale.  dweight, dscale may be NULL; dz,
+ * dresidual and dscale are given only with z, residual_out and scale.
  */
 typedef struct {
     int64_t rows, dim, group_size;

@@ -536,6 +536,8 @@ ssd_status_t ssd_block_norm_bwd(const ssd_norm_shape_t *shape, const ssd_rows_t 
         !aligned(dscale, 4))
         return SSD_ERR_INVALID_ARG;
     if ((z && !dz) || (residual_out && !dresidual) || (dresidual_out && !residual_out)) return SSD_ERR_INVALID_ARG;
+    // a gradient of what is absent would be left unwritten
+    if ((dz && !z) || (dresidual && !residual_out) || (dscale && !scale)) return SSD_ERR_INVALID_ARG;
     if (rows > 0) {
         if (!row_ok(*dout, es) || !row_ok(*x, es) || !rows_out_ok(*dx, es, 1, rows, dim)) return SSD_ERR_INVALID_ARG;
         if (z && (!row_ok(*z, es) || !rows_out_ok(*dz, es, 1, rows, dim))) return SSD_ERR_INVALID_ARG;

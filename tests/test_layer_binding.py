@@ -1,5 +1,6 @@
 """Host side of the operators around the scan: what the binding makes of
 strides, devices, workspaces and arguments.  No call here reaches a kernel."""
+import ctypes
 import os
 import re
 
@@ -197,3 +198,23 @@ def test_without_a_group_size_all_columns_are_one_group(monkeypatch):
     monkeypatch.setattr(_layer, "_current_device", lambda: 0)
     shape, _ = _layer._norm_shape(torch.zeros(4, 64).as_subclass(OnCuda0), None, 1e-5, None, False)
     assert shape.group_size == 64
+
+
+# ---- gradients of absent operands ------------------------------------------
+FAKE = 1 << 20  # never read
+
+
+@pytest.mark.parametrize("given", ["dz", "dresidual", "dscale"])
+def test_the_norms_gradient_of_an_absent_operand_is_refused(lib, given):
+    """Workspace too small on purpose: what passes the checks ends there."""
+    shape, r = _layer._norm_shape_t(4, 64, 64, 1e-5, 1, 1, 0), _layer._rows_t(FAKE, 0, 64)
+    ref = ctypes.byref(r)
+    call = lambda **kw: lib.ssd_block_norm_bwd(
+        ctypes.byref(shape), ref, ref, FAKE, kw.get("z"), kw.get("scale"), kw.get("residual_out"), None, ref, FAKE,
+        kw.get("dz"), kw.get("dresidual"), kw.get("dscale"), None, 0, None)
+    operand = {"dz": "z", "dresidual": "residual_out", "dscale": "scale"}[given]
+    value = FAKE if given == "dscale" else ref
+    INVALID, WORKSPACE = 1, 4
+    assert call() == WORKSPACE
+    assert call(**{operand: value, given: value}) == WORKSPACE
+    assert call(**{given: value}) == INVALID
