@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import state_space_model_fwd_gb300 as ssd
+from tests import layer_reference as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +37,32 @@ def test_broadcast_rows_of_the_norm(name, dtype, dim):
     wide = rnd(dim).to(dtype).expand(b, L, dim)
     for u, v in zip(norm_calls(dict(t, **{name: wide})), norm_calls(dict(t, **{name: wide.contiguous()}))):
         assert torch.equal(u, v)
+
+
+# ---- non-finite values at the end of a sequence ----------------------------
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("C", [24, 21])
+@pytest.mark.parametrize("cu", [None, [0, 5, 6, 50, 50, 83]], ids=["equal", "packed"])
+def test_conv_gradient_where_the_last_token_is_not_finite(value, dtype, C, cu):
+    """Without SiLU dp is dy: a value in a sequence's last row reaches dweight's
+    last tap alone, and one in its last but one row the last two."""
+    b, L, W = (2, 83, 4) if cu is None else (1, 83, 4)
+    g = torch.Generator().manual_seed(C)
+    n = lambda *s: torch.randn(*s, generator=g)
+    x, dy = n(b, L, C), n(b, L, C)
+    x[0, 82, 3] = value
+    x[0, 81, 5] = value
+    if cu:
+        x[0, 5, 7], x[0, 49, 9] = value, value
+    x, dy = x.to(dtype).cuda(), dy.to(dtype).cuda()
+    weight = n(C, W).cuda()
+    got = ssd.ssd_conv_bwd(dy, x, weight, silu=False, cu_seqlens=cu)
+    leaves = [ref.d(x).requires_grad_(True), ref.d(weight).requires_grad_(True)]
+    want = ref.gradients(ref.conv(*leaves, None, None, cu, False), [ref.d(dy), None], leaves)
+    assert not bool(torch.isfinite(want[1]).all()) and bool(torch.isfinite(want[1][[3, 5], :2]).all())
+    ref.check(got[0], want[0], "dx", rel=1e-5)
+    ref.check(got[1], want[1], "dweight", rel=1e-5, scale=float(b * L) ** 0.5 * 3)
 
 
 # ---- the longest sequence --------------------------------------------------
