@@ -37,6 +37,13 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// p ? fma2(a, b, c) : c, as a predicated instruction rather than two selects
+__device__ __forceinline__ f2 fma2_if(bool p, f2 a, f2 b, f2 c) {
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p fma.rn.f32x2 %0, %1, %2, %0;\n\t}"
+        : "+l"(c)
+        : "l"(a), "l"(b), "r"((unsigned)p));
+    return c;
+}
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     f2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));

@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
             }
             // backward
             for (int sb = ns - 1; sb >= 0; --sb) {
+                const int left = e - begin - sb * TB;  // tokens of these TB that are the piece's
                 // this channel's values, in flight until the outputs
                 T rx[TB], rg[TB], rz[TB], rd[TB];
 #pragma unroll
@@ -535,7 +536,8 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                             r[i][m] = mul2(decay[jj][i][m], dh);
                             const f2 w = mul2(r[i][m], before[jj][i][m]);
                             dd_A = fma2(w, A2[i][m], dd_A);
-                            dA[i][m] = fma2(w, dd, dA[i][m]);
+                            // (past the piece w may be 0 times an infinity)
+                            dA[i][m] = jj == 0 ? fma2(w, dd, dA[i][m]) : fma2_if(jj < left, w, dd, dA[i][m]);
                         }
                         sums[i][0] = sum2(du);
                         sums[i][1] = sum2(dd_A);
@@ -554,7 +556,6 @@ __global__ void __launch_bounds__(kWarps * 32) channel_bwd_kernel(const __grid_c
                 }
                 // (outputs only here: a branch inside the loop would keep its tokens from overlapping)
                 __syncwarp();
-                const int left = e - begin - sb * TB;  // tokens of these TB that are the piece's
 #pragma unroll
                 for (int jj = 0; jj < TB; ++jj) {
                     if (jj < left) {

@@ -65,6 +65,33 @@ def test_conv_gradient_where_the_last_token_is_not_finite(value, dtype, C, cu):
     ref.check(got[1], want[1], "dweight", rel=1e-5, scale=float(b * L) ** 0.5 * 3)
 
 
+SCAN = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init")
+
+
+@pytest.mark.parametrize("name", ["x", "B"])
+@pytest.mark.parametrize("N", [8, 16, 32])
+@pytest.mark.parametrize("cu", [None, [0, 30, 31, 31, 61]], ids=["equal", "packed"])
+def test_scan_gradient_where_the_last_token_is_not_finite(name, N, cu):
+    """The last token's x or B reaches the last state, and no earlier one: dA,
+    which takes the state before each token, stays finite."""
+    b, L, ch = (2, 61, 40) if cu is None else (1, 61, 40)
+    g = torch.Generator().manual_seed(N)
+    n = lambda *s: torch.randn(*s, generator=g)
+    nst = b if cu is None else len(cu) - 1
+    t = dict(x=n(b, L, ch), dt=0.5 * n(b, L, ch), A=-torch.arange(1, N + 1.0) * torch.exp(0.2 * n(ch, N)), B=n(b, L, 1, N),
+             C=n(b, L, 1, N), D=n(ch), z=n(b, L, ch), dt_bias=n(ch) - 3, init=n(nst, ch, N))
+    dy, dfin = n(b, L, ch), n(nst, ch, N)
+    bad = float("nan") if name == "x" else float("inf")
+    for k in [L - 1] if cu is None else [29, L - 1]:
+        t[name][0, k].view(-1)[3] = bad
+    leaves = [t[k].double().requires_grad_(True) for k in SCAN]
+    want = ref.gradients(ref.scan(*leaves, cu), [dy.double(), dfin.double()], leaves)
+    assert bool(torch.isfinite(want[2]).all())
+    got = ssd.ssd_channel_scan_bwd(dy.cuda(), *[t[k].cuda() for k in SCAN], cu_seqlens=cu, dfinal_state=dfin.cuda())
+    for k, a, w in zip(SCAN, got, want):
+        ref.check(a, w, "d" + k, rel=3e-5)
+
+
 # ---- the longest sequence --------------------------------------------------
 def test_channel_scan_over_the_longest_sequence():
     """2^31 - 4096 tokens of one channel: the last of 1216 chunks ends less than
