@@ -311,13 +311,17 @@ __global__ void __launch_bounds__(kLanes *kSub, 2) conv_bwd_kernel(const __grid_
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         if constexpr (!decltype(inside)::value) g[v] = in_seq ? g[v] : 0.f;
-                        // a token past the tile only completes rows (and must not bring in 0 times an infinity)
-                        if (decltype(inside)::value || mine) {
+                        float own = g[v], last = c[v];
+                        if constexpr (!decltype(inside)::value) {
+                            // a token past the tile only completes rows, and must not bring in 0 times an infinity
+                            own = mine ? own : 0.f, last = mine ? last : 0.f;
 #pragma unroll
-                            for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(g[v], old[k][v], dw[k][v]);
-                            dw[W - 1][v] = fmaf(g[v], c[v], dw[W - 1][v]);
-                            db[v] += g[v];
+                            for (int k = 0; k < W - 1; ++k) old[k][v] = mine ? old[k][v] : 0.f;
                         }
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(own, old[k][v], dw[k][v]);
+                        dw[W - 1][v] = fmaf(own, last, dw[W - 1][v]);
+                        db[v] += own;
                         // dpw holds the last W-1 dp
                         float r = w[0][v] * g[v];
 #pragma unroll
