@@ -86,7 +86,7 @@ __device__ __forceinline__ void for_pieces(int64_t tile, int tile_len, int L, co
     }
 }
 
-template <typename T, int V>
+template <typename T>
 __device__ __forceinline__ Rows<T> part_of(const ConvArgs<T> &a, int c0) {
     Rows<T> r = a.y[0];
     int begin = 0;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kLanes *kSub, 3) conv_fwd_kernel(const __grid_
     load_weights<T, W, V>(a, c0, w, bias);
     Rows<const T> x = a.x;
     x.p += c0;
-    const Rows<T> y = part_of<T, V>(a, c0);
+    const Rows<T> y = part_of<T>(a, c0);
     for_pieces<PACKED>(tile, a.tile, a.L, set, [&](const Piece &p, int row) {
         Vec<T, V> nxt[kAhead];
 #pragma unroll
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kLanes *kSub, 2) conv_bwd_kernel(const __grid_
         load_weights<T, W, V>(a, c0, w, bias);
         Rows<const T> x = a.x;
         x.p += c0;
-        const Rows<T> dy = part_of<T, V>(a, c0);
+        const Rows<T> dy = part_of<T>(a, c0);
         Rows<T> dx = a.dx;
         dx.p += c0;
         for (int64_t tile = (int64_t)slot * kSub + threadIdx.y; tile < a.ntiles; tile += (int64_t)slots * kSub) {
@@ -461,10 +461,6 @@ ssd_status_t check(const ssd_conv_shape_t *s, const int64_t *cu, int64_t nseq) {
     }
     return SSD_OK;
 }
-
-struct Plan {
-    int V, nvec, ncb, tile;
-};
 
 // Tokens per tile: the longest of 128, 64, .. 8 that still makes 16 warps an SM
 // (a tile reads W-1 rows beyond its own).
