@@ -341,10 +341,11 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_shape_t *shape, const void *x, co
  *
  * Rows.  Token-major operands are given as ssd_rows_t: element (b, t, c) is
  * data[b * batch_stride + t * row_stride + c], strides in elements (row
- * strides below 2^31), c contiguous.  So a column slice of a wider projection is read (or a slice
- * of its gradient written) in place.  `data` needs only its element type's
- * alignment; 16-byte aligned rows (pointer and strides) take the vector
- * path.  Rows that are written must not overlap each other or any operand.
+ * strides below 2^31), c contiguous.  So a column slice of a wider projection
+ * is read (or a slice of its gradient written) in place, and a stride of 0
+ * reads one row for all.  `data` needs only its element type's alignment;
+ * 16-byte aligned rows (pointer and strides) take the vector path.  Rows that
+ * are written must not overlap each other or any operand.
  * Batches.  cu_seqlens NULL: `batch` sequences of `seqlen` tokens (nseq is
  * ignored, and is `batch` below).  Otherwise batch is 1 and the `nseq`
  * sequences lie back to back along seqlen: cu_seqlens is a HOST array of
@@ -353,8 +354,9 @@ SSD_API ssd_status_t ssd_decode_step(const ssd_shape_t *shape, const void *x, co
  * boundary, not even a non-finite value.  An empty sequence hands its
  * initial state on as its final state, and the other way for gradients.
  * State and parameter arrays are contiguous and need their element type's
- * alignment; a final state must not be the initial state's array.  Everything else (streams, ownership, errors, reproducibility)
- * is as for the other entry points; dtype is fp32 or bf16.
+ * alignment, the channel scan's A and states 16 bytes; a final state must not
+ * be the initial state's array.  Everything else (streams, ownership, errors,
+ * reproducibility) is as for the other entry points; dtype is fp32 or bf16.
  * ------------------------------------------------------------------------ */
 typedef struct {
     void *data;
@@ -408,8 +410,7 @@ SSD_API ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, const ssd_rows
  * x, dt, z, y [b, L, Ch] T; B, C rows of [b, L, G, N] T (G N contiguous;
  * channels g Ch/G .. share group g); A [Ch, N], D, dt_bias [Ch] fp32; states
  * [nseq, Ch, N] fp32.  z (data NULL), D, dt_bias, init_state, final_state may
- * be absent.  A must be finite.  N 8, 16 or 32; A and the state arrays are
- * 16-byte aligned.  States, sums and gradients are held in fp32; y is rounded
+ * be absent.  A must be finite.  N 8, 16 or 32.  States, sums and gradients are held in fp32; y is rounded
  * once.  The workspace (size 0 where none is needed) holds chunk states and
  * the packed offsets, and needs no initialisation.
  * ssd_channel_scan_bwd: dy and dfinal_state (NULL: zero) -> the gradients of
@@ -456,10 +457,11 @@ SSD_API ssd_status_t ssd_channel_scan_step(const ssd_channel_shape_t *shape, con
  *   v = z && !gate_after ? x silu(z) : x
  *   s = residual + scale v      (scale NULL: 1; residual NULL: 0)
  *   out = s / sqrt(mean_group(s^2) + eps) * weight  (times silu(z) with gate_after)
- * and residual_out = s (which may be the residual itself).  x, z, out [rows, dim] T; residual, residual_out in
- * residual_dtype (fp32, or T); weight, scale [dim] fp32.  Rows use row_stride
- * (batch_stride is ignored).  The norm is of s before it is rounded to
- * residual_dtype.  Supported: group_size up to 32768.
+ * and residual_out = s (which may be the residual itself).  x, z, out
+ * [rows, dim] T; residual, residual_out in residual_dtype (fp32, or T);
+ * weight, scale [dim] fp32.  Rows use row_stride (batch_stride is ignored).
+ * The norm is of s before it is rounded to residual_dtype.  Supported:
+ * group_size up to 32768.
  * ssd_block_norm_bwd: dout, and dresidual_out (NULL: zero) for the sum's own
  * use elsewhere -> dx, dz, dresidual, dweight, dscale.  With a residual it
  * takes the stored sum, residual_out, in the residual's place; x is then read

@@ -7,14 +7,19 @@
 // state from a zero start (or from the sequence's own start) and the sum of its
 // deltas; the second starts a chunk from the combination of the earlier ones,
 // where a chunk's decay is exp(A sum delta), and writes y.  That costs up to
-// 1.6 times the arithmetic on SMs that would otherwise idle.  Chunks are cut
-// without regard to sequences, which restart the state inside a chunk.
+// 1.6 times the arithmetic on SMs that would otherwise idle, and on top one
+// step a chunk for every earlier chunk of its sequence: few beside its tokens,
+// except where one or two block rows are cut into a thousand chunks (1 x 100000
+// x 32, 1137 chunks of 88 tokens: 17 us for the first launch, 152 for the
+// second).  Chunks are cut without regard to sequences, which restart the state
+// inside a chunk.
 //
 // Bound by instruction issue and what two warps a scheduler leave uncovered of
-// the instructions' latencies: 109 instructions a token and warp (16 states), 32
-// of them packed multiply-adds that take two issue cycles, 16 exponentials; 804
-// us at 8 x 4096 x 5120 bf16 with gate, three quarters of the issue cycles.  The
-// bytes would take 199 us, the fp32 results alone (4 a state) 290 us.
+// the instructions' latencies: 108 instructions a token and warp (16 states), 32
+// of them packed multiply-adds that take two issue cycles, 16 exponentials; 805
+// us at 8 x 4096 x 5120 bf16 with gate, an instruction in 58 % of the main
+// launch's cycles, 75 % with the packed ones' second cycle.  The bytes would
+// take 199 us, the fp32 results alone (4 a state) 290 us.
 #include <type_traits>
 
 #include "ssd_channel.h"
@@ -399,8 +404,8 @@ FwdPlan plan_fwd(const ssd_channel_shape_t *s, const int64_t *cu, int64_t nseq) 
     p.whole = cu || base < 2 * kSched ? 0 : base / kSched * kSched;
     p.cut = base - p.whole;
     // A tail of more than 7/8 of a warp for every scheduler, or behind eight of them, is not worth cutting
-    // (11 x 2048 x 5120, 2.9 warps each: 633 us whole, 685 cut; 60 x 512 x 5120, 15.8: 756 and 788; on the
-    // other side 8 x 4096 x 5120, 2.1: 1180 and 804).
+    // (11 x 2048 x 5120, 2.9 warps each: 626 us whole, 645 cut; 60 x 512 x 5120, 15.8: 748 and 776; on the
+    // other side 8 x 4096 x 5120, 2.1: 1237 and 805).
     if (p.whole && (p.cut * 8 > kSched * 7 || base >= 8 * kSched)) p.whole = base, p.cut = 0;
     int64_t want = p.cut ? 2 * kSched / p.cut : 1;  // two for every scheduler, at most
     if (want > (L + 63) / 64) want = (L + 63) / 64;

@@ -19,9 +19,9 @@
 //     chunks a block walks;
 //   4 the sums over channel blocks and over blocks, in a fixed order.
 // Bound by instruction issue.  At 4 x 2048 x 1536, 16 states, bf16 with gate
-// the launches take 95, 15, 270 and 5 us: 162 and 449 instructions a token and
-// warp in 1 and 3, 48 and 125 of them packed multiply-adds of two issue cycles
-// each.  3 runs eight warps an SM (254 registers: the states and decays of four
+// a call takes 393 us, the launches each by itself with cold caches 93, 19, 280
+// and 9: 162 and 459 instructions a token and warp in 1 and 3, 48 and 125 of
+// them packed multiply-adds of two issue cycles each.  3 runs eight warps an SM (254 registers: the states and decays of four
 // tokens are 128 of them) at 55 % issue; what its loads cost it was hidden by
 // taking a chunk's values half a chunk at a time, all in flight (618 -> 272 us
 // with a grid of one wave).
@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kWarps * 32, N == 32 ? 2 : 3) channel_bwd_chun
 // ---------------------------------------------------------------------------
 // 2: the recurrences over chunks.  A block owns one float4 a lane of a channel
 // block's states over all chunks of a sequence row; blockIdx.y picks the
-// direction.  One warp walks them all where there are enough blocks (it is
-// then bound by memory: 29 MB each way in 20 us at 4 x 2048 x 1536).  With few
-// blocks the latency of the loads bounds it, and RUNS warps take a run of
+// direction.  One warp walks them all where there are enough blocks (at 4 x
+// 2048 x 1536 60 MB of both directions read in 19 us, what is written stays in
+// L2).  The latency of the loads bounds it, and with few blocks RUNS warps take a run of
 // chunks each: every warp combines its run from zero, then starts it again
 // from the runs before (257 chunks of 640 channels: 37 -> 25 us).
 // ---------------------------------------------------------------------------

@@ -9,11 +9,13 @@
 // in registers, so each row is read once (and W-1 rows more per tile); a warp
 // reads 256 (bf16) or 512 consecutive bytes of a row, and the next four rows
 // are in flight while four are computed.  (Eight channels a thread halve the
-// address arithmetic but leave 16 warps an SM instead of 24: 292 against 261
-// us.)  Channels are independent, so y is written straight into the x, B and C
+// address arithmetic but leave 16 warps an SM instead of 24: 259 against 244
+// us at 65536 x 5376.)  Channels are independent, so y is written straight into the x, B and C
 // arrays a scan takes, out of the projection's rows in place.
 // bf16, W 4: 65537 packed tokens x 5376 channels in 246 us, 5.7 TB/s; the
-// gradient at 4 x 4095 x 2560 in 55 us and 4 for the sums, 4.2 TB/s.
+// gradient at 4 x 4095 x 2560 in 59 us with the sums, 4.2 TB/s.  fp32 spills
+// registers: 8 x 2048 x 5120 in 126 us, 5.3 TB/s; the gradient at 4 x 4095 x
+// 2560 in 138 us, 3.6 TB/s.
 //
 // Tokens are cut into tiles without regard to sequences: a tile walks its
 // pieces of sequences one after another and rebuilds the window (from the

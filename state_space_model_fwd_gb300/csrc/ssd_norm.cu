@@ -10,9 +10,12 @@
 // groups, several to a block, and otherwise a block of just enough threads
 // for NV vectors each, so that few threads idle whatever the width.  The gate
 // is fixed at compile time for widths up to 8192 (read at run time inside the
-// loops it cost the gradient 117 us instead of 73).
+// loops: 91 us instead of 71 for the gradient at 4096 x 5120 gated, 89 instead
+// of 82 forward at 16384 x 5120).
 // bf16: 16384 x 5120 gated in 81 us, 6.2 TB/s; the gradient with an fp32
-// residual and scale at 8191 x 2560 in 70 us and 4 for the sums, 5.1 TB/s.
+// residual and scale at 8191 x 2560 in 75 us with the sums, 5.1 TB/s.  Gated
+// gradients, fp32 and groups over 8192 columns spill registers: 8191 x 2560
+// gated in 62 us against 31 for its bytes, 2048 x 16384 in 296 against 30.
 #include <type_traits>
 
 #include "ssd_layer.cuh"
@@ -218,7 +221,8 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : GATE == kAnyGate ? 10
                 if (a.dres.p) dres[i].load(a.dres.at(row, c));
             }
         }
-        if (r64 + slots < a.rows) {  // the next row on its way to L2 meanwhile (4096 x 5120: 89 -> 70 us, narrow rows alike)
+        // the next row on its way to L2 meanwhile (4096 x 5120 gated: 71 us, 85 without; 512 columns: 32 and 33)
+        if (r64 + slots < a.rows) {
             const int next = row + slots;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -388,7 +392,10 @@ ssd_status_t check(const ssd_norm_shape_t *s) {
 }
 
 // Teams that share the rows of a group of columns in the gradient: one wave
-// of the 12 (warp teams) or 15 warps that fit an SM beside each other.
+// of 12 warps an SM (warp teams) or of the blocks whose warps are 15 at most,
+// of the 16 that the registers allow (21 M elements, bf16 with an fp32 residual
+// and scale, as rows of 1024, 2048, 4096 and 5120: 77, 73, 75 and 75 us, although
+// one block of 8 warps stands on an SM at 4096).
 int64_t bwd_slots(const ssd_norm_shape_t *s) {
     const int64_t ngroups = s->dim / s->group_size, warps = (s->group_size + 511) / 512;
     const int64_t per_sm = warps == 1 ? 12 : warps < 15 ? 15 / warps : 1;
