@@ -452,6 +452,57 @@ SSD_API ssd_status_t ssd_channel_scan_step(const ssd_channel_shape_t *shape, con
                                            float *state, const ssd_rows_t *y, cudaStream_t stream);
 
 /*
+ * Gated scan: a linear recurrence with one state a channel, whose decay and
+ * input are gated by the token (s(v) = 1 / (1 + exp(-v))):
+ *   a[t, c] = exp(-rate softplus(decay[c]) s(r[t, c]))
+ *   h[c] <- a h[c] + sqrt(1 - a^2) s(i[t, c]) x[t, c]
+ *   y[t, c] = h[c] silu(z[t, c])
+ * x, r, i, z, y [b, L, Ch] T; decay [Ch] fp32; states [nseq, Ch] fp32.  i
+ * (data NULL: s(i) = 1), z (y = h), init_state, final_state may be absent;
+ * rate > 0.  States, decays and sums are held in fp32; y is rounded once.
+ * chunk_states (NULL: not wanted), [b, ssd_gated_scan_chunk_states(), Ch]
+ * fp32, takes the state that enters every 64th token, for the gradient.  A
+ * block that waits for an earlier block's state gives up after 100 ms, which
+ * ssd_get_device_status reports.
+ * ssd_gated_scan_bwd: dy and dfinal_state (NULL: zero) -> the gradients of
+ * every input given: rows dx, dr, di, dz in T, ddecay, dinit_state in fp32
+ * (either NULL: not written; di and dz ignored without i and z).
+ * chunk_states: what the forward call wrote; NULL: formed again, in the
+ * workspace.
+ * ssd_gated_scan_step: one token per sequence; rows are [b, Ch] (row_stride
+ * ignored), state [b, Ch] advanced in place, init_state ignored.
+ */
+typedef struct {
+    int64_t batch, seqlen, channels;
+    float rate;
+    ssd_dtype_t dtype;
+} ssd_gated_shape_t;
+
+typedef struct {
+    ssd_rows_t x, r, i, z;
+    const float *decay, *init_state;
+} ssd_gated_inputs_t;
+
+typedef struct {
+    ssd_rows_t dx, dr, di, dz;
+    float *ddecay, *dinit_state;
+} ssd_gated_grads_t;
+
+SSD_API int64_t ssd_gated_scan_chunk_states(const ssd_gated_shape_t *shape);
+SSD_API size_t ssd_gated_scan_workspace_size(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq);
+SSD_API ssd_status_t ssd_gated_scan_fwd(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                        const ssd_gated_inputs_t *in, const ssd_rows_t *y, float *final_state,
+                                        float *chunk_states, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+SSD_API size_t ssd_gated_scan_bwd_workspace_size(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                                 int with_chunk_states);
+SSD_API ssd_status_t ssd_gated_scan_bwd(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                        const ssd_rows_t *dy, const ssd_gated_inputs_t *in, const float *dfinal_state,
+                                        const float *chunk_states, const ssd_gated_grads_t *out, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream);
+SSD_API ssd_status_t ssd_gated_scan_step(const ssd_gated_shape_t *shape, const ssd_gated_inputs_t *in, float *state,
+                                         const ssd_rows_t *y, cudaStream_t stream);
+
+/*
  * Block norm: the RMS norm before or after a block, fused with its gate and
  * the scaled residual.  Per row of `dim` columns, in groups of group_size:
  *   v = z && !gate_after ? x silu(z) : x

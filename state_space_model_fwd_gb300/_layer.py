@@ -1,5 +1,5 @@
 """Binding of the operators around the scan: the short causal convolution, the
-channel scan and the block norm.
+channel scan, the gated scan and the block norm.
 
 Token-major operands (x, y, gradients) may be strided views whose last
 dimension is contiguous, such as column slices of a projection's rows; states
@@ -50,6 +50,21 @@ class _channel_grads_t(ctypes.Structure):
                 ("dinit_state", ctypes.c_void_p)]
 
 
+class _gated_shape_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("rate", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class _gated_inputs_t(ctypes.Structure):
+    _fields_ = [("x", _rows_t), ("r", _rows_t), ("i", _rows_t), ("z", _rows_t), ("decay", ctypes.c_void_p),
+                ("init_state", ctypes.c_void_p)]
+
+
+class _gated_grads_t(ctypes.Structure):
+    _fields_ = [("dx", _rows_t), ("dr", _rows_t), ("di", _rows_t), ("dz", _rows_t), ("ddecay", ctypes.c_void_p),
+                ("dinit_state", ctypes.c_void_p)]
+
+
 class _norm_shape_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("group_size", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
@@ -77,8 +92,18 @@ def declare(lib):
     lib.ssd_channel_scan_fwd.argtypes = [vp, vp, i64] + [vp] * 4 + [sz, vp]
     lib.ssd_channel_scan_bwd.argtypes = [vp, vp, i64] + [vp] * 5 + [sz, vp]
     lib.ssd_channel_scan_step.argtypes = [vp] * 5
+    lib.ssd_gated_scan_chunk_states.argtypes = [vp]
+    lib.ssd_gated_scan_chunk_states.restype = i64
+    lib.ssd_gated_scan_workspace_size.argtypes = [vp, vp, i64]
+    lib.ssd_gated_scan_workspace_size.restype = sz
+    lib.ssd_gated_scan_bwd_workspace_size.argtypes = [vp, vp, i64, i32]
+    lib.ssd_gated_scan_bwd_workspace_size.restype = sz
+    lib.ssd_gated_scan_fwd.argtypes = [vp, vp, i64] + [vp] * 5 + [sz, vp]
+    lib.ssd_gated_scan_bwd.argtypes = [vp, vp, i64] + [vp] * 6 + [sz, vp]
+    lib.ssd_gated_scan_step.argtypes = [vp] * 5
     for name in ("ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd",
-                 "ssd_channel_scan_step", "ssd_block_norm_fwd", "ssd_block_norm_bwd"):
+                 "ssd_channel_scan_step", "ssd_block_norm_fwd", "ssd_block_norm_bwd", "ssd_gated_scan_fwd",
+                 "ssd_gated_scan_bwd", "ssd_gated_scan_step"):
         getattr(lib, name).restype = i32
 
 
@@ -451,6 +476,131 @@ def ssd_channel_scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state
                                    ctypes.byref(yr), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _fail("ssd_channel_scan_step", st)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# gated scan
+# ---------------------------------------------------------------------------
+_NO_ROWS = _rows_t(None, 0, 0)
+
+
+def _gated_inputs(x, r, decay, i, z, init_state, nseq, rows, dev):
+    ty, full = x.dtype, x.shape
+    return _gated_inputs_t(rows(x, "x", ty, full, dev), rows(r, "r", ty, full, dev),
+                           _NO_ROWS if i is None else rows(i, "i", ty, full, dev),
+                           _NO_ROWS if z is None else rows(z, "z", ty, full, dev),
+                           _given(decay, "decay", _F32, full[-1:], dev), _flat(init_state, "init_state", _F32, (nseq, full[-1]), dev))
+
+
+def _given(t, name, dtype, shape, idx):
+    """_flat of an operand that has to be there."""
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _flat(t, name, dtype, shape, idx)
+
+
+@_on_stream
+def ssd_gated_scan_fwd(x, r, decay, i=None, z=None, init_state=None, *, rate=8.0, cu_seqlens=None, y=None, final_state=None,
+                       return_final_state=True, return_chunk_states=False, workspace=None):
+    """Linear recurrence with one state a channel, gated by the token:
+
+        a = exp(-rate * softplus(decay) * sigmoid(r))
+        h <- a h + sqrt(1 - a^2) * sigmoid(i) * x,   y = h * silu(z)
+
+    x, r, i, z [b, L, Ch] (without i the input is not gated, without z y = h);
+    decay [Ch] fp32; states [nseq, Ch] fp32.  Returns ``(y, final_state)``,
+    and with ``return_chunk_states`` the states that enter every 64th token as
+    a third, for ssd_gated_scan_bwd."""
+    lib = _lib()
+    code, dev = _code(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, Ch]")
+    b, L, ch = x.shape
+    cu, nseq = _offsets(cu_seqlens, b)
+    ins = _gated_inputs(x, r, decay, i, z, init_state, nseq, _rows, dev)
+    if y is None:
+        y = _empty((b, L, ch), x.dtype, x)
+        yr = _rows_t(y.data_ptr(), L * ch, ch)
+    else:
+        yr = _rows(y, "y", x.dtype, (b, L, ch), dev)
+    fp = None
+    if final_state is not None:
+        fp = _flat(final_state, "final_state", _F32, (nseq, ch), dev)
+        if fp and fp == ins.init_state:
+            raise ValueError("final_state must not be init_state")
+    elif return_final_state:
+        final_state = _empty((nseq, ch), _F32, x)
+        fp = final_state.data_ptr()
+    shape = _gated_shape_t(b, L, ch, rate, code)
+    states = _empty((b, (L + 63) // 64, ch), _F32, x) if return_chunk_states else None
+    need = lib.ssd_gated_scan_workspace_size(ctypes.byref(shape), cu, nseq)
+    ws = _workspace(workspace, need, x) if need else None
+    st = lib.ssd_gated_scan_fwd(
+        ctypes.byref(shape), cu, nseq, ctypes.byref(ins), ctypes.byref(yr), fp, None if states is None else states.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_gated_scan_fwd", st)
+    return (y, final_state, states) if return_chunk_states else (y, final_state)
+
+
+@_on_stream
+def ssd_gated_scan_bwd(dy, x, r, decay, i=None, z=None, init_state=None, *, rate=8.0, cu_seqlens=None, dfinal_state=None,
+                       chunk_states=None, workspace=None):
+    """Gradient of ssd_gated_scan_fwd from its inputs and dy (and that of the
+    final state, zero without it).  ``chunk_states`` is what the forward call
+    returned as its third; without it those states are formed again.  Returns
+    ``(dx, dr, ddecay, di, dz, dinit_state)``, None where the input was None;
+    ddecay and dinit_state in fp32, the others in x's type."""
+    lib = _lib()
+    code, dev = _code(x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, Ch]")
+    b, L, ch = x.shape
+    cu, nseq = _offsets(cu_seqlens, b)
+    ins = _gated_inputs(x, r, decay, i, z, init_state, nseq, _rows, dev)
+    gr = _rows(dy, "dy", x.dtype, (b, L, ch), dev)
+    fp = _flat(dfinal_state, "dfinal_state", _F32, (nseq, ch), dev)
+    sp = _flat(chunk_states, "chunk_states", _F32, (b, (L + 63) // 64, ch), dev)
+    dx, dr = (_empty((b, L, ch), x.dtype, x) for _ in range(2))
+    di = None if i is None else _empty((b, L, ch), x.dtype, x)
+    dz = None if z is None else _empty((b, L, ch), x.dtype, x)
+    ddecay = _empty((ch,), _F32, x)
+    dinit = None if init_state is None else _empty((nseq, ch), _F32, x)
+    row = lambda t: _NO_ROWS if t is None else _rows_t(t.data_ptr(), L * ch, ch)
+    grads = _gated_grads_t(row(dx), row(dr), row(di), row(dz), ddecay.data_ptr(), None if dinit is None else dinit.data_ptr())
+    shape = _gated_shape_t(b, L, ch, rate, code)
+    ws = _workspace(workspace, lib.ssd_gated_scan_bwd_workspace_size(ctypes.byref(shape), cu, nseq, sp is not None), x)
+    st = lib.ssd_gated_scan_bwd(
+        ctypes.byref(shape), cu, nseq, ctypes.byref(gr), ctypes.byref(ins), fp, sp, ctypes.byref(grads), ws.data_ptr(),
+        ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_gated_scan_bwd", st)
+    return dx, dr, ddecay, di, dz, dinit
+
+
+@_on_stream
+def ssd_gated_scan_step(x, r, decay, i=None, z=None, *, state, rate=8.0, y=None):
+    """One token per sequence: x, r, i, z [b, Ch]; ``state`` [b, Ch] fp32 is
+    advanced in place.  Returns y [b, Ch]."""
+    lib = _lib()
+    code, dev = _code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [b, Ch]")
+    b, ch = x.shape
+    ins = _gated_inputs(x, r, decay, i, z, None, b, _rows2, dev)
+    sp = _given(state, "state", _F32, (b, ch), dev)
+    if y is None:
+        y = _empty((b, ch), x.dtype, x)
+        yr = _rows_t(y.data_ptr(), ch, 0)
+    else:
+        yr = _rows2(y, "y", x.dtype, (b, ch), dev)
+    shape = _gated_shape_t(b, 1, ch, rate, code)
+    st = lib.ssd_gated_scan_step(ctypes.byref(shape), ctypes.byref(ins), sp, ctypes.byref(yr),
+                                 torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_gated_scan_step", st)
     return y
 
 

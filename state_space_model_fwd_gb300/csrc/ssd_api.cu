@@ -10,11 +10,13 @@
 
 #include "ssd.h"
 #include "ssd_common.cuh"
+#include "ssd_status.h"
 #include "ssd_tc.cuh"
 
 namespace {
 
 using ssd::bf16;
+using ssd::device_status_word;
 using ssd::Dims;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -128,12 +130,16 @@ static __device__ unsigned g_device_status;
 static __device__ unsigned g_device_status_read;
 SymbolCache g_status_cache, g_status_read_cache;
 
-cudaError_t device_status_word(unsigned **out) {
+}  // namespace
+
+cudaError_t ssd::device_status_word(unsigned **out) {
     void *p = nullptr;
     const cudaError_t e = symbol_address(g_device_status, g_status_cache, &p);
     *out = static_cast<unsigned *>(p);
     return e;
 }
+
+namespace {
 
 // Atomically take the status word (so no bit latched by a kernel on another
 // stream between a read and a clear is lost).

@@ -1,0 +1,272 @@
+// ssd_gated.cuh -- pieces shared by the gated scan's kernels.
+//
+// Per channel, with s(v) = 1 / (1 + exp(-v)):
+//   l = -rate softplus(decay) s(r),  a = exp(l),  beta = sqrt(1 - a^2),
+//   h <- a h + beta s(i) x,  y = h (times silu(z)).
+// Everything is formed from v = 1 - a = -expm1(l): 1 - a^2 = v (2 - v) keeps
+// its digits where a is close to 1, which is where such layers work.
+//
+// A block of the prompt's kernels is a tile: kCols channels, two a lane, and
+// kWarps x S consecutive tokens, S a warp, whose inputs stay in registers from
+// the one read to the output.  What a run of tokens does to the state is
+// h -> A h + H; warps exchange their (A, H) through shared memory, tiles
+// theirs through the workspace (Links).  A run that holds a sequence's
+// boundary does not let the state through, whatever its value: A = -1 says so.
+#pragma once
+
+#include "ssd_channel.h"
+#include "ssd_status.h"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+
+constexpr int kCols = 64;        // channels of a block
+constexpr int kStateEvery = 64;  // tokens between the states kept for the gradient
+constexpr int kGroup = 16;       // tiles from one entry state to the next
+
+// Two channels of one token as they lie in memory.
+template <typename T>
+struct Two;
+template <>
+struct Two<bf16> {
+    uint32_t w;
+};
+template <>
+struct Two<float> {
+    float2 w;
+};
+__device__ __forceinline__ Two<bf16> two_of(bf16, float v) {
+    const __nv_bfloat162 h = __float2bfloat162_rn(v);
+    return {*reinterpret_cast<const uint32_t *>(&h)};
+}
+__device__ __forceinline__ Two<float> two_of(float, float v) { return {make_float2(v, v)}; }
+__device__ __forceinline__ float2 widen(const Two<bf16> &v) {
+    return make_float2(__uint_as_float(v.w << 16), __uint_as_float(v.w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 widen(const Two<float> &v) { return v.w; }
+
+// A lane's channels: c0 and c1 of the block's 64.  Rows whose pairs lie on
+// their own size's boundary are read in pairs, two neighbours a lane; others
+// one element at a time, 32 neighbours a warp.
+template <bool PAIRS>
+struct Lane {
+    int64_t c0;
+    int step;       // from c0 to the second channel
+    bool in0, in1;  // which exist
+    __device__ __forceinline__ Lane(int blk, int lane, int ch) {
+        c0 = (int64_t)blk * kCols + (PAIRS ? 2 * lane : lane);
+        step = PAIRS ? 1 : 32;
+        in0 = c0 < ch, in1 = c0 + step < ch;
+    }
+};
+
+template <typename T, bool PAIRS>
+__device__ __forceinline__ Two<T> load_two(const T *p, const Lane<PAIRS> &k, float fill) {  // p: at the lane's c0
+    Two<T> v = two_of(T(), fill);
+    if constexpr (PAIRS) {
+        if (k.in0) v.w = *reinterpret_cast<const decltype(v.w) *>(p);
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t lo = v.w & 0xFFFFu, hi = v.w >> 16;
+        if (k.in0) lo = *reinterpret_cast<const uint16_t *>(p);
+        if (k.in1) hi = *reinterpret_cast<const uint16_t *>(p + 32);
+        v.w = lo | hi << 16;
+    } else {
+        if (k.in0) v.w.x = p[0];
+        if (k.in1) v.w.y = p[32];
+    }
+    return v;
+}
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void store_two(T *p, const Lane<PAIRS> &k, float2 f) {
+    if constexpr (PAIRS) {
+        if (!k.in0) return;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16x2(f.x, f.y);
+        else
+            *reinterpret_cast<float2 *>(p) = f;
+    } else {
+        if (k.in0) p[0] = from_f32<T>(f.x);
+        if (k.in1) p[32] = from_f32<T>(f.y);
+    }
+}
+// The same for fp32 arrays of the channels (states, parameters): p is the array's row.
+template <bool PAIRS>
+__device__ __forceinline__ float2 load_state(const float *p, const Lane<PAIRS> &k) {
+    return make_float2(p && k.in0 ? p[k.c0] : 0.f, p && k.in1 ? p[k.c0 + k.step] : 0.f);
+}
+template <bool PAIRS>
+__device__ __forceinline__ void store_state(float *p, const Lane<PAIRS> &k, float2 v) {
+    if (k.in0) p[k.c0] = v.x;
+    if (k.in1) p[k.c0 + k.step] = v.y;
+}
+
+// -rate softplus(decay), per token at most a few times: the library's functions
+__device__ __forceinline__ float decay_rate(float decay, float rate) {
+    return -rate * (fmaxf(decay, 0.f) + log1pf(expf(-fabsf(decay))));
+}
+
+__device__ __forceinline__ f2 splat(float v) { return pack2(v, v); }
+__device__ __forceinline__ f2 both(float2 v) { return pack2(v.x, v.y); }
+__device__ __forceinline__ float2 apart(f2 v) {
+    float2 r;
+    unpack2(v, r.x, r.y);
+    return r;
+}
+
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 t = apart(mul2(both(v), splat(-kLog2e)));
+    const float2 d = apart(add2(pack2(ex2(t.x), ex2(t.y)), splat(1.f)));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+
+// v = 1 - a and a from l <= 0.  Above -1/4 the series of -expm1(l) (the first
+// term left out is l^6 / 5040 of the sum, 5e-8); below it 1 - exp(l), whose
+// absolute error 2^-23 is at most 5e-7 of v >= 0.22.
+__device__ __forceinline__ void decay2(f2 l, f2 &v, f2 &a) {
+    f2 q = fma2(l, splat(1.f / 720.f), splat(1.f / 120.f));
+    q = fma2(q, l, splat(1.f / 24.f));
+    q = fma2(q, l, splat(1.f / 6.f));
+    q = fma2(q, l, splat(0.5f));
+    q = fma2(q, l, splat(1.f));
+    const f2 m = mul2(l, splat(-1.f));
+    const float2 s = apart(mul2(q, m)), e = apart(mul2(l, splat(kLog2e))), lv = apart(l);
+    const float ex = ex2(e.x), ey = ex2(e.y);
+    const bool nx = lv.x > -0.25f, ny = lv.y > -0.25f;
+    const float vx = nx ? s.x : 1.f - ex, vy = ny ? s.y : 1.f - ey;
+    v = pack2(vx, vy);
+    a = pack2(nx ? 1.f - vx : ex, ny ? 1.f - vy : ey);
+}
+__device__ __forceinline__ float sqrt_approx(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// What a run of tokens does to the state that enters it.
+struct Run {
+    float2 A, H;
+};
+__device__ __forceinline__ float through(float A, float H, float h) { return A < 0.f ? H : fmaf(A, h, H); }
+__device__ __forceinline__ float2 through(const Run &r, float2 h) {
+    return make_float2(through(r.A.x, r.H.x, h.x), through(r.A.y, r.H.y, h.y));
+}
+// r, then s
+__device__ __forceinline__ Run then(const Run &r, const Run &s) {
+    Run o;
+    o.H = through(s, r.H);
+    o.A.x = s.A.x < 0.f || r.A.x < 0.f ? -1.f : r.A.x * s.A.x;
+    o.A.y = s.A.y < 0.f || r.A.y < 0.f ? -1.f : r.A.y * s.A.y;
+    return o;
+}
+
+// What tiles of a block row (one channel block of one sequence row) hand on,
+// [row][tile][64] in the workspace: every tile's (A, H), and the state that
+// enters every group of kGroup tiles.  The words are their own flags: the
+// workspace is filled with ones before the launch, and no A is that NaN (a
+// computed NaN is the canonical one, and -1 stands for a boundary).  A tile's
+// run does not depend on other tiles, so a tile waits for the entry state of
+// its group and the runs before it in the group, in one round of loads; the
+// last of a group hands the next entry state on.  The order of every sum is
+// fixed.  Tiles are numbered by a counter, earlier tokens first, so what a
+// block waits for has started before it.
+struct Links {
+    unsigned long long *run, *entry;  // null: one tile a row, nothing to wait for
+    unsigned *ticket;
+    unsigned *status;
+};
+constexpr unsigned kUnset = 0xFFFFFFFFu;
+__device__ __forceinline__ unsigned long long link_word(float A, float H) {
+    // (a NaN that came in through an operand may have any bits)
+    const unsigned a = A != A ? 0x7FFFFFFFu : __float_as_uint(A);
+    return (unsigned long long)a << 32 | __float_as_uint(H);
+}
+__device__ __forceinline__ void link_store(unsigned long long *p, const Run &r) {
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(link_word(r.A.x, r.H.x)) : "memory");
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + 32), "l"(link_word(r.A.y, r.H.y)) : "memory");
+}
+__device__ __forceinline__ unsigned long long link_load(const unsigned long long *p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+// Waits until both words are there; gives up after 100 ms and says so in the status word.
+__device__ __forceinline__ Run link_wait(const unsigned long long *p, unsigned *status) {
+    unsigned long long u = link_load(p), v = link_load(p + 32);
+    if ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset) {
+        const uint64_t t0 = tc::globaltimer_ns();
+        do {
+            __nanosleep(40);
+            u = link_load(p), v = link_load(p + 32);
+            const uint64_t spent = tc::globaltimer_ns() - t0;
+            if (spent > 100000000ull) atomicOr(status, 1u);
+            if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
+        } while ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset);
+    }
+    Run r;
+    r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
+    r.H = make_float2(__uint_as_float((unsigned)u), __uint_as_float((unsigned)v));
+    return r;
+}
+
+// Sequence boundaries in a warp's tokens t0 .. t0 + S - 1 (the same in all lanes).
+struct Cuts {
+    unsigned first, last;  // bit s: token t0 + s is its sequence's first, last
+    int seq;               // of token t0
+};
+template <int S>
+__device__ __forceinline__ Cuts cuts_of(const Seqs &q, int t0) {
+    const int *start = q.offsets();
+    Cuts c{0, 0, seq_of(start, q.n, t0)};
+    if (start[c.seq] == t0) c.first = 1;
+    for (int s = c.seq + 1; s <= q.n; ++s) {  // (an empty sequence has the next one's bit, or none past the last token)
+        const int d = start[s] - t0;
+        if (d > S) break;
+        if (d < S && start[s] < q.L) c.first |= 1u << d;
+        c.last |= 1u << (d - 1);
+    }
+    return c;
+}
+// The sequence of token t, at or after sequence s.
+__device__ __forceinline__ int seq_from(const Seqs &q, int s, int t) {
+    const int *start = q.offsets();
+    while (start[s + 1] <= t) ++s;
+    return s;
+}
+
+template <typename T>
+struct GatedArgs {
+    Rows<const T> x, r, i, z, dy;  // i.p, z.p null: absent
+    Rows<T> y, dx, dr, di, dz;     // y.p null: only the kept states are wanted
+    const float *decay, *init, *dfinal, *kept;
+    float *fin, *keep, *dinit, *ddecay_part;  // keep, kept: [b][ceil(L / 64)][ch] states entering every 64 tokens
+    float rate;
+    int ch, nblk, batch, ntile, nkeep;
+    Seqs seqs;
+    Links links;
+};
+
+// host side (ssd_gated.cu)
+ssd_status_t check_gated(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq);
+bool gated_inputs_ok(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, bool rows);
+inline int64_t gated_blocks(const ssd_gated_shape_t *s) { return (s->channels + kCols - 1) / kCols; }
+inline int64_t gated_kept(const ssd_gated_shape_t *s) { return (s->seqlen + kStateEvery - 1) / kStateEvery; }
+// Workspace of the links of `rows` block rows of `ntile` tiles each, and their place in it.
+size_t links_bytes(int64_t rows, int64_t ntile);
+cudaError_t place_links(char *ws, int64_t rows, int64_t ntile, Links &l, cudaStream_t st);
+// Pairs of channels that lie on their own size's boundary in every row.
+bool rows_pairs(const ssd_rows_t &r, size_t esize, int64_t b, int64_t L);
+template <typename T>
+GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, int64_t nseq);
+bool gated_pairs(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
+// Every empty sequence's dst = src (zeros without src).
+cudaError_t launch_empty(const Seqs &q, const int64_t *cu, int64_t nseq, int64_t ch, const float *src, float *dst, cudaStream_t st);
+template <typename T>
+cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st);
+size_t gated_fwd_links(const ssd_gated_shape_t *s);
+
+}  // namespace ssd

@@ -1,0 +1,342 @@
+// ssd_gated_bwd.cu -- gradient of the gated scan.
+//
+// With g_t the gradient of h_t and d_t = dy_t silu(z_t):
+//   g_t = d_t + a_{t+1} g_{t+1}
+//   dx = g beta s(i),  di = g beta x s(i) (1 - s(i)),  dz = dy h silu'(z)
+//   dl = g (a h_{t-1} - s(i) x a^2 / beta),  dr = dl l (1 - s(r)),
+//   ddecay = softplus'/softplus sum_t dl l       (l = log a)
+// l / beta goes to zero with l, so dl l is formed as one: no division by beta.
+//
+// A block is a tile as in the forward kernel, later tokens first: the state
+// that enters comes from those kept every 64 tokens, what comes back from
+// later tokens (c_t = a_t g_t, so c -> P c + Q over a run of tokens) through
+// the links.  Everything is read once and written once; what bounds it is in
+// the kernel's comment.
+#include "ssd_gated.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int S = kStateEvery / kWarps;  // tokens a warp: a tile starts at a kept state
+
+template <typename T, bool PAIRS, bool GATE, bool PACKED>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
+    __shared__ float4 fore[kWarps][32], back[kWarps][32];
+    __shared__ float4 tiles[kGroup][32];
+    __shared__ float2 enter[32];
+    __shared__ unsigned ticket;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    unsigned n = blockIdx.x;
+    if (a.links.run) {
+        if (threadIdx.x == 0) ticket = atomicAdd(a.links.ticket, 1u) + 1u;
+        __syncthreads();
+        n = ticket;
+    }
+    const int rows = a.nblk * a.batch, later = n / rows, row = n % rows, b = row / a.nblk;  // later: tiles behind this one
+    const int tile = a.ntile - 1 - later;
+    const Lane<PAIRS> k(row % a.nblk, lane, a.ch);
+    const int L = a.seqs.L, t0 = (tile * nw + warp) * S;
+
+    Two<T> x[S], r[S], g[S], dy[S], z[S];
+    {
+        const T *px = a.x.at(b, 0) + k.c0, *pr = a.r.at(b, 0) + k.c0, *pi = a.i.p ? a.i.at(b, 0) + k.c0 : nullptr;
+        const T *pd = a.dy.at(b, 0) + k.c0, *pz = GATE ? a.z.at(b, 0) + k.c0 : nullptr;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            x[s] = two_of(T(), 0.f), r[s] = two_of(T(), -30000.f), g[s] = two_of(T(), 128.f), dy[s] = z[s] = two_of(T(), 0.f);
+            if (t0 + s < L) {
+                r[s] = load_two<T, PAIRS>(pr + a.r.step(t0 + s), k, -30000.f);
+                x[s] = load_two<T, PAIRS>(px + a.x.step(t0 + s), k, 0.f);
+                if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(t0 + s), k, 128.f);
+                dy[s] = load_two<T, PAIRS>(pd + a.dy.step(t0 + s), k, 0.f);
+                if constexpr (GATE) z[s] = load_two<T, PAIRS>(pz + a.z.step(t0 + s), k, 0.f);
+            }
+        }
+    }
+    Cuts cut{0, 0, b};
+    if (PACKED && t0 < L) cut = cuts_of<S>(a.seqs, t0);
+    const float2 dec = load_state(a.decay, k);
+    const f2 rate = pack2(decay_rate(dec.x, a.rate), decay_rate(dec.y, a.rate));
+    auto init_at = [&](int s) {
+        return load_state(a.init ? a.init + (int64_t)(PACKED ? seq_from(a.seqs, cut.seq, t0 + s) : b) * a.ch : nullptr, k);
+    };
+    auto dfinal_at = [&](int s) {
+        return load_state(a.dfinal ? a.dfinal + (int64_t)(PACKED ? seq_from(a.seqs, cut.seq, t0 + s) : b) * a.ch : nullptr, k);
+    };
+
+    f2 sr[S], si[S], vv[S], av[S], d[S];
+    f2 A = splat(1.f), H = splat(0.f);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        sr[s] = both(sigmoid2(widen(r[s])));
+        si[s] = both(sigmoid2(widen(g[s])));
+        decay2(mul2(rate, sr[s]), vv[s], av[s]);
+        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
+        const f2 u = mul2(mul2(pack2(sqrt_approx(w.x), sqrt_approx(w.y)), si[s]), both(widen(x[s])));
+        if (PACKED && (cut.first >> s & 1)) H = both(init_at(s));
+        A = mul2(A, av[s]);
+        H = fma2(av[s], H, u);
+        d[s] = both(widen(dy[s]));
+        if constexpr (GATE) {
+            const float2 zf = widen(z[s]);
+            d[s] = mul2(d[s], mul2(both(zf), both(sigmoid2(zf))));
+        }
+    }
+    f2 Q = splat(0.f);
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        if (PACKED && (cut.last >> s & 1)) Q = both(dfinal_at(s));
+        Q = mul2(av[s], add2(d[s], Q));
+    }
+    if (nw > 1) {
+        const float2 fa = apart(A), fh = apart(H), fq = apart(Q);
+        const bool cf = PACKED && cut.first, cl = PACKED && cut.last;
+        fore[warp][lane] = cf ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
+        back[warp][lane] = cl ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
+        __syncthreads();
+    }
+    auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
+
+    // What comes back from the tokens after the tile.
+    float2 c = make_float2(0.f, 0.f);
+    if (!PACKED) c = load_state(a.dfinal ? a.dfinal + (int64_t)b * a.ch : nullptr, k);
+    if (a.links.run) {
+        unsigned long long *mine = a.links.run + ((int64_t)row * a.ntile + later) * kCols + lane;
+        const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
+        unsigned long long *entry = a.links.entry + (int64_t)row * groups * kCols + lane;
+        const int in_group = later % kGroup, group = later / kGroup;
+        Run all{};
+        if (warp == 0) {
+            all = run_of(back[nw - 1][lane]);
+            for (int w = nw - 2; w >= 0; --w) all = then(all, run_of(back[w][lane]));
+            if (in_group != kGroup - 1 && tile > 0) link_store(mine, all);
+        }
+        for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
+            const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
+            tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
+        }
+        if (warp == 0 && group > 0) c = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
+        __syncthreads();
+        if (warp == 0) {
+            for (int j = 0; j < in_group; ++j) c = through(run_of(tiles[j][lane]), c);
+            if (in_group == kGroup - 1 && tile > 0)
+                link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, c)});
+            enter[lane] = c;
+        }
+        __syncthreads();
+        c = enter[lane];
+    }
+    for (int w = nw - 1; w > warp; --w) c = through(run_of(back[w][lane]), c);
+    float2 h = load_state(a.kept + ((int64_t)b * a.nkeep + tile) * a.ch, k);
+    for (int w = 0; w < warp; ++w) h = through(run_of(fore[w][lane]), h);
+
+    f2 prev[S], hv = both(h);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (PACKED && (cut.first >> s & 1)) hv = both(init_at(s));
+        prev[s] = hv;
+        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
+        const f2 u = mul2(mul2(pack2(sqrt_approx(w.x), sqrt_approx(w.y)), si[s]), both(widen(x[s])));
+        hv = fma2(av[s], hv, u);
+        if constexpr (GATE) {
+            if (t0 + s < L) {
+                const float2 zf = widen(z[s]), sz = sigmoid2(zf);
+                const f2 slope = pack2(silu_slope(zf.x, sz.x), silu_slope(zf.y, sz.y));
+                store_two<T, PAIRS>(a.dz.at(b, t0 + s) + k.c0, k, apart(mul2(mul2(both(widen(dy[s])), hv), slope)));
+            }
+        }
+    }
+    f2 cv = both(c), sum = splat(0.f);
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        if (PACKED && (cut.last >> s & 1)) cv = both(dfinal_at(s));
+        const f2 gh = add2(d[s], cv), xf = both(widen(x[s])), l = mul2(rate, sr[s]);
+        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
+        const float wx = fmaxf(w.x, 1e-37f), wy = fmaxf(w.y, 1e-37f);
+        const f2 rb = pack2(rsqrt_approx(wx), rsqrt_approx(wy)), beta = mul2(pack2(w.x, w.y), rb);
+        const f2 sx = mul2(si[s], xf);
+        // dl l = g a (l h_{t-1} - s(i) x a l / beta)
+        const f2 ga = mul2(gh, av[s]);
+        const f2 inner = fma2(mul2(mul2(sx, av[s]), mul2(l, rb)), splat(-1.f), mul2(l, prev[s]));
+        const f2 dll = mul2(ga, inner);
+        sum = add2(sum, dll);
+        cv = ga;
+        if (PACKED && (cut.first >> s & 1)) {
+            if (a.dinit) store_state(a.dinit + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch, k, apart(cv));
+        }
+        if (t0 + s < L) {
+            const f2 gb = mul2(mul2(gh, beta), si[s]);
+            store_two<T, PAIRS>(a.dx.at(b, t0 + s) + k.c0, k, apart(gb));
+            store_two<T, PAIRS>(a.dr.at(b, t0 + s) + k.c0, k, apart(mul2(dll, fma2(sr[s], splat(-1.f), splat(1.f)))));
+            if (a.i.p)
+                store_two<T, PAIRS>(a.di.at(b, t0 + s) + k.c0, k,
+                                    apart(mul2(mul2(gb, xf), fma2(si[s], splat(-1.f), splat(1.f)))));
+        }
+    }
+    if (!PACKED && t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)b * a.ch, k, apart(cv));
+    if (a.ddecay_part) {
+        const float2 f = apart(sum);
+        if (nw > 1) {
+            __syncthreads();
+            fore[warp][lane] = make_float4(f.x, f.y, 0.f, 0.f);
+            __syncthreads();
+        }
+        if (warp == 0) {
+            float2 s = f;
+            for (int w = 1; w < nw; ++w) s.x += fore[w][lane].x, s.y += fore[w][lane].y;
+            store_state(a.ddecay_part + ((int64_t)tile * a.batch + b) * a.ch, k, s);
+        }
+    }
+}
+
+// ddecay[c] = softplus'(decay) / softplus(decay) sum over the tiles' parts, in a fixed order.  The quotient's limit for
+// decay -> -inf is 1.
+__global__ void __launch_bounds__(1024) gated_ddecay_kernel(const float *part, int64_t n, int64_t ch, const float *decay, float *out) {
+    __shared__ float sums[32][33];
+    launch_next();
+    wait_previous();
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (c < ch) {
+        int64_t t = w;
+        for (; t + 96 < n; t += 128) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += part[(t + 32 * j) * ch + c];
+        }
+        for (; t < n; t += 32) v[0] += part[t * ch + c];
+    }
+    sums[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+    __syncthreads();
+    if (w == 0 && c < ch) {
+        float s = 0.f;
+        for (int j = 0; j < 32; ++j) s += sums[j][lane];
+        const float d = decay[c], sp = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d)));
+        out[c] = s * (d < -15.f ? 1.f : 1.f / (1.f + expf(-d)) / sp);
+    }
+}
+
+int64_t bwd_warps(int64_t L) {
+    const int64_t w = (L + S - 1) / S;
+    return w < 1 ? 1 : w < kWarps ? w : kWarps;
+}
+
+struct BwdPlan {
+    size_t kept, fwd_links, links, part, bytes;
+};
+BwdPlan plan_bwd(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq, bool with_states) {
+    BwdPlan p{};
+    const int64_t rows = gated_blocks(s) * s->batch, ntile = gated_kept(s);
+    size_t at = cu ? offsets_bytes(cu, nseq) : 0;
+    p.kept = at;
+    if (!with_states) at += align256(sizeof(float) * s->batch * ntile * s->channels);
+    p.fwd_links = at;
+    if (!with_states) at += gated_fwd_links(s);
+    p.links = at;
+    at += links_bytes(rows, ntile);
+    p.part = at;
+    at += align256(sizeof(float) * ntile * s->batch * s->channels);
+    p.bytes = at;
+    return p;
+}
+
+template <typename T>
+ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq, const ssd_rows_t *dy,
+                       const ssd_gated_inputs_t *in, const float *dfinal, const float *kept, const ssd_gated_grads_t *out,
+                       char *ws, cudaStream_t st) {
+    timing_begin(st);
+    cudaError_t e = cudaSuccess;
+    if (s->seqlen == 0) {
+        if (out->dinit_state) e = copy_states(dfinal, out->dinit_state, nseq * s->channels, st);
+        if (e == cudaSuccess && out->ddecay) e = cudaMemsetAsync(out->ddecay, 0, sizeof(float) * s->channels, st);
+        return status_of(e);
+    }
+    const BwdPlan p = plan_bwd(s, cu, nseq, kept != nullptr);
+    GatedArgs<T> a = gated_args<T>(s, in, nseq);
+    if (cu) {
+        bool launched;
+        e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws), a.seqs, &launched, st);
+        if (e == cudaSuccess && out->dinit_state) e = launch_empty(a.seqs, cu, nseq, s->channels, dfinal, out->dinit_state, st);
+        if (e != cudaSuccess) return status_of(e);
+    }
+    bool pairs = gated_pairs(s, in);
+    if (!kept) {
+        a.keep = reinterpret_cast<float *>(ws + p.kept);
+        e = launch_gated_fwd(a, s, pairs, cu != nullptr, ws + p.fwd_links, st);
+        if (e != cudaSuccess) return status_of(e);
+        kept = a.keep;
+    }
+    a.kept = kept, a.dfinal = dfinal;
+    a.dy = rows_of<const T>(*dy);
+    a.dx = rows_of<T>(out->dx), a.dr = rows_of<T>(out->dr), a.di = rows_of<T>(out->di), a.dz = rows_of<T>(out->dz);
+    a.dinit = out->dinit_state;
+    a.ddecay_part = out->ddecay ? reinterpret_cast<float *>(ws + p.part) : nullptr;
+    for (const ssd_rows_t *r : {dy, &out->dx, &out->dr}) pairs = pairs && rows_pairs(*r, sizeof(T), s->batch, s->seqlen);
+    if (in->i.data) pairs = pairs && rows_pairs(out->di, sizeof(T), s->batch, s->seqlen);
+    if (in->z.data) pairs = pairs && rows_pairs(out->dz, sizeof(T), s->batch, s->seqlen);
+    const int64_t ntile = gated_kept(s), nw = bwd_warps(s->seqlen);
+    a.ntile = (int)ntile;
+    e = place_links(ws + p.links, gated_blocks(s) * s->batch, ntile, a.links, st);
+    if (e != cudaSuccess) return status_of(e);
+    const unsigned blocks = (unsigned)(ntile * a.nblk * a.batch);
+    auto go = [&](auto pr, auto g, auto c) {
+        gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value><<<blocks, (unsigned)(nw * 32), 0, st>>>(a);
+    };
+    auto with_cuts = [&](auto pr, auto g) { cu ? go(pr, g, std::true_type{}) : go(pr, g, std::false_type{}); };
+    auto with_gate = [&](auto pr) { a.z.p ? with_cuts(pr, std::true_type{}) : with_cuts(pr, std::false_type{}); };
+    pairs ? with_gate(std::true_type{}) : with_gate(std::false_type{});
+    timing_mark(st, "gated_bwd");
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !out->ddecay) return status_of(e);
+    e = launch(gated_ddecay_kernel, dim3((unsigned)((s->channels + 31) / 32)), 1024, 0, st, true, a.ddecay_part,
+               ntile * s->batch, s->channels, a.decay, out->ddecay);
+    timing_mark(st, "gated_ddecay");
+    return status_of(e);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" {
+
+size_t ssd_gated_scan_bwd_workspace_size(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq,
+                                         int with_chunk_states) {
+    using namespace ssd;
+    if (check_gated(shape, cu_seqlens, nseq) != SSD_OK || shape->batch == 0 || shape->seqlen == 0) return 0;
+    return plan_bwd(shape, cu_seqlens, nseq, with_chunk_states != 0).bytes;
+}
+
+ssd_status_t ssd_gated_scan_bwd(const ssd_gated_shape_t *shape, const int64_t *cu_seqlens, int64_t nseq, const ssd_rows_t *dy,
+                                const ssd_gated_inputs_t *in, const float *dfinal_state, const float *chunk_states,
+                                const ssd_gated_grads_t *out, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    using namespace ssd;
+    const ssd_status_t st = check_gated(shape, cu_seqlens, nseq);
+    if (st != SSD_OK) return st;
+    if (!cu_seqlens) nseq = shape->batch;
+    if (!in || !out || !dy) return SSD_ERR_INVALID_ARG;
+    if (nseq == 0) {
+        if (out->ddecay)
+            return status_of(cudaMemsetAsync(out->ddecay, 0, sizeof(float) * shape->channels, stream));
+        return SSD_OK;
+    }
+    const bool rows = shape->seqlen > 0;
+    const size_t es = dtype_size(shape->dtype);
+    if (!gated_inputs_ok(shape, in, rows) || !aligned(dfinal_state, 4) || !aligned(chunk_states, 4) || !aligned(out->ddecay, 4) ||
+        !aligned(out->dinit_state, 4) || (out->dinit_state && out->dinit_state == dfinal_state))
+        return SSD_ERR_INVALID_ARG;
+    if (rows) {
+        const int64_t b = shape->batch, L = shape->seqlen, ch = shape->channels;
+        if (!rows_in_ok(*dy, es) || !rows_out_ok(out->dx, es, b, L, ch) || !rows_out_ok(out->dr, es, b, L, ch)) return SSD_ERR_INVALID_ARG;
+        if (in->i.data && !rows_out_ok(out->di, es, b, L, ch)) return SSD_ERR_INVALID_ARG;
+        if (in->z.data && !rows_out_ok(out->dz, es, b, L, ch)) return SSD_ERR_INVALID_ARG;
+    }
+    const size_t need = ssd_gated_scan_bwd_workspace_size(shape, cu_seqlens, nseq, chunk_states != nullptr);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return SSD_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    return shape->dtype == SSD_DTYPE_BF16
+               ? bwd_typed<bf16>(shape, cu_seqlens, nseq, dy, in, dfinal_state, chunk_states, out, ws, stream)
+               : bwd_typed<float>(shape, cu_seqlens, nseq, dy, in, dfinal_state, chunk_states, out, ws, stream);
+}
+
+}  // extern "C"
