@@ -538,6 +538,39 @@ SSD_API ssd_status_t ssd_block_norm_bwd(const ssd_norm_shape_t *shape, const ssd
                                         size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Token log-probabilities: per row z of `vocab` logits,
+ *   lse = log sum_v exp(z_v),  logprob = z_target - lse,
+ *   entropy = lse - sum_v p_v z_v  (p = exp(z - lse)),
+ * and the `top` most probable tokens, the most probable first, equal ones by
+ * index (NaN before everything).  logits [rows, vocab] T (row_stride;
+ * batch_stride is ignored), targets [rows]; outputs fp32, top_logprob and
+ * top_index [rows, top] (top up to SSD_LOGPROB_MAX_TOP); logprob (and targets
+ * with it), lse, entropy may be NULL.  Sums are held in fp32.
+ * A negative target gives no token: logprob 0, no gradient.  A target past
+ * the vocabulary gives NaN.  Minus infinity masks a token out; a row that is
+ * masked throughout has lse and log-probabilities of minus infinity, entropy
+ * 0 and a gradient of zeros.
+ * ssd_token_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
+ *   dlogits_v = p_v (dlse - dlogprob - dentropy (log p_v + entropy)) + [v = target] dlogprob
+ * from the logits and what the forward call gave (entropy only with
+ * dentropy).  dlogits may be the logits themselves (the same rows), otherwise
+ * must not overlap them; `top` is ignored beyond its check.
+ */
+#define SSD_LOGPROB_MAX_TOP 64
+typedef struct {
+    int64_t rows, vocab, top;
+    ssd_dtype_t dtype;
+} ssd_logprob_shape_t;
+
+SSD_API ssd_status_t ssd_token_logprob_fwd(const ssd_logprob_shape_t *shape, const ssd_rows_t *logits,
+                                           const int64_t *targets, float *logprob, float *lse, float *entropy,
+                                           float *top_logprob, int64_t *top_index, cudaStream_t stream);
+SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, const ssd_rows_t *logits,
+                                           const int64_t *targets, const float *lse, const float *entropy,
+                                           const float *dlogprob, const float *dlse, const float *dentropy,
+                                           const ssd_rows_t *dlogits, cudaStream_t stream);
+
+/*
  * Launch timing (instrumentation; the pages have no counterpart).  While
  * enabled, every entry point records a CUDA event on its stream before each
  * kernel it launches and one after the last, so a caller can read the device
