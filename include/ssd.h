@@ -571,6 +571,36 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
                                            const ssd_rows_t *dlogits, cudaStream_t stream);
 
 /*
+ * Head log-probabilities: logprob, lse and entropy as ssd_token_logprob_fwd
+ * gives them, of the logits z = hidden weight^T, which are formed on the
+ * tensor cores (bf16 operands, fp32 sums) and not stored.  hidden [rows, dim],
+ * weight [vocab, dim] bf16, rows 16-byte aligned (pointer and row_stride);
+ * targets, outputs and masked or absent targets as there.
+ * ssd_head_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
+ * dhidden [rows, dim], dweight [vocab, dim] in bf16 (either NULL: not wanted).
+ * The logits are formed again; their gradient is rounded to bf16 (2^-9
+ * relative, as the operands are) and takes 2 rows vocab bytes of the
+ * workspace; sums over it are fp32, in a fixed order, and rounded once.
+ * Supported: bf16, dim a multiple of 8.  A wait that gives up in a kernel is
+ * reported by ssd_get_device_status.
+ */
+typedef struct {
+    int64_t rows, vocab, dim;
+    ssd_dtype_t dtype;
+} ssd_head_shape_t;
+
+SSD_API size_t ssd_head_logprob_workspace_size(const ssd_head_shape_t *shape);
+SSD_API ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_t *hidden, const ssd_rows_t *weight,
+                                          const int64_t *targets, float *logprob, float *lse, float *entropy,
+                                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+SSD_API size_t ssd_head_logprob_bwd_workspace_size(const ssd_head_shape_t *shape);
+SSD_API ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_t *hidden, const ssd_rows_t *weight,
+                                          const int64_t *targets, const float *lse, const float *entropy,
+                                          const float *dlogprob, const float *dlse, const float *dentropy,
+                                          const ssd_rows_t *dhidden, const ssd_rows_t *dweight, void *workspace,
+                                          size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Launch timing (instrumentation; the pages have no counterpart).  While
  * enabled, every entry point records a CUDA event on its stream before each
  * kernel it launches and one after the last, so a caller can read the device

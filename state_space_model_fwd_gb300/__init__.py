@@ -41,7 +41,8 @@ EXPORTED = ("ssd_status_string", "ssd_abi_version", "ssd_fwd_workspace_size", "s
             "ssd_block_norm_fwd", "ssd_block_norm_bwd_workspace_size", "ssd_block_norm_bwd",
             "ssd_gated_scan_chunk_states", "ssd_gated_scan_workspace_size", "ssd_gated_scan_fwd",
             "ssd_gated_scan_bwd_workspace_size", "ssd_gated_scan_bwd", "ssd_gated_scan_step",
-            "ssd_token_logprob_fwd", "ssd_token_logprob_bwd")
+            "ssd_token_logprob_fwd", "ssd_token_logprob_bwd", "ssd_head_logprob_workspace_size", "ssd_head_logprob_fwd",
+            "ssd_head_logprob_bwd_workspace_size", "ssd_head_logprob_bwd")
 
 
 class ssd_shape_t(ctypes.Structure):
@@ -463,8 +464,9 @@ def launch_times_ms() -> list:
 from ._layer import (  # noqa: E402  (built on the helpers above)
     ssd_block_norm_bwd, ssd_block_norm_fwd, ssd_channel_scan_bwd, ssd_channel_scan_fwd, ssd_channel_scan_step,
     ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step, ssd_gated_scan_bwd, ssd_gated_scan_fwd, ssd_gated_scan_step)
-from ._logprob import ssd_token_logprob_bwd, ssd_token_logprob_fwd  # noqa: E402
+from ._logprob import (  # noqa: E402
+    ssd_head_logprob_bwd, ssd_head_logprob_fwd, ssd_token_logprob_bwd, ssd_token_logprob_fwd)
 
-__all__ = ["ssd_token_logprob_fwd", "ssd_token_logprob_bwd", "ssd_block_norm_fwd", "ssd_block_norm_bwd", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd", "ssd_channel_scan_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_gated_scan_fwd", "ssd_gated_scan_bwd", "ssd_gated_scan_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
+__all__ = ["ssd_token_logprob_fwd", "ssd_token_logprob_bwd", "ssd_head_logprob_fwd", "ssd_head_logprob_bwd", "ssd_block_norm_fwd", "ssd_block_norm_bwd", "ssd_channel_scan_fwd", "ssd_channel_scan_bwd", "ssd_channel_scan_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step", "ssd_gated_scan_fwd", "ssd_gated_scan_bwd", "ssd_gated_scan_step", "ssd_fwd_quadratic", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size", "ssd_decode_step", "get_device_status", "check_device_status", "selftest_scan_timeout", "ssd_fwd_noalloc", "launch_timing", "launch_times_ms", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_chunk_cumsum", "ssd_chunk_state",
            "ssd_state_passing", "ssd_chunk_scan", "selective_scan_fwd", "ssd_shape_t", "SSDError",
            "load_library", "status_string", "EXPORTED", "LIB_PATH"]

@@ -1,5 +1,6 @@
 """Binding of the end of a language model: log-probabilities of given tokens,
-the log of the sum, entropies and the top alternatives, from logits.
+the log of the sum, entropies and the top alternatives, from logits or from
+hidden states and the output weights.
 
 Rows of an operand lie at one stride (column slices and one row for all are
 fine).  Operands are on the current device; every function takes ``stream``
@@ -11,11 +12,15 @@ import ctypes
 
 import torch
 
-from ._layer import _F32, _code, _empty, _fail, _flat, _given, _lib, _norm_rows, _on_stream, _rows_t
+from ._layer import _F32, _code, _empty, _fail, _flat, _given, _lib, _norm_rows, _on_stream, _rows_t, _workspace
 
 
 class _logprob_shape_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("top", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class _head_shape_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
 def declare(lib):
@@ -23,7 +28,12 @@ def declare(lib):
     vp = ctypes.c_void_p
     lib.ssd_token_logprob_fwd.argtypes = [vp] * 9
     lib.ssd_token_logprob_bwd.argtypes = [vp] * 10
-    for name in ("ssd_token_logprob_fwd", "ssd_token_logprob_bwd"):
+    for name in ("ssd_head_logprob_workspace_size", "ssd_head_logprob_bwd_workspace_size"):
+        getattr(lib, name).argtypes = [vp]
+        getattr(lib, name).restype = ctypes.c_size_t
+    lib.ssd_head_logprob_fwd.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.ssd_head_logprob_bwd.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
+    for name in ("ssd_token_logprob_fwd", "ssd_token_logprob_bwd", "ssd_head_logprob_fwd", "ssd_head_logprob_bwd"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -95,3 +105,71 @@ def ssd_token_logprob_bwd(logits, targets, lse, entropy=None, *, dlogprob=None, 
     if st:
         _fail("ssd_token_logprob_bwd", st)
     return dlogits
+
+
+# ---------------------------------------------------------------------------
+# from hidden states
+# ---------------------------------------------------------------------------
+def _head(hidden, weight):
+    """(shape, rows of hidden, rows of weight, device, leading dimensions)"""
+    code, dev = _code(hidden, "hidden")
+    if hidden.dim() < 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("hidden must be [..., dim] and weight [vocab, dim]")
+    dim, lead = hidden.shape[-1], hidden.shape[:-1]
+    hr = _norm_rows(hidden, "hidden", hidden.dtype, hidden.shape, dev)
+    wr = _norm_rows(weight, "weight", hidden.dtype, (weight.shape[0], dim), dev)
+    return _head_shape_t(hidden.numel() // dim if dim else 0, weight.shape[0], dim, code), hr, wr, dev, lead
+
+
+@_on_stream
+def ssd_head_logprob_fwd(hidden, weight, targets=None, *, return_entropy=True, workspace=None):
+    """ssd_token_logprob_fwd of the logits hidden @ weight.T, which are formed
+    on the tensor cores and not stored.
+
+    hidden [..., dim], weight [vocab, dim] bf16 with rows on 16-byte
+    boundaries (dim a multiple of 8); targets [...] int64.  Returns
+    ``(logprob, lse, entropy)``, None for what was not asked for."""
+    lib = _lib()
+    shape, hr, wr, dev, lead = _head(hidden, weight)
+    tp = _flat(targets, "targets", torch.int64, lead, dev)
+    logprob = None if targets is None else _empty(lead, _F32, hidden)
+    lse = _empty(lead, _F32, hidden)
+    entropy = _empty(lead, _F32, hidden) if return_entropy else None
+    ws = _workspace(workspace, lib.ssd_head_logprob_workspace_size(ctypes.byref(shape)), hidden)
+    st = lib.ssd_head_logprob_fwd(ctypes.byref(shape), ctypes.byref(hr), ctypes.byref(wr), tp, _ptr(logprob), lse.data_ptr(),
+                                  _ptr(entropy), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_head_logprob_fwd", st)
+    return logprob, lse, entropy
+
+
+@_on_stream
+def ssd_head_logprob_bwd(hidden, weight, targets, lse, entropy=None, *, dlogprob=None, dlse=None, dentropy=None,
+                         need_dhidden=True, need_dweight=True, workspace=None):
+    """Gradient of ssd_head_logprob_fwd from its inputs, what it returned and
+    the gradients of logprob, lse and entropy (zero without them; ``entropy``
+    is needed with ``dentropy`` only).  Returns ``(dhidden, dweight)`` in
+    bf16, None for what is not needed.  The workspace holds the logits'
+    gradient, 2 bytes each."""
+    lib = _lib()
+    shape, hr, wr, dev, lead = _head(hidden, weight)
+    tp = _flat(targets, "targets", torch.int64, lead, dev)
+    lp = _given(lse, "lse", _F32, lead, dev)
+    ep = _flat(entropy, "entropy", _F32, lead, dev)
+    g = [_flat(v, n, _F32, lead, dev) for v, n in ((dlogprob, "dlogprob"), (dlse, "dlse"), (dentropy, "dentropy"))]
+    if dlogprob is not None and targets is None:
+        raise ValueError("dlogprob needs targets")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    dim = hidden.shape[-1]
+    dhidden = _empty(hidden.shape, hidden.dtype, hidden) if need_dhidden else None
+    dweight = _empty(weight.shape, hidden.dtype, hidden) if need_dweight else None
+    dhr = None if dhidden is None else ctypes.byref(_rows_t(dhidden.data_ptr(), 0, dim))
+    dwr = None if dweight is None else ctypes.byref(_rows_t(dweight.data_ptr(), 0, dim))
+    ws = _workspace(workspace, lib.ssd_head_logprob_bwd_workspace_size(ctypes.byref(shape)), hidden)
+    st = lib.ssd_head_logprob_bwd(ctypes.byref(shape), ctypes.byref(hr), ctypes.byref(wr), tp, lp, ep, *g, dhr, dwr,
+                                  ws.data_ptr(), ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _fail("ssd_head_logprob_bwd", st)
+    return dhidden, dweight

@@ -1,0 +1,532 @@
+// ssd_head.cu -- the head's log-probabilities: z = hidden weight^T is formed
+// tile by tile on the tensor cores and never stored; what a row of logits is
+// needed for is taken from the accumulator.  The gradient forms z again, stores
+// dz in bf16 and multiplies it with the weights and with the hidden states.
+//
+// All products run in one kernel: a block (one on each SM) walks over tiles of
+// 128 rows and up to 256 columns.  One warp copies operands by TMA into a ring
+// of stages, one issues the MMAs into one of two accumulators in TMEM, four
+// read the other accumulator meanwhile, a row of the tile a thread.
+#include <cudaTypedefs.h>
+
+#include "ssd_logprob.cuh"
+#include "ssd_status.h"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kGemmThreads = 256;  // warps: copy, MMA, TMEM, -, four for the accumulators
+constexpr uint64_t kWaitNs = 100000000ull;
+
+// What becomes of an accumulator.
+enum Use { kStats, kGrad, kStore };
+
+struct GemmArgs {
+    int M, N, K;          // D[M, N] = A[M, K] B[N, K]^T
+    int bn, mt, nt, kc;   // columns of a tile; tiles; chunks of kBK
+    int group;            // row tiles that are walked together before the next column tile
+    int units, whole, split;  // the first `whole` tiles are a unit each, the others `split` units, a share of K each
+    // kStats, kGrad: rows are tokens, columns the vocabulary
+    const int64_t *targets;
+    float4 *stats;        // [nt][M] (m, sum, moment, 0)
+    float *given;         // [M] the given tokens' logits
+    RowGradIn grad;
+    bf16 *dz;
+    int64_t dz_pitch;
+    // kStore
+    bf16 *out;
+    int64_t out_pitch;
+    float *parts;         // [units - whole][128][bn] of the tiles that are split
+    unsigned *status;
+};
+
+struct Unit {
+    int m, n, k0, k1, part;  // part < 0: a whole tile
+};
+__device__ __forceinline__ Unit unit_of(const GemmArgs &a, int u) {
+    Unit r;
+    int tile = u;
+    r.k0 = 0, r.k1 = a.kc, r.part = -1;
+    if (u >= a.whole) {
+        const int e = u - a.whole, q = e % a.split;
+        tile = a.whole + e / a.split;
+        r.part = e;
+        r.k0 = (int)((int64_t)a.kc * q / a.split), r.k1 = (int)((int64_t)a.kc * (q + 1) / a.split);
+    }
+    const int per = a.group * a.nt, g = tile / per, in = tile % per, gm = min(a.group, a.mt - g * a.group);
+    r.m = g * a.group + in % gm, r.n = in / gm;
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages], ready[2], taken[2], drain;
+    uint32_t tmem;
+    int gave_up;
+};
+// False once any wait of the block has given up.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, Bars *b) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+        if (*reinterpret_cast<volatile int *>(&b->gave_up)) return false;
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            *reinterpret_cast<volatile int *>(&b->gave_up) = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void store16(bf16 *p, const float *v) {
+    uint4 w;
+    w.x = pack_bf16x2(v[0], v[1]), w.y = pack_bf16x2(v[2], v[3]);
+    w.z = pack_bf16x2(v[4], v[5]), w.w = pack_bf16x2(v[6], v[7]);
+    *reinterpret_cast<uint4 *>(p) = w;
+}
+
+// A_MN, B_MN: the operand lies with its rows (M or N) contiguous, in blocks of 64 rows by kBK.
+template <int USE, bool A_MN, bool B_MN, bool ENT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], 4);
+        mbar_init(&bars.drain, 1);
+        bars.gave_up = 0;
+        fence_mbar_init();
+        prefetch_tmap(&ma), prefetch_tmap(&mb);
+    }
+    if (warp == 2) {
+        tmem_alloc(&bars.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    const int bblocks = a.bn / 64;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t bytes = kABytes + a.bn * kBK * 2;
+            uint32_t it = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+                const Unit t = unit_of(a, u);
+                for (int k = t.k0; k < t.k1; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !(ok = wait_for(&bars.empty[s], (it / kStages - 1) & 1, &bars))) break;
+                    uint8_t *sa = smem + s * kStageBytes, *sb = sa + kABytes;
+                    mbar_arrive_expect_tx(&bars.full[s], bytes);
+                    if constexpr (A_MN) {
+                        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * 8192, &ma, &bars.full[s], t.m * kBM + j * 64, k * kBK);
+                    } else {
+                        tma_load_2d(sa, &ma, &bars.full[s], k * kBK, t.m * kBM);
+                    }
+                    if constexpr (B_MN) {
+                        for (int j = 0; j < bblocks; ++j) tma_load_2d(sb + j * 8192, &mb, &bars.full[s], t.n * a.bn + j * 64, k * kBK);
+                    } else {
+                        tma_load_2d(sb, &mb, &bars.full[s], k * kBK, t.n * a.bn);
+                    }
+                }
+            }
+            // no block ends with copies in flight
+            for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, kWaitNs / 5);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(kBM, a.bn, A_MN, B_MN);
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x, ++n) {
+                const Unit t = unit_of(a, u);
+                const uint32_t acc = n & 1, d = tmem + acc * kBN;
+                if (n >= 2 && !(ok = wait_for(&bars.taken[acc], (n / 2 - 1) & 1, &bars))) break;
+                tc_fence_after();
+                for (int k = t.k0; k < t.k1; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = wait_for(&bars.full[s], (it / kStages) & 1, &bars))) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kABytes;
+                    const uint64_t da = A_MN ? sdesc(sa, 8192, 1024) : sdesc(sa, 16, 1024);
+                    const uint64_t db = B_MN ? sdesc(sb, 8192, 1024) : sdesc(sb, 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < kBK / 16; ++j)
+                        mma_bf16(d, desc_add(da, j * (A_MN ? 2048 : 32)), desc_add(db, j * (B_MN ? 2048 : 32)), idesc,
+                                 j > 0 || k > t.k0);
+                    mma_commit(&bars.empty[s]);
+                }
+                if (!ok) break;
+                mma_commit(&bars.ready[acc]);
+            }
+            mma_commit(&bars.drain);  // nor with MMAs
+            mbar_wait(&bars.drain, 0, kWaitNs / 5);
+        }
+    } else if (warp >= 4) {
+        const int q = warp - 4;
+        uint32_t n = 0;
+        for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++n) {
+            const Unit t = unit_of(a, u);
+            const uint32_t acc = n & 1, at = tmem + acc * kBN + ((uint32_t)(q * 32) << 16);
+            const int row = t.m * kBM + q * 32 + lane, c0 = t.n * a.bn;
+            const bool live = row < a.M;
+            int64_t target = -1;
+            Stat st{-INFINITY, 0.f, 0.f};
+            RowGrad g{};
+            if constexpr (USE == kStats) target = live && a.targets ? a.targets[row] - c0 : -1;
+            if constexpr (USE == kGrad) {
+                if (live) g = row_grad(a.grad, row, a.N);
+            }
+            if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
+            tc_fence_after();
+            for (int c = 0; c < a.bn; c += 32) {
+                float z[32];
+                tmem_ld32(at + c, z);
+                tmem_ld_wait();
+                if constexpr (USE == kStats) {
+                    const int limit = min(a.N - c0, a.bn);  // (a tile's columns are a multiple of 16)
+                    if (c + 32 > limit) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= limit) z[i] = -INFINITY;
+                    }
+                    if (target >= c && target < c + 32 && target < limit) {
+                        float v = z[0];
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) v = target == c + i ? z[i] : v;
+                        a.given[row] = v;
+                    }
+                    add_to(st, z);
+                } else if constexpr (USE == kGrad) {
+                    if (live) {
+                        bf16 *p = a.dz + row * a.dz_pitch + c0 + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            z[i] = g.none ? 0.f : grad_of<ENT>(g, z[i]);
+                        }
+                        if (g.target >= c0 + c && g.target < c0 + c + 32 && !g.none) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c0 + c + i == g.target) z[i] += g.dlp;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c0 + c + i < a.dz_pitch) store16(p + i, z + i);
+                    }
+                } else {
+                    if (t.part >= 0) {
+                        float *p = a.parts + ((int64_t)t.part * kBM + q * 32 + lane) * a.bn + c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(p + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+                    } else if (live) {
+                        bf16 *p = a.out + row * a.out_pitch + c0 + c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c0 + c + i < a.N) store16(p + i, z + i);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.taken[acc]);
+            if constexpr (USE == kStats) {
+                if (live) a.stats[(int64_t)t.n * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && bars.gave_up) atomicOr(a.status, 1u);
+    if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// The numbers of every row from its tiles' statistics, joined in the tiles' order by one thread of 8 each, then the eight.
+__global__ void __launch_bounds__(256) head_rows_kernel(const float4 *stats, const float *given, const int64_t *targets, int rows,
+                                                        int nt, int vocab, float *logprob, float *lse, float *entropy) {
+    __shared__ Stat part[8][32];
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32, row = blockIdx.x * 32 + lane;
+    Stat st{-INFINITY, 0.f, 0.f};
+    if (row < rows) {
+        for (int n = w; n < nt; n += 8) {
+            const float4 v = stats[(int64_t)n * rows + row];
+            st = join(st, Stat{v.x, v.y, v.z});
+        }
+    }
+    part[w][lane] = st;
+    __syncthreads();
+    if (w || row >= rows) return;
+    for (int k = 1; k < 8; ++k) st = join(st, part[k][lane]);
+    const float l = lse_of(st);
+    if (lse) lse[row] = l;
+    if (entropy) entropy[row] = entropy_of(st);
+    if (logprob) {
+        const int64_t t = targets[row];
+        logprob[row] = t < 0 ? 0.f : t >= vocab ? __uint_as_float(0x7FC00000u) : logprob_of(given[row], l);
+    }
+}
+
+// The tiles that were split: their parts' sum, in order.
+__global__ void __launch_bounds__(256) head_parts_kernel(const __grid_constant__ GemmArgs a) {
+    const int tile = blockIdx.y;
+    const Unit t = unit_of(a, a.whole + tile * a.split);
+    const int per = a.bn / 8, i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= kBM * per) return;
+    const int r = i / per, c = i % per * 8, row = t.m * kBM + r, col = t.n * a.bn + c;
+    if (row >= a.M || col >= a.N) return;
+    float v[8] = {};
+    for (int k = 0; k < a.split; ++k) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.parts + (((int64_t)tile * a.split + k) * kBM + r) * a.bn + c);
+        const float4 x = p[0], y = p[1];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    store16(a.out + row * a.out_pitch + col, v);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [rows][cols] bf16, boxes of 64 columns and `box` rows, 128-byte swizzle; what lies outside reads as 0.
+bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t pitch, int box) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, str[1] = {(cuuint64_t)pitch * 2};
+    const cuuint32_t b[2] = {64, (cuuint32_t)box}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, str, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSMs = 152;
+
+// Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share.
+GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split) {
+    GemmArgs a{};
+    a.M = (int)M, a.N = (int)N, a.K = (int)K, a.bn = bn;
+    a.mt = (int)((M + kBM - 1) / kBM), a.nt = (int)((N + bn - 1) / bn), a.kc = (int)((K + kBK - 1) / kBK);
+    a.group = 32;
+    const int tiles = a.mt * a.nt;
+    a.whole = tiles, a.split = 1;
+    const int rest = tiles % kSMs;
+    if (split && rest) {
+        int s = kSMs / rest;
+        if (s > a.kc / 4) s = a.kc / 4;  // (a share of fewer chunks is mostly filling the ring)
+        if (s > 1) a.whole = tiles - rest, a.split = s;
+    }
+    a.units = a.whole + (tiles - a.whole) * a.split;
+    return a;
+}
+size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)(a.units - a.whole) * kBM * a.bn); }
+
+int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); }
+
+// Columns of a forward tile.  With one row of tiles the weights' one pass sets the time: the widest of the column counts
+// that leave the fewest columns to the busiest SM.
+int forward_columns(int64_t T, int64_t V) {
+    if (T > kBM) return fit_columns(V);
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 16) {
+        const int64_t tiles = (V + bn - 1) / bn, cost = (tiles + kSMs - 1) / kSMs * bn;
+        if (cost < least) least = cost, best = bn;
+    }
+    return best;
+}
+
+struct HeadPlan {
+    size_t stats, given, dz, parts, bytes;
+    int64_t pitch;
+    GemmArgs z, dh, dw;
+};
+HeadPlan plan_fwd(const ssd_head_shape_t *s) {
+    HeadPlan p{};
+    p.z = plan_gemm(s->rows, s->vocab, s->dim, forward_columns(s->rows, s->vocab), false);
+    p.stats = 0;
+    p.given = align256(sizeof(float4) * p.z.nt * s->rows);
+    p.bytes = p.given + align256(sizeof(float) * s->rows);
+    return p;
+}
+HeadPlan plan_bwd(const ssd_head_shape_t *s) {
+    HeadPlan p{};
+    p.z = plan_gemm(s->rows, s->vocab, s->dim, fit_columns(s->vocab), false);
+    p.dh = plan_gemm(s->rows, s->dim, s->vocab, fit_columns(s->dim), true);
+    p.dw = plan_gemm(s->vocab, s->dim, s->rows, fit_columns(s->dim), true);
+    p.pitch = (s->vocab + 63) / 64 * 64;
+    p.dz = 0;
+    p.parts = align256(2 * s->rows * p.pitch);
+    const size_t a = parts_bytes(p.dh), b = parts_bytes(p.dw);
+    p.bytes = p.parts + (a > b ? a : b);
+    return p;
+}
+
+template <int USE, bool A_MN, bool B_MN, bool ENT>
+cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a, const char *name, cudaStream_t st) {
+    auto kernel = gemm_kernel<USE, A_MN, B_MN, ENT>;
+    // (set on every call: cheap, and right for each device and context)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(a.units < kSMs ? a.units : kSMs), kGemmThreads, kSmem, st>>>(ma, mb, a);
+    timing_mark(st, name);
+    return cudaGetLastError();
+}
+
+cudaError_t run_parts(const GemmArgs &a, cudaStream_t st) {
+    const int tiles = (a.units - a.whole) / a.split;
+    if (a.units == a.whole) return cudaSuccess;
+    head_parts_kernel<<<dim3((unsigned)((kBM * (a.bn / 8) + 255) / 256), (unsigned)tiles), 256, 0, st>>>(a);
+    timing_mark(st, "head_parts");
+    return cudaGetLastError();
+}
+
+ssd_status_t check_head(const ssd_head_shape_t *s) {
+    if (!s || s->rows < 0 || s->dim <= 0 || s->vocab <= 0) return SSD_ERR_INVALID_ARG;
+    if (s->dtype != SSD_DTYPE_F32 && s->dtype != SSD_DTYPE_BF16) return SSD_ERR_INVALID_ARG;
+    if (s->dtype != SSD_DTYPE_BF16 || s->dim % 8 || s->dim > (1 << 20) || s->vocab > (1 << 22) || s->rows > (1 << 22))
+        return SSD_ERR_UNSUPPORTED;
+    // tiles are counted in 31 bits
+    if ((s->rows / kBM + 1) * (s->vocab / 64 + 1) > (1 << 28)) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+// Rows that TMA reads: 16-byte aligned, each of them.
+bool tma_rows(const ssd_rows_t &r, int64_t rows, int64_t dim) {
+    return rows_in_ok(r, 2) && aligned(r.data, 16) && (rows <= 1 || (r.row_stride % 8 == 0 && r.row_stride >= dim));
+}
+int64_t pitch_of(const ssd_rows_t &r, int64_t rows, int64_t dim) { return rows > 1 ? r.row_stride : dim; }
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" {
+
+size_t ssd_head_logprob_workspace_size(const ssd_head_shape_t *shape) {
+    using namespace ssd;
+    return check_head(shape) != SSD_OK || shape->rows == 0 ? 0 : plan_fwd(shape).bytes;
+}
+size_t ssd_head_logprob_bwd_workspace_size(const ssd_head_shape_t *shape) {
+    using namespace ssd;
+    return check_head(shape) != SSD_OK || shape->rows == 0 ? 0 : plan_bwd(shape).bytes;
+}
+
+ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_t *hidden, const ssd_rows_t *weight,
+                                  const int64_t *targets, float *logprob, float *lse, float *entropy, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+    using namespace ssd;
+    const ssd_status_t ok = check_head(shape);
+    if (ok != SSD_OK) return ok;
+    if (shape->rows == 0) return SSD_OK;
+    const int64_t T = shape->rows, V = shape->vocab, D = shape->dim;
+    if (!hidden || !weight || !tma_rows(*hidden, T, D) || !tma_rows(*weight, V, D) || !aligned(targets, 8) || !aligned(logprob, 4) ||
+        !aligned(lse, 4) || !aligned(entropy, 4) || (logprob && !targets))
+        return SSD_ERR_INVALID_ARG;
+    HeadPlan p = plan_fwd(shape);
+    if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    CUtensorMap mh, mw;
+    if (!map_of(&mh, hidden->data, T, D, pitch_of(*hidden, T, D), kBM) ||
+        !map_of(&mw, weight->data, V, D, pitch_of(*weight, V, D), p.z.bn))
+        return SSD_ERR_CUDA;
+    GemmArgs a = p.z;
+    a.targets = logprob ? targets : nullptr;
+    a.stats = reinterpret_cast<float4 *>(ws + p.stats);
+    a.given = reinterpret_cast<float *>(ws + p.given);
+    cudaError_t e = device_status_word(&a.status);
+    if (e != cudaSuccess) return status_of(e);
+    timing_begin(stream);
+    e = run_gemm<kStats, false, false, false>(mh, mw, a, "head_logprob", stream);
+    if (e != cudaSuccess) return status_of(e);
+    head_rows_kernel<<<(unsigned)((T + 31) / 32), 256, 0, stream>>>(a.stats, a.given, a.targets, (int)T, a.nt, (int)V, logprob, lse, entropy);
+    timing_mark(stream, "head_rows");
+    return status_of(cudaGetLastError());
+}
+
+ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_t *hidden, const ssd_rows_t *weight,
+                                  const int64_t *targets, const float *lse, const float *entropy, const float *dlogprob,
+                                  const float *dlse, const float *dentropy, const ssd_rows_t *dhidden, const ssd_rows_t *dweight,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    using namespace ssd;
+    const ssd_status_t ok = check_head(shape);
+    if (ok != SSD_OK) return ok;
+    const int64_t T = shape->rows, V = shape->vocab, D = shape->dim;
+    if (dweight && (!tma_rows(*dweight, V, D) || !rows_out_ok(*dweight, 2, 1, V, D))) return SSD_ERR_INVALID_ARG;
+    if (T == 0) {
+        if (!dweight) return SSD_OK;
+        return status_of(cudaMemset2DAsync(dweight->data, pitch_of(*dweight, V, D) * 2, 0, D * 2, V, stream));
+    }
+    if (!hidden || !weight || !tma_rows(*hidden, T, D) || !tma_rows(*weight, V, D) || !lse || !aligned(lse, 4) || !aligned(entropy, 4) ||
+        !aligned(targets, 8) || !aligned(dlogprob, 4) || !aligned(dlse, 4) || !aligned(dentropy, 4) || (dlogprob && !targets) ||
+        (dentropy && !entropy))
+        return SSD_ERR_INVALID_ARG;
+    if (dhidden && (!tma_rows(*dhidden, T, D) || !rows_out_ok(*dhidden, 2, 1, T, D))) return SSD_ERR_INVALID_ARG;
+    if (!dhidden && !dweight) return SSD_OK;
+    HeadPlan p = plan_bwd(shape);
+    if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    bf16 *dz = reinterpret_cast<bf16 *>(ws + p.dz);
+    const int64_t hp = pitch_of(*hidden, T, D), wp = pitch_of(*weight, V, D);
+    CUtensorMap mh, mw, mz, mz_t, mw_t, mh_t;
+    // dz: only its V columns are read, whatever lies behind them
+    if (!map_of(&mh, hidden->data, T, D, hp, kBM) || !map_of(&mw, weight->data, V, D, wp, p.z.bn) ||
+        !map_of(&mz, dz, T, V, p.pitch, kBM) || !map_of(&mw_t, weight->data, V, D, wp, kBK) ||
+        !map_of(&mz_t, dz, T, V, p.pitch, kBK) || !map_of(&mh_t, hidden->data, T, D, hp, kBK))
+        return SSD_ERR_CUDA;
+    unsigned *status = nullptr;
+    cudaError_t e = device_status_word(&status);
+    if (e != cudaSuccess) return status_of(e);
+    timing_begin(stream);
+    GemmArgs a = p.z;
+    a.status = status;
+    a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
+    a.dz = dz, a.dz_pitch = p.pitch;
+    e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, a, "head_dlogits", stream)
+                 : run_gemm<kGrad, false, false, false>(mh, mw, a, "head_dlogits", stream);
+    if (e == cudaSuccess && dhidden) {
+        GemmArgs b = p.dh;
+        b.status = status;
+        b.out = static_cast<bf16 *>(dhidden->data), b.out_pitch = pitch_of(*dhidden, T, D);
+        b.parts = reinterpret_cast<float *>(ws + p.parts);
+        e = run_gemm<kStore, false, true, false>(mz, mw_t, b, "head_dhidden", stream);
+        if (e == cudaSuccess) e = run_parts(b, stream);
+    }
+    if (e == cudaSuccess && dweight) {
+        GemmArgs b = p.dw;
+        b.status = status;
+        b.out = static_cast<bf16 *>(dweight->data), b.out_pitch = pitch_of(*dweight, V, D);
+        b.parts = reinterpret_cast<float *>(ws + p.parts);
+        e = run_gemm<kStore, true, true, false>(mz_t, mh_t, b, "head_dweight", stream);
+        if (e == cudaSuccess) e = run_parts(b, stream);
+    }
+    return status_of(e);
+}
+
+}  // extern "C"
