@@ -6,10 +6,10 @@
 //   sum = sum e^(z - m)  and  moment = sum e^(z - m) (z - m) log2(e),
 // rescaled where m grows; from the joined ones
 //   lse = m + log(sum),  entropy = log(sum) - ln 2 moment / sum.
-// Alternatives: of the threads' maxima the k-th largest, tau, is not above the
-// k-th largest element, and fewer than k threads hold anything above it, so
-// only the few threads whose maximum reaches tau look through their elements
-// again, and what reaches tau is ranked by (value, lowest index).
+// Alternatives: the k-th largest of the maxima of groups of threads, tau, is
+// not above the k-th largest element.  Only what the few threads hold whose
+// maximum reaches tau is looked through again, and what reaches tau is ranked
+// by (value, lowest index).
 #include <cooperative_groups.h>
 
 #include "ssd_logprob.cuh"
@@ -19,7 +19,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+// A row is 100 KB: a block spends as long on joining its threads' statistics
+// and on the alternatives as on loads, so small blocks, many of them, keep
+// memory busy (forward and gradient of 8192 x 50280 bf16 / five alternatives of
+// 2047 x 65537: eight blocks of 256 an SM 399 / 60 us, six 408 / 65, three of
+// 512 419 / 70, two of 512 449 / 77, one of 1024 580 / 115).
+constexpr int kThreads = 256, kBlocks = 8;
+constexpr int kLoads = 4;  // in flight a thread (2: 404 / 58 us, 1: 438 / 71)
 constexpr int kMaxTop = SSD_LOGPROB_MAX_TOP;
 constexpr int kFound = 1024;  // candidates kept: above tau
 constexpr int kSame = 512;    // and equal to it
@@ -86,12 +92,19 @@ __device__ __forceinline__ unsigned long long entry_of(float v, int index) {
     return (unsigned long long)key_of(v) << 32 | (0xFFFFFFFFu - (unsigned)index);
 }
 
+// Of which maxima tau is found: those of groups of lanes, as few as leave k of them with room to spare (the more groups,
+// the fewer elements reach tau: about n log(n / (n - k)) of n groups; the fewer, the shorter the search for it).
+constexpr int kFewGroups = 16, kManyGroups = 128;
+constexpr int kFewTop = kFewGroups / 2;
+static_assert(kMaxTop <= kManyGroups / 2, "");
+
 struct TopShared {
-    unsigned maxima[kThreads];
+    unsigned maxima[kManyGroups];
     unsigned long long found[kFound + kSame];
     unsigned long long best[kMaxTop];  // sorted
+    short threads[kThreads];
     unsigned tau;
-    int above, equal, warps[kThreads / 32];
+    int above, equal, holders, warps[kThreads / 32];
 };
 
 // The k largest of the `n` entries, sorted, to best: each entry's rank is counted.
@@ -103,45 +116,71 @@ __device__ __forceinline__ void rank(const unsigned long long *e, int n, int k, 
     }
 }
 
+// The largest key that k of a warp's values reach, bit by bit; the lower half of a bf16 value's key is zeros, a
+// negative one's ones.
+template <typename T, int N>
+__device__ __forceinline__ unsigned reached_by(const unsigned (&v)[N], int k) {
+    unsigned tau = 0;
+    for (int bit = 31; bit >= (sizeof(T) == 2 ? 16 : 0); --bit) {
+        const unsigned want = tau | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) n += v[i] >= want;
+        if ((int)__reduce_add_sync(0xffffffffu, n) >= k) tau = want;
+    }
+    return sizeof(T) == 2 && !(tau & 0x80000000u) ? tau | 0xFFFFu : tau;
+}
+
 // The part's k largest elements, sorted, in t.best (fewer elements: zeros, below every entry).  m: this thread's maximum.
 template <typename T>
 __device__ void top_of_part(const Slots<T> &s, float m, bool any, int k, TopShared &t) {
     constexpr int V = Slots<T>::V;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const unsigned mine = any ? key_of(m) : 0;
-    t.maxima[tid] = mine;
+    const int wide = k <= kFewTop ? kThreads / kFewGroups : kThreads / kManyGroups;  // threads of a group
+    unsigned g = mine;
+    for (int d = 1; d < wide; d *= 2) g = max(g, __shfl_xor_sync(0xffffffffu, g, d));
+    if (tid % wide == 0) t.maxima[tid / wide] = g;
     if (tid < k) t.best[tid] = 0;
-    if (tid == 0) t.above = t.equal = 0;
+    if (tid == 0) t.above = t.equal = t.holders = 0;
     __syncthreads();
-    if (warp == 0) {  // tau, the largest key that k maxima reach, bit by bit
-        unsigned v[kThreads / 32], tau = 0;
+    if (warp == 0) {
+        unsigned tau;
+        if (k <= kFewTop) {
+            const unsigned v[1] = {lane < kFewGroups ? t.maxima[lane] : 0};
+            tau = reached_by<T>(v, k);
+        } else {
+            unsigned v[kManyGroups / 32];
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) v[i] = t.maxima[i * 32 + lane];
-        for (int bit = 31; bit >= 0; --bit) {
-            const unsigned want = tau | 1u << bit;
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) n += v[i] >= want;
-            if ((int)__reduce_add_sync(0xffffffffu, n) >= k) tau = want;
+            for (int i = 0; i < kManyGroups / 32; ++i) v[i] = t.maxima[i * 32 + lane];
+            tau = reached_by<T>(v, k);
         }
         if (lane == 0) t.tau = tau;
     }
     __syncthreads();
     const unsigned tau = t.tau;
+    auto look = [&](int i, float z) {
+        const unsigned key = key_of(z);
+        if (key < tau) return;
+        if (key == tau) {
+            const int at = atomicAdd(&t.equal, 1);
+            if (at < kSame) t.found[kFound + at] = entry_of(z, i);
+            return;
+        }
+        const int at = atomicAdd(&t.above, 1);
+        if (at < kFound) t.found[at] = entry_of(z, i);
+    };
+    // The threads that hold something of tau or above; all threads share their slots.
     if (any && mine >= tau) {
-        auto look = [&](int i, float z) {
-            const unsigned key = key_of(z);
-            if (key < tau) return;
-            if (key == tau) {
-                const int at = atomicAdd(&t.equal, 1);
-                if (at < kSame) t.found[kFound + at] = entry_of(z, i);
-                return;
-            }
-            const int at = atomicAdd(&t.above, 1);
-            if (at < kFound) t.found[at] = entry_of(z, i);
-        };
+        t.threads[atomicAdd(&t.holders, 1)] = (short)tid;
         s.cut(tid, look);
-        for (int j = s.full0 + tid; j < s.full1; j += kThreads) {
+    }
+    __syncthreads();
+    {
+        const int each = (s.full1 - s.full0 + kThreads - 1) / kThreads, n = t.holders * each;
+        for (int q = tid; q < n; q += kThreads) {
+            const int j = s.full0 + t.threads[q / each] + q % each * kThreads;
+            if (j >= s.full1) continue;
             float z[V];
             widen<T, V>(s.load(j), z);
 #pragma unroll
@@ -231,8 +270,23 @@ __device__ void top_of_part(const Slots<T> &s, float m, bool any, int k, TopShar
     __syncthreads();
 }
 
+template <int U>
+__device__ __forceinline__ void add_vecs(Stat &st, const Vec<bf16, 8> (&v)[U]) {
+    uint32_t w[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[4 * u] = v[u].r.x, w[4 * u + 1] = v[u].r.y, w[4 * u + 2] = v[u].r.z, w[4 * u + 3] = v[u].r.w;
+    add_to(st, w);
+}
+template <int U>
+__device__ __forceinline__ void add_vecs(Stat &st, const Vec<float, 4> (&v)[U]) {
+    float z[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) z[4 * u] = v[u].r.x, z[4 * u + 1] = v[u].r.y, z[4 * u + 2] = v[u].r.z, z[4 * u + 3] = v[u].r.w;
+    add_to(st, z);
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_constant__ LogprobArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) logprob_fwd_kernel(const __grid_constant__ LogprobArgs<T> a) {
     constexpr int V = Slots<T>::V;
     __shared__ Stat stats[kThreads / 32], joined;
     __shared__ std::conditional_t<TOP, TopShared, char> top;
@@ -248,37 +302,25 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_c
         add_to(st, one);
         any = true;
     });
-    constexpr int U = 4;  // loads in flight
+    constexpr int U = kLoads;
     int j = s.full0 + tid;
     for (; j + (U - 1) * kThreads < s.full1; j += U * kThreads) {
         Vec<T, V> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = s.load(j + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float z[V];
-            widen<T, V>(v[u], z);
-            add_to(st, z);
-        }
+        add_vecs(st, v);
     }
     for (; j < s.full1; j += kThreads) {
-        float z[V];
-        widen<T, V>(s.load(j), z);
-        add_to(st, z);
+        const Vec<T, V> v[1] = {s.load(j)};
+        add_vecs(st, v);
     }
     const float mine = st.m;
-    for (int d = 16; d; d /= 2) {
-        Stat o;
-        o.m = __shfl_xor_sync(0xffffffffu, st.m, d);
-        o.sum = __shfl_xor_sync(0xffffffffu, st.sum, d);
-        o.moment = __shfl_xor_sync(0xffffffffu, st.moment, d);
-        st = lane & d ? join(o, st) : join(st, o);  // (one order in both lanes)
-    }
+    st = join_lanes<32>(st);
     if (lane == 0) stats[warp] = st;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) st = join(st, stats[w]);
-        joined = st;
+    if (warp == 0) {
+        st = join_lanes<kThreads / 32>(stats[lane % (kThreads / 32)]);
+        if (tid == 0) joined = st;
     }
     if constexpr (TOP) top_of_part(s, mine, any, a.top, top);
 

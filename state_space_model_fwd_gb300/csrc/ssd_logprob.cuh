@@ -13,66 +13,131 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// What is known of a set of logits: the largest, m, and over all z
+//   sum = sum 2^t,  moment = sum 2^t t,  t = z log2(e) - ref(m).
+// t is one fused multiply-add: ref(m) is m log2(e) rounded, and what it was
+// rounded by comes back in lse_of.  Entropies do not depend on the reference.
+// Far from zero, where the rounding would not be small, t = (z - m) log2(e).
 struct Stat {
     float m, sum, moment;
 };
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
-// Exponents below this add nothing in fp32; clamping keeps minus infinity out of the moment.
-constexpr float kNothing = -200.f;
-// Of two disjoint sets.
-__device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
-    const float m = max_nan(a.m, b.m), base = base_of(m);
-    Stat r{m, 0.f, 0.f};
-    if (a.sum > 0.f) {
-        const float d = fmaxf((a.m - base) * kLog2e, kNothing), f = ex2(d);
-        r.sum = f * a.sum, r.moment = f * fmaf(d, a.sum, a.moment);
+constexpr float kFar = 65536.f;
+__device__ __forceinline__ bool is_far(float m) { return !(fabsf(m) <= kFar); }
+// A z below kLeast counts as kLeast, an exponent below kNothing as kNothing: they add nothing in fp32, and minus infinity
+// stays out of the moment.
+constexpr float kLeast = -1e38f, kNothing = -200.f;
+// (Not contracted with what uses it: the same m has to give the same reference.)
+__device__ __forceinline__ float ref_of(float m) { return __fmul_rn(m, kLog2e); }
+// What t of a set with the maximum m0 changes by when m takes its place.
+__device__ __forceinline__ float shift_of(float m0, float m) {
+    if (m0 == m) return 0.f;
+    float d;
+    if (is_far(m))
+        d = is_far(m0) ? (m0 - m) * kLog2e : fmaf(-m, kLog2e, ref_of(m0));
+    else
+        d = is_far(m0) ? fmaf(m0, kLog2e, -ref_of(m)) : ref_of(m0) - ref_of(m);
+    return fmaxf(d, kNothing);
+}
+__device__ __forceinline__ void move_to(Stat &s, float m) {
+    const float d = shift_of(s.m, m), f = ex2(d);
+    s.moment = f * fmaf(d, s.sum, s.moment), s.sum *= f, s.m = m;
+}
+// Of two disjoint sets; an empty one has sum 0 and m = -inf.
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+    const float m = max_nan(a.m, b.m);
+    move_to(a, m), move_to(b, m);
+    return Stat{m, a.sum + b.sum, a.moment + b.moment};
+}
+// Of the 32 (or, 16 lanes wide, 16) sets of a warp's lanes, in all lanes; one order of additions.
+template <int WIDTH>
+__device__ __forceinline__ Stat join_lanes(Stat s) {
+    float m = s.m;
+#pragma unroll
+    for (int d = WIDTH / 2; d; d /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d, WIDTH));
+    move_to(s, m);
+#pragma unroll
+    for (int d = WIDTH / 2; d; d /= 2) {
+        s.sum += __shfl_xor_sync(0xffffffffu, s.sum, d, WIDTH);
+        s.moment += __shfl_xor_sync(0xffffffffu, s.moment, d, WIDTH);
     }
-    if (b.sum > 0.f) {
-        const float d = fmaxf((b.m - base) * kLog2e, kNothing), f = ex2(d);
-        r.sum += f * b.sum, r.moment += f * fmaf(d, b.sum, b.moment);
-    }
-    return r;
+    return s;
 }
 
+// N more logits whose maximum is m.
 template <int N>
-__device__ __forceinline__ void add_to(Stat &s, const float (&z)[N]) {
-    float m = z[0];
+__device__ __forceinline__ void add_to(Stat &s, const float (&z)[N], float m) {
+    if (!(m <= s.m)) move_to(s, max_nan(s.m, m));  // (or NaN)
+    if (is_far(s.m)) {
+        if (s.m == -INFINITY) return;
 #pragma unroll
-    for (int i = 1; i < N; ++i) m = max_nan(m, z[i]);
-    if (!(m <= s.m)) {  // (or NaN)
-        const float top = max_nan(s.m, m);
-        if (s.sum > 0.f) {
-            const float d = fmaxf((s.m - top) * kLog2e, kNothing), f = ex2(d);
-            s.moment = f * fmaf(d, s.sum, s.moment), s.sum *= f;
+        for (int i = 0; i < N; ++i) {
+            const float t = fmaxf((z[i] - s.m) * kLog2e, kNothing), e = ex2(t);
+            s.sum += e, s.moment = fmaf(e, t, s.moment);
         }
-        s.m = top;
+        return;
     }
-    const float base = base_of(s.m);
-    f2 sum = pack2(s.sum, 0.f), moment = pack2(s.moment, 0.f);
-    const f2 minus = pack2(-base, -base), scale = pack2(kLog2e, kLog2e);
+    const float ref = -ref_of(s.m);
     if constexpr (N % 2 == 0) {
+        f2 sum = pack2(s.sum, 0.f), moment = pack2(s.moment, 0.f);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            float t0, t1;
-            unpack2(mul2(add2(pack2(z[i], z[i + 1]), minus), scale), t0, t1);
-            t0 = fmaxf(t0, kNothing), t1 = fmaxf(t1, kNothing);
-            const f2 e = pack2(ex2(t0), ex2(t1));
+            const f2 t = fma2(pack2(fmaxf(z[i], kLeast), fmaxf(z[i + 1], kLeast)), pack2(kLog2e, kLog2e), pack2(ref, ref));
+            const f2 e = ex2x2(t);
             sum = add2(sum, e);
-            moment = fma2(e, pack2(t0, t1), moment);
+            moment = fma2(e, t, moment);
         }
         s.sum = sum2(sum), s.moment = sum2(moment);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float t = fmaxf((z[i] - base) * kLog2e, kNothing), e = ex2(t);
+            const float t = fmaf(fmaxf(z[i], kLeast), kLog2e, ref), e = ex2(t);
             s.sum += e, s.moment = fmaf(e, t, s.moment);
         }
     }
 }
+template <int N>
+__device__ __forceinline__ void add_to(Stat &s, const float (&z)[N]) {
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = max_nan(m, z[i]);
+    add_to(s, z, m);
+}
+// The same for pairs of bf16 as they lie in memory: the maximum and the clamp work on two at once.
+template <int NW>
+__device__ __forceinline__ void add_to(Stat &s, const uint32_t (&w)[NW]) {
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(w);
+    __nv_bfloat162 top = p[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) top = __hmax2_nan(top, p[i]);
+    const float m = max_nan(__low2float(top), __high2float(top));
+    if (!(m <= s.m)) move_to(s, max_nan(s.m, m));
+    if (is_far(s.m)) {
+        float z[2 * NW];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) z[2 * i] = __low2float(p[i]), z[2 * i + 1] = __high2float(p[i]);
+        add_to(s, z, m);
+        return;
+    }
+    const float ref = -ref_of(s.m);
+    const __nv_bfloat162 least = __float2bfloat162_rn(kLeast);
+    f2 sum = pack2(s.sum, 0.f), moment = pack2(s.moment, 0.f);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const __nv_bfloat162 c = __hmax2_nan(p[i], least);
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(&c);
+        const f2 z = pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        const f2 t = fma2(z, pack2(kLog2e, kLog2e), pack2(ref, ref)), e = ex2x2(t);
+        sum = add2(sum, e);
+        moment = fma2(e, t, moment);
+    }
+    s.sum = sum2(sum), s.moment = sum2(moment);
+}
 
 // The numbers of a row from its joined statistics and the given token's logit.
 __device__ __forceinline__ float lse_of(const Stat &s) {
-    return s.m == -INFINITY || s.m == INFINITY ? s.m : s.m + logf(s.sum);
+    if (s.m == -INFINITY || s.m == INFINITY) return s.m;
+    const float off = !is_far(s.m) ? fmaf(s.m, kLog2e, -ref_of(s.m)) : 0.f;
+    return s.m + (logf(s.sum) - kLn2 * off);
 }
 // nothing left in the row: 0; infinity or NaN in it: NaN
 __device__ __forceinline__ float entropy_of(const Stat &s) {
