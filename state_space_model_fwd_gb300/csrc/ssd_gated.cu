@@ -8,62 +8,118 @@ namespace {
 
 constexpr int kWarps = 8;  // of a tile; fewer where a row has fewer tokens
 constexpr int S = 16;      // tokens a warp
+constexpr int kBlocks = 2;  // an SM
+
+// What a warp knows of its tokens.
+template <typename T, bool PAIRS>
+struct Warp {
+    Lane<PAIRS> k;
+    int b, t0, L;
+    Cuts cut;
+    f2 rate;
+    __device__ __forceinline__ float2 init_of(const GatedArgs<T> &a, int s) const {
+        return load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch : nullptr, k);
+    }
+};
+
+// The tokens' decays and inputs, and the run they make.  PLAIN: S tokens of one sequence that neither begins nor ends among
+// them, decays with m <= 1.
+template <typename T, bool PAIRS, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, f2 (&av)[S], f2 (&uv)[S], f2 &A, f2 &H) {
+    Two<T> x[S], r[S], g[S];
+    const T *px = a.x.at(w.b, w.t0), *pr = a.r.at(w.b, w.t0), *pi = a.i.p ? a.i.at(w.b, w.t0) : nullptr;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        // past the end, and in channels that are none: a = 1 and nothing enters
+        r[s] = two_of(T(), -30000.f), x[s] = two_of(T(), 0.f), g[s] = two_of(T(), 128.f);
+        if (PLAIN || w.t0 + s < w.L) {
+            r[s] = load_two<T, PAIRS>(pr + a.r.step(s), w.k, -30000.f);
+            x[s] = load_two<T, PAIRS>(px + a.x.step(s), w.k, 0.f);
+            if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(s), w.k, 128.f);  // without it s(i) = s(128) = 1
+        }
+    }
+    A = splat(1.f), H = splat(0.f);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        f2 v;
+        decay2<PLAIN>(mul2(w.rate, both(sigmoid2(widen(r[s])))), v, av[s]);
+        const float2 b2 = apart(fma2(v, av[s], v));
+        const f2 beta = pack2(sqrt_approx(b2.x), sqrt_approx(b2.y));
+        uv[s] = mul2(mul2(beta, both(sigmoid2(widen(g[s])))), both(widen(x[s])));
+        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) H = both(w.init_of(a, s));
+        A = mul2(A, av[s]);
+        H = fma2(av[s], H, uv[s]);
+    }
+    if (PACKED && !PLAIN && w.cut.first) A = splat(-1.f);
+}
+
+// The outputs, from the state that enters.
+template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const f2 (&av)[S], const f2 (&uv)[S],
+                                             const Two<T> (&z)[S], f2 hv) {
+    T *py = a.y.at(w.b, w.t0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (!PLAIN && w.t0 + s >= w.L) break;
+        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) hv = both(w.init_of(a, s));
+        hv = fma2(av[s], hv, uv[s]);
+        f2 o = hv;
+        if constexpr (GATE) {
+            const float2 zf = widen(z[s]);
+            o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
+        }
+        store_two<T, PAIRS>(py + a.y.step(s), w.k, apart(o));
+        if (!PLAIN && (w.cut.last >> s & 1) && a.fin) {
+            const int q = PACKED ? seq_from(a.seqs, w.cut.seq, w.t0 + s) : w.b;
+            store_state(a.fin + (int64_t)q * a.ch, w.k, apart(hv));
+        }
+    }
+}
 
 template <typename T, bool PAIRS, bool GATE, bool PACKED>
-__global__ void __launch_bounds__(kWarps * 32, 2) gated_fwd_kernel(const __grid_constant__ GatedArgs<T> a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const __grid_constant__ GatedArgs<T> a) {
     __shared__ float4 runs[kWarps][32];
     __shared__ float4 tiles[kGroup][32];
     __shared__ float2 enter[32];
     __shared__ unsigned ticket;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32;
     unsigned n = blockIdx.x;
     if (a.links.run) {
         if (threadIdx.x == 0) ticket = atomicAdd(a.links.ticket, 1u) + 1u;  // (it starts at -1)
         __syncthreads();
-        n = ticket;
+        n = (unsigned)uniform((int)ticket);
     }
-    const int rows = a.nblk * a.batch, tile = n / rows, row = n % rows, b = row / a.nblk;
-    const Lane<PAIRS> k(row % a.nblk, lane, a.ch);
-    const int L = a.seqs.L, t0 = (tile * nw + warp) * S;
-
-    Two<T> x[S], r[S], g[S];
-    {
-        const T *px = a.x.at(b, 0) + k.c0, *pr = a.r.at(b, 0) + k.c0, *pi = a.i.p ? a.i.at(b, 0) + k.c0 : nullptr;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            // past the end, and in channels that are none: a = 1 and nothing enters
-            x[s] = two_of(T(), 0.f), r[s] = two_of(T(), -30000.f), g[s] = two_of(T(), 128.f);
-            if (t0 + s < L) {
-                x[s] = load_two<T, PAIRS>(px + a.x.step(t0 + s), k, 0.f);
-                r[s] = load_two<T, PAIRS>(pr + a.r.step(t0 + s), k, -30000.f);
-                if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(t0 + s), k, 128.f);  // without it s(i) = s(128) = 1
-            }
+    const int rows = a.nblk * a.batch, tile = n / rows, row = n % rows, b = row / a.nblk, L = a.seqs.L;
+    Warp<T, PAIRS> w{Lane<PAIRS>(row % a.nblk, lane, a.ch), b, (tile * nw + warp) * S, L, Cuts{0, 0, b}, 0};
+    const Lane<PAIRS> &k = w.k;
+    if (w.t0 < L) {
+        if constexpr (PACKED) {
+            w.cut = cuts_of<S>(a.seqs, w.t0);
+            w.cut.first = (unsigned)uniform((int)w.cut.first), w.cut.last = (unsigned)uniform((int)w.cut.last);
+            w.cut.seq = uniform(w.cut.seq);
+        } else if (w.t0 + S >= L) {
+            w.cut.last = 1u << (L - 1 - w.t0);
         }
     }
-    Cuts cut{0, 0, b};
-    if (t0 < L) {
-        if constexpr (PACKED)
-            cut = cuts_of<S>(a.seqs, t0);
-        else if (t0 + S >= L)
-            cut.last = 1u << (L - 1 - t0);
-    }
     const float2 dec = load_state(a.decay, k);
-    const f2 rate = pack2(decay_rate(dec.x, a.rate), decay_rate(dec.y, a.rate));
+    const float ra = decay_rate(dec.x, a.rate), rb = decay_rate(dec.y, a.rate);
+    w.rate = pack2(ra, rb);
+    const bool plain = w.t0 + S <= L && !(w.cut.first | w.cut.last) && __all_sync(0xffffffffu, (ra <= 1.f || !k.in0) && (rb <= 1.f || !k.in1));
 
-    f2 av[S], uv[S], A = splat(1.f), H = splat(0.f);
+    f2 av[S], uv[S], A, H;
+    if (plain)
+        run_tokens<T, PAIRS, PACKED, true>(a, w, av, uv, A, H);
+    else
+        run_tokens<T, PAIRS, PACKED, false>(a, w, av, uv, A, H);
+    Two<T> z[S];  // (in flight while the tiles exchange their runs)
+    if constexpr (GATE) {
+        const T *pz = a.z.at(b, w.t0);
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const f2 l = mul2(rate, both(sigmoid2(widen(r[s]))));
-        f2 v;
-        decay2(l, v, av[s]);
-        const float2 w = apart(mul2(v, fma2(v, splat(-1.f), splat(2.f))));
-        const f2 beta = pack2(sqrt_approx(w.x), sqrt_approx(w.y));
-        uv[s] = mul2(mul2(beta, both(sigmoid2(widen(g[s])))), both(widen(x[s])));
-        if (PACKED && (cut.first >> s & 1)) H = both(load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch : nullptr, k));
-        A = mul2(A, av[s]);
-        H = fma2(av[s], H, uv[s]);
+        for (int s = 0; s < S; ++s) {
+            z[s] = two_of(T(), 0.f);
+            if (a.y.p && w.t0 + s < L) z[s] = load_two<T, PAIRS>(pz + a.z.step(s), k, 0.f);
+        }
     }
-    if (PACKED && cut.first) A = splat(-1.f);
     if (nw > 1) {
         const float2 fa = apart(A), fh = apart(H);
         runs[warp][lane] = make_float4(fa.x, fa.y, fh.x, fh.y);
@@ -81,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gated_fwd_kernel(const __grid_
         Run all{};
         if (warp == 0) {
             all = run_of(runs[0][lane]);
-            for (int w = 1; w < nw; ++w) all = then(all, run_of(runs[w][lane]));
+            for (int j = 1; j < nw; ++j) all = then(all, run_of(runs[j][lane]));
             if (in_group != kGroup - 1 && tile + 1 < a.ntile) link_store(mine, all);
         }
         for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
@@ -99,37 +155,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gated_fwd_kernel(const __grid_
         __syncthreads();
         h = enter[lane];
     }
-    for (int w = 0; w < warp; ++w) h = through(run_of(runs[w][lane]), h);
-    if (a.keep && t0 % kStateEvery == 0 && t0 < L) store_state(a.keep + ((int64_t)b * a.nkeep + t0 / kStateEvery) * a.ch, k, h);
+    for (int j = 0; j < warp; ++j) h = through(run_of(runs[j][lane]), h);
+    if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
+        store_state(a.keep + ((int64_t)b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
     if (!a.y.p) return;
-
-    T *py = a.y.at(b, 0) + k.c0;
-    const T *pz = GATE ? a.z.at(b, 0) + k.c0 : nullptr;
-    f2 hv = both(h);
-    Two<T> z[S];
-    if constexpr (GATE) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (t0 + s < L) z[s] = load_two<T, PAIRS>(pz + a.z.step(t0 + s), k, 0.f);
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        if (t0 + s < L) {
-            if (PACKED && (cut.first >> s & 1))
-                hv = both(load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch : nullptr, k));
-            hv = fma2(av[s], hv, uv[s]);
-            f2 o = hv;
-            if constexpr (GATE) {
-                const float2 zf = widen(z[s]);
-                o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
-            }
-            store_two<T, PAIRS>(py + a.y.step(t0 + s), k, apart(o));
-            if ((cut.last >> s & 1) && a.fin) {
-                const int q = PACKED ? seq_from(a.seqs, cut.seq, t0 + s) : b;
-                store_state(a.fin + (int64_t)q * a.ch, k, apart(hv));
-            }
-        }
-    }
+    if (plain)
+        write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, av, uv, z, both(h));
+    else
+        write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, av, uv, z, both(h));
 }
 
 __global__ void __launch_bounds__(256) gated_empty_kernel(const __grid_constant__ Seqs q, int64_t ch, const float *src, float *dst) {
@@ -146,16 +179,15 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
     const Lane<PAIRS> k(n % a.nblk, threadIdx.x % 32, a.ch);
     const int b = n / a.nblk;
     if (b >= a.batch) return;
-    const Two<T> x = load_two<T, PAIRS>(a.x.at(b, 0) + k.c0, k, 0.f), r = load_two<T, PAIRS>(a.r.at(b, 0) + k.c0, k, 0.f);
-    const Two<T> g = a.i.p ? load_two<T, PAIRS>(a.i.at(b, 0) + k.c0, k, 0.f) : two_of(T(), 128.f);
-    const Two<T> z = a.z.p ? load_two<T, PAIRS>(a.z.at(b, 0) + k.c0, k, 0.f) : two_of(T(), 0.f);
+    const Two<T> x = load_two<T, PAIRS>(a.x.at(b, 0), k, 0.f), r = load_two<T, PAIRS>(a.r.at(b, 0), k, 0.f);
+    const Two<T> g = a.i.p ? load_two<T, PAIRS>(a.i.at(b, 0), k, 0.f) : two_of(T(), 128.f);
+    const Two<T> z = a.z.p ? load_two<T, PAIRS>(a.z.at(b, 0), k, 0.f) : two_of(T(), 0.f);
     float *h = state + (int64_t)b * a.ch;
     const f2 old = both(load_state(h, k));
     const float2 dec = load_state(a.decay, k);
-    const f2 l = mul2(pack2(decay_rate(dec.x, a.rate), decay_rate(dec.y, a.rate)), both(sigmoid2(widen(r))));
     f2 v, av;
-    decay2(l, v, av);
-    const float2 w = apart(mul2(v, fma2(v, splat(-1.f), splat(2.f))));
+    decay2<false>(mul2(pack2(decay_rate(dec.x, a.rate), decay_rate(dec.y, a.rate)), both(sigmoid2(widen(r)))), v, av);
+    const float2 w = apart(fma2(v, av, v));
     const f2 u = mul2(mul2(pack2(sqrt_approx(w.x), sqrt_approx(w.y)), both(sigmoid2(widen(g)))), both(widen(x)));
     const f2 now = fma2(av, old, u);
     store_state(h, k, apart(now));
@@ -164,7 +196,7 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
         const float2 zf = widen(z);
         o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
     }
-    store_two<T, PAIRS>(a.y.at(b, 0) + k.c0, k, apart(o));
+    store_two<T, PAIRS>(a.y.at(b, 0), k, apart(o));
 }
 
 int64_t fwd_tokens(int64_t L) {  // of a tile

@@ -1,9 +1,9 @@
 // ssd_gated.cuh -- pieces shared by the gated scan's kernels.
 //
 // Per channel, with s(v) = 1 / (1 + exp(-v)):
-//   l = -rate softplus(decay) s(r),  a = exp(l),  beta = sqrt(1 - a^2),
+//   m = rate softplus(decay) s(r),  a = exp(-m),  beta = sqrt(1 - a^2),
 //   h <- a h + beta s(i) x,  y = h (times silu(z)).
-// Everything is formed from v = 1 - a = -expm1(l): 1 - a^2 = v (2 - v) keeps
+// Everything is formed from v = 1 - a = -expm1(-m): 1 - a^2 = v + v a keeps
 // its digits where a is close to 1, which is where such layers work.
 //
 // A block of the prompt's kernels is a tile: kCols channels, two a lane, and
@@ -50,18 +50,26 @@ __device__ __forceinline__ float2 widen(const Two<float> &v) { return v.w; }
 // one element at a time, 32 neighbours a warp.
 template <bool PAIRS>
 struct Lane {
-    int64_t c0;
+    int c0;
     int step;       // from c0 to the second channel
     bool in0, in1;  // which exist
     __device__ __forceinline__ Lane(int blk, int lane, int ch) {
-        c0 = (int64_t)blk * kCols + (PAIRS ? 2 * lane : lane);
+        c0 = blk * kCols + (PAIRS ? 2 * lane : lane);
         step = PAIRS ? 1 : 32;
         in0 = c0 < ch, in1 = c0 + step < ch;
     }
 };
 
+// The lane's place in a row.  Rows are the same in all lanes and lanes keep one 32-bit offset: an access needs no
+// arithmetic of its own.
+template <typename P, bool PAIRS>
+__device__ __forceinline__ P *place(P *row, const Lane<PAIRS> &k) {
+    using B = std::conditional_t<std::is_const_v<P>, const char, char>;
+    return reinterpret_cast<P *>(reinterpret_cast<B *>(row) + (size_t)((unsigned)k.c0 * (unsigned)sizeof(P)));
+}
 template <typename T, bool PAIRS>
-__device__ __forceinline__ Two<T> load_two(const T *p, const Lane<PAIRS> &k, float fill) {  // p: at the lane's c0
+__device__ __forceinline__ Two<T> load_two(const T *row, const Lane<PAIRS> &k, float fill) {
+    const T *p = place(row, k);
     Two<T> v = two_of(T(), fill);
     if constexpr (PAIRS) {
         if (k.in0) v.w = *reinterpret_cast<const decltype(v.w) *>(p);
@@ -77,7 +85,8 @@ __device__ __forceinline__ Two<T> load_two(const T *p, const Lane<PAIRS> &k, flo
     return v;
 }
 template <typename T, bool PAIRS>
-__device__ __forceinline__ void store_two(T *p, const Lane<PAIRS> &k, float2 f) {
+__device__ __forceinline__ void store_two(T *row, const Lane<PAIRS> &k, float2 f) {
+    T *p = place(row, k);
     if constexpr (PAIRS) {
         if (!k.in0) return;
         if constexpr (sizeof(T) == 2)
@@ -100,9 +109,9 @@ __device__ __forceinline__ void store_state(float *p, const Lane<PAIRS> &k, floa
     if (k.in1) p[k.c0 + k.step] = v.y;
 }
 
-// -rate softplus(decay), per token at most a few times: the library's functions
+// rate softplus(decay), once a tile: the library's functions
 __device__ __forceinline__ float decay_rate(float decay, float rate) {
-    return -rate * (fmaxf(decay, 0.f) + log1pf(expf(-fabsf(decay))));
+    return rate * (fmaxf(decay, 0.f) + log1pf(expf(-fabsf(decay))));
 }
 
 __device__ __forceinline__ f2 splat(float v) { return pack2(v, v); }
@@ -119,22 +128,32 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
     return make_float2(rcp(d.x), rcp(d.y));
 }
 
-// v = 1 - a and a from l <= 0.  Above -1/4 the series of -expm1(l) (the first
-// term left out is l^6 / 5040 of the sum, 5e-8); below it 1 - exp(l), whose
-// absolute error 2^-23 is at most 5e-7 of v >= 0.22.
-__device__ __forceinline__ void decay2(f2 l, f2 &v, f2 &a) {
-    f2 q = fma2(l, splat(1.f / 720.f), splat(1.f / 120.f));
-    q = fma2(q, l, splat(1.f / 24.f));
-    q = fma2(q, l, splat(1.f / 6.f));
-    q = fma2(q, l, splat(0.5f));
-    q = fma2(q, l, splat(1.f));
-    const f2 m = mul2(l, splat(-1.f));
-    const float2 s = apart(mul2(q, m)), e = apart(mul2(l, splat(kLog2e))), lv = apart(l);
-    const float ex = ex2(e.x), ey = ex2(e.y);
-    const bool nx = lv.x > -0.25f, ny = lv.y > -0.25f;
-    const float vx = nx ? s.x : 1.f - ex, vy = ny ? s.y : 1.f - ey;
-    v = pack2(vx, vy);
-    a = pack2(nx ? 1.f - vx : ex, ny ? 1.f - vy : ey);
+// v = 1 - a and a from m = -log a >= 0.  Up to m = 1, v = m q(m), q the
+// polynomial of degree 6 of least relative error (2.5e-9, by the exchange
+// algorithm) to (1 - e^-m) / m on [0, 1]: 1.4e-7 in fp32.  Beyond, 1 - e^-m,
+// whose absolute error of 2^-24 or so is 1e-7 of v >= 0.63.  SMALL: no m is
+// above 1.  (Layers keep their states for tens of tokens: rate softplus(decay)
+// is below 1 throughout, which a warp finds out from its channels' decays;
+// the test and the second form cost 14 of 80 instructions a token.)
+template <bool SMALL>
+__device__ __forceinline__ void decay2(f2 m, f2 &v, f2 &a) {
+    f2 q = fma2(m, splat(1.2838072e-4f), splat(-1.2986638e-3f));
+    q = fma2(q, m, splat(8.2730958e-3f));
+    q = fma2(q, m, splat(-4.1645579e-2f));
+    q = fma2(q, m, splat(0.1666631f));
+    q = fma2(q, m, splat(-0.49999976f));
+    q = fma2(q, m, splat(1.f));
+    v = mul2(q, m);
+    if constexpr (SMALL) {
+        a = fma2(v, splat(-1.f), splat(1.f));
+    } else {
+        const float2 s = apart(v), e = apart(mul2(m, splat(-kLog2e))), mv = apart(m);
+        const float ex = ex2(e.x), ey = ex2(e.y);
+        const bool nx = mv.x <= 1.f, ny = mv.y <= 1.f;
+        const float vx = nx ? s.x : 1.f - ex, vy = ny ? s.y : 1.f - ey;
+        v = pack2(vx, vy);
+        a = pack2(nx ? 1.f - vx : ex, ny ? 1.f - vy : ey);
+    }
 }
 __device__ __forceinline__ float sqrt_approx(float v) {
     float r;
@@ -199,13 +218,15 @@ __device__ __forceinline__ Run link_wait(const unsigned long long *p, unsigned *
     unsigned long long u = link_load(p), v = link_load(p + 32);
     if ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset) {
         const uint64_t t0 = tc::globaltimer_ns();
-        do {
-            __nanosleep(40);
+        for (int i = 1;; ++i) {
             u = link_load(p), v = link_load(p + 32);
-            const uint64_t spent = tc::globaltimer_ns() - t0;
-            if (spent > 100000000ull) atomicOr(status, 1u);
-            if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
-        } while ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset);
+            if ((unsigned)(u >> 32) != kUnset && (unsigned)(v >> 32) != kUnset) break;
+            if (i % 64 == 0) {
+                const uint64_t spent = tc::globaltimer_ns() - t0;
+                if (spent > 100000000ull) atomicOr(status, 1u);
+                if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
+            }
+        }
     }
     Run r;
     r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
@@ -231,6 +252,9 @@ __device__ __forceinline__ Cuts cuts_of(const Seqs &q, int t0) {
     }
     return c;
 }
+// The number of a value that is the same in all lanes, as the compiler cannot know.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // The sequence of token t, at or after sequence s.
 __device__ __forceinline__ int seq_from(const Seqs &q, int s, int t) {
     const int *start = q.offsets();

@@ -18,82 +18,155 @@ namespace ssd {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int S = kStateEvery / kWarps;  // tokens a warp: a tile starts at a kept state
+constexpr int S = 8;        // tokens a warp
+constexpr int kBlocks = 2;  // an SM (bf16)
+constexpr int kTile = kWarps * S;
+static_assert(kTile % kStateEvery == 0, "a tile starts at a kept state");
+
+template <typename T, bool PAIRS>
+struct Warp {
+    Lane<PAIRS> k;
+    int b, t0, L;
+    Cuts cut;
+    f2 rate;  // rate softplus(decay)
+};
+template <typename T, bool PAIRS>
+__device__ __forceinline__ f2 state_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const float *states, int s) {
+    return both(load_state(states ? states + (int64_t)seq_from(a.seqs, w.cut.seq, w.t0 + s) * a.ch : nullptr, w.k));
+}
+
+// What is kept of a token between the passes, two channels each: the gates, v = 1 - a, x, the gradient of h_t by its own
+// output, and dy times the slope of the output's gate.
+template <typename T>
+struct Kept {
+    f2 sr, si, v, d, e;
+    Two<T> x;
+};
+__device__ __forceinline__ f2 one_minus(f2 v) { return fma2(v, splat(-1.f), splat(1.f)); }
+__device__ __forceinline__ f2 input_of(f2 v, f2 si, f2 x) {  // beta s(i) x
+    const float2 b2 = apart(fma2(v, one_minus(v), v));
+    return mul2(mul2(pack2(sqrt_approx(b2.x), sqrt_approx(b2.y)), si), x);
+}
+
+// PLAIN as in the forward kernel.
+template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Kept<T> (&t)[S], f2 &A, f2 &H, f2 &Q) {
+    Two<T> r[S], g[S], dy[S], z[S];
+    {
+        const T *px = a.x.at(w.b, w.t0), *pr = a.r.at(w.b, w.t0), *pi = a.i.p ? a.i.at(w.b, w.t0) : nullptr;
+        const T *pd = a.dy.at(w.b, w.t0), *pz = GATE ? a.z.at(w.b, w.t0) : nullptr;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            t[s].x = two_of(T(), 0.f), r[s] = two_of(T(), -30000.f), g[s] = two_of(T(), 128.f), dy[s] = z[s] = two_of(T(), 0.f);
+            if (PLAIN || w.t0 + s < w.L) {
+                r[s] = load_two<T, PAIRS>(pr + a.r.step(s), w.k, -30000.f);
+                t[s].x = load_two<T, PAIRS>(px + a.x.step(s), w.k, 0.f);
+                if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(s), w.k, 128.f);
+                dy[s] = load_two<T, PAIRS>(pd + a.dy.step(s), w.k, 0.f);
+                if constexpr (GATE) z[s] = load_two<T, PAIRS>(pz + a.z.step(s), w.k, 0.f);
+            }
+        }
+    }
+    A = splat(1.f), H = splat(0.f), Q = splat(0.f);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        t[s].sr = both(sigmoid2(widen(r[s])));
+        t[s].si = both(sigmoid2(widen(g[s])));
+        f2 av;
+        decay2<PLAIN>(mul2(w.rate, t[s].sr), t[s].v, av);
+        av = one_minus(t[s].v);
+        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) H = state_of(a, w, a.init, s);
+        A = mul2(A, av);
+        H = fma2(av, H, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
+        t[s].d = both(widen(dy[s]));
+        t[s].e = splat(0.f);
+        if constexpr (GATE) {
+            // silu(z) = z s, its slope s + z s (1 - s)
+            const f2 zf = both(widen(z[s])), sz = both(sigmoid2(widen(z[s]))), gate = mul2(zf, sz);
+            t[s].e = mul2(t[s].d, fma2(gate, one_minus(sz), sz));
+            t[s].d = mul2(t[s].d, gate);
+        }
+    }
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        if (PACKED && !PLAIN && (w.cut.last >> s & 1)) Q = state_of(a, w, a.dfinal, s);
+        Q = mul2(one_minus(t[s].v), add2(t[s].d, Q));
+    }
+}
+
+// h: the state that enters; c: what comes back from later tokens, and on return what goes back to earlier ones.
+template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Kept<T> (&t)[S], f2 h, f2 &c, f2 &sum) {
+    f2 prev[S];
+    T *pz = GATE ? a.dz.at(w.b, w.t0) : nullptr;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) h = state_of(a, w, a.init, s);
+        prev[s] = h;
+        h = fma2(one_minus(t[s].v), h, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
+        if (GATE && (PLAIN || w.t0 + s < w.L)) store_two<T, PAIRS>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
+    }
+    T *px = a.dx.at(w.b, w.t0), *pr = a.dr.at(w.b, w.t0), *pi = a.i.p ? a.di.at(w.b, w.t0) : nullptr;
+    sum = splat(0.f);
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+        if (PACKED && !PLAIN && (w.cut.last >> s & 1)) c = state_of(a, w, a.dfinal, s);
+        const f2 av = one_minus(t[s].v), gh = add2(t[s].d, c), xf = both(widen(t[s].x)), m = mul2(w.rate, t[s].sr);
+        const float2 b2 = apart(fma2(t[s].v, av, t[s].v));
+        const f2 rb = pack2(rsqrt_approx(fmaxf(b2.x, 1e-37f)), rsqrt_approx(fmaxf(b2.y, 1e-37f))), beta = mul2(both(b2), rb);
+        c = mul2(gh, av);
+        // dl l = g a (s(i) x a m / beta - m h_{t-1}),  l = -m
+        const f2 sx = mul2(t[s].si, xf);
+        const f2 dll = mul2(mul2(c, m), fma2(mul2(sx, av), rb, mul2(prev[s], splat(-1.f))));
+        sum = add2(sum, dll);
+        if (PACKED && !PLAIN && (w.cut.first >> s & 1) && a.dinit)
+            store_state(a.dinit + (int64_t)seq_from(a.seqs, w.cut.seq, w.t0 + s) * a.ch, w.k, apart(c));
+        if (PLAIN || w.t0 + s < w.L) {
+            const f2 gx = mul2(mul2(gh, beta), t[s].si);
+            store_two<T, PAIRS>(px + a.dx.step(s), w.k, apart(gx));
+            store_two<T, PAIRS>(pr + a.dr.step(s), w.k, apart(mul2(dll, one_minus(t[s].sr))));
+            if (pi) store_two<T, PAIRS>(pi + a.di.step(s), w.k, apart(mul2(mul2(gx, xf), one_minus(t[s].si))));
+        }
+    }
+}
 
 template <typename T, bool PAIRS, bool GATE, bool PACKED>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
     __shared__ float4 fore[kWarps][32], back[kWarps][32];
     __shared__ float4 tiles[kGroup][32];
     __shared__ float2 enter[32];
     __shared__ unsigned ticket;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32;
     unsigned n = blockIdx.x;
     if (a.links.run) {
         if (threadIdx.x == 0) ticket = atomicAdd(a.links.ticket, 1u) + 1u;
         __syncthreads();
-        n = ticket;
+        n = (unsigned)uniform((int)ticket);
     }
     const int rows = a.nblk * a.batch, later = n / rows, row = n % rows, b = row / a.nblk;  // later: tiles behind this one
-    const int tile = a.ntile - 1 - later;
-    const Lane<PAIRS> k(row % a.nblk, lane, a.ch);
-    const int L = a.seqs.L, t0 = (tile * nw + warp) * S;
-
-    Two<T> x[S], r[S], g[S], dy[S], z[S];
-    {
-        const T *px = a.x.at(b, 0) + k.c0, *pr = a.r.at(b, 0) + k.c0, *pi = a.i.p ? a.i.at(b, 0) + k.c0 : nullptr;
-        const T *pd = a.dy.at(b, 0) + k.c0, *pz = GATE ? a.z.at(b, 0) + k.c0 : nullptr;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            x[s] = two_of(T(), 0.f), r[s] = two_of(T(), -30000.f), g[s] = two_of(T(), 128.f), dy[s] = z[s] = two_of(T(), 0.f);
-            if (t0 + s < L) {
-                r[s] = load_two<T, PAIRS>(pr + a.r.step(t0 + s), k, -30000.f);
-                x[s] = load_two<T, PAIRS>(px + a.x.step(t0 + s), k, 0.f);
-                if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(t0 + s), k, 128.f);
-                dy[s] = load_two<T, PAIRS>(pd + a.dy.step(t0 + s), k, 0.f);
-                if constexpr (GATE) z[s] = load_two<T, PAIRS>(pz + a.z.step(t0 + s), k, 0.f);
-            }
-        }
+    const int tile = a.ntile - 1 - later, L = a.seqs.L;
+    Warp<T, PAIRS> w{Lane<PAIRS>(row % a.nblk, lane, a.ch), b, (tile * nw + warp) * S, L, Cuts{0, 0, b}, 0};
+    const Lane<PAIRS> &k = w.k;
+    if (PACKED && w.t0 < L) {
+        w.cut = cuts_of<S>(a.seqs, w.t0);
+        w.cut.first = (unsigned)uniform((int)w.cut.first), w.cut.last = (unsigned)uniform((int)w.cut.last);
+        w.cut.seq = uniform(w.cut.seq);
     }
-    Cuts cut{0, 0, b};
-    if (PACKED && t0 < L) cut = cuts_of<S>(a.seqs, t0);
     const float2 dec = load_state(a.decay, k);
-    const f2 rate = pack2(decay_rate(dec.x, a.rate), decay_rate(dec.y, a.rate));
-    auto init_at = [&](int s) {
-        return load_state(a.init ? a.init + (int64_t)(PACKED ? seq_from(a.seqs, cut.seq, t0 + s) : b) * a.ch : nullptr, k);
-    };
-    auto dfinal_at = [&](int s) {
-        return load_state(a.dfinal ? a.dfinal + (int64_t)(PACKED ? seq_from(a.seqs, cut.seq, t0 + s) : b) * a.ch : nullptr, k);
-    };
+    const float ra = decay_rate(dec.x, a.rate), rb = decay_rate(dec.y, a.rate);
+    w.rate = pack2(ra, rb);
+    const bool plain = w.t0 + S <= L && !(w.cut.first | w.cut.last) && __all_sync(0xffffffffu, (ra <= 1.f || !k.in0) && (rb <= 1.f || !k.in1));
 
-    f2 sr[S], si[S], vv[S], av[S], d[S];
-    f2 A = splat(1.f), H = splat(0.f);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        sr[s] = both(sigmoid2(widen(r[s])));
-        si[s] = both(sigmoid2(widen(g[s])));
-        decay2(mul2(rate, sr[s]), vv[s], av[s]);
-        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
-        const f2 u = mul2(mul2(pack2(sqrt_approx(w.x), sqrt_approx(w.y)), si[s]), both(widen(x[s])));
-        if (PACKED && (cut.first >> s & 1)) H = both(init_at(s));
-        A = mul2(A, av[s]);
-        H = fma2(av[s], H, u);
-        d[s] = both(widen(dy[s]));
-        if constexpr (GATE) {
-            const float2 zf = widen(z[s]);
-            d[s] = mul2(d[s], mul2(both(zf), both(sigmoid2(zf))));
-        }
-    }
-    f2 Q = splat(0.f);
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-        if (PACKED && (cut.last >> s & 1)) Q = both(dfinal_at(s));
-        Q = mul2(av[s], add2(d[s], Q));
-    }
+    Kept<T> t[S];
+    f2 A, H, Q;
+    if (plain)
+        read_tokens<T, PAIRS, GATE, PACKED, true>(a, w, t, A, H, Q);
+    else
+        read_tokens<T, PAIRS, GATE, PACKED, false>(a, w, t, A, H, Q);
     if (nw > 1) {
         const float2 fa = apart(A), fh = apart(H), fq = apart(Q);
-        const bool cf = PACKED && cut.first, cl = PACKED && cut.last;
-        fore[warp][lane] = cf ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
-        back[warp][lane] = cl ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
+        fore[warp][lane] = w.cut.first ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
+        back[warp][lane] = w.cut.last ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
         __syncthreads();
     }
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
@@ -109,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) gated_bwd
         Run all{};
         if (warp == 0) {
             all = run_of(back[nw - 1][lane]);
-            for (int w = nw - 2; w >= 0; --w) all = then(all, run_of(back[w][lane]));
+            for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[j][lane]));
             if (in_group != kGroup - 1 && tile > 0) link_store(mine, all);
         }
         for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
@@ -127,54 +200,16 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) gated_bwd
         __syncthreads();
         c = enter[lane];
     }
-    for (int w = nw - 1; w > warp; --w) c = through(run_of(back[w][lane]), c);
-    float2 h = load_state(a.kept + ((int64_t)b * a.nkeep + tile) * a.ch, k);
-    for (int w = 0; w < warp; ++w) h = through(run_of(fore[w][lane]), h);
+    for (int j = nw - 1; j > warp; --j) c = through(run_of(back[j][lane]), c);
+    float2 h = load_state(a.kept + ((int64_t)b * a.nkeep + tile * (kTile / kStateEvery)) * a.ch, k);
+    for (int j = 0; j < warp; ++j) h = through(run_of(fore[j][lane]), h);
 
-    f2 prev[S], hv = both(h);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        if (PACKED && (cut.first >> s & 1)) hv = both(init_at(s));
-        prev[s] = hv;
-        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
-        const f2 u = mul2(mul2(pack2(sqrt_approx(w.x), sqrt_approx(w.y)), si[s]), both(widen(x[s])));
-        hv = fma2(av[s], hv, u);
-        if constexpr (GATE) {
-            if (t0 + s < L) {
-                const float2 zf = widen(z[s]), sz = sigmoid2(zf);
-                const f2 slope = pack2(silu_slope(zf.x, sz.x), silu_slope(zf.y, sz.y));
-                store_two<T, PAIRS>(a.dz.at(b, t0 + s) + k.c0, k, apart(mul2(mul2(both(widen(dy[s])), hv), slope)));
-            }
-        }
-    }
-    f2 cv = both(c), sum = splat(0.f);
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-        if (PACKED && (cut.last >> s & 1)) cv = both(dfinal_at(s));
-        const f2 gh = add2(d[s], cv), xf = both(widen(x[s])), l = mul2(rate, sr[s]);
-        const float2 w = apart(mul2(vv[s], fma2(vv[s], splat(-1.f), splat(2.f))));
-        const float wx = fmaxf(w.x, 1e-37f), wy = fmaxf(w.y, 1e-37f);
-        const f2 rb = pack2(rsqrt_approx(wx), rsqrt_approx(wy)), beta = mul2(pack2(w.x, w.y), rb);
-        const f2 sx = mul2(si[s], xf);
-        // dl l = g a (l h_{t-1} - s(i) x a l / beta)
-        const f2 ga = mul2(gh, av[s]);
-        const f2 inner = fma2(mul2(mul2(sx, av[s]), mul2(l, rb)), splat(-1.f), mul2(l, prev[s]));
-        const f2 dll = mul2(ga, inner);
-        sum = add2(sum, dll);
-        cv = ga;
-        if (PACKED && (cut.first >> s & 1)) {
-            if (a.dinit) store_state(a.dinit + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch, k, apart(cv));
-        }
-        if (t0 + s < L) {
-            const f2 gb = mul2(mul2(gh, beta), si[s]);
-            store_two<T, PAIRS>(a.dx.at(b, t0 + s) + k.c0, k, apart(gb));
-            store_two<T, PAIRS>(a.dr.at(b, t0 + s) + k.c0, k, apart(mul2(dll, fma2(sr[s], splat(-1.f), splat(1.f)))));
-            if (a.i.p)
-                store_two<T, PAIRS>(a.di.at(b, t0 + s) + k.c0, k,
-                                    apart(mul2(mul2(gb, xf), fma2(si[s], splat(-1.f), splat(1.f)))));
-        }
-    }
-    if (!PACKED && t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)b * a.ch, k, apart(cv));
+    f2 cv = both(c), sum;
+    if (plain)
+        write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, t, both(h), cv, sum);
+    else
+        write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, t, both(h), cv, sum);
+    if (!PACKED && w.t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)b * a.ch, k, apart(cv));
     if (a.ddecay_part) {
         const float2 f = apart(sum);
         if (nw > 1) {
@@ -184,7 +219,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) gated_bwd
         }
         if (warp == 0) {
             float2 s = f;
-            for (int w = 1; w < nw; ++w) s.x += fore[w][lane].x, s.y += fore[w][lane].y;
+            for (int j = 1; j < nw; ++j) s.x += fore[j][lane].x, s.y += fore[j][lane].y;
             store_state(a.ddecay_part + ((int64_t)tile * a.batch + b) * a.ch, k, s);
         }
     }
@@ -222,15 +257,17 @@ int64_t bwd_warps(int64_t L) {
     return w < 1 ? 1 : w < kWarps ? w : kWarps;
 }
 
+int64_t bwd_tiles(int64_t L) { return (L + kTile - 1) / kTile; }
+
 struct BwdPlan {
     size_t kept, fwd_links, links, part, bytes;
 };
 BwdPlan plan_bwd(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq, bool with_states) {
     BwdPlan p{};
-    const int64_t rows = gated_blocks(s) * s->batch, ntile = gated_kept(s);
+    const int64_t rows = gated_blocks(s) * s->batch, ntile = bwd_tiles(s->seqlen);
     size_t at = cu ? offsets_bytes(cu, nseq) : 0;
     p.kept = at;
-    if (!with_states) at += align256(sizeof(float) * s->batch * ntile * s->channels);
+    if (!with_states) at += align256(sizeof(float) * s->batch * gated_kept(s) * s->channels);
     p.fwd_links = at;
     if (!with_states) at += gated_fwd_links(s);
     p.links = at;
@@ -275,7 +312,7 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     for (const ssd_rows_t *r : {dy, &out->dx, &out->dr}) pairs = pairs && rows_pairs(*r, sizeof(T), s->batch, s->seqlen);
     if (in->i.data) pairs = pairs && rows_pairs(out->di, sizeof(T), s->batch, s->seqlen);
     if (in->z.data) pairs = pairs && rows_pairs(out->dz, sizeof(T), s->batch, s->seqlen);
-    const int64_t ntile = gated_kept(s), nw = bwd_warps(s->seqlen);
+    const int64_t ntile = bwd_tiles(s->seqlen), nw = bwd_warps(s->seqlen);
     a.ntile = (int)ntile;
     e = place_links(ws + p.links, gated_blocks(s) * s->batch, ntile, a.links, st);
     if (e != cudaSuccess) return status_of(e);
