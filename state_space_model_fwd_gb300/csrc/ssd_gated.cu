@@ -7,70 +7,86 @@ namespace ssd {
 namespace {
 
 constexpr int kWarps = 8;  // of a tile; fewer where a row has fewer tokens
-constexpr int S = 16;      // tokens a warp
 constexpr int kBlocks = 2;  // an SM
+template <typename T>
+constexpr int kTokens = 32 / sizeof(T);  // a warp: fp32 takes twice the shared memory
+
+// The next tile's x, r and i, and two tiles' z: each lane's own.
+template <typename T>
+struct Stage {
+    static constexpr int S = kTokens<T>;
+    Two<T> in[3][S][kWarps][32], z[2][S][kWarps][32];
+};
 
 // What a warp knows of its tokens.
 template <typename T, bool PAIRS>
 struct Warp {
     Lane<PAIRS> k;
-    int b, t0, L;
-    Cuts cut;
-    f2 rate;
-    __device__ __forceinline__ float2 init_of(const GatedArgs<T> &a, int s) const {
-        return load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, t0 + s) * a.ch : nullptr, k);
+    int tile, row, b, t0;
+    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
+        : k((n % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch;
+        tile = n / rows, row = n % rows, b = row / a.nblk, t0 = tile * tokens + warp * kTokens<T>;
     }
 };
+template <typename T, bool PAIRS>
+__device__ __forceinline__ float2 init_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, int s) {
+    return load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch : nullptr, w.k);
+}
+
+// Starts the copies of a tile's inputs.
+template <typename T, bool PAIRS, bool GATE>
+__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Stage<T> &st, int warp, int lane, int zbuf) {
+    // past the end, and in channels that are none: a = 1 and nothing enters
+    const int left = a.seqs.L - w.t0, stride = kWarps * 32;
+    auto rows = [&](Two<T> *dst, const Rows<const T> &r, float fill) {
+        fetch_rows<T, PAIRS, kTokens<T>>(dst, stride, r.at(w.b, w.t0), r.rs, w.k, lane, left, a.wide, a.ch, fill);
+    };
+    rows(&st.in[1][0][warp][0], a.r, -30000.f);
+    rows(&st.in[0][0][warp][0], a.x, 0.f);
+    if (a.i.p) rows(&st.in[2][0][warp][0], a.i, 128.f);
+    if (GATE) rows(&st.z[zbuf][0][warp][0], a.z, 0.f);
+}
 
 // The tokens' decays and inputs, and the run they make.  PLAIN: S tokens of one sequence that neither begins nor ends among
 // them, decays with m <= 1.
-template <typename T, bool PAIRS, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, f2 (&av)[S], f2 (&uv)[S], f2 &A, f2 &H) {
-    Two<T> x[S], r[S], g[S];
-    const T *px = a.x.at(w.b, w.t0), *pr = a.r.at(w.b, w.t0), *pi = a.i.p ? a.i.at(w.b, w.t0) : nullptr;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        // past the end, and in channels that are none: a = 1 and nothing enters
-        r[s] = two_of(T(), -30000.f), x[s] = two_of(T(), 0.f), g[s] = two_of(T(), 128.f);
-        if (PLAIN || w.t0 + s < w.L) {
-            r[s] = load_two<T, PAIRS>(pr + a.r.step(s), w.k, -30000.f);
-            x[s] = load_two<T, PAIRS>(px + a.x.step(s), w.k, 0.f);
-            if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(s), w.k, 128.f);  // without it s(i) = s(128) = 1
-        }
-    }
+template <typename T, bool PAIRS, bool PACKED, bool PLAIN, int S>
+__device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, const Stage<T> &st,
+                                           int warp, int lane, f2 (&av)[S], f2 (&uv)[S], f2 &A, f2 &H) {
     A = splat(1.f), H = splat(0.f);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         f2 v;
-        decay2<PLAIN>(mul2(w.rate, both(sigmoid2(widen(r[s])))), v, av[s]);
+        decay2<PLAIN>(mul2(rate, both(sigmoid2(widen(st.in[1][s][warp][lane])))), v, av[s]);
         const float2 b2 = apart(fma2(v, av[s], v));
-        const f2 beta = pack2(sqrt_approx(b2.x), sqrt_approx(b2.y));
-        uv[s] = mul2(mul2(beta, both(sigmoid2(widen(g[s])))), both(widen(x[s])));
-        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) H = both(w.init_of(a, s));
+        uv[s] = mul2(mul2(pack2(sqrt_approx(b2.x), sqrt_approx(b2.y)), both(sigmoid2(widen(st.in[2][s][warp][lane])))),
+                     both(widen(st.in[0][s][warp][lane])));
+        if (PACKED && !PLAIN && (cut.first >> s & 1)) H = both(init_of(a, w, cut, s));
         A = mul2(A, av[s]);
         H = fma2(av[s], H, uv[s]);
     }
-    if (PACKED && !PLAIN && w.cut.first) A = splat(-1.f);
+    if (PACKED && !PLAIN && cut.first) A = splat(-1.f);
 }
 
 // The outputs, from the state that enters.
-template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const f2 (&av)[S], const f2 (&uv)[S],
-                                             const Two<T> (&z)[S], f2 hv) {
+template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN, int S>
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, const Stage<T> &st, int warp,
+                                             int lane, int zbuf, const f2 (&av)[S], const f2 (&uv)[S], f2 hv) {
     T *py = a.y.at(w.b, w.t0);
+    const int L = a.seqs.L;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        if (!PLAIN && w.t0 + s >= w.L) break;
-        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) hv = both(w.init_of(a, s));
+        if (!PLAIN && w.t0 + s >= L) break;
+        if (PACKED && !PLAIN && (cut.first >> s & 1)) hv = both(init_of(a, w, cut, s));
         hv = fma2(av[s], hv, uv[s]);
         f2 o = hv;
         if constexpr (GATE) {
-            const float2 zf = widen(z[s]);
+            const float2 zf = widen(st.z[zbuf][s][warp][lane]);
             o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
         }
         store_two<T, PAIRS>(py + a.y.step(s), w.k, apart(o));
-        if (!PLAIN && (w.cut.last >> s & 1) && a.fin) {
-            const int q = PACKED ? seq_from(a.seqs, w.cut.seq, w.t0 + s) : w.b;
+        if (!PLAIN && (cut.last >> s & 1) && a.fin) {
+            const int q = PACKED ? seq_from(a.seqs, cut.seq, w.t0 + s) : w.b;
             store_state(a.fin + (int64_t)q * a.ch, w.k, apart(hv));
         }
     }
@@ -78,99 +94,102 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
 
 template <typename T, bool PAIRS, bool GATE, bool PACKED>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const __grid_constant__ GatedArgs<T> a) {
-    __shared__ float4 runs[kWarps][32];
+    constexpr int S = kTokens<T>;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
+    __shared__ float4 runs[2][kWarps][32];
     __shared__ float4 tiles[kGroup][32];
     __shared__ float2 enter[32];
-    __shared__ unsigned ticket;
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32;
-    unsigned n = blockIdx.x;
-    if (a.links.run) {
-        if (threadIdx.x == 0) ticket = atomicAdd(a.links.ticket, 1u) + 1u;  // (it starts at -1)
-        __syncthreads();
-        n = (unsigned)uniform((int)ticket);
-    }
-    const int rows = a.nblk * a.batch, tile = n / rows, row = n % rows, b = row / a.nblk, L = a.seqs.L;
-    Warp<T, PAIRS> w{Lane<PAIRS>(row % a.nblk, lane, a.ch), b, (tile * nw + warp) * S, L, Cuts{0, 0, b}, 0};
-    const Lane<PAIRS> &k = w.k;
-    if (w.t0 < L) {
-        if constexpr (PACKED) {
-            w.cut = cuts_of<S>(a.seqs, w.t0);
-            w.cut.first = (unsigned)uniform((int)w.cut.first), w.cut.last = (unsigned)uniform((int)w.cut.last);
-            w.cut.seq = uniform(w.cut.seq);
-        } else if (w.t0 + S >= L) {
-            w.cut.last = 1u << (L - 1 - w.t0);
-        }
-    }
-    const float2 dec = load_state(a.decay, k);
-    const float ra = decay_rate(dec.x, a.rate), rb = decay_rate(dec.y, a.rate);
-    w.rate = pack2(ra, rb);
-    const bool plain = w.t0 + S <= L && !(w.cut.first | w.cut.last) && __all_sync(0xffffffffu, (ra <= 1.f || !k.in0) && (rb <= 1.f || !k.in1));
-
-    f2 av[S], uv[S], A, H;
-    if (plain)
-        run_tokens<T, PAIRS, PACKED, true>(a, w, av, uv, A, H);
-    else
-        run_tokens<T, PAIRS, PACKED, false>(a, w, av, uv, A, H);
-    Two<T> z[S];  // (in flight while the tiles exchange their runs)
-    if constexpr (GATE) {
-        const T *pz = a.z.at(b, w.t0);
+    __shared__ unsigned ticket[2];
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
+    const bool linked = a.links.run != nullptr;
+    auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };  // (it starts at -1)
+    if (!a.i.p) {  // no input gate: s(128) = 1
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            z[s] = two_of(T(), 0.f);
-            if (a.y.p && w.t0 + s < L) z[s] = load_two<T, PAIRS>(pz + a.z.step(s), k, 0.f);
-        }
+        for (int s = 0; s < S; ++s) st.in[2][s][warp][lane] = two_of(T(), 128.f);
     }
-    if (nw > 1) {
+    wait_previous();
+    if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
+    __syncthreads();
+    int n = uniform((int)ticket[1]);
+    Warp<T, PAIRS> w(a, n, warp, lane, tokens);
+    float2 rate = make_float2(0.f, 0.f);
+    if (n < a.tiles) {
+        rate = load_state(a.rates, w.k);
+        fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane, 0);
+    }
+    for (int p = 0; n < a.tiles; p ^= 1) {
+        const Lane<PAIRS> &k = w.k;
+        if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
+        Cuts cut{0, 0, w.b};
+        if (w.t0 < L) {
+            if constexpr (PACKED) {
+                cut = cuts_of<S>(a.seqs, w.t0);
+                cut.first = (unsigned)uniform((int)cut.first), cut.last = (unsigned)uniform((int)cut.last), cut.seq = uniform(cut.seq);
+            } else if (w.t0 + S >= L) {
+                cut.last = 1u << (L - 1 - w.t0);
+            }
+        }
+        const bool plain = w.t0 + S <= L && !(cut.first | cut.last) && __all_sync(0xffffffffu, rate.x <= 1.f && rate.y <= 1.f);
+        // The state that enters the row, or the group of tiles.
+        float2 h = !PACKED && w.tile < kGroup ? load_state(a.init ? a.init + (int64_t)w.b * a.ch : nullptr, k) : make_float2(0.f, 0.f);
+
+        copies_done();
+        __syncwarp();
+        f2 av[S], uv[S], A, H;
+        if (plain)
+            run_tokens<T, PAIRS, PACKED, true>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
+        else
+            run_tokens<T, PAIRS, PACKED, false>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
         const float2 fa = apart(A), fh = apart(H);
-        runs[warp][lane] = make_float4(fa.x, fa.y, fh.x, fh.y);
+        runs[p][warp][lane] = make_float4(fa.x, fa.y, fh.x, fh.y);
         __syncthreads();
-    }
-    auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
+        n = uniform((int)ticket[p]);
+        const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        if (n < a.tiles) {
+            rate = load_state(a.rates, after.k);
+            fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane, p ^ 1);
+        }
 
-    // The state that enters the tile.
-    float2 h = !PACKED ? load_state(a.init ? a.init + (int64_t)b * a.ch : nullptr, k) : make_float2(0.f, 0.f);
-    if (a.links.run) {
-        unsigned long long *mine = a.links.run + ((int64_t)row * a.ntile + tile) * kCols + lane;
-        const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
-        unsigned long long *entry = a.links.entry + (int64_t)row * groups * kCols + lane;
-        const int in_group = tile % kGroup, group = tile / kGroup;
-        Run all{};
-        if (warp == 0) {
-            all = run_of(runs[0][lane]);
-            for (int j = 1; j < nw; ++j) all = then(all, run_of(runs[j][lane]));
-            if (in_group != kGroup - 1 && tile + 1 < a.ntile) link_store(mine, all);
+        auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
+        if (linked) {
+            unsigned long long *mine = a.links.run + ((int64_t)w.row * a.ntile + w.tile) * kCols + lane;
+            const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
+            unsigned long long *entry = a.links.entry + (int64_t)w.row * groups * kCols + lane;
+            const int in_group = w.tile % kGroup, group = w.tile / kGroup;
+            Run all{};
+            if (warp == 0) {
+                all = run_of(runs[p][0][lane]);
+                for (int j = 1; j < nw; ++j) all = then(all, run_of(runs[p][j][lane]));
+                if (in_group != kGroup - 1 && w.tile + 1 < a.ntile) link_store(mine, all);
+            }
+            for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
+                const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
+                tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
+            }
+            if (warp == 0 && group > 0) h = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
+            __syncthreads();
+            if (warp == 0) {
+                for (int j = 0; j < in_group; ++j) h = through(run_of(tiles[j][lane]), h);
+                if (in_group == kGroup - 1 && w.tile + 1 < a.ntile)
+                    link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, h)});
+                enter[lane] = h;
+            }
+            __syncthreads();
+            h = enter[lane];
         }
-        for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
-            const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
-            tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
+        for (int j = 0; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
+        if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
+            store_state(a.keep + ((int64_t)w.b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
+        if (a.y.p) {
+            if (plain)
+                write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, st, warp, lane, p, av, uv, both(h));
+            else
+                write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, st, warp, lane, p, av, uv, both(h));
         }
-        if (warp == 0 && group > 0) h = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
-        __syncthreads();
-        if (warp == 0) {
-            for (int j = 0; j < in_group; ++j) h = through(run_of(tiles[j][lane]), h);
-            if (in_group == kGroup - 1 && tile + 1 < a.ntile)
-                link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, h)});
-            enter[lane] = h;
-        }
-        __syncthreads();
-        h = enter[lane];
+        w = after;
     }
-    for (int j = 0; j < warp; ++j) h = through(run_of(runs[j][lane]), h);
-    if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
-        store_state(a.keep + ((int64_t)b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
-    if (!a.y.p) return;
-    if (plain)
-        write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, av, uv, z, both(h));
-    else
-        write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, av, uv, z, both(h));
-}
-
-__global__ void __launch_bounds__(256) gated_empty_kernel(const __grid_constant__ Seqs q, int64_t ch, const float *src, float *dst) {
-    const int *start = q.offsets();
-    for (int s = blockIdx.x; s < q.n; s += gridDim.x) {
-        if (start[s] != start[s + 1]) continue;
-        for (int64_t c = threadIdx.x; c < ch; c += 256) dst[s * ch + c] = src ? src[s * ch + c] : 0.f;
-    }
+    if (PACKED && a.some_empty) pass_empty(a.seqs, a.ch, a.init, a.fin);
 }
 
 template <typename T, bool PAIRS>
@@ -199,10 +218,11 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
     store_two<T, PAIRS>(a.y.at(b, 0), k, apart(o));
 }
 
-int64_t fwd_tokens(int64_t L) {  // of a tile
-    const int64_t w = (L + S - 1) / S;
-    return S * (w < kWarps ? (w < 1 ? 1 : w) : kWarps);
+int64_t fwd_warps(const ssd_gated_shape_t *s) {
+    const int64_t per = 32 / dtype_size(s->dtype), w = (s->seqlen + per - 1) / per;
+    return w < kWarps ? (w < 1 ? 1 : w) : kWarps;
 }
+int64_t fwd_tokens(const ssd_gated_shape_t *s) { return 32 / dtype_size(s->dtype) * fwd_warps(s); }  // of a tile
 
 }  // namespace
 
@@ -237,6 +257,14 @@ bool gated_pairs(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
     return true;
 }
 
+bool gated_wide(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
+    const size_t es = dtype_size(s->dtype);
+    if (s->channels * es % 16) return false;
+    for (const ssd_rows_t *r : {&in->x, &in->r, &in->i, &in->z})
+        if (r->data && !rows_vec(*r, es, s->batch, s->seqlen)) return false;
+    return true;
+}
+
 template <typename T>
 GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, int64_t nseq) {
     GatedArgs<T> a{};
@@ -244,58 +272,77 @@ GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in
     a.decay = in->decay, a.init = in->init_state, a.rate = s->rate;
     a.ch = (int)s->channels, a.nblk = (int)gated_blocks(s), a.batch = (int)s->batch, a.nkeep = (int)gated_kept(s);
     a.seqs.n = (int)nseq, a.seqs.L = (int)s->seqlen;
+    a.wide = gated_wide(s, in);
     return a;
 }
 template GatedArgs<float> gated_args<float>(const ssd_gated_shape_t *, const ssd_gated_inputs_t *, int64_t);
 template GatedArgs<bf16> gated_args<bf16>(const ssd_gated_shape_t *, const ssd_gated_inputs_t *, int64_t);
 
-size_t links_bytes(int64_t rows, int64_t ntile) {
-    if (ntile <= 1) return 0;
-    return align256(8 * kCols * rows * (ntile + (ntile + kGroup - 1) / kGroup) + 256);
+namespace {
+__global__ void __launch_bounds__(256) gated_prepare_kernel(uint4 *links, int64_t n, const float *decay, float rate, float *rates, int ch) {
+    launch_next();
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t c = first; c < ch; c += step) rates[c] = decay_rate(decay[c], rate);
+    for (int64_t i = first; i < n; i += step) links[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
 }
-cudaError_t place_links(char *ws, int64_t rows, int64_t ntile, Links &l, cudaStream_t st) {
-    l = Links{};
-    const size_t bytes = links_bytes(rows, ntile);
-    if (!bytes) return cudaSuccess;
-    cudaError_t e = device_status_word(&l.status);
-    if (e != cudaSuccess) return e;
-    l.ticket = reinterpret_cast<unsigned *>(ws);
-    l.run = reinterpret_cast<unsigned long long *>(ws + 256);
-    l.entry = l.run + kCols * rows * ntile;
-    e = cudaMemsetAsync(ws, 0xFF, bytes, st);
-    timing_mark(st, "gated_links");
-    return e;
-}
+}  // namespace
 
-cudaError_t launch_empty(const Seqs &q, const int64_t *cu, int64_t nseq, int64_t ch, const float *src, float *dst, cudaStream_t st) {
-    bool any = false;
-    for (int64_t s = 0; s < nseq && !any; ++s) any = cu[s] == cu[s + 1];
-    if (!any) return cudaSuccess;
-    gated_empty_kernel<<<(unsigned)(nseq < 1024 ? nseq : 1024), 256, 0, st>>>(q, ch, src, dst);
-    timing_mark(st, "gated_empty");
+size_t links_bytes(int64_t ch, int64_t rows, int64_t ntile) {
+    const size_t rates = align256(sizeof(float) * ch);
+    if (ntile <= 1) return rates;
+    return rates + align256(8 * kCols * rows * (ntile + (ntile + kGroup - 1) / kGroup) + 256);
+}
+template <typename T>
+cudaError_t prepare(GatedArgs<T> &a, char *ws, int64_t rows, int64_t ntile, cudaStream_t st) {
+    a.links = Links{};
+    a.rates = reinterpret_cast<float *>(ws);
+    const size_t before = align256(sizeof(float) * a.ch), bytes = links_bytes(a.ch, rows, ntile) - before;
+    ws += before;
+    if (bytes) {
+        const cudaError_t e = device_status_word(&a.links.status);
+        if (e != cudaSuccess) return e;
+        a.links.ticket = reinterpret_cast<unsigned *>(ws);
+        a.links.run = reinterpret_cast<unsigned long long *>(ws + 256);
+        a.links.entry = a.links.run + kCols * rows * ntile;
+    }
+    const int64_t want = (int64_t)(bytes / 16 + 1023) / 1024 + a.ch / 256;
+    gated_prepare_kernel<<<(unsigned)(want < 1 ? 1 : want < 4 * kSMs ? want : 4 * kSMs), 256, 0, st>>>(
+        reinterpret_cast<uint4 *>(ws), (int64_t)(bytes / 16), a.decay, a.rate, a.rates, a.ch);
+    timing_mark(st, "gated_prepare");
     return cudaGetLastError();
+}
+template cudaError_t prepare<float>(GatedArgs<float> &, char *, int64_t, int64_t, cudaStream_t);
+template cudaError_t prepare<bf16>(GatedArgs<bf16> &, char *, int64_t, int64_t, cudaStream_t);
+
+bool any_empty(const int64_t *cu, int64_t nseq) {
+    for (int64_t s = 0; s < nseq; ++s)
+        if (cu[s] == cu[s + 1]) return true;
+    return false;
 }
 
 size_t gated_fwd_links(const ssd_gated_shape_t *s) {
-    const int64_t per = fwd_tokens(s->seqlen);
-    return links_bytes(gated_blocks(s) * s->batch, (s->seqlen + per - 1) / per);
+    const int64_t per = fwd_tokens(s);
+    return links_bytes(s->channels, gated_blocks(s) * s->batch, (s->seqlen + per - 1) / per);
 }
 
 template <typename T>
 cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st) {
-    const int64_t per = fwd_tokens(s->seqlen), ntile = (s->seqlen + per - 1) / per;
+    const int64_t per = fwd_tokens(s), ntile = (s->seqlen + per - 1) / per;
     a.ntile = (int)ntile;
-    cudaError_t e = place_links(links, gated_blocks(s) * s->batch, ntile, a.links, st);
+    a.tiles = (int)(ntile * a.nblk * a.batch);
+    cudaError_t e = prepare(a, links, gated_blocks(s) * s->batch, ntile, st);
     if (e != cudaSuccess) return e;
-    const unsigned blocks = (unsigned)(ntile * a.nblk * a.batch), threads = (unsigned)(per / S * 32);
+    const unsigned blocks = (unsigned)(a.tiles < kSMs * kBlocks ? a.tiles : kSMs * kBlocks), threads = (unsigned)(fwd_warps(s) * 32);
     auto go = [&](auto p, auto g, auto c) {
-        gated_fwd_kernel<T, decltype(p)::value, decltype(g)::value, decltype(c)::value><<<blocks, threads, 0, st>>>(a);
+        auto kernel = gated_fwd_kernel<T, decltype(p)::value, decltype(g)::value, decltype(c)::value>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)threads, sizeof(Stage<T>), st, true, a);
     };
     auto with_cuts = [&](auto p, auto g) { packed ? go(p, g, std::true_type{}) : go(p, g, std::false_type{}); };
     auto with_gate = [&](auto p) { a.z.p && a.y.p ? with_cuts(p, std::true_type{}) : with_cuts(p, std::false_type{}); };
     pairs ? with_gate(std::true_type{}) : with_gate(std::false_type{});
     timing_mark(st, a.y.p ? "gated_scan" : "gated_states");
-    return cudaGetLastError();
+    return e;
 }
 template cudaError_t launch_gated_fwd<float>(GatedArgs<float> &, const ssd_gated_shape_t *, bool, bool, char *, cudaStream_t);
 template cudaError_t launch_gated_fwd<bf16>(GatedArgs<bf16> &, const ssd_gated_shape_t *, bool, bool, char *, cudaStream_t);
@@ -315,7 +362,7 @@ ssd_status_t fwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (cu) {
         bool launched;
         e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws), a.seqs, &launched, st);
-        if (e == cudaSuccess && fin) e = launch_empty(a.seqs, cu, nseq, s->channels, a.init, fin, st);
+        a.some_empty = fin && any_empty(cu, nseq);
         if (e != cudaSuccess) return status_of(e);
         ws += offsets_bytes(cu, nseq);
     }

@@ -6,9 +6,10 @@
 // Everything is formed from v = 1 - a = -expm1(-m): 1 - a^2 = v + v a keeps
 // its digits where a is close to 1, which is where such layers work.
 //
-// A block of the prompt's kernels is a tile: kCols channels, two a lane, and
-// kWarps x S consecutive tokens, S a warp, whose inputs stay in registers from
-// the one read to the output.  What a run of tokens does to the state is
+// The blocks of the prompt's kernels, a few on each SM, take one tile after
+// another: kCols channels, two a lane, and kWarps x S consecutive tokens, S a
+// warp, whose inputs stay in registers from the one read to the output; the
+// next tile's are copied into shared memory meanwhile.  What a run of tokens does to the state is
 // h -> A h + H; warps exchange their (A, H) through shared memory, tiles
 // theirs through the workspace (Links).  A run that holds a sequence's
 // boundary does not let the state through, whatever its value: A = -1 says so.
@@ -22,6 +23,7 @@ namespace ssd {
 
 constexpr int kCols = 64;        // channels of a block
 constexpr int kStateEvery = 64;  // tokens between the states kept for the gradient
+constexpr int kSMs = 152;
 constexpr int kGroup = 16;       // tiles from one entry state to the next
 
 // Two channels of one token as they lie in memory.
@@ -84,6 +86,69 @@ __device__ __forceinline__ Two<T> load_two(const T *row, const Lane<PAIRS> &k, f
     }
     return v;
 }
+// The same into shared memory, where the lane itself reads it later: an asynchronous copy, of rows whose elements lie on
+// four-byte boundaries.  `there`: the token exists.
+template <typename T, bool PAIRS>
+constexpr bool kAsync = PAIRS || sizeof(T) == 4;
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
+    if (bytes == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void fetch_two(Two<T> *dst, const T *row, const Lane<PAIRS> &k, bool there, float fill) {
+    if constexpr (kAsync<T, PAIRS>) {
+        const T *p = place(row, k);
+        if constexpr (PAIRS) {
+            if (there && k.in0)
+                copy_async(dst, p, 2 * sizeof(T));
+            else
+                *dst = two_of(T(), fill);
+        } else {
+            float *d = reinterpret_cast<float *>(dst);
+            if (there && k.in0)
+                copy_async(d, p, 4);
+            else
+                d[0] = fill;
+            if (there && k.in1)
+                copy_async(d + 1, p + 32, 4);
+            else
+                d[1] = fill;
+        }
+    } else {
+        *dst = there ? load_two<T, PAIRS>(row, k, fill) : two_of(T(), fill);
+    }
+}
+// The copies of a warp's S tokens from one array, each lane's pair to dst[s * stride + lane].  Where rows lie on 16-byte
+// boundaries (`wide`) a lane copies 16 bytes of one of the rows that an instruction spans, for others to read: a quarter
+// (fp32: half) of the instructions.
+template <typename T, bool PAIRS, int S>
+__device__ __forceinline__ void fetch_rows(Two<T> *dst, int stride, const T *row, int64_t step, const Lane<PAIRS> &k, int lane, int left,
+                                           bool wide, int ch, float fill) {
+    if (PAIRS && wide) {
+        constexpr int CHUNKS = kCols * sizeof(T) / 16, ROWS = 32 / CHUNKS, EACH = 16 / sizeof(T);
+        const int at = lane % CHUNKS, c = k.c0 - 2 * lane + at * EACH, first = lane / CHUNKS;
+        const char *src = reinterpret_cast<const char *>(row + c) + (int64_t)first * step * (int)sizeof(T);
+        char *d = reinterpret_cast<char *>(dst + first * stride) + at * 16;
+        const Two<T> f = two_of(T(), fill);
+#pragma unroll
+        for (int s = 0; s < S; s += ROWS) {
+            if (s + first < left && c < ch) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(d)), "l"(src) : "memory");
+            } else {
+                Two<T> *e = reinterpret_cast<Two<T> *>(d);
+#pragma unroll
+                for (int i = 0; i < EACH / 2; ++i) e[i] = f;
+            }
+            src += step * (ROWS * (int)sizeof(T)), d += ROWS * stride * sizeof(Two<T>);
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s) fetch_two<T, PAIRS>(dst + s * stride + lane, row + step * s, k, s < left, fill);
+    }
+}
 template <typename T, bool PAIRS>
 __device__ __forceinline__ void store_two(T *row, const Lane<PAIRS> &k, float2 f) {
     T *p = place(row, k);
@@ -109,7 +174,7 @@ __device__ __forceinline__ void store_state(float *p, const Lane<PAIRS> &k, floa
     if (k.in1) p[k.c0 + k.step] = v.y;
 }
 
-// rate softplus(decay), once a tile: the library's functions
+// rate softplus(decay), by the library's functions: once a call and channel, by the kernel that clears the links
 __device__ __forceinline__ float decay_rate(float decay, float rate) {
     return rate * (fmaxf(decay, 0.f) + log1pf(expf(-fabsf(decay))));
 }
@@ -218,15 +283,13 @@ __device__ __forceinline__ Run link_wait(const unsigned long long *p, unsigned *
     unsigned long long u = link_load(p), v = link_load(p + 32);
     if ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset) {
         const uint64_t t0 = tc::globaltimer_ns();
-        for (int i = 1;; ++i) {
+        do {
+            __nanosleep(40);  // (other blocks of the SM need the issue slots)
             u = link_load(p), v = link_load(p + 32);
-            if ((unsigned)(u >> 32) != kUnset && (unsigned)(v >> 32) != kUnset) break;
-            if (i % 64 == 0) {
-                const uint64_t spent = tc::globaltimer_ns() - t0;
-                if (spent > 100000000ull) atomicOr(status, 1u);
-                if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
-            }
-        }
+            const uint64_t spent = tc::globaltimer_ns() - t0;
+            if (spent > 100000000ull) atomicOr(status, 1u);
+            if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
+        } while ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset);
     }
     Run r;
     r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
@@ -252,6 +315,16 @@ __device__ __forceinline__ Cuts cuts_of(const Seqs &q, int t0) {
     }
     return c;
 }
+// Every empty sequence's dst = src (zeros without src).
+__device__ __forceinline__ void pass_empty(const Seqs &q, int ch, const float *src, float *dst) {
+    const int *start = q.offsets();
+    for (int s = blockIdx.x; s < q.n; s += gridDim.x) {
+        if (start[s] != start[s + 1]) continue;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < ch; c += blockDim.x) dst[(int64_t)s * ch + c] = src ? src[(int64_t)s * ch + c] : 0.f;
+    }
+}
+
 // The number of a value that is the same in all lanes, as the compiler cannot know.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -267,9 +340,12 @@ struct GatedArgs {
     Rows<const T> x, r, i, z, dy;  // i.p, z.p null: absent
     Rows<T> y, dx, dr, di, dz;     // y.p null: only the kept states are wanted
     const float *decay, *init, *dfinal, *kept;
+    float *rates;  // [ch] rate softplus(decay)
     float *fin, *keep, *dinit, *ddecay_part;  // keep, kept: [b][ceil(L / 64)][ch] states entering every 64 tokens
     float rate;
     int ch, nblk, batch, ntile, nkeep;
+    int tiles, some_empty;  // tiles in all; whether a sequence has no tokens
+    int wide;               // every row that is read lies on a 16-byte boundary
     Seqs seqs;
     Links links;
 };
@@ -279,16 +355,18 @@ ssd_status_t check_gated(const ssd_gated_shape_t *s, const int64_t *cu, int64_t 
 bool gated_inputs_ok(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, bool rows);
 inline int64_t gated_blocks(const ssd_gated_shape_t *s) { return (s->channels + kCols - 1) / kCols; }
 inline int64_t gated_kept(const ssd_gated_shape_t *s) { return (s->seqlen + kStateEvery - 1) / kStateEvery; }
-// Workspace of the links of `rows` block rows of `ntile` tiles each, and their place in it.
-size_t links_bytes(int64_t rows, int64_t ntile);
-cudaError_t place_links(char *ws, int64_t rows, int64_t ntile, Links &l, cudaStream_t st);
+// Workspace of the rates and of the links of `rows` block rows of `ntile` tiles each; their place in it, and the launch that
+// prepares them.
+size_t links_bytes(int64_t ch, int64_t rows, int64_t ntile);
+template <typename T>
+cudaError_t prepare(GatedArgs<T> &a, char *ws, int64_t rows, int64_t ntile, cudaStream_t st);
 // Pairs of channels that lie on their own size's boundary in every row.
 bool rows_pairs(const ssd_rows_t &r, size_t esize, int64_t b, int64_t L);
 template <typename T>
 GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, int64_t nseq);
 bool gated_pairs(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
-// Every empty sequence's dst = src (zeros without src).
-cudaError_t launch_empty(const Seqs &q, const int64_t *cu, int64_t nseq, int64_t ch, const float *src, float *dst, cudaStream_t st);
+bool gated_wide(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
+bool any_empty(const int64_t *cu, int64_t nseq);
 template <typename T>
 cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st);
 size_t gated_fwd_links(const ssd_gated_shape_t *s);

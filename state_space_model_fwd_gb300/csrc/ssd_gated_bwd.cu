@@ -23,16 +23,39 @@ constexpr int kBlocks = 2;  // an SM (bf16)
 constexpr int kTile = kWarps * S;
 static_assert(kTile % kStateEvery == 0, "a tile starts at a kept state");
 
+// The next tile's x, r, i, dy and z: each lane's own.
+template <typename T>
+struct Stage {
+    Two<T> in[5][S][kWarps][32];
+};
+
 template <typename T, bool PAIRS>
 struct Warp {
     Lane<PAIRS> k;
-    int b, t0, L;
-    Cuts cut;
-    f2 rate;  // rate softplus(decay)
+    int later, tile, row, b, t0;  // later: tiles behind this one
+    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
+        : k((n % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch;
+        later = n / rows, tile = a.ntile - 1 - later, row = n % rows, b = row / a.nblk, t0 = tile * tokens + warp * S;
+    }
 };
 template <typename T, bool PAIRS>
-__device__ __forceinline__ f2 state_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const float *states, int s) {
-    return both(load_state(states ? states + (int64_t)seq_from(a.seqs, w.cut.seq, w.t0 + s) * a.ch : nullptr, w.k));
+__device__ __forceinline__ f2 state_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, const float *states, int s) {
+    return both(load_state(states ? states + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch : nullptr, w.k));
+}
+
+// Starts the copies of a tile's inputs.
+template <typename T, bool PAIRS, bool GATE>
+__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Stage<T> &st, int warp, int lane) {
+    const int left = a.seqs.L - w.t0, stride = kWarps * 32;
+    auto rows = [&](int which, const Rows<const T> &r, float fill) {
+        fetch_rows<T, PAIRS, S>(&st.in[which][0][warp][0], stride, r.at(w.b, w.t0), r.rs, w.k, lane, left, a.wide, a.ch, fill);
+    };
+    rows(1, a.r, -30000.f);
+    rows(0, a.x, 0.f);
+    if (a.i.p) rows(2, a.i, 128.f);
+    rows(3, a.dy, 0.f);
+    if (GATE) rows(4, a.z, 0.f);
 }
 
 // What is kept of a token between the passes, two channels each: the gates, v = 1 - a, x, the gradient of h_t by its own
@@ -50,68 +73,57 @@ __device__ __forceinline__ f2 input_of(f2 v, f2 si, f2 x) {  // beta s(i) x
 
 // PLAIN as in the forward kernel.
 template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Kept<T> (&t)[S], f2 &A, f2 &H, f2 &Q) {
-    Two<T> r[S], g[S], dy[S], z[S];
-    {
-        const T *px = a.x.at(w.b, w.t0), *pr = a.r.at(w.b, w.t0), *pi = a.i.p ? a.i.at(w.b, w.t0) : nullptr;
-        const T *pd = a.dy.at(w.b, w.t0), *pz = GATE ? a.z.at(w.b, w.t0) : nullptr;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            t[s].x = two_of(T(), 0.f), r[s] = two_of(T(), -30000.f), g[s] = two_of(T(), 128.f), dy[s] = z[s] = two_of(T(), 0.f);
-            if (PLAIN || w.t0 + s < w.L) {
-                r[s] = load_two<T, PAIRS>(pr + a.r.step(s), w.k, -30000.f);
-                t[s].x = load_two<T, PAIRS>(px + a.x.step(s), w.k, 0.f);
-                if (pi) g[s] = load_two<T, PAIRS>(pi + a.i.step(s), w.k, 128.f);
-                dy[s] = load_two<T, PAIRS>(pd + a.dy.step(s), w.k, 0.f);
-                if constexpr (GATE) z[s] = load_two<T, PAIRS>(pz + a.z.step(s), w.k, 0.f);
-            }
-        }
-    }
+__device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, const Stage<T> &st,
+                                            int warp, int lane, Kept<T> (&t)[S], f2 &A, f2 &H, f2 &Q) {
     A = splat(1.f), H = splat(0.f), Q = splat(0.f);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        t[s].sr = both(sigmoid2(widen(r[s])));
-        t[s].si = both(sigmoid2(widen(g[s])));
+        t[s].x = st.in[0][s][warp][lane];
+        t[s].sr = both(sigmoid2(widen(st.in[1][s][warp][lane])));
+        t[s].si = both(sigmoid2(widen(st.in[2][s][warp][lane])));
         f2 av;
-        decay2<PLAIN>(mul2(w.rate, t[s].sr), t[s].v, av);
+        decay2<PLAIN>(mul2(rate, t[s].sr), t[s].v, av);
         av = one_minus(t[s].v);
-        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) H = state_of(a, w, a.init, s);
+        if (PACKED && !PLAIN && (cut.first >> s & 1)) H = state_of(a, w, cut, a.init, s);
         A = mul2(A, av);
         H = fma2(av, H, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
-        t[s].d = both(widen(dy[s]));
+        t[s].d = both(widen(st.in[3][s][warp][lane]));
         t[s].e = splat(0.f);
         if constexpr (GATE) {
             // silu(z) = z s, its slope s + z s (1 - s)
-            const f2 zf = both(widen(z[s])), sz = both(sigmoid2(widen(z[s]))), gate = mul2(zf, sz);
+            const float2 z = widen(st.in[4][s][warp][lane]);
+            const f2 zf = both(z), sz = both(sigmoid2(z)), gate = mul2(zf, sz);
             t[s].e = mul2(t[s].d, fma2(gate, one_minus(sz), sz));
             t[s].d = mul2(t[s].d, gate);
         }
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
-        if (PACKED && !PLAIN && (w.cut.last >> s & 1)) Q = state_of(a, w, a.dfinal, s);
+        if (PACKED && !PLAIN && (cut.last >> s & 1)) Q = state_of(a, w, cut, a.dfinal, s);
         Q = mul2(one_minus(t[s].v), add2(t[s].d, Q));
     }
 }
 
 // h: the state that enters; c: what comes back from later tokens, and on return what goes back to earlier ones.
 template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Kept<T> (&t)[S], f2 h, f2 &c, f2 &sum) {
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, Kept<T> (&t)[S], f2 h,
+                                             f2 &c, f2 &sum) {
+    const int L = a.seqs.L;
     f2 prev[S];
     T *pz = GATE ? a.dz.at(w.b, w.t0) : nullptr;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        if (PACKED && !PLAIN && (w.cut.first >> s & 1)) h = state_of(a, w, a.init, s);
+        if (PACKED && !PLAIN && (cut.first >> s & 1)) h = state_of(a, w, cut, a.init, s);
         prev[s] = h;
         h = fma2(one_minus(t[s].v), h, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
-        if (GATE && (PLAIN || w.t0 + s < w.L)) store_two<T, PAIRS>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
+        if (GATE && (PLAIN || w.t0 + s < L)) store_two<T, PAIRS>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
     }
     T *px = a.dx.at(w.b, w.t0), *pr = a.dr.at(w.b, w.t0), *pi = a.i.p ? a.di.at(w.b, w.t0) : nullptr;
     sum = splat(0.f);
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
-        if (PACKED && !PLAIN && (w.cut.last >> s & 1)) c = state_of(a, w, a.dfinal, s);
-        const f2 av = one_minus(t[s].v), gh = add2(t[s].d, c), xf = both(widen(t[s].x)), m = mul2(w.rate, t[s].sr);
+        if (PACKED && !PLAIN && (cut.last >> s & 1)) c = state_of(a, w, cut, a.dfinal, s);
+        const f2 av = one_minus(t[s].v), gh = add2(t[s].d, c), xf = both(widen(t[s].x)), m = mul2(rate, t[s].sr);
         const float2 b2 = apart(fma2(t[s].v, av, t[s].v));
         const f2 rb = pack2(rsqrt_approx(fmaxf(b2.x, 1e-37f)), rsqrt_approx(fmaxf(b2.y, 1e-37f))), beta = mul2(both(b2), rb);
         c = mul2(gh, av);
@@ -119,9 +131,9 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
         const f2 sx = mul2(t[s].si, xf);
         const f2 dll = mul2(mul2(c, m), fma2(mul2(sx, av), rb, mul2(prev[s], splat(-1.f))));
         sum = add2(sum, dll);
-        if (PACKED && !PLAIN && (w.cut.first >> s & 1) && a.dinit)
-            store_state(a.dinit + (int64_t)seq_from(a.seqs, w.cut.seq, w.t0 + s) * a.ch, w.k, apart(c));
-        if (PLAIN || w.t0 + s < w.L) {
+        if (PACKED && !PLAIN && (cut.first >> s & 1) && a.dinit)
+            store_state(a.dinit + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch, w.k, apart(c));
+        if (PLAIN || w.t0 + s < L) {
             const f2 gx = mul2(mul2(gh, beta), t[s].si);
             store_two<T, PAIRS>(px + a.dx.step(s), w.k, apart(gx));
             store_two<T, PAIRS>(pr + a.dr.step(s), w.k, apart(mul2(dll, one_minus(t[s].sr))));
@@ -132,97 +144,115 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
 
 template <typename T, bool PAIRS, bool GATE, bool PACKED>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
-    __shared__ float4 fore[kWarps][32], back[kWarps][32];
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
+    __shared__ float4 fore[2][kWarps][32], back[2][kWarps][32];
     __shared__ float4 tiles[kGroup][32];
-    __shared__ float2 enter[32];
-    __shared__ unsigned ticket;
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32;
-    unsigned n = blockIdx.x;
-    if (a.links.run) {
-        if (threadIdx.x == 0) ticket = atomicAdd(a.links.ticket, 1u) + 1u;
-        __syncthreads();
-        n = (unsigned)uniform((int)ticket);
-    }
-    const int rows = a.nblk * a.batch, later = n / rows, row = n % rows, b = row / a.nblk;  // later: tiles behind this one
-    const int tile = a.ntile - 1 - later, L = a.seqs.L;
-    Warp<T, PAIRS> w{Lane<PAIRS>(row % a.nblk, lane, a.ch), b, (tile * nw + warp) * S, L, Cuts{0, 0, b}, 0};
-    const Lane<PAIRS> &k = w.k;
-    if (PACKED && w.t0 < L) {
-        w.cut = cuts_of<S>(a.seqs, w.t0);
-        w.cut.first = (unsigned)uniform((int)w.cut.first), w.cut.last = (unsigned)uniform((int)w.cut.last);
-        w.cut.seq = uniform(w.cut.seq);
-    }
-    const float2 dec = load_state(a.decay, k);
-    const float ra = decay_rate(dec.x, a.rate), rb = decay_rate(dec.y, a.rate);
-    w.rate = pack2(ra, rb);
-    const bool plain = w.t0 + S <= L && !(w.cut.first | w.cut.last) && __all_sync(0xffffffffu, (ra <= 1.f || !k.in0) && (rb <= 1.f || !k.in1));
-
-    Kept<T> t[S];
-    f2 A, H, Q;
-    if (plain)
-        read_tokens<T, PAIRS, GATE, PACKED, true>(a, w, t, A, H, Q);
-    else
-        read_tokens<T, PAIRS, GATE, PACKED, false>(a, w, t, A, H, Q);
-    if (nw > 1) {
-        const float2 fa = apart(A), fh = apart(H), fq = apart(Q);
-        fore[warp][lane] = w.cut.first ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
-        back[warp][lane] = w.cut.last ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
-        __syncthreads();
-    }
+    __shared__ float2 enter[32], sums[2][kWarps][32];
+    __shared__ unsigned ticket[2];
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
+    const bool linked = a.links.run != nullptr;
+    auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
-
-    // What comes back from the tokens after the tile.
-    float2 c = make_float2(0.f, 0.f);
-    if (!PACKED) c = load_state(a.dfinal ? a.dfinal + (int64_t)b * a.ch : nullptr, k);
-    if (a.links.run) {
-        unsigned long long *mine = a.links.run + ((int64_t)row * a.ntile + later) * kCols + lane;
-        const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
-        unsigned long long *entry = a.links.entry + (int64_t)row * groups * kCols + lane;
-        const int in_group = later % kGroup, group = later / kGroup;
-        Run all{};
-        if (warp == 0) {
-            all = run_of(back[nw - 1][lane]);
-            for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[j][lane]));
-            if (in_group != kGroup - 1 && tile > 0) link_store(mine, all);
-        }
-        for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
-            const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
-            tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
-        }
-        if (warp == 0 && group > 0) c = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
-        __syncthreads();
-        if (warp == 0) {
-            for (int j = 0; j < in_group; ++j) c = through(run_of(tiles[j][lane]), c);
-            if (in_group == kGroup - 1 && tile > 0)
-                link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, c)});
-            enter[lane] = c;
-        }
-        __syncthreads();
-        c = enter[lane];
+    if (!a.i.p) {  // no input gate: s(128) = 1
+#pragma unroll
+        for (int s = 0; s < S; ++s) st.in[2][s][warp][lane] = two_of(T(), 128.f);
     }
-    for (int j = nw - 1; j > warp; --j) c = through(run_of(back[j][lane]), c);
-    float2 h = load_state(a.kept + ((int64_t)b * a.nkeep + tile * (kTile / kStateEvery)) * a.ch, k);
-    for (int j = 0; j < warp; ++j) h = through(run_of(fore[j][lane]), h);
-
-    f2 cv = both(c), sum;
-    if (plain)
-        write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, t, both(h), cv, sum);
-    else
-        write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, t, both(h), cv, sum);
-    if (!PACKED && w.t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)b * a.ch, k, apart(cv));
-    if (a.ddecay_part) {
-        const float2 f = apart(sum);
-        if (nw > 1) {
-            __syncthreads();
-            fore[warp][lane] = make_float4(f.x, f.y, 0.f, 0.f);
-            __syncthreads();
-        }
-        if (warp == 0) {
-            float2 s = f;
-            for (int j = 1; j < nw; ++j) s.x += fore[j][lane].x, s.y += fore[j][lane].y;
-            store_state(a.ddecay_part + ((int64_t)tile * a.batch + b) * a.ch, k, s);
-        }
+    wait_previous();
+    if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
+    __syncthreads();
+    int n = uniform((int)ticket[1]);
+    Warp<T, PAIRS> w(a, n, warp, lane, tokens);
+    auto entering = [&](const Warp<T, PAIRS> &w) {
+        return load_state(a.kept + ((int64_t)w.b * a.nkeep + w.tile * (kTile / kStateEvery)) * a.ch, w.k);
+    };
+    float2 rate = make_float2(0.f, 0.f), kept = rate;
+    if (n < a.tiles) {
+        rate = load_state(a.rates, w.k), kept = entering(w);
+        fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane);
     }
+    for (int p = 0; n < a.tiles; p ^= 1) {
+        const Lane<PAIRS> &k = w.k;
+        if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
+        Cuts cut{0, 0, w.b};
+        if (PACKED && w.t0 < L) {
+            cut = cuts_of<S>(a.seqs, w.t0);
+            cut.first = (unsigned)uniform((int)cut.first), cut.last = (unsigned)uniform((int)cut.last), cut.seq = uniform(cut.seq);
+        }
+        float2 h = kept;
+        const f2 rates = both(rate);
+        // What comes back from behind the row, or the group of tiles.
+        float2 c = !PACKED && w.later < kGroup ? load_state(a.dfinal ? a.dfinal + (int64_t)w.b * a.ch : nullptr, k) : make_float2(0.f, 0.f);
+        const bool plain = w.t0 + S <= L && !(cut.first | cut.last) && __all_sync(0xffffffffu, rate.x <= 1.f && rate.y <= 1.f);
+
+        copies_done();
+        __syncwarp();
+        Kept<T> t[S];
+        f2 A, H, Q;
+        if (plain)
+            read_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
+        else
+            read_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
+        {
+            const float2 fa = apart(A), fh = apart(H), fq = apart(Q);
+            fore[p][warp][lane] = cut.first ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
+            back[p][warp][lane] = cut.last ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
+        }
+        __syncthreads();
+        n = uniform((int)ticket[p]);
+        const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        if (n < a.tiles) {
+            rate = load_state(a.rates, after.k), kept = entering(after);
+            fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane);
+        }
+
+        if (linked) {
+            unsigned long long *mine = a.links.run + ((int64_t)w.row * a.ntile + w.later) * kCols + lane;
+            const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
+            unsigned long long *entry = a.links.entry + (int64_t)w.row * groups * kCols + lane;
+            const int in_group = w.later % kGroup, group = w.later / kGroup;
+            Run all{};
+            if (warp == 0) {
+                all = run_of(back[p][nw - 1][lane]);
+                for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[p][j][lane]));
+                if (in_group != kGroup - 1 && w.tile > 0) link_store(mine, all);
+            }
+            for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
+                const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
+                tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
+            }
+            if (warp == 0 && group > 0) c = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
+            __syncthreads();
+            if (warp == 0) {
+                for (int j = 0; j < in_group; ++j) c = through(run_of(tiles[j][lane]), c);
+                if (in_group == kGroup - 1 && w.tile > 0)
+                    link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, c)});
+                enter[lane] = c;
+            }
+            __syncthreads();
+            c = enter[lane];
+        }
+        for (int j = nw - 1; j > warp; --j) c = through(run_of(back[p][j][lane]), c);
+        for (int j = 0; j < warp; ++j) h = through(run_of(fore[p][j][lane]), h);
+
+        f2 cv = both(c), sum;
+        if (plain)
+            write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, rates, t, both(h), cv, sum);
+        else
+            write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, rates, t, both(h), cv, sum);
+        if (!PACKED && w.t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)w.b * a.ch, k, apart(cv));
+        if (a.ddecay_part) {
+            sums[p][warp][lane] = apart(sum);
+            __syncthreads();
+            if (warp == 0) {
+                float2 s = make_float2(0.f, 0.f);
+                for (int j = 0; j < nw; ++j) s.x += sums[p][j][lane].x, s.y += sums[p][j][lane].y;
+                store_state(a.ddecay_part + ((int64_t)w.tile * a.batch + w.b) * a.ch, k, s);
+            }
+        }
+        w = after;
+    }
+    if (PACKED && a.some_empty) pass_empty(a.seqs, a.ch, a.dfinal, a.dinit);
 }
 
 // ddecay[c] = softplus'(decay) / softplus(decay) sum over the tiles' parts, in a fixed order.  The quotient's limit for
@@ -271,7 +301,7 @@ BwdPlan plan_bwd(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq, bo
     p.fwd_links = at;
     if (!with_states) at += gated_fwd_links(s);
     p.links = at;
-    at += links_bytes(rows, ntile);
+    at += links_bytes(s->channels, rows, ntile);
     p.part = at;
     at += align256(sizeof(float) * ntile * s->batch * s->channels);
     p.bytes = at;
@@ -294,7 +324,6 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (cu) {
         bool launched;
         e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws), a.seqs, &launched, st);
-        if (e == cudaSuccess && out->dinit_state) e = launch_empty(a.seqs, cu, nseq, s->channels, dfinal, out->dinit_state, st);
         if (e != cudaSuccess) return status_of(e);
     }
     bool pairs = gated_pairs(s, in);
@@ -306,6 +335,7 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     }
     a.kept = kept, a.dfinal = dfinal;
     a.dy = rows_of<const T>(*dy);
+    a.wide = a.wide && rows_vec(*dy, sizeof(T), s->batch, s->seqlen);
     a.dx = rows_of<T>(out->dx), a.dr = rows_of<T>(out->dr), a.di = rows_of<T>(out->di), a.dz = rows_of<T>(out->dz);
     a.dinit = out->dinit_state;
     a.ddecay_part = out->ddecay ? reinterpret_cast<float *>(ws + p.part) : nullptr;
@@ -314,17 +344,21 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (in->z.data) pairs = pairs && rows_pairs(out->dz, sizeof(T), s->batch, s->seqlen);
     const int64_t ntile = bwd_tiles(s->seqlen), nw = bwd_warps(s->seqlen);
     a.ntile = (int)ntile;
-    e = place_links(ws + p.links, gated_blocks(s) * s->batch, ntile, a.links, st);
+    e = prepare(a, ws + p.links, gated_blocks(s) * s->batch, ntile, st);
     if (e != cudaSuccess) return status_of(e);
-    const unsigned blocks = (unsigned)(ntile * a.nblk * a.batch);
+    a.some_empty = cu && a.dinit && any_empty(cu, nseq);
+    a.tiles = (int)(ntile * a.nblk * a.batch);
+    const int most = kSMs * (sizeof(T) == 2 ? kBlocks : 1);
+    const unsigned blocks = (unsigned)(a.tiles < most ? a.tiles : most);
     auto go = [&](auto pr, auto g, auto c) {
-        gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value><<<blocks, (unsigned)(nw * 32), 0, st>>>(a);
+        auto kernel = gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)(nw * 32), sizeof(Stage<T>), st, true, a);
     };
     auto with_cuts = [&](auto pr, auto g) { cu ? go(pr, g, std::true_type{}) : go(pr, g, std::false_type{}); };
     auto with_gate = [&](auto pr) { a.z.p ? with_cuts(pr, std::true_type{}) : with_cuts(pr, std::false_type{}); };
     pairs ? with_gate(std::true_type{}) : with_gate(std::false_type{});
     timing_mark(st, "gated_bwd");
-    e = cudaGetLastError();
     if (e != cudaSuccess || !out->ddecay) return status_of(e);
     e = launch(gated_ddecay_kernel, dim3((unsigned)((s->channels + 31) / 32)), 1024, 0, st, true, a.ddecay_part,
                ntile * s->batch, s->channels, a.decay, out->ddecay);
