@@ -98,11 +98,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     extern __shared__ __align__(16) uint8_t dynamic[];
     Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
     __shared__ float4 runs[2][kWarps][32];
-    __shared__ float4 tiles[kGroup][32];
-    __shared__ float2 enter[32];
+    __shared__ LinkShared sh;
     __shared__ unsigned ticket[2];
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
     const bool linked = a.links.run != nullptr;
+    auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };  // (it starts at -1)
     if (!a.i.p) {  // no input gate: s(128) = 1
 #pragma unroll
@@ -114,26 +114,30 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     int n = uniform((int)ticket[1]);
     Warp<T, PAIRS> w(a, n, warp, lane, tokens);
     float2 rate = make_float2(0.f, 0.f);
+    Cuts cut{};
+    auto cuts = [&](const Warp<T, PAIRS> &w) {
+        Cuts c{0, 0, w.b};
+        if (w.t0 < L) {
+            if constexpr (PACKED)
+                c = cuts_of<S>(a.seqs, w.t0);
+            else if (w.t0 + S >= L)
+                c.last = 1u << (L - 1 - w.t0);
+        }
+        return c;
+    };
     if (n < a.tiles) {
         rate = load_state(a.rates, w.k);
         fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane, 0);
+        cut = cuts(w);
     }
     for (int p = 0; n < a.tiles; p ^= 1) {
         const Lane<PAIRS> &k = w.k;
         if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
-        Cuts cut{0, 0, w.b};
-        if (w.t0 < L) {
-            if constexpr (PACKED) {
-                cut = cuts_of<S>(a.seqs, w.t0);
-                cut.first = (unsigned)uniform((int)cut.first), cut.last = (unsigned)uniform((int)cut.last), cut.seq = uniform(cut.seq);
-            } else if (w.t0 + S >= L) {
-                cut.last = 1u << (L - 1 - w.t0);
-            }
-        }
         const bool plain = w.t0 + S <= L && !(cut.first | cut.last) && __all_sync(0xffffffffu, rate.x <= 1.f && rate.y <= 1.f);
         // The state that enters the row, or the group of tiles.
         float2 h = !PACKED && w.tile < kGroup ? load_state(a.init ? a.init + (int64_t)w.b * a.ch : nullptr, k) : make_float2(0.f, 0.f);
 
+        Place place(a.links, w.row, w.tile, linked ? a.ntile : 1, warp, nw, lane, true);
         copies_done();
         __syncwarp();
         f2 av[S], uv[S], A, H;
@@ -144,40 +148,22 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         const float2 fa = apart(A), fh = apart(H);
         runs[p][warp][lane] = make_float4(fa.x, fa.y, fh.x, fh.y);
         __syncthreads();
+        Run all{};
+        if (linked && warp == 0) {
+            all = run_of(runs[p][0][lane]);
+            for (int j = 1; j < nw; ++j) all = then(all, run_of(runs[p][j][lane]));
+            place.publish(all);
+        }
         n = uniform((int)ticket[p]);
         const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        Cuts next_cut{};
         if (n < a.tiles) {
             rate = load_state(a.rates, after.k);
             fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane, p ^ 1);
+            next_cut = cuts(after);  // (while others' runs are on their way)
         }
 
-        auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
-        if (linked) {
-            unsigned long long *mine = a.links.run + ((int64_t)w.row * a.ntile + w.tile) * kCols + lane;
-            const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
-            unsigned long long *entry = a.links.entry + (int64_t)w.row * groups * kCols + lane;
-            const int in_group = w.tile % kGroup, group = w.tile / kGroup;
-            Run all{};
-            if (warp == 0) {
-                all = run_of(runs[p][0][lane]);
-                for (int j = 1; j < nw; ++j) all = then(all, run_of(runs[p][j][lane]));
-                if (in_group != kGroup - 1 && w.tile + 1 < a.ntile) link_store(mine, all);
-            }
-            for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
-                const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
-                tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
-            }
-            if (warp == 0 && group > 0) h = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
-            __syncthreads();
-            if (warp == 0) {
-                for (int j = 0; j < in_group; ++j) h = through(run_of(tiles[j][lane]), h);
-                if (in_group == kGroup - 1 && w.tile + 1 < a.ntile)
-                    link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, h)});
-                enter[lane] = h;
-            }
-            __syncthreads();
-            h = enter[lane];
-        }
+        if (linked) h = pass_links(place, a.links, sh, h, all, w.tile >= kGroup, warp, nw, lane);
         for (int j = 0; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
         if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
             store_state(a.keep + ((int64_t)w.b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
@@ -187,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
             else
                 write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, st, warp, lane, p, av, uv, both(h));
         }
-        w = after;
+        w = after, cut = next_cut;
     }
     if (PACKED && a.some_empty) pass_empty(a.seqs, a.ch, a.init, a.fin);
 }

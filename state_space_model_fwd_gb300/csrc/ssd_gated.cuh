@@ -278,24 +278,83 @@ __device__ __forceinline__ unsigned long long link_load(const unsigned long long
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-// Waits until both words are there; gives up after 100 ms and says so in the status word.
-__device__ __forceinline__ Run link_wait(const unsigned long long *p, unsigned *status) {
-    unsigned long long u = link_load(p), v = link_load(p + 32);
-    if ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset) {
-        const uint64_t t0 = tc::globaltimer_ns();
-        do {
-            __nanosleep(40);  // (other blocks of the SM need the issue slots)
-            u = link_load(p), v = link_load(p + 32);
-            const uint64_t spent = tc::globaltimer_ns() - t0;
-            if (spent > 100000000ull) atomicOr(status, 1u);
-            if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
-        } while ((unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset);
+// A run on its way: asked for before a tile's tokens are gone through, and mostly there when they are.
+struct Asked {
+    unsigned long long u, v;
+    __device__ __forceinline__ void ask(const unsigned long long *p) { u = link_load(p), v = link_load(p + 32); }
+    __device__ __forceinline__ bool unset() const { return (unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset; }
+    // Waits until both words are there; gives up after 100 ms and says so in the status word.
+    __device__ __forceinline__ Run wait(const unsigned long long *p, unsigned *status) {
+        if (unset()) ask(p);
+        if (unset()) {
+            const uint64_t t0 = tc::globaltimer_ns();
+            for (;;) {
+                ask(p);
+                if (!unset()) break;
+                const uint64_t spent = tc::globaltimer_ns() - t0;
+                if (spent > 100000000ull) atomicOr(status, 1u);
+                if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
+                __nanosleep(40);  // (other warps of the SM need the issue slots)
+            }
+        }
+        Run r;
+        r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
+        r.H = make_float2(__uint_as_float((unsigned)u), __uint_as_float((unsigned)v));
+        return r;
     }
-    Run r;
-    r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
-    r.H = make_float2(__uint_as_float((unsigned)u), __uint_as_float((unsigned)v));
-    return r;
+};
+
+// A tile's place among the links: `at`, in the order in which states pass.  Warp j looks after the j-th run before it in its
+// group (and the (j + nw)-th), the last warp after the state that enters the group.
+struct Place {
+    unsigned long long *mine, *entry;  // this tile's run; the state that enters its group
+    int in_group;
+    bool more;  // a tile follows in the row
+    Asked run, state;
+    // early: ask now (eight registers until pass_links)
+    __device__ __forceinline__ Place(const Links &l, int row, int at, int ntile, int warp, int nw, int lane, bool early) {
+        const int groups = (ntile + kGroup - 1) / kGroup;
+        mine = l.run + ((int64_t)row * ntile + at) * kCols + lane;
+        entry = l.entry + ((int64_t)row * groups + at / kGroup) * kCols + lane;
+        in_group = at % kGroup, more = at + 1 < ntile;
+        run.u = run.v = state.u = state.v = ~0ull;
+        if (early && warp < in_group) run.ask(mine - (int64_t)(warp + 1) * kCols);
+        if (early && warp == nw - 1 && at >= kGroup) state.ask(entry);
+    }
+    __device__ __forceinline__ void publish(const Run &all) const {
+        if (in_group != kGroup - 1 && more) link_store(mine, all);
+    }
+};
+struct LinkShared {
+    float4 tiles[kGroup][32];
+    float2 group[32], enter[32];
+};
+// The state that enters the tile; `first`: the one that enters the row.  `all`: the tile's own run, published, in warp 0.
+__device__ __forceinline__ float2 pass_links(Place &q, const Links &l, LinkShared &sh, float2 first, const Run &all, bool has_entry, int warp,
+                                             int nw, int lane) {
+    for (int j = warp; j < q.in_group; j += nw) {
+        const unsigned long long *p = q.mine - (int64_t)(j + 1) * kCols;
+        if (j != warp) q.run.ask(p);
+        const Run r = q.run.wait(p, l.status);
+        sh.tiles[j][lane] = make_float4(r.A.x, r.A.y, r.H.x, r.H.y);
+    }
+    if (warp == nw - 1 && has_entry) sh.group[lane] = q.state.wait(q.entry, l.status).H;
+    __syncthreads();
+    if (warp == 0) {
+        float2 h = has_entry ? sh.group[lane] : first;
+        for (int j = q.in_group - 1; j >= 0; --j) {
+            const float4 v = sh.tiles[j][lane];
+            h = through(Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}, h);
+        }
+        if (q.in_group == kGroup - 1 && q.more) link_store(q.entry + kCols, Run{make_float2(0.f, 0.f), through(all, h)});
+        sh.enter[lane] = h;
+    }
+    __syncthreads();
+    return sh.enter[lane];
 }
+
+// The number of a value that is the same in all lanes, as the compiler cannot know.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Sequence boundaries in a warp's tokens t0 .. t0 + S - 1 (the same in all lanes).
 struct Cuts {
@@ -313,6 +372,7 @@ __device__ __forceinline__ Cuts cuts_of(const Seqs &q, int t0) {
         if (d < S && start[s] < q.L) c.first |= 1u << d;
         c.last |= 1u << (d - 1);
     }
+    c.first = (unsigned)uniform((int)c.first), c.last = (unsigned)uniform((int)c.last), c.seq = uniform(c.seq);
     return c;
 }
 // Every empty sequence's dst = src (zeros without src).
@@ -324,9 +384,6 @@ __device__ __forceinline__ void pass_empty(const Seqs &q, int ch, const float *s
         for (int c = threadIdx.x; c < ch; c += blockDim.x) dst[(int64_t)s * ch + c] = src ? src[(int64_t)s * ch + c] : 0.f;
     }
 }
-
-// The number of a value that is the same in all lanes, as the compiler cannot know.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // The sequence of token t, at or after sequence s.
 __device__ __forceinline__ int seq_from(const Seqs &q, int s, int t) {

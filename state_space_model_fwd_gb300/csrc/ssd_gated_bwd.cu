@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gat
     extern __shared__ __align__(16) uint8_t dynamic[];
     Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
     __shared__ float4 fore[2][kWarps][32], back[2][kWarps][32];
-    __shared__ float4 tiles[kGroup][32];
-    __shared__ float2 enter[32], sums[2][kWarps][32];
+    __shared__ LinkShared sh;
+    __shared__ float2 sums[2][kWarps][32];
     __shared__ unsigned ticket[2];
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
     const bool linked = a.links.run != nullptr;
@@ -167,18 +167,15 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gat
         return load_state(a.kept + ((int64_t)w.b * a.nkeep + w.tile * (kTile / kStateEvery)) * a.ch, w.k);
     };
     float2 rate = make_float2(0.f, 0.f), kept = rate;
+    Cuts cut{0, 0, w.b};
     if (n < a.tiles) {
         rate = load_state(a.rates, w.k), kept = entering(w);
         fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane);
+        if (PACKED && w.t0 < L) cut = cuts_of<S>(a.seqs, w.t0);
     }
     for (int p = 0; n < a.tiles; p ^= 1) {
         const Lane<PAIRS> &k = w.k;
         if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
-        Cuts cut{0, 0, w.b};
-        if (PACKED && w.t0 < L) {
-            cut = cuts_of<S>(a.seqs, w.t0);
-            cut.first = (unsigned)uniform((int)cut.first), cut.last = (unsigned)uniform((int)cut.last), cut.seq = uniform(cut.seq);
-        }
         float2 h = kept;
         const f2 rates = both(rate);
         // What comes back from behind the row, or the group of tiles.
@@ -199,38 +196,24 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gat
             back[p][warp][lane] = cut.last ? make_float4(-1.f, -1.f, fq.x, fq.y) : make_float4(fa.x, fa.y, fq.x, fq.y);
         }
         __syncthreads();
+        Run all{};
+        if (linked && warp == 0) {
+            all = run_of(back[p][nw - 1][lane]);
+            for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[p][j][lane]));
+            Place(a.links, w.row, w.later, a.ntile, warp, nw, lane, false).publish(all);
+        }
         n = uniform((int)ticket[p]);
         const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        Cuts next_cut{0, 0, after.b};
         if (n < a.tiles) {
             rate = load_state(a.rates, after.k), kept = entering(after);
             fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane);
+            if (PACKED && after.t0 < L) next_cut = cuts_of<S>(a.seqs, after.t0);
         }
 
         if (linked) {
-            unsigned long long *mine = a.links.run + ((int64_t)w.row * a.ntile + w.later) * kCols + lane;
-            const int64_t groups = (a.ntile + kGroup - 1) / kGroup;
-            unsigned long long *entry = a.links.entry + (int64_t)w.row * groups * kCols + lane;
-            const int in_group = w.later % kGroup, group = w.later / kGroup;
-            Run all{};
-            if (warp == 0) {
-                all = run_of(back[p][nw - 1][lane]);
-                for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[p][j][lane]));
-                if (in_group != kGroup - 1 && w.tile > 0) link_store(mine, all);
-            }
-            for (int j = in_group - 1 - warp; j >= 0; j -= nw) {
-                const Run q = link_wait(mine - (int64_t)(in_group - j) * kCols, a.links.status);
-                tiles[j][lane] = make_float4(q.A.x, q.A.y, q.H.x, q.H.y);
-            }
-            if (warp == 0 && group > 0) c = link_wait(entry + (int64_t)group * kCols, a.links.status).H;
-            __syncthreads();
-            if (warp == 0) {
-                for (int j = 0; j < in_group; ++j) c = through(run_of(tiles[j][lane]), c);
-                if (in_group == kGroup - 1 && w.tile > 0)
-                    link_store(entry + (int64_t)(group + 1) * kCols, Run{make_float2(0.f, 0.f), through(all, c)});
-                enter[lane] = c;
-            }
-            __syncthreads();
-            c = enter[lane];
+            Place place(a.links, w.row, w.later, a.ntile, warp, nw, lane, false);
+            c = pass_links(place, a.links, sh, c, all, w.later >= kGroup, warp, nw, lane);
         }
         for (int j = nw - 1; j > warp; --j) c = through(run_of(back[p][j][lane]), c);
         for (int j = 0; j < warp; ++j) h = through(run_of(fore[p][j][lane]), h);
@@ -250,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gat
                 store_state(a.ddecay_part + ((int64_t)w.tile * a.batch + w.b) * a.ch, k, s);
             }
         }
-        w = after;
+        w = after, cut = next_cut;
     }
     if (PACKED && a.some_empty) pass_empty(a.seqs, a.ch, a.dfinal, a.dinit);
 }
