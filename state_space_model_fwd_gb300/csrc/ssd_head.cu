@@ -6,7 +6,14 @@
 // All products run in one kernel: a block (one on each SM) walks over tiles of
 // 128 rows and up to 256 columns.  One warp copies operands by TMA into a ring
 // of stages, one issues the MMAs into one of two accumulators in TMEM, four
-// read the other accumulator meanwhile, a row of the tile a thread.
+// (eight for the statistics) read the other accumulator meanwhile, a row of the
+// tile a thread.
+//
+// The tensor cores add into fp32 with truncation, so a sum over K comes out
+// too small by 2^-25 or so of itself for every 16 of K: 2.6e-6 at K = 2560,
+// which scales all logits alike and shows in the entropy (1.2e-6 of it).  For
+// the statistics a tile's sum is therefore taken in shares of at most
+// kShare chunks, which are added in registers with rounding.
 #include <cudaTypedefs.h>
 
 #include "ssd_logprob.cuh"
@@ -18,23 +25,29 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024;
-constexpr int kGemmThreads = 256;  // warps: copy, MMA, TMEM, -, four for the accumulators
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kMaxStages = 8, kRing = 4 * (kBM + kBN) * kBK * 2;  // bytes of the ring: four stages of full tiles
+constexpr int kSmem = kRing + 1024;
+constexpr int kShare = 16;  // chunks of K
 constexpr uint64_t kWaitNs = 100000000ull;
 
 // What becomes of an accumulator.
 enum Use { kStats, kGrad, kStore };
+// warps: copy, MMA, TMEM, -, and those that read the accumulators, each 32 rows and (statistics) half of the columns
+constexpr int readers(int use) { return use == kStats ? 8 : 4; }
+constexpr int gemm_threads(int use) { return 128 + 32 * readers(use); }
 
 struct GemmArgs {
     int M, N, K;          // D[M, N] = A[M, K] B[N, K]^T
     int bn, mt, nt, kc;   // columns of a tile; tiles; chunks of kBK
+    int arows;            // rows that are copied of a row tile: what lies behind them is read, and only by rows that are none
+    int stages, abytes, stage_bytes;
+    int shares;           // of K, for the statistics
     int group;            // row tiles that are walked together before the next column tile
     int units, whole, split;  // the first `whole` tiles are a unit each, the others `split` units, a share of K each
     // kStats, kGrad: rows are tokens, columns the vocabulary
     const int64_t *targets;
-    float4 *stats;        // [nt][M] (m, sum, moment, 0)
+    float4 *stats;        // [nt][halves][M] (m, sum, moment, 0)
     float *given;         // [M] the given tokens' logits
     RowGradIn grad;
     bf16 *dz;
@@ -73,7 +86,7 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
 }
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages], ready[2], taken[2], drain;
+    uint64_t full[kMaxStages], empty[kMaxStages], ready[2], taken[2], drain;
     uint32_t tmem;
     int gave_up;
 };
@@ -98,17 +111,27 @@ __device__ __forceinline__ void store16(bf16 *p, const float *v) {
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
+// A place in the ring.
+struct Ring {
+    int stages, s = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
+    __device__ __forceinline__ void next() {
+        if (++s == stages) s = 0, ++round;
+    }
+};
+
 // A_MN, B_MN: the operand lies with its rows (M or N) contiguous, in blocks of 64 rows by kBK.
 template <int USE, bool A_MN, bool B_MN, bool ENT>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(USE), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], 4);
+        for (int i = 0; i < kMaxStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], readers(USE));
         mbar_init(&bars.drain, 1);
         bars.gave_up = 0;
         fence_mbar_init();
@@ -122,117 +145,156 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-    const int bblocks = a.bn / 64;
-
-    if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t bytes = kABytes + a.bn * kBK * 2;
+    const int shares = USE == kStats ? a.shares : 1;
+    // (Statistics: the readers' sums take 128 registers.  384 threads are launched with 168 each: 128 x 56 + 256 x 224.)
+    if (warp < 4) {
+        if constexpr (USE == kStats) reg_dec<56>();
+        if (warp == 0 && lane == 0) {
+            const uint32_t bytes = (a.arows + a.bn) * kBK * 2;
+            Ring r(a.stages);
             uint32_t it = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
                 const Unit t = unit_of(a, u);
-                for (int k = t.k0; k < t.k1; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !(ok = wait_for(&bars.empty[s], (it / kStages - 1) & 1, &bars))) break;
-                    uint8_t *sa = smem + s * kStageBytes, *sb = sa + kABytes;
-                    mbar_arrive_expect_tx(&bars.full[s], bytes);
+                for (int k = t.k0; k < t.k1; ++k, ++it, r.next()) {
+                    if (r.round > 0 && !(ok = wait_for(&bars.empty[r.s], (r.round - 1) & 1, &bars))) break;
+                    uint64_t *full = &bars.full[r.s];
+                    uint8_t *sa = smem + r.s * a.stage_bytes, *sb = sa + a.abytes;
+                    mbar_arrive_expect_tx(full, bytes);
                     if constexpr (A_MN) {
-                        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * 8192, &ma, &bars.full[s], t.m * kBM + j * 64, k * kBK);
+                        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * 8192, &ma, full, t.m * kBM + j * 64, k * kBK);
                     } else {
-                        tma_load_2d(sa, &ma, &bars.full[s], k * kBK, t.m * kBM);
+                        tma_load_2d(sa, &ma, full, k * kBK, t.m * kBM);
                     }
                     if constexpr (B_MN) {
-                        for (int j = 0; j < bblocks; ++j) tma_load_2d(sb + j * 8192, &mb, &bars.full[s], t.n * a.bn + j * 64, k * kBK);
+                        for (int j = 0; j < a.bn / 64; ++j) tma_load_2d(sb + j * 8192, &mb, full, t.n * a.bn + j * 64, k * kBK);
                     } else {
-                        tma_load_2d(sb, &mb, &bars.full[s], k * kBK, t.n * a.bn);
+                        tma_load_2d(sb, &mb, full, k * kBK, t.n * a.bn);
                     }
                 }
             }
             // no block ends with copies in flight
-            for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, kWaitNs / 5);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
+            for (uint32_t i = it < (uint32_t)a.stages ? 0 : it - a.stages; i < it; ++i)
+                mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1, kWaitNs / 5);
+        } else if (warp == 1 && lane == 0) {
             const uint32_t idesc = idesc_bf16(kBM, a.bn, A_MN, B_MN);
-            uint32_t it = 0, n = 0;
+            Ring r(a.stages);
+            uint32_t n = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x, ++n) {
+            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
                 const Unit t = unit_of(a, u);
-                const uint32_t acc = n & 1, d = tmem + acc * kBN;
-                if (n >= 2 && !(ok = wait_for(&bars.taken[acc], (n / 2 - 1) & 1, &bars))) break;
-                tc_fence_after();
-                for (int k = t.k0; k < t.k1; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!(ok = wait_for(&bars.full[s], (it / kStages) & 1, &bars))) break;
+                for (int q = 0; q < shares && ok; ++q, ++n) {
+                    const int k0 = USE == kStats ? a.kc * q / shares : t.k0, k1 = USE == kStats ? a.kc * (q + 1) / shares : t.k1;
+                    const uint32_t acc = n & 1, d = tmem + acc * kBN;
+                    if (n >= 2 && !(ok = wait_for(&bars.taken[acc], (n / 2 - 1) & 1, &bars))) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kABytes;
-                    const uint64_t da = A_MN ? sdesc(sa, 8192, 1024) : sdesc(sa, 16, 1024);
-                    const uint64_t db = B_MN ? sdesc(sb, 8192, 1024) : sdesc(sb, 16, 1024);
+                    for (int k = k0; k < k1; ++k, r.next()) {
+                        if (!(ok = wait_for(&bars.full[r.s], r.round & 1, &bars))) break;
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + r.s * a.stage_bytes), sb = sa + a.abytes;
+                        const uint64_t da = A_MN ? sdesc(sa, 8192, 1024) : sdesc(sa, 16, 1024);
+                        const uint64_t db = B_MN ? sdesc(sb, 8192, 1024) : sdesc(sb, 16, 1024);
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j)
-                        mma_bf16(d, desc_add(da, j * (A_MN ? 2048 : 32)), desc_add(db, j * (B_MN ? 2048 : 32)), idesc,
-                                 j > 0 || k > t.k0);
-                    mma_commit(&bars.empty[s]);
+                        for (int j = 0; j < kBK / 16; ++j)
+                            mma_bf16(d, desc_add(da, j * (A_MN ? 2048 : 32)), desc_add(db, j * (B_MN ? 2048 : 32)), idesc,
+                                     j > 0 || k > k0);
+                        mma_commit(&bars.empty[r.s]);
+                    }
+                    if (ok) mma_commit(&bars.ready[acc]);
                 }
-                if (!ok) break;
-                mma_commit(&bars.ready[acc]);
             }
             mma_commit(&bars.drain);  // nor with MMAs
             mbar_wait(&bars.drain, 0, kWaitNs / 5);
         }
-    } else if (warp >= 4) {
-        const int q = warp - 4;
+    } else {
+        if constexpr (USE == kStats) reg_inc<224>();
+        const int q = warp % 4, half = (warp - 4) / 4, first = half * (kBN / 2);  // (a warp reads the 32 rows of its number mod 4)
         uint32_t n = 0;
-        for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++n) {
+        for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
             const Unit t = unit_of(a, u);
-            const uint32_t acc = n & 1, at = tmem + acc * kBN + ((uint32_t)(q * 32) << 16);
             const int row = t.m * kBM + q * 32 + lane, c0 = t.n * a.bn;
             const bool live = row < a.M;
-            int64_t target = -1;
-            Stat st{-INFINITY, 0.f, 0.f};
-            RowGrad g{};
-            if constexpr (USE == kStats) target = live && a.targets ? a.targets[row] - c0 : -1;
-            if constexpr (USE == kGrad) {
-                if (live) g = row_grad(a.grad, row, a.N);
-            }
-            if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
-            tc_fence_after();
-            for (int c = 0; c < a.bn; c += 32) {
-                float z[32];
-                tmem_ld32(at + c, z);
-                tmem_ld_wait();
-                if constexpr (USE == kStats) {
-                    const int limit = min(a.N - c0, a.bn);  // (a tile's columns are a multiple of 16)
-                    if (c + 32 > limit) {
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+            if constexpr (USE == kStats) {
+                const int64_t target = live && a.targets ? a.targets[row] - c0 : -1;
+                const int limit = min(a.N - c0, a.bn);  // (a tile's columns are a multiple of 16)
+                Stat st{-INFINITY, 0.f, 0.f};
+                float part[kBN / 2];
+                bool ok = true;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= limit) z[i] = -INFINITY;
-                    }
-                    if (target >= c && target < c + 32 && target < limit) {
-                        float v = z[0];
+                for (int i = 0; i < kBN / 2; ++i) part[i] = 0.f;
+                for (int share = 0; share + 1 < shares; ++share, ++n) {
+                    const uint32_t acc = n & 1;
+                    if (!(ok = wait_for(&bars.ready[acc], (n / 2) & 1, &bars))) break;
+                    tc_fence_after();
 #pragma unroll
-                        for (int i = 1; i < 32; ++i) v = target == c + i ? z[i] : v;
-                        a.given[row] = v;
-                    }
-                    add_to(st, z);
-                } else if constexpr (USE == kGrad) {
-                    if (live) {
-                        bf16 *p = a.dz + row * a.dz_pitch + c0 + c;
+                    for (int c = 0; c < kBN / 2; c += 16) {
+                        if (first + c < a.bn) {
+                            float z[16];
+                            tmem_ld16(lanes + acc * kBN + first + c, z);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            z[i] = g.none ? 0.f : grad_of<ENT>(g, z[i]);
+                            for (int i = 0; i < 16; ++i) part[c + i] += z[i];
                         }
-                        if (g.target >= c0 + c && g.target < c0 + c + 32 && !g.none) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c0 + c + i == g.target) z[i] += g.dlp;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (c0 + c + i < a.dz_pitch) store16(p + i, z + i);
                     }
-                } else {
-                    if (t.part >= 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.taken[acc]);
+                }
+                const uint32_t acc = n & 1;
+                if (!ok || !wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
+                ++n;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kBN / 2; c += 16) {
+                    const int at = first + c;
+                    if (at < limit) {
+                        float z[16];
+                        tmem_ld16(lanes + acc * kBN + at, z);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) z[i] = at + i < limit ? z[i] + part[c + i] : -INFINITY;
+                        if (target >= at && target < at + 16 && target < limit) {
+                            float v = z[0];
+#pragma unroll
+                            for (int i = 1; i < 16; ++i) v = target == at + i ? z[i] : v;
+                            a.given[row] = v;
+                        }
+                        add_to(st, z);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.taken[acc]);
+                if (live && first < a.bn) a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
+            } else {
+                const uint32_t acc = n & 1, at = lanes + acc * kBN;
+                RowGrad g{};
+                if constexpr (USE == kGrad) {
+                    if (live) g = row_grad(a.grad, row, a.N);
+                }
+                if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
+                ++n;
+                tc_fence_after();
+                for (int c = 0; c < a.bn; c += 32) {
+                    float z[32];
+                    tmem_ld32(at + c, z);
+                    tmem_ld_wait();
+                    if constexpr (USE == kGrad) {
+                        if (live) {
+                            bf16 *p = a.dz + row * a.dz_pitch + c0 + c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) z[i] = g.none ? 0.f : grad_of<ENT>(g, z[i]);
+                            if (g.target >= c0 + c && g.target < c0 + c + 32 && !g.none) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (c0 + c + i == g.target) z[i] += g.dlp;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                if (c0 + c + i < a.dz_pitch) store16(p + i, z + i);
+                        }
+                    } else if (t.part >= 0) {
                         float *p = a.parts + ((int64_t)t.part * kBM + q * 32 + lane) * a.bn + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
@@ -244,12 +306,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             if (c0 + c + i < a.N) store16(p + i, z + i);
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.taken[acc]);
-            if constexpr (USE == kStats) {
-                if (live) a.stats[(int64_t)t.n * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.taken[acc]);
             }
         }
     }
@@ -259,22 +318,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
-// The numbers of every row from its tiles' statistics, joined in the tiles' order by one thread of 8 each, then the eight.
+// The numbers of every row from its tiles' statistics.  A block has `per` neighbouring rows (1, or 8 where there are many) and
+// joins a row's tiles in 256 / per threads, then those, in a fixed order.
 __global__ void __launch_bounds__(256) head_rows_kernel(const float4 *stats, const float *given, const int64_t *targets, int rows,
-                                                        int nt, int vocab, float *logprob, float *lse, float *entropy) {
-    __shared__ Stat part[8][32];
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32, row = blockIdx.x * 32 + lane;
+                                                        int nt, int vocab, int per, float *logprob, float *lse, float *entropy) {
+    __shared__ Stat part[256];
+    wait_previous();
+    const int in = threadIdx.x % per, w = threadIdx.x / per, step = 256 / per, row = blockIdx.x * per + in;
     Stat st{-INFINITY, 0.f, 0.f};
     if (row < rows) {
-        for (int n = w; n < nt; n += 8) {
-            const float4 v = stats[(int64_t)n * rows + row];
-            st = join(st, Stat{v.x, v.y, v.z});
+        for (int n = w; n < nt; n += 4 * step) {
+            float4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = n + i * step < nt ? stats[(int64_t)(n + i * step) * rows + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st = join(st, Stat{v[i].x, v[i].y, v[i].z});
         }
     }
-    part[w][lane] = st;
-    __syncthreads();
+    part[threadIdx.x] = st;
+    for (int d = step / 2; d; d /= 2) {
+        __syncthreads();
+        if (w < d) part[threadIdx.x] = st = join(st, part[threadIdx.x + d * per]);
+    }
     if (w || row >= rows) return;
-    for (int k = 1; k < 8; ++k) st = join(st, part[k][lane]);
     const float l = lse_of(st);
     if (lse) lse[row] = l;
     if (entropy) entropy[row] = entropy_of(st);
@@ -331,11 +398,15 @@ bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t p
 constexpr int kSMs = 152;
 
 // Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share.
-GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split) {
+GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split, bool a_mn = false) {
     GemmArgs a{};
     a.M = (int)M, a.N = (int)N, a.K = (int)K, a.bn = bn;
     a.mt = (int)((M + kBM - 1) / kBM), a.nt = (int)((N + bn - 1) / bn), a.kc = (int)((K + kBK - 1) / kBK);
     a.group = 32;
+    a.arows = M < kBM && !a_mn ? (int)((M + 7) / 8 * 8) : kBM;
+    a.abytes = (a.arows * kBK * 2 + 1023) / 1024 * 1024, a.stage_bytes = a.abytes + (bn * kBK * 2 + 1023) / 1024 * 1024;
+    a.stages = kRing / a.stage_bytes < kMaxStages ? kRing / a.stage_bytes : kMaxStages;
+    a.shares = (a.kc + kShare - 1) / kShare;
     const int tiles = a.mt * a.nt;
     a.whole = tiles, a.split = 1;
     const int rest = tiles % kSMs;
@@ -364,6 +435,8 @@ int forward_columns(int64_t T, int64_t V) {
     return best;
 }
 
+int halves(const GemmArgs &a) { return a.bn > kBN / 2 ? 2 : 1; }
+
 struct HeadPlan {
     size_t stats, given, dz, parts, bytes;
     int64_t pitch;
@@ -373,7 +446,7 @@ HeadPlan plan_fwd(const ssd_head_shape_t *s) {
     HeadPlan p{};
     p.z = plan_gemm(s->rows, s->vocab, s->dim, forward_columns(s->rows, s->vocab), false);
     p.stats = 0;
-    p.given = align256(sizeof(float4) * p.z.nt * s->rows);
+    p.given = align256(sizeof(float4) * p.z.nt * halves(p.z) * s->rows);
     p.bytes = p.given + align256(sizeof(float) * s->rows);
     return p;
 }
@@ -381,7 +454,7 @@ HeadPlan plan_bwd(const ssd_head_shape_t *s) {
     HeadPlan p{};
     p.z = plan_gemm(s->rows, s->vocab, s->dim, fit_columns(s->vocab), false);
     p.dh = plan_gemm(s->rows, s->dim, s->vocab, fit_columns(s->dim), true);
-    p.dw = plan_gemm(s->vocab, s->dim, s->rows, fit_columns(s->dim), true);
+    p.dw = plan_gemm(s->vocab, s->dim, s->rows, fit_columns(s->dim), true, true);
     p.pitch = (s->vocab + 63) / 64 * 64;
     p.dz = 0;
     p.parts = align256(2 * s->rows * p.pitch);
@@ -396,7 +469,7 @@ cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArg
     // (set on every call: cheap, and right for each device and context)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.units < kSMs ? a.units : kSMs), kGemmThreads, kSmem, st>>>(ma, mb, a);
+    kernel<<<(unsigned)(a.units < kSMs ? a.units : kSMs), gemm_threads(USE), kSmem, st>>>(ma, mb, a);
     timing_mark(st, name);
     return cudaGetLastError();
 }
@@ -453,7 +526,7 @@ ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_
     if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     CUtensorMap mh, mw;
-    if (!map_of(&mh, hidden->data, T, D, pitch_of(*hidden, T, D), kBM) ||
+    if (!map_of(&mh, hidden->data, T, D, pitch_of(*hidden, T, D), p.z.arows) ||
         !map_of(&mw, weight->data, V, D, pitch_of(*weight, V, D), p.z.bn))
         return SSD_ERR_CUDA;
     GemmArgs a = p.z;
@@ -465,9 +538,11 @@ ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_
     timing_begin(stream);
     e = run_gemm<kStats, false, false, false>(mh, mw, a, "head_logprob", stream);
     if (e != cudaSuccess) return status_of(e);
-    head_rows_kernel<<<(unsigned)((T + 31) / 32), 256, 0, stream>>>(a.stats, a.given, a.targets, (int)T, a.nt, (int)V, logprob, lse, entropy);
+    const int per = T > 8 * kSMs ? 8 : 1;
+    e = launch(head_rows_kernel, dim3((unsigned)((T + per - 1) / per)), 256, 0, stream, true, a.stats, a.given, a.targets, (int)T,
+               a.nt * halves(a), (int)V, per, logprob, lse, entropy);
     timing_mark(stream, "head_rows");
-    return status_of(cudaGetLastError());
+    return status_of(e);
 }
 
 ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_t *hidden, const ssd_rows_t *weight,
@@ -496,8 +571,8 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     const int64_t hp = pitch_of(*hidden, T, D), wp = pitch_of(*weight, V, D);
     CUtensorMap mh, mw, mz, mz_t, mw_t, mh_t;
     // dz: only its V columns are read, whatever lies behind them
-    if (!map_of(&mh, hidden->data, T, D, hp, kBM) || !map_of(&mw, weight->data, V, D, wp, p.z.bn) ||
-        !map_of(&mz, dz, T, V, p.pitch, kBM) || !map_of(&mw_t, weight->data, V, D, wp, kBK) ||
+    if (!map_of(&mh, hidden->data, T, D, hp, p.z.arows) || !map_of(&mw, weight->data, V, D, wp, p.z.bn) ||
+        !map_of(&mz, dz, T, V, p.pitch, p.dh.arows) || !map_of(&mw_t, weight->data, V, D, wp, kBK) ||
         !map_of(&mz_t, dz, T, V, p.pitch, kBK) || !map_of(&mh_t, hidden->data, T, D, hp, kBK))
         return SSD_ERR_CUDA;
     unsigned *status = nullptr;
