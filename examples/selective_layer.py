@@ -1,9 +1,13 @@
-"""Two small state-space models built from the library's operators.
+"""Small recurrent models built from the library's operators.
 
 ChannelModel: blocks of [norm | projection | short convolution | channel scan
 with its gate | projection], the norm that opens a block adding the previous
 block's output to the residual stream.  It trains (the operators' gradients
-as autograd functions below), reads prompts, and continues token by token.
+as autograd functions below) on the given tokens' log-probabilities, which in
+bf16 come straight from the hidden states, reads prompts, continues token by
+token and lists the alternatives of an answer.
+
+GatedModel: the same around the gated scan.
 
 HeadBlock: a Mamba-2-shaped block around the chunked scan ssd_fwd: the
 convolution writes x, B and C as the scan takes them, the norm gates its
@@ -66,6 +70,49 @@ class AddNorm(torch.autograd.Function):
         return dx, dweight, dres
 
 
+class GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, decay, i, z):
+        y, _, states = ssd.ssd_gated_scan_fwd(x, r, decay, i, z, return_final_state=False, return_chunk_states=True)
+        ctx.save_for_backward(x, r, decay, i, z, states)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        *inputs, states = ctx.saved_tensors
+        return ssd.ssd_gated_scan_bwd(dy.contiguous(), *inputs, chunk_states=states)[:5]
+
+
+class TokenLogprob(torch.autograd.Function):
+    """log-probabilities of the targets from logits"""
+
+    @staticmethod
+    def forward(ctx, logits, targets):
+        logprob, lse, _, _, _ = ssd.ssd_token_logprob_fwd(logits, targets, return_entropy=False)
+        ctx.save_for_backward(logits, targets, lse)
+        return logprob
+
+    @staticmethod
+    def backward(ctx, dlogprob):
+        logits, targets, lse = ctx.saved_tensors
+        return ssd.ssd_token_logprob_bwd(logits, targets, lse, dlogprob=dlogprob.contiguous()), None
+
+
+class HeadLogprob(torch.autograd.Function):
+    """the same from hidden states and the output weights, without logits"""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets):
+        logprob, lse, _ = ssd.ssd_head_logprob_fwd(hidden, weight, targets, return_entropy=False)
+        ctx.save_for_backward(hidden, weight, targets, lse)
+        return logprob
+
+    @staticmethod
+    def backward(ctx, dlogprob):
+        hidden, weight, targets, lse = ctx.saved_tensors
+        return (*ssd.ssd_head_logprob_bwd(hidden, weight, targets, lse, dlogprob=dlogprob.contiguous()), None)
+
+
 # ---------------------------------------------------------------------------
 # a model of channel-scan blocks
 # ---------------------------------------------------------------------------
@@ -125,23 +172,80 @@ class ChannelBlock(torch.nn.Module):
         return y @ self.w_out.t(), residual
 
 
+class GatedBlock(torch.nn.Module):
+    def __init__(self, dim, inner, width=4, dtype=torch.bfloat16):
+        super().__init__()
+        self.inner = inner
+        lin = lambda i, o: torch.nn.Parameter((torch.randn(o, i) / math.sqrt(i)).to(dtype))
+        f32 = lambda v: torch.nn.Parameter(v.float())
+        self.norm = f32(torch.ones(dim))
+        self.w_in, self.w_gates, self.w_out = lin(dim, 2 * inner), lin(inner, 2 * inner), lin(inner, dim)
+        self.conv_w, self.conv_b = f32(torch.randn(inner, width) / math.sqrt(width)), f32(torch.zeros(inner))
+        sp = -torch.log(0.9 + 0.099 * torch.rand(inner))  # a^rate between 0.9 and 0.999
+        self.decay = f32(sp + torch.log(-torch.expm1(-sp)))
+
+    def parts(self, h):
+        xz = h @ self.w_in.t()
+        return xz[..., :self.inner], xz[..., self.inner:]
+
+    def gates(self, x):
+        g = x @ self.w_gates.t()
+        return g[..., :self.inner], g[..., self.inner:]
+
+    def forward(self, x, residual):
+        h, residual = AddNorm.apply(x, self.norm, residual)
+        x, z = self.parts(h)
+        x = Conv.apply(x, self.conv_w, self.conv_b)
+        r, i = self.gates(x)
+        return GatedScan.apply(x, r, self.decay, i, z) @ self.w_out.t(), residual
+
+    @torch.no_grad()
+    def prompt(self, x, residual):
+        h, residual = ssd.ssd_block_norm_fwd(x, self.norm.data, residual=residual)
+        x, z = self.parts(h)
+        x, conv = ssd.ssd_conv_fwd(x, self.conv_w.data, self.conv_b.data)
+        r, i = self.gates(x)
+        y, state = ssd.ssd_gated_scan_fwd(x, r, self.decay.data, i, z)
+        return y @ self.w_out.t(), residual, (conv, state)
+
+    @torch.no_grad()
+    def token(self, x, residual, cache):
+        conv, state = cache
+        h, residual = ssd.ssd_block_norm_fwd(x, self.norm.data, residual=residual, residual_out=residual)
+        x, z = self.parts(h)
+        x = ssd.ssd_conv_step(x, self.conv_w.data, self.conv_b.data, state=conv)
+        r, i = self.gates(x)
+        return ssd.ssd_gated_scan_step(x, r, self.decay.data, i, z, state=state) @ self.w_out.t(), residual
+
+
 class ChannelModel(torch.nn.Module):
+    block = ChannelBlock
+
     def __init__(self, vocab=128, dim=64, inner=128, blocks=2, dtype=torch.bfloat16):
         super().__init__()
         self.embed = torch.nn.Parameter((0.5 * torch.randn(vocab, dim)).to(dtype))
-        self.blocks = torch.nn.ModuleList(ChannelBlock(dim, inner, dtype=dtype) for _ in range(blocks))
+        self.blocks = torch.nn.ModuleList(self.block(dim, inner, dtype=dtype) for _ in range(blocks))
         self.norm = torch.nn.Parameter(torch.ones(dim))
 
     def start(self, ids):
         x = self.embed[ids]
         return x, torch.zeros(x.shape, device=x.device)  # the residual stream in fp32
 
-    def forward(self, ids):
+    def hidden(self, ids):
         x, residual = self.start(ids)
         for block in self.blocks:
             x, residual = block(x, residual)
-        h, _ = AddNorm.apply(x, self.norm, residual)
-        return (h @ self.embed.t()).float()
+        return AddNorm.apply(x, self.norm, residual)[0]
+
+    def forward(self, ids):
+        return (self.hidden(ids) @ self.embed.t()).float()
+
+    def logprobs(self, ids, targets):
+        """Of targets [b, L] (negative: none, 0) after each of ids [b, L]."""
+        h = self.hidden(ids)
+        if h.dtype == torch.bfloat16:
+            return HeadLogprob.apply(h, self.embed, targets)
+        return TokenLogprob.apply(h @ self.embed.t(), targets)
 
     @torch.no_grad()
     def prompt(self, ids):
@@ -162,13 +266,16 @@ class ChannelModel(torch.nn.Module):
         return (h @ self.embed.t()).float()
 
 
+class GatedModel(ChannelModel):
+    block = GatedBlock
+
+
 def train(model, ids, steps=20, lr=0.02):
     """Next-token training on one batch; the losses."""
     opt = torch.optim.Adam(model.parameters(), lr=lr)
     losses = []
     for _ in range(steps):
-        logits = model(ids[:, :-1].contiguous())
-        loss = torch.nn.functional.cross_entropy(logits.flatten(0, 1), ids[:, 1:].flatten())
+        loss = -model.logprobs(ids[:, :-1].contiguous(), ids[:, 1:].contiguous()).mean()
         opt.zero_grad()
         loss.backward()
         opt.step()
@@ -185,6 +292,20 @@ def generate(model, ids, count):
         last = model.token(last, caches).argmax(-1)
         out.append(last)
     return torch.stack(out, 1)
+
+
+@torch.no_grad()
+def answer(model, ids, count, top=4):
+    """The greedy continuation [b, count] with every token's log-probability [b, count] and the `top` most probable tokens
+    in its place, [b, count, top]."""
+    logits, caches = model.prompt(ids)
+    logits, out = logits[:, -1], []
+    while True:
+        _, _, _, value, index = ssd.ssd_token_logprob_fwd(logits, top=top, return_entropy=False)
+        out.append((index[:, 0], value[:, 0], index))
+        if len(out) == count:
+            return tuple(torch.stack(v, 1) for v in zip(*out))
+        logits = model.token(index[:, 0].contiguous(), caches)
 
 
 # ---------------------------------------------------------------------------
@@ -237,6 +358,11 @@ def main():
     losses = train(model, ids)
     print(f"training: loss {losses[0]:.3f} -> {losses[-1]:.3f}")
     print("continuation:", generate(model, ids[:1, :16].contiguous(), 8).tolist()[0])
+    gated = GatedModel().cuda()
+    losses = train(gated, ids)
+    print(f"gated model: loss {losses[0]:.3f} -> {losses[-1]:.3f}")
+    tokens, logprobs, others = answer(gated, ids[:1, :16].contiguous(), 8)
+    print("answer:", tokens.tolist()[0], [round(v, 2) for v in logprobs.tolist()[0]], "instead of the last:", others[0, -1, 1:].tolist())
     block = HeadBlock()
     u = torch.randn(2, 100, 256, device="cuda").bfloat16()
     whole, _ = block.prompt(u)

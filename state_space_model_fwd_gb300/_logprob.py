@@ -49,6 +49,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _row_outputs(lead, like, targets, return_entropy):
+    """(logprob or None, lse, entropy or None), from one allocation: each costs a few microseconds, as long as a call for one
+    token takes on the GPU."""
+    n = 1 + (targets is not None) + bool(return_entropy)
+    parts = list(_empty((n, *lead), _F32, like).unbind(0))
+    return parts.pop(0) if targets is not None else None, parts.pop(0), parts.pop(0) if return_entropy else None
+
+
 @_on_stream
 def ssd_token_logprob_fwd(logits, targets=None, *, top=0, return_entropy=True):
     """Log-probabilities of the given tokens, entropy and top alternatives:
@@ -65,9 +73,7 @@ def ssd_token_logprob_fwd(logits, targets=None, *, top=0, return_entropy=True):
     shape, dev, lead = _shape_of(logits, top)
     zr = _norm_rows(logits, "logits", logits.dtype, logits.shape, dev)
     tp = _flat(targets, "targets", torch.int64, lead, dev)
-    logprob = None if targets is None else _empty(lead, _F32, logits)
-    lse = _empty(lead, _F32, logits)
-    entropy = _empty(lead, _F32, logits) if return_entropy else None
+    logprob, lse, entropy = _row_outputs(lead, logits, targets, return_entropy)
     value = index = None
     if top:
         value, index = _empty((*lead, top), _F32, logits), _empty((*lead, top), torch.int64, logits)
@@ -132,9 +138,7 @@ def ssd_head_logprob_fwd(hidden, weight, targets=None, *, return_entropy=True, w
     lib = _lib()
     shape, hr, wr, dev, lead = _head(hidden, weight)
     tp = _flat(targets, "targets", torch.int64, lead, dev)
-    logprob = None if targets is None else _empty(lead, _F32, hidden)
-    lse = _empty(lead, _F32, hidden)
-    entropy = _empty(lead, _F32, hidden) if return_entropy else None
+    logprob, lse, entropy = _row_outputs(lead, hidden, targets, return_entropy)
     ws = _workspace(workspace, lib.ssd_head_logprob_workspace_size(ctypes.byref(shape)), hidden)
     st = lib.ssd_head_logprob_fwd(ctypes.byref(shape), ctypes.byref(hr), ctypes.byref(wr), tp, _ptr(logprob), lse.data_ptr(),
                                   _ptr(entropy), ws.data_ptr(), ws.numel() * ws.element_size(),

@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int S = 8;        // tokens a warp
-constexpr int kBlocks = 2;  // an SM (bf16)
+constexpr int kBlocks = 2;  // an SM
 constexpr int kTile = kWarps * S;
 static_assert(kTile % kStateEvery == 0, "a tile starts at a kept state");
 
@@ -143,7 +143,7 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
 }
 
 template <typename T, bool PAIRS, bool GATE, bool PACKED>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? kBlocks : 1) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
     __shared__ float4 fore[2][kWarps][32], back[2][kWarps][32];
@@ -331,7 +331,7 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (e != cudaSuccess) return status_of(e);
     a.some_empty = cu && a.dinit && any_empty(cu, nseq);
     a.tiles = (int)(ntile * a.nblk * a.batch);
-    const int most = kSMs * (sizeof(T) == 2 ? kBlocks : 1);
+    const int most = kSMs * (kBlocks);
     const unsigned blocks = (unsigned)(a.tiles < most ? a.tiles : most);
     auto go = [&](auto pr, auto g, auto c) {
         auto kernel = gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value>;
