@@ -50,11 +50,9 @@ def _ptr(t):
 
 
 def _row_outputs(lead, like, targets, return_entropy):
-    """(logprob or None, lse, entropy or None), from one allocation: each costs a few microseconds, as long as a call for one
-    token takes on the GPU."""
-    n = 1 + (targets is not None) + bool(return_entropy)
-    parts = list(_empty((n, *lead), _F32, like).unbind(0))
-    return parts.pop(0) if targets is not None else None, parts.pop(0), parts.pop(0) if return_entropy else None
+    """(logprob or None, lse, entropy or None)"""
+    return (None if targets is None else _empty(lead, _F32, like), _empty(lead, _F32, like),
+            _empty(lead, _F32, like) if return_entropy else None)
 
 
 @_on_stream
