@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         return c;
     };
     if (n < a.tiles) {
-        rate = load_state(a.rates, w.k);
+        rate = rates_of(a, w.k);
         fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane, 0);
         cut = cuts(w);
     }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
         Cuts next_cut{};
         if (n < a.tiles) {
-            rate = load_state(a.rates, after.k);
+            rate = rates_of(a, after.k);
             fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane, p ^ 1);
             next_cut = cuts(after);  // (while others' runs are on their way)
         }
@@ -274,23 +274,22 @@ __global__ void __launch_bounds__(256) gated_prepare_kernel(uint4 *links, int64_
 }  // namespace
 
 size_t links_bytes(int64_t ch, int64_t rows, int64_t ntile) {
-    const size_t rates = align256(sizeof(float) * ch);
-    if (ntile <= 1) return rates;
-    return rates + align256(8 * kCols * rows * (ntile + (ntile + kGroup - 1) / kGroup) + 256);
+    if (ntile <= 1) return 0;
+    return align256(sizeof(float) * ch) + align256(8 * kCols * rows * (ntile + (ntile + kGroup - 1) / kGroup) + 256);
 }
 template <typename T>
 cudaError_t prepare(GatedArgs<T> &a, char *ws, int64_t rows, int64_t ntile, cudaStream_t st) {
     a.links = Links{};
+    a.rates = nullptr;
+    if (ntile <= 1) return cudaSuccess;
+    const cudaError_t e = device_status_word(&a.links.status);
+    if (e != cudaSuccess) return e;
     a.rates = reinterpret_cast<float *>(ws);
     const size_t before = align256(sizeof(float) * a.ch), bytes = links_bytes(a.ch, rows, ntile) - before;
     ws += before;
-    if (bytes) {
-        const cudaError_t e = device_status_word(&a.links.status);
-        if (e != cudaSuccess) return e;
-        a.links.ticket = reinterpret_cast<unsigned *>(ws);
-        a.links.run = reinterpret_cast<unsigned long long *>(ws + 256);
-        a.links.entry = a.links.run + kCols * rows * ntile;
-    }
+    a.links.ticket = reinterpret_cast<unsigned *>(ws);
+    a.links.run = reinterpret_cast<unsigned long long *>(ws + 256);
+    a.links.entry = a.links.run + kCols * rows * ntile;
     const int64_t want = (int64_t)(bytes / 16 + 1023) / 1024 + a.ch / 256;
     gated_prepare_kernel<<<(unsigned)(want < 1 ? 1 : want < 4 * kSMs ? want : 4 * kSMs), 256, 0, st>>>(
         reinterpret_cast<uint4 *>(ws), (int64_t)(bytes / 16), a.decay, a.rate, a.rates, a.ch);
@@ -322,7 +321,7 @@ cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool p
     auto go = [&](auto p, auto g, auto c) {
         auto kernel = gated_fwd_kernel<T, decltype(p)::value, decltype(g)::value, decltype(c)::value>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
-        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)threads, sizeof(Stage<T>), st, true, a);
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)threads, sizeof(Stage<T>), st, a.rates != nullptr, a);
     };
     auto with_cuts = [&](auto p, auto g) { packed ? go(p, g, std::true_type{}) : go(p, g, std::false_type{}); };
     auto with_gate = [&](auto p) { a.z.p && a.y.p ? with_cuts(p, std::true_type{}) : with_cuts(p, std::false_type{}); };

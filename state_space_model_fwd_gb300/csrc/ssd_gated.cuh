@@ -174,7 +174,8 @@ __device__ __forceinline__ void store_state(float *p, const Lane<PAIRS> &k, floa
     if (k.in1) p[k.c0 + k.step] = v.y;
 }
 
-// rate softplus(decay), by the library's functions: once a call and channel, by the kernel that clears the links
+// rate softplus(decay), by the library's functions: once a call and channel, by the kernel that clears the links, where
+// there are any
 __device__ __forceinline__ float decay_rate(float decay, float rate) {
     return rate * (fmaxf(decay, 0.f) + log1pf(expf(-fabsf(decay))));
 }
@@ -397,7 +398,7 @@ struct GatedArgs {
     Rows<const T> x, r, i, z, dy;  // i.p, z.p null: absent
     Rows<T> y, dx, dr, di, dz;     // y.p null: only the kept states are wanted
     const float *decay, *init, *dfinal, *kept;
-    float *rates;  // [ch] rate softplus(decay)
+    float *rates;  // [ch] rate softplus(decay); null: formed by the tiles (one a row)
     float *fin, *keep, *dinit, *ddecay_part;  // keep, kept: [b][ceil(L / 64)][ch] states entering every 64 tokens
     float rate;
     int ch, nblk, batch, ntile, nkeep;
@@ -407,13 +408,20 @@ struct GatedArgs {
     Links links;
 };
 
+template <typename T, bool PAIRS>
+__device__ __forceinline__ float2 rates_of(const GatedArgs<T> &a, const Lane<PAIRS> &k) {
+    if (a.rates) return load_state(a.rates, k);
+    const float2 d = load_state(a.decay, k);
+    return make_float2(k.in0 ? decay_rate(d.x, a.rate) : 0.f, k.in1 ? decay_rate(d.y, a.rate) : 0.f);
+}
+
 // host side (ssd_gated.cu)
 ssd_status_t check_gated(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq);
 bool gated_inputs_ok(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, bool rows);
 inline int64_t gated_blocks(const ssd_gated_shape_t *s) { return (s->channels + kCols - 1) / kCols; }
 inline int64_t gated_kept(const ssd_gated_shape_t *s) { return (s->seqlen + kStateEvery - 1) / kStateEvery; }
-// Workspace of the rates and of the links of `rows` block rows of `ntile` tiles each; their place in it, and the launch that
-// prepares them.
+// Workspace of the rates and of the links of `rows` block rows of `ntile` tiles each (none of one tile each); their place in
+// it, and the launch that prepares them.
 size_t links_bytes(int64_t ch, int64_t rows, int64_t ntile);
 template <typename T>
 cudaError_t prepare(GatedArgs<T> &a, char *ws, int64_t rows, int64_t ntile, cudaStream_t st);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
     float2 rate = make_float2(0.f, 0.f), kept = rate;
     Cuts cut{0, 0, w.b};
     if (n < a.tiles) {
-        rate = load_state(a.rates, w.k), kept = entering(w);
+        rate = rates_of(a, w.k), kept = entering(w);
         fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane);
         if (PACKED && w.t0 < L) cut = cuts_of<S>(a.seqs, w.t0);
     }
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
         const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
         Cuts next_cut{0, 0, after.b};
         if (n < a.tiles) {
-            rate = load_state(a.rates, after.k), kept = entering(after);
+            rate = rates_of(a, after.k), kept = entering(after);
             fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane);
             if (PACKED && after.t0 < L) next_cut = cuts_of<S>(a.seqs, after.t0);
         }
@@ -331,12 +331,12 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (e != cudaSuccess) return status_of(e);
     a.some_empty = cu && a.dinit && any_empty(cu, nseq);
     a.tiles = (int)(ntile * a.nblk * a.batch);
-    const int most = kSMs * (kBlocks);
+    const int most = kSMs * kBlocks;
     const unsigned blocks = (unsigned)(a.tiles < most ? a.tiles : most);
     auto go = [&](auto pr, auto g, auto c) {
         auto kernel = gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
-        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)(nw * 32), sizeof(Stage<T>), st, true, a);
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)(nw * 32), sizeof(Stage<T>), st, a.rates != nullptr, a);
     };
     auto with_cuts = [&](auto pr, auto g) { cu ? go(pr, g, std::true_type{}) : go(pr, g, std::false_type{}); };
     auto with_gate = [&](auto pr) { a.z.p ? with_cuts(pr, std::true_type{}) : with_cuts(pr, std::false_type{}); };
