@@ -9,11 +9,23 @@
 // (eight for the statistics) read the other accumulator meanwhile, a row of the
 // tile a thread.
 //
+// Where there are rows enough, two blocks, a cluster on neighbouring SMs, share
+// tiles of 256 rows (PAIR): each copies its 128 rows of A and half of B, the
+// first one's MMAs read both, and each has its 128 rows of the sum in its own
+// TMEM.  B's copies and reads are halved.
+//
 // The tensor cores add into fp32 with truncation, so a sum over K comes out
 // too small by 2^-25 or so of itself for every 16 of K: 2.6e-6 at K = 2560,
 // which scales all logits alike and shows in the entropy (1.2e-6 of it).  For
 // the statistics a tile's sum is therefore taken in shares of at most
-// kShare chunks, which are added in registers with rounding.
+// kShare chunks, which are added in registers with rounding: 5.5e-7, for 856
+// instead of 839 us at 8192 x 2560 x 32000 (16 chunks: 884 us).
+//
+// What bounds it: the tensor cores under the power limit (1.05 TFLOP for dz in
+// 640 us, 1.65 PFLOP/s; a library product sustains 1.71).  Pairs: forward and
+// gradient of 4095 x 2560 x 50277 2617 us, single blocks 2928; the forward
+// product alone gains nothing from them.  With few rows the weights' one pass
+// bounds it: 16 rows x 2560 x 50280 55 us, 38 at the copy rate.
 #include <cudaTypedefs.h>
 
 #include "ssd_logprob.cuh"
@@ -28,7 +40,7 @@ using namespace tc;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kMaxStages = 8, kRing = 4 * (kBM + kBN) * kBK * 2;  // bytes of the ring: four stages of full tiles
 constexpr int kSmem = kRing + 1024;
-constexpr int kShare = 16;  // chunks of K
+constexpr int kShare = 20;  // chunks of K
 constexpr uint64_t kWaitNs = 100000000ull;
 
 // What becomes of an accumulator.
@@ -39,6 +51,7 @@ constexpr int gemm_threads(int use) { return 128 + 32 * readers(use); }
 
 struct GemmArgs {
     int M, N, K;          // D[M, N] = A[M, K] B[N, K]^T
+    int pair;             // tiles of 256 rows, two blocks each
     int bn, mt, nt, kc;   // columns of a tile; tiles; chunks of kBK
     int arows;            // rows that are copied of a row tile: what lies behind them is read, and only by rows that are none
     int stages, abytes, stage_bytes;
@@ -55,7 +68,7 @@ struct GemmArgs {
     // kStore
     bf16 *out;
     int64_t out_pitch;
-    float *parts;         // [units - whole][128][bn] of the tiles that are split
+    float *parts;         // [units - whole][rows of a tile][bn] of the tiles that are split
     unsigned *status;
 };
 
@@ -83,6 +96,57 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
             smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
         : "memory");
+}
+
+// ---- the pair: this block's number in it, the first one's address of something in shared memory, the barrier of both
+__device__ __forceinline__ uint32_t pair_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t at_first(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A copy into this block's memory that counts on a barrier of the pair's first block.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    if (accumulate)
+        asm volatile("tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, 1;" ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+    else
+        asm volatile("tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, 0;" ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+}
+// Arrives on the same barrier of both blocks (or of this one) once the MMAs issued so far are complete.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_here(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+                 "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)),
+                 "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 struct Bars {
@@ -122,27 +186,35 @@ struct Ring {
 };
 
 // A_MN, B_MN: the operand lies with its rows (M or N) contiguous, in blocks of 64 rows by kBK.
-template <int USE, bool A_MN, bool B_MN, bool ENT>
+template <int USE, bool A_MN, bool B_MN, bool ENT, bool PAIR>
 __global__ void __launch_bounds__(gemm_threads(USE), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = PAIR ? pair_rank() : 0;
+    const int first_unit = PAIR ? blockIdx.x / 2 : blockIdx.x, every = PAIR ? gridDim.x / 2 : gridDim.x;
+    constexpr int HALF = PAIR ? 2 : 1;  // blocks that share B and the columns' work
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], readers(USE));
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], HALF * readers(USE));
         mbar_init(&bars.drain, 1);
         bars.gave_up = 0;
         fence_mbar_init();
         prefetch_tmap(&ma), prefetch_tmap(&mb);
     }
     if (warp == 2) {
-        tmem_alloc(&bars.tmem, 512);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(&bars.tmem, 512);
+        } else {
+            tmem_alloc(&bars.tmem, 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) pair_sync();  // both blocks' barriers are there
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
     const int shares = USE == kStats ? a.shares : 1;
@@ -150,38 +222,54 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
     if (warp < 4) {
         if constexpr (USE == kStats) reg_dec<56>();
         if (warp == 0 && lane == 0) {
-            const uint32_t bytes = (a.arows + a.bn) * kBK * 2;
+            const int bn = a.bn / HALF;  // columns that this block copies
+            const uint32_t bytes = HALF * (a.arows + bn) * kBK * 2;
             Ring r(a.stages);
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+            for (int u = first_unit; u < a.units && ok; u += every) {
                 const Unit t = unit_of(a, u);
+                const int m0 = (t.m * HALF + rank) * kBM, n0 = t.n * a.bn + rank * bn;
                 for (int k = t.k0; k < t.k1; ++k, ++it, r.next()) {
                     if (r.round > 0 && !(ok = wait_for(&bars.empty[r.s], (r.round - 1) & 1, &bars))) break;
                     uint64_t *full = &bars.full[r.s];
+                    const uint32_t full_first = PAIR ? at_first(full) : 0;
+                    auto load = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1) {
+                        if constexpr (PAIR)
+                            tma_load_2d_pair(dst, map, full_first, c0, c1);
+                        else
+                            tma_load_2d(dst, map, full, c0, c1);
+                    };
                     uint8_t *sa = smem + r.s * a.stage_bytes, *sb = sa + a.abytes;
-                    mbar_arrive_expect_tx(full, bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(full, bytes);  // (both blocks' copies)
                     if constexpr (A_MN) {
-                        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * 8192, &ma, full, t.m * kBM + j * 64, k * kBK);
+                        for (int j = 0; j < kBM / 64; ++j) load(sa + j * 8192, &ma, m0 + j * 64, k * kBK);
                     } else {
-                        tma_load_2d(sa, &ma, full, k * kBK, t.m * kBM);
+                        load(sa, &ma, k * kBK, m0);
                     }
                     if constexpr (B_MN) {
-                        for (int j = 0; j < a.bn / 64; ++j) tma_load_2d(sb + j * 8192, &mb, full, t.n * a.bn + j * 64, k * kBK);
+                        for (int j = 0; j < bn / 64; ++j) load(sb + j * 8192, &mb, n0 + j * 64, k * kBK);
                     } else {
-                        tma_load_2d(sb, &mb, full, k * kBK, t.n * a.bn);
+                        load(sb, &mb, k * kBK, n0);
                     }
                 }
             }
-            // no block ends with copies in flight
-            for (uint32_t i = it < (uint32_t)a.stages ? 0 : it - a.stages; i < it; ++i)
-                mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1, kWaitNs / 5);
-        } else if (warp == 1 && lane == 0) {
-            const uint32_t idesc = idesc_bf16(kBM, a.bn, A_MN, B_MN);
+            // no block ends with copies in flight (the pair's second waits for the first at the end)
+            if (rank == 0)
+                for (uint32_t i = it < (uint32_t)a.stages ? 0 : it - a.stages; i < it; ++i)
+                    mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1, kWaitNs / 5);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_bf16(HALF * kBM, a.bn, A_MN, B_MN);
+            auto commit = [](uint64_t *bar) {
+                if constexpr (PAIR)
+                    mma_commit_pair(bar);
+                else
+                    mma_commit(bar);
+            };
             Ring r(a.stages);
             uint32_t n = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+            for (int u = first_unit; u < a.units && ok; u += every) {
                 const Unit t = unit_of(a, u);
                 for (int q = 0; q < shares && ok; ++q, ++n) {
                     const int k0 = USE == kStats ? a.kc * q / shares : t.k0, k1 = USE == kStats ? a.kc * (q + 1) / shares : t.k1;
@@ -195,24 +283,40 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                         const uint64_t da = A_MN ? sdesc(sa, 8192, 1024) : sdesc(sa, 16, 1024);
                         const uint64_t db = B_MN ? sdesc(sb, 8192, 1024) : sdesc(sb, 16, 1024);
 #pragma unroll
-                        for (int j = 0; j < kBK / 16; ++j)
-                            mma_bf16(d, desc_add(da, j * (A_MN ? 2048 : 32)), desc_add(db, j * (B_MN ? 2048 : 32)), idesc,
-                                     j > 0 || k > k0);
-                        mma_commit(&bars.empty[r.s]);
+                        for (int j = 0; j < kBK / 16; ++j) {
+                            const uint64_t dj = desc_add(da, j * (A_MN ? 2048 : 32)), ej = desc_add(db, j * (B_MN ? 2048 : 32));
+                            if constexpr (PAIR)
+                                mma_bf16_pair(d, dj, ej, idesc, j > 0 || k > k0);
+                            else
+                                mma_bf16(d, dj, ej, idesc, j > 0 || k > k0);
+                        }
+                        commit(&bars.empty[r.s]);
                     }
-                    if (ok) mma_commit(&bars.ready[acc]);
+                    if (ok) commit(&bars.ready[acc]);
                 }
             }
-            mma_commit(&bars.drain);  // nor with MMAs
+            if constexpr (PAIR)
+                mma_commit_pair_here(&bars.drain);  // nor with MMAs
+            else
+                mma_commit(&bars.drain);
             mbar_wait(&bars.drain, 0, kWaitNs / 5);
         }
     } else {
         if constexpr (USE == kStats) reg_inc<224>();
         const int q = warp % 4, half = (warp - 4) / 4, first = half * (kBN / 2);  // (a warp reads the 32 rows of its number mod 4)
         uint32_t n = 0;
-        for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+        auto taken = [&](uint32_t acc) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane != 0) return;
+            if (rank == 0)
+                mbar_arrive(&bars.taken[acc]);
+            else
+                mbar_arrive_at(at_first(&bars.taken[acc]));
+        };
+        for (int u = first_unit; u < a.units; u += every) {
             const Unit t = unit_of(a, u);
-            const int row = t.m * kBM + q * 32 + lane, c0 = t.n * a.bn;
+            const int row = (t.m * HALF + rank) * kBM + q * 32 + lane, c0 = t.n * a.bn;
             const bool live = row < a.M;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             if constexpr (USE == kStats) {
@@ -237,9 +341,7 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                             for (int i = 0; i < 16; ++i) part[c + i] += z[i];
                         }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.taken[acc]);
+                    taken(acc);
                 }
                 const uint32_t acc = n & 1;
                 if (!ok || !wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
@@ -263,9 +365,7 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                         add_to(st, z);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.taken[acc]);
+                taken(acc);
                 if (live && first < a.bn) a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
             } else {
                 const uint32_t acc = n & 1, at = lanes + acc * kBN;
@@ -295,7 +395,7 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                                 if (c0 + c + i < a.dz_pitch) store16(p + i, z + i);
                         }
                     } else if (t.part >= 0) {
-                        float *p = a.parts + ((int64_t)t.part * kBM + q * 32 + lane) * a.bn + c;
+                        float *p = a.parts + (((int64_t)t.part * HALF + rank) * kBM + q * 32 + lane) * a.bn + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<float4 *>(p + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
@@ -306,16 +406,19 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                             if (c0 + c + i < a.N) store16(p + i, z + i);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.taken[acc]);
+                taken(acc);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && bars.gave_up) atomicOr(a.status, 1u);
-    if (warp == 2) tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) {
+        pair_sync();  // nothing is on its way to either block
+        if (warp == 2) tmem_dealloc_pair(tmem, 512);
+    } else {
+        if (warp == 2) tmem_dealloc(tmem, 512);
+    }
 }
 
 // The numbers of every row from its tiles' statistics.  A block has `per` neighbouring rows (1, or 8 where there are many) and
@@ -355,13 +458,13 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const float4 *stats, con
 __global__ void __launch_bounds__(256) head_parts_kernel(const __grid_constant__ GemmArgs a) {
     const int tile = blockIdx.y;
     const Unit t = unit_of(a, a.whole + tile * a.split);
-    const int per = a.bn / 8, i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= kBM * per) return;
-    const int r = i / per, c = i % per * 8, row = t.m * kBM + r, col = t.n * a.bn + c;
+    const int per = a.bn / 8, i = blockIdx.x * 256 + threadIdx.x, tall = a.pair ? 2 * kBM : kBM;
+    if (i >= tall * per) return;
+    const int r = i / per, c = i % per * 8, row = t.m * tall + r, col = t.n * a.bn + c;
     if (row >= a.M || col >= a.N) return;
     float v[8] = {};
     for (int k = 0; k < a.split; ++k) {
-        const float4 *p = reinterpret_cast<const float4 *>(a.parts + (((int64_t)tile * a.split + k) * kBM + r) * a.bn + c);
+        const float4 *p = reinterpret_cast<const float4 *>(a.parts + (((int64_t)tile * a.split + k) * tall + r) * a.bn + c);
         const float4 x = p[0], y = p[1];
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
     }
@@ -397,28 +500,37 @@ bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t p
 
 constexpr int kSMs = 152;
 
+// Tiles of 256 rows where they leave no more than an eighth of the rows empty (the work of a row that is none costs as much as
+// the pairs save).
+bool takes_pairs(int64_t M, int bn) {
+    const int64_t padded = (M + 2 * kBM - 1) / (2 * kBM) * (2 * kBM);
+    return bn % 128 == 0 && padded - M <= padded / 8;
+}
+
 // Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share.
 GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split, bool a_mn = false) {
     GemmArgs a{};
     a.M = (int)M, a.N = (int)N, a.K = (int)K, a.bn = bn;
-    a.mt = (int)((M + kBM - 1) / kBM), a.nt = (int)((N + bn - 1) / bn), a.kc = (int)((K + kBK - 1) / kBK);
-    a.group = 32;
+    a.pair = takes_pairs(M, bn);
+    const int tall = a.pair ? 2 * kBM : kBM, places = a.pair ? kSMs / 2 : kSMs;
+    a.mt = (int)((M + tall - 1) / tall), a.nt = (int)((N + bn - 1) / bn), a.kc = (int)((K + kBK - 1) / kBK);
+    a.group = a.pair ? 16 : 32;
     a.arows = M < kBM && !a_mn ? (int)((M + 7) / 8 * 8) : kBM;
-    a.abytes = (a.arows * kBK * 2 + 1023) / 1024 * 1024, a.stage_bytes = a.abytes + (bn * kBK * 2 + 1023) / 1024 * 1024;
+    a.abytes = (a.arows * kBK * 2 + 1023) / 1024 * 1024, a.stage_bytes = a.abytes + (bn / (a.pair ? 2 : 1) * kBK * 2 + 1023) / 1024 * 1024;
     a.stages = kRing / a.stage_bytes < kMaxStages ? kRing / a.stage_bytes : kMaxStages;
     a.shares = (a.kc + kShare - 1) / kShare;
     const int tiles = a.mt * a.nt;
     a.whole = tiles, a.split = 1;
-    const int rest = tiles % kSMs;
+    const int rest = tiles % places;
     if (split && rest) {
-        int s = kSMs / rest;
+        int s = places / rest;
         if (s > a.kc / 4) s = a.kc / 4;  // (a share of fewer chunks is mostly filling the ring)
         if (s > 1) a.whole = tiles - rest, a.split = s;
     }
     a.units = a.whole + (tiles - a.whole) * a.split;
     return a;
 }
-size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)(a.units - a.whole) * kBM * a.bn); }
+size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)(a.units - a.whole) * (a.pair ? 2 : 1) * kBM * a.bn); }
 
 int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); }
 
@@ -465,19 +577,30 @@ HeadPlan plan_bwd(const ssd_head_shape_t *s) {
 
 template <int USE, bool A_MN, bool B_MN, bool ENT>
 cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a, const char *name, cudaStream_t st) {
-    auto kernel = gemm_kernel<USE, A_MN, B_MN, ENT>;
+    auto kernel = a.pair ? gemm_kernel<USE, A_MN, B_MN, ENT, true> : gemm_kernel<USE, A_MN, B_MN, ENT, false>;
     // (set on every call: cheap, and right for each device and context)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.units < kSMs ? a.units : kSMs), gemm_threads(USE), kSmem, st>>>(ma, mb, a);
+    const int blocks = a.pair ? 2 : 1, places = kSMs / blocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * (a.units < places ? a.units : places)));
+    cfg.blockDim = dim3(gemm_threads(USE));
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.pair ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
     timing_mark(st, name);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t run_parts(const GemmArgs &a, cudaStream_t st) {
     const int tiles = (a.units - a.whole) / a.split;
     if (a.units == a.whole) return cudaSuccess;
-    head_parts_kernel<<<dim3((unsigned)((kBM * (a.bn / 8) + 255) / 256), (unsigned)tiles), 256, 0, st>>>(a);
+    head_parts_kernel<<<dim3((unsigned)(((a.pair ? 2 : 1) * kBM * (a.bn / 8) + 255) / 256), (unsigned)tiles), 256, 0, st>>>(a);
     timing_mark(st, "head_parts");
     return cudaGetLastError();
 }
@@ -527,7 +650,7 @@ ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_
     char *ws = static_cast<char *>(workspace);
     CUtensorMap mh, mw;
     if (!map_of(&mh, hidden->data, T, D, pitch_of(*hidden, T, D), p.z.arows) ||
-        !map_of(&mw, weight->data, V, D, pitch_of(*weight, V, D), p.z.bn))
+        !map_of(&mw, weight->data, V, D, pitch_of(*weight, V, D), p.z.bn / (p.z.pair ? 2 : 1)))
         return SSD_ERR_CUDA;
     GemmArgs a = p.z;
     a.targets = logprob ? targets : nullptr;
@@ -571,7 +694,7 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     const int64_t hp = pitch_of(*hidden, T, D), wp = pitch_of(*weight, V, D);
     CUtensorMap mh, mw, mz, mz_t, mw_t, mh_t;
     // dz: only its V columns are read, whatever lies behind them
-    if (!map_of(&mh, hidden->data, T, D, hp, p.z.arows) || !map_of(&mw, weight->data, V, D, wp, p.z.bn) ||
+    if (!map_of(&mh, hidden->data, T, D, hp, p.z.arows) || !map_of(&mw, weight->data, V, D, wp, p.z.bn / (p.z.pair ? 2 : 1)) ||
         !map_of(&mz, dz, T, V, p.pitch, p.dh.arows) || !map_of(&mw_t, weight->data, V, D, wp, kBK) ||
         !map_of(&mz_t, dz, T, V, p.pitch, kBK) || !map_of(&mh_t, hidden->data, T, D, hp, kBK))
         return SSD_ERR_CUDA;
