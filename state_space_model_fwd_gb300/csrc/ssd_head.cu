@@ -40,7 +40,8 @@ using namespace tc;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kMaxStages = 8, kRing = 4 * (kBM + kBN) * kBK * 2;  // bytes of the ring: four stages of full tiles
 constexpr int kSmem = kRing + 1024;
-constexpr int kShare = 20;  // chunks of K
+constexpr int kShare = 20;      // chunks of K
+constexpr int kLongest = 4096;  // and at most in one sum of the gradient: 2.7e-4 too small, a tenth of a step of its bf16 result
 constexpr uint64_t kWaitNs = 100000000ull;
 
 // What becomes of an accumulator.
@@ -456,9 +457,9 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const float4 *stats, con
 
 // The tiles that were split: their parts' sum, in order.
 __global__ void __launch_bounds__(256) head_parts_kernel(const __grid_constant__ GemmArgs a) {
-    const int tile = blockIdx.y;
+    const int per = a.bn / 8, tall = a.pair ? 2 * kBM : kBM, blocks = (tall * per + 255) / 256;
+    const int tile = blockIdx.x / blocks, i = blockIdx.x % blocks * 256 + threadIdx.x;
     const Unit t = unit_of(a, a.whole + tile * a.split);
-    const int per = a.bn / 8, i = blockIdx.x * 256 + threadIdx.x, tall = a.pair ? 2 * kBM : kBM;
     if (i >= tall * per) return;
     const int r = i / per, c = i % per * 8, row = t.m * tall + r, col = t.n * a.bn + c;
     if (row >= a.M || col >= a.N) return;
@@ -527,6 +528,7 @@ GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split, bool a_m
         if (s > a.kc / 4) s = a.kc / 4;  // (a share of fewer chunks is mostly filling the ring)
         if (s > 1) a.whole = tiles - rest, a.split = s;
     }
+    if (split && a.kc > kLongest) a.whole = 0, a.split = (a.kc + kLongest - 1) / kLongest;
     a.units = a.whole + (tiles - a.whole) * a.split;
     return a;
 }
@@ -600,7 +602,9 @@ cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArg
 cudaError_t run_parts(const GemmArgs &a, cudaStream_t st) {
     const int tiles = (a.units - a.whole) / a.split;
     if (a.units == a.whole) return cudaSuccess;
-    head_parts_kernel<<<dim3((unsigned)(((a.pair ? 2 : 1) * kBM * (a.bn / 8) + 255) / 256), (unsigned)tiles), 256, 0, st>>>(a);
+    const int64_t blocks = ((a.pair ? 2 : 1) * kBM * (a.bn / 8) + 255) / 256;
+    if (blocks * tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    head_parts_kernel<<<(unsigned)(blocks * tiles), 256, 0, st>>>(a);
     timing_mark(st, "head_parts");
     return cudaGetLastError();
 }
@@ -610,8 +614,11 @@ ssd_status_t check_head(const ssd_head_shape_t *s) {
     if (s->dtype != SSD_DTYPE_F32 && s->dtype != SSD_DTYPE_BF16) return SSD_ERR_INVALID_ARG;
     if (s->dtype != SSD_DTYPE_BF16 || s->dim % 8 || s->dim > (1 << 20) || s->vocab > (1 << 22) || s->rows > (1 << 22))
         return SSD_ERR_UNSUPPORTED;
-    // tiles are counted in 31 bits
-    if ((s->rows / kBM + 1) * (s->vocab / 64 + 1) > (1 << 28)) return SSD_ERR_UNSUPPORTED;
+    // tiles and their parts are counted in 31 bits
+    const int64_t most = 1 << 28;
+    if ((s->rows / kBM + 1) * (s->vocab / 64 + 1) > most || (s->vocab / kBM + 1) * (s->dim / 64 + 1) * (s->rows / (kLongest * kBK) + 1) > most / 64 ||
+        (s->rows / kBM + 1) * (s->dim / 64 + 1) * (s->vocab / (kLongest * kBK) + 1) > most / 64)
+        return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 // Rows that TMA reads: 16-byte aligned, each of them.
