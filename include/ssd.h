@@ -579,8 +579,9 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
  * ssd_head_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
  * dhidden [rows, dim], dweight [vocab, dim] in bf16 (either NULL: not wanted).
  * The logits are formed again; their gradient is rounded to bf16 (2^-9
- * relative, as the operands are) and takes 2 rows vocab bytes of the
- * workspace; sums over it are fp32, in a fixed order, and rounded once.
+ * relative, as the operands are), but for the given tokens' elements, which
+ * keep fp32 accuracy, and takes 2 rows vocab bytes of the workspace; sums over
+ * it are fp32, in a fixed order, and rounded once.
  * Supported: bf16, dim a multiple of 8.  A wait that gives up in a kernel is
  * reported by ssd_get_device_status.
  */

@@ -43,12 +43,58 @@ constexpr int kSmem = kRing + 1024;
 constexpr int kShare = 20;      // chunks of K
 constexpr int kLongest = 4096;  // and at most in one sum of the gradient: 2.7e-4 too small, a tenth of a step of its bf16 result
 constexpr uint64_t kWaitNs = 100000000ull;
+constexpr int kNoLead = 0x7F7F7F7F;
 
 // What becomes of an accumulator.
 enum Use { kStats, kGrad, kStore };
 // warps: copy, MMA, TMEM, -, and those that read the accumulators, each 32 rows and (statistics) half of the columns
 constexpr int readers(int use) { return use == kStats ? 8 : 4; }
 constexpr int gemm_threads(int use) { return 128 + 32 * readers(use); }
+
+// dz is rounded to bf16 (2^-9 relative, as its products' other operands are), which would show where one element outweighs all
+// others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
+//   dhidden[row] += rest[row] weight[target[row]],   dweight[v] += sum over rows with target v of rest[row] hidden[row],
+// the latter summed by fix_kernel into the row of the first of them.  (4095 x 2560 x 50277: error against 64 bits 1.4 times a
+// bf16 rounding without it, 1.0 with it, for 1% of the time; with few rows up to 1.8 times.)
+struct Fix {
+    const int64_t *targets;  // dhidden
+    const float *rest;
+    const bf16 *weight;
+    int64_t weight_pitch;
+    int vocab;
+    const int *lead;         // dweight
+    const float *sums;
+    int64_t dim;
+};
+// What is added to 8 columns of a row of the product; `which`: 1 dhidden, 2 dweight.
+struct FixRow {
+    const bf16 *w;
+    const float *e;
+    float scale;
+};
+__device__ __forceinline__ FixRow fix_row(const Fix &f, int row, bool live) {
+    FixRow r{nullptr, nullptr, 0.f};
+    if (!live) return r;
+    if (f.targets) {
+        const int64_t t = f.targets[row];
+        if (t >= 0 && t < f.vocab) r.w = f.weight + t * f.weight_pitch, r.scale = f.rest[row];
+    } else if (f.lead) {
+        const int first = f.lead[row];
+        if (first != kNoLead) r.e = f.sums + first * f.dim;
+    }
+    return r;
+}
+__device__ __forceinline__ void fix_add(const FixRow &r, int col, float *z) {  // 8 columns
+    if (r.w) {
+        float w[8];
+        widen<bf16, 8>(load_vec<bf16, 8>(r.w + col), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = fmaf(r.scale, w[i], z[i]);
+    } else if (r.e) {
+        const float4 a = *reinterpret_cast<const float4 *>(r.e + col), b = *reinterpret_cast<const float4 *>(r.e + col + 4);
+        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w, z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+    }
+}
 
 struct GemmArgs {
     int M, N, K;          // D[M, N] = A[M, K] B[N, K]^T
@@ -66,9 +112,12 @@ struct GemmArgs {
     RowGradIn grad;
     bf16 *dz;
     int64_t dz_pitch;
+    float *rest;          // [M] what rounding left of the given token's dz (0 without one)
+    int *lead;            // [N] the first row that has a token as its given one (null: not wanted)
     // kStore
     bf16 *out;
     int64_t out_pitch;
+    Fix fix;
     float *parts;         // [units - whole][rows of a tile][bn] of the tiles that are split
     unsigned *status;
 };
@@ -371,8 +420,12 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
             } else {
                 const uint32_t acc = n & 1, at = lanes + acc * kBN;
                 RowGrad g{};
+                FixRow fix{};
                 if constexpr (USE == kGrad) {
                     if (live) g = row_grad(a.grad, row, a.N);
+                    if (live && t.n == 0 && (g.target < 0 || g.none)) a.rest[row] = 0.f;
+                } else if (t.part < 0) {
+                    fix = fix_row(a.fix, row, live);
                 }
                 if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
                 ++n;
@@ -389,7 +442,11 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                             if (g.target >= c0 + c && g.target < c0 + c + 32 && !g.none) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (c0 + c + i == g.target) z[i] += g.dlp;
+                                    if (c0 + c + i == g.target) {
+                                        z[i] += g.dlp;
+                                        a.rest[row] = z[i] - to_f32(from_f32<bf16>(z[i]));
+                                    }
+                                if (a.lead) atomicMin(&a.lead[g.target], row);
                             }
 #pragma unroll
                             for (int i = 0; i < 32; i += 8)
@@ -404,7 +461,10 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
                         bf16 *p = a.out + row * a.out_pitch + c0 + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
-                            if (c0 + c + i < a.N) store16(p + i, z + i);
+                            if (c0 + c + i < a.N) {
+                                fix_add(fix, c0 + c + i, z + i);
+                                store16(p + i, z + i);
+                            }
                     }
                 }
                 taken(acc);
@@ -469,7 +529,55 @@ __global__ void __launch_bounds__(256) head_parts_kernel(const __grid_constant__
         const float4 x = p[0], y = p[1];
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
     }
+    fix_add(fix_row(a.fix, row, true), col, v);
     store16(a.out + row * a.out_pitch + col, v);
+}
+
+// sums[r] = sum of rest[row] hidden[row] over the rows with row r's target, in order, for rows r that are the first with theirs.
+// A block a row, 8 columns a thread.
+constexpr int kFixList = 1024;
+__global__ void __launch_bounds__(256) head_fix_kernel(const int64_t *targets, const int *lead, const float *rest, const bf16 *hidden,
+                                                       int64_t pitch, int rows, int dim, int vocab, float *sums) {
+    __shared__ int list[kFixList], counts[8];
+    const int r = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t t = targets[r];
+    if (t < 0 || t >= vocab || lead[t] != r) return;
+    float *out = sums + (int64_t)r * dim;
+    int n = 0;
+    bool begun = false;
+    for (int base = r; base < rows; base += 256) {
+        const int row = base + threadIdx.x;
+        const unsigned same = __ballot_sync(0xffffffffu, row < rows && targets[row] == t);
+        if (lane == 0) counts[warp] = __popc(same);
+        __syncthreads();
+        int at = n, total = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) at += counts[w];
+            total += counts[w];
+        }
+        if (same >> lane & 1) list[at + __popc(same & ((1u << lane) - 1))] = row;
+        n += total;
+        __syncthreads();
+        if (n + 256 <= kFixList && base + 256 < rows) continue;
+        for (int c = threadIdx.x * 8; c < dim; c += 2048) {
+            float v[8] = {};
+            if (begun) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = out[c + i];
+            }
+            for (int k = 0; k < n; ++k) {
+                float h[8];
+                widen<bf16, 8>(load_vec<bf16, 8>(hidden + list[k] * pitch + c), h);
+                const float q = rest[list[k]];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(q, h[i], v[i]);
+            }
+            *reinterpret_cast<float4 *>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(out + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        n = 0, begun = true;
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -552,7 +660,7 @@ int forward_columns(int64_t T, int64_t V) {
 int halves(const GemmArgs &a) { return a.bn > kBN / 2 ? 2 : 1; }
 
 struct HeadPlan {
-    size_t stats, given, dz, parts, bytes;
+    size_t stats, given, dz, rest, lead, sums, parts, bytes;
     int64_t pitch;
     GemmArgs z, dh, dw;
 };
@@ -571,7 +679,10 @@ HeadPlan plan_bwd(const ssd_head_shape_t *s) {
     p.dw = plan_gemm(s->vocab, s->dim, s->rows, fit_columns(s->dim), true, true);
     p.pitch = (s->vocab + 63) / 64 * 64;
     p.dz = 0;
-    p.parts = align256(2 * s->rows * p.pitch);
+    p.rest = align256(2 * s->rows * p.pitch);
+    p.lead = p.rest + align256(sizeof(float) * s->rows);
+    p.sums = p.lead + align256(sizeof(int) * s->vocab);
+    p.parts = p.sums + align256(sizeof(float) * s->rows * s->dim);
     const size_t a = parts_bytes(p.dh), b = parts_bytes(p.dw);
     p.bytes = p.parts + (a > b ? a : b);
     return p;
@@ -713,6 +824,14 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     a.status = status;
     a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
     a.dz = dz, a.dz_pitch = p.pitch;
+    a.rest = reinterpret_cast<float *>(ws + p.rest);
+    const bool given = targets && dlogprob;  // otherwise no element of dz stands out
+    if (dweight && given) {
+        a.lead = reinterpret_cast<int *>(ws + p.lead);
+        e = cudaMemsetAsync(a.lead, 0x7F, sizeof(int) * V, stream);
+        timing_mark(stream, "head_leads");
+        if (e != cudaSuccess) return status_of(e);
+    }
     e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, a, "head_dlogits", stream)
                  : run_gemm<kGrad, false, false, false>(mh, mw, a, "head_dlogits", stream);
     if (e == cudaSuccess && dhidden) {
@@ -720,6 +839,7 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         b.status = status;
         b.out = static_cast<bf16 *>(dhidden->data), b.out_pitch = pitch_of(*dhidden, T, D);
         b.parts = reinterpret_cast<float *>(ws + p.parts);
+        if (given) b.fix = Fix{targets, a.rest, static_cast<const bf16 *>(weight->data), wp, (int)V, nullptr, nullptr, D};
         e = run_gemm<kStore, false, true, false>(mz, mw_t, b, "head_dhidden", stream);
         if (e == cudaSuccess) e = run_parts(b, stream);
     }
@@ -728,6 +848,15 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         b.status = status;
         b.out = static_cast<bf16 *>(dweight->data), b.out_pitch = pitch_of(*dweight, V, D);
         b.parts = reinterpret_cast<float *>(ws + p.parts);
+        if (given) {
+            float *sums = reinterpret_cast<float *>(ws + p.sums);
+            head_fix_kernel<<<(unsigned)T, 256, 0, stream>>>(targets, a.lead, a.rest, static_cast<const bf16 *>(hidden->data), hp, (int)T,
+                                                             (int)D, (int)V, sums);
+            timing_mark(stream, "head_fix");
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return status_of(e);
+            b.fix = Fix{nullptr, nullptr, nullptr, 0, (int)V, a.lead, sums, D};
+        }
         e = run_gemm<kStore, true, true, false>(mz_t, mh_t, b, "head_dweight", stream);
         if (e == cudaSuccess) e = run_parts(b, stream);
     }

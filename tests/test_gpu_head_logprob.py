@@ -85,6 +85,34 @@ def test_gradient(rows, dim, vocab, pad, which):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,dim,vocab,kinds", [(1, 64, 300, 1), (40, 72, 1000, 2), (1500, 64, 500, 1), (3000, 2056, 257, 3)])
+def test_the_given_tokens_part_is_not_rounded(rows, dim, vocab, kinds):
+    """Where the given token's element outweighs the others; few and many rows with the same one, some without."""
+    h, w, _ = make(rows, dim, vocab, seed=9)
+    g = torch.Generator().manual_seed(4)
+    targets = torch.tensor([5, vocab - 1, 130])[:kinds].cuda()[torch.randint(0, kinds, (rows,), generator=g).cuda()]
+    if rows > 30:
+        targets[::7] = -100
+    glp = upstream(rows)[0]
+    _, lse, _ = ssd.ssd_head_logprob_fwd(h, w, targets)
+    dh, dw = ssd.ssd_head_logprob_bwd(h, w, targets, lse, dlogprob=glp)
+    z = logits(h, w)
+    zero = torch.zeros(rows, dtype=torch.float64)
+    _, wlse, went = definition(z, targets)
+    d = want_gradient(z, targets.cpu(), wlse, went, ref.d(glp), zero, zero)
+    # as in test_gradient, but the given token's dz counts with its fp32 error only
+    p = torch.exp(z - wlse[:, None])
+    err = d.abs() * 2.0 ** -8 + 2e-5 * p * ref.d(glp).abs()[:, None]
+    has = targets.cpu() >= 0
+    err[has, targets.cpu()[has]] = 2e-5 * ref.d(glp).abs()[has]
+    for got, x, e2, name in ((dh, d @ ref.d(w), (err ** 2) @ (ref.d(w) ** 2), "dhidden"),
+                             (dw, d.t() @ ref.d(h), (err.t() ** 2) @ (ref.d(h) ** 2), "dweight")):
+        ref.check(got, x, name, rel=1.0, scale=5 / math.sqrt(3) * e2.sqrt() + 1e-30)
+    again = ssd.ssd_head_logprob_bwd(h, w, targets, lse, dlogprob=glp)
+    assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
+
+
+@pytest.mark.gpu
 def test_gradient_agrees_with_differences():
     h, w, targets = make(96, 128, 900, seed=4)
     glp, glse, gent = upstream(96)
