@@ -609,18 +609,21 @@ bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t p
 
 constexpr int kSMs = 152;
 
-// Tiles of 256 rows where they leave no more than an eighth of the rows empty (the work of a row that is none costs as much as
-// the pairs save).
-bool takes_pairs(int64_t M, int bn) {
+// Tiles of 256 rows where they leave no more than an eighth of the rows empty and sums are long enough for a pair's longer
+// start (8192 x 512 x 32000: 241 us, in pairs 288; forward and gradient of T x 2560 x 50277, T = 300: 463 us, pairs wherever the columns allow 536; T = 300, 500, 768,
+// 1000: pairs for dweight, a sum over T, in spite of its length 478, 574, 710, 944 us, otherwise 463, 564, 709, -; no pairs at
+// all -, -, -, 1017).
+bool takes_pairs(int64_t M, int64_t K, int bn) {
     const int64_t padded = (M + 2 * kBM - 1) / (2 * kBM) * (2 * kBM);
-    return bn % 128 == 0 && padded - M <= padded / 8;
+    return bn % 128 == 0 && K >= 640 && padded - M <= padded / 8;
 }
 
-// Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share.
+// Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share
+// (forward and gradient of 300 x 2560 x 50277: 478 us, whole tiles only 709; 64 rows: 349 and 606).
 GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split, bool a_mn = false) {
     GemmArgs a{};
     a.M = (int)M, a.N = (int)N, a.K = (int)K, a.bn = bn;
-    a.pair = takes_pairs(M, bn);
+    a.pair = takes_pairs(M, K, bn);
     const int tall = a.pair ? 2 * kBM : kBM, places = a.pair ? kSMs / 2 : kSMs;
     a.mt = (int)((M + tall - 1) / tall), a.nt = (int)((N + bn - 1) / bn), a.kc = (int)((K + kBK - 1) / kBK);
     a.group = a.pair ? 16 : 32;
@@ -645,7 +648,8 @@ size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)
 int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); }
 
 // Columns of a forward tile.  With one row of tiles the weights' one pass sets the time: the widest of the column counts
-// that leave the fewest columns to the busiest SM.
+// that leave the fewest columns to the busiest SM (16 x 2560 x 20000: 27.1 us, with 256 columns 28.2; 128 x 2560 x 50280: 55.2
+// and 56.9).
 int forward_columns(int64_t T, int64_t V) {
     if (T > kBM) return fit_columns(V);
     int best = 256;

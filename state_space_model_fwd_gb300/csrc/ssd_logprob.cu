@@ -19,6 +19,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int kSMs = 152;
+
 // A row is 100 KB: a block spends as long on joining its threads' statistics
 // and on the alternatives as on loads, so small blocks, many of them, keep
 // memory busy (forward and gradient of 8192 x 50280 bf16 / five alternatives of
@@ -92,14 +94,13 @@ __device__ __forceinline__ unsigned long long entry_of(float v, int index) {
     return (unsigned long long)key_of(v) << 32 | (0xFFFFFFFFu - (unsigned)index);
 }
 
-// Of which maxima tau is found: those of groups of lanes, as few as leave k of them with room to spare (the more groups,
-// the fewer elements reach tau: about n log(n / (n - k)) of n groups; the fewer, the shorter the search for it).
-constexpr int kFewGroups = 16, kManyGroups = 128;
-constexpr int kFewTop = kFewGroups / 2;
-static_assert(kMaxTop <= kManyGroups / 2, "");
+// tau is found among the maxima of groups of threads, twice as many as alternatives can be asked for: then about
+// n log(n / (n - k)) <= 1.4 k elements reach it.
+constexpr int kGroups = 2 * kMaxTop, kWide = kThreads / kGroups;
+static_assert(kWide >= 1 && 32 % kWide == 0, "");
 
 struct TopShared {
-    unsigned maxima[kManyGroups];
+    unsigned maxima[kGroups];
     unsigned long long found[kFound + kSame];
     unsigned long long best[kMaxTop];  // sorted
     short threads[kThreads];
@@ -137,24 +138,18 @@ __device__ void top_of_part(const Slots<T> &s, float m, bool any, int k, TopShar
     constexpr int V = Slots<T>::V;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const unsigned mine = any ? key_of(m) : 0;
-    const int wide = k <= kFewTop ? kThreads / kFewGroups : kThreads / kManyGroups;  // threads of a group
     unsigned g = mine;
-    for (int d = 1; d < wide; d *= 2) g = max(g, __shfl_xor_sync(0xffffffffu, g, d));
-    if (tid % wide == 0) t.maxima[tid / wide] = g;
+#pragma unroll
+    for (int d = 1; d < kWide; d *= 2) g = max(g, __shfl_xor_sync(0xffffffffu, g, d));
+    if (tid % kWide == 0) t.maxima[tid / kWide] = g;
     if (tid < k) t.best[tid] = 0;
     if (tid == 0) t.above = t.equal = t.holders = 0;
     __syncthreads();
     if (warp == 0) {
-        unsigned tau;
-        if (k <= kFewTop) {
-            const unsigned v[1] = {lane < kFewGroups ? t.maxima[lane] : 0};
-            tau = reached_by<T>(v, k);
-        } else {
-            unsigned v[kManyGroups / 32];
+        unsigned v[kGroups / 32];
 #pragma unroll
-            for (int i = 0; i < kManyGroups / 32; ++i) v[i] = t.maxima[i * 32 + lane];
-            tau = reached_by<T>(v, k);
-        }
+        for (int i = 0; i < kGroups / 32; ++i) v[i] = t.maxima[i * 32 + lane];
+        const unsigned tau = reached_by<T>(v, k);
         if (lane == 0) t.tau = tau;
     }
     __syncthreads();
@@ -428,8 +423,11 @@ ssd_status_t fwd_typed(const ssd_logprob_shape_t *s, const ssd_rows_t *logits, c
     a.targets = targets, a.logprob = logprob, a.lse = lse, a.entropy = entropy;
     a.top_logprob = top_logprob, a.top_index = top_index;
     a.rows = s->rows, a.vocab = (int)s->vocab, a.top = (int)s->top;
+    // Few long rows: up to four blocks, a cluster, share one (4 rows with eight alternatives in a graph: of 131072 15.5 us by
+    // one block, 12.0 by two, 9.5 by four or eight; of 50280 9.5, -, 9.3, 10.4; of 8192 6.5 by one, 8.1 by two), as long as
+    // that gives no SM more than two (152 rows of 50280: 10 us, by four blocks each 20).
     a.parts = 1;
-    while (a.parts < 8 && s->rows * a.parts * 2 <= 304 && s->vocab / (a.parts * 2) >= 4096) a.parts *= 2;
+    while (a.parts < 4 && s->rows * a.parts * 2 <= 2 * kSMs && s->vocab / (a.parts * 2) >= 12288) a.parts *= 2;
     timing_begin(st);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(s->rows * a.parts));
