@@ -5,9 +5,9 @@
 //
 // All products run in one kernel: a block (one on each SM) walks over tiles of
 // 128 rows and up to 256 columns.  One warp copies operands by TMA into a ring
-// of stages, one issues the MMAs into one of two accumulators in TMEM, four
-// (eight for the statistics) read the other accumulator meanwhile, a row of the
-// tile a thread.
+// of stages, one issues the MMAs into one of two accumulators in TMEM, eight
+// read the other accumulator meanwhile, half a row of the tile a thread, and
+// store bf16 results by TMA.
 //
 // Where there are rows enough, two blocks, a cluster on neighbouring SMs, share
 // tiles of 256 rows (PAIR): each copies its 128 rows of A and half of B, the
@@ -39,7 +39,8 @@ using namespace tc;
 
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kMaxStages = 8, kRing = 4 * (kBM + kBN) * kBK * 2;  // bytes of the ring: four stages of full tiles
-constexpr int kSmem = kRing + 1024;
+constexpr int kReaders = 8;  // warps that read the accumulators, 32 rows and half of the columns each
+constexpr int kSmem = kRing + kReaders * 4096 + 1024;
 constexpr int kShare = 20;      // chunks of K
 constexpr int kLongest = 4096;  // and at most in one sum of the gradient: 2.7e-4 too small, a tenth of a step of its bf16 result
 constexpr uint64_t kWaitNs = 100000000ull;
@@ -47,9 +48,7 @@ constexpr int kNoLead = 0x7F7F7F7F;
 
 // What becomes of an accumulator.
 enum Use { kStats, kGrad, kStore };
-// warps: copy, MMA, TMEM, -, and those that read the accumulators, each 32 rows and (statistics) half of the columns
-constexpr int readers(int use) { return use == kStats ? 8 : 4; }
-constexpr int gemm_threads(int use) { return 128 + 32 * readers(use); }
+constexpr int kGemmThreads = 128 + 32 * kReaders;  // warps: copy, MMA, TMEM, -, the readers
 
 // dz is rounded to bf16 (2^-9 relative, as its products' other operands are), which would show where one element outweighs all
 // others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
@@ -110,8 +109,6 @@ struct GemmArgs {
     float4 *stats;        // [nt][halves][M] (m, sum, moment, 0)
     float *given;         // [M] the given tokens' logits
     RowGradIn grad;
-    bf16 *dz;
-    int64_t dz_pitch;
     float *rest;          // [M] what rounding left of the given token's dz (0 without one)
     int *lead;            // [N] the first row that has a token as its given one (null: not wanted)
     // kStore
@@ -225,6 +222,57 @@ __device__ __forceinline__ void store16(bf16 *p, const float *v) {
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
+// Tiled copy shared -> global; elements outside the tensor are not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+
+// Waits for the loads from TMEM; nothing that uses their results moves before.
+template <int N>
+__device__ __forceinline__ void loaded(float (&z)[N]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(z[i]));
+}
+
+// The statistics of finite logits (and of any, but for the entropy, which minus infinity makes NaN): the maximum first, then
+// four sums side by side, so that no addition waits for the one before.
+__device__ __forceinline__ Stat stat_of(const float (&z)[4][32]) {
+    constexpr int N = 128;
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = z[0][i];
+#pragma unroll
+    for (int i = 8; i < N; ++i) m[i % 8] = max_nan(m[i % 8], z[i / 32][i % 32]);
+#pragma unroll
+    for (int d = 4; d; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i) m[i] = max_nan(m[i], m[i + d]);
+    Stat s{m[0], 0.f, 0.f};
+    if (is_far(s.m)) {
+        if (s.m == -INFINITY) return s;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float t = fmaxf((z[i / 32][i % 32] - s.m) * kLog2e, kNothing), e = ex2(t);
+            s.sum += e, s.moment = fmaf(e, t, s.moment);
+        }
+        return s;
+    }
+    const float ref = -ref_of(s.m);
+    f2 sum[4] = {0, 0, 0, 0}, moment[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const f2 t = fma2(pack2(z[i / 16][2 * i % 32], z[i / 16][2 * i % 32 + 1]), pack2(kLog2e, kLog2e), pack2(ref, ref)), e = ex2x2(t);
+        sum[i % 4] = add2(sum[i % 4], e);
+        moment[i % 4] = fma2(e, t, moment[i % 4]);
+    }
+    s.sum = sum2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+    s.moment = sum2(add2(add2(moment[0], moment[1]), add2(moment[2], moment[3])));
+    return s;
+}
+
 // A place in the ring.
 struct Ring {
     int stages, s = 0;
@@ -237,8 +285,9 @@ struct Ring {
 
 // A_MN, B_MN: the operand lies with its rows (M or N) contiguous, in blocks of 64 rows by kBK.
 template <int USE, bool A_MN, bool B_MN, bool ENT, bool PAIR>
-__global__ void __launch_bounds__(gemm_threads(USE), 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ GemmArgs a) {
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mo,
+                const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -248,7 +297,7 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
     constexpr int HALF = PAIR ? 2 : 1;  // blocks that share B and the columns' work
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], HALF * readers(USE));
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], HALF * kReaders);
         mbar_init(&bars.drain, 1);
         bars.gave_up = 0;
         fence_mbar_init();
@@ -354,6 +403,7 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
     } else {
         if constexpr (USE == kStats) reg_inc<224>();
         const int q = warp % 4, half = (warp - 4) / 4, first = half * (kBN / 2);  // (a warp reads the 32 rows of its number mod 4)
+        uint8_t *stage = smem + kRing + (warp - 4) * 4096;
         uint32_t n = 0;
         auto taken = [&](uint32_t acc) {
             tc_fence_before();
@@ -370,106 +420,124 @@ __global__ void __launch_bounds__(gemm_threads(USE), 1)
             const bool live = row < a.M;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             if constexpr (USE == kStats) {
-                const int64_t target = live && a.targets ? a.targets[row] - c0 : -1;
-                const int limit = min(a.N - c0, a.bn);  // (a tile's columns are a multiple of 16)
-                Stat st{-INFINITY, 0.f, 0.f};
-                float part[kBN / 2];
+                const int limit = min(min(a.N - c0, a.bn) - first, kBN / 2);  // of this warp's columns
+                const int64_t given = live && a.targets ? a.targets[row] - c0 - first : -1;
+                const int target = given >= 0 && given < limit ? (int)given : -1;
+                float z[4][32];
                 bool ok = true;
-#pragma unroll
-                for (int i = 0; i < kBN / 2; ++i) part[i] = 0.f;
-                for (int share = 0; share + 1 < shares; ++share, ++n) {
-                    const uint32_t acc = n & 1;
+                for (int share = 0; share < shares; ++share, ++n) {
+                    const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
                     if (!(ok = wait_for(&bars.ready[acc], (n / 2) & 1, &bars))) break;
                     tc_fence_after();
+                    if (share == 0) {
 #pragma unroll
-                    for (int c = 0; c < kBN / 2; c += 16) {
-                        if (first + c < a.bn) {
-                            float z[16];
-                            tmem_ld16(lanes + acc * kBN + first + c, z);
-                            tmem_ld_wait();
+                        for (int j = 0; j < 4; ++j)
+                            if (32 * j < limit) tmem_ld32(at + 32 * j, z[j]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) part[c + i] += z[i];
+                        for (int j = 0; j < 4; ++j) loaded(z[j]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kBN / 2; c += 16) {
+                            if (c < limit) {
+                                float v[16];
+                                tmem_ld16(at + c, v);
+                                loaded(v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[c / 32][c % 32 + i] += v[i];
+                            }
                         }
                     }
                     taken(acc);
                 }
-                const uint32_t acc = n & 1;
-                if (!ok || !wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
-                ++n;
-                tc_fence_after();
+                if (!ok) break;
+                if (limit < kBN / 2) {
 #pragma unroll
-                for (int c = 0; c < kBN / 2; c += 16) {
-                    const int at = first + c;
-                    if (at < limit) {
-                        float z[16];
-                        tmem_ld16(lanes + acc * kBN + at, z);
-                        tmem_ld_wait();
+                    for (int i = 0; i < kBN / 2; ++i) z[i / 32][i % 32] = i < limit ? z[i / 32][i % 32] : kLeast;
+                }
+                if (target >= 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) z[i] = at + i < limit ? z[i] + part[c + i] : -INFINITY;
-                        if (target >= at && target < at + 16 && target < limit) {
-                            float v = z[0];
+                    for (int c = 0; c < kBN / 2; c += 16) {
+                        int in = target - c;
+                        asm volatile("" : "+r"(in));  // (or all of z is kept in memory and indexed)
+                        if (in >= 0 && in < 16) {
+                            float v = z[c / 32][c % 32];
 #pragma unroll
-                            for (int i = 1; i < 16; ++i) v = target == at + i ? z[i] : v;
+                            for (int i = 1; i < 16; ++i) v = in == i ? z[c / 32][c % 32 + i] : v;
                             a.given[row] = v;
                         }
-                        add_to(st, z);
                     }
                 }
-                taken(acc);
+                const Stat st = stat_of(z);
                 if (live && first < a.bn) a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
             } else {
-                const uint32_t acc = n & 1, at = lanes + acc * kBN;
+                const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
+                const int row0 = row - lane, limit = min(min(a.N - c0, a.bn) - first, kBN / 2);  // of this warp's columns
                 RowGrad g{};
                 FixRow fix{};
                 if constexpr (USE == kGrad) {
                     if (live) g = row_grad(a.grad, row, a.N);
-                    if (live && t.n == 0 && (g.target < 0 || g.none)) a.rest[row] = 0.f;
+                    if (live && t.n == 0 && half == 0 && (g.target < 0 || g.none)) a.rest[row] = 0.f;
                 } else if (t.part < 0) {
                     fix = fix_row(a.fix, row, live);
                 }
                 if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
                 ++n;
                 tc_fence_after();
-                for (int c = 0; c < a.bn; c += 32) {
-                    float z[32];
-                    tmem_ld32(at + c, z);
-                    tmem_ld_wait();
+                float z[2][32] = {};
+                if (limit > 0) {
+                    tmem_ld32(at, z[0]);
+                    loaded(z[0]);
+                }
+#pragma unroll
+                for (int c = 0; c < kBN / 2; c += 32) {
+                    float (&now)[32] = z[c / 32 % 2];
+                    if (c >= limit) continue;
+                    if (c + 32 < kBN / 2 && c + 32 < limit) tmem_ld32(at + c + 32, z[(c / 32 + 1) % 2]);
+                    const int col = c0 + first + c;
                     if constexpr (USE == kGrad) {
-                        if (live) {
-                            bf16 *p = a.dz + row * a.dz_pitch + c0 + c;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) z[i] = g.none ? 0.f : grad_of<ENT>(g, z[i]);
-                            if (g.target >= c0 + c && g.target < c0 + c + 32 && !g.none) {
+                        for (int i = 0; i < 32; ++i) now[i] = g.none ? 0.f : grad_of<ENT>(g, now[i]);
+                        if (g.target >= col && g.target < col + 32 && !g.none && live) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (c0 + c + i == g.target) {
-                                        z[i] += g.dlp;
-                                        a.rest[row] = z[i] - to_f32(from_f32<bf16>(z[i]));
-                                    }
-                                if (a.lead) atomicMin(&a.lead[g.target], row);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                if (c0 + c + i < a.dz_pitch) store16(p + i, z + i);
+                            for (int i = 0; i < 32; ++i)
+                                if (col + i == g.target) {
+                                    now[i] += g.dlp;
+                                    a.rest[row] = now[i] - to_f32(from_f32<bf16>(now[i]));
+                                }
+                            if (a.lead) atomicMin(&a.lead[g.target], row);
                         }
-                    } else if (t.part >= 0) {
-                        float *p = a.parts + (((int64_t)t.part * HALF + rank) * kBM + q * 32 + lane) * a.bn + c;
+                    }
+                    if (USE == kStore && t.part >= 0) {
+                        float *p = a.parts + (((int64_t)t.part * HALF + rank) * kBM + q * 32 + lane) * a.bn + first + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(p + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
-                    } else if (live) {
-                        bf16 *p = a.out + row * a.out_pitch + c0 + c;
+                            *reinterpret_cast<float4 *>(p + i) = make_float4(now[i], now[i + 1], now[i + 2], now[i + 3]);
+                    } else if (row0 < a.M) {
+                        // by way of shared memory, 32 rows of 64 columns in the layout that the copy expects
+                        if (c % 64 == 0) {
+                            if (lane == 0) bulk_wait_read_all();
+                            __syncwarp();
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (c0 + c + i < a.N) {
-                                fix_add(fix, c0 + c + i, z + i);
-                                store16(p + i, z + i);
+                        for (int i = 0; i < 32; i += 8) {
+                            if (USE == kStore && col + i < a.N) fix_add(fix, col + i, now + i);
+                            store16(reinterpret_cast<bf16 *>(stage + lane * 128 + (((c % 64 + i) / 8 ^ (lane & 7)) * 16)), now + i);
+                        }
+                        if (c % 64 == 32 || c + 32 >= limit) {
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(&mo, stage, col / 64 * 64, row0);
+                                bulk_commit_group();
                             }
+                        }
                     }
+                    loaded(z[(c / 32 + 1) % 2]);
                 }
                 taken(acc);
             }
         }
+        if (USE != kStats && lane == 0) bulk_wait_all();  // the copies have read what they store
     }
     tc_fence_before();
     __syncthreads();
@@ -693,7 +761,8 @@ HeadPlan plan_bwd(const ssd_head_shape_t *s) {
 }
 
 template <int USE, bool A_MN, bool B_MN, bool ENT>
-cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a, const char *name, cudaStream_t st) {
+cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const GemmArgs &a, const char *name,
+                     cudaStream_t st) {
     auto kernel = a.pair ? gemm_kernel<USE, A_MN, B_MN, ENT, true> : gemm_kernel<USE, A_MN, B_MN, ENT, false>;
     // (set on every call: cheap, and right for each device and context)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -701,7 +770,7 @@ cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArg
     const int blocks = a.pair ? 2 : 1, places = kSMs / blocks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * (a.units < places ? a.units : places)));
-    cfg.blockDim = dim3(gemm_threads(USE));
+    cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -709,7 +778,7 @@ cudaError_t run_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArg
     attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.pair ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, a);
     timing_mark(st, name);
     return e;
 }
@@ -781,7 +850,7 @@ ssd_status_t ssd_head_logprob_fwd(const ssd_head_shape_t *shape, const ssd_rows_
     cudaError_t e = device_status_word(&a.status);
     if (e != cudaSuccess) return status_of(e);
     timing_begin(stream);
-    e = run_gemm<kStats, false, false, false>(mh, mw, a, "head_logprob", stream);
+    e = run_gemm<kStats, false, false, false>(mh, mw, mw, a, "head_logprob", stream);
     if (e != cudaSuccess) return status_of(e);
     const int per = T > 8 * kSMs ? 8 : 1;
     e = launch(head_rows_kernel, dim3((unsigned)((T + per - 1) / per)), 256, 0, stream, true, a.stats, a.given, a.targets, (int)T,
@@ -814,11 +883,13 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     char *ws = static_cast<char *>(workspace);
     bf16 *dz = reinterpret_cast<bf16 *>(ws + p.dz);
     const int64_t hp = pitch_of(*hidden, T, D), wp = pitch_of(*weight, V, D);
-    CUtensorMap mh, mw, mz, mz_t, mw_t, mh_t;
+    CUtensorMap mh, mw, mz, mz_t, mw_t, mh_t, mz_out, mdh, mdw;
     // dz: only its V columns are read, whatever lies behind them
     if (!map_of(&mh, hidden->data, T, D, hp, p.z.arows) || !map_of(&mw, weight->data, V, D, wp, p.z.bn / (p.z.pair ? 2 : 1)) ||
         !map_of(&mz, dz, T, V, p.pitch, p.dh.arows) || !map_of(&mw_t, weight->data, V, D, wp, kBK) ||
-        !map_of(&mz_t, dz, T, V, p.pitch, kBK) || !map_of(&mh_t, hidden->data, T, D, hp, kBK))
+        !map_of(&mz_t, dz, T, V, p.pitch, kBK) || !map_of(&mh_t, hidden->data, T, D, hp, kBK) ||
+        !map_of(&mz_out, dz, T, V, p.pitch, 32) || (dhidden && !map_of(&mdh, dhidden->data, T, D, pitch_of(*dhidden, T, D), 32)) ||
+        (dweight && !map_of(&mdw, dweight->data, V, D, pitch_of(*dweight, V, D), 32)))
         return SSD_ERR_CUDA;
     unsigned *status = nullptr;
     cudaError_t e = device_status_word(&status);
@@ -827,7 +898,6 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     GemmArgs a = p.z;
     a.status = status;
     a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
-    a.dz = dz, a.dz_pitch = p.pitch;
     a.rest = reinterpret_cast<float *>(ws + p.rest);
     const bool given = targets && dlogprob;  // otherwise no element of dz stands out
     if (dweight && given) {
@@ -836,15 +906,15 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         timing_mark(stream, "head_leads");
         if (e != cudaSuccess) return status_of(e);
     }
-    e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, a, "head_dlogits", stream)
-                 : run_gemm<kGrad, false, false, false>(mh, mw, a, "head_dlogits", stream);
+    e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, mz_out, a, "head_dlogits", stream)
+                 : run_gemm<kGrad, false, false, false>(mh, mw, mz_out, a, "head_dlogits", stream);
     if (e == cudaSuccess && dhidden) {
         GemmArgs b = p.dh;
         b.status = status;
         b.out = static_cast<bf16 *>(dhidden->data), b.out_pitch = pitch_of(*dhidden, T, D);
         b.parts = reinterpret_cast<float *>(ws + p.parts);
         if (given) b.fix = Fix{targets, a.rest, static_cast<const bf16 *>(weight->data), wp, (int)V, nullptr, nullptr, D};
-        e = run_gemm<kStore, false, true, false>(mz, mw_t, b, "head_dhidden", stream);
+        e = run_gemm<kStore, false, true, false>(mz, mw_t, mdh, b, "head_dhidden", stream);
         if (e == cudaSuccess) e = run_parts(b, stream);
     }
     if (e == cudaSuccess && dweight) {
@@ -861,7 +931,7 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
             if (e != cudaSuccess) return status_of(e);
             b.fix = Fix{nullptr, nullptr, nullptr, 0, (int)V, a.lead, sums, D};
         }
-        e = run_gemm<kStore, true, true, false>(mz_t, mh_t, b, "head_dweight", stream);
+        e = run_gemm<kStore, true, true, false>(mz_t, mh_t, mdw, b, "head_dweight", stream);
         if (e == cudaSuccess) e = run_parts(b, stream);
     }
     return status_of(e);
