@@ -9,10 +9,14 @@
 // The blocks of the prompt's kernels, a few on each SM, take one tile after
 // another: kCols channels, two a lane, and kWarps x S consecutive tokens, S a
 // warp, whose inputs stay in registers from the one read to the output; the
-// next tile's are copied into shared memory meanwhile.  What a run of tokens does to the state is
-// h -> A h + H; warps exchange their (A, H) through shared memory, tiles
-// theirs through the workspace (Links).  A run that holds a sequence's
-// boundary does not let the state through, whatever its value: A = -1 says so.
+// next tile's are copied into shared memory meanwhile.  What a run of tokens
+// does to the state is h -> A h + H; warps exchange their (A, H) through shared
+// memory, tiles theirs through the workspace (Links).  A run that holds a
+// sequence's boundary does not let the state through, whatever its value:
+// A = -1 says so.
+//
+// Why one pass: a pass that only sums tiles up, and another from the states
+// that enter them, would read x, r and i twice (1.6 times the bytes).
 #pragma once
 
 #include "ssd_channel.h"
@@ -49,7 +53,8 @@ __device__ __forceinline__ float2 widen(const Two<float> &v) { return v.w; }
 
 // A lane's channels: c0 and c1 of the block's 64.  Rows whose pairs lie on
 // their own size's boundary are read in pairs, two neighbours a lane; others
-// one element at a time, 32 neighbours a warp.
+// one element at a time, 32 neighbours a warp (65537 x 2560 packed bf16, rows
+// of 2560: 449 us; of 2562, pairs without 16-byte copies: 529; of 2561: 1174).
 template <bool PAIRS>
 struct Lane {
     int c0;
@@ -86,10 +91,11 @@ __device__ __forceinline__ Two<T> load_two(const T *row, const Lane<PAIRS> &k, f
     }
     return v;
 }
-// The same into shared memory, where the lane itself reads it later: an asynchronous copy, of rows whose elements lie on
-// four-byte boundaries.  `there`: the token exists.
+// The same into shared memory, where the lane itself reads it later: an asynchronous copy, of rows whose elements or pairs lie
+// on four-byte boundaries.  `there`: the token exists.
 template <typename T, bool PAIRS>
 constexpr bool kAsync = PAIRS || sizeof(T) == 4;
+constexpr int kAtOnce = 8;
 __device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
     if (bytes == 8)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
@@ -99,26 +105,22 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <typename T, bool PAIRS>
 __device__ __forceinline__ void fetch_two(Two<T> *dst, const T *row, const Lane<PAIRS> &k, bool there, float fill) {
-    if constexpr (kAsync<T, PAIRS>) {
-        const T *p = place(row, k);
-        if constexpr (PAIRS) {
-            if (there && k.in0)
-                copy_async(dst, p, 2 * sizeof(T));
-            else
-                *dst = two_of(T(), fill);
-        } else {
-            float *d = reinterpret_cast<float *>(dst);
-            if (there && k.in0)
-                copy_async(d, p, 4);
-            else
-                d[0] = fill;
-            if (there && k.in1)
-                copy_async(d + 1, p + 32, 4);
-            else
-                d[1] = fill;
-        }
+    const T *p = place(row, k);
+    if constexpr (PAIRS) {
+        if (there && k.in0)
+            copy_async(dst, p, 2 * sizeof(T));
+        else
+            *dst = two_of(T(), fill);
     } else {
-        *dst = there ? load_two<T, PAIRS>(row, k, fill) : two_of(T(), fill);
+        float *d = reinterpret_cast<float *>(dst);
+        if (there && k.in0)
+            copy_async(d, p, 4);
+        else
+            d[0] = fill;
+        if (there && k.in1)
+            copy_async(d + 1, p + 32, 4);
+        else
+            d[1] = fill;
     }
 }
 // The copies of a warp's S tokens from one array, each lane's pair to dst[s * stride + lane].  Where rows lie on 16-byte
@@ -144,9 +146,32 @@ __device__ __forceinline__ void fetch_rows(Two<T> *dst, int stride, const T *row
             }
             src += step * (ROWS * (int)sizeof(T)), d += ROWS * stride * sizeof(Two<T>);
         }
-    } else {
+    } else if constexpr (kAsync<T, PAIRS>) {
 #pragma unroll
         for (int s = 0; s < S; ++s) fetch_two<T, PAIRS>(dst + s * stride + lane, row + step * s, k, s < left, fill);
+    } else {
+        // bf16 off its four-byte boundaries goes through registers: loads without conditions, so that kAtOnce tokens' are in
+        // flight (what is not there reads the last that is; with a condition each 2280 us)
+        const int last = max(min(S, left) - 1, 0), o0 = min(k.c0, ch - 1), o1 = min(k.c0 + 32, ch - 1);
+#pragma unroll
+        for (int s0 = 0; s0 < S; s0 += kAtOnce) {
+            T lo[kAtOnce], hi[kAtOnce];
+            if (left > 0) {
+#pragma unroll
+                for (int s = 0; s < kAtOnce; ++s) {
+                    const T *p = row + step * min(s0 + s, last);
+                    lo[s] = p[o0], hi[s] = p[o1];
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < kAtOnce; ++s) {
+                const bool there = s0 + s < left;
+                T v[2] = {there && k.in0 ? lo[s] : from_f32<T>(fill), there && k.in1 ? hi[s] : from_f32<T>(fill)};
+                Two<T> w;
+                memcpy(&w, v, sizeof(w));
+                dst[(s0 + s) * stride + lane] = w;
+            }
+        }
     }
 }
 template <typename T, bool PAIRS>
@@ -257,8 +282,10 @@ __device__ __forceinline__ Run then(const Run &r, const Run &s) {
 // run does not depend on other tiles, so a tile waits for the entry state of
 // its group and the runs before it in the group, in one round of loads; the
 // last of a group hands the next entry state on.  The order of every sum is
-// fixed.  Tiles are numbered by a counter, earlier tokens first, so what a
-// block waits for has started before it.
+// fixed.  Tiles are numbered by a counter, earlier tokens first, and a block
+// finishes its tiles in that order, so the first unfinished one never waits.
+// Groups of 16: one sequence of 65537 tokens, 64 channels 35 us (8: 58, 32:
+// 26), 48 packed ones of 2560 channels 461 (455, 487).
 struct Links {
     unsigned long long *run, *entry;  // null: one tile a row, nothing to wait for
     unsigned *ticket;
@@ -279,48 +306,36 @@ __device__ __forceinline__ unsigned long long link_load(const unsigned long long
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-// A run on its way: asked for before a tile's tokens are gone through, and mostly there when they are.
-struct Asked {
-    unsigned long long u, v;
-    __device__ __forceinline__ void ask(const unsigned long long *p) { u = link_load(p), v = link_load(p + 32); }
-    __device__ __forceinline__ bool unset() const { return (unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset; }
-    // Waits until both words are there; gives up after 100 ms and says so in the status word.
-    __device__ __forceinline__ Run wait(const unsigned long long *p, unsigned *status) {
-        if (unset()) ask(p);
-        if (unset()) {
-            const uint64_t t0 = tc::globaltimer_ns();
-            for (;;) {
-                ask(p);
-                if (!unset()) break;
-                const uint64_t spent = tc::globaltimer_ns() - t0;
-                if (spent > 100000000ull) atomicOr(status, 1u);
-                if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
-                __nanosleep(40);  // (other warps of the SM need the issue slots)
-            }
-        }
-        Run r;
-        r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
-        r.H = make_float2(__uint_as_float((unsigned)u), __uint_as_float((unsigned)v));
-        return r;
+// Waits until both words are there; gives up after 100 ms and says so in the status word.
+__device__ __forceinline__ Run link_wait(const unsigned long long *p, unsigned *status) {
+    unsigned long long u = link_load(p), v = link_load(p + 32);
+    auto unset = [&] { return (unsigned)(u >> 32) == kUnset || (unsigned)(v >> 32) == kUnset; };
+    if (unset()) {
+        const uint64_t t0 = tc::globaltimer_ns();
+        do {
+            __nanosleep(40);  // (other warps of the SM need the issue slots)
+            u = link_load(p), v = link_load(p + 32);
+            const uint64_t spent = tc::globaltimer_ns() - t0;
+            if (spent > 100000000ull) atomicOr(status, 1u);
+            if (spent > 1000000ull && *reinterpret_cast<volatile unsigned *>(status)) break;  // (another block's, too)
+        } while (unset());
     }
-};
+    Run r;
+    r.A = make_float2(__uint_as_float((unsigned)(u >> 32)), __uint_as_float((unsigned)(v >> 32)));
+    r.H = make_float2(__uint_as_float((unsigned)u), __uint_as_float((unsigned)v));
+    return r;
+}
 
-// A tile's place among the links: `at`, in the order in which states pass.  Warp j looks after the j-th run before it in its
-// group (and the (j + nw)-th), the last warp after the state that enters the group.
+// A tile's place among the links: number `at` of its row in the order in which states pass.
 struct Place {
     unsigned long long *mine, *entry;  // this tile's run; the state that enters its group
     int in_group;
     bool more;  // a tile follows in the row
-    Asked run, state;
-    // early: ask now (eight registers until pass_links)
-    __device__ __forceinline__ Place(const Links &l, int row, int at, int ntile, int warp, int nw, int lane, bool early) {
+    __device__ __forceinline__ Place(const Links &l, int row, int at, int ntile, int lane) {
         const int groups = (ntile + kGroup - 1) / kGroup;
         mine = l.run + ((int64_t)row * ntile + at) * kCols + lane;
         entry = l.entry + ((int64_t)row * groups + at / kGroup) * kCols + lane;
         in_group = at % kGroup, more = at + 1 < ntile;
-        run.u = run.v = state.u = state.v = ~0ull;
-        if (early && warp < in_group) run.ask(mine - (int64_t)(warp + 1) * kCols);
-        if (early && warp == nw - 1 && at >= kGroup) state.ask(entry);
     }
     __device__ __forceinline__ void publish(const Run &all) const {
         if (in_group != kGroup - 1 && more) link_store(mine, all);
@@ -330,16 +345,16 @@ struct LinkShared {
     float4 tiles[kGroup][32];
     float2 group[32], enter[32];
 };
-// The state that enters the tile; `first`: the one that enters the row.  `all`: the tile's own run, published, in warp 0.
-__device__ __forceinline__ float2 pass_links(Place &q, const Links &l, LinkShared &sh, float2 first, const Run &all, bool has_entry, int warp,
-                                             int nw, int lane) {
+// The state that enters the tile; `first`: the one that enters the row, for its first group.  `all`: the tile's own run,
+// published, in warp 0.  Warp j looks after the j-th run before it in its group (and the (j + nw)-th), the last warp after the
+// state that enters the group; warp 0 puts them together.
+__device__ __forceinline__ float2 pass_links(const Place &q, const Links &l, LinkShared &sh, float2 first, const Run &all, bool has_entry,
+                                             int warp, int nw, int lane) {
     for (int j = warp; j < q.in_group; j += nw) {
-        const unsigned long long *p = q.mine - (int64_t)(j + 1) * kCols;
-        if (j != warp) q.run.ask(p);
-        const Run r = q.run.wait(p, l.status);
+        const Run r = link_wait(q.mine - (int64_t)(j + 1) * kCols, l.status);
         sh.tiles[j][lane] = make_float4(r.A.x, r.A.y, r.H.x, r.H.y);
     }
-    if (warp == nw - 1 && has_entry) sh.group[lane] = q.state.wait(q.entry, l.status).H;
+    if (warp == nw - 1 && has_entry) sh.group[lane] = link_wait(q.entry, l.status).H;
     __syncthreads();
     if (warp == 0) {
         float2 h = has_entry ? sh.group[lane] : first;

@@ -10,8 +10,13 @@
 // A block is a tile as in the forward kernel, later tokens first: the state
 // that enters comes from those kept every 64 tokens, what comes back from
 // later tokens (c_t = a_t g_t, so c -> P c + Q over a run of tokens) through
-// the links.  Everything is read once and written once; what bounds it is in
-// the kernel's comment.
+// the links.  Everything is read once and written once.
+//
+// What bounds it: issue, 236 instructions a token and warp in 54% of the
+// cycles, with 15 registers a token kept between the passes (4 x 4096 x 2560
+// bf16 with a gate 236 us, 39% of the DRAM rate).  16 warps of 4 tokens or of 8
+// are slower (8 x 4096 x 2560: 606 and 559 us against 471), and so is keeping
+// beta s(i) x instead of forming it again (477).
 #include "ssd_gated.cuh"
 
 namespace ssd {
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
         if (linked && warp == 0) {
             all = run_of(back[p][nw - 1][lane]);
             for (int j = nw - 2; j >= 0; --j) all = then(all, run_of(back[p][j][lane]));
-            Place(a.links, w.row, w.later, a.ntile, warp, nw, lane, false).publish(all);
+            Place(a.links, w.row, w.later, a.ntile, lane).publish(all);
         }
         n = uniform((int)ticket[p]);
         const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
@@ -211,10 +216,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
             if (PACKED && after.t0 < L) next_cut = cuts_of<S>(a.seqs, after.t0);
         }
 
-        if (linked) {
-            Place place(a.links, w.row, w.later, a.ntile, warp, nw, lane, false);
-            c = pass_links(place, a.links, sh, c, all, w.later >= kGroup, warp, nw, lane);
-        }
+        if (linked)
+            c = pass_links(Place(a.links, w.row, w.later, a.ntile, lane), a.links, sh, c, all, w.later >= kGroup, warp, nw, lane);
         for (int j = nw - 1; j > warp; --j) c = through(run_of(back[p][j][lane]), c);
         for (int j = 0; j < warp; ++j) h = through(run_of(fore[p][j][lane]), h);
 

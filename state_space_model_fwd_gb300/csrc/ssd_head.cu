@@ -23,9 +23,11 @@
 //
 // What bounds it: the tensor cores under the power limit (1.05 TFLOP for dz in
 // 640 us, 1.65 PFLOP/s; a library product sustains 1.71).  Pairs: forward and
-// gradient of 4095 x 2560 x 50277 2617 us, single blocks 2928; the forward
-// product alone gains nothing from them.  With few rows the weights' one pass
-// bounds it: 16 rows x 2560 x 50280 55 us, 38 at the copy rate.
+// gradient of 4095 x 2560 x 50277 2617 us, single blocks 2928.  Below dim 512
+// or so the readers bound it: 8192 x 128 x 32000 in 94 us, 4.5 instructions and
+// one exponential a logit with two warps a scheduler (storing by thread and
+// taking the maximum anew every 16 columns: 243).  With few rows the weights'
+// one pass does: 16 x 2560 x 50280 in 54 us, 38 at the copy rate.
 #include <cudaTypedefs.h>
 
 #include "ssd_logprob.cuh"
@@ -678,16 +680,15 @@ bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t p
 constexpr int kSMs = 152;
 
 // Tiles of 256 rows where they leave no more than an eighth of the rows empty and sums are long enough for a pair's longer
-// start (8192 x 512 x 32000: 241 us, in pairs 288; forward and gradient of T x 2560 x 50277, T = 300: 463 us, pairs wherever the columns allow 536; T = 300, 500, 768,
-// 1000: pairs for dweight, a sum over T, in spite of its length 478, 574, 710, 944 us, otherwise 463, 564, 709, -; no pairs at
-// all -, -, -, 1017).
+// start.  8192 x 256 x 32000 120 us, in pairs 134; x 512 193 and 199.  Forward and gradient of T x 2560 x 50277, T = 300: 349 us,
+// with pairs for dweight, a sum over T, 362; T = 1000: 793 us, without any pairs 875.
 bool takes_pairs(int64_t M, int64_t K, int bn) {
     const int64_t padded = (M + 2 * kBM - 1) / (2 * kBM) * (2 * kBM);
     return bn % 128 == 0 && K >= 640 && padded - M <= padded / 8;
 }
 
 // Tiles and units of a product.  `split`: tiles beyond the last full round of blocks are cut along K, so that every SM has a share
-// (forward and gradient of 300 x 2560 x 50277: 478 us, whole tiles only 709; 64 rows: 349 and 606).
+// (forward and gradient of 300 x 2560 x 50277, at the time 478 us: whole tiles only 709; of 64 rows: 349 and 606).
 GemmArgs plan_gemm(int64_t M, int64_t N, int64_t K, int bn, bool split, bool a_mn = false) {
     GemmArgs a{};
     a.M = (int)M, a.N = (int)N, a.K = (int)K, a.bn = bn;
@@ -715,20 +716,6 @@ size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)
 
 int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); }
 
-// Columns of a forward tile.  With one row of tiles the weights' one pass sets the time: the widest of the column counts
-// that leave the fewest columns to the busiest SM (16 x 2560 x 20000: 27.1 us, with 256 columns 28.2; 128 x 2560 x 50280: 55.2
-// and 56.9).
-int forward_columns(int64_t T, int64_t V) {
-    if (T > kBM) return fit_columns(V);
-    int best = 256;
-    int64_t least = INT64_MAX;
-    for (int bn = 256; bn >= 64; bn -= 16) {
-        const int64_t tiles = (V + bn - 1) / bn, cost = (tiles + kSMs - 1) / kSMs * bn;
-        if (cost < least) least = cost, best = bn;
-    }
-    return best;
-}
-
 int halves(const GemmArgs &a) { return a.bn > kBN / 2 ? 2 : 1; }
 
 struct HeadPlan {
@@ -738,7 +725,7 @@ struct HeadPlan {
 };
 HeadPlan plan_fwd(const ssd_head_shape_t *s) {
     HeadPlan p{};
-    p.z = plan_gemm(s->rows, s->vocab, s->dim, forward_columns(s->rows, s->vocab), false);
+    p.z = plan_gemm(s->rows, s->vocab, s->dim, fit_columns(s->vocab), false);
     p.stats = 0;
     p.given = align256(sizeof(float4) * p.z.nt * halves(p.z) * s->rows);
     p.bytes = p.given + align256(sizeof(float) * s->rows);
