@@ -542,8 +542,8 @@ SSD_API ssd_status_t ssd_block_norm_bwd(const ssd_norm_shape_t *shape, const ssd
  *   lse = log sum_v exp(z_v),  logprob = z_target - lse,
  *   entropy = lse - sum_v p_v z_v  (p = exp(z - lse)),
  * and the `top` most probable tokens, the most probable first, equal ones by
- * index (NaN before everything).  logits [rows, vocab] T (row_stride;
- * batch_stride is ignored), targets [rows]; outputs fp32, top_logprob and
+ * index (NaN before everything).  logits [rows, vocab] T (row_stride, here
+ * below 2^40; batch_stride is ignored), targets [rows]; outputs fp32, top_logprob and
  * top_index [rows, top] (top up to SSD_LOGPROB_MAX_TOP); logprob (and targets
  * with it), lse, entropy may be NULL.  Sums are held in fp32.
  * A negative target gives no token: logprob 0, no gradient.  A target past
@@ -582,8 +582,10 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
  * relative, as the operands are), but for the given tokens' elements, which
  * keep fp32 accuracy, and takes 2 rows vocab bytes of the workspace; sums over
  * it are fp32, in a fixed order, and rounded once.
- * Supported: bf16, dim a multiple of 8.  A wait that gives up in a kernel is
- * reported by ssd_get_device_status.
+ * Supported: bf16, dim a multiple of 8 up to 2^20, vocab and rows up to 2^22,
+ * row strides below 2^39.  Logits are taken to be above -1e38: minus infinity
+ * among them (an infinite weight) makes the entropy NaN.  A wait that gives up
+ * in a kernel is reported by ssd_get_device_status.
  */
 typedef struct {
     int64_t rows, vocab, dim;

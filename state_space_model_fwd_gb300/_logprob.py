@@ -15,6 +15,9 @@ import torch
 from ._layer import _F32, _code, _empty, _fail, _flat, _given, _lib, _norm_rows, _on_stream, _rows_t, _workspace
 
 
+_MAX_TOP = 64
+
+
 class _logprob_shape_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("top", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
@@ -73,7 +76,7 @@ def ssd_token_logprob_fwd(logits, targets=None, *, top=0, return_entropy=True):
     tp = _flat(targets, "targets", torch.int64, lead, dev)
     logprob, lse, entropy = _row_outputs(lead, logits, targets, return_entropy)
     value = index = None
-    if top:
+    if 0 < top <= _MAX_TOP:  # (others are refused by the call)
         value, index = _empty((*lead, top), _F32, logits), _empty((*lead, top), torch.int64, logits)
     st = lib.ssd_token_logprob_fwd(ctypes.byref(shape), ctypes.byref(zr), tp, _ptr(logprob), lse.data_ptr(), _ptr(entropy),
                                    _ptr(value), _ptr(index), torch._C._cuda_getCurrentRawStream(dev))

@@ -175,4 +175,10 @@ __device__ __forceinline__ float grad_of(const RowGrad &g, float z) {
     return p * g.coef;
 }
 
+// Rows at one stride, which may be as far apart as batches elsewhere (the last rows of long prompts' logits).
+inline bool far_rows_ok(const ssd_rows_t &r, size_t esize) { return rows_in_ok(ssd_rows_t{r.data, r.row_stride, 0}, esize); }
+inline bool far_rows_out_ok(const ssd_rows_t &r, size_t esize, int64_t rows, int64_t cols) {
+    return rows_out_ok(ssd_rows_t{r.data, r.row_stride, 0}, esize, rows, 1, cols);
+}
+
 }  // namespace ssd

@@ -243,6 +243,22 @@ def test_in_place_strided_and_leading_dimensions(dtype, vocab):
 
 
 @pytest.mark.gpu
+def test_rows_far_apart():
+    """The last rows of long prompts' logits: more than 2^31 elements from one to the next."""
+    far = (1 << 31) + 8
+    rows = torch.empty(far + 1000, dtype=torch.bfloat16, device="cuda").as_strided((2, 1000), (far, 1))
+    rows[:] = make("bf16", 2, 1000, seed=11)[0]
+    targets = torch.tensor([3, 999], device="cuda")
+    got = ssd.ssd_token_logprob_fwd(rows, targets, top=3)
+    for a, b in zip(got, ssd.ssd_token_logprob_fwd(rows.contiguous(), targets, top=3)):
+        assert torch.equal(a, b)
+    want = ssd.ssd_token_logprob_bwd(rows.contiguous(), targets, got[1], dlogprob=got[1])
+    assert torch.equal(ssd.ssd_token_logprob_bwd(rows, targets, got[1], dlogprob=got[1], dlogits=rows), want)
+    one = rows[:1].as_strided((1, 1000), (1 << 39, 1))  # (a single row's stride means nothing)
+    assert torch.equal(ssd.ssd_token_logprob_fwd(one)[1], ssd.ssd_token_logprob_fwd(want[:1] * 0 + one)[1])
+
+
+@pytest.mark.gpu
 def test_captured_on_a_stream_and_bitwise():
     z, targets = make("bf16", 3, 50280, seed=9)
     glp = grads(3)[0]
@@ -302,7 +318,7 @@ def c_call(lib, bwd=False, logits=(FAKE, 0, 1000), out=(FAKE, 0, 1000), targets=
     (dict(vocab=0), INVALID), (dict(rows=-1), INVALID), (dict(dtype=3), INVALID), (dict(top=-1), INVALID),
     (dict(vocab=10, top=11), INVALID), (dict(top=65), UNSUPPORTED), (dict(vocab=(1 << 30) + 1), UNSUPPORTED),
     (dict(rows=(1 << 28) + 1), UNSUPPORTED), (dict(logits=(None, 0, 1000)), INVALID), (dict(logits=(FAKE + 1, 0, 1000)), INVALID),
-    (dict(logits=(FAKE, 0, -1)), INVALID), (dict(logits=(FAKE, 0, 1 << 31)), INVALID), (dict(targets=FAKE + 4), INVALID),
+    (dict(logits=(FAKE, 0, -1)), INVALID), (dict(logits=(FAKE, 0, 1 << 40)), INVALID), (dict(targets=FAKE + 4), INVALID),
     (dict(targets=None), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(rows=0), OK),
 ])
 def test_arguments_are_checked(lib, bwd, kw, code):
@@ -333,6 +349,9 @@ def test_binding_refuses_on_the_gpu():
         ssd.ssd_token_logprob_fwd(z, targets, top=65)
     with pytest.raises(ssd.SSDError):
         ssd.ssd_token_logprob_fwd(z, targets, top=101)
+    for top in (-1, 1 << 50):
+        with pytest.raises(ssd.SSDError):
+            ssd.ssd_token_logprob_fwd(z, targets, top=top)
     with pytest.raises(TypeError):
         ssd.ssd_token_logprob_bwd(z, targets, None)
     with pytest.raises(ValueError):
