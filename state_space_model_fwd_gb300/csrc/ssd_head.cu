@@ -55,7 +55,7 @@ constexpr int kGemmThreads = 128 + 32 * kReaders;  // warps: copy, MMA, TMEM, -,
 // dz is rounded to bf16 (2^-9 relative, as its products' other operands are), which would show where one element outweighs all
 // others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
 //   dhidden[row] += rest[row] weight[target[row]],   dweight[v] += sum over rows with target v of rest[row] hidden[row],
-// the latter summed by fix_kernel into the row of the first of them.  (4095 x 2560 x 50277: error against 64 bits 1.4 times a
+// the latter summed by head_fix_kernel and found by way of lead[v], one of those rows.  (4095 x 2560 x 50277: error against 64 bits 1.4 times a
 // bf16 rounding without it, 1.0 with it, for 1% of the time; with few rows up to 1.8 times.)
 struct Fix {
     const int64_t *targets;  // dhidden
@@ -112,7 +112,6 @@ struct GemmArgs {
     float *given;         // [M] the given tokens' logits
     RowGradIn grad;
     float *rest;          // [M] what rounding left of the given token's dz (0 without one)
-    int *lead;            // [N] the first row that has a token as its given one (null: not wanted)
     // kStore
     bf16 *out;
     int64_t out_pitch;
@@ -506,7 +505,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                     now[i] += g.dlp;
                                     a.rest[row] = now[i] - to_f32(from_f32<bf16>(now[i]));
                                 }
-                            if (a.lead) atomicMin(&a.lead[g.target], row);
                         }
                     }
                     if (USE == kStore && t.part >= 0) {
@@ -603,50 +601,99 @@ __global__ void __launch_bounds__(256) head_parts_kernel(const __grid_constant__
     store16(a.out + row * a.out_pitch + col, v);
 }
 
-// sums[r] = sum of rest[row] hidden[row] over the rows with row r's target, in order, for rows r that are the first with theirs.
-// A block a row, 8 columns a thread.
-constexpr int kFixList = 1024;
-__global__ void __launch_bounds__(256) head_fix_kernel(const int64_t *targets, const int *lead, const float *rest, const bf16 *hidden,
-                                                       int64_t pitch, int rows, int dim, int vocab, float *sums) {
-    __shared__ int list[kFixList], counts[8];
+// What dweight's rows are given for rounding dz: sums[r] = sum of rest[row] hidden[row] over the rows with row r's target, in
+// two steps so that neither many rows nor many of one target cost more than their share.  Rows are taken in chunks of
+// fix_chunk(); the first row of a target in each chunk (a block a row, 8 columns a thread) sums the chunk's, in order, and
+// enters the target's chain of chunks.  (4095 x 2560 x 50277, random targets 35 us, one for all rows 86; 131072 rows 1.1 ms of
+// 72.  One scan of all rows by the first of each target: 27 us, 3.8 ms and 8.2 ms.)
+constexpr int kFixRows = 4096, kFixChunks = 1024;  // the largest chunk, and how many there are at most
+static_assert((int64_t)kFixRows * kFixChunks >= 1 << 22, "every number of rows that is supported");
+int fix_chunk(int64_t rows) {
+    const int64_t c = (rows + kFixChunks - 1) / kFixChunks;
+    return (int)((c + 255) / 256 * 256);
+}
+__global__ void __launch_bounds__(256, 4) head_fix_kernel(const int64_t *targets, const float *rest, const bf16 *hidden, int64_t pitch,
+                                                       int rows, int dim, int vocab, int chunk, int *lead, int *next, float *sums) {
+    __shared__ int list[kFixRows], counts[8];
     const int r = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t t = targets[r];
-    if (t < 0 || t >= vocab || lead[t] != r) return;
-    float *out = sums + (int64_t)r * dim;
+    if (t < 0 || t >= vocab) return;
+    const int begin = r / chunk * chunk, end = min(begin + chunk, rows);
     int n = 0;
-    bool begun = false;
-    for (int base = r; base < rows; base += 256) {
+    for (int base = begin; base < end; base += 256) {
         const int row = base + threadIdx.x;
-        const unsigned same = __ballot_sync(0xffffffffu, row < rows && targets[row] == t);
-        if (lane == 0) counts[warp] = __popc(same);
-        __syncthreads();
-        int at = n, total = 0;
+        const bool same = row < end && targets[row] == t;
+        const unsigned which = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) counts[warp] = __popc(which);
+        if (__syncthreads_or(same && row < r)) return;  // not the first
+        int at = n;
         for (int w = 0; w < 8; ++w) {
             if (w < warp) at += counts[w];
-            total += counts[w];
+            n += counts[w];
         }
-        if (same >> lane & 1) list[at + __popc(same & ((1u << lane) - 1))] = row;
-        n += total;
+        if (same) list[at + __popc(which & ((1u << lane) - 1))] = row;
         __syncthreads();
-        if (n + 256 <= kFixList && base + 256 < rows) continue;
-        for (int c = threadIdx.x * 8; c < dim; c += 2048) {
-            float v[8] = {};
-            if (begun) {
+    }
+    constexpr int U = 8;
+    for (int c = threadIdx.x * 8; c < dim; c += 2048) {
+        float v[8] = {};
+        int k = 0;
+        for (; k + U <= n; k += U) {
+            Vec<bf16, 8> h[U];
+            float q[U];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = out[c + i];
-            }
-            for (int k = 0; k < n; ++k) {
-                float h[8];
-                widen<bf16, 8>(load_vec<bf16, 8>(hidden + list[k] * pitch + c), h);
-                const float q = rest[list[k]];
+            for (int u = 0; u < U; ++u) h[u] = load_vec<bf16, 8>(hidden + list[k + u] * pitch + c), q[u] = rest[list[k + u]];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = fmaf(q, h[i], v[i]);
+            for (int u = 0; u < U; ++u) {
+                float f[8];
+                widen<bf16, 8>(h[u], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(q[u], f[i], v[i]);
             }
-            *reinterpret_cast<float4 *>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(out + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
-        n = 0, begun = true;
-        __syncthreads();
+        for (; k < n; ++k) {
+            float f[8];
+            widen<bf16, 8>(load_vec<bf16, 8>(hidden + list[k] * pitch + c), f);
+            const float q = rest[list[k]];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(q, f[i], v[i]);
+        }
+        float *out = sums + (int64_t)r * dim + c;
+        *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    if (threadIdx.x == 0) next[r] = atomicExch(&lead[t], r);
+}
+// The chunks of each target, in the order of their rows, to sums of the row that the chain begins with (any of them: rows
+// enter as blocks end).
+__global__ void __launch_bounds__(256) head_chains_kernel(const int64_t *targets, const int *lead, const int *next, int dim, int vocab,
+                                                          float *sums) {
+    __shared__ int chain[kFixChunks], sorted[kFixChunks], count;
+    const int r = blockIdx.x;
+    wait_previous();
+    const int64_t t = targets[r];
+    if (t < 0 || t >= vocab || lead[t] != r || next[r] == kNoLead) return;
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int q = r; q != kNoLead && n < kFixChunks; q = next[q]) chain[n++] = q;
+        count = n;
+    }
+    __syncthreads();
+    const int n = count;
+    for (int i = threadIdx.x; i < n; i += 256) {
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += chain[j] < chain[i];
+        sorted[before] = chain[i];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < dim; c += 1024) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(sums + (int64_t)sorted[i] * dim + c);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        *reinterpret_cast<float4 *>(sums + (int64_t)r * dim + c) = v;
     }
 }
 
@@ -719,7 +766,7 @@ int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); 
 int halves(const GemmArgs &a) { return a.bn > kBN / 2 ? 2 : 1; }
 
 struct HeadPlan {
-    size_t stats, given, dz, rest, lead, sums, parts, bytes;
+    size_t stats, given, dz, rest, lead, next, sums, parts, bytes;
     int64_t pitch;
     GemmArgs z, dh, dw;
 };
@@ -740,7 +787,8 @@ HeadPlan plan_bwd(const ssd_head_shape_t *s) {
     p.dz = 0;
     p.rest = align256(2 * s->rows * p.pitch);
     p.lead = p.rest + align256(sizeof(float) * s->rows);
-    p.sums = p.lead + align256(sizeof(int) * s->vocab);
+    p.next = p.lead + align256(sizeof(int) * s->vocab);
+    p.sums = p.next + align256(sizeof(int) * s->rows);
     p.parts = p.sums + align256(sizeof(float) * s->rows * s->dim);
     const size_t a = parts_bytes(p.dh), b = parts_bytes(p.dw);
     p.bytes = p.parts + (a > b ? a : b);
@@ -794,7 +842,8 @@ ssd_status_t check_head(const ssd_head_shape_t *s) {
 }
 // Rows that TMA reads: 16-byte aligned, each of them.
 bool tma_rows(const ssd_rows_t &r, int64_t rows, int64_t dim) {
-    return rows_in_ok(r, 2) && aligned(r.data, 16) && (rows <= 1 || (r.row_stride % 8 == 0 && r.row_stride >= dim));
+    return far_rows_ok(r, 2) && aligned(r.data, 16) &&
+           (rows <= 1 || (r.row_stride % 8 == 0 && r.row_stride >= dim && r.row_stride < kMaxBatchStride / 2));
 }
 int64_t pitch_of(const ssd_rows_t &r, int64_t rows, int64_t dim) { return rows > 1 ? r.row_stride : dim; }
 
@@ -854,7 +903,7 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     const ssd_status_t ok = check_head(shape);
     if (ok != SSD_OK) return ok;
     const int64_t T = shape->rows, V = shape->vocab, D = shape->dim;
-    if (dweight && (!tma_rows(*dweight, V, D) || !rows_out_ok(*dweight, 2, 1, V, D))) return SSD_ERR_INVALID_ARG;
+    if (dweight && (!tma_rows(*dweight, V, D) || !far_rows_out_ok(*dweight, 2, V, D))) return SSD_ERR_INVALID_ARG;
     if (T == 0) {
         if (!dweight) return SSD_OK;
         return status_of(cudaMemset2DAsync(dweight->data, pitch_of(*dweight, V, D) * 2, 0, D * 2, V, stream));
@@ -863,7 +912,7 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         !aligned(targets, 8) || !aligned(dlogprob, 4) || !aligned(dlse, 4) || !aligned(dentropy, 4) || (dlogprob && !targets) ||
         (dentropy && !entropy))
         return SSD_ERR_INVALID_ARG;
-    if (dhidden && (!tma_rows(*dhidden, T, D) || !rows_out_ok(*dhidden, 2, 1, T, D))) return SSD_ERR_INVALID_ARG;
+    if (dhidden && (!tma_rows(*dhidden, T, D) || !far_rows_out_ok(*dhidden, 2, T, D))) return SSD_ERR_INVALID_ARG;
     if (!dhidden && !dweight) return SSD_OK;
     HeadPlan p = plan_bwd(shape);
     if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
@@ -887,12 +936,6 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
     a.rest = reinterpret_cast<float *>(ws + p.rest);
     const bool given = targets && dlogprob;  // otherwise no element of dz stands out
-    if (dweight && given) {
-        a.lead = reinterpret_cast<int *>(ws + p.lead);
-        e = cudaMemsetAsync(a.lead, 0x7F, sizeof(int) * V, stream);
-        timing_mark(stream, "head_leads");
-        if (e != cudaSuccess) return status_of(e);
-    }
     e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, mz_out, a, "head_dlogits", stream)
                  : run_gemm<kGrad, false, false, false>(mh, mw, mz_out, a, "head_dlogits", stream);
     if (e == cudaSuccess && dhidden) {
@@ -911,12 +954,21 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         b.parts = reinterpret_cast<float *>(ws + p.parts);
         if (given) {
             float *sums = reinterpret_cast<float *>(ws + p.sums);
-            head_fix_kernel<<<(unsigned)T, 256, 0, stream>>>(targets, a.lead, a.rest, static_cast<const bf16 *>(hidden->data), hp, (int)T,
-                                                             (int)D, (int)V, sums);
+            int *lead = reinterpret_cast<int *>(ws + p.lead), *next = reinterpret_cast<int *>(ws + p.next);
+            const int chunk = fix_chunk(T);
+            e = cudaMemsetAsync(lead, 0x7F, sizeof(int) * V, stream);  // kNoLead
+            timing_mark(stream, "head_leads");
+            if (e != cudaSuccess) return status_of(e);
+            head_fix_kernel<<<(unsigned)T, 256, 0, stream>>>(targets, a.rest, static_cast<const bf16 *>(hidden->data), hp, (int)T, (int)D,
+                                                             (int)V, chunk, lead, next, sums);
             timing_mark(stream, "head_fix");
             e = cudaGetLastError();
+            if (e == cudaSuccess && T > chunk) {
+                e = launch(head_chains_kernel, dim3((unsigned)T), 256, 0, stream, true, targets, lead, next, (int)D, (int)V, sums);
+                timing_mark(stream, "head_chains");
+            }
             if (e != cudaSuccess) return status_of(e);
-            b.fix = Fix{nullptr, nullptr, nullptr, 0, (int)V, a.lead, sums, D};
+            b.fix = Fix{nullptr, nullptr, nullptr, 0, (int)V, lead, sums, D};
         }
         e = run_gemm<kStore, true, true, false>(mz_t, mh_t, mdw, b, "head_dweight", stream);
         if (e == cudaSuccess) e = run_parts(b, stream);

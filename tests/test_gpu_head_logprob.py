@@ -56,6 +56,33 @@ def test_forward(rows, dim, vocab, pad):
     check_forward(ssd.ssd_head_logprob_fwd(h, w), z, None, dim)
 
 
+@pytest.mark.gpu
+def test_many_rows_with_the_same_tokens():
+    """So many that the chunks they are summed in are longer than a block, and there are hundreds of them."""
+    rows, dim, vocab = 270000, 8, 40
+    h, w, targets = make(rows, dim, vocab, seed=2)
+    targets[:1000] = 7
+    targets[100000:160000] = -1
+    glp = upstream(rows)[0]
+    _, lse, _ = ssd.ssd_head_logprob_fwd(h, w, targets)
+    _, dw = ssd.ssd_head_logprob_bwd(h, w, targets, lse, dlogprob=glp, need_dhidden=False)
+    z = logits(h, w)
+    _, wlse, went = definition(z, targets)
+    zero = torch.zeros(rows, dtype=torch.float64)
+    d = want_gradient(z, targets.cpu(), wlse, went, ref.d(glp), zero, zero)
+    # as in test_the_given_tokens_part_is_not_rounded; and the fp32 sums, two parts of 8438 additions of 16 rows, each cut off by
+    # up to 2^-24 of the sum so far: 5e-4 of that, which stays within the result and 3 of the terms' root sum of squares
+    p = torch.exp(z - wlse[:, None])
+    err = d.abs() * 2.0 ** -8 + 2e-5 * p * ref.d(glp).abs()[:, None]
+    has = targets.cpu() >= 0
+    err[has, targets.cpu()[has]] = 2e-5 * ref.d(glp).abs()[has]
+    x = d.t() @ ref.d(h)
+    h2 = ref.d(h) ** 2
+    scale = 5 / math.sqrt(3) * ((err.t() ** 2) @ h2).sqrt() + 5e-4 * (x.abs() + 3 * ((d.t() ** 2) @ h2).sqrt())
+    ref.check(dw, x, "dweight", rel=1.0, scale=scale)
+    assert torch.equal(ssd.ssd_head_logprob_bwd(h, w, targets, lse, dlogprob=glp, need_dhidden=False)[1], dw)
+
+
 def upstream(rows, seed=3):
     g = torch.Generator().manual_seed(seed)
     return [(torch.rand(rows, generator=g) - 0.3).cuda() for _ in range(3)]
@@ -85,12 +112,13 @@ def test_gradient(rows, dim, vocab, pad, which):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,dim,vocab,kinds", [(1, 64, 300, 1), (40, 72, 1000, 2), (1500, 64, 500, 1), (3000, 2056, 257, 3)])
+@pytest.mark.parametrize("rows,dim,vocab,kinds", [(1, 64, 300, 1), (40, 72, 1000, 2), (1500, 64, 500, 1), (3000, 2056, 257, 3),
+                                                  (255, 64, 300, 1), (257, 72, 300, 2), (5000, 8, 131, 131)])
 def test_the_given_tokens_part_is_not_rounded(rows, dim, vocab, kinds):
     """Where the given token's element outweighs the others; few and many rows with the same one, some without."""
     h, w, _ = make(rows, dim, vocab, seed=9)
     g = torch.Generator().manual_seed(4)
-    targets = torch.tensor([5, vocab - 1, 130])[:kinds].cuda()[torch.randint(0, kinds, (rows,), generator=g).cuda()]
+    targets = torch.tensor([5, vocab - 1, 130, *range(6, 130), 0, 1, 2, 3, 4])[:kinds].cuda()[torch.randint(0, kinds, (rows,), generator=g).cuda()]
     if rows > 30:
         targets[::7] = -100
     glp = upstream(rows)[0]
