@@ -578,7 +578,7 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
  * targets, outputs and masked or absent targets as there.
  * ssd_head_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
  * dhidden [rows, dim], dweight [vocab, dim] in bf16 (either NULL: not wanted).
- * The logits are formed again; their gradient is rounded to bf16 (2^-9
+ * The logits are formed again; their gradient is rounded to bf16 (2^-8
  * relative, as the operands are), but for the given tokens' elements, which
  * keep fp32 accuracy, and takes 2 rows vocab bytes of the workspace; sums over
  * it are fp32, in a fixed order, and rounded once.

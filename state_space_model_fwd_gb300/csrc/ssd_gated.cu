@@ -31,10 +31,11 @@ template <typename T, bool PAIRS>
 struct Warp {
     Lane<PAIRS> k;
     int tile, row, b, t0;
+    // (A block's rows past the last one count as a tile behind it: no token is there.)
     __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
-        : k((n % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
-        const int rows = a.nblk * a.batch;
-        tile = n / rows, row = n % rows, b = row / a.nblk, t0 = tile * tokens + warp * kTokens<T>;
+        : k(((n * a.per + warp / a.sub) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch, q = n * a.per + warp / a.sub;
+        tile = q / rows, row = q % rows, b = row / a.nblk, t0 = tile * tokens + warp % a.sub * kTokens<T>;
     }
 };
 template <typename T, bool PAIRS>
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     __shared__ float4 runs[2][kWarps][32];
     __shared__ LinkShared sh;
     __shared__ unsigned ticket[2];
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = a.sub * S, L = a.seqs.L;
     const bool linked = a.links.run != nullptr;
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };  // (it starts at -1)
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         }
 
         if (linked) h = pass_links(place, a.links, sh, h, all, w.tile >= kGroup, warp, nw, lane);
-        for (int j = 0; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
+        for (int j = warp - warp % a.sub; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
         if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
             store_state(a.keep + ((int64_t)w.b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
         if (a.y.p) {
@@ -320,12 +321,14 @@ size_t gated_fwd_links(const ssd_gated_shape_t *s) {
 
 template <typename T>
 cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st) {
-    const int64_t per = fwd_tokens(s), ntile = (s->seqlen + per - 1) / per;
+    const int64_t tokens = fwd_tokens(s), ntile = (s->seqlen + tokens - 1) / tokens, rows = gated_blocks(s) * s->batch;
     a.ntile = (int)ntile;
-    a.tiles = (int)(ntile * a.nblk * a.batch);
-    cudaError_t e = prepare(a, links, gated_blocks(s) * s->batch, ntile, st);
+    a.sub = (int)fwd_warps(s);
+    a.per = rows_of_block(rows, ntile, a.sub, kWarps, kSMs * kBlocks);
+    a.tiles = (int)(ntile * ((rows + a.per - 1) / a.per));
+    cudaError_t e = prepare(a, links, rows, ntile, st);
     if (e != cudaSuccess) return e;
-    const unsigned blocks = (unsigned)(a.tiles < kSMs * kBlocks ? a.tiles : kSMs * kBlocks), threads = (unsigned)(fwd_warps(s) * 32);
+    const unsigned blocks = (unsigned)(a.tiles < kSMs * kBlocks ? a.tiles : kSMs * kBlocks), threads = (unsigned)(a.sub * a.per * 32);
     auto go = [&](auto p, auto g, auto c) {
         auto kernel = gated_fwd_kernel<T, decltype(p)::value, decltype(g)::value, decltype(c)::value>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));

@@ -417,11 +417,20 @@ struct GatedArgs {
     float *fin, *keep, *dinit, *ddecay_part;  // keep, kept: [b][ceil(L / 64)][ch] states entering every 64 tokens
     float rate;
     int ch, nblk, batch, ntile, nkeep;
-    int tiles, some_empty;  // tiles in all; whether a sequence has no tokens
+    int sub, per;           // warps of a row's tile; rows of a block (linked rows: 1)
+    int tiles, some_empty;  // tiles in all (of `per` rows each); whether a sequence has no tokens
     int wide;               // every row that is read lies on a 16-byte boundary
     Seqs seqs;
     Links links;
 };
+
+// Rows of one short tile each: as many to a block as leave every place of a block filled (4096 x 16 x 2560 bf16 403 us, one a
+// block 1729; gradient with the states formed again 1237, 3617).
+inline int rows_of_block(int64_t rows, int64_t ntile, int sub, int warps, int places) {
+    if (ntile > 1) return 1;
+    const int64_t most = warps / sub, want = (rows + places - 1) / places;
+    return (int)(want < most ? want : most);
+}
 
 template <typename T, bool PAIRS>
 __device__ __forceinline__ float2 rates_of(const GatedArgs<T> &a, const Lane<PAIRS> &k) {

@@ -39,9 +39,10 @@ struct Warp {
     Lane<PAIRS> k;
     int later, tile, row, b, t0;  // later: tiles behind this one
     __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
-        : k((n % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
-        const int rows = a.nblk * a.batch;
-        later = n / rows, tile = a.ntile - 1 - later, row = n % rows, b = row / a.nblk, t0 = tile * tokens + warp * S;
+        : k(((n * a.per + warp / a.sub) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch, q = n * a.per + warp / a.sub;
+        later = q / rows, tile = max(a.ntile - 1 - later, 0), row = q % rows, b = row / a.nblk, t0 = tile * tokens + warp % a.sub * S;
+        if (later >= a.ntile) t0 = a.seqs.L;  // a block's row past the last one: no token is there
     }
 };
 template <typename T, bool PAIRS>
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
     __shared__ LinkShared sh;
     __shared__ float2 sums[2][kWarps][32];
     __shared__ unsigned ticket[2];
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = nw * S, L = a.seqs.L;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = a.sub * S, L = a.seqs.L;
+    const int own = warp - warp % a.sub;  // the first warp of this one's row
     const bool linked = a.links.run != nullptr;
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
@@ -218,8 +220,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
 
         if (linked)
             c = pass_links(Place(a.links, w.row, w.later, a.ntile, lane), a.links, sh, c, all, w.later >= kGroup, warp, nw, lane);
-        for (int j = nw - 1; j > warp; --j) c = through(run_of(back[p][j][lane]), c);
-        for (int j = 0; j < warp; ++j) h = through(run_of(fore[p][j][lane]), h);
+        for (int j = own + a.sub - 1; j > warp; --j) c = through(run_of(back[p][j][lane]), c);
+        for (int j = own; j < warp; ++j) h = through(run_of(fore[p][j][lane]), h);
 
         f2 cv = both(c), sum;
         if (plain)
@@ -230,9 +232,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
         if (a.ddecay_part) {
             sums[p][warp][lane] = apart(sum);
             __syncthreads();
-            if (warp == 0) {
+            if (warp == own && w.t0 < L) {
                 float2 s = make_float2(0.f, 0.f);
-                for (int j = 0; j < nw; ++j) s.x += sums[p][j][lane].x, s.y += sums[p][j][lane].y;
+                for (int j = own; j < own + a.sub; ++j) s.x += sums[p][j][lane].x, s.y += sums[p][j][lane].y;
                 store_state(a.ddecay_part + ((int64_t)w.tile * a.batch + w.b) * a.ch, k, s);
             }
         }
@@ -328,18 +330,20 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     for (const ssd_rows_t *r : {dy, &out->dx, &out->dr}) pairs = pairs && rows_pairs(*r, sizeof(T), s->batch, s->seqlen);
     if (in->i.data) pairs = pairs && rows_pairs(out->di, sizeof(T), s->batch, s->seqlen);
     if (in->z.data) pairs = pairs && rows_pairs(out->dz, sizeof(T), s->batch, s->seqlen);
-    const int64_t ntile = bwd_tiles(s->seqlen), nw = bwd_warps(s->seqlen);
+    const int64_t ntile = bwd_tiles(s->seqlen), rows = gated_blocks(s) * s->batch;
+    const int most = kSMs * kBlocks;
     a.ntile = (int)ntile;
-    e = prepare(a, ws + p.links, gated_blocks(s) * s->batch, ntile, st);
+    a.sub = (int)bwd_warps(s->seqlen);
+    a.per = rows_of_block(rows, ntile, a.sub, kWarps, most);
+    a.tiles = (int)(ntile * ((rows + a.per - 1) / a.per));
+    e = prepare(a, ws + p.links, rows, ntile, st);
     if (e != cudaSuccess) return status_of(e);
     a.some_empty = cu && a.dinit && any_empty(cu, nseq);
-    a.tiles = (int)(ntile * a.nblk * a.batch);
-    const int most = kSMs * kBlocks;
     const unsigned blocks = (unsigned)(a.tiles < most ? a.tiles : most);
     auto go = [&](auto pr, auto g, auto c) {
         auto kernel = gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
-        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)(nw * 32), sizeof(Stage<T>), st, a.rates != nullptr, a);
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), a.sub * a.per * 32, sizeof(Stage<T>), st, a.rates != nullptr, a);
     };
     auto with_cuts = [&](auto pr, auto g) { cu ? go(pr, g, std::true_type{}) : go(pr, g, std::false_type{}); };
     auto with_gate = [&](auto pr) { a.z.p ? with_cuts(pr, std::true_type{}) : with_cuts(pr, std::false_type{}); };

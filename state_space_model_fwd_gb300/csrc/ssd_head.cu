@@ -52,7 +52,7 @@ constexpr int kNoLead = 0x7F7F7F7F;
 enum Use { kStats, kGrad, kStore };
 constexpr int kGemmThreads = 128 + 32 * kReaders;  // warps: copy, MMA, TMEM, -, the readers
 
-// dz is rounded to bf16 (2^-9 relative, as its products' other operands are), which would show where one element outweighs all
+// dz is rounded to bf16 (2^-8 relative at most, as its products' other operands are), which would show where one element outweighs all
 // others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
 //   dhidden[row] += rest[row] weight[target[row]],   dweight[v] += sum over rows with target v of rest[row] hidden[row],
 // the latter summed by head_fix_kernel and found by way of lead[v], one of those rows.  (4095 x 2560 x 50277: error against 64 bits 1.4 times a

@@ -100,6 +100,30 @@ def test_gradient(case, kept):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,b,L,ch,gate", [
+    ("bf16", 1001, 5, 64, True), ("f32", 1001, 9, 64, False), ("bf16", 500, 17, 100, True), ("f32", 403, 20, 40, True),
+    ("bf16", 2601, 3, 6, False), ("f32", 2601, 1, 5, True), ("bf16", 333, 33, 63, False), ("f32", 333, 26, 64, True),
+])
+def test_many_short_rows(dtype, b, L, ch, gate):
+    """Several rows to a block, some blocks with fewer than others."""
+    t = make(dtype, b, L, ch, gate=gate, seed=6)
+    want, wfin = definition(*[ref.d(t[k]) for k in NAMES])
+    y, fin, states = ssd.ssd_gated_scan_fwd(*args_of(t), return_chunk_states=True)
+    ref.check(y, want, "y", rel=1e-5)  # as in test_forward, of fewer tokens
+    ref.check(fin, wfin, "final_state", rel=1e-5)
+    assert torch.equal(states[:, 0], t["init"])
+    dy = torch.randn(b, L, ch, generator=torch.Generator().manual_seed(12)).to(DT[dtype]).cuda()
+    got = ssd.ssd_gated_scan_bwd(dy, *args_of(t), chunk_states=states)
+    leaves = [ref.d(t[k]) for k in NAMES]
+    for v in leaves:
+        if v is not None:
+            v.requires_grad_(True)
+    want = ref.gradients(definition(*leaves), [ref.d(dy), None], leaves)
+    for name, a, w in zip(("dx", "dr", "ddecay", "di", "dz", "dinit"), got, want):
+        ref.check(a, w, name, rel=1e-4 if name in ("dr", "ddecay") else 2e-5)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_all_decays(dtype):
     """From states that are forgotten at once to ones that are kept for good, gates shut and open."""
