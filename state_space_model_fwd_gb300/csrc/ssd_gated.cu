@@ -32,10 +32,10 @@ struct Warp {
     Lane<PAIRS> k;
     int tile, row, b, t0;
     // (A block's rows past the last one count as a tile behind it: no token is there.)
-    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
-        : k(((n * a.per + warp / a.sub) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
-        const int rows = a.nblk * a.batch, q = n * a.per + warp / a.sub;
-        tile = q / rows, row = q % rows, b = row / a.nblk, t0 = tile * tokens + warp % a.sub * kTokens<T>;
+    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int in_block, int in_row, int lane, int tokens)
+        : k(((n * a.per + in_block) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch, q = n * a.per + in_block;
+        tile = q / rows, row = q % rows, b = row / a.nblk, t0 = tile * tokens + in_row * kTokens<T>;
     }
 };
 template <typename T, bool PAIRS>
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     __shared__ LinkShared sh;
     __shared__ unsigned ticket[2];
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = a.sub * S, L = a.seqs.L;
+    const int in_block = uniform(warp / a.sub), in_row = warp - in_block * a.sub;  // this warp's row of the block's, its place in it
     const bool linked = a.links.run != nullptr;
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };  // (it starts at -1)
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
     __syncthreads();
     int n = uniform((int)ticket[1]);
-    Warp<T, PAIRS> w(a, n, warp, lane, tokens);
+    Warp<T, PAIRS> w(a, n, in_block, in_row, lane, tokens);
     float2 rate = make_float2(0.f, 0.f);
     Cuts cut{};
     auto cuts = [&](const Warp<T, PAIRS> &w) {
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
             place.publish(all);
         }
         n = uniform((int)ticket[p]);
-        const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        const Warp<T, PAIRS> after(a, n, in_block, in_row, lane, tokens);
         Cuts next_cut{};
         if (n < a.tiles) {
             rate = rates_of(a, after.k);
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         }
 
         if (linked) h = pass_links(place, a.links, sh, h, all, w.tile >= kGroup, warp, nw, lane);
-        for (int j = warp - warp % a.sub; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
+        for (int j = warp - in_row; j < warp; ++j) h = through(run_of(runs[p][j][lane]), h);
         if (a.keep && w.t0 % kStateEvery == 0 && w.t0 < L)
             store_state(a.keep + ((int64_t)w.b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
         if (a.y.p) {

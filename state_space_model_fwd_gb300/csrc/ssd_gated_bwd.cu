@@ -38,10 +38,10 @@ template <typename T, bool PAIRS>
 struct Warp {
     Lane<PAIRS> k;
     int later, tile, row, b, t0;  // later: tiles behind this one
-    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int warp, int lane, int tokens)
-        : k(((n * a.per + warp / a.sub) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
-        const int rows = a.nblk * a.batch, q = n * a.per + warp / a.sub;
-        later = q / rows, tile = max(a.ntile - 1 - later, 0), row = q % rows, b = row / a.nblk, t0 = tile * tokens + warp % a.sub * S;
+    __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int in_block, int in_row, int lane, int tokens)
+        : k(((n * a.per + in_block) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
+        const int rows = a.nblk * a.batch, q = n * a.per + in_block;
+        later = q / rows, tile = max(a.ntile - 1 - later, 0), row = q % rows, b = row / a.nblk, t0 = tile * tokens + in_row * S;
         if (later >= a.ntile) t0 = a.seqs.L;  // a block's row past the last one: no token is there
     }
 };
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
     __shared__ float2 sums[2][kWarps][32];
     __shared__ unsigned ticket[2];
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = a.sub * S, L = a.seqs.L;
-    const int own = warp - warp % a.sub;  // the first warp of this one's row
+    const int in_block = uniform(warp / a.sub), in_row = warp - in_block * a.sub, own = warp - in_row;  // (own: the row's first)
     const bool linked = a.links.run != nullptr;
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
     if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
     __syncthreads();
     int n = uniform((int)ticket[1]);
-    Warp<T, PAIRS> w(a, n, warp, lane, tokens);
+    Warp<T, PAIRS> w(a, n, in_block, in_row, lane, tokens);
     auto entering = [&](const Warp<T, PAIRS> &w) {
         return load_state(a.kept + ((int64_t)w.b * a.nkeep + w.tile * (kTile / kStateEvery)) * a.ch, w.k);
     };
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
             Place(a.links, w.row, w.later, a.ntile, lane).publish(all);
         }
         n = uniform((int)ticket[p]);
-        const Warp<T, PAIRS> after(a, n, warp, lane, tokens);
+        const Warp<T, PAIRS> after(a, n, in_block, in_row, lane, tokens);
         Cuts next_cut{0, 0, after.b};
         if (n < a.tiles) {
             rate = rates_of(a, after.k), kept = entering(after);

@@ -52,11 +52,11 @@ constexpr int kNoLead = 0x7F7F7F7F;
 enum Use { kStats, kGrad, kStore };
 constexpr int kGemmThreads = 128 + 32 * kReaders;  // warps: copy, MMA, TMEM, -, the readers
 
-// dz is rounded to bf16 (2^-8 relative at most, as its products' other operands are), which would show where one element outweighs all
-// others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
+// dz is rounded to bf16 (2^-8 relative at most, as its products' other operands are), which would show where one element
+// outweighs all others: the given token's.  What its rounding left, `rest`, is kept in fp32 and added to the products:
 //   dhidden[row] += rest[row] weight[target[row]],   dweight[v] += sum over rows with target v of rest[row] hidden[row],
-// the latter summed by head_fix_kernel and found by way of lead[v], one of those rows.  (4095 x 2560 x 50277: error against 64 bits 1.4 times a
-// bf16 rounding without it, 1.0 with it, for 1% of the time; with few rows up to 1.8 times.)
+// the latter summed by head_fix_kernel and found by way of lead[v], one of those rows.  (4095 x 2560 x 50277: error against
+// 64 bits 1.4 times a bf16 rounding without it, 1.0 with it, for 1% of the time; with few rows up to 1.8 times.)
 struct Fix {
     const int64_t *targets;  // dhidden
     const float *rest;
