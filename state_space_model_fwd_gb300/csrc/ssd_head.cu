@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
                 const Stat st = stat_of(z);
-                if (live && first < a.bn) a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
+                if (live && first < a.bn)
+                    a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
             } else {
                 const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
                 const int row0 = row - lane, limit = min(min(a.N - c0, a.bn) - first, kBN / 2);  // of this warp's columns
@@ -835,7 +836,8 @@ ssd_status_t check_head(const ssd_head_shape_t *s) {
         return SSD_ERR_UNSUPPORTED;
     // tiles and their parts are counted in 31 bits
     const int64_t most = 1 << 28;
-    if ((s->rows / kBM + 1) * (s->vocab / 64 + 1) > most || (s->vocab / kBM + 1) * (s->dim / 64 + 1) * (s->rows / (kLongest * kBK) + 1) > most / 64 ||
+    if ((s->rows / kBM + 1) * (s->vocab / 64 + 1) > most ||
+        (s->vocab / kBM + 1) * (s->dim / 64 + 1) * (s->rows / (kLongest * kBK) + 1) > most / 64 ||
         (s->rows / kBM + 1) * (s->dim / 64 + 1) * (s->vocab / (kLongest * kBK) + 1) > most / 64)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
