@@ -27,7 +27,7 @@
 // or so the readers bound it: 8192 x 128 x 32000 in 94 us, 4.5 instructions and
 // one exponential a logit with two warps a scheduler (storing by thread and
 // taking the maximum anew every 16 columns: 243).  With few rows the weights'
-// one pass does: 16 x 2560 x 50280 in 54 us, 38 at the copy rate.
+// one pass does: 16 x 2560 x 50280 in 51 us, 38 at the copy rate.
 #include <cudaTypedefs.h>
 
 #include "ssd_logprob.cuh"
@@ -764,6 +764,14 @@ size_t parts_bytes(const GemmArgs &a) { return align256(sizeof(float) * (size_t)
 
 int fit_columns(int64_t n) { return n >= 256 ? 256 : (int)((n + 63) / 64 * 64); }
 
+// Up to 128 rows the weights' one pass is what takes time: tiles of the statistics as wide as gives every SM the same number
+// (in a graph, 16 x 2560 x 50280 48.2 us, tiles of 256 52.1; of 131072 106.6, 109.0; 128 x 2560 x 20000 26.5, 28.2), unless
+// they were narrow (16 x 2560 x 5000 22.1, 21.1).
+int forward_columns(int64_t rows, int64_t vocab) {
+    const int64_t rounds = (vocab + kBN * kSMs - 1) / (kBN * kSMs), n = (vocab + rounds * kSMs - 1) / (rounds * kSMs);
+    return rows > kBM || n < 64 ? fit_columns(vocab) : (int)(n + 15) / 16 * 16;
+}
+
 int halves(const GemmArgs &a) { return a.bn > kBN / 2 ? 2 : 1; }
 
 struct HeadPlan {
@@ -773,7 +781,7 @@ struct HeadPlan {
 };
 HeadPlan plan_fwd(const ssd_head_shape_t *s) {
     HeadPlan p{};
-    p.z = plan_gemm(s->rows, s->vocab, s->dim, fit_columns(s->vocab), false);
+    p.z = plan_gemm(s->rows, s->vocab, s->dim, forward_columns(s->rows, s->vocab), false);
     p.stats = 0;
     p.given = align256(sizeof(float4) * p.z.nt * halves(p.z) * s->rows);
     p.bytes = p.given + align256(sizeof(float) * s->rows);
