@@ -20,16 +20,16 @@ template <typename T>
 constexpr int kTokens = 32 / sizeof(T);  // a warp: fp32 takes twice the shared memory
 
 // The next tile's x, r and i, and two tiles' z: each lane's own.
-template <typename T>
+template <typename T, int ALIGN>
 struct Stage {
     static constexpr int S = kTokens<T>;
-    Two<T> in[3][S][kWarps][32], z[2][S][kWarps][32];
+    Slot<T, ALIGN> in[3][S][kWarps], z[2][S][kWarps];
 };
 
 // What a warp knows of its tokens.
-template <typename T, bool PAIRS>
+template <typename T, int ALIGN>
 struct Warp {
-    Lane<PAIRS> k;
+    Lane<ALIGN> k;
     int tile, row, b, t0;
     // (A block's rows past the last one count as a tile behind it: no token is there.)
     __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int in_block, int in_row, int lane, int tokens)
@@ -38,38 +38,40 @@ struct Warp {
         tile = q / rows, row = q % rows, b = row / a.nblk, t0 = tile * tokens + in_row * kTokens<T>;
     }
 };
-template <typename T, bool PAIRS>
-__device__ __forceinline__ float2 init_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, int s) {
+template <typename T, int ALIGN>
+__device__ __forceinline__ float2 init_of(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, int s) {
     return load_state(a.init ? a.init + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch : nullptr, w.k);
 }
 
 // Starts the copies of a tile's inputs.
-template <typename T, bool PAIRS, bool GATE>
-__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Stage<T> &st, int warp, int lane, int zbuf) {
+template <typename T, int ALIGN, bool GATE>
+__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, Stage<T, ALIGN> &st, int warp, int lane, int zbuf) {
     // past the end, and in channels that are none: a = 1 and nothing enters
-    const int left = a.seqs.L - w.t0, stride = kWarps * 32;
-    auto rows = [&](Two<T> *dst, const Rows<const T> &r, float fill) {
-        fetch_rows<T, PAIRS, kTokens<T>>(dst, stride, r.at(w.b, w.t0), r.rs, w.k, lane, left, a.wide, a.ch, fill);
+    const int left = a.seqs.L - w.t0;
+    auto rows = [&](Slot<T, ALIGN> *dst, const Rows<const T> &r, float fill) {
+        fetch_rows<T, ALIGN, kTokens<T>, kWarps>(dst, r, w.b, w.t0, w.k, lane, left, a.ch, fill);
     };
-    rows(&st.in[1][0][warp][0], a.r, -30000.f);
-    rows(&st.in[0][0][warp][0], a.x, 0.f);
-    if (a.i.p) rows(&st.in[2][0][warp][0], a.i, 128.f);
-    if (GATE) rows(&st.z[zbuf][0][warp][0], a.z, 0.f);
+    rows(&st.in[1][0][warp], a.r, -30000.f);
+    rows(&st.in[0][0][warp], a.x, 0.f);
+    if (a.i.p) rows(&st.in[2][0][warp], a.i, 128.f);
+    if (GATE) rows(&st.z[zbuf][0][warp], a.z, 0.f);
 }
 
 // The tokens' decays and inputs, and the run they make.  PLAIN: S tokens of one sequence that neither begins nor ends among
 // them, decays with m <= 1.
-template <typename T, bool PAIRS, bool PACKED, bool PLAIN, int S>
-__device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, const Stage<T> &st,
+template <typename T, int ALIGN, bool PACKED, bool PLAIN, int S>
+__device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, f2 rate, const Stage<T, ALIGN> &st,
                                            int warp, int lane, f2 (&av)[S], f2 (&uv)[S], f2 &A, f2 &H) {
     A = splat(1.f), H = splat(0.f);
+    const Skew<T, ALIGN> sx(a.x, w.b, w.t0), sr(a.r, w.b, w.t0), si(a.i, w.b, w.t0);
+    auto in = [&](int which, int s, const Skew<T, ALIGN> &skew) { return widen(two_in(st.in[which][s][warp], lane, skew(s))); };
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         f2 v;
-        decay2<PLAIN>(mul2(rate, both(sigmoid2(widen(st.in[1][s][warp][lane])))), v, av[s]);
+        decay2<PLAIN>(mul2(rate, both(sigmoid2(in(1, s, sr)))), v, av[s]);
         const float2 b2 = apart(fma2(v, av[s], v));
-        uv[s] = mul2(mul2(pack2(sqrt_approx(b2.x), sqrt_approx(b2.y)), both(sigmoid2(widen(st.in[2][s][warp][lane])))),
-                     both(widen(st.in[0][s][warp][lane])));
+        uv[s] = mul2(mul2(pack2(sqrt_approx(b2.x), sqrt_approx(b2.y)), both(sigmoid2(in(2, s, si)))),
+                     both(in(0, s, sx)));
         if (PACKED && !PLAIN && (cut.first >> s & 1)) H = both(init_of(a, w, cut, s));
         A = mul2(A, av[s]);
         H = fma2(av[s], H, uv[s]);
@@ -78,11 +80,12 @@ __device__ __forceinline__ void run_tokens(const GatedArgs<T> &a, const Warp<T, 
 }
 
 // The outputs, from the state that enters.
-template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN, int S>
-__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, const Stage<T> &st, int warp,
+template <typename T, int ALIGN, bool GATE, bool PACKED, bool PLAIN, int S>
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, const Stage<T, ALIGN> &st, int warp,
                                              int lane, int zbuf, const f2 (&av)[S], const f2 (&uv)[S], f2 hv) {
     T *py = a.y.at(w.b, w.t0);
     const int L = a.seqs.L;
+    const Skew<T, ALIGN> sz(a.z, w.b, w.t0);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (!PLAIN && w.t0 + s >= L) break;
@@ -90,10 +93,10 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
         hv = fma2(av[s], hv, uv[s]);
         f2 o = hv;
         if constexpr (GATE) {
-            const float2 zf = widen(st.z[zbuf][s][warp][lane]);
+            const float2 zf = widen(two_in(st.z[zbuf][s][warp], lane, sz(s)));
             o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
         }
-        store_two<T, PAIRS>(py + a.y.step(s), w.k, apart(o));
+        store_two<T, ALIGN>(py + a.y.step(s), w.k, apart(o));
         if (!PLAIN && (cut.last >> s & 1) && a.fin) {
             const int q = PACKED ? seq_from(a.seqs, cut.seq, w.t0 + s) : w.b;
             store_state(a.fin + (int64_t)q * a.ch, w.k, apart(hv));
@@ -101,11 +104,11 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
     }
 }
 
-template <typename T, bool PAIRS, bool GATE, bool PACKED>
+template <typename T, int ALIGN, bool GATE, bool PACKED>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const __grid_constant__ GatedArgs<T> a) {
     constexpr int S = kTokens<T>;
     extern __shared__ __align__(16) uint8_t dynamic[];
-    Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
+    Stage<T, ALIGN> &st = *reinterpret_cast<Stage<T, ALIGN> *>(dynamic);
     __shared__ float4 runs[2][kWarps][32];
     __shared__ LinkShared sh;
     __shared__ unsigned ticket[2];
@@ -116,16 +119,16 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     auto next = [&](unsigned n) { return linked ? atomicAdd(a.links.ticket, 1u) + 1u : n + gridDim.x; };  // (it starts at -1)
     if (!a.i.p) {  // no input gate: s(128) = 1
 #pragma unroll
-        for (int s = 0; s < S; ++s) st.in[2][s][warp][lane] = two_of(T(), 128.f);
+        for (int s = 0; s < S; ++s) fill_slot(st.in[2][s][warp], lane, 128.f);
     }
     wait_previous();
     if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
     __syncthreads();
     int n = uniform((int)ticket[1]);
-    Warp<T, PAIRS> w(a, n, in_block, in_row, lane, tokens);
+    Warp<T, ALIGN> w(a, n, in_block, in_row, lane, tokens);
     float2 rate = make_float2(0.f, 0.f);
     Cuts cut{};
-    auto cuts = [&](const Warp<T, PAIRS> &w) {
+    auto cuts = [&](const Warp<T, ALIGN> &w) {
         Cuts c{0, 0, w.b};
         if (w.t0 < L) {
             if constexpr (PACKED)
@@ -137,11 +140,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
     };
     if (n < a.tiles) {
         rate = rates_of(a, w.k);
-        fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane, 0);
+        fetch_tile<T, ALIGN, GATE>(a, w, st, warp, lane, 0);
         cut = cuts(w);
     }
     for (int p = 0; n < a.tiles; p ^= 1) {
-        const Lane<PAIRS> &k = w.k;
+        const Lane<ALIGN> &k = w.k;
         if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
         const bool plain = w.t0 + S <= L && !(cut.first | cut.last) && __all_sync(0xffffffffu, rate.x <= 1.f && rate.y <= 1.f);
         // The state that enters the row, or the group of tiles.
@@ -152,9 +155,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
         __syncwarp();
         f2 av[S], uv[S], A, H;
         if (plain)
-            run_tokens<T, PAIRS, PACKED, true>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
+            run_tokens<T, ALIGN, PACKED, true>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
         else
-            run_tokens<T, PAIRS, PACKED, false>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
+            run_tokens<T, ALIGN, PACKED, false>(a, w, cut, both(rate), st, warp, lane, av, uv, A, H);
         const float2 fa = apart(A), fh = apart(H);
         runs[p][warp][lane] = make_float4(fa.x, fa.y, fh.x, fh.y);
         __syncthreads();
@@ -165,11 +168,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
             place.publish(all);
         }
         n = uniform((int)ticket[p]);
-        const Warp<T, PAIRS> after(a, n, in_block, in_row, lane, tokens);
+        const Warp<T, ALIGN> after(a, n, in_block, in_row, lane, tokens);
         Cuts next_cut{};
         if (n < a.tiles) {
             rate = rates_of(a, after.k);
-            fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane, p ^ 1);
+            fetch_tile<T, ALIGN, GATE>(a, after, st, warp, lane, p ^ 1);
             next_cut = cuts(after);  // (while others' runs are on their way)
         }
 
@@ -179,24 +182,24 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_fwd_kernel(const _
             store_state(a.keep + ((int64_t)w.b * a.nkeep + w.t0 / kStateEvery) * a.ch, k, h);
         if (a.y.p) {
             if (plain)
-                write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, st, warp, lane, p, av, uv, both(h));
+                write_tokens<T, ALIGN, GATE, PACKED, true>(a, w, cut, st, warp, lane, p, av, uv, both(h));
             else
-                write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, st, warp, lane, p, av, uv, both(h));
+                write_tokens<T, ALIGN, GATE, PACKED, false>(a, w, cut, st, warp, lane, p, av, uv, both(h));
         }
         w = after, cut = next_cut;
     }
     if (PACKED && a.some_empty) pass_empty(a.seqs, a.ch, a.init, a.fin);
 }
 
-template <typename T, bool PAIRS>
+template <typename T, int ALIGN>
 __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__ GatedArgs<T> a, float *state) {
     const int n = blockIdx.x * 4 + threadIdx.x / 32;
-    const Lane<PAIRS> k(n % a.nblk, threadIdx.x % 32, a.ch);
+    const Lane<ALIGN> k(n % a.nblk, threadIdx.x % 32, a.ch);
     const int b = n / a.nblk;
     if (b >= a.batch) return;
-    const Two<T> x = load_two<T, PAIRS>(a.x.at(b, 0), k, 0.f), r = load_two<T, PAIRS>(a.r.at(b, 0), k, 0.f);
-    const Two<T> g = a.i.p ? load_two<T, PAIRS>(a.i.at(b, 0), k, 0.f) : two_of(T(), 128.f);
-    const Two<T> z = a.z.p ? load_two<T, PAIRS>(a.z.at(b, 0), k, 0.f) : two_of(T(), 0.f);
+    const Two<T> x = load_two<T, ALIGN>(a.x.at(b, 0), k, 0.f), r = load_two<T, ALIGN>(a.r.at(b, 0), k, 0.f);
+    const Two<T> g = a.i.p ? load_two<T, ALIGN>(a.i.at(b, 0), k, 0.f) : two_of(T(), 128.f);
+    const Two<T> z = a.z.p ? load_two<T, ALIGN>(a.z.at(b, 0), k, 0.f) : two_of(T(), 0.f);
     float *h = state + (int64_t)b * a.ch;
     const f2 old = both(load_state(h, k));
     const float2 dec = load_state(a.decay, k);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
         const float2 zf = widen(z);
         o = mul2(o, mul2(both(zf), both(sigmoid2(zf))));
     }
-    store_two<T, PAIRS>(a.y.at(b, 0), k, apart(o));
+    store_two<T, ALIGN>(a.y.at(b, 0), k, apart(o));
 }
 
 int64_t fwd_warps(const ssd_gated_shape_t *s) {
@@ -245,20 +248,12 @@ bool gated_inputs_ok(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, b
 bool rows_pairs(const ssd_rows_t &r, size_t esize, int64_t b, int64_t L) {
     return aligned(r.data, 2 * esize) && (b <= 1 || r.batch_stride % 2 == 0) && (L <= 1 || r.row_stride % 2 == 0);
 }
-bool gated_pairs(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
+Align gated_align(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
     const size_t es = dtype_size(s->dtype);
-    if (s->channels % 2) return false;
+    bool pairs = s->channels % 2 == 0, sixteen = s->channels * es % 16 == 0;
     for (const ssd_rows_t *r : {&in->x, &in->r, &in->i, &in->z})
-        if (r->data && !rows_pairs(*r, es, s->batch, s->seqlen)) return false;
-    return true;
-}
-
-bool gated_wide(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
-    const size_t es = dtype_size(s->dtype);
-    if (s->channels * es % 16) return false;
-    for (const ssd_rows_t *r : {&in->x, &in->r, &in->i, &in->z})
-        if (r->data && !rows_vec(*r, es, s->batch, s->seqlen)) return false;
-    return true;
+        if (r->data) pairs = pairs && rows_pairs(*r, es, s->batch, s->seqlen), sixteen = sixteen && rows_vec(*r, es, s->batch, s->seqlen);
+    return sixteen ? kSixteen : pairs ? kPairs : kElements;
 }
 
 template <typename T>
@@ -268,7 +263,6 @@ GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in
     a.decay = in->decay, a.init = in->init_state, a.rate = s->rate;
     a.ch = (int)s->channels, a.nblk = (int)gated_blocks(s), a.batch = (int)s->batch, a.nkeep = (int)gated_kept(s);
     a.seqs.n = (int)nseq, a.seqs.L = (int)s->seqlen;
-    a.wide = gated_wide(s, in);
     return a;
 }
 template GatedArgs<float> gated_args<float>(const ssd_gated_shape_t *, const ssd_gated_inputs_t *, int64_t);
@@ -321,7 +315,7 @@ size_t gated_fwd_links(const ssd_gated_shape_t *s) {
 }
 
 template <typename T>
-cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st) {
+cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, Align align, bool packed, char *links, cudaStream_t st) {
     const int64_t tokens = fwd_tokens(s), ntile = (s->seqlen + tokens - 1) / tokens, rows = gated_blocks(s) * s->batch;
     a.ntile = (int)ntile;
     a.sub = (int)fwd_warps(s);
@@ -331,18 +325,19 @@ cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool p
     if (e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)(a.tiles < kSMs * kBlocks ? a.tiles : kSMs * kBlocks), threads = (unsigned)(a.sub * a.per * 32);
     auto go = [&](auto p, auto g, auto c) {
+        constexpr int kStage = (int)sizeof(Stage<T, decltype(p)::value>);
         auto kernel = gated_fwd_kernel<T, decltype(p)::value, decltype(g)::value, decltype(c)::value>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
-        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)threads, sizeof(Stage<T>), st, a.rates != nullptr, a);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStage);
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), (int)threads, kStage, st, a.rates != nullptr, a);
     };
     auto with_cuts = [&](auto p, auto g) { packed ? go(p, g, std::true_type{}) : go(p, g, std::false_type{}); };
     auto with_gate = [&](auto p) { a.z.p && a.y.p ? with_cuts(p, std::true_type{}) : with_cuts(p, std::false_type{}); };
-    pairs ? with_gate(std::true_type{}) : with_gate(std::false_type{});
+    by_align(align, with_gate);
     timing_mark(st, a.y.p ? "gated_scan" : "gated_states");
     return e;
 }
-template cudaError_t launch_gated_fwd<float>(GatedArgs<float> &, const ssd_gated_shape_t *, bool, bool, char *, cudaStream_t);
-template cudaError_t launch_gated_fwd<bf16>(GatedArgs<bf16> &, const ssd_gated_shape_t *, bool, bool, char *, cudaStream_t);
+template cudaError_t launch_gated_fwd<float>(GatedArgs<float> &, const ssd_gated_shape_t *, Align, bool, char *, cudaStream_t);
+template cudaError_t launch_gated_fwd<bf16>(GatedArgs<bf16> &, const ssd_gated_shape_t *, Align, bool, char *, cudaStream_t);
 
 namespace {
 
@@ -363,7 +358,8 @@ ssd_status_t fwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
         if (e != cudaSuccess) return status_of(e);
         ws += offsets_bytes(cu, nseq);
     }
-    return status_of(launch_gated_fwd(a, s, gated_pairs(s, in) && rows_pairs(*y, sizeof(T), s->batch, s->seqlen), cu != nullptr, ws, st));
+    const Align align = rows_pairs(*y, sizeof(T), s->batch, s->seqlen) ? gated_align(s, in) : kElements;
+    return status_of(launch_gated_fwd(a, s, align, cu != nullptr, ws, st));
 }
 
 template <typename T>
@@ -372,10 +368,10 @@ ssd_status_t step_typed(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in
     a.y = rows_of<T>(*y);
     timing_begin(st);
     const unsigned blocks = (unsigned)(((int64_t)a.nblk * a.batch + 3) / 4);
-    if (gated_pairs(s, in) && rows_pairs(*y, sizeof(T), s->batch, 1))
-        gated_step_kernel<T, true><<<blocks, 128, 0, st>>>(a, state);
+    if (gated_align(s, in) != kElements && rows_pairs(*y, sizeof(T), s->batch, 1))
+        gated_step_kernel<T, kPairs><<<blocks, 128, 0, st>>>(a, state);
     else
-        gated_step_kernel<T, false><<<blocks, 128, 0, st>>>(a, state);
+        gated_step_kernel<T, kElements><<<blocks, 128, 0, st>>>(a, state);
     timing_mark(st, "gated_step");
     return status_of(cudaGetLastError());
 }

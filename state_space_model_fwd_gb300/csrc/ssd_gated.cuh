@@ -51,34 +51,36 @@ __device__ __forceinline__ float2 widen(const Two<bf16> &v) {
 }
 __device__ __forceinline__ float2 widen(const Two<float> &v) { return v.w; }
 
+// How rows lie: anywhere, their pairs of channels on their own size's boundary,
+// or each on a 16-byte boundary.
+enum Align { kElements, kPairs, kSixteen };
 // A lane's channels: c0 and c1 of the block's 64.  Rows whose pairs lie on
 // their own size's boundary are read in pairs, two neighbours a lane; others
-// one element at a time, 32 neighbours a warp (65537 x 2560 packed bf16, rows
-// of 2560: 449 us; of 2562, pairs without 16-byte copies: 529; of 2561: 1174).
-template <bool PAIRS>
+// one element at a time, 32 neighbours a warp.
+template <int ALIGN>
 struct Lane {
     int c0;
     int step;       // from c0 to the second channel
     bool in0, in1;  // which exist
     __device__ __forceinline__ Lane(int blk, int lane, int ch) {
-        c0 = blk * kCols + (PAIRS ? 2 * lane : lane);
-        step = PAIRS ? 1 : 32;
+        c0 = blk * kCols + (ALIGN ? 2 * lane : lane);
+        step = ALIGN ? 1 : 32;
         in0 = c0 < ch, in1 = c0 + step < ch;
     }
 };
 
 // The lane's place in a row.  Rows are the same in all lanes and lanes keep one 32-bit offset: an access needs no
 // arithmetic of its own.
-template <typename P, bool PAIRS>
-__device__ __forceinline__ P *place(P *row, const Lane<PAIRS> &k) {
+template <typename P, int ALIGN>
+__device__ __forceinline__ P *place(P *row, const Lane<ALIGN> &k) {
     using B = std::conditional_t<std::is_const_v<P>, const char, char>;
     return reinterpret_cast<P *>(reinterpret_cast<B *>(row) + (size_t)((unsigned)k.c0 * (unsigned)sizeof(P)));
 }
-template <typename T, bool PAIRS>
-__device__ __forceinline__ Two<T> load_two(const T *row, const Lane<PAIRS> &k, float fill) {
+template <typename T, int ALIGN>
+__device__ __forceinline__ Two<T> load_two(const T *row, const Lane<ALIGN> &k, float fill) {
     const T *p = place(row, k);
     Two<T> v = two_of(T(), fill);
-    if constexpr (PAIRS) {
+    if constexpr (ALIGN) {
         if (k.in0) v.w = *reinterpret_cast<const decltype(v.w) *>(p);
     } else if constexpr (sizeof(T) == 2) {
         uint32_t lo = v.w & 0xFFFFu, hi = v.w >> 16;
@@ -91,93 +93,88 @@ __device__ __forceinline__ Two<T> load_two(const T *row, const Lane<PAIRS> &k, f
     }
     return v;
 }
-// The same into shared memory, where the lane itself reads it later: an asynchronous copy, of rows whose elements or pairs lie
-// on four-byte boundaries.  `there`: the token exists.
-template <typename T, bool PAIRS>
-constexpr bool kAsync = PAIRS || sizeof(T) == 4;
-constexpr int kAtOnce = 8;
-__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
-    if (bytes == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+// A warp's 64 channels of one token in shared memory.  Rows on 16-byte boundaries lie as the lanes read them; others as they
+// lie in memory from the boundary before them on, so that they are copied 16 bytes at a time all the same.  (What is read
+// before a row is not used.  It is in the row's allocation, which begins on such a boundary; nothing is read behind a row.)
+template <typename T, int ALIGN>
+struct alignas(16) Slot {
+    char b[kCols * sizeof(T) + (ALIGN == kSixteen ? 0 : 16)];
+};
+// Where a row lies in its slot, token by token.
+template <typename T, int ALIGN>
+struct Skew {
+    unsigned first = 0, step = 0;
+    __device__ __forceinline__ Skew(const Rows<const T> &r, int b, int t0) {
+        if constexpr (ALIGN != kSixteen) first = (unsigned)reinterpret_cast<uintptr_t>(r.at(b, t0)), step = (unsigned)r.rs * (unsigned)sizeof(T);
+    }
+    __device__ __forceinline__ unsigned operator()(int s) const { return ALIGN == kSixteen ? 0 : (first + s * step) & 15; }
+};
+template <typename T, int ALIGN>
+__device__ __forceinline__ Two<T> two_in(const Slot<T, ALIGN> &slot, int lane, unsigned skew) {
+    if constexpr (ALIGN != kElements) {
+        return reinterpret_cast<const Two<T> *>(slot.b + skew)[lane];
+    } else if constexpr (sizeof(T) == 2) {
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(slot.b + skew) + lane;
+        return {(uint32_t)p[0] | (uint32_t)p[32] << 16};
+    } else {
+        const float *p = reinterpret_cast<const float *>(slot.b + skew) + lane;
+        return {make_float2(p[0], p[32])};
+    }
+}
+template <typename T, int ALIGN>
+__device__ __forceinline__ void fill_slot(Slot<T, ALIGN> &slot, int lane, float v) {
+    const Two<T> f = two_of(T(), v);
+    for (int i = lane; i < (int)(sizeof(slot) / sizeof(f)); i += 32) reinterpret_cast<Two<T> *>(slot.b)[i] = f;
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-template <typename T, bool PAIRS>
-__device__ __forceinline__ void fetch_two(Two<T> *dst, const T *row, const Lane<PAIRS> &k, bool there, float fill) {
-    const T *p = place(row, k);
-    if constexpr (PAIRS) {
-        if (there && k.in0)
-            copy_async(dst, p, 2 * sizeof(T));
-        else
-            *dst = two_of(T(), fill);
-    } else {
-        float *d = reinterpret_cast<float *>(dst);
-        if (there && k.in0)
-            copy_async(d, p, 4);
-        else
-            d[0] = fill;
-        if (there && k.in1)
-            copy_async(d + 1, p + 32, 4);
-        else
-            d[1] = fill;
-    }
-}
-// The copies of a warp's S tokens from one array, each lane's pair to dst[s * stride + lane].  Where rows lie on 16-byte
-// boundaries (`wide`) a lane copies 16 bytes of one of the rows that an instruction spans, for others to read: a quarter
-// (fp32: half) of the instructions.
-template <typename T, bool PAIRS, int S>
-__device__ __forceinline__ void fetch_rows(Two<T> *dst, int stride, const T *row, int64_t step, const Lane<PAIRS> &k, int lane, int left,
-                                           bool wide, int ch, float fill) {
-    if (PAIRS && wide) {
-        constexpr int CHUNKS = kCols * sizeof(T) / 16, ROWS = 32 / CHUNKS, EACH = 16 / sizeof(T);
-        const int at = lane % CHUNKS, c = k.c0 - 2 * lane + at * EACH, first = lane / CHUNKS;
-        const char *src = reinterpret_cast<const char *>(row + c) + (int64_t)first * step * (int)sizeof(T);
-        char *d = reinterpret_cast<char *>(dst + first * stride) + at * 16;
-        const Two<T> f = two_of(T(), fill);
+// Asynchronous copies of a warp's S tokens of one array from token t0 on, `left` of which exist, to every STRIDE-th slot
+// (others: `fill`).  A lane copies 16 bytes of one of the rows that an instruction spans, for others to read.  65537 x 2560
+// packed bf16, rows of 2560: 452 us; of 2562 515 (copied by the lanes that read them, four bytes each: 527); of 2561 528
+// (through registers: 1092).
+template <typename T, int ALIGN, int S, int STRIDE>
+__device__ __forceinline__ void fetch_rows(Slot<T, ALIGN> *dst, const Rows<const T> &r, int b, int t0, const Lane<ALIGN> &k, int lane,
+                                           int left, int ch, float fill) {
+    constexpr int CHUNKS = kCols * sizeof(T) / 16, ROWS = 32 / CHUNKS, EACH = 16 / sizeof(T);
+    const int64_t step = (int64_t)r.rs * (int)sizeof(T);
+    const int first = lane / CHUNKS, q = lane % CHUNKS, c0 = k.c0 - (ALIGN ? 2 : 1) * lane;
+    const Two<T> f = two_of(T(), fill);
+    auto fill16 = [&](char *d) {
+#pragma unroll
+        for (int i = 0; i < EACH / 2; ++i) reinterpret_cast<Two<T> *>(d)[i] = f;
+    };
+    if constexpr (ALIGN == kSixteen) {
+        const int c = c0 + q * EACH;
+        const char *src = reinterpret_cast<const char *>(r.at(b, t0) + c) + first * step;
+        char *d = dst[first * STRIDE].b + q * 16;
 #pragma unroll
         for (int s = 0; s < S; s += ROWS) {
-            if (s + first < left && c < ch) {
+            if (s + first < left && c < ch)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(d)), "l"(src) : "memory");
-            } else {
-                Two<T> *e = reinterpret_cast<Two<T> *>(d);
-#pragma unroll
-                for (int i = 0; i < EACH / 2; ++i) e[i] = f;
-            }
-            src += step * (ROWS * (int)sizeof(T)), d += ROWS * stride * sizeof(Two<T>);
+            else
+                fill16(d);
+            src += step * ROWS, d += ROWS * STRIDE * sizeof(*dst);
         }
-    } else if constexpr (kAsync<T, PAIRS>) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) fetch_two<T, PAIRS>(dst + s * stride + lane, row + step * s, k, s < left, fill);
     } else {
-        // bf16 off its four-byte boundaries goes through registers: loads without conditions, so that kAtOnce tokens' are in
-        // flight (what is not there reads the last that is; with a condition each 2280 us)
-        const int last = max(min(S, left) - 1, 0), o0 = min(k.c0, ch - 1), o1 = min(k.c0 + 32, ch - 1);
-#pragma unroll
-        for (int s0 = 0; s0 < S; s0 += kAtOnce) {
-            T lo[kAtOnce], hi[kAtOnce];
-            if (left > 0) {
-#pragma unroll
-                for (int s = 0; s < kAtOnce; ++s) {
-                    const T *p = row + step * min(s0 + s, last);
-                    lo[s] = p[o0], hi[s] = p[o1];
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < kAtOnce; ++s) {
-                const bool there = s0 + s < left;
-                T v[2] = {there && k.in0 ? lo[s] : from_f32<T>(fill), there && k.in1 ? hi[s] : from_f32<T>(fill)};
-                Two<T> w;
-                memcpy(&w, v, sizeof(w));
-                dst[(s0 + s) * stride + lane] = w;
-            }
-        }
+        const int before = c0 * (int)sizeof(T), row = ch * (int)sizeof(T);  // bytes of the row before the block's, in all
+        const char *src = reinterpret_cast<const char *>(r.at(b, t0)) + before;
+        auto one = [&](int s, int c, const char *p) {  // the c-th 16 bytes of token s, whose channels begin at p
+            const int at = c * 16 - (int)(reinterpret_cast<uintptr_t>(p) & 15), valid = row - before - at;
+            char *d = dst[s * STRIDE].b + c * 16;
+            if (s < left && valid > 0)  // (of fewer than 16 bytes zeros behind them)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(d)), "l"(p + at), "r"(min(valid, 16))
+                             : "memory");
+            else
+                fill16(d);
+        };
+#pragma unroll 2
+        for (int s = 0; s < S; s += ROWS) one(s + first, q, src + (s + first) * step);
+        if (lane < S) one(lane, CHUNKS, src + lane * step);
     }
 }
-template <typename T, bool PAIRS>
-__device__ __forceinline__ void store_two(T *row, const Lane<PAIRS> &k, float2 f) {
+template <typename T, int ALIGN>
+__device__ __forceinline__ void store_two(T *row, const Lane<ALIGN> &k, float2 f) {
     T *p = place(row, k);
-    if constexpr (PAIRS) {
+    if constexpr (ALIGN) {
         if (!k.in0) return;
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16x2(f.x, f.y);
@@ -189,12 +186,12 @@ __device__ __forceinline__ void store_two(T *row, const Lane<PAIRS> &k, float2 f
     }
 }
 // The same for fp32 arrays of the channels (states, parameters): p is the array's row.
-template <bool PAIRS>
-__device__ __forceinline__ float2 load_state(const float *p, const Lane<PAIRS> &k) {
+template <int ALIGN>
+__device__ __forceinline__ float2 load_state(const float *p, const Lane<ALIGN> &k) {
     return make_float2(p && k.in0 ? p[k.c0] : 0.f, p && k.in1 ? p[k.c0 + k.step] : 0.f);
 }
-template <bool PAIRS>
-__device__ __forceinline__ void store_state(float *p, const Lane<PAIRS> &k, float2 v) {
+template <int ALIGN>
+__device__ __forceinline__ void store_state(float *p, const Lane<ALIGN> &k, float2 v) {
     if (k.in0) p[k.c0] = v.x;
     if (k.in1) p[k.c0 + k.step] = v.y;
 }
@@ -342,7 +339,7 @@ struct Place {
     }
 };
 struct LinkShared {
-    float4 tiles[kGroup][32];
+    float4 tiles[kGroup - 1][32];
     float2 group[32], enter[32];
 };
 // The state that enters the tile; `first`: the one that enters the row, for its first group.  `all`: the tile's own run,
@@ -419,7 +416,6 @@ struct GatedArgs {
     int ch, nblk, batch, ntile, nkeep;
     int sub, per;           // warps of a row's tile; rows of a block (linked rows: 1)
     int tiles, some_empty;  // tiles in all (of `per` rows each); whether a sequence has no tokens
-    int wide;               // every row that is read lies on a 16-byte boundary
     Seqs seqs;
     Links links;
 };
@@ -432,8 +428,8 @@ inline int rows_of_block(int64_t rows, int64_t ntile, int sub, int warps, int pl
     return (int)(want < most ? want : most);
 }
 
-template <typename T, bool PAIRS>
-__device__ __forceinline__ float2 rates_of(const GatedArgs<T> &a, const Lane<PAIRS> &k) {
+template <typename T, int ALIGN>
+__device__ __forceinline__ float2 rates_of(const GatedArgs<T> &a, const Lane<ALIGN> &k) {
     if (a.rates) return load_state(a.rates, k);
     const float2 d = load_state(a.decay, k);
     return make_float2(k.in0 ? decay_rate(d.x, a.rate) : 0.f, k.in1 ? decay_rate(d.y, a.rate) : 0.f);
@@ -449,15 +445,21 @@ inline int64_t gated_kept(const ssd_gated_shape_t *s) { return (s->seqlen + kSta
 size_t links_bytes(int64_t ch, int64_t rows, int64_t ntile);
 template <typename T>
 cudaError_t prepare(GatedArgs<T> &a, char *ws, int64_t rows, int64_t ntile, cudaStream_t st);
+template <typename F>
+void by_align(Align a, F &&f) {
+    a == kSixteen ? f(std::integral_constant<int, kSixteen>{})
+    : a == kPairs ? f(std::integral_constant<int, kPairs>{})
+                  : f(std::integral_constant<int, kElements>{});
+}
 // Pairs of channels that lie on their own size's boundary in every row.
 bool rows_pairs(const ssd_rows_t &r, size_t esize, int64_t b, int64_t L);
 template <typename T>
 GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, int64_t nseq);
-bool gated_pairs(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
-bool gated_wide(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
+// of the rows that are read
+Align gated_align(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in);
 bool any_empty(const int64_t *cu, int64_t nseq);
 template <typename T>
-cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, bool pairs, bool packed, char *links, cudaStream_t st);
+cudaError_t launch_gated_fwd(GatedArgs<T> &a, const ssd_gated_shape_t *s, Align align, bool packed, char *links, cudaStream_t st);
 size_t gated_fwd_links(const ssd_gated_shape_t *s);
 
 }  // namespace ssd

@@ -29,14 +29,14 @@ constexpr int kTile = kWarps * S;
 static_assert(kTile % kStateEvery == 0, "a tile starts at a kept state");
 
 // The next tile's x, r, i, dy and z: each lane's own.
-template <typename T>
+template <typename T, int ALIGN>
 struct Stage {
-    Two<T> in[5][S][kWarps][32];
+    Slot<T, ALIGN> in[5][S][kWarps];
 };
 
-template <typename T, bool PAIRS>
+template <typename T, int ALIGN>
 struct Warp {
-    Lane<PAIRS> k;
+    Lane<ALIGN> k;
     int later, tile, row, b, t0;  // later: tiles behind this one
     __device__ __forceinline__ Warp(const GatedArgs<T> &a, int n, int in_block, int in_row, int lane, int tokens)
         : k(((n * a.per + in_block) % (a.nblk * a.batch)) % a.nblk, lane, a.ch) {
@@ -45,17 +45,17 @@ struct Warp {
         if (later >= a.ntile) t0 = a.seqs.L;  // a block's row past the last one: no token is there
     }
 };
-template <typename T, bool PAIRS>
-__device__ __forceinline__ f2 state_of(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, const float *states, int s) {
+template <typename T, int ALIGN>
+__device__ __forceinline__ f2 state_of(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, const float *states, int s) {
     return both(load_state(states ? states + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch : nullptr, w.k));
 }
 
 // Starts the copies of a tile's inputs.
-template <typename T, bool PAIRS, bool GATE>
-__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, Stage<T> &st, int warp, int lane) {
-    const int left = a.seqs.L - w.t0, stride = kWarps * 32;
+template <typename T, int ALIGN, bool GATE>
+__device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, Stage<T, ALIGN> &st, int warp, int lane) {
+    const int left = a.seqs.L - w.t0;
     auto rows = [&](int which, const Rows<const T> &r, float fill) {
-        fetch_rows<T, PAIRS, S>(&st.in[which][0][warp][0], stride, r.at(w.b, w.t0), r.rs, w.k, lane, left, a.wide, a.ch, fill);
+        fetch_rows<T, ALIGN, S, kWarps>(&st.in[which][0][warp], r, w.b, w.t0, w.k, lane, left, a.ch, fill);
     };
     rows(1, a.r, -30000.f);
     rows(0, a.x, 0.f);
@@ -78,28 +78,30 @@ __device__ __forceinline__ f2 input_of(f2 v, f2 si, f2 x) {  // beta s(i) x
 }
 
 // PLAIN as in the forward kernel.
-template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, const Stage<T> &st,
+template <typename T, int ALIGN, bool GATE, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, f2 rate, const Stage<T, ALIGN> &st,
                                             int warp, int lane, Kept<T> (&t)[S], f2 &A, f2 &H, f2 &Q) {
     A = splat(1.f), H = splat(0.f), Q = splat(0.f);
+    const Skew<T, ALIGN> sx(a.x, w.b, w.t0), sr(a.r, w.b, w.t0), si(a.i, w.b, w.t0), sdy(a.dy, w.b, w.t0), sz(a.z, w.b, w.t0);
+    auto in = [&](int which, int s, const Skew<T, ALIGN> &skew) { return two_in(st.in[which][s][warp], lane, skew(s)); };
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        t[s].x = st.in[0][s][warp][lane];
-        t[s].sr = both(sigmoid2(widen(st.in[1][s][warp][lane])));
-        t[s].si = both(sigmoid2(widen(st.in[2][s][warp][lane])));
+        t[s].x = in(0, s, sx);
+        t[s].sr = both(sigmoid2(widen(in(1, s, sr))));
+        t[s].si = both(sigmoid2(widen(in(2, s, si))));
         f2 av;
         decay2<PLAIN>(mul2(rate, t[s].sr), t[s].v, av);
         av = one_minus(t[s].v);
         if (PACKED && !PLAIN && (cut.first >> s & 1)) H = state_of(a, w, cut, a.init, s);
         A = mul2(A, av);
         H = fma2(av, H, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
-        t[s].d = both(widen(st.in[3][s][warp][lane]));
+        t[s].d = both(widen(in(3, s, sdy)));
         t[s].e = splat(0.f);
         if constexpr (GATE) {
             // silu(z) = z s, its slope s + z s (1 - s)
-            const float2 z = widen(st.in[4][s][warp][lane]);
-            const f2 zf = both(z), sz = both(sigmoid2(z)), gate = mul2(zf, sz);
-            t[s].e = mul2(t[s].d, fma2(gate, one_minus(sz), sz));
+            const float2 z = widen(in(4, s, sz));
+            const f2 zf = both(z), open = both(sigmoid2(z)), gate = mul2(zf, open);
+            t[s].e = mul2(t[s].d, fma2(gate, one_minus(open), open));
             t[s].d = mul2(t[s].d, gate);
         }
     }
@@ -111,8 +113,8 @@ __device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T,
 }
 
 // h: the state that enters; c: what comes back from later tokens, and on return what goes back to earlier ones.
-template <typename T, bool PAIRS, bool GATE, bool PACKED, bool PLAIN>
-__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, PAIRS> &w, const Cuts &cut, f2 rate, Kept<T> (&t)[S], f2 h,
+template <typename T, int ALIGN, bool GATE, bool PACKED, bool PLAIN>
+__device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, f2 rate, Kept<T> (&t)[S], f2 h,
                                              f2 &c, f2 &sum) {
     const int L = a.seqs.L;
     f2 prev[S];
@@ -122,7 +124,7 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
         if (PACKED && !PLAIN && (cut.first >> s & 1)) h = state_of(a, w, cut, a.init, s);
         prev[s] = h;
         h = fma2(one_minus(t[s].v), h, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
-        if (GATE && (PLAIN || w.t0 + s < L)) store_two<T, PAIRS>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
+        if (GATE && (PLAIN || w.t0 + s < L)) store_two<T, ALIGN>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
     }
     T *px = a.dx.at(w.b, w.t0), *pr = a.dr.at(w.b, w.t0), *pi = a.i.p ? a.di.at(w.b, w.t0) : nullptr;
     sum = splat(0.f);
@@ -141,20 +143,20 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
             store_state(a.dinit + (int64_t)seq_from(a.seqs, cut.seq, w.t0 + s) * a.ch, w.k, apart(c));
         if (PLAIN || w.t0 + s < L) {
             const f2 gx = mul2(mul2(gh, beta), t[s].si);
-            store_two<T, PAIRS>(px + a.dx.step(s), w.k, apart(gx));
-            store_two<T, PAIRS>(pr + a.dr.step(s), w.k, apart(mul2(dll, one_minus(t[s].sr))));
-            if (pi) store_two<T, PAIRS>(pi + a.di.step(s), w.k, apart(mul2(mul2(gx, xf), one_minus(t[s].si))));
+            store_two<T, ALIGN>(px + a.dx.step(s), w.k, apart(gx));
+            store_two<T, ALIGN>(pr + a.dr.step(s), w.k, apart(mul2(dll, one_minus(t[s].sr))));
+            if (pi) store_two<T, ALIGN>(pi + a.di.step(s), w.k, apart(mul2(mul2(gx, xf), one_minus(t[s].si))));
         }
     }
 }
 
-template <typename T, bool PAIRS, bool GATE, bool PACKED>
+template <typename T, int ALIGN, bool GATE, bool PACKED>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const __grid_constant__ GatedArgs<T> a) {
     extern __shared__ __align__(16) uint8_t dynamic[];
-    Stage<T> &st = *reinterpret_cast<Stage<T> *>(dynamic);
+    Stage<T, ALIGN> &st = *reinterpret_cast<Stage<T, ALIGN> *>(dynamic);
     __shared__ float4 fore[2][kWarps][32], back[2][kWarps][32];
     __shared__ LinkShared sh;
-    __shared__ float2 sums[2][kWarps][32];
+    __shared__ float2 sums[2][kWarps - 1][32];
     __shared__ unsigned ticket[2];
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, nw = blockDim.x / 32, tokens = a.sub * S, L = a.seqs.L;
     const int in_block = uniform(warp / a.sub), in_row = warp - in_block * a.sub, own = warp - in_row;  // (own: the row's first)
@@ -163,25 +165,25 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
     auto run_of = [](const float4 &v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; };
     if (!a.i.p) {  // no input gate: s(128) = 1
 #pragma unroll
-        for (int s = 0; s < S; ++s) st.in[2][s][warp][lane] = two_of(T(), 128.f);
+        for (int s = 0; s < S; ++s) fill_slot(st.in[2][s][warp], lane, 128.f);
     }
     wait_previous();
     if (threadIdx.x == 0) ticket[1] = next(blockIdx.x - gridDim.x);
     __syncthreads();
     int n = uniform((int)ticket[1]);
-    Warp<T, PAIRS> w(a, n, in_block, in_row, lane, tokens);
-    auto entering = [&](const Warp<T, PAIRS> &w) {
+    Warp<T, ALIGN> w(a, n, in_block, in_row, lane, tokens);
+    auto entering = [&](const Warp<T, ALIGN> &w) {
         return load_state(a.kept + ((int64_t)w.b * a.nkeep + w.tile * (kTile / kStateEvery)) * a.ch, w.k);
     };
     float2 rate = make_float2(0.f, 0.f), kept = rate;
     Cuts cut{0, 0, w.b};
     if (n < a.tiles) {
         rate = rates_of(a, w.k), kept = entering(w);
-        fetch_tile<T, PAIRS, GATE>(a, w, st, warp, lane);
+        fetch_tile<T, ALIGN, GATE>(a, w, st, warp, lane);
         if (PACKED && w.t0 < L) cut = cuts_of<S>(a.seqs, w.t0);
     }
     for (int p = 0; n < a.tiles; p ^= 1) {
-        const Lane<PAIRS> &k = w.k;
+        const Lane<ALIGN> &k = w.k;
         if (threadIdx.x == 0) ticket[p] = next((unsigned)n);
         float2 h = kept;
         const f2 rates = both(rate);
@@ -194,9 +196,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
         Kept<T> t[S];
         f2 A, H, Q;
         if (plain)
-            read_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
+            read_tokens<T, ALIGN, GATE, PACKED, true>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
         else
-            read_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
+            read_tokens<T, ALIGN, GATE, PACKED, false>(a, w, cut, rates, st, warp, lane, t, A, H, Q);
         {
             const float2 fa = apart(A), fh = apart(H), fq = apart(Q);
             fore[p][warp][lane] = cut.first ? make_float4(-1.f, -1.f, fh.x, fh.y) : make_float4(fa.x, fa.y, fh.x, fh.y);
@@ -210,11 +212,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
             Place(a.links, w.row, w.later, a.ntile, lane).publish(all);
         }
         n = uniform((int)ticket[p]);
-        const Warp<T, PAIRS> after(a, n, in_block, in_row, lane, tokens);
+        const Warp<T, ALIGN> after(a, n, in_block, in_row, lane, tokens);
         Cuts next_cut{0, 0, after.b};
         if (n < a.tiles) {
             rate = rates_of(a, after.k), kept = entering(after);
-            fetch_tile<T, PAIRS, GATE>(a, after, st, warp, lane);
+            fetch_tile<T, ALIGN, GATE>(a, after, st, warp, lane);
             if (PACKED && after.t0 < L) next_cut = cuts_of<S>(a.seqs, after.t0);
         }
 
@@ -225,16 +227,16 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) gated_bwd_kernel(const _
 
         f2 cv = both(c), sum;
         if (plain)
-            write_tokens<T, PAIRS, GATE, PACKED, true>(a, w, cut, rates, t, both(h), cv, sum);
+            write_tokens<T, ALIGN, GATE, PACKED, true>(a, w, cut, rates, t, both(h), cv, sum);
         else
-            write_tokens<T, PAIRS, GATE, PACKED, false>(a, w, cut, rates, t, both(h), cv, sum);
+            write_tokens<T, ALIGN, GATE, PACKED, false>(a, w, cut, rates, t, both(h), cv, sum);
         if (!PACKED && w.t0 == 0 && a.dinit) store_state(a.dinit + (int64_t)w.b * a.ch, k, apart(cv));
         if (a.ddecay_part) {
-            sums[p][warp][lane] = apart(sum);
+            if (warp != own) sums[p][warp - 1][lane] = apart(sum);
             __syncthreads();
             if (warp == own && w.t0 < L) {
-                float2 s = make_float2(0.f, 0.f);
-                for (int j = own; j < own + a.sub; ++j) s.x += sums[p][j][lane].x, s.y += sums[p][j][lane].y;
+                float2 s = apart(sum);
+                for (int j = own; j < own + a.sub - 1; ++j) s.x += sums[p][j][lane].x, s.y += sums[p][j][lane].y;
                 store_state(a.ddecay_part + ((int64_t)w.tile * a.batch + w.b) * a.ch, k, s);
             }
         }
@@ -314,22 +316,24 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
         e = place_offsets(cu, nseq, reinterpret_cast<int *>(ws), a.seqs, &launched, st);
         if (e != cudaSuccess) return status_of(e);
     }
-    bool pairs = gated_pairs(s, in);
+    Align align = gated_align(s, in);
     if (!kept) {
         a.keep = reinterpret_cast<float *>(ws + p.kept);
-        e = launch_gated_fwd(a, s, pairs, cu != nullptr, ws + p.fwd_links, st);
+        e = launch_gated_fwd(a, s, align, cu != nullptr, ws + p.fwd_links, st);
         if (e != cudaSuccess) return status_of(e);
         kept = a.keep;
     }
     a.kept = kept, a.dfinal = dfinal;
     a.dy = rows_of<const T>(*dy);
-    a.wide = a.wide && rows_vec(*dy, sizeof(T), s->batch, s->seqlen);
     a.dx = rows_of<T>(out->dx), a.dr = rows_of<T>(out->dr), a.di = rows_of<T>(out->di), a.dz = rows_of<T>(out->dz);
     a.dinit = out->dinit_state;
     a.ddecay_part = out->ddecay ? reinterpret_cast<float *>(ws + p.part) : nullptr;
-    for (const ssd_rows_t *r : {dy, &out->dx, &out->dr}) pairs = pairs && rows_pairs(*r, sizeof(T), s->batch, s->seqlen);
+    if (align == kSixteen && !rows_vec(*dy, sizeof(T), s->batch, s->seqlen)) align = kPairs;
+    bool pairs = rows_pairs(*dy, sizeof(T), s->batch, s->seqlen);
+    for (const ssd_rows_t *r : {&out->dx, &out->dr}) pairs = pairs && rows_pairs(*r, sizeof(T), s->batch, s->seqlen);
     if (in->i.data) pairs = pairs && rows_pairs(out->di, sizeof(T), s->batch, s->seqlen);
     if (in->z.data) pairs = pairs && rows_pairs(out->dz, sizeof(T), s->batch, s->seqlen);
+    if (!pairs) align = kElements;
     const int64_t ntile = bwd_tiles(s->seqlen), rows = gated_blocks(s) * s->batch;
     const int most = kSMs * kBlocks;
     a.ntile = (int)ntile;
@@ -341,13 +345,16 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     a.some_empty = cu && a.dinit && any_empty(cu, nseq);
     const unsigned blocks = (unsigned)(a.tiles < most ? a.tiles : most);
     auto go = [&](auto pr, auto g, auto c) {
+        constexpr int kStage = (int)sizeof(Stage<T, decltype(pr)::value>);
+        constexpr int kBeside = (int)(4 * kWarps * 32 * sizeof(float4) + sizeof(LinkShared) + 2 * (kWarps - 1) * 32 * sizeof(float2) + 8);
+        static_assert(kBlocks * (kStage + kBeside + 1024) <= 228 * 1024, "two blocks an SM");
         auto kernel = gated_bwd_kernel<T, decltype(pr)::value, decltype(g)::value, decltype(c)::value>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Stage<T>));
-        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), a.sub * a.per * 32, sizeof(Stage<T>), st, a.rates != nullptr, a);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStage);
+        if (e == cudaSuccess) e = launch(kernel, dim3(blocks), a.sub * a.per * 32, kStage, st, a.rates != nullptr, a);
     };
     auto with_cuts = [&](auto pr, auto g) { cu ? go(pr, g, std::true_type{}) : go(pr, g, std::false_type{}); };
     auto with_gate = [&](auto pr) { a.z.p ? with_cuts(pr, std::true_type{}) : with_cuts(pr, std::false_type{}); };
-    pairs ? with_gate(std::true_type{}) : with_gate(std::false_type{});
+    by_align(align, with_gate);
     timing_mark(st, "gated_bwd");
     if (e != cudaSuccess || !out->ddecay) return status_of(e);
     e = launch(gated_ddecay_kernel, dim3((unsigned)((s->channels + 31) / 32)), 1024, 0, st, true, a.ddecay_part,

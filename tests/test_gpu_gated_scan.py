@@ -286,6 +286,34 @@ def test_reads_and_writes_among_nans():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,L,ch,pads", [
+    ("bf16", 70, 64, (1, 7, 8, 2, 3)), ("bf16", 33, 130, (5, 4, 0, 9, 1)), ("bf16", 20, 5, (3, 1, 6, 0, 2)), ("bf16", 300, 72, (8, 16, 0, 24, 8)),
+    ("bf16", 41, 192, (2, 4, 6, 2, 10)), ("f32", 50, 64, (1, 3, 2, 4, 1)), ("f32", 21, 3, (1, 2, 3, 0, 1)), ("f32", 90, 100, (2, 4, 0, 6, 2)),
+])
+def test_every_alignment(dtype, L, ch, pads):
+    """Each operand at its own distance from a 16-byte boundary, in rows at every one, among NaN."""
+    t = make(dtype, 2, L, ch, seed=15)
+    dy = torch.randn(2, L, ch, generator=torch.Generator().manual_seed(3)).to(DT[dtype]).cuda()
+    far = {}
+    for k, pad in zip(("x", "r", "i", "z", "dy"), pads):
+        odd = pad % 2
+        w = torch.full((2, L, ch + pad + odd), float("nan"), dtype=DT[dtype], device="cuda")
+        far[k] = w[:, :, pad:pad + ch]
+        far[k][:] = dy if k == "dy" else t[k]
+    far_dy = far.pop("dy")
+    got = ssd.ssd_gated_scan_fwd(*args_of(dict(t, **far)), return_chunk_states=True)
+    want = ssd.ssd_gated_scan_fwd(*args_of(t), return_chunk_states=True)
+    for a, w in zip(got, want):
+        assert torch.equal(a, w)
+    for a, w in zip(ssd.ssd_gated_scan_bwd(far_dy, *args_of(dict(t, **far))), ssd.ssd_gated_scan_bwd(dy, *args_of(t))):
+        assert torch.equal(a, w)
+    state, one = t["init"].clone(), t["init"].clone()
+    token = lambda d: [d[k][:, 0] for k in ("x", "r")] + [t["decay"]] + [d[k][:, 0] for k in ("i", "z")]
+    assert torch.equal(ssd.ssd_gated_scan_step(*token(far), state=state), ssd.ssd_gated_scan_step(*token(t), state=one))
+    assert torch.equal(state, one)
+
+
+@pytest.mark.gpu
 def test_one_row_for_all():
     t = make("f32", 2, 100, 64, seed=13)
     one = t["r"][:, :1].expand(2, 100, 64)
