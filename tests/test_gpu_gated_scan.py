@@ -314,6 +314,24 @@ def test_every_alignment(dtype, L, ch, pads):
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_elements():
+    L, ch, cut = 262400, 8192, 260000
+    x, r, i = (torch.empty(1, L, ch, device="cuda", dtype=torch.bfloat16).normal_() for _ in range(3))
+    decay = torch.randn(ch, device="cuda") - 4
+    y, fin, states = ssd.ssd_gated_scan_fwd(x, r, decay, i, return_chunk_states=True)
+    mid = ssd.ssd_gated_scan_fwd(x[:, :cut], r[:, :cut], decay, i[:, :cut])[1]
+    last = [v[:, cut:] for v in (x, r, i)]
+    want = ssd.ssd_gated_scan_fwd(last[0], last[1], decay, last[2], init_state=mid)
+    got = ssd.ssd_gated_scan_bwd(x, x, r, decay, i, chunk_states=states)
+    grads = ssd.ssd_gated_scan_bwd(last[0], last[0], last[1], decay, last[2], init_state=mid)
+    # the states differ by fp32 roundings (test_forward, test_gradient), which may take a bf16 result to the next value
+    for a, w, rel in ((y, want[0], 1e-5), *((got[k], grads[k], 1e-4) for k in (0, 1, 3))):
+        a, w = a[:, cut:].float(), w.float()
+        assert bool(((a - w).abs() <= 2.0 ** -7 * w.abs() + rel * w.square().mean().sqrt()).all())
+    assert bool(((fin - want[1]).abs() <= 1e-5 * want[1].square().mean().sqrt()).all())
+
+
+@pytest.mark.gpu
 def test_one_row_for_all():
     t = make("f32", 2, 100, 64, seed=13)
     one = t["r"][:, :1].expand(2, 100, 64)

@@ -57,6 +57,24 @@ def test_forward(rows, dim, vocab, pad):
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_logits():
+    rows, dim, vocab, few = 43100, 64, 50277, 200
+    h, w, targets = make(rows, dim, vocab, seed=4)
+    glp, _, gent = upstream(rows)
+    logprob, lse, entropy = ssd.ssd_head_logprob_fwd(h, w, targets)
+    part = ssd.ssd_head_logprob_fwd(h[-few:], w, targets[-few:])
+    for a, b in zip((logprob, lse, entropy), part):  # (other tiles: fp32 sums in another order)
+        assert bool(((a[-few:] - b).abs() <= 2e-6 * (1 + b.abs())).all())
+    dh, dw = ssd.ssd_head_logprob_bwd(h, w, targets, lse, entropy, dlogprob=glp, dentropy=gent)
+    want, _ = ssd.ssd_head_logprob_bwd(h[-few:], w, targets[-few:], part[1], part[2], dlogprob=glp[-few:], dentropy=gent[-few:],
+                                       need_dweight=False)
+    # one step of bf16 of dz here and there, and one of the result
+    d, rms = (dh[-few:].float() - want.float()).abs(), want.float().square().mean().sqrt()
+    assert bool((d <= 2.0 ** -7 * want.float().abs() + 2.0 ** -7 * rms).all())
+    assert torch.isfinite(dw).all()
+
+
+@pytest.mark.gpu
 def test_many_rows_with_the_same_tokens():
     """So many that the chunks they are summed in are longer than a block, and there are hundreds of them."""
     rows, dim, vocab = 270000, 8, 40

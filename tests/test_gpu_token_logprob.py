@@ -259,6 +259,24 @@ def test_rows_far_apart():
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_elements():
+    rows, vocab, few = 43000, 50277, 100
+    z = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda").normal_()
+    targets = torch.randint(0, vocab, (rows,), device="cuda")
+    glp = torch.randn(rows, device="cuda")
+    got = ssd.ssd_token_logprob_fwd(z, targets, top=3)
+    part = ssd.ssd_token_logprob_fwd(z[-few:], targets[-few:], top=3)
+    # Of few rows each is shared by two blocks, of many it is not: the same positive terms in another order.  A thread adds up
+    # to 200 of them, each addition off by 2^-24 of the sum so far, so the sums of two calls differ by 2 * 200 * 2^-24 = 2.4e-5
+    # at most, lse and log-probabilities by as much, the entropy by (1 + 2 moment / sum) times that, below 17 times.
+    for a, b, size in zip(got, part, (1, 1, 17, 1)):
+        assert bool(((a[-few:] - b).abs() <= 2.5e-5 * size).all())
+    assert torch.equal(got[4][-few:], part[4])
+    want = ssd.ssd_token_logprob_bwd(z[-few:], targets[-few:], got[1][-few:].contiguous(), dlogprob=glp[-few:])
+    assert torch.equal(ssd.ssd_token_logprob_bwd(z, targets, got[1], dlogprob=glp, dlogits=z)[-few:], want)
+
+
+@pytest.mark.gpu
 def test_captured_on_a_stream_and_bitwise():
     z, targets = make("bf16", 3, 50280, seed=9)
     glp = grads(3)[0]
