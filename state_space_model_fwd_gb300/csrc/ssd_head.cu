@@ -46,7 +46,7 @@ constexpr int kSmem = kRing + kReaders * 4096 + 1024;
 constexpr int kShare = 20;      // chunks of K
 constexpr int kLongest = 4096;  // and at most in one sum of the gradient: 2.7e-4 too small, a tenth of a step of its bf16 result
 constexpr uint64_t kWaitNs = 100000000ull;
-constexpr int kNoLead = 0x7F7F7F7F;
+constexpr int kNoLead = 0x7FFFFFFF;  // above every row
 
 // What becomes of an accumulator.
 enum Use { kStats, kGrad, kStore };
@@ -112,6 +112,7 @@ struct GemmArgs {
     float *given;         // [M] the given tokens' logits
     RowGradIn grad;
     float *rest;          // [M] what rounding left of the given token's dz (0 without one)
+    int *lead;            // [N] set to kNoLead (null: not wanted)
     // kStore
     bf16 *out;
     int64_t out_pitch;
@@ -479,6 +480,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if constexpr (USE == kGrad) {
                     if (live) g = row_grad(a.grad, row, a.N);
                     if (live && t.n == 0 && half == 0 && (g.target < 0 || g.none)) a.rest[row] = 0.f;
+                    if (a.lead && t.m == 0 && rank == 0 && q == 0)
+                        for (int c = lane; c < limit; c += 32) a.lead[c0 + first + c] = kNoLead;
                 } else if (t.part < 0) {
                     fix = fix_row(a.fix, row, live);
                 }
@@ -946,6 +949,8 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
     a.rest = reinterpret_cast<float *>(ws + p.rest);
     const bool given = targets && dlogprob;  // otherwise no element of dz stands out
+    int *lead = dweight && given ? reinterpret_cast<int *>(ws + p.lead) : nullptr;
+    a.lead = lead;
     e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, mz_out, a, "head_dlogits", stream)
                  : run_gemm<kGrad, false, false, false>(mh, mw, mz_out, a, "head_dlogits", stream);
     if (e == cudaSuccess && dhidden) {
@@ -962,13 +967,10 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
         b.status = status;
         b.out = static_cast<bf16 *>(dweight->data), b.out_pitch = pitch_of(*dweight, V, D);
         b.parts = reinterpret_cast<float *>(ws + p.parts);
-        if (given) {
+        if (lead) {
             float *sums = reinterpret_cast<float *>(ws + p.sums);
-            int *lead = reinterpret_cast<int *>(ws + p.lead), *next = reinterpret_cast<int *>(ws + p.next);
+            int *next = reinterpret_cast<int *>(ws + p.next);
             const int chunk = fix_chunk(T);
-            e = cudaMemsetAsync(lead, 0x7F, sizeof(int) * V, stream);  // kNoLead
-            timing_mark(stream, "head_leads");
-            if (e != cudaSuccess) return status_of(e);
             head_fix_kernel<<<(unsigned)T, 256, 0, stream>>>(targets, a.rest, static_cast<const bf16 *>(hidden->data), hp, (int)T, (int)D,
                                                              (int)V, chunk, lead, next, sums);
             timing_mark(stream, "head_fix");
