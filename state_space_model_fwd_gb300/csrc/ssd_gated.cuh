@@ -171,18 +171,19 @@ __device__ __forceinline__ void fetch_rows(Slot<T, ALIGN> *dst, const Rows<const
         if (lane < S) one(lane, CHUNKS, src + lane * step);
     }
 }
-template <typename T, int ALIGN>
+// ALL: every channel of the block exists.
+template <typename T, int ALIGN, bool ALL = false>
 __device__ __forceinline__ void store_two(T *row, const Lane<ALIGN> &k, float2 f) {
     T *p = place(row, k);
     if constexpr (ALIGN) {
-        if (!k.in0) return;
+        if (!ALL && !k.in0) return;
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16x2(f.x, f.y);
         else
             *reinterpret_cast<float2 *>(p) = f;
     } else {
-        if (k.in0) p[0] = from_f32<T>(f.x);
-        if (k.in1) p[32] = from_f32<T>(f.y);
+        if (ALL || k.in0) p[0] = from_f32<T>(f.x);
+        if (ALL || k.in1) p[32] = from_f32<T>(f.y);
     }
 }
 // The same for fp32 arrays of the channels (states, parameters): p is the array's row.
