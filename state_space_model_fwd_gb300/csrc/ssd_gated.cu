@@ -3,11 +3,11 @@
 // tile is in ssd_gated.cuh.
 //
 // What bounds the prompt's kernel: issue and waiting in turn.  A token and warp
-// of 64 channels takes 93 instructions (8 of the special function unit a
+// of 64 channels takes 89 instructions (8 of the special function unit a
 // channel with a gate), issued in half of the cycles: with 128 registers for 16
 // tokens' a and beta s(i) x there are four warps a scheduler, and a tile's two
 // meetings with the links cost 2000 of its 13000 cycles.  4 x 4096 x 2560 bf16
-// with a gate 101 us, 51% of the DRAM rate; 8 tokens a warp in 32 warps an SM
+// with a gate 103 us, 50% of the DRAM rate; 8 tokens a warp in 32 warps an SM
 // are as fast (less to wait for, twice the meetings), tiles of 64 tokens too.
 #include "ssd_gated.cuh"
 

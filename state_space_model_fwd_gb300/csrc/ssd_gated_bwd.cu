@@ -12,11 +12,12 @@
 // later tokens (c_t = a_t g_t, so c -> P c + Q over a run of tokens) through
 // the links.  Everything is read once and written once.
 //
-// What bounds it: issue, 236 instructions a token and warp in 54% of the
-// cycles, with 15 registers a token kept between the passes (4 x 4096 x 2560
-// bf16 with a gate 236 us, 39% of the DRAM rate).  16 warps of 4 tokens or of 8
-// are slower (8 x 4096 x 2560: 606 and 559 us against 471), and so is keeping
-// beta s(i) x instead of forming it again (477).
+// What bounds it: issue and waiting in turn, 211 instructions a token and warp
+// in half of the cycles, with 15 registers a token kept between the passes (4 x
+// 4096 x 2560 bf16 with a gate 226 us, 40% of the DRAM rate).  16 warps of 4
+// tokens or of 8 are slower (8 x 4096 x 2560: 606 and 559 us against 471 at the
+// time), and so is keeping beta s(i) x instead of forming it again (477);
+// leaving x in shared memory instead of registers gives 0.5%.
 #include "ssd_gated.cuh"
 
 namespace ssd {
@@ -117,8 +118,8 @@ template <typename T, int ALIGN, bool GATE, bool PACKED, bool PLAIN>
 __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T, ALIGN> &w, const Cuts &cut, f2 rate, Kept<T> (&t)[S], f2 h,
                                              f2 &c, f2 &sum) {
     const int L = a.seqs.L;
-    // Stores without a condition each: 8 x 4096 x 2560 bf16 437 us for 463.  (Without a gate it costs registers that are spilled:
-    // 566 us forward and gradient, 550 so.)
+    // Stores without a condition each: forward and gradient of 8 x 4096 x 2560 bf16 643 us for 668.  (Without a gate it costs
+    // registers that are spilled: 566 us, 547 so.)
     constexpr bool ALL = PLAIN && GATE;
     f2 prev[S];
     T *pz = GATE ? a.dz.at(w.b, w.t0) : nullptr;
