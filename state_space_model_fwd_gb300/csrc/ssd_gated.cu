@@ -259,7 +259,8 @@ Align gated_align(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in) {
 template <typename T>
 GatedArgs<T> gated_args(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, int64_t nseq) {
     GatedArgs<T> a{};
-    a.x = rows_of<const T>(in->x), a.r = rows_of<const T>(in->r), a.i = rows_of<const T>(in->i), a.z = rows_of<const T>(in->z);
+    a.x = gated_rows<const T>(s, in->x), a.r = gated_rows<const T>(s, in->r);
+    a.i = gated_rows<const T>(s, in->i), a.z = gated_rows<const T>(s, in->z);
     a.decay = in->decay, a.init = in->init_state, a.rate = s->rate;
     a.ch = (int)s->channels, a.nblk = (int)gated_blocks(s), a.batch = (int)s->batch, a.nkeep = (int)gated_kept(s);
     a.seqs.n = (int)nseq, a.seqs.L = (int)s->seqlen;
@@ -348,7 +349,7 @@ ssd_status_t fwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
     if (s->seqlen == 0)
         return status_of(fin ? copy_states(in->init_state, fin, nseq * s->channels, st) : cudaSuccess);
     GatedArgs<T> a = gated_args<T>(s, in, nseq);
-    a.y = rows_of<T>(*y);
+    a.y = gated_rows<T>(s, *y);
     a.fin = fin, a.keep = keep;
     cudaError_t e = cudaSuccess;
     if (cu) {
@@ -365,7 +366,7 @@ ssd_status_t fwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
 template <typename T>
 ssd_status_t step_typed(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, float *state, const ssd_rows_t *y, cudaStream_t st) {
     GatedArgs<T> a = gated_args<T>(s, in, s->batch);
-    a.y = rows_of<T>(*y);
+    a.y = gated_rows<T>(s, *y);
     timing_begin(st);
     const unsigned blocks = (unsigned)(((int64_t)a.nblk * a.batch + 3) / 4);
     if (gated_align(s, in) != kElements && rows_pairs(*y, sizeof(T), s->batch, 1))

@@ -436,6 +436,17 @@ __device__ __forceinline__ float2 rates_of(const GatedArgs<T> &a, const Lane<ALI
     return make_float2(k.in0 ? decay_rate(d.x, a.rate) : 0.f, k.in1 ? decay_rate(d.y, a.rate) : 0.f);
 }
 
+// An operand's rows as the kernels get them.  A stride between rows of which there is one, or none, is 0 whatever the caller
+// left there: alignment goes by the strides that mean something, and Skew steps by the row stride over all tokens of a warp,
+// those past the end too.
+template <typename P>
+Rows<P> gated_rows(const ssd_gated_shape_t *s, const ssd_rows_t &r) {
+    Rows<P> v = rows_of<P>(r);
+    if (!r.data || s->batch <= 1) v.bs = 0;
+    if (!r.data || s->seqlen <= 1) v.rs = 0;
+    return v;
+}
+
 // host side (ssd_gated.cu)
 ssd_status_t check_gated(const ssd_gated_shape_t *s, const int64_t *cu, int64_t nseq);
 bool gated_inputs_ok(const ssd_gated_shape_t *s, const ssd_gated_inputs_t *in, bool rows);

@@ -328,8 +328,8 @@ ssd_status_t bwd_typed(const ssd_gated_shape_t *s, const int64_t *cu, int64_t ns
         kept = a.keep;
     }
     a.kept = kept, a.dfinal = dfinal;
-    a.dy = rows_of<const T>(*dy);
-    a.dx = rows_of<T>(out->dx), a.dr = rows_of<T>(out->dr), a.di = rows_of<T>(out->di), a.dz = rows_of<T>(out->dz);
+    a.dy = gated_rows<const T>(s, *dy);
+    a.dx = gated_rows<T>(s, out->dx), a.dr = gated_rows<T>(s, out->dr), a.di = gated_rows<T>(s, out->di), a.dz = gated_rows<T>(s, out->dz);
     a.dinit = out->dinit_state;
     a.ddecay_part = out->ddecay ? reinterpret_cast<float *>(ws + p.part) : nullptr;
     if (align == kSixteen && !rows_vec(*dy, sizeof(T), s->batch, s->seqlen)) align = kPairs;

@@ -314,6 +314,67 @@ def test_every_alignment(dtype, L, ch, pads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cu", [None, [0, 0, 1, 1]], ids=["equal", "packed"])
+@pytest.mark.parametrize("which", ["x", "r", "i", "z", "dy", "y", "all"])
+@pytest.mark.parametrize("dtype,b,ch,width", [("bf16", 1, 66, 67), ("f32", 1, 66, 69), ("bf16", 2, 1002, 1003), ("f32", 3, 130, 131),
+                                              ("bf16", 1, 64, 67), ("f32", 1, 5, 7)])
+def test_one_token_out_of_odd_rows(dtype, b, ch, width, which, cu):
+    """A prompt of one token has no next row: the stride to it means nothing."""
+    if cu and b > 1:
+        pytest.skip("a packed batch is one row")
+    t = make(dtype, b, 1, ch, cu=cu, seed=16)
+    dy = torch.randn(b, 1, ch, generator=torch.Generator().manual_seed(4)).to(DT[dtype]).cuda()
+    first = lambda: torch.full((b, 4, width), float("nan"), dtype=DT[dtype], device="cuda")[:, :1, :ch]
+
+    def far(k, v):
+        if which not in (k, "all"):
+            return v
+        w = first()
+        w[:] = v
+        assert w.stride()[1:] == (width, 1)
+        return w
+    odd = {k: far(k, v) if k in ("x", "r", "i", "z") else v for k, v in t.items()}
+    y = first() if which in ("y", "all") else None
+    got = ssd.ssd_gated_scan_fwd(*args_of(odd), cu_seqlens=cu, y=y, return_chunk_states=True)
+    want = ssd.ssd_gated_scan_fwd(*args_of(t), cu_seqlens=cu, return_chunk_states=True)
+    wy, wfin = definition(*[ref.d(t[k]) for k in NAMES], cu)
+    ref.check(got[0], wy, "y", rel=1e-5)  # as in test_forward
+    ref.check(got[1], wfin, "final_state", rel=1e-5)
+    for a, w in zip(got, want):
+        assert torch.equal(a, w)
+    for states in (want[2], None):
+        for a, w in zip(ssd.ssd_gated_scan_bwd(far("dy", dy), *args_of(odd), cu_seqlens=cu, chunk_states=states),
+                        ssd.ssd_gated_scan_bwd(dy, *args_of(t), cu_seqlens=cu, chunk_states=states)):
+            assert torch.equal(a, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,L,ch", [("bf16", 1, 66), ("f32", 1, 66), ("bf16", 40, 66), ("f32", 40, 66)])
+def test_the_strides_of_an_absent_gate_mean_nothing(lib, dtype, L, ch):
+    from state_space_model_fwd_gb300 import _layer
+    t = make(dtype, 2, L, ch, igate=False, gate=False, seed=17)
+    dy = torch.randn(2, L, ch, generator=torch.Generator().manual_seed(5)).to(DT[dtype]).cuda()
+    want = ssd.ssd_gated_scan_fwd(*args_of(t))
+    grads = ssd.ssd_gated_scan_bwd(dy, *args_of(t))
+    rows = lambda v: _layer._rows_t(v.data_ptr(), L * ch, ch)
+    absent = _layer._rows_t(None, 335, 67)
+    shape = _layer._gated_shape_t(2, L, ch, 8.0, 1 if dtype == "bf16" else 0)
+    ins = _layer._gated_inputs_t(rows(t["x"]), rows(t["r"]), absent, absent, t["decay"].data_ptr(), t["init"].data_ptr())
+    y, fin = torch.empty_like(want[0]), torch.empty_like(want[1])
+    dx, dr, ddecay, dinit = (torch.empty_like(grads[k]) for k in (0, 1, 2, 5))
+    out = _layer._gated_grads_t(rows(dx), rows(dr), absent, absent, ddecay.data_ptr(), dinit.data_ptr())
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.ssd_gated_scan_bwd_workspace_size(ctypes.byref(shape), None, 0, 0) <= ws.numel()
+    assert lib.ssd_gated_scan_fwd(ctypes.byref(shape), None, 0, ctypes.byref(ins), ctypes.byref(rows(y)), fin.data_ptr(), None,
+                                  ws.data_ptr(), ws.numel(), stream) == OK
+    assert lib.ssd_gated_scan_bwd(ctypes.byref(shape), None, 0, ctypes.byref(rows(dy)), ctypes.byref(ins), None, None,
+                                  ctypes.byref(out), ws.data_ptr(), ws.numel(), stream) == OK
+    for a, w in zip((y, fin, dx, dr, ddecay, dinit), (*want, *(grads[k] for k in (0, 1, 2, 5)))):
+        assert torch.equal(a, w)
+
+
+@pytest.mark.gpu
 def test_more_than_2_31_elements():
     L, ch, cut = 262400, 8192, 260000
     x, r, i = (torch.empty(1, L, ch, device="cuda", dtype=torch.bfloat16).normal_() for _ in range(3))
