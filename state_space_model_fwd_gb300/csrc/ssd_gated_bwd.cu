@@ -65,16 +65,37 @@ __device__ __forceinline__ void fetch_tile(const GatedArgs<T> &a, const Warp<T, 
     if (GATE) rows(4, a.z, 0.f);
 }
 
-// What is kept of a token between the passes, two channels each: the gates, v = 1 - a, x, the gradient of h_t by its own
+// What is kept of a token between the passes, two channels each: the gates, the decay, x, the gradient of h_t by its own
 // output, and dy times the slope of the output's gate.
 template <typename T>
 struct Kept {
-    f2 sr, si, v, d, e;
+    f2 sr, si, w, d, e;
     Two<T> x;
 };
 __device__ __forceinline__ f2 one_minus(f2 v) { return fma2(v, splat(-1.f), splat(1.f)); }
-__device__ __forceinline__ f2 input_of(f2 v, f2 si, f2 x) {  // beta s(i) x
-    const float2 b2 = apart(fma2(v, one_minus(v), v));
+// The decay in one register: v = 1 - a, or -a where v is above a half and 1 - v would have lost a's digits (6% of it at
+// a = e^-14).  The sign bit says which, as a may be 0.  (8 x 4096 x 2560 bf16 whose warps all hold some such channel: this kernel
+// 517 us for 502; a formed again from m wherever it is needed takes twice the spills.)
+struct Decay {
+    f2 v, a;
+};
+template <bool PLAIN>
+__device__ __forceinline__ f2 kept_decay(f2 v, f2 a) {
+    if constexpr (PLAIN) return v;
+    const float2 vv = apart(v), aa = apart(a);
+    return pack2(vv.x > 0.5f ? -aa.x : vv.x, vv.y > 0.5f ? -aa.y : vv.y);
+}
+template <bool PLAIN>
+__device__ __forceinline__ Decay decay_of(f2 w) {
+    if constexpr (PLAIN) return {w, one_minus(w)};
+    const float2 f = apart(w);
+    const f2 p = pack2(fabsf(f.x), fabsf(f.y));
+    const float2 g = apart(p), o = apart(one_minus(p));
+    const bool x = signbit(f.x), y = signbit(f.y);
+    return {pack2(x ? o.x : g.x, y ? o.y : g.y), pack2(x ? g.x : o.x, y ? g.y : o.y)};
+}
+__device__ __forceinline__ f2 input_of(const Decay &q, f2 si, f2 x) {  // beta s(i) x
+    const float2 b2 = apart(fma2(q.v, q.a, q.v));
     return mul2(mul2(pack2(sqrt_approx(b2.x), sqrt_approx(b2.y)), si), x);
 }
 
@@ -90,12 +111,12 @@ __device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T,
         t[s].x = in(0, s, sx);
         t[s].sr = both(sigmoid2(widen(in(1, s, sr))));
         t[s].si = both(sigmoid2(widen(in(2, s, si))));
-        f2 av;
-        decay2<PLAIN>(mul2(rate, t[s].sr), t[s].v, av);
-        av = one_minus(t[s].v);
+        Decay q;
+        decay2<PLAIN>(mul2(rate, t[s].sr), q.v, q.a);
+        t[s].w = kept_decay<PLAIN>(q.v, q.a);
         if (PACKED && !PLAIN && (cut.first >> s & 1)) H = state_of(a, w, cut, a.init, s);
-        A = mul2(A, av);
-        H = fma2(av, H, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
+        A = mul2(A, q.a);
+        H = fma2(q.a, H, input_of(q, t[s].si, both(widen(t[s].x))));
         t[s].d = both(widen(in(3, s, sdy)));
         t[s].e = splat(0.f);
         if constexpr (GATE) {
@@ -109,7 +130,7 @@ __device__ __forceinline__ void read_tokens(const GatedArgs<T> &a, const Warp<T,
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
         if (PACKED && !PLAIN && (cut.last >> s & 1)) Q = state_of(a, w, cut, a.dfinal, s);
-        Q = mul2(one_minus(t[s].v), add2(t[s].d, Q));
+        Q = mul2(decay_of<PLAIN>(t[s].w).a, add2(t[s].d, Q));
     }
 }
 
@@ -127,7 +148,8 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
     for (int s = 0; s < S; ++s) {
         if (PACKED && !PLAIN && (cut.first >> s & 1)) h = state_of(a, w, cut, a.init, s);
         prev[s] = h;
-        h = fma2(one_minus(t[s].v), h, input_of(t[s].v, t[s].si, both(widen(t[s].x))));
+        const Decay q = decay_of<PLAIN>(t[s].w);
+        h = fma2(q.a, h, input_of(q, t[s].si, both(widen(t[s].x))));
         if (GATE && (PLAIN || w.t0 + s < L)) store_two<T, ALIGN, ALL>(pz + a.dz.step(s), w.k, apart(mul2(t[s].e, h)));
     }
     T *px = a.dx.at(w.b, w.t0), *pr = a.dr.at(w.b, w.t0), *pi = a.i.p ? a.di.at(w.b, w.t0) : nullptr;
@@ -135,8 +157,9 @@ __device__ __forceinline__ void write_tokens(const GatedArgs<T> &a, const Warp<T
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
         if (PACKED && !PLAIN && (cut.last >> s & 1)) c = state_of(a, w, cut, a.dfinal, s);
-        const f2 av = one_minus(t[s].v), gh = add2(t[s].d, c), xf = both(widen(t[s].x)), m = mul2(rate, t[s].sr);
-        const float2 b2 = apart(fma2(t[s].v, av, t[s].v));
+        const Decay q = decay_of<PLAIN>(t[s].w);
+        const f2 av = q.a, gh = add2(t[s].d, c), xf = both(widen(t[s].x)), m = mul2(rate, t[s].sr);
+        const float2 b2 = apart(fma2(q.v, av, q.v));
         const f2 rb = pack2(rsqrt_approx(fmaxf(b2.x, 1e-37f)), rsqrt_approx(fmaxf(b2.y, 1e-37f))), beta = mul2(both(b2), rb);
         c = mul2(gh, av);
         // dl l = g a (s(i) x a m / beta - m h_{t-1}),  l = -m

@@ -148,6 +148,74 @@ def test_all_decays(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gates", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("dtype,L,cu", [("f32", 40, None), ("bf16", 150, None), ("f32", 150, [0, 1, 60, 64, 129, 150])])
+def test_gradient_of_states_that_fade_within_a_token(dtype, L, cu, gates):
+    """m = -log a from 1 to 16, signs chosen so that nothing cancels: every gradient is good relative to itself."""
+    ch = 64
+    g = torch.Generator().manual_seed(21)
+    uni = lambda *s: 1 + torch.rand(*s, generator=g)
+    n = 1 if cu is None else len(cu) - 1
+    sign = 1 - 2.0 * (torch.arange(L) % 2)[:, None]  # x against the state that the tokens before it leave
+    softplus = torch.linspace(1.3, 15, ch) / 4      # rate 8, s(r) around 1/2
+    t = dict(x=uni(1, L, ch) * sign, r=0.2 * torch.randn(1, L, ch, generator=g), i=None, z=None,
+             decay=softplus + torch.log(-torch.expm1(-softplus)), init=torch.empty(n, ch))
+    starts = [0] if cu is None else cu[:-1]
+    for s, at in enumerate(starts):
+        t["init"][s] = -uni(ch) * sign[at]
+    if gates:
+        t["i"], t["z"] = torch.randn(1, L, ch, generator=g), uni(1, L, ch)
+    t = {k: None if v is None else v.to(DT[dtype] if k in ("x", "r", "i", "z") else torch.float32).cuda() for k, v in t.items()}
+    dy = uni(1, L, ch).to(DT[dtype]).cuda()
+    dfin = uni(n, ch).cuda()
+    m = 8 * ref.softplus(ref.d(t["decay"])) * torch.sigmoid(ref.d(t["r"]))
+    assert m.min() > 0.8 and 12 < m.max() < 20
+    leaves = [None if t[k] is None else ref.d(t[k]) for k in NAMES]
+    leaves[2] = leaves[2].expand(L, ch).clone()      # a decay for every token: its gradient's terms
+    for v in leaves:
+        if v is not None:
+            v.requires_grad_(True)
+    want = ref.gradients(definition(*leaves, cu), [ref.d(dy), ref.d(dfin)], leaves)
+    terms, want[2] = want[2], want[2].sum(0)
+    got = ssd.ssd_gated_scan_bwd(dy, *args_of(t), cu_seqlens=cu, dfinal_state=dfin)
+    # m is good to 2^-20.5 of itself (softplus and the sigmoid a few 2^-23 each), 1.2e-5 at 17, which is a's relative error; its
+    # exponential adds 2^-20 for the rounded argument; dr and ddecay have m once more, and a state of the same kind beside it
+    for name, a, w in zip(("dx", "dr", "ddecay", "di", "dz", "dinit"), got, want):
+        ref.check(a, w, name, rel=4e-5, scale=None if w is None else terms.abs().sum(0) if name == "ddecay" else w.abs())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_all_decays_all_gradients(dtype):
+    """As test_all_decays; every gradient, dr and ddecay against their own channel's size."""
+    t = make(dtype, 1, 90, 64, seed=2)
+    t["decay"] = torch.linspace(-30, 30, 64, device="cuda")
+    t["r"] = (t["r"].float() * 20).to(DT[dtype])
+    t["r"][:, 5], t["r"][:, 50], t["i"][:, 7], t["i"][:, 9] = 300.0, -300.0, 300.0, -300.0
+    g = torch.Generator().manual_seed(22)
+    dy = torch.randn(1, 90, 64, generator=g).to(DT[dtype]).cuda()
+    dfin = torch.randn(1, 64, generator=g).cuda()
+    got = ssd.ssd_gated_scan_bwd(dy, *args_of(t), dfinal_state=dfin)
+    leaves = [ref.d(t[k]) for k in NAMES]
+    leaves[2] = leaves[2].expand(90, 64).clone()
+    for v in leaves:
+        v.requires_grad_(True)
+    want = ref.gradients(definition(*leaves), [ref.d(dy), ref.d(dfin)], leaves)
+    shut = ref.d(t["r"]) < -200  # the limit, where autograd multiplies infinity and zero
+    want[1] = torch.where(shut, 0.0, want[1])
+    terms = torch.where(shut[0], 0.0, want[2])
+    want[2] = terms.sum(0)
+    channel = lambda w: torch.maximum(w.abs(), w.square().mean(-2, keepdim=True).sqrt())
+    # as in test_gradient; a is good to 2^-20.5 m, 6e-5 where it leaves fp32's range
+    ref.check(got[0], want[0], "dx", rel=2e-5)
+    ref.check(got[1], want[1], "dr", rel=2e-4, scale=channel(want[1]))
+    ref.check(got[2], want[2], "ddecay", rel=2e-4, scale=terms.abs().sum(0))
+    ref.check(got[3], want[3], "di", rel=2e-5)
+    ref.check(got[4], want[4], "dz", rel=2e-5)
+    ref.check(got[5], want[5], "dinit", rel=1e-4, scale=want[5].abs())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,ch,igate,gate", [("f32", 40, True, True), ("bf16", 64, True, False), ("bf16", 1001, False, True)])
 def test_tokens_one_by_one(dtype, ch, igate, gate):
     t = make(dtype, 3, 6, ch, igate=igate, gate=gate, seed=3)
