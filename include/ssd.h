@@ -578,10 +578,14 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
  * targets, outputs and masked or absent targets as there.
  * ssd_head_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
  * dhidden [rows, dim], dweight [vocab, dim] in bf16 (either NULL: not wanted).
- * The logits are formed again; their gradient is rounded to bf16 (2^-8
- * relative, as the operands are), but for the given tokens' elements, which
- * keep fp32 accuracy, and takes 2 rows vocab bytes of the workspace; sums over
- * it are fp32, in a fixed order, and rounded once.
+ * The logits are formed again, by the same sums as in lse (fp32; the tensor
+ * cores cut off up to 2^-23 of the sum so far for every 16 of dim, at most 80
+ * times in a row before an addition that rounds); their gradient is
+ * rounded to bf16 (2^-8 relative, as the operands are), but for the given
+ * tokens' elements, which keep fp32 accuracy: dlogprob (1 - p) is good to the
+ * rounding of lse, 2^-24 |lse| dlogprob.  It takes 2 rows vocab bytes of the
+ * workspace and, for those elements, 4 rows dim; sums over it are fp32, in a
+ * fixed order, and rounded once.
  * Supported: bf16, dim a multiple of 8 up to 2^20, vocab and rows up to 2^22,
  * row strides below 2^39.  Logits are taken to be above -1e38: minus infinity
  * among them (an infinite weight) makes the entropy NaN.  A wait that gives up

@@ -16,10 +16,13 @@
 //
 // The tensor cores add into fp32 with truncation, so a sum over K comes out
 // too small by 2^-25 or so of itself for every 16 of K: 2.6e-6 at K = 2560,
-// which scales all logits alike and shows in the entropy (1.2e-6 of it).  For
-// the statistics a tile's sum is therefore taken in shares of at most
-// kShare chunks, which are added in registers with rounding: 5.5e-7, for 856
-// instead of 839 us at 8192 x 2560 x 32000 (16 chunks: 884 us).
+// which scales all logits alike and shows in the entropy (1.2e-6 of it).  A
+// tile's sum of logits is therefore taken in shares of at most kShare chunks,
+// which are added in registers with rounding: 5.5e-7, for 856 instead of 839 us
+// at 8192 x 2560 x 32000 (16 chunks: 884 us).  The gradient takes the same
+// shares (4095 x 2560 x 50277: 694 us for 681): p = exp(z - lse) needs the z that
+// is in lse.  Where a given token is nearly certain its dz, dlogprob (1 - p), is
+// a difference of the two, and 2.6e-6 of z = 30 would be 80% of it at p = 0.9999.
 //
 // What bounds it: the tensor cores under the power limit (1.05 TFLOP for dz in
 // 640 us, 1.65 PFLOP/s; a library product sustains 1.71).  Pairs: forward and
@@ -48,8 +51,8 @@ constexpr int kLongest = 4096;  // and at most in one sum of the gradient: 2.7e-
 constexpr uint64_t kWaitNs = 100000000ull;
 constexpr int kNoLead = 0x7FFFFFFF;  // above every row
 
-// What becomes of an accumulator.
-enum Use { kStats, kGrad, kStore };
+// What becomes of an accumulator: statistics of the logits, their gradient (of sums in one share, or in several), the product.
+enum Use { kStats, kGrad, kGradShares, kStore };
 constexpr int kGemmThreads = 128 + 32 * kReaders;  // warps: copy, MMA, TMEM, -, the readers
 
 // dz is rounded to bf16 (2^-8 relative at most, as its products' other operands are), which would show where one element
@@ -239,6 +242,30 @@ __device__ __forceinline__ void loaded(float (&z)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(z[i]));
 }
 
+// One column, of the warp's 32 rows.
+__device__ __forceinline__ float tmem_column(uint32_t at) {
+    float v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(at));
+    tmem_ld_wait();
+    asm volatile("" : "+f"(v));
+    return v;
+}
+// One of 128 registers.
+__device__ __forceinline__ float pick(const float (&z)[4][32], int at) {
+    float v = 0.f;
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+        int in = at - c;
+        asm volatile("" : "+r"(in));  // (or all of z is kept in memory and indexed)
+        if (in >= 0 && in < 16) {
+            v = z[c / 32][c % 32];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) v = in == i ? z[c / 32][c % 32 + i] : v;
+        }
+    }
+    return v;
+}
+
 // The statistics of finite logits (and of any, but for the entropy, which minus infinity makes NaN): the maximum first, then
 // four sums side by side, so that no addition waits for the one before.
 __device__ __forceinline__ Stat stat_of(const float (&z)[4][32]) {
@@ -297,6 +324,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t rank = PAIR ? pair_rank() : 0;
     const int first_unit = PAIR ? blockIdx.x / 2 : blockIdx.x, every = PAIR ? gridDim.x / 2 : gridDim.x;
     constexpr int HALF = PAIR ? 2 : 1;  // blocks that share B and the columns' work
+    constexpr bool GRAD = USE == kGrad || USE == kGradShares, SHARES = USE == kStats || USE == kGradShares;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&bars.ready[i], 1), mbar_init(&bars.taken[i], HALF * kReaders);
@@ -318,10 +346,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if constexpr (PAIR) pair_sync();  // both blocks' barriers are there
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-    const int shares = USE == kStats ? a.shares : 1;
-    // (Statistics: the readers' sums take 128 registers.  384 threads are launched with 168 each: 128 x 56 + 256 x 224.)
+    const int shares = SHARES ? a.shares : 1;
+    // (Where there are shares the readers' sums take 128 registers.  384 threads are launched with 168 each: 128 x 56 + 256 x 224.)
     if (warp < 4) {
-        if constexpr (USE == kStats) reg_dec<56>();
+        if constexpr (SHARES) reg_dec<56>();
         if (warp == 0 && lane == 0) {
             const int bn = a.bn / HALF;  // columns that this block copies
             const uint32_t bytes = HALF * (a.arows + bn) * kBK * 2;
@@ -373,7 +401,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int u = first_unit; u < a.units && ok; u += every) {
                 const Unit t = unit_of(a, u);
                 for (int q = 0; q < shares && ok; ++q, ++n) {
-                    const int k0 = USE == kStats ? a.kc * q / shares : t.k0, k1 = USE == kStats ? a.kc * (q + 1) / shares : t.k1;
+                    const int k0 = SHARES ? a.kc * q / shares : t.k0, k1 = SHARES ? a.kc * (q + 1) / shares : t.k1;
                     const uint32_t acc = n & 1, d = tmem + acc * kBN;
                     if (n >= 2 && !(ok = wait_for(&bars.taken[acc], (n / 2 - 1) & 1, &bars))) break;
                     tc_fence_after();
@@ -403,7 +431,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_wait(&bars.drain, 0, kWaitNs / 5);
         }
     } else {
-        if constexpr (USE == kStats) reg_inc<224>();
+        if constexpr (SHARES) reg_inc<224>();
         const int q = warp % 4, half = (warp - 4) / 4, first = half * (kBN / 2);  // (a warp reads the 32 rows of its number mod 4)
         uint8_t *stage = smem + kRing + (warp - 4) * 4096;
         uint32_t n = 0;
@@ -416,6 +444,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             else
                 mbar_arrive_at(at_first(&bars.taken[acc]));
         };
+        // The sums of this warp's columns (`limit` of them) over all shares; false: a wait gave up.
+        auto sum_shares = [&](uint32_t lanes, int limit, float (&z)[4][32]) {
+            for (int share = 0; share < shares; ++share, ++n) {
+                const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
+                if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) return false;
+                tc_fence_after();
+                if (share == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (32 * j < limit) tmem_ld32(at + 32 * j, z[j]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) loaded(z[j]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kBN / 2; c += 16) {
+                        if (c < limit) {
+                            float v[16];
+                            tmem_ld16(at + c, v);
+                            loaded(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) z[c / 32][c % 32 + i] += v[i];
+                        }
+                    }
+                }
+                taken(acc);
+            }
+            return true;
+        };
         for (int u = first_unit; u < a.units; u += every) {
             const Unit t = unit_of(a, u);
             const int row = (t.m * HALF + rank) * kBM + q * 32 + lane, c0 = t.n * a.bn;
@@ -426,58 +482,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int64_t given = live && a.targets ? a.targets[row] - c0 - first : -1;
                 const int target = given >= 0 && given < limit ? (int)given : -1;
                 float z[4][32];
-                bool ok = true;
-                for (int share = 0; share < shares; ++share, ++n) {
-                    const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
-                    if (!(ok = wait_for(&bars.ready[acc], (n / 2) & 1, &bars))) break;
-                    tc_fence_after();
-                    if (share == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (32 * j < limit) tmem_ld32(at + 32 * j, z[j]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) loaded(z[j]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kBN / 2; c += 16) {
-                            if (c < limit) {
-                                float v[16];
-                                tmem_ld16(at + c, v);
-                                loaded(v);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) z[c / 32][c % 32 + i] += v[i];
-                            }
-                        }
-                    }
-                    taken(acc);
-                }
-                if (!ok) break;
+                if (!sum_shares(lanes, limit, z)) break;
                 if (limit < kBN / 2) {
 #pragma unroll
                     for (int i = 0; i < kBN / 2; ++i) z[i / 32][i % 32] = i < limit ? z[i / 32][i % 32] : kLeast;
                 }
-                if (target >= 0) {
-#pragma unroll
-                    for (int c = 0; c < kBN / 2; c += 16) {
-                        int in = target - c;
-                        asm volatile("" : "+r"(in));  // (or all of z is kept in memory and indexed)
-                        if (in >= 0 && in < 16) {
-                            float v = z[c / 32][c % 32];
-#pragma unroll
-                            for (int i = 1; i < 16; ++i) v = in == i ? z[c / 32][c % 32 + i] : v;
-                            a.given[row] = v;
-                        }
-                    }
-                }
+                if (target >= 0) a.given[row] = pick(z, target);
                 const Stat st = stat_of(z);
                 if (live && first < a.bn)
                     a.stats[((int64_t)t.n * (a.bn > kBN / 2 ? 2 : 1) + half) * a.M + row] = make_float4(st.m, st.sum, st.moment, 0.f);
             } else {
-                const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
                 const int row0 = row - lane, limit = min(min(a.N - c0, a.bn) - first, kBN / 2);  // of this warp's columns
                 RowGrad g{};
                 FixRow fix{};
-                if constexpr (USE == kGrad) {
+                if constexpr (GRAD) {
                     if (live) g = row_grad(a.grad, row, a.N);
                     if (live && t.n == 0 && half == 0 && (g.target < 0 || g.none)) a.rest[row] = 0.f;
                     if (a.lead && t.m == 0 && rank == 0 && q == 0)
@@ -485,30 +503,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 } else if (t.part < 0) {
                     fix = fix_row(a.fix, row, live);
                 }
-                if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
-                ++n;
-                tc_fence_after();
-                float z[2][32] = {};
-                if (limit > 0) {
-                    tmem_ld32(at, z[0]);
-                    loaded(z[0]);
-                }
-#pragma unroll
-                for (int c = 0; c < kBN / 2; c += 32) {
-                    float (&now)[32] = z[c / 32 % 2];
-                    if (c >= limit) continue;
-                    if (c + 32 < kBN / 2 && c + 32 < limit) tmem_ld32(at + c + 32, z[(c / 32 + 1) % 2]);
+                // The given token, where it is among this warp's columns, and its dz.
+                const int in = g.target - c0 - first, target = GRAD && live && !g.none && g.target >= 0 && in >= 0 && in < limit ? in : -1;
+                float given = 0.f;
+                auto give = [&](float z) {
+                    given = given_grad<ENT>(g, z);
+                    a.rest[row] = given - to_f32(from_f32<bf16>(given));
+                };
+                // What becomes of 32 of the columns, from the c-th on.
+                auto put = [&](float (&now)[32], int c) {
                     const int col = c0 + first + c;
-                    if constexpr (USE == kGrad) {
+                    if constexpr (GRAD) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) now[i] = g.none ? 0.f : grad_of<ENT>(g, now[i]);
-                        if (g.target >= col && g.target < col + 32 && !g.none && live) {
+                        if (target >= c && target < c + 32) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (col + i == g.target) {
-                                    now[i] += g.dlp;
-                                    a.rest[row] = now[i] - to_f32(from_f32<bf16>(now[i]));
-                                }
+                            for (int i = 0; i < 32; ++i) now[i] = c + i == target ? given : now[i];
                         }
                     }
                     if (USE == kStore && t.part >= 0) {
@@ -536,9 +546,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             }
                         }
                     }
-                    loaded(z[(c / 32 + 1) % 2]);
+                };
+                if constexpr (SHARES) {
+                    float z[4][32] = {};
+                    if (!sum_shares(lanes, limit, z)) break;
+                    if (target >= 0) give(pick(z, target));
+#pragma unroll
+                    for (int c = 0; c < kBN / 2; c += 32)
+                        if (c < limit) put(z[c / 32], c);
+                } else {
+                    const uint32_t acc = n & 1, at = lanes + acc * kBN + first;
+                    if (!wait_for(&bars.ready[acc], (n / 2) & 1, &bars)) break;
+                    ++n;
+                    tc_fence_after();
+                    if constexpr (GRAD) {  // (as many columns as there are different given tokens: few or none)
+                        float zt = 0.f;
+                        for (unsigned todo = __ballot_sync(0xffffffffu, target >= 0); todo;) {
+                            const int c = __shfl_sync(0xffffffffu, target, __ffs(todo) - 1);
+                            const float v = tmem_column(at + c);
+                            if (target == c) zt = v;
+                            todo &= ~__ballot_sync(0xffffffffu, target == c);
+                        }
+                        if (target >= 0) give(zt);
+                    }
+                    float z[2][32] = {};
+                    if (limit > 0) {
+                        tmem_ld32(at, z[0]);
+                        loaded(z[0]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kBN / 2; c += 32) {
+                        if (c >= limit) continue;
+                        if (c + 32 < kBN / 2 && c + 32 < limit) tmem_ld32(at + c + 32, z[(c / 32 + 1) % 2]);
+                        put(z[c / 32 % 2], c);
+                        loaded(z[(c / 32 + 1) % 2]);
+                    }
+                    taken(acc);
                 }
-                taken(acc);
             }
         }
         if (USE != kStats && lane == 0) bulk_wait_all();  // the copies have read what they store
@@ -951,8 +995,13 @@ ssd_status_t ssd_head_logprob_bwd(const ssd_head_shape_t *shape, const ssd_rows_
     const bool given = targets && dlogprob;  // otherwise no element of dz stands out
     int *lead = dweight && given ? reinterpret_cast<int *>(ws + p.lead) : nullptr;
     a.lead = lead;
-    e = dentropy ? run_gemm<kGrad, false, false, true>(mh, mw, mz_out, a, "head_dlogits", stream)
-                 : run_gemm<kGrad, false, false, false>(mh, mw, mz_out, a, "head_dlogits", stream);
+    auto dlogits = [&](auto use, auto ent) {
+        e = run_gemm<decltype(use)::value, false, false, decltype(ent)::value>(mh, mw, mz_out, a, "head_dlogits", stream);
+    };
+    auto with_shares = [&](auto ent) {
+        a.shares > 1 ? dlogits(std::integral_constant<int, kGradShares>{}, ent) : dlogits(std::integral_constant<int, kGrad>{}, ent);
+    };
+    dentropy ? with_shares(std::true_type{}) : with_shares(std::false_type{});
     if (e == cudaSuccess && dhidden) {
         GemmArgs b = p.dh;
         b.status = status;

@@ -147,7 +147,7 @@ __device__ __forceinline__ float logprob_of(float z, float lse) { return lse == 
 
 // dz = p (dlse - dlogprob - dentropy (log p + entropy)) + dlogprob [v = target]
 struct RowGrad {
-    float lse, coef, ent, dent, dlp;
+    float lse, coef, ent, dent, dlp, dlse;
     int target;
     bool none;  // nothing left in the row: zeros
 };
@@ -162,7 +162,8 @@ __device__ __forceinline__ RowGrad row_grad(const RowGradIn &a, int64_t row, int
     g.lse = a.lse[row];
     g.dlp = a.dlogprob && t >= 0 ? a.dlogprob[row] : 0.f;
     if (t >= vocab) g.dlp = __uint_as_float(0x7FC00000u);
-    g.coef = (a.dlse ? a.dlse[row] : 0.f) - g.dlp;
+    g.dlse = a.dlse ? a.dlse[row] : 0.f;
+    g.coef = g.dlse - g.dlp;
     g.dent = a.dentropy ? a.dentropy[row] : 0.f;
     g.ent = a.dentropy ? a.entropy[row] : 0.f;
     g.none = g.lse == -INFINITY;
@@ -173,6 +174,14 @@ __device__ __forceinline__ float grad_of(const RowGrad &g, float z) {
     const float t = z - g.lse, p = ex2(t * kLog2e);
     if constexpr (ENT) return p * fmaf(-g.dent, fmaxf(t, kNothing) + g.ent, g.coef);  // (a masked element's p is 0)
     return p * g.coef;
+}
+
+// The given token's: dlogprob (1 - p) keeps its digits where p is close to 1.
+template <bool ENT>
+__device__ __forceinline__ float given_grad(const RowGrad &g, float z) {
+    const float t = z - g.lse, p = ex2(t * kLog2e);
+    const float other = ENT ? p * fmaf(-g.dent, fmaxf(t, kNothing) + g.ent, g.dlse) : p * g.dlse;
+    return fmaf(-g.dlp, expm1f(t), other);
 }
 
 // Rows at one stride, which may be as far apart as batches elsewhere (the last rows of long prompts' logits).

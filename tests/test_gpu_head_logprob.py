@@ -158,6 +158,47 @@ def test_the_given_tokens_part_is_not_rounded(rows, dim, vocab, kinds):
     assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
 
 
+def peaked(rows, dim, vocab, seed=0):
+    """Rows whose given token is nearly certain: its logit 26 and more, 1 - p from 1e-2 to 1e-4 and less; the others around 15."""
+    g = torch.Generator().manual_seed(seed + rows + dim)
+    w = torch.randn(vocab, dim, generator=g) * 2 / math.sqrt(dim)
+    w[:, 0] = 1
+    targets = torch.randperm(vocab, generator=g)[:rows]
+    h = w[targets] * torch.linspace(2.9, 4.0, rows)[:, None]
+    h[:, 0] = 15
+    return h.bfloat16().cuda(), w.bfloat16().cuda(), targets.cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,dim,vocab", [(40, 2560, 1000), (256, 2560, 1000), (300, 2560, 1003), (40, 40960, 500), (256, 16384, 600),
+                                            (200, 640, 1000)])
+@pytest.mark.parametrize("which", ["logprob", "all"])
+def test_gradient_of_rows_that_are_nearly_certain(rows, dim, vocab, which):
+    h, w, targets = peaked(rows, dim, vocab)
+    glp, glse, gent = upstream(rows)
+    z = logits(h, w)
+    at, wlse, went = definition(z, targets)
+    rest = -torch.expm1(at)  # 1 - p
+    assert rest.min() < 5e-4 and rest.max() < 0.2 and z.max() < 40
+    _, lse, entropy = ssd.ssd_head_logprob_fwd(h, w, targets)
+    kw = dict(dlogprob=glp) if which == "logprob" else dict(dlogprob=glp, dlse=1e-4 * glse, dentropy=1e-4 * gent)
+    dh, dw = ssd.ssd_head_logprob_bwd(h, w, targets, lse, entropy, **kw)
+    zero = torch.zeros(rows, dtype=torch.float64)
+    a, b, c = (ref.d(glp), ref.d(1e-4 * glse), ref.d(1e-4 * gent)) if which == "all" else (ref.d(glp), zero, zero)
+    d = want_gradient(z, targets.cpu(), wlse, went, a, b, c)
+    # The given token's dz: 1 - p is exp of a difference of logits, which are fp32 sums in shares of at most 1280 (80 additions,
+    # each off by up to 2^-23 of a sum up to 35, 3e-4; both sides alike), so 1e-3 of it; and lse's rounding, half a step, with its
+    # logarithm's, 3e-7.  What else is given to the row: 1e-4 of p, good to 2e-5 of that.  The others as in
+    # test_gradient.
+    size = a.abs() + b.abs() + 40 * c.abs()
+    err = d.abs() * 2.0 ** -8 + 1e-3 * torch.exp(z - wlse[:, None]) * size[:, None]
+    k = torch.arange(rows)
+    err[k, targets.cpu()] = a.abs() * (1e-3 * rest + 2.0 ** -24 * wlse + 3e-7) + 2e-5 * (b.abs() + 40 * c.abs())
+    for got, x, e2, name in ((dh, d @ ref.d(w), (err ** 2) @ (ref.d(w) ** 2), "dhidden"),
+                             (dw, d.t() @ ref.d(h), (err.t() ** 2) @ (ref.d(h) ** 2), "dweight")):
+        ref.check(got, x, name, rel=1.0, scale=5 / math.sqrt(3) * e2.sqrt() + 1e-30)
+
+
 @pytest.mark.gpu
 def test_gradient_agrees_with_differences():
     h, w, targets = make(96, 128, 900, seed=4)
