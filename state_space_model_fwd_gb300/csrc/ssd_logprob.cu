@@ -235,13 +235,13 @@ __device__ void top_of_part(const Slots<T> &s, float m, bool any, int k, TopShar
         return;
     }
     // More above tau than there is room for (they sit in fewer than k threads): one after another, the largest below the last.
-    unsigned long long last = ~0ull;
+    unsigned long long last = 0;
     unsigned long long *part = t.found;
     for (int r = 0; r < k; ++r) {
         unsigned long long big = 0;
         auto look = [&](int i, float z) {
             const unsigned long long e = entry_of(z, i);
-            if (e < last && e > big) big = e;
+            if ((r == 0 || e < last) && e > big) big = e;  // (a NaN of the first token is the largest entry there is)
         };
         s.cut(tid, look);
         for (int j = s.full0 + tid; j < s.full1; j += kThreads) {

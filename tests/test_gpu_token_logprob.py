@@ -128,6 +128,36 @@ def test_alternatives_in_any_order(what, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 700])
+@pytest.mark.parametrize("what", ["all nan", "mostly nan", "nan first", "equal", "two values", "rising", "falling", "few threads"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_alternatives_of_either_type_in_any_order(dtype, what, rows):
+    """More equal ones than there is room for, NaN among them, the first token's included."""
+    vocab = 50003
+    i = torch.arange(vocab, dtype=torch.float32)
+    if what == "all nan":
+        z = torch.full((vocab,), math.nan)
+    elif what == "mostly nan":
+        z = torch.where(i % 9 == 4, torch.sin(i), torch.tensor(math.nan))
+    elif what == "nan first":
+        z = torch.where(i < 30, torch.tensor(math.nan), torch.sin(i))
+    elif what == "equal":
+        z = torch.full((vocab,), 1.5)
+    elif what == "two values":
+        z = (i % 1000 == 7).float()
+    elif what == "rising":
+        z = i * 1e-3
+    elif what == "falling":
+        z = -i * 1e-3
+    else:
+        z = torch.where((i % 4096 < 128) | (i % 2048 < 64), 5 + i * 1e-5, -i * 1e-6)
+    z = z.to(DT[dtype]).expand(rows, vocab).contiguous().cuda()
+    for top in (1, 5, 64):
+        got = ssd.ssd_token_logprob_fwd(z, top=top)
+        assert torch.equal(got[4].cpu(), top_of(ref.d(z[:1]), top).expand(rows, top)), top
+
+
+@pytest.mark.gpu
 def test_infinity_and_nan():
     z, targets = make("f32", 3, 9000, seed=2)
     z[0, 77] = math.inf
