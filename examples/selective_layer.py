@@ -4,8 +4,8 @@ ChannelModel: blocks of [norm | projection | short convolution | channel scan
 with its gate | projection], the norm that opens a block adding the previous
 block's output to the residual stream.  It trains (the operators' gradients
 as autograd functions below) on the given tokens' log-probabilities, which in
-bf16 come straight from the hidden states, reads prompts, continues token by
-token and lists the alternatives of an answer.
+bf16 come straight from the hidden states (of a multiple of 8 columns), reads
+prompts, continues token by token and lists the alternatives of an answer.
 
 GatedModel: the same around the gated scan.
 
@@ -243,7 +243,7 @@ class ChannelModel(torch.nn.Module):
     def logprobs(self, ids, targets):
         """Of targets [b, L] (negative: none, 0) after each of ids [b, L]."""
         h = self.hidden(ids)
-        if h.dtype == torch.bfloat16:
+        if h.dtype == torch.bfloat16 and h.shape[-1] % 8 == 0:  # (rows on 16-byte boundaries)
             return HeadLogprob.apply(h, self.embed, targets)
         return TokenLogprob.apply(h @ self.embed.t(), targets)
 
