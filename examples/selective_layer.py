@@ -110,7 +110,8 @@ class HeadLogprob(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dlogprob):
         hidden, weight, targets, lse = ctx.saved_tensors
-        return (*ssd.ssd_head_logprob_bwd(hidden, weight, targets, lse, dlogprob=dlogprob.contiguous()), None)
+        return (*ssd.ssd_head_logprob_bwd(hidden, weight, targets, lse, dlogprob=dlogprob.contiguous(),
+                                          need_dhidden=ctx.needs_input_grad[0], need_dweight=ctx.needs_input_grad[1]), None)
 
 
 # ---------------------------------------------------------------------------

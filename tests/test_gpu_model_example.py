@@ -85,6 +85,23 @@ def test_bf16_models_of_any_width(ex, kind):
     assert all(math.isfinite(v) for v in ex.train(model, ids, steps=2))
 
 
+def test_only_the_gradients_that_are_asked_for(ex, monkeypatch):
+    torch.manual_seed(10)
+    model = ex.GatedModel(vocab=96, dim=32, inner=64).cuda()
+    ids = torch.randint(0, 96, (2, 20), device="cuda")
+    h = model.hidden(ids).detach()
+    asked, real = [], ssd.ssd_head_logprob_bwd
+    monkeypatch.setattr(ssd, "ssd_head_logprob_bwd", lambda *a, **kw: asked.append((kw["need_dhidden"], kw["need_dweight"])) or real(*a, **kw))
+    w = model.embed.detach()
+    both = [v.clone().requires_grad_(True) for v in (h, w)]
+    ex.HeadLogprob.apply(*both, ids).sum().backward()
+    for k in range(2):
+        one = [v.clone().requires_grad_(i == k) for i, v in enumerate((h, w))]
+        ex.HeadLogprob.apply(*one, ids).sum().backward()
+        assert torch.equal(one[k].grad, both[k].grad) and one[1 - k].grad is None
+    assert asked == [(True, True), (True, False), (False, True)]
+
+
 def test_training_runs(ex):
     torch.manual_seed(5)
     model = ex.GatedModel().cuda()
