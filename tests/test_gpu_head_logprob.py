@@ -75,6 +75,26 @@ def test_more_than_2_31_logits():
 
 
 @pytest.mark.gpu
+def test_gradient_of_the_weights_beyond_2_31_logits():
+    """Only the last rows have a gradient: what the weights get is what those rows alone give."""
+    rows, dim, vocab, few = 43100, 64, 50277, 200
+    assert (rows - few) * vocab > 1 << 31
+    h, w, targets = make(rows, dim, vocab, seed=4)
+    glp, _, gent = upstream(rows)
+    glp[:-few], gent[:-few] = 0, 0
+    _, lse, entropy = ssd.ssd_head_logprob_fwd(h, w, targets)
+    dh, dw = ssd.ssd_head_logprob_bwd(h, w, targets, lse, entropy, dlogprob=glp, dentropy=gent)
+    part = ssd.ssd_head_logprob_fwd(h[-few:], w, targets[-few:])
+    want = ssd.ssd_head_logprob_bwd(h[-few:], w, targets[-few:], part[1], part[2], dlogprob=glp[-few:], dentropy=gent[-few:])
+    assert bool((dh[:-few] == 0).all())
+    # dz from an lse that is 2e-6 (1 + |lse|) apart: the next bf16 value here and there, one step (2^-7) of a term of the sum, of
+    # which the largest, the given tokens', have none; and a step of the result
+    for a, b in ((dh[-few:], want[0]), (dw, want[1])):
+        a, b = a.float(), b.float()
+        assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -7 * b.square().mean().sqrt()).all())
+
+
+@pytest.mark.gpu
 def test_many_rows_with_the_same_tokens():
     """So many that the chunks they are summed in are longer than a block, and there are hundreds of them."""
     rows, dim, vocab = 270000, 8, 40
