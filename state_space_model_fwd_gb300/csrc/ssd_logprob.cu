@@ -42,7 +42,6 @@ struct LogprobArgs {
     float *logprob, *lse, *entropy, *top_logprob;
     int64_t *top_index;
     RowGradIn grad;
-    int64_t rows;
     int vocab, top, parts;
 };
 
@@ -432,7 +431,7 @@ ssd_status_t fwd_typed(const ssd_logprob_shape_t *s, const ssd_rows_t *logits, c
     a.logits = static_cast<const T *>(logits->data), a.row_stride = logits->row_stride;
     a.targets = targets, a.logprob = logprob, a.lse = lse, a.entropy = entropy;
     a.top_logprob = top_logprob, a.top_index = top_index;
-    a.rows = s->rows, a.vocab = (int)s->vocab, a.top = (int)s->top;
+    a.vocab = (int)s->vocab, a.top = (int)s->top;
     // Few long rows: up to four blocks, a cluster, share one (4 rows with eight alternatives in a graph: of 131072 15.5 us by
     // one block, 12.0 by two, 9.5 by four or eight; of 50280 9.5, -, 9.3, 10.4; of 8192 6.5 by one, 8.1 by two), as long as
     // that gives no SM more than two (152 rows of 50280: 10 us, by four blocks each 20).
@@ -462,7 +461,7 @@ ssd_status_t bwd_typed(const ssd_logprob_shape_t *s, const ssd_rows_t *logits, c
     a.logits = static_cast<const T *>(logits->data), a.row_stride = logits->row_stride;
     a.dlogits = static_cast<T *>(dlogits->data), a.drow_stride = dlogits->row_stride;
     a.grad = RowGradIn{targets, lse, entropy, dlogprob, dlse, dentropy};
-    a.rows = s->rows, a.vocab = (int)s->vocab;
+    a.vocab = (int)s->vocab;
     const int64_t per = 256 * 4 * Slots<T>::V;  // elements of a block: one round of loads
     a.parts = (int)((s->vocab + per - 1) / per);
     if (s->rows * a.parts > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
