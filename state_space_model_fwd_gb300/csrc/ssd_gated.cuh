@@ -27,7 +27,6 @@ namespace ssd {
 
 constexpr int kCols = 64;        // channels of a block
 constexpr int kStateEvery = 64;  // tokens between the states kept for the gradient
-constexpr int kSMs = 152;
 constexpr int kGroup = 16;       // tiles from one entry state to the next
 
 // Two channels of one token as they lie in memory.

@@ -772,8 +772,6 @@ bool map_of(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t p
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kSMs = 152;
-
 // Tiles of 256 rows where they leave no more than an eighth of the rows empty and sums are long enough for a pair's longer
 // start.  8192 x 256 x 32000 120 us, in pairs 134; x 512 193 and 199.  Forward and gradient of T x 2560 x 50277, T = 300: 349 us,
 // with pairs for dweight, a sum over T, 362; T = 1000: 793 us, without any pairs 875.

@@ -167,6 +167,8 @@ inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr
 
 inline size_t dtype_size(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
 
+constexpr int kSMs = 152;
+
 constexpr int64_t kMaxBatchStride = int64_t(1) << 40;  // keeps every offset far inside 63 bits
 constexpr int64_t kMaxRowStride = int64_t(1) << 31;
 

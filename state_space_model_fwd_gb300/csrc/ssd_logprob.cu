@@ -19,8 +19,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSMs = 152;
-
 // A row is 100 KB: a block spends as long on joining its threads' statistics
 // and on the alternatives as on loads, so small blocks, many of them, keep
 // memory busy (forward and gradient of 8192 x 50280 bf16 / five alternatives of
