@@ -553,8 +553,9 @@ SSD_API ssd_status_t ssd_block_norm_bwd(const ssd_norm_shape_t *shape, const ssd
  * ssd_token_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
  *   dlogits_v = p_v (dlse - dlogprob - dentropy (log p_v + entropy)) + [v = target] dlogprob
  * from the logits and what the forward call gave (entropy only with
- * dentropy).  dlogits may be the logits themselves (the same rows), otherwise
- * must not overlap them; `top` is ignored beyond its check.
+ * dentropy); p = exp(z - lse), good to 2^-24 of lse and of z - lse and a few
+ * 2^-24 of itself.  dlogits may be the logits themselves (the same rows),
+ * otherwise must not overlap them; `top` is ignored beyond its check.
  */
 #define SSD_LOGPROB_MAX_TOP 64
 typedef struct {
@@ -574,7 +575,8 @@ SSD_API ssd_status_t ssd_token_logprob_bwd(const ssd_logprob_shape_t *shape, con
  * Head log-probabilities: logprob, lse and entropy as ssd_token_logprob_fwd
  * gives them, of the logits z = hidden weight^T, which are formed on the
  * tensor cores (bf16 operands, fp32 sums) and not stored.  hidden [rows, dim],
- * weight [vocab, dim] bf16, rows 16-byte aligned (pointer and row_stride);
+ * weight [vocab, dim] bf16, rows 16-byte aligned (pointer and row_stride) and
+ * apart (no stride of 0);
  * targets, outputs and masked or absent targets as there.
  * ssd_head_logprob_bwd: dlogprob, dlse, dentropy [rows] (any NULL: zero) ->
  * dhidden [rows, dim], dweight [vocab, dim] in bf16 (either NULL: not wanted).

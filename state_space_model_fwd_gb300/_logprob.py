@@ -2,8 +2,8 @@
 the log of the sum, entropies and the top alternatives, from logits or from
 hidden states and the output weights.
 
-Rows of an operand lie at one stride (column slices and one row for all are
-fine).  Operands are on the current device; every function takes ``stream``
+Rows of an operand lie at one stride.  Column slices are fine, from hidden
+states on 16-byte boundaries; one row for all is, for logits.  Operands are on the current device; every function takes ``stream``
 (the current one by default).  Argument marshalling only.
 """
 from __future__ import annotations

@@ -6,8 +6,9 @@
 // of 64 channels takes 89 instructions (8 of the special function unit a
 // channel with a gate), issued in half of the cycles: with 128 registers for 16
 // tokens' a and beta s(i) x there are four warps a scheduler, and a tile's two
-// meetings with the links cost 2000 of its 13000 cycles.  4 x 4096 x 2560 bf16
-// with a gate 103 us, 50% of the DRAM rate; 8 tokens a warp in 32 warps an SM
+// meetings with the links cost 2000 of its 13000 cycles.  The special function
+// unit is active for 47% of the time.  4 x 4096 x 2560 bf16 with a gate 103 us,
+// 50% of the DRAM rate; 8 tokens a warp in 32 warps an SM
 // are as fast (less to wait for, twice the meetings), tiles of 64 tokens too.
 #include "ssd_gated.cuh"
 

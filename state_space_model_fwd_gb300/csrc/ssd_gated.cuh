@@ -128,7 +128,7 @@ __device__ __forceinline__ void fill_slot(Slot<T, ALIGN> &slot, int lane, float 
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Asynchronous copies of a warp's S tokens of one array from token t0 on, `left` of which exist, to every STRIDE-th slot
 // (others: `fill`).  A lane copies 16 bytes of one of the rows that an instruction spans, for others to read.  65537 x 2560
-// packed bf16, rows of 2560: 452 us; of 2562 515 (copied by the lanes that read them, four bytes each: 527); of 2561 528
+// packed bf16, rows of 2560: 447 us; of 2562 516 (copied by the lanes that read them, four bytes each: 527); of 2561 532
 // (through registers: 1092).
 template <typename T, int ALIGN, int S, int STRIDE>
 __device__ __forceinline__ void fetch_rows(Slot<T, ALIGN> *dst, const Rows<const T> &r, int b, int t0, const Lane<ALIGN> &k, int lane,
@@ -282,7 +282,7 @@ __device__ __forceinline__ Run then(const Run &r, const Run &s) {
 // fixed.  Tiles are numbered by a counter, earlier tokens first, and a block
 // finishes its tiles in that order, so the first unfinished one never waits.
 // Groups of 16: one sequence of 65537 tokens, 64 channels 35 us (8: 58, 32:
-// 26), 48 packed ones of 2560 channels 461 (455, 487).
+// 26), 48 packed ones of 2560 channels out of rows of 2568 461 (455, 487).
 struct Links {
     unsigned long long *run, *entry;  // null: one tile a row, nothing to wait for
     unsigned *ticket;
@@ -420,8 +420,8 @@ struct GatedArgs {
     Links links;
 };
 
-// Rows of one short tile each: as many to a block as leave every place of a block filled (4096 x 16 x 2560 bf16 403 us, one a
-// block 1729; gradient with the states formed again 1237, 3617).
+// Rows of one short tile each: as many to a block as leave every place of a block filled (4096 x 16 x 2560 bf16 394 us, one a
+// block 1729; gradient with the states formed again 1068, 3617).
 inline int rows_of_block(int64_t rows, int64_t ntile, int sub, int warps, int places) {
     if (ntile > 1) return 1;
     const int64_t most = warps / sub, want = (rows + places - 1) / places;

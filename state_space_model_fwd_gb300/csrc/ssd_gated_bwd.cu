@@ -14,7 +14,8 @@
 //
 // What bounds it: issue and waiting in turn, 211 instructions a token and warp
 // in half of the cycles, with 15 registers a token kept between the passes (4 x
-// 4096 x 2560 bf16 with a gate 226 us, 40% of the DRAM rate).  16 warps of 4
+// 4096 x 2560 bf16 with a gate 226 us, 40% of the DRAM rate, the special
+// function unit active for 29%).  16 warps of 4
 // tokens or of 8 are slower (8 x 4096 x 2560: 606 and 559 us against 471 at the
 // time), and so is keeping beta s(i) x instead of forming it again (477);
 // leaving x in shared memory instead of registers gives 0.5%.

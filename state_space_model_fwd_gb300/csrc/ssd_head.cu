@@ -70,7 +70,7 @@ struct Fix {
     const float *sums;
     int64_t dim;
 };
-// What is added to 8 columns of a row of the product; `which`: 1 dhidden, 2 dweight.
+// What is added to 8 columns of a row of the product: a multiple of the given token's weights, or a row of the sums.
 struct FixRow {
     const bf16 *w;
     const float *e;
