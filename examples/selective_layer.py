@@ -299,6 +299,8 @@ def generate(model, ids, count):
 def answer(model, ids, count, top=4):
     """The greedy continuation [b, count] with every token's log-probability [b, count] and the `top` most probable tokens
     in its place, [b, count, top]."""
+    if count < 1:
+        raise ValueError(f"count must be at least 1, got {count}")
     logits, caches = model.prompt(ids)
     logits, out = logits[:, -1], []
     while True:

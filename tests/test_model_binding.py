@@ -1,5 +1,8 @@
 """Host side of the gated scan and of the log-probabilities: what the binding
 makes of devices, strides and workspaces.  No call here reaches a kernel."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -43,3 +46,17 @@ def test_entry_points_are_exported_and_documented():
     for name in ENTRIES:
         assert name in ssd.__all__ and name in ssd.EXPORTED
         assert "Returns" in getattr(ssd, name).__doc__
+
+
+def test_an_answer_of_no_tokens_is_refused():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "selective_layer.py")
+    spec = importlib.util.spec_from_file_location("selective_layer_answers", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+
+    class Model:  # gives up where a program would go on for ever
+        def prompt(self, ids):
+            raise AssertionError("asked for a prompt")
+    for count in (0, -1):
+        with pytest.raises(ValueError, match="count"):
+            ex.answer(Model(), torch.zeros(1, 4, dtype=torch.int64), count)
